@@ -14,7 +14,8 @@ _BINDING_NAMES = {
     "raise_for", "pair_loss_scores_fwd_bwd", "pair_loss_scores_workspace_bytes",
     "pair_loss_sigmoid_matryoshka_fwd_bwd", "pair_loss_sigmoid_matryoshka_workspace_bytes",
     "pair_loss_sigmoid_groups_fwd_bwd", "maxsim_scores_named", "maxsim_named_workspace_bytes",
-    "maxsim_backward_named", "selftest_bounded_wait",
+    "maxsim_backward_named", "selftest_bounded_wait", "rotary_table", "rotary_heads", "rotary_heads_backward",
+    "norm_rotary_heads", "norm_rotary_heads_backward", "cross_attention", "cross_attention_backward",
 }
 
 

@@ -139,6 +139,43 @@ class MaxSimBackwardNamedArgs(ctypes.Structure):
     _fields_ = [("base", MaxSimBackwardArgs), ("pairs", Edges)]
 
 
+class HeadsArgs(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("row_stride", c_size_t), ("head_stride", c_size_t)]
+
+
+class RotaryTableArgs(ctypes.Structure):
+    _fields_ = [("positions", c_size_t), ("rotary_dim", c_size_t), ("base", ctypes.c_double), ("scaling", c_int),
+                ("factor", ctypes.c_double), ("trained_positions", c_size_t), ("table", c_void_p),
+                ("stream", c_void_p)]
+
+
+class RotaryPartArgs(ctypes.Structure):
+    _fields_ = [("rows", c_size_t), ("heads", c_size_t), ("positions", c_void_p), ("x", HeadsArgs), ("y", HeadsArgs),
+                ("d_y", HeadsArgs), ("d_x", HeadsArgs), ("gain", c_void_p), ("d_gain", c_void_p)]
+
+
+class RotaryArgs(ctypes.Structure):
+    _fields_ = [("dtype", c_int), ("interleaved", c_int), ("head_dim", c_size_t), ("rotary_dim", c_size_t),
+                ("table", c_void_p), ("table_rows", c_size_t), ("epsilon", c_float), ("q", RotaryPartArgs),
+                ("k", RotaryPartArgs), ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+                ("device_status", c_void_p), ("stream", c_void_p)]
+
+
+class AttentionArgs(ctypes.Structure):
+    _fields_ = [("dtype", c_int), ("items", c_size_t), ("query_rows", c_size_t), ("key_rows", c_size_t),
+                ("query_offsets", c_void_p), ("key_offsets", c_void_p), ("max_query_rows", c_size_t),
+                ("max_key_rows", c_size_t), ("query_heads", c_size_t), ("key_heads", c_size_t),
+                ("head_dim", c_size_t), ("scale", c_float), ("key_mask", c_void_p), ("q", HeadsArgs),
+                ("k", HeadsArgs), ("v", HeadsArgs), ("output", HeadsArgs), ("lse", c_void_p),
+                ("d_output", HeadsArgs), ("d_q", HeadsArgs), ("d_k", HeadsArgs), ("d_v", HeadsArgs),
+                ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("device_status", c_void_p),
+                ("stream", c_void_p)]
+
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # cli_dtype_t
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
 EXPORTS = {
     "cli_status_name": (ctypes.c_char_p, [c_int]),
     "pair_loss_sigmoid_fwd_bwd": (c_int, [ctypes.POINTER(PairLossSigmoidArgs)]),
@@ -158,6 +195,16 @@ EXPORTS = {
     "maxsim_backward_named": (c_int, [ctypes.POINTER(MaxSimBackwardNamedArgs)]),
     "maxsim_backward_workspace_bytes": (c_size_t, [c_size_t, c_size_t, c_size_t, c_size_t, c_size_t]),
     "maxsim_backward_no_alloc": (c_int, [ctypes.POINTER(MaxSimBackwardArgs)]),
+    "rotary_table": (c_int, [ctypes.POINTER(RotaryTableArgs)]),
+    "rotary_heads": (c_int, [ctypes.POINTER(RotaryArgs)]),
+    "rotary_heads_backward": (c_int, [ctypes.POINTER(RotaryArgs)]),
+    "norm_rotary_heads": (c_int, [ctypes.POINTER(RotaryArgs)]),
+    "norm_rotary_heads_backward": (c_int, [ctypes.POINTER(RotaryArgs)]),
+    "norm_rotary_heads_backward_workspace_bytes": (c_size_t, [c_size_t]),
+    "cross_attention": (c_int, [ctypes.POINTER(AttentionArgs)]),
+    "cross_attention_workspace_bytes": (c_size_t, [ctypes.POINTER(AttentionArgs)]),
+    "cross_attention_backward": (c_int, [ctypes.POINTER(AttentionArgs)]),
+    "cross_attention_backward_workspace_bytes": (c_size_t, [ctypes.POINTER(AttentionArgs)]),
     "cli_selftest_bounded_wait": (c_int, [c_void_p, c_void_p, ctypes.c_uint32, c_void_p]),
 }
 NO_ALLOC_MAX_QUERY_ROWS = 262144   # CLI_MAXSIM_NO_ALLOC_MAX_QUERY_ROWS in include/cli.h
@@ -558,3 +605,249 @@ def maxsim_backward_named(q_data, q_offsets, d_data, d_offsets, argmax, d_scores
     args = MaxSimBackwardNamedArgs(base=base, pairs=_edges(pairs, Q.count))
     raise_for(lib.maxsim_backward_named(ctypes.byref(args)), "maxsim_backward_named")
     return dict(d_queries=dq, d_documents=dd, device_status=st)
+
+
+# ----------------------------------------------------------------------------
+# token states
+# ----------------------------------------------------------------------------
+
+def _heads(t, name, rows, heads, dim, dtype):
+    """A [rows, heads, dim] tensor of `dtype` whose heads are contiguous -> HeadsArgs."""
+    _check_cuda(t, name, dtype)
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[1] != heads or t.shape[2] != dim:
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name} must be [{rows}, {heads}, {dim}], not {list(t.shape)}")
+    row, head, inner = t.stride()
+    if inner != 1 and dim > 1:
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name}: the elements of a head must be contiguous")
+    return HeadsArgs(t.data_ptr(), row, head)
+
+
+def _out(out, name, like, rows=None):
+    """The caller's output `name`, or a new packed one of the shape of `like` (with `rows` rows)."""
+    t = out.get(name) if out else None
+    if t is not None:
+        return t
+    return torch.empty((like.shape[0] if rows is None else rows, *like.shape[1:]), dtype=like.dtype,
+                       device=like.device)
+
+
+def _status(device_status, device):
+    if device_status is None:
+        return torch.empty(1, dtype=torch.int32, device=device)   # the call writes it
+    _check_cuda(device_status, "device_status", torch.int32)
+    return device_status
+
+
+def rotary_table(positions, rotary_dim, base=10000.0, scaling="plain", factor=1.0, trained_positions=0, out=None,
+                 device="cuda", stream=None):
+    """The (cos, sin) table [positions, rotary_dim / 2, 2] fp32 that the rotation verbs read.  `scaling` is 'plain',
+    'linear', 'ntk' or 'yarn' for contexts `factor` times the trained one.  Returns dict(table)."""
+    if scaling not in ROTARY_SCALINGS:
+        raise UnsupportedError(CLI_UNSUPPORTED, f"rotary_table: scaling {scaling!r}")
+    if positions < 0 or rotary_dim < 0 or trained_positions < 0:
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, "rotary_table: negative size")
+    t = out.get("table") if out else None
+    if t is None:
+        t = torch.empty(positions, rotary_dim // 2, 2, device=device)
+    _check_cuda(t, "table", torch.float32)
+    if list(t.shape) != [positions, rotary_dim // 2, 2] or not t.is_contiguous():
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, "rotary_table: table must be [positions, rotary_dim / 2, 2], packed")
+    args = RotaryTableArgs(positions=positions, rotary_dim=rotary_dim, base=base, scaling=ROTARY_SCALINGS[scaling],
+                           factor=factor, trained_positions=trained_positions, table=_ptr(t), stream=_stream(stream))
+    raise_for(lib.rotary_table(ctypes.byref(args)), "rotary_table")
+    return dict(table=t)
+
+
+def _rotary_call(verb, tensors, table, positions, gains, d_gains, interleaved, epsilon, workspace, device_status,
+                 stream):
+    """One rotation verb over its two parts.  `tensors`: per part (None: absent) the struct's fields by name."""
+    first = next(iter(tensors[0].values()))
+    _check_cuda(first, "q")
+    if first.dim() != 3:
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: queries must be [rows, heads, head_dim]")
+    dtype, dim, dev = first.dtype, first.shape[2], first.device
+    if dtype not in DTYPES:
+        raise UnsupportedError(CLI_UNSUPPORTED, f"{verb}: {dtype}")
+    _check_cuda(table, "table", torch.float32)
+    if table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous():
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: table must be [positions, rotary_dim / 2, 2], packed")
+    parts = []
+    for p, name in enumerate("qk"):
+        if tensors[p] is None:
+            parts.append(RotaryPartArgs())
+            continue
+        lead = next(iter(tensors[p].values()))
+        if lead.dim() != 3:
+            raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: {name} must be [rows, heads, head_dim]")
+        rows, heads = lead.shape[0], lead.shape[1]
+        pos, gain, d_gain = positions[p], gains[p], d_gains[p]
+        _check_cuda(pos, f"{name} positions", torch.int32)
+        if pos is not None and (pos.numel() != rows or not pos.is_contiguous()):
+            raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: {name} positions must be [{rows}], packed")
+        for g, what in ((gain, "gain"), (d_gain, "d_gain")):
+            _check_cuda(g, f"{name}_{what}", torch.float32)
+            if g is not None and (g.numel() != dim or not g.is_contiguous()):
+                raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: {name}_{what} must be [{dim}], packed")
+        parts.append(RotaryPartArgs(rows=rows, heads=heads, positions=_ptr(pos), gain=_ptr(gain), d_gain=_ptr(d_gain),
+                                    **{f: _heads(t, f"{name}.{f}", rows, heads, dim, dtype)
+                                       for f, t in tensors[p].items()}))
+    st = _status(device_status, dev)
+    ws = workspace
+    if ws is None and (d_gains[0] is not None or d_gains[1] is not None):
+        ws = _ws(lib.norm_rotary_heads_backward_workspace_bytes(dim), dev)
+    args = RotaryArgs(dtype=DTYPES[dtype], interleaved=int(bool(interleaved)), head_dim=dim,
+                      rotary_dim=2 * table.shape[1], table=table.data_ptr(), table_rows=table.shape[0],
+                      epsilon=epsilon, q=parts[0], k=parts[1], workspace=_ptr(ws),
+                      workspace_bytes=0 if ws is None else ws.numel(), device_status=st.data_ptr(),
+                      stream=_stream(stream))
+    raise_for(getattr(lib, verb)(ctypes.byref(args)), verb)
+    return st
+
+
+def rotary_heads(q, table, positions=None, k=None, k_positions=None, interleaved=False, out=None, device_status=None,
+                 stream=None):
+    """Rotates queries [rows, heads, dim] (and keys, of their own rows and heads) by their rows' positions (int32;
+    None: row r is at position r), over the first 2 * table.shape[1] elements of each head.  bf16, fp16 or fp32.
+    Returns dict(q, k, device_status); out['q'] may be `q` itself."""
+    yq, yk = _out(out, "q", q), None if k is None else _out(out, "k", k)
+    st = _rotary_call("rotary_heads", (dict(x=q, y=yq), None if k is None else dict(x=k, y=yk)), table,
+                      (positions, k_positions), (None, None), (None, None), interleaved, 0.0, None, device_status,
+                      stream)
+    return dict(q=yq, k=yk, device_status=st)
+
+
+def rotary_heads_backward(d_q, table, positions=None, d_k=None, k_positions=None, interleaved=False, out=None,
+                          device_status=None, stream=None):
+    """The gradient of rotary_heads for its inputs.  Returns dict(d_q, d_k, device_status)."""
+    xq, xk = _out(out, "d_q", d_q), None if d_k is None else _out(out, "d_k", d_k)
+    st = _rotary_call("rotary_heads_backward",
+                      (dict(d_y=d_q, d_x=xq), None if d_k is None else dict(d_y=d_k, d_x=xk)), table,
+                      (positions, k_positions), (None, None), (None, None), interleaved, 0.0, None, device_status,
+                      stream)
+    return dict(d_q=xq, d_k=xk, device_status=st)
+
+
+def norm_rotary_heads(q, table, positions=None, q_gain=None, k=None, k_positions=None, k_gain=None, interleaved=False,
+                      epsilon=1e-6, out=None, device_status=None, stream=None):
+    """Normalises each head, rotate(gain * x / sqrt(mean(x^2) + epsilon)), of queries and keys in one pass.  Gains
+    are fp32 [dim] (None: ones); the rest as in rotary_heads.  Returns dict(q, k, device_status)."""
+    yq, yk = _out(out, "q", q), None if k is None else _out(out, "k", k)
+    st = _rotary_call("norm_rotary_heads", (dict(x=q, y=yq), None if k is None else dict(x=k, y=yk)), table,
+                      (positions, k_positions), (q_gain, k_gain), (None, None), interleaved, epsilon, None,
+                      device_status, stream)
+    return dict(q=yq, k=yk, device_status=st)
+
+
+def norm_rotary_heads_backward(q, d_q, table, positions=None, q_gain=None, k=None, d_k=None, k_positions=None,
+                               k_gain=None, interleaved=False, epsilon=1e-6, out=None, workspace=None,
+                               device_status=None, stream=None):
+    """The gradients of norm_rotary_heads for its inputs `q`, `k` and its gains, given those of its outputs, `d_q`
+    and `d_k`.  A gain's gradient (fp32 [dim]) is None where the gain is.  Returns dict(d_q, d_q_gain, d_k,
+    d_k_gain, device_status)."""
+    if (k is None) != (d_k is None):
+        raise InvalidArgumentError(CLI_INVALID_ARGUMENT, "norm_rotary_heads_backward: k and d_k go together")
+    xq, xk = _out(out, "d_q", q), None if k is None else _out(out, "d_k", k)
+    gq = None if q_gain is None else _out(out, "d_q_gain", q_gain)
+    gk = None if k is None or k_gain is None else _out(out, "d_k_gain", k_gain)
+    st = _rotary_call("norm_rotary_heads_backward",
+                      (dict(x=q, d_y=d_q, d_x=xq), None if k is None else dict(x=k, d_y=d_k, d_x=xk)), table,
+                      (positions, k_positions), (q_gain, k_gain), (gq, gk), interleaved, epsilon, workspace,
+                      device_status, stream)
+    return dict(d_q=xq, d_q_gain=gq, d_k=xk, d_k_gain=gk, device_status=st)
+
+
+def _attention_args(verb, q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_rows, max_key_rows):
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _check_cuda(t, name, q.dtype)
+        if t.dim() != 3:
+            raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: {name} must be [rows, heads, head_dim]")
+    if q.dtype not in DTYPES:
+        raise UnsupportedError(CLI_UNSUPPORTED, f"{verb}: {q.dtype}")
+    rows_q, hq, dim = q.shape
+    rows_k, hk, _ = k.shape
+    _check_cuda(k_offsets, "k_offsets", torch.int64)
+    _check_cuda(q_offsets, "q_offsets", torch.int64)
+    items = k_offsets.numel() - 1
+    if not k_offsets.is_contiguous() or (q_offsets is not None and (q_offsets.numel() != items + 1 or
+                                                                    not q_offsets.is_contiguous())):
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: offsets must be [items + 1] each, packed")
+    if key_mask is not None:
+        _check_cuda(key_mask, "key_mask")
+        if key_mask.dtype not in (torch.uint8, torch.bool):
+            raise InvalidArgumentError(CLI_INVALID_ARGUMENT, "key_mask must be torch.uint8 or torch.bool")
+        if key_mask.numel() != rows_k or not key_mask.is_contiguous():
+            raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: key_mask must be [{rows_k}], packed")
+    if min(rows_q if max_query_rows is None else max_query_rows, rows_k if max_key_rows is None else max_key_rows) < 0:
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: max_query_rows and max_key_rows must be >= 0")
+    return AttentionArgs(
+        dtype=DTYPES[q.dtype], items=max(items, 0), query_rows=rows_q, key_rows=rows_k, query_offsets=_ptr(q_offsets),
+        key_offsets=k_offsets.data_ptr(), max_query_rows=rows_q if max_query_rows is None else max_query_rows,
+        max_key_rows=rows_k if max_key_rows is None else max_key_rows, query_heads=hq, key_heads=hk, head_dim=dim,
+        scale=dim ** -0.5 if scale is None else scale, key_mask=_ptr(key_mask),
+        q=_heads(q, "q", rows_q, hq, dim, q.dtype), k=_heads(k, "k", rows_k, hk, dim, q.dtype),
+        v=_heads(v, "v", rows_k, hk, dim, q.dtype))
+
+
+def cross_attention(q, q_offsets, k, v, k_offsets, key_mask=None, scale=None, max_query_rows=None, max_key_rows=None,
+                    want_lse=True, out=None, workspace=None, device_status=None, stream=None):
+    """Every query row of `q` [rows, heads, dim] attends to the states `k`, `v` [states, key_heads, dim] of its item
+    on the tapes `q_offsets`, `k_offsets` (int64 [items + 1]).  q_offsets None: all of `q` belongs to every item, and
+    the outputs have items * rows rows.  `key_mask` (uint8 or bool [states]) drops states where it is 0; `scale`
+    defaults to dim^-0.5; the two maxima bound the items' rows (default: the tapes').  bf16 or fp16.  Returns
+    dict(output, lse, device_status), lse fp32 [output rows, heads] or None."""
+    args = _attention_args("cross_attention", q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_rows,
+                           max_key_rows)
+    dev = q.device
+    rows = q.shape[0] if q_offsets is not None else q.shape[0] * args.items
+    o = _out(out, "output", q, rows)
+    args.output = _heads(o, "output", rows, q.shape[1], q.shape[2], q.dtype)
+    lse = None
+    if want_lse:
+        lse = out.get("lse") if out else None
+        if lse is None:
+            lse = torch.empty(rows, q.shape[1], device=dev)
+        _check_lse(lse, rows, q.shape[1], "cross_attention")
+        args.lse = lse.data_ptr()
+    st = _status(device_status, dev)
+    _attention_call("cross_attention", args, workspace, st, dev, stream)
+    return dict(output=o, lse=lse, device_status=st)
+
+
+def _check_lse(lse, rows, heads, verb):
+    _check_cuda(lse, "lse", torch.float32)
+    if list(lse.shape) != [rows, heads] or not lse.is_contiguous():
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: lse must be [{rows}, {heads}], packed")
+
+
+def _attention_call(verb, args, workspace, status, device, stream):
+    ws = workspace
+    if ws is None:
+        need = getattr(lib, verb + "_workspace_bytes")(ctypes.byref(args))
+        ws = _ws(need, device) if need else None
+    args.workspace = _ptr(ws)
+    args.workspace_bytes = 0 if ws is None else ws.numel()
+    args.device_status = status.data_ptr()
+    args.stream = _stream(stream)
+    raise_for(getattr(lib, verb)(ctypes.byref(args)), verb)
+
+
+def cross_attention_backward(q, q_offsets, k, v, k_offsets, output, lse, d_output, key_mask=None, scale=None,
+                             max_query_rows=None, max_key_rows=None, out=None, workspace=None, device_status=None,
+                             stream=None):
+    """The gradients of cross_attention for `q`, `k` and `v`, given its `output` and `lse` and the output's gradient;
+    the rest as there.  Returns dict(d_q, d_k, d_v, device_status)."""
+    verb = "cross_attention_backward"
+    args = _attention_args(verb, q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_rows, max_key_rows)
+    dev, (rows_q, hq, dim), (rows_k, hk, _) = q.device, q.shape, k.shape
+    rows = rows_q if q_offsets is not None else rows_q * args.items
+    _check_lse(lse, rows, hq, verb)
+    dq, dk, dv = _out(out, "d_q", q), _out(out, "d_k", k), _out(out, "d_v", v)
+    args.output = _heads(output, "output", rows, hq, dim, q.dtype)
+    args.lse = lse.data_ptr()
+    args.d_output = _heads(d_output, "d_output", rows, hq, dim, q.dtype)
+    args.d_q = _heads(dq, "d_q", rows_q, hq, dim, q.dtype)
+    args.d_k = _heads(dk, "d_k", rows_k, hk, dim, q.dtype)
+    args.d_v = _heads(dv, "d_v", rows_k, hk, dim, q.dtype)
+    st = _status(device_status, dev)
+    _attention_call(verb, args, workspace, st, dev, stream)
+    return dict(d_q=dq, d_k=dk, d_v=dv, device_status=st)

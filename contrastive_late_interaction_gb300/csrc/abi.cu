@@ -10,24 +10,11 @@
 #include <cmath>
 
 #include "../../include/cli.h"
+#include "abi_checks.h"
 #include "cli_internal.h"
 
 namespace cli {
 namespace {
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void *p, size_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return {a, a + bytes};
-}
-
-bool overlaps(const Range &a, const Range &b) {
-    if (a.lo == a.hi || b.lo == b.hi || a.lo == 0 || b.lo == 0) return false;
-    return a.lo < b.hi && b.lo < a.hi;
-}
 
 // True when any output range overlaps any input range or another output.
 bool any_overlap(const Range *in, int nin, const Range *out, int nout) {
@@ -40,19 +27,10 @@ bool any_overlap(const Range *in, int nin, const Range *out, int nout) {
     return false;
 }
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 // bf16 [rows x cols] with row stride ld (elements), boxes of 64 x 128 with the
 // 128-byte swizzle; out-of-range elements read as zero.
 bool encode_bf16_rows(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t ld) {
     return encode_bf16_tiles(map, base, cols, rows, ld, 64, 128, true);
-}
-
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return n;
 }
 
 bool edges_ok(const cli_edges_t &e) {

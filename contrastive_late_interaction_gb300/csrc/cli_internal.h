@@ -183,4 +183,62 @@ cudaError_t launch_validate_groups(const int32_t *group, int n, int groups, int3
 cudaError_t launch_validate_tape(const uint64_t *offsets, int count, uint64_t rows, int32_t *status,
                                  cudaStream_t stream);
 
+// ----------------------------------------------------------------------------
+// token states (rotary.cu, attention*.cu)
+// ----------------------------------------------------------------------------
+
+// One set of rows of a rotation call.  `in` is what is rotated (x, or d_y in a
+// backward call), `x` the norm's input in its backward.  Strides in elements.
+struct RotaryPartLaunch {
+    int rows, heads;
+    const int32_t *positions;
+    const void *in, *x;
+    void *out;
+    long long in_row, in_head, x_row, x_head, out_row, out_head;
+    const float *gain;
+    float *d_gain, *gain_partials;   // gain_partials: [blocks][head_dim], or NULL
+};
+
+struct RotaryLaunch {
+    int dtype, interleaved, norm, backward;
+    int head_dim, rotary_dim, lph_log2;
+    const float2 *table;
+    int table_rows;
+    float epsilon, inv_dim, sin_sign;
+    RotaryPartLaunch part[2];
+    int32_t *status;
+    int sm_count;
+};
+
+// The most blocks a part's grid has.
+inline int rotary_blocks(int sm_count) { return sm_count * 8; }
+cudaError_t launch_rotary(RotaryLaunch L, cudaStream_t stream);
+cudaError_t launch_rotary_table(float *table, long long positions, int half, const double *frequencies,
+                                double amplitude, cudaStream_t stream);
+
+// Rows of heads as the attention kernels address them, strides in elements.
+struct HeadsView {
+    void *data;
+    long long row, head;
+};
+
+struct AttentionLaunch {
+    int dtype, items, query_rows, key_rows;
+    const uint64_t *q_off, *k_off;   // q_off NULL: every item has all query rows
+    int max_q, max_k;
+    int query_heads, key_heads, group, head_dim;
+    float scale;
+    const uint8_t *key_mask;
+    HeadsView q, k, v, o, d_o, d_q, d_k, d_v;
+    float *lse;
+    uint8_t *workspace;
+    int32_t *status;
+    int sm_count;
+};
+
+size_t attention_workspace(const AttentionLaunch &L);
+size_t attention_backward_workspace(const AttentionLaunch &L);
+cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t stream);
+cudaError_t launch_attention_backward(const AttentionLaunch &L, cudaStream_t stream);
+
 }  // namespace cli

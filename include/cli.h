@@ -449,6 +449,198 @@ cli_status_t maxsim_backward_named(const cli_maxsim_backward_named_t *args);
 #define CLI_MAXSIM_NO_ALLOC_MAX_QUERY_ROWS 262144
 cli_status_t maxsim_backward_no_alloc(const cli_maxsim_backward_t *args);
 
+/* ---------------------------------------------------------------------------
+ * Token states: rotary positions, head norms and cross attention.
+ *
+ * What stands between a tower's token states and the vectors the losses above
+ * score: queries and keys are normalised per head and rotated by their
+ * positions, and a few queries, or the rows of another tape, attend to each
+ * item's states ("UForm": RMSNorm and rotary positions in the tower, one
+ * learned query pooling the per-byte outputs).
+ * ------------------------------------------------------------------------- */
+
+/* Element types of the token-state verbs. */
+typedef enum { CLI_BF16 = 0, CLI_F16 = 1, CLI_F32 = 2 } cli_dtype_t;
+
+/* Rows of several heads in device memory: element i of head h of row r is
+ * data[r * row_stride + h * head_stride + i], strides in elements.  `data` and
+ * both strides are multiples of 16 bytes (a stride that nothing steps over,
+ * one row's or one head's, is not read).  An output's rows and heads may not
+ * overlap one another. */
+typedef struct {
+    void *data;
+    size_t row_stride, head_stride;
+} cli_heads_t;
+
+/*
+ * rotary_table -- the (cos, sin) pairs that the rotation verbs read.
+ *
+ *     table[p][i] = amplitude * (cos, sin)(p * f_i),  i < rotary_dim / 2,
+ *
+ * with f_i = base^(-2 i / rotary_dim) stretched for contexts `factor` times
+ * the one a model was trained at (angles in 64 bits, rounded once):
+ *   CLI_ROTARY_PLAIN    f_i as it is, amplitude 1
+ *   CLI_ROTARY_LINEAR   f_i / factor
+ *   CLI_ROTARY_NTK      base * factor^(rotary_dim / (rotary_dim - 2)) in the
+ *                       place of base: the fastest pair keeps its angle, the
+ *                       slowest turns 1 / factor as fast (rotary_dim > 2)
+ *   CLI_ROTARY_YARN     pairs that turn more than 32 times over
+ *                       `trained_positions` keep f_i, those that turn less
+ *                       than once take f_i / factor, those between them a
+ *                       blend linear in i; amplitude 0.1 ln(factor) + 1
+ *                       (Peng, Quesnelle, Fan, Shippole 2023)
+ *
+ *   positions      rows of the table, 1 .. 2^31 - 1
+ *   rotary_dim     even, 2 .. 256
+ *   base           > 1; factor >= 1; trained_positions >= 1 (YARN alone reads it)
+ *   table          device fp32 [positions][rotary_dim / 2][2] (written), 16-byte aligned
+ */
+enum { CLI_ROTARY_PLAIN = 0, CLI_ROTARY_LINEAR = 1, CLI_ROTARY_NTK = 2, CLI_ROTARY_YARN = 3 };
+typedef struct {
+    size_t positions, rotary_dim;
+    double base;
+    int scaling;
+    double factor;
+    size_t trained_positions;
+    float *table;
+    void *stream;
+} cli_rotary_table_t;
+
+cli_status_t rotary_table(const cli_rotary_table_t *args);
+
+/*
+ * rotary_heads -- rotates each head of each row by the row's position:
+ *     y_a = x_a cos - x_b sin,   y_b = x_b cos + x_a sin
+ * for the pairs (a, b) = (i, i + rotary_dim / 2), or (2 i, 2 i + 1) where
+ * `interleaved`, i < rotary_dim / 2; the rest of the head is copied.
+ * rotary_heads_backward -- its gradient, the transposed rotation of d_y.
+ * norm_rotary_heads -- the same after a norm of each head:
+ *     y = rotate(gain * x / sqrt(mean(x^2) + epsilon)).
+ * norm_rotary_heads_backward -- the gradients of that for x and the gain:
+ * with dz = d_y rotated back, n = x / sqrt(mean(x^2) + epsilon), t = gain dz:
+ *     d_x = (t - n mean(t n)) / sqrt(mean(x^2) + epsilon),
+ *     d_gain = sum over rows and heads of dz n.
+ * Each takes two sets of rows, queries and keys, in one pass; `k` is absent
+ * where its heads are 0.  Arithmetic is in 32 bits, rounded once at the end;
+ * d_gain is summed in a fixed order and is bit-reproducible.
+ *
+ *   dtype           of x, y, d_y and d_x: CLI_BF16, CLI_F16 or CLI_F32
+ *   head_dim        a multiple of 8, 8 .. 256
+ *   rotary_dim      even, 2 .. head_dim
+ *   table           device fp32 [table_rows][rotary_dim / 2][2] from
+ *                   rotary_table, 8-byte aligned
+ *   epsilon         > 0 (the norm verbs)
+ *   rows, heads     of a part; rows < 2^31 (0 is a call on no rows), heads at most 65535
+ *   positions       device int32 [rows], row r's position; NULL: r itself.  One
+ *                   outside [0, table_rows) sets CLI_MALFORMED
+ *   x, y, d_y, d_x  rotary_heads reads x and writes y; rotary_heads_backward
+ *                   reads d_y and writes d_x; norm_rotary_heads reads x and
+ *                   writes y; norm_rotary_heads_backward reads x and d_y and
+ *                   writes d_x.  The output may be an input in place: the same
+ *                   data and strides
+ *   gain, d_gain    device fp32 [head_dim] (the norm verbs); gain NULL: ones;
+ *                   d_gain NULL: not wanted
+ *   workspace       norm_rotary_heads_backward with a d_gain alone: device, >=
+ *                   norm_rotary_heads_backward_workspace_bytes(head_dim),
+ *                   256-byte aligned; contents on entry are ignored
+ *   device_status   device int32 (written: 0 or a cli_status_t)
+ */
+typedef struct {
+    size_t rows, heads;
+    const int32_t *positions;
+    cli_heads_t x, y, d_y, d_x;
+    const float *gain;
+    float *d_gain;
+} cli_rotary_part_t;
+
+typedef struct {
+    int dtype;
+    int interleaved;
+    size_t head_dim, rotary_dim;
+    const float *table;
+    size_t table_rows;
+    float epsilon;
+    cli_rotary_part_t q, k;
+    void *workspace;
+    size_t workspace_bytes;
+    int32_t *device_status;
+    void *stream;
+} cli_rotary_t;
+
+cli_status_t rotary_heads(const cli_rotary_t *args);
+cli_status_t rotary_heads_backward(const cli_rotary_t *args);
+cli_status_t norm_rotary_heads(const cli_rotary_t *args);
+cli_status_t norm_rotary_heads_backward(const cli_rotary_t *args);
+size_t norm_rotary_heads_backward_workspace_bytes(size_t head_dim);
+
+/*
+ * cross_attention -- every query row attends to its item's states:
+ *     S = scale q k^T,  P = softmax of S over the item's kept states,
+ *     O = P v,  lse = log sum exp S,
+ * and cross_attention_backward, its gradients: with D = rowsum(dO * O),
+ *     dV = P^T dO,  dS = P * (dO v^T - D),  dQ = scale dS k,  dK = scale dS^T q.
+ * Query head h reads key head h / (query_heads / key_heads).
+ *
+ * Queries and states lie on tapes, item after item: item i's rows are
+ * offsets[i] .. offsets[i + 1] - 1.  With query_offsets NULL all query_rows
+ * queries belong to every item (learned pooling queries): outputs, lse and
+ * d_output then have items * query_rows rows, item after item, and dQ sums
+ * over the items.  An item may have no queries or no states; a row with no
+ * kept state has output 0 and lse -infinity, and passes no gradient.
+ *
+ *   dtype            of every matrix: CLI_BF16 or CLI_F16
+ *   head_dim         a multiple of 8, 8 .. 128
+ *   query_heads      a multiple of key_heads, at most 128 times it; both
+ *                    1 .. 65535
+ *   items            1 .. 2^31 - 1
+ *   query_rows, key_rows   rows of the tapes, < 2^31 (key_rows may be 0, as may
+ *                    query_rows); outputs' rows < 2^31 too
+ *   query_offsets, key_offsets   device uint64 [items + 1]; malformed ones set
+ *                    CLI_MALFORMED, as does an item longer than the two below
+ *   max_query_rows, max_key_rows   at least the longest item's rows: they choose
+ *                    the kernel and the split of long items (the tape's rows
+ *                    always do)
+ *   key_mask         device uint8 [key_rows], 0 drops a state (its k and v may
+ *                    hold anything, NaN included); NULL keeps all
+ *   scale            finite
+ *   q, k, v          row strides of at least head_dim; see cli_heads_t
+ *   output           written by the forward, read by the backward
+ *   lse              device fp32 [output rows][query_heads], packed; written by
+ *                    the forward (NULL: not wanted), read by the backward
+ *   d_output         read by the backward
+ *   d_q, d_k, d_v    written by the backward: the inputs' type, sums in 32 bits
+ *                    rounded once; zeros for dropped states
+ *   workspace        device, >= the verb's *_workspace_bytes of the same
+ *                    arguments (which reads the sizes alone), 256-byte aligned;
+ *                    contents on entry are ignored; may be NULL where that is 0
+ *   device_status    device int32 (written: 0 or a cli_status_t)
+ *
+ * P and dS are rounded to `dtype` as operands of the tensor cores; everything
+ * else between input and output is in 32 bits.  Results are bit-reproducible:
+ * no sum depends on the order in which blocks run.
+ */
+typedef struct {
+    int dtype;
+    size_t items, query_rows, key_rows;
+    const uint64_t *query_offsets, *key_offsets;
+    size_t max_query_rows, max_key_rows;
+    size_t query_heads, key_heads, head_dim;
+    float scale;
+    const uint8_t *key_mask;
+    cli_heads_t q, k, v, output;
+    float *lse;
+    cli_heads_t d_output, d_q, d_k, d_v;
+    void *workspace;
+    size_t workspace_bytes;
+    int32_t *device_status;
+    void *stream;
+} cli_attention_t;
+
+cli_status_t cross_attention(const cli_attention_t *args);
+size_t cross_attention_workspace_bytes(const cli_attention_t *args);
+cli_status_t cross_attention_backward(const cli_attention_t *args);
+size_t cross_attention_backward_workspace_bytes(const cli_attention_t *args);
+
 /*
  * cli_selftest_bounded_wait -- runs the failure path of the kernels' bounded
  * waits, faulting nothing.  Every wait of the tensor-core kernels gives up
