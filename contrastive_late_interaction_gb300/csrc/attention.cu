@@ -53,7 +53,8 @@ __device__ __forceinline__ int item_of(const uint64_t *off, int items, int row) 
 
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) forward_kernel(const __grid_constant__ AttentionLaunch L, int out_rows) {
-    check_items(L);
+    check_items(L, (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
+                static_cast<long long>(gridDim.x) * gridDim.y * blockDim.x);
     const int row = blockIdx.x * kWarps + (threadIdx.x >> 5), h = blockIdx.y;
     if (row >= out_rows) return;
     const int i = L.q_off ? item_of(L.q_off, L.items, row) : row / L.query_rows;
@@ -84,7 +85,8 @@ __global__ void __launch_bounds__(kWarps * 32) forward_kernel(const __grid_const
 
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) dq_kernel(const __grid_constant__ AttentionLaunch L) {
-    check_items(L);
+    check_items(L, (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
+                static_cast<long long>(gridDim.x) * gridDim.y * blockDim.x);
     const int row = blockIdx.x * kWarps + (threadIdx.x >> 5), h = blockIdx.y;
     if (row >= L.query_rows) return;
     const int kh = h / L.group;
@@ -116,7 +118,8 @@ __global__ void __launch_bounds__(kWarps * 32) dq_kernel(const __grid_constant__
 
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) dkv_kernel(const __grid_constant__ AttentionLaunch L) {
-    check_items(L);
+    check_items(L, (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
+                static_cast<long long>(gridDim.x) * gridDim.y * blockDim.x);
     const int j = blockIdx.x * kWarps + (threadIdx.x >> 5), kh = blockIdx.y;
     if (j >= L.key_rows) return;
     const Item t = load_item(L, item_of(L.k_off, L.items, j));
@@ -165,6 +168,7 @@ size_t attention_workspace(const AttentionLaunch &) { return 0; }
 size_t attention_backward_workspace(const AttentionLaunch &) { return 0; }
 
 cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t stream) {
+    if (L.query_rows && L.key_rows) return attn::launch_forward_tiles(L, stream);
     if (L.dtype == CLI_BF16) attn::forward<__nv_bfloat16>(L, stream); else attn::forward<__half>(L, stream);
     return cudaGetLastError();
 }

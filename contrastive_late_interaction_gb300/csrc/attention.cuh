@@ -1,9 +1,11 @@
-// What the attention kernels share: the tapes' items and the element types.
+// What the attention kernels share: the tapes' items, the element types and
+// the pieces of their tensor-core pipelines.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "cli_device.cuh"
@@ -11,6 +13,8 @@
 
 namespace cli {
 namespace attn {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // One item's rows on the tapes.  With shared queries q0 is 0 for every item,
 // and its outputs start at o0.
@@ -45,13 +49,104 @@ __device__ __forceinline__ Item load_item(const AttentionLaunch &L, int i) {
     return t;
 }
 
-// Checks every item's offsets, the grid's threads sharing the items: kernels
-// that reach items through their rows would not see all of a malformed tape.
-__device__ __forceinline__ void check_items(const AttentionLaunch &L) {
-    const long long threads = static_cast<long long>(gridDim.x) * gridDim.y * blockDim.x;
-    for (long long i = (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x;
-         i < L.items; i += threads)
-        load_item(L, static_cast<int>(i));
+// Checks every item's offsets, `threads` threads of the grid sharing them:
+// kernels that reach items through their rows would not see all of a
+// malformed tape.
+__device__ __forceinline__ void check_items(const AttentionLaunch &L, long long thread, long long threads) {
+    for (long long i = thread; i < L.items; i += threads) load_item(L, static_cast<int>(i));
+}
+
+// Rows of a tape are worked on in blocks of `span` rows that start at each
+// item's first row.  Block slot x belongs to the item i with
+//     first(i) <= x < first(i + 1),   first(i) = offsets[i] / span + i,
+// and is its block x - first(i): an item of n rows has ceil(n / span) blocks
+// and at least that many slots, since floor((o + n) / span) - floor(o / span)
+// + 1 >= ceil(n / span); at most one slot per item stays empty.  So the slots
+// (rows / span + items of them) need no table and no scan: a warp finds the
+// item by a 32-way search over the offsets.
+__device__ __forceinline__ int find_item(const uint64_t *off, int items, unsigned span, long long x, int lane) {
+    int lo = 0, n = items;   // the item is one of lo .. lo + n - 1
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int at = lo + lane * step;
+        const bool le = lane * step < n && static_cast<long long>(off[at] / span) + at <= x;
+        const unsigned hits = __ballot_sync(0xffffffffu, le);
+        const int k = hits ? 31 - __clz(hits) : 0;
+        const int left = n - k * step;
+        lo += k * step;
+        n = left < step ? left : step;
+    }
+    return lo;
+}
+
+template <typename T> struct Type;
+template <> struct Type<__nv_bfloat16> {
+    static constexpr bool bf16 = true;
+    static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_bf16x2(a, b); }
+    static __device__ __forceinline__ float2 unpack(uint32_t v) {
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    }
+};
+template <> struct Type<__half> {
+    static constexpr bool bf16 = false;
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t v) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+    }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Word w of the kept-states mask of a block of which the first n are there.
+__device__ __forceinline__ uint32_t first_bits(int n, int w) {
+    const int left = n - 32 * w;
+    return left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+}
+
+__device__ __forceinline__ uint32_t round16(int n) { return static_cast<uint32_t>((n + 15) & ~15); }
+
+// Shared-memory tiles: rows of 64 elements (128 bytes, 128-byte swizzle), one
+// box of kBoxBytes per 64 elements of the head.
+constexpr uint32_t kTileRows = 128;
+constexpr uint32_t kBoxBytes = kTileRows * 128;
+
+// D (+)= A B^T over `dim` elements, A and B K-major tiles of rows of heads.
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, int dim) {
+    const int steps = (dim + 15) / 16;
+    for (int k = 0; k < steps; ++k) {
+        const uint32_t at = (k >> 2) * kBoxBytes + (k & 3) * 32;
+        mma_bf16(d, sdesc_sw128(a + at, 16, 1024), sdesc_sw128(b + at, 16, 1024), idesc, k != 0);
+    }
+}
+
+// D (+)= A B over `rows` rows of B, A in TMEM (16-bit pairs), B a tile of rows
+// of heads read MN-major.
+__device__ __forceinline__ void mma_pairs(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, int rows,
+                                          bool accumulate) {
+    const int steps = (rows + 15) / 16;
+    for (int k = 0; k < steps; ++k)
+        mma_ts(d, a + k * 8, sdesc_sw128(b + k * 2048, kBoxBytes, 1024), idesc, accumulate || k != 0);
+}
+
+// Zeroes rows of a tile of `boxes` boxes: those of the first `rows` whose bit
+// in `keep` (one word per 32 rows) is 0.  One warp.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int boxes, int rows, const uint32_t (&keep)[4], int lane) {
+    const int sub = lane >> 3, chunk = lane & 7;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if (32 * w >= rows || keep[w] == 0xffffffffu) continue;
+        for (int r = sub; r < 32 && 32 * w + r < rows; r += 4)
+            if (!((keep[w] >> r) & 1u))
+                for (int x = 0; x < boxes; ++x)
+                    st_shared_v4(tile + x * kBoxBytes + (32 * w + r) * 128 + chunk * 16, 0, 0, 0, 0);
+    }
 }
 
 }  // namespace attn

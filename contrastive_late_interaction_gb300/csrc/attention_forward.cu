@@ -1,0 +1,442 @@
+// Cross attention over tapes: the tensor-core forward.
+//
+// Mathematics.  For a query row with scores s_j = scale <q, k_j>:
+//     m = max s_j,  p_j = exp(s_j - m),  l = sum p_j,
+//     output = sum p_j v_j / l,  lse = m + ln l,
+// in one pass over the states: m, l and the output accumulator are kept
+// running, and when the maximum grows the earlier sums are scaled by exp of
+// the difference.  Any reference value serves in the place of m as long as
+// nothing overflows, so the accumulator is rescaled only when the maximum has
+// grown by more than a factor of 2^8 over the reference: rarely after an
+// item's first block.
+//
+// Work.  A tile is 128 rows of (query row, head of the group): the heads that
+// share a key head are packed next to one another, so K and V are read once
+// for all of them.  A CTA takes two tiles at a time against blocks of 128
+// states, one persistent CTA per SM.  Warp roles:
+//   0      finds the next pair of tiles (find_item) and issues the TMA loads:
+//          Q, and K and V blocks through a ring of four stages;
+//   1      issues the products: S = Q K^T into TMEM, then O += P V with P read
+//          from TMEM, alternating between the two tiles so that one tile's
+//          softmax runs under the other's products;
+//   2      makes V blocks safe: rows past the item's end and dropped rows are
+//          zeroed (0 x NaN would reach the output through the product), and
+//          the dropped states' bits are gathered;
+//   3      checks the offsets of every item;
+//   4..11  softmax, four warps a tile, one row a thread: S from TMEM, P back
+//          over the same columns, and at the end O / l to global memory.
+// TMEM: S0 | S1 | O0 | O1, 128 columns each.
+
+#include <cuda.h>
+
+#include "attention.cuh"
+
+namespace cli {
+namespace attn {
+namespace {
+
+constexpr int kStages = 4;   // even: K blocks in the even stages, V blocks in the odd ones
+constexpr int kThreads = 384;
+constexpr int kBits = 4;
+constexpr int kReaders = 10;   // of a published pair: warp 1, warp 2, eight softmax warps
+
+struct Pair {
+    int q0, o0, rows, k0, nk, head;   // rows < 0: no more work
+};
+
+template <int BOXES>
+struct Storage {
+    alignas(1024) uint8_t q[2][BOXES * kBoxBytes];
+    alignas(1024) uint8_t kv[kStages][BOXES * kBoxBytes];
+    uint32_t bits[kBits][4];
+    Pair pair[2];
+    uint64_t pair_full[2], pair_empty[2];
+    uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages], v_ready[kStages], bits_full[kBits];
+    uint64_t s_full[2], p_ready[2], o_full[2], done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+template <typename T, int BOXES>
+__global__ void __launch_bounds__(kThreads, 1)
+    forward_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
+                   long long slots, long long tiles) {
+    extern __shared__ uint8_t smem_raw[];
+    using Smem = Storage<BOXES>;
+    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.pair_full[i], 1);
+            mbar_init(&sm.pair_empty[i], kReaders);
+            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_empty[i], 1);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_ready[i], 4);
+            mbar_init(&sm.o_full[i], 1);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sm.kv_full[i], 1);
+            mbar_init(&sm.kv_empty[i], 1);
+            mbar_init(&sm.v_ready[i], 1);
+        }
+        for (int i = 0; i < kBits; ++i) mbar_init(&sm.bits_full[i], 1);
+        mbar_init(&sm.done, 1);
+        sm.abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&M.q);
+        prefetch_tmap(&M.k);
+        prefetch_tmap(&M.v);
+    }
+    if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    volatile int *abort_flag = &sm.abort_flag;
+    const int group = L.group, dim = L.head_dim, span = 2 * rows_per_tile;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, L.status); };
+    // The next published pair, for a reader; false where there is none or the CTA gave up.
+    auto next_pair = [&](uint32_t it, Pair &p) {
+        if (!wait(&sm.pair_full[it & 1], (it >> 1) & 1)) return false;
+        p = sm.pair[it & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.pair_empty[it & 1]);
+        return p.rows >= 0;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ work and TMA
+        uint32_t it = 0, entry = 0, q_phase = 0;
+        bool ok = true;
+        const uint32_t q_bytes = BOXES * static_cast<uint32_t>(rows_per_tile * group) * 128u;
+        const int per_item = L.q_off ? 0 : (L.query_rows + span - 1) / span;
+        for (long long id = blockIdx.x; ok; id += gridDim.x) {
+            Pair p = {0, 0, -1, 0, 0, 0};
+            if (id < tiles) {
+                const long long x = id % slots;
+                int i;
+                long long block;
+                if (L.q_off) {
+                    i = find_item(L.q_off, L.items, span, x, lane);
+                    block = x - (static_cast<long long>(L.q_off[i] / span) + i);
+                } else {
+                    i = static_cast<int>(x / per_item);
+                    block = x - static_cast<long long>(i) * per_item;
+                }
+                const Item t = load_item(L, i);
+                if (!t.ok || block < 0 || block * span >= t.nq) continue;   // an empty slot
+                const int r0 = static_cast<int>(block) * span;
+                p = {t.q0 + r0, t.o0 + r0, min(span, t.nq - r0), t.k0, t.nk, static_cast<int>(id / slots)};
+            }
+            if (!wait(&sm.pair_empty[it & 1], ((it >> 1) & 1) ^ 1)) break;
+            if (lane == 0) {
+                sm.pair[it & 1] = p;
+                mbar_arrive(&sm.pair_full[it & 1]);
+            }
+            ++it;
+            if (p.rows < 0) break;
+            const int blocks = (p.nk + 127) / 128, nt = p.rows > rows_per_tile ? 2 : 1;
+            if (lane == 0 && blocks) {
+                auto load = [&](uint8_t *dst, const CUtensorMap *map, uint64_t *bar, int head, int row) {
+#pragma unroll
+                    for (int b = 0; b < BOXES; ++b) tma_load_3d(dst + b * kBoxBytes, map, bar, 64 * b, head, row);
+                };
+                auto load_q = [&](int t) {
+                    if (!wait(&sm.q_empty[t], ((q_phase >> t) & 1) ^ 1)) return false;
+                    q_phase ^= 1u << t;
+                    mbar_arrive_expect_tx(&sm.q_full[t], q_bytes);
+                    load(sm.q[t], &M.q, &sm.q_full[t], p.head * group, p.q0 + t * rows_per_tile);
+                    return true;
+                };
+                auto load_kv = [&](const CUtensorMap *map, int j) {
+                    const uint32_t s = entry % kStages;
+                    if (!wait(&sm.kv_empty[s], ((entry / kStages) & 1) ^ 1)) return false;
+                    mbar_arrive_expect_tx(&sm.kv_full[s], BOXES * kBoxBytes);
+                    load(sm.kv[s], map, &sm.kv_full[s], p.head, p.k0 + 128 * j);
+                    ++entry;
+                    return true;
+                };
+                ok = load_q(0) && load_kv(&M.k, 0) && (nt == 1 || load_q(1)) && load_kv(&M.v, 0);
+                for (int j = 1; j < blocks && ok; ++j) ok = load_kv(&M.k, j) && load_kv(&M.v, j);
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        // Let the loads in flight land before the CTA can exit.
+        if (lane == 0)
+            for (int s = 0; s < kStages; ++s) {
+                // the last use of stage s: entry - 1 - ((entry - 1 - s) mod kStages), where there is one
+                if (entry > static_cast<uint32_t>(s)) {
+                    const uint32_t last = (entry - 1 - s) / kStages;
+                    wait(&sm.kv_empty[s], last & 1);
+                }
+            }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ products
+        const uint32_t idesc_s = idesc_16bit(Type<T>::bf16, 128, 0, 0, 0);   // N by block
+        const uint32_t idesc_o = idesc_16bit(Type<T>::bf16, 128, round16(dim), 0, 1);
+        uint32_t entry = 0, q_phase = 0, p_phase = 0;
+        bool ok = true;
+        Pair p;
+        for (uint32_t it = 0; ok && next_pair(it, p); ++it) {
+            const int blocks = (p.nk + 127) / 128, nt = p.rows > rows_per_tile ? 2 : 1;
+            if (lane == 0 && blocks) {
+                auto scores = [&](int t, int j, uint32_t e) {
+                    const uint32_t n = round16(min(128, p.nk - 128 * j));
+                    mma_rows(tmem + t * 128, smem_u32(sm.q[t]), smem_u32(sm.kv[e % kStages]), idesc_s | (n >> 3) << 17, dim);
+                    mma_commit(&sm.s_full[t]);
+                    if (j + 1 == blocks) mma_commit(&sm.q_empty[t]);
+                };
+                ok = wait(&sm.kv_full[entry % kStages], (entry / kStages) & 1);
+                for (int t = 0; t < nt && ok; ++t) {
+                    ok = wait(&sm.q_full[t], (q_phase >> t) & 1);
+                    if (!ok) break;
+                    q_phase ^= 1u << t;
+                    tc_fence_after();
+                    scores(t, 0, entry);
+                }
+                if (ok) mma_commit(&sm.kv_empty[entry % kStages]);
+                for (int j = 0; j < blocks && ok; ++j) {
+                    const uint32_t ev = entry + 2 * j + 1, ek = ev + 1;
+                    ok = wait(&sm.v_ready[ev % kStages], (ev / kStages) & 1);
+                    for (int t = 0; t < nt && ok; ++t) {
+                        if (!wait(&sm.p_ready[t], (p_phase >> t) & 1)) { ok = false; break; }
+                        p_phase ^= 1u << t;
+                        tc_fence_after();
+                        mma_pairs(tmem + 256 + t * 128, tmem + t * 128, smem_u32(sm.kv[ev % kStages]), idesc_o,
+                                  min(128, p.nk - 128 * j), j != 0);
+                        if (j + 1 == blocks) {
+                            mma_commit(&sm.o_full[t]);
+                        } else {
+                            if (t == 0 && !wait(&sm.kv_full[ek % kStages], (ek / kStages) & 1)) { ok = false; break; }
+                            tc_fence_after();
+                            scores(t, j + 1, ek);
+                        }
+                    }
+                    if (!ok) break;
+                    mma_commit(&sm.kv_empty[ev % kStages]);
+                    if (j + 1 < blocks) mma_commit(&sm.kv_empty[ek % kStages]);
+                }
+                entry += 2 * blocks;
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        if (lane == 0) {
+            mma_commit(&sm.done);
+            wait(&sm.done, 0);
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ V blocks made safe, dropped states
+        uint32_t entry = 0, block = 0;
+        bool ok = true;
+        Pair p;
+        for (uint32_t it = 0; ok && next_pair(it, p); ++it) {
+            const int blocks = (p.nk + 127) / 128;
+            for (int j = 0; j < blocks && ok; ++j, ++block, entry += 2) {
+                const int n = min(128, p.nk - 128 * j);
+                uint32_t keep[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int at = 32 * w + lane;
+                    keep[w] = first_bits(n, w);
+                    if (L.key_mask)
+                        keep[w] = __ballot_sync(0xffffffffu, at < n && L.key_mask[p.k0 + 128 * j + at] != 0);
+                }
+                if (L.key_mask) {
+                    if (lane == 0) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) sm.bits[block % kBits][w] = keep[w];
+                        mbar_arrive(&sm.bits_full[block % kBits]);
+                    }
+                }
+                const uint32_t e = entry + 1, s = e % kStages;
+                if (!wait(&sm.kv_full[s], (e / kStages) & 1)) { ok = false; break; }
+                zero_rows(smem_u32(sm.kv[s]), BOXES, round16(n), keep, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.v_ready[s]);
+            }
+        }
+    } else if (warp == 3) {
+        check_items(L, static_cast<long long>(blockIdx.x) * 32 + lane, static_cast<long long>(gridDim.x) * 32);
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int t = (warp - 4) >> 2, quad = warp & 3, m_row = quad * 32 + lane;
+        const int r_in = m_row / group, head_in = m_row - r_in * group;
+        const bool in_tile = r_in < rows_per_tile;
+        const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * 128;
+        const float sl2 = fmaxf(fabsf(L.scale) * kLog2e, 1e-30f);   // above 0, so that -infinity stays that
+        const float sign = L.scale < 0.0f ? -1.0f : 1.0f;
+        const float lazy = 8.0f / sl2;   // in units of a raw score
+        const float2 sl22 = make_float2(sl2, sl2);
+        uint32_t phase = 0, o_phase = 0, block = 0;
+        bool ok = true;
+        Pair p;
+        for (uint32_t it = 0; ok && next_pair(it, p); ++it) {
+            const int blocks = (p.nk + 127) / 128;
+            if (t * rows_per_tile >= p.rows) {
+                block += blocks;
+                continue;
+            }
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < blocks; ++j, ++block) {
+                if (!wait(&sm.s_full[t], phase)) { ok = false; break; }
+                phase ^= 1;
+                tc_fence_after();
+                const int n = min(128, p.nk - 128 * j);
+                uint32_t r[4][32];
+                float top;
+                if (n == 128 && !L.key_mask && sign > 0.0f) {
+                    float t0, t1, t2, t3;
+                    tmem_ld32_max_async(s_at, r[0], t0);
+                    tmem_ld32_max_async(s_at + 32, r[1], t1);
+                    tmem_ld32_max_async(s_at + 64, r[2], t2);
+                    tmem_ld32_max_async(s_at + 96, r[3], t3);
+                    tmem_wait_ld();
+                    tmem_regs_ready(r[0], t0);
+                    tmem_regs_ready(r[1], t1);
+                    tmem_regs_ready(r[2], t2);
+                    tmem_regs_ready(r[3], t3);
+                    top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+                } else {
+                    if (L.key_mask && !wait(&sm.bits_full[block % kBits], (block / kBits) & 1)) { ok = false; break; }
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) tmem_ld32_async(s_at + 32 * w, r[w]);
+                    tmem_wait_ld();
+                    top = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        tmem_regs_ready(r[w]);
+                        const uint32_t keep = L.key_mask ? sm.bits[block % kBits][w] : first_bits(n, w);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float v = (keep >> i) & 1u ? sign * __uint_as_float(r[w][i]) : -INFINITY;
+                            r[w][i] = __float_as_uint(v);
+                            top = fmaxf(top, v);
+                        }
+                    }
+                }
+                // The reference follows the maximum only when that has grown past 2^8.
+                if (__any_sync(0xffffffffu, top > m + lazy || (m == -INFINITY && top > m))) {
+                    const float m1 = fmaxf(m, top);
+                    const float c = m1 > m ? ex2((m - m1) * sl2) : 1.0f;
+                    m = m1;
+                    l *= c;
+                    if (j > 0) {   // S of this block is ready, so the product before it is done
+#pragma unroll 1
+                        for (int x = 0; x < BOXES * 64; x += 16) {
+                            uint32_t o[16];
+                            tmem_ld16_async(o_at + x, o);
+                            tmem_wait_ld();
+                            tmem_regs_ready_n(o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
+                            tmem_st16(o_at + x, o);
+                            tmem_wait_st();
+                        }
+                    }
+                }
+                const float shift = m == -INFINITY ? 0.0f : -m * sl2;
+                const float2 shift2 = make_float2(shift, shift);
+                float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t packed[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        float2 a = __ffma2_rn(make_float2(__uint_as_float(r[w][i]), __uint_as_float(r[w][i + 1])), sl22, shift2);
+                        float2 b = __ffma2_rn(make_float2(__uint_as_float(r[w][i + 2]), __uint_as_float(r[w][i + 3])), sl22, shift2);
+                        a = make_float2(ex2(a.x), ex2(a.y));
+                        b = make_float2(ex2(b.x), ex2(b.y));
+                        sum = __fadd2_rn(sum, a);
+                        sum1 = __fadd2_rn(sum1, b);
+                        packed[i / 2] = Type<T>::pack(a.x, a.y);
+                        packed[i / 2 + 1] = Type<T>::pack(b.x, b.y);
+                    }
+                    tmem_st16(s_at + 16 * w, packed);
+                }
+                l += (sum.x + sum1.x) + (sum.y + sum1.y);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_ready[t]);
+            }
+            if (!ok) break;
+            if (blocks) {
+                if (!wait(&sm.o_full[t], o_phase)) break;
+                o_phase ^= 1;
+                tc_fence_after();
+            }
+            const int row = t * rows_per_tile + r_in, head = p.head * group + head_in;
+            const bool mine = in_tile && row < p.rows;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // no kept state: zero
+            T *out = static_cast<T *>(L.o.data) + (static_cast<long long>(p.o0) + row) * L.o.row + head * L.o.head;
+#pragma unroll 1
+            for (int x = 0; x < dim; x += 16) {
+                uint32_t o[16];
+                if (blocks) {
+                    tmem_ld16_async(o_at + x, o);
+                    tmem_wait_ld();
+                    tmem_regs_ready_n(o);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!mine || x + 8 * h >= dim) continue;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = l == 0.0f ? 0u
+                                         : Type<T>::pack(__uint_as_float(o[8 * h + 2 * i]) * inv,
+                                                         __uint_as_float(o[8 * h + 2 * i + 1]) * inv);
+                    *reinterpret_cast<uint4 *>(out + x + 8 * h) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            if (L.lse && mine)
+                L.lse[(static_cast<long long>(p.o0) + row) * L.query_heads + head] =
+                    l == 0.0f ? -INFINITY : m * (sl2 * kLn2) + logf(l);
+            tc_fence_before();
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <typename T, int BOXES>
+cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
+    const int rows_per_tile = 128 / L.group;
+    const long long span = 2 * rows_per_tile;
+    const long long slots = L.q_off ? L.query_rows / span + L.items
+                                    : static_cast<long long>(L.items) * ((L.query_rows + span - 1) / span);
+    const long long tiles = slots * L.key_heads;
+    Maps M;
+    const bool bf16 = Type<T>::bf16;
+    if (!encode_heads_tiles(&M.q, L.q, bf16, L.head_dim, L.query_heads, L.query_rows, L.group, rows_per_tile) ||
+        !encode_heads_tiles(&M.k, L.k, bf16, L.head_dim, L.key_heads, L.key_rows, 1, kTileRows) ||
+        !encode_heads_tiles(&M.v, L.v, bf16, L.head_dim, L.key_heads, L.key_rows, 1, kTileRows))
+        return cudaErrorInvalidValue;
+    const size_t smem = sizeof(Storage<BOXES>) + 1024;
+    auto kernel = forward_kernel<T, BOXES>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(tiles < L.sm_count ? tiles : L.sm_count);
+    kernel<<<grid, kThreads, smem, stream>>>(L, M, rows_per_tile, slots, tiles);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Needs at least one query row and one state (the tensor maps have no empty form).
+cudaError_t launch_forward_tiles(const AttentionLaunch &L, cudaStream_t stream) {
+    const bool wide = L.head_dim > 64;
+    if (L.dtype == CLI_BF16) return wide ? launch<__nv_bfloat16, 2>(L, stream) : launch<__nv_bfloat16, 1>(L, stream);
+    return wide ? launch<__half, 2>(L, stream) : launch<__half, 1>(L, stream);
+}
+
+}  // namespace attn
+}  // namespace cli

@@ -222,6 +222,12 @@ struct HeadsView {
     long long row, head;
 };
 
+// A map of 16-bit rows of heads [rows][heads][dim], boxes of 64 elements x
+// box_heads x box_rows with the 128-byte swizzle; elements past the head, the
+// heads or the rows read as zero.
+bool encode_heads_tiles(CUtensorMap *map, const HeadsView &v, bool bf16, uint64_t dim, uint64_t heads, uint64_t rows,
+                        uint32_t box_heads, uint32_t box_rows);
+
 struct AttentionLaunch {
     int dtype, items, query_rows, key_rows;
     const uint64_t *q_off, *k_off;   // q_off NULL: every item has all query rows
@@ -238,6 +244,9 @@ struct AttentionLaunch {
 
 size_t attention_workspace(const AttentionLaunch &L);
 size_t attention_backward_workspace(const AttentionLaunch &L);
+namespace attn {
+cudaError_t launch_forward_tiles(const AttentionLaunch &L, cudaStream_t stream);
+}
 cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t stream);
 cudaError_t launch_attention_backward(const AttentionLaunch &L, cudaStream_t stream);
 

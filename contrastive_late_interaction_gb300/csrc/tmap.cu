@@ -36,4 +36,21 @@ bool encode_bf16_tiles(CUtensorMap *map, const void *base, uint64_t cols, uint64
     return r == CUDA_SUCCESS;
 }
 
+bool encode_heads_tiles(CUtensorMap *map, const HeadsView &v, bool bf16, uint64_t dim, uint64_t heads, uint64_t rows,
+                        uint32_t box_heads, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {dim, heads, rows};
+    // A stride that nothing steps over may hold anything; the encoder wants a valid one.
+    const cuuint64_t any = (dim * 2 + 15) / 16 * 16;
+    cuuint64_t strides[2] = {heads > 1 ? static_cast<cuuint64_t>(v.head) * 2 : any,
+                             rows > 1 ? static_cast<cuuint64_t>(v.row) * 2 : any};
+    cuuint32_t box[3] = {64, box_heads, box_rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, v.data, dims,
+                    strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 }  // namespace cli
