@@ -165,7 +165,7 @@ void backward(const AttentionLaunch &L, cudaStream_t stream) {
 }  // namespace attn
 
 size_t attention_workspace(const AttentionLaunch &) { return 0; }
-size_t attention_backward_workspace(const AttentionLaunch &) { return 0; }
+size_t attention_backward_workspace(const AttentionLaunch &L) { return attn::backward_tiles_workspace(L); }
 
 cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t stream) {
     if (L.query_rows && L.key_rows) return attn::launch_forward_tiles(L, stream);
@@ -173,6 +173,7 @@ cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t stream) {
     return cudaGetLastError();
 }
 cudaError_t launch_attention_backward(const AttentionLaunch &L, cudaStream_t stream) {
+    if (L.query_rows && L.key_rows) return attn::launch_backward_tiles(L, stream);
     if (L.dtype == CLI_BF16) attn::backward<__nv_bfloat16>(L, stream); else attn::backward<__half>(L, stream);
     return cudaGetLastError();
 }

@@ -1,0 +1,758 @@
+// Gradients of cross attention over tapes: the tensor-core backward.
+//
+// Mathematics.  With p_rj = exp(scale <q_r, k_j> - lse_r) recomputed from the
+// forward's lse and delta_r = <dO_r, O_r>:
+//     dV_j = sum_r p_rj dO_r,      ds_rj = p_rj (<dO_r, v_j> - delta_r),
+//     dQ_r = scale sum_j ds_rj k_j,   dK_j = scale sum_r ds_rj q_r.
+//
+// Two kernels, each the owner of what it sums, so no sum crosses CTAs and the
+// results do not depend on the order in which CTAs run.  dkv_kernel holds 128
+// states and walks the item's queries (four products of 128 x 128 x D a block:
+// S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q); dq_kernel holds 128
+// rows and walks the item's states (three: S, dP, dQ += dS K).  One kernel
+// would need five products in the place of seven, but sums dQ across CTAs:
+// with fp32 reductions in memory, in whatever order they arrive.
+//
+// Both keep the scores' tiles in TMEM: S is turned into P in place, dP into dS
+// (16-bit, over the first half of the columns of each reader), and the second
+// products read them from there as their A operand.  Rows are packed as in the
+// forward: the heads of a group lie side by side in a tile.  Warp roles are
+// those of the forward, with eight warps for the tiles' arithmetic: each
+// thread has one row of TMEM and half of its columns.
+
+#include <cuda.h>
+
+#include "attention.cuh"
+
+namespace cli {
+namespace attn {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kReaders = 10;   // of a published work item: warp 1, warp 2, eight arithmetic warps
+
+// What the scores' rows need in the backward, one entry per output row and
+// head at stat_at: lse in powers of two (+infinity where the row kept no
+// state, so that p is 0) and delta.
+__device__ __forceinline__ long long stat_at(const AttentionLaunch &L, int out_rows, int key_head, long long row) {
+    return (static_cast<long long>(key_head) * out_rows + row) * L.group;
+}
+
+// A group of 16 lanes per (output row, head): 8 elements a lane.
+template <typename T>
+__global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ AttentionLaunch L, int out_rows,
+                                                    float2 *stats) {
+    check_items(L, static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, static_cast<long long>(gridDim.x) * 256);
+    const int lane = threadIdx.x & 15;
+    const long long cells = static_cast<long long>(out_rows) * L.query_heads;
+    for (long long c = static_cast<long long>(blockIdx.x) * 16 + (threadIdx.x >> 4); c - (threadIdx.x >> 4) < cells;
+         c += static_cast<long long>(gridDim.x) * 16) {
+        const bool on = c < cells;
+        const long long row = on ? c / L.query_heads : 0;
+        const int head = on ? static_cast<int>(c - row * L.query_heads) : 0;
+        float d = 0.0f;
+        if (on && 8 * lane < L.head_dim) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const T *>(L.o.data) + row * L.o.row +
+                                                             head * L.o.head + 8 * lane);
+            const uint4 b = *reinterpret_cast<const uint4 *>(static_cast<const T *>(L.d_o.data) + row * L.d_o.row +
+                                                             head * L.d_o.head + 8 * lane);
+            const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = Type<T>::unpack(wa[i]), y = Type<T>::unpack(wb[i]);
+                d = fmaf(x.x, y.x, fmaf(x.y, y.y, d));
+            }
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        if (on && lane == 0) {
+            const float lse = L.lse[c];
+            const int kh = head / L.group;
+            stats[stat_at(L, out_rows, kh, row) + head - kh * L.group] =
+                make_float2(lse == -INFINITY ? INFINITY : lse * kLog2e, d);
+        }
+    }
+}
+
+// One CTA's current work: a tile of 128 states or of 128 packed rows.
+struct Work {
+    int q0, o0, nq, k0, nk, head;   // nq, nk: rows of the item to walk, or of the tile; head < 0: no more work
+};
+
+template <int BOXES>
+struct Storage {
+    alignas(1024) uint8_t held[2][BOXES * kBoxBytes];      // K and V, or Q and dO
+    alignas(1024) uint8_t ring[2][2][BOXES * kBoxBytes];   // stages of (Q, dO), or of (K, V)
+    alignas(16) float stat[2][2][128];                      // dkv: lse and delta of a stage's rows
+    uint32_t bits[4][4];                                    // dq: a block's kept states
+    Work work[2];
+    uint64_t work_full[2], work_empty[2];
+    uint64_t held_full, held_empty, ring_full[2], ring_empty[2], ring_ready[2];
+    uint64_t s_full[2], dp_full, p_ready, ds_ready[2], sum_full, done;   // the dkv kernel uses the first of two
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+struct Maps {
+    CUtensorMap q, k, v, d_o;
+};
+
+template <typename Smem>
+__device__ __forceinline__ uint32_t begin(Smem &sm, const Maps &M) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.work_full[i], 1);
+            mbar_init(&sm.work_empty[i], kReaders);
+            mbar_init(&sm.ring_full[i], 1);
+            mbar_init(&sm.ring_empty[i], 1);
+            mbar_init(&sm.ring_ready[i], 1);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.ds_ready[i], 8);
+        }
+        mbar_init(&sm.held_full, 1);
+        mbar_init(&sm.held_empty, 1);
+        mbar_init(&sm.dp_full, 1);
+        mbar_init(&sm.p_ready, 8);
+        mbar_init(&sm.sum_full, 1);
+        mbar_init(&sm.done, 1);
+        sm.abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&M.q);
+        prefetch_tmap(&M.k);
+        prefetch_tmap(&M.v);
+        prefetch_tmap(&M.d_o);
+    }
+    if (threadIdx.x / 32 == 1) tmem_alloc(&sm.tmem_base, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    return sm.tmem_base;
+}
+
+template <typename Smem>
+__device__ __forceinline__ bool next_work(Smem &sm, const AttentionLaunch &L, uint32_t it, Work &w) {
+    if (!mbar_wait(&sm.work_full[it & 1], (it >> 1) & 1, &sm.abort_flag, L.status)) return false;
+    w = sm.work[it & 1];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.work_empty[it & 1]);
+    return w.head >= 0;
+}
+
+// The TMA producer's side: publishes work and loads its tiles.
+template <int BOXES, typename Smem>
+struct Producer {
+    Smem &sm;
+    const AttentionLaunch &L;
+    uint32_t it = 0, entry = 0, held = 0;
+    __device__ bool wait(uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, &sm.abort_flag, L.status); }
+    __device__ bool publish(const Work &w) {
+        if (!wait(&sm.work_empty[it & 1], ((it >> 1) & 1) ^ 1)) return false;
+        if ((threadIdx.x & 31) == 0) {
+            sm.work[it & 1] = w;
+            mbar_arrive(&sm.work_full[it & 1]);
+        }
+        ++it;
+        return true;
+    }
+    __device__ void load(uint8_t *dst, const CUtensorMap *map, uint64_t *bar, int head, int row) {
+#pragma unroll
+        for (int b = 0; b < BOXES; ++b) tma_load_3d(dst + b * kBoxBytes, map, bar, 64 * b, head, row);
+    }
+    // One thread: the held pair of tiles (bytes: of one), then a stage's pair.
+    __device__ bool hold(const CUtensorMap *a, const CUtensorMap *b, uint32_t bytes, int head, int row_a, int row_b) {
+        if (!wait(&sm.held_empty, (held & 1) ^ 1)) return false;
+        ++held;
+        mbar_arrive_expect_tx(&sm.held_full, 2 * bytes);
+        load(sm.held[0], a, &sm.held_full, head, row_a);
+        load(sm.held[1], b, &sm.held_full, head, row_b);
+        return true;
+    }
+    __device__ bool stage(const CUtensorMap *a, const CUtensorMap *b, uint32_t bytes, int head, int row_a, int row_b) {
+        const uint32_t s = entry & 1;
+        if (!wait(&sm.ring_empty[s], ((entry >> 1) & 1) ^ 1)) return false;
+        ++entry;
+        mbar_arrive_expect_tx(&sm.ring_full[s], 2 * bytes);
+        load(sm.ring[s][0], a, &sm.ring_full[s], head, row_a);
+        load(sm.ring[s][1], b, &sm.ring_full[s], head, row_b);
+        return true;
+    }
+    // Lets the loads in flight land before the CTA can exit.
+    __device__ void drain() {
+        for (uint32_t s = 0; s < 2; ++s)
+            if (entry > s) wait(&sm.ring_empty[s], ((entry - 1 - s) >> 1) & 1);
+        if (held) wait(&sm.held_empty, (held - 1) & 1);
+    }
+};
+
+// A row of sums from TMEM, scaled, to `out`.
+template <typename T>
+__device__ __forceinline__ void store_sums(uint32_t at, int dim, float scale, bool have, bool mine, T *out) {
+#pragma unroll 1
+    for (int x = 0; x < dim; x += 16) {
+        uint32_t o[16];
+        if (have) {
+            tmem_ld16_async(at + x, o);
+            tmem_wait_ld();
+            tmem_regs_ready_n(o);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!mine || x + 8 * h >= dim) continue;
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = have ? Type<T>::pack(__uint_as_float(o[8 * h + 2 * i]) * scale,
+                                            __uint_as_float(o[8 * h + 2 * i + 1]) * scale)
+                            : 0u;
+            *reinterpret_cast<uint4 *>(out + x + 8 * h) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// ----------------------------------------------------------------------------
+// dK, dV
+// ----------------------------------------------------------------------------
+
+// TMEM: S^T / P^T | dP^T / dS^T | dV | dK.  The products of block j + 1's
+// scores run between those of block j, so that each of the two arithmetic
+// steps (P from S, dS from dP) has two products to hide under:
+//     ... [dV(j) S(j+1)] [dK(j) dP(j+1)] [dV(j+1) S(j+2)] ...
+template <typename T, int BOXES>
+__global__ void __launch_bounds__(kThreads, 1)
+    dkv_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
+               int out_rows, const float2 *stats, long long slots, long long tiles) {
+    extern __shared__ uint8_t smem_raw[];
+    using Smem = Storage<BOXES>;
+    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t tmem = begin(sm, M);
+    const int group = L.group, dim = L.head_dim;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, &sm.abort_flag, L.status); };
+    auto q_blocks = [&](const Work &w) { return (w.nq + rows_per_tile - 1) / rows_per_tile; };
+    auto q_rows = [&](const Work &w, int j) { return min(rows_per_tile, w.nq - j * rows_per_tile) * group; };
+
+    if (warp == 0) {
+        Producer<BOXES, Smem> P{sm, L};
+        const uint32_t q_bytes = BOXES * static_cast<uint32_t>(rows_per_tile * group) * 128u;
+        bool ok = true;
+        for (long long id = blockIdx.x; ok; id += gridDim.x) {
+            Work w = {0, 0, 0, 0, 0, -1};
+            if (id < tiles) {
+                const long long x = id % slots;
+                const int i = find_item(L.k_off, L.items, 128, x, lane);
+                const long long block = x - (static_cast<long long>(L.k_off[i] / 128) + i);
+                const Item t = load_item(L, i);
+                if (!t.ok || block < 0 || block * 128 >= t.nk) continue;   // an empty slot
+                const int r0 = static_cast<int>(block) * 128;
+                w = {t.q0, t.o0, t.nq, t.k0 + r0, min(128, t.nk - r0), static_cast<int>(id / slots)};
+            }
+            if (!P.publish(w) || w.head < 0) break;
+            if (lane == 0 && w.nq) {
+                ok = P.hold(&M.k, &M.v, BOXES * kBoxBytes, w.head, w.k0, w.k0);
+                for (int j = 0; j < q_blocks(w) && ok; ++j)
+                    ok = P.stage(&M.q, &M.d_o, q_bytes, w.head * group, w.q0 + j * rows_per_tile, w.o0 + j * rows_per_tile);
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        if (lane == 0) P.drain();
+    } else if (warp == 1) {
+        const uint32_t idesc_s = idesc_16bit(Type<T>::bf16, 128, 0, 0, 0);
+        const uint32_t idesc_d = idesc_16bit(Type<T>::bf16, 128, round16(dim), 0, 1);
+        uint32_t entry = 0, held = 0, j_all = 0;
+        bool ok = true;
+        Work w;
+        const uint32_t k_at = smem_u32(sm.held[0]), v_at = smem_u32(sm.held[1]);
+        for (uint32_t it = 0; ok && next_work(sm, L, it, w); ++it) {
+            const int blocks = q_blocks(w);
+            if (lane == 0 && blocks) {
+                // A 16-bit TMEM operand whose halves lie 64 columns apart.
+                auto sum = [&](uint32_t d, uint32_t a, uint32_t b, int rows, bool more) {
+                    mma_pairs(d, a, b, idesc_d, min(rows, 64), more);
+                    if (rows > 64) mma_pairs(d, a + 64, b + 4 * 2048, idesc_d, rows - 64, true);
+                };
+                auto scores = [&](int j, uint32_t e, int which) {
+                    const uint32_t n = round16(q_rows(w, j));
+                    mma_rows(tmem + which * 128, which ? v_at : k_at, smem_u32(sm.ring[e & 1][which]), idesc_s | (n >> 3) << 17, dim);
+                    mma_commit(which ? &sm.dp_full : &sm.s_full[0]);
+                };
+                ok = wait(&sm.held_full, held & 1) && wait(&sm.ring_ready[entry & 1], (entry >> 1) & 1);
+                ++held;
+                tc_fence_after();
+                if (ok) {
+                    scores(0, entry, 0);
+                    scores(0, entry, 1);
+                    if (blocks == 1) mma_commit(&sm.held_empty);
+                }
+                for (int j = 0; j < blocks && ok; ++j, ++j_all) {
+                    const uint32_t e = entry + j, en = e + 1;
+                    if (!wait(&sm.p_ready, j_all & 1)) { ok = false; break; }
+                    tc_fence_after();
+                    sum(tmem + 256, tmem, smem_u32(sm.ring[e & 1][1]), q_rows(w, j), j != 0);
+                    if (j + 1 < blocks) {
+                        if (!wait(&sm.ring_ready[en & 1], (en >> 1) & 1)) { ok = false; break; }
+                        tc_fence_after();
+                        scores(j + 1, en, 0);
+                    }
+                    if (!wait(&sm.ds_ready[0], j_all & 1)) { ok = false; break; }
+                    tc_fence_after();
+                    sum(tmem + 384, tmem + 128, smem_u32(sm.ring[e & 1][0]), q_rows(w, j), j != 0);
+                    mma_commit(&sm.ring_empty[e & 1]);
+                    if (j + 1 < blocks) {
+                        scores(j + 1, en, 1);
+                        if (j + 2 == blocks) mma_commit(&sm.held_empty);
+                    } else {
+                        mma_commit(&sm.sum_full);
+                    }
+                }
+                entry += blocks;
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        if (lane == 0) {
+            mma_commit(&sm.done);
+            wait(&sm.done, 0);
+        }
+    } else if (warp == 2) {
+        // Rows past the item's end are zeroed (they are summed over), and the rows' lse and delta staged.
+        uint32_t entry = 0;
+        bool ok = true;
+        Work w;
+        for (uint32_t it = 0; ok && next_work(sm, L, it, w); ++it) {
+            const int blocks = q_blocks(w);
+            for (int j = 0; j < blocks; ++j, ++entry) {
+                const int n = q_rows(w, j);
+                const float2 *src = stats + stat_at(L, out_rows, w.head, static_cast<long long>(w.o0) + j * rows_per_tile);
+                float2 f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = 32 * i + lane;
+                    f[i] = at < n ? src[at] : make_float2(INFINITY, 0.0f);
+                }
+                const uint32_t s = entry & 1;
+                if (!wait(&sm.ring_full[s], (entry >> 1) & 1)) { ok = false; break; }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sm.stat[s][0][32 * i + lane] = f[i].x;
+                    sm.stat[s][1][32 * i + lane] = f[i].y;
+                }
+                const uint32_t keep[4] = {first_bits(n, 0), first_bits(n, 1), first_bits(n, 2), first_bits(n, 3)};
+                zero_rows(smem_u32(sm.ring[s][0]), BOXES, round16(n), keep, lane);
+                zero_rows(smem_u32(sm.ring[s][1]), BOXES, round16(n), keep, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.ring_ready[s]);
+            }
+        }
+    } else if (warp >= 4) {
+        const int side = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t s_at = tmem + lanes + side * 64, dp_at = s_at + 128;
+        const float sl2 = L.scale * kLog2e;
+        uint32_t j_all = 0, works = 0;
+        bool ok = true;
+        Work w;
+        for (uint32_t it = 0; ok && next_work(sm, L, it, w); ++it) {
+            const int blocks = q_blocks(w);
+            const bool mine = row < w.nk, live = mine && (!L.key_mask || L.key_mask[w.k0 + row] != 0);
+            for (int j = 0; j < blocks; ++j, ++j_all) {
+                const int n = round16(q_rows(w, j)) - side * 64;   // columns of this side
+                const uint32_t s = j_all & 1, ph = (j_all >> 1) & 1;
+                if (!wait(&sm.ring_ready[s], ph) || !wait(&sm.s_full[0], j_all & 1)) { ok = false; break; }
+                tc_fence_after();
+                const float *lse = sm.stat[s][0] + side * 64, *delta = sm.stat[s][1] + side * 64;
+                float p[64];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (32 * c >= n) continue;
+                    uint32_t r[32], packed[16];
+                    tmem_ld32_async(s_at + 32 * c, r);
+                    tmem_wait_ld();
+                    tmem_regs_ready(r);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 l = *reinterpret_cast<const float4 *>(lse + 32 * c + i);
+                        const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float e = ex2(fmaf(__uint_as_float(r[i + k]), sl2, -lv[k]));
+                            p[32 * c + i + k] = live ? e : 0.0f;
+                        }
+                        packed[i / 2] = Type<T>::pack(p[32 * c + i], p[32 * c + i + 1]);
+                        packed[i / 2 + 1] = Type<T>::pack(p[32 * c + i + 2], p[32 * c + i + 3]);
+                    }
+                    tmem_st16(s_at + 16 * c, packed);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_ready);
+                if (!wait(&sm.dp_full, j_all & 1)) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (32 * c >= n) continue;
+                    uint32_t r[32], packed[16];
+                    tmem_ld32_async(dp_at + 32 * c, r);
+                    tmem_wait_ld();
+                    tmem_regs_ready(r);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 dl = *reinterpret_cast<const float4 *>(delta + 32 * c + i);
+                        const float dv[4] = {dl.x, dl.y, dl.z, dl.w};
+                        float ds[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float d = p[32 * c + i + k] * (__uint_as_float(r[i + k]) - dv[k]);
+                            ds[k] = live ? d : 0.0f;
+                        }
+                        packed[i / 2] = Type<T>::pack(ds[0], ds[1]);
+                        packed[i / 2 + 1] = Type<T>::pack(ds[2], ds[3]);
+                    }
+                    tmem_st16(dp_at + 16 * c, packed);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.ds_ready[0]);
+            }
+            if (!ok) break;
+            if (blocks) {
+                if (!wait(&sm.sum_full, works & 1)) break;
+                ++works;
+                tc_fence_after();
+            }
+            const HeadsView &v = side ? L.d_k : L.d_v;
+            T *out = static_cast<T *>(v.data) + (static_cast<long long>(w.k0) + row) * v.row + w.head * v.head;
+            store_sums<T>(tmem + lanes + 256 + side * 128, dim, side ? L.scale : 1.0f, blocks != 0, mine, out);
+            tc_fence_before();
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ----------------------------------------------------------------------------
+// dQ
+// ----------------------------------------------------------------------------
+
+// TMEM: S / dS of even blocks | of odd blocks | dP | dQ.  p_ready says here
+// that dP has been read, so that the next block's may be written.  s_full and
+// ds_ready alternate: the scores of block j + 1 are issued before block j's
+// are waited for, and dP of block j + 1 before ds of block j is, so with one
+// barrier each a phase could pass unseen.
+template <typename T, int BOXES>
+__global__ void __launch_bounds__(kThreads, 1)
+    dq_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
+              int out_rows, const float2 *stats, float *partials, long long slots, long long tiles) {
+    extern __shared__ uint8_t smem_raw[];
+    using Smem = Storage<BOXES>;
+    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t tmem = begin(sm, M);
+    const int group = L.group, dim = L.head_dim;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, &sm.abort_flag, L.status); };
+
+    if (warp == 0) {
+        Producer<BOXES, Smem> P{sm, L};
+        const uint32_t q_bytes = BOXES * static_cast<uint32_t>(rows_per_tile * group) * 128u;
+        const int per_item = L.q_off ? 0 : (L.query_rows + rows_per_tile - 1) / rows_per_tile;
+        bool ok = true;
+        for (long long id = blockIdx.x; ok; id += gridDim.x) {
+            Work w = {0, 0, 0, 0, 0, -1};
+            if (id < tiles) {
+                const long long x = id % slots;
+                int i;
+                long long block;
+                if (L.q_off) {
+                    i = find_item(L.q_off, L.items, rows_per_tile, x, lane);
+                    block = x - (static_cast<long long>(L.q_off[i] / rows_per_tile) + i);
+                } else {
+                    i = static_cast<int>(x / per_item);
+                    block = x - static_cast<long long>(i) * per_item;
+                }
+                const Item t = load_item(L, i);
+                if (!t.ok || block < 0 || block * rows_per_tile >= t.nq) continue;   // an empty slot
+                const int r0 = static_cast<int>(block) * rows_per_tile;
+                w = {t.q0 + r0, t.o0 + r0, min(rows_per_tile, t.nq - r0), t.k0, t.nk, static_cast<int>(id / slots)};
+            }
+            if (!P.publish(w) || w.head < 0) break;
+            if (lane == 0 && w.nk) {
+                ok = P.hold(&M.q, &M.d_o, q_bytes, w.head * group, w.q0, w.o0);
+                for (int j = 0; j < (w.nk + 127) / 128 && ok; ++j)
+                    ok = P.stage(&M.k, &M.v, BOXES * kBoxBytes, w.head, w.k0 + 128 * j, w.k0 + 128 * j);
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        if (lane == 0) P.drain();
+    } else if (warp == 1) {
+        const uint32_t idesc_s = idesc_16bit(Type<T>::bf16, 128, 0, 0, 0);
+        const uint32_t idesc_d = idesc_16bit(Type<T>::bf16, 128, round16(dim), 0, 1);
+        uint32_t entry = 0, held = 0, j_all = 0;
+        bool ok = true;
+        Work w;
+        for (uint32_t it = 0; ok && next_work(sm, L, it, w); ++it) {
+            const int blocks = (w.nk + 127) / 128;
+            if (lane == 0 && blocks) {
+                auto scores = [&](int j, uint32_t e, int which) {
+                    const uint32_t n = round16(min(128, w.nk - 128 * j));
+                    const uint32_t d = which ? tmem + 256 : tmem + (e & 1) * 128;
+                    mma_rows(d, smem_u32(sm.held[which]), smem_u32(sm.ring[e & 1][which]), idesc_s | (n >> 3) << 17, dim);
+                    mma_commit(which ? &sm.dp_full : &sm.s_full[e & 1]);
+                };
+                ok = wait(&sm.held_full, held & 1) && wait(&sm.ring_ready[entry & 1], (entry >> 1) & 1);
+                ++held;
+                tc_fence_after();
+                if (ok) {
+                    scores(0, entry, 0);
+                    scores(0, entry, 1);
+                    if (blocks == 1) mma_commit(&sm.held_empty);
+                }
+                for (int j = 0; j < blocks && ok; ++j, ++j_all) {
+                    const uint32_t e = entry + j, en = e + 1;
+                    if (j + 1 < blocks) {
+                        if (!wait(&sm.ring_ready[en & 1], (en >> 1) & 1)) { ok = false; break; }
+                        tc_fence_after();
+                        scores(j + 1, en, 0);
+                    }
+                    if (!wait(&sm.p_ready, j_all & 1)) { ok = false; break; }
+                    tc_fence_after();
+                    if (j + 1 < blocks) {
+                        scores(j + 1, en, 1);
+                        if (j + 2 == blocks) mma_commit(&sm.held_empty);
+                    }
+                    if (!wait(&sm.ds_ready[j_all & 1], (j_all >> 1) & 1)) { ok = false; break; }
+                    tc_fence_after();
+                    const int n = min(128, w.nk - 128 * j);
+                    const uint32_t a = tmem + (e & 1) * 128, b = smem_u32(sm.ring[e & 1][0]);
+                    mma_pairs(tmem + 384, a, b, idesc_d, min(n, 64), j != 0);
+                    if (n > 64) mma_pairs(tmem + 384, a + 64, b + 4 * 2048, idesc_d, n - 64, true);
+                    mma_commit(&sm.ring_empty[e & 1]);
+                    if (j + 1 == blocks) mma_commit(&sm.sum_full);
+                }
+                entry += blocks;
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        if (lane == 0) {
+            mma_commit(&sm.done);
+            wait(&sm.done, 0);
+        }
+    } else if (warp == 2) {
+        // Dropped states and those past the item's end: their K rows are zeroed (they are summed over), and
+        // their bits staged.  V's rows only reach their own columns of dP, which are not used.
+        uint32_t entry = 0;
+        bool ok = true;
+        Work w;
+        for (uint32_t it = 0; ok && next_work(sm, L, it, w); ++it) {
+            const int blocks = (w.nk + 127) / 128;
+            for (int j = 0; j < blocks; ++j, ++entry) {
+                const int n = min(128, w.nk - 128 * j);
+                uint32_t keep[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int at = 32 * k + lane;
+                    keep[k] = first_bits(n, k);
+                    if (L.key_mask)
+                        keep[k] = __ballot_sync(0xffffffffu, at < n && L.key_mask[w.k0 + 128 * j + at] != 0);
+                }
+                const uint32_t s = entry & 1;
+                if (!wait(&sm.ring_full[s], (entry >> 1) & 1)) { ok = false; break; }
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sm.bits[entry & 3][k] = keep[k];
+                }
+                zero_rows(smem_u32(sm.ring[s][0]), BOXES, round16(n), keep, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.ring_ready[s]);
+            }
+        }
+    } else if (warp >= 4) {
+        const int side = (warp - 4) >> 2, quad = warp & 3, m_row = quad * 32 + lane;
+        const int r_in = m_row / group, head_in = m_row - r_in * group;
+        const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t dp_at = tmem + lanes + 256 + side * 64;
+        const float sl2 = L.scale * kLog2e;
+        uint32_t j_all = 0, works = 0;
+        bool ok = true;
+        Work w;
+        for (uint32_t it = 0; ok && next_work(sm, L, it, w); ++it) {
+            const int blocks = (w.nk + 127) / 128;
+            const bool mine = r_in < w.nq && m_row < rows_per_tile * group;
+            float2 st = make_float2(INFINITY, 0.0f);
+            if (mine)
+                st = stats[stat_at(L, out_rows, w.head, static_cast<long long>(w.o0) + r_in) + head_in];
+            const float2 sl22 = make_float2(sl2, sl2), shift = make_float2(-st.x, -st.x);
+            for (int j = 0; j < blocks; ++j, ++j_all) {
+                const int n = min(128, w.nk - 128 * j) - side * 64;   // columns of this side
+                const bool whole = !L.key_mask && n >= 64;
+                const uint32_t s_at = tmem + lanes + (j_all & 1) * 128 + side * 64;
+                if (!wait(&sm.ring_ready[j_all & 1], (j_all >> 1) & 1) || !wait(&sm.s_full[j_all & 1], (j_all >> 1) & 1)) { ok = false; break; }
+                tc_fence_after();
+                float p[64];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (32 * c >= n) continue;
+                    uint32_t r[32];
+                    tmem_ld32_async(s_at + 32 * c, r);
+                    tmem_wait_ld();
+                    tmem_regs_ready(r);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), sl22, shift);
+                        p[32 * c + i] = ex2(x.x);
+                        p[32 * c + i + 1] = ex2(x.y);
+                    }
+                }
+                if (!wait(&sm.dp_full, j_all & 1)) { ok = false; break; }
+                tc_fence_after();
+                uint32_t packed[2][16];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (32 * c >= n) continue;
+                    uint32_t r[32];
+                    tmem_ld32_async(dp_at + 32 * c, r);
+                    tmem_wait_ld();
+                    tmem_regs_ready(r);
+                    const uint32_t keep = whole ? 0xffffffffu : sm.bits[j_all & 3][2 * side + c];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float a = p[32 * c + i] * (__uint_as_float(r[i]) - st.y);
+                        float b = p[32 * c + i + 1] * (__uint_as_float(r[i + 1]) - st.y);
+                        if (!whole) {
+                            a = (keep >> i) & 1u ? a : 0.0f;
+                            b = (keep >> (i + 1)) & 1u ? b : 0.0f;
+                        }
+                        packed[c][i / 2] = Type<T>::pack(a, b);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_ready);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (32 * c < n) tmem_st16(s_at + 16 * c, packed[c]);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.ds_ready[j_all & 1]);
+            }
+            if (!ok) break;
+            if (blocks) {
+                if (!wait(&sm.sum_full, works & 1)) break;
+                ++works;
+                tc_fence_after();
+            }
+            const int head = w.head * group + head_in;
+            if (side == 0) {
+                if (partials) {
+                    float *out = partials + ((static_cast<long long>(w.o0) + r_in) * L.query_heads + head) * dim;
+#pragma unroll 1
+                    for (int x = 0; x < dim; x += 16) {
+                        uint32_t o[16];
+                        if (blocks) {
+                            tmem_ld16_async(tmem + lanes + 384 + x, o);
+                            tmem_wait_ld();
+                            tmem_regs_ready_n(o);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            if (mine && x + i < dim)
+                                *reinterpret_cast<uint4 *>(out + x + i) =
+                                    blocks ? make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]) : make_uint4(0, 0, 0, 0);
+                    }
+                } else {
+                    T *out = static_cast<T *>(L.d_q.data) + (static_cast<long long>(w.q0) + r_in) * L.d_q.row + head * L.d_q.head;
+                    store_sums<T>(tmem + lanes + 384, dim, L.scale, blocks != 0, mine, out);
+                }
+            }
+            tc_fence_before();
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// dQ of shared queries: the items' sums, in their order, eight elements a thread.
+template <typename T>
+__global__ void __launch_bounds__(256) dq_sum_kernel(const __grid_constant__ AttentionLaunch L, const float *partials) {
+    const long long row_elems = static_cast<long long>(L.query_heads) * L.head_dim, all = row_elems * L.query_rows;
+    const long long at = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 8;
+    if (at >= all) return;
+    float s[8] = {};
+    for (int i = 0; i < L.items; ++i) {
+        const float4 *src = reinterpret_cast<const float4 *>(partials + i * all + at);
+        const float4 a = src[0], b = src[1];
+        s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;
+        s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
+    }
+    const long long row = at / row_elems;
+    const int in_row = static_cast<int>(at - row * row_elems), head = in_row / L.head_dim;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = Type<T>::pack(s[2 * i] * L.scale, s[2 * i + 1] * L.scale);
+    *reinterpret_cast<uint4 *>(static_cast<T *>(L.d_q.data) + row * L.d_q.row + head * L.d_q.head + in_row -
+                               head * L.head_dim) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+size_t stats_bytes(const AttentionLaunch &L) {
+    const size_t out_rows = static_cast<size_t>(L.query_rows) * (L.q_off ? 1 : L.items);
+    return align256(out_rows * L.query_heads * sizeof(float2));
+}
+
+template <typename T, int BOXES>
+cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
+    const int rows_per_tile = 128 / L.group;
+    const int out_rows = L.query_rows * (L.q_off ? 1 : L.items);
+    float2 *stats = reinterpret_cast<float2 *>(L.workspace);
+    float *partials = L.q_off ? nullptr : reinterpret_cast<float *>(L.workspace + stats_bytes(L));
+    Maps M;
+    const bool bf16 = Type<T>::bf16;
+    if (!encode_heads_tiles(&M.q, L.q, bf16, L.head_dim, L.query_heads, L.query_rows, L.group, rows_per_tile) ||
+        !encode_heads_tiles(&M.d_o, L.d_o, bf16, L.head_dim, L.query_heads, out_rows, L.group, rows_per_tile) ||
+        !encode_heads_tiles(&M.k, L.k, bf16, L.head_dim, L.key_heads, L.key_rows, 1, kTileRows) ||
+        !encode_heads_tiles(&M.v, L.v, bf16, L.head_dim, L.key_heads, L.key_rows, 1, kTileRows))
+        return cudaErrorInvalidValue;
+    const long long cells = static_cast<long long>(out_rows) * L.query_heads;
+    const long long blocks = (cells + 15) / 16, most = 16ll * L.sm_count;
+    stats_kernel<T><<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, stream>>>(L, out_rows, stats);
+
+    const size_t smem = sizeof(Storage<BOXES>) + 1024;
+    auto dkv = dkv_kernel<T, BOXES>;
+    auto dq = dq_kernel<T, BOXES>;
+    cudaError_t e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    auto grid = [&](long long tiles) { return static_cast<unsigned>(tiles < L.sm_count ? tiles : L.sm_count); };
+    const long long k_slots = L.key_rows / 128 + L.items, k_tiles = k_slots * L.key_heads;
+    dkv<<<grid(k_tiles), kThreads, smem, stream>>>(L, M, rows_per_tile, out_rows, stats, k_slots, k_tiles);
+    const long long q_slots = L.q_off ? static_cast<long long>(L.query_rows) / rows_per_tile + L.items
+                                      : static_cast<long long>(L.items) * ((L.query_rows + rows_per_tile - 1) / rows_per_tile);
+    const long long q_tiles = q_slots * L.key_heads;
+    dq<<<grid(q_tiles), kThreads, smem, stream>>>(L, M, rows_per_tile, out_rows, stats, partials, q_slots, q_tiles);
+    if (partials) {
+        const long long all = static_cast<long long>(L.query_rows) * L.query_heads * L.head_dim;
+        dq_sum_kernel<T><<<static_cast<unsigned>((all / 8 + 255) / 256), 256, 0, stream>>>(L, partials);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t backward_tiles_workspace(const AttentionLaunch &L) {
+    const size_t partials = L.q_off ? 0
+                                    : static_cast<size_t>(L.items) * L.query_rows * L.query_heads * L.head_dim * sizeof(float);
+    return stats_bytes(L) + align256(partials);
+}
+
+// Needs at least one query row and one state (the tensor maps have no empty form).
+cudaError_t launch_backward_tiles(const AttentionLaunch &L, cudaStream_t stream) {
+    const bool wide = L.head_dim > 64;
+    if (L.dtype == CLI_BF16) return wide ? launch<__nv_bfloat16, 2>(L, stream) : launch<__nv_bfloat16, 1>(L, stream);
+    return wide ? launch<__half, 2>(L, stream) : launch<__half, 1>(L, stream);
+}
+
+}  // namespace attn
+}  // namespace cli

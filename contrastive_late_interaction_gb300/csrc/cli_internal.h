@@ -246,6 +246,8 @@ size_t attention_workspace(const AttentionLaunch &L);
 size_t attention_backward_workspace(const AttentionLaunch &L);
 namespace attn {
 cudaError_t launch_forward_tiles(const AttentionLaunch &L, cudaStream_t stream);
+cudaError_t launch_backward_tiles(const AttentionLaunch &L, cudaStream_t stream);
+size_t backward_tiles_workspace(const AttentionLaunch &L);
 }
 cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t stream);
 cudaError_t launch_attention_backward(const AttentionLaunch &L, cudaStream_t stream);
