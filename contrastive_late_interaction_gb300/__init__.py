@@ -16,11 +16,14 @@ _BINDING_NAMES = {
     "pair_loss_sigmoid_groups_fwd_bwd", "maxsim_scores_named", "maxsim_named_workspace_bytes",
     "maxsim_backward_named", "selftest_bounded_wait", "rotary_table", "rotary_heads", "rotary_heads_backward",
     "norm_rotary_heads", "norm_rotary_heads_backward", "cross_attention", "cross_attention_backward",
+    "cross_attention_workspace_bytes", "cross_attention_backward_workspace_bytes",
+    "norm_rotary_heads_backward_workspace_bytes",
 }
 
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import _binding
-        return getattr(_binding, name)
+        value = globals()[name] = getattr(_binding, name)   # the next look-up finds it without this function
+        return value
     raise AttributeError(name)

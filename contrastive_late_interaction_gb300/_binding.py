@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -609,31 +610,82 @@ def maxsim_backward_named(q_data, q_offsets, d_data, d_offsets, argmax, d_scores
 
 # ----------------------------------------------------------------------------
 # token states
+#
+# These calls are often short, so their host side is kept to a few microseconds: the argument struct is packed in one
+# call (its layout checked against the ctypes structure), and a tensor's checks are a few comparisons.
 # ----------------------------------------------------------------------------
 
-def _heads(t, name, rows, heads, dim, dtype):
-    """A [rows, heads, dim] tensor of `dtype` whose heads are contiguous -> HeadsArgs."""
-    _check_cuda(t, name, dtype)
-    if t.dim() != 3 or t.shape[0] != rows or t.shape[1] != heads or t.shape[2] != dim:
-        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name} must be [{rows}, {heads}, {dim}], not {list(t.shape)}")
+def _fast(name):
+    """The C function `name`, taking its argument struct as packed bytes."""
+    fn = lib[name]   # a function object of its own, beside lib.name
+    fn.restype, fn.argtypes = EXPORTS[name][0], [ctypes.c_char_p]
+    return fn
+
+
+_PART = "17Q"       # rows, heads, positions, x, y, d_y, d_x, gain, d_gain
+_pack_rotary = struct.Struct("@2i4Qf4x" + _PART + _PART + "4Q")
+_pack_attention = struct.Struct("@i4x10Qf4x" + "Q12QQ12Q" + "4Q")
+assert _pack_rotary.size == ctypes.sizeof(RotaryArgs) and _pack_attention.size == ctypes.sizeof(AttentionArgs)
+_ROTARY = {v: _fast(v) for v in ("rotary_heads", "rotary_heads_backward", "norm_rotary_heads",
+                                 "norm_rotary_heads_backward")}
+_ATTENTION = {v: (_fast(v), _fast(v + "_workspace_bytes")) for v in ("cross_attention", "cross_attention_backward")}
+_NO_HEADS = (0, 0, 0)
+
+
+def _raw_stream(stream, tensor):
+    return (stream if stream is not None else torch.cuda.current_stream(tensor.device)).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):   # the same without building a Stream object
+    def _raw_stream(stream, tensor):   # noqa: F811
+        return torch._C._cuda_getCurrentRawStream(tensor.get_device()) if stream is None else stream.cuda_stream
+
+
+def _heads(t, name, shape, dtype):
+    """(data, row stride, head stride) of a tensor of `shape` [rows, heads, dim] whose heads are contiguous."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
+        _check_cuda(t, name, dtype)
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name} must be {list(shape)}, not {list(t.shape)}")
     row, head, inner = t.stride()
-    if inner != 1 and dim > 1:
+    if inner != 1 and shape[2] > 1:
         raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name}: the elements of a head must be contiguous")
-    return HeadsArgs(t.data_ptr(), row, head)
+    return t.data_ptr(), row, head
 
 
-def _out(out, name, like, rows=None):
-    """The caller's output `name`, or a new packed one of the shape of `like` (with `rows` rows)."""
+def _vector(t, name, n, dtype):
+    """The address of a packed vector of n elements, 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or not t.is_cuda:
+        _check_cuda(t, name, dtype)
+    if t.numel() != n or not t.is_contiguous():
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name} must be [{n}], packed")
+    return t.data_ptr()
+
+
+def _states(t, name):
+    """The shape of a matrix [rows, heads, dim] on the device."""
+    if not t.is_cuda:
+        _check_cuda(t, name)
+    if t.dim() != 3:
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name} must be [rows, heads, head_dim], not {list(t.shape)}")
+    if t.dtype not in DTYPES:
+        raise UnsupportedError(CLI_UNSUPPORTED, f"{name}: {t.dtype}")
+    return t.shape
+
+
+def _out(out, name, like):
+    """The caller's output `name`, or a new packed one of the shape of `like`."""
     t = out.get(name) if out else None
     if t is not None:
         return t
-    return torch.empty((like.shape[0] if rows is None else rows, *like.shape[1:]), dtype=like.dtype,
-                       device=like.device)
+    return torch.empty_like(like) if like.is_contiguous() else torch.empty(like.shape, dtype=like.dtype,
+                                                                           device=like.device)
 
 
-def _status(device_status, device):
+def _status(device_status, like):
     if device_status is None:
-        return torch.empty(1, dtype=torch.int32, device=device)   # the call writes it
+        return torch.empty(1, dtype=torch.int32, device=like.device)   # the call writes it
     _check_cuda(device_status, "device_status", torch.int32)
     return device_status
 
@@ -658,50 +710,35 @@ def rotary_table(positions, rotary_dim, base=10000.0, scaling="plain", factor=1.
     return dict(table=t)
 
 
-def _rotary_call(verb, tensors, table, positions, gains, d_gains, interleaved, epsilon, workspace, device_status,
-                 stream):
-    """One rotation verb over its two parts.  `tensors`: per part (None: absent) the struct's fields by name."""
-    first = next(iter(tensors[0].values()))
-    _check_cuda(first, "q")
-    if first.dim() != 3:
-        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: queries must be [rows, heads, head_dim]")
-    dtype, dim, dev = first.dtype, first.shape[2], first.device
-    if dtype not in DTYPES:
-        raise UnsupportedError(CLI_UNSUPPORTED, f"{verb}: {dtype}")
-    _check_cuda(table, "table", torch.float32)
-    if table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous():
+def _part(name, lead, positions, x, y, d_y, d_x, gain, d_gain, dtype, dim):
+    """One part of a rotation call, as the struct's 17 words; the matrices given have the shape of `lead`."""
+    shape = lead.shape
+    if len(shape) != 3 or shape[2] != dim:
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name} must be [rows, heads, {dim}], not {list(shape)}")
+    rows, heads, _ = shape
+    return (rows, heads, _vector(positions, name + " positions", rows, torch.int32),
+            *(_NO_HEADS if x is None else _heads(x, name, shape, dtype)),
+            *(_NO_HEADS if y is None else _heads(y, "out " + name, shape, dtype)),
+            *(_NO_HEADS if d_y is None else _heads(d_y, "d_" + name, shape, dtype)),
+            *(_NO_HEADS if d_x is None else _heads(d_x, "out d_" + name, shape, dtype)),
+            _vector(gain, name + "_gain", dim, torch.float32), _vector(d_gain, f"d_{name}_gain", dim, torch.float32))
+
+
+_NO_PART = (0,) * 17
+
+
+def _rotary_call(verb, lead, q_part, k_part, table, interleaved, epsilon, workspace, status, stream):
+    if table.dtype is not torch.float32 or not table.is_cuda:
+        _check_cuda(table, "table", torch.float32)
+    shape = table.shape
+    if len(shape) != 3 or shape[2] != 2 or not table.is_contiguous():
         raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: table must be [positions, rotary_dim / 2, 2], packed")
-    parts = []
-    for p, name in enumerate("qk"):
-        if tensors[p] is None:
-            parts.append(RotaryPartArgs())
-            continue
-        lead = next(iter(tensors[p].values()))
-        if lead.dim() != 3:
-            raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: {name} must be [rows, heads, head_dim]")
-        rows, heads = lead.shape[0], lead.shape[1]
-        pos, gain, d_gain = positions[p], gains[p], d_gains[p]
-        _check_cuda(pos, f"{name} positions", torch.int32)
-        if pos is not None and (pos.numel() != rows or not pos.is_contiguous()):
-            raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: {name} positions must be [{rows}], packed")
-        for g, what in ((gain, "gain"), (d_gain, "d_gain")):
-            _check_cuda(g, f"{name}_{what}", torch.float32)
-            if g is not None and (g.numel() != dim or not g.is_contiguous()):
-                raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: {name}_{what} must be [{dim}], packed")
-        parts.append(RotaryPartArgs(rows=rows, heads=heads, positions=_ptr(pos), gain=_ptr(gain), d_gain=_ptr(d_gain),
-                                    **{f: _heads(t, f"{name}.{f}", rows, heads, dim, dtype)
-                                       for f, t in tensors[p].items()}))
-    st = _status(device_status, dev)
-    ws = workspace
-    if ws is None and (d_gains[0] is not None or d_gains[1] is not None):
-        ws = _ws(lib.norm_rotary_heads_backward_workspace_bytes(dim), dev)
-    args = RotaryArgs(dtype=DTYPES[dtype], interleaved=int(bool(interleaved)), head_dim=dim,
-                      rotary_dim=2 * table.shape[1], table=table.data_ptr(), table_rows=table.shape[0],
-                      epsilon=epsilon, q=parts[0], k=parts[1], workspace=_ptr(ws),
-                      workspace_bytes=0 if ws is None else ws.numel(), device_status=st.data_ptr(),
-                      stream=_stream(stream))
-    raise_for(getattr(lib, verb)(ctypes.byref(args)), verb)
-    return st
+    ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    rc = _ROTARY[verb](_pack_rotary.pack(DTYPES[lead.dtype], 1 if interleaved else 0, lead.shape[2], 2 * shape[1],
+                                         table.data_ptr(), shape[0], epsilon, *q_part, *k_part, ws, ws_bytes,
+                                         status.data_ptr(), _raw_stream(stream, lead)))
+    if rc:
+        raise_for(rc, verb)
 
 
 def rotary_heads(q, table, positions=None, k=None, k_positions=None, interleaved=False, out=None, device_status=None,
@@ -709,33 +746,39 @@ def rotary_heads(q, table, positions=None, k=None, k_positions=None, interleaved
     """Rotates queries [rows, heads, dim] (and keys, of their own rows and heads) by their rows' positions (int32;
     None: row r is at position r), over the first 2 * table.shape[1] elements of each head.  bf16, fp16 or fp32.
     Returns dict(q, k, device_status); out['q'] may be `q` itself."""
-    yq, yk = _out(out, "q", q), None if k is None else _out(out, "k", k)
-    st = _rotary_call("rotary_heads", (dict(x=q, y=yq), None if k is None else dict(x=k, y=yk)), table,
-                      (positions, k_positions), (None, None), (None, None), interleaved, 0.0, None, device_status,
-                      stream)
-    return dict(q=yq, k=yk, device_status=st)
+    dtype, dim = q.dtype, _states(q, "q")[2]
+    yq, yk, st = _out(out, "q", q), None if k is None else _out(out, "k", k), _status(device_status, q)
+    _rotary_call("rotary_heads", q, _part("q", q, positions, q, yq, None, None, None, None, dtype, dim),
+                 _NO_PART if k is None else _part("k", k, k_positions, k, yk, None, None, None, None, dtype, dim),
+                 table, interleaved, 0.0, None, st, stream)
+    return {"q": yq, "k": yk, "device_status": st}
 
 
 def rotary_heads_backward(d_q, table, positions=None, d_k=None, k_positions=None, interleaved=False, out=None,
                           device_status=None, stream=None):
     """The gradient of rotary_heads for its inputs.  Returns dict(d_q, d_k, device_status)."""
-    xq, xk = _out(out, "d_q", d_q), None if d_k is None else _out(out, "d_k", d_k)
-    st = _rotary_call("rotary_heads_backward",
-                      (dict(d_y=d_q, d_x=xq), None if d_k is None else dict(d_y=d_k, d_x=xk)), table,
-                      (positions, k_positions), (None, None), (None, None), interleaved, 0.0, None, device_status,
-                      stream)
-    return dict(d_q=xq, d_k=xk, device_status=st)
+    dtype, dim = d_q.dtype, _states(d_q, "d_q")[2]
+    xq, xk, st = _out(out, "d_q", d_q), None if d_k is None else _out(out, "d_k", d_k), _status(device_status, d_q)
+    _rotary_call("rotary_heads_backward", d_q, _part("q", d_q, positions, None, None, d_q, xq, None, None, dtype, dim),
+                 _NO_PART if d_k is None else _part("k", d_k, k_positions, None, None, d_k, xk, None, None, dtype, dim),
+                 table, interleaved, 0.0, None, st, stream)
+    return {"d_q": xq, "d_k": xk, "device_status": st}
 
 
 def norm_rotary_heads(q, table, positions=None, q_gain=None, k=None, k_positions=None, k_gain=None, interleaved=False,
                       epsilon=1e-6, out=None, device_status=None, stream=None):
     """Normalises each head, rotate(gain * x / sqrt(mean(x^2) + epsilon)), of queries and keys in one pass.  Gains
     are fp32 [dim] (None: ones); the rest as in rotary_heads.  Returns dict(q, k, device_status)."""
-    yq, yk = _out(out, "q", q), None if k is None else _out(out, "k", k)
-    st = _rotary_call("norm_rotary_heads", (dict(x=q, y=yq), None if k is None else dict(x=k, y=yk)), table,
-                      (positions, k_positions), (q_gain, k_gain), (None, None), interleaved, epsilon, None,
-                      device_status, stream)
-    return dict(q=yq, k=yk, device_status=st)
+    dtype, dim = q.dtype, _states(q, "q")[2]
+    yq, yk, st = _out(out, "q", q), None if k is None else _out(out, "k", k), _status(device_status, q)
+    _rotary_call("norm_rotary_heads", q, _part("q", q, positions, q, yq, None, None, q_gain, None, dtype, dim),
+                 _NO_PART if k is None else _part("k", k, k_positions, k, yk, None, None, k_gain, None, dtype, dim),
+                 table, interleaved, epsilon, None, st, stream)
+    return {"q": yq, "k": yk, "device_status": st}
+
+
+def norm_rotary_heads_backward_workspace_bytes(head_dim):
+    return int(lib.norm_rotary_heads_backward_workspace_bytes(head_dim))
 
 
 def norm_rotary_heads_backward(q, d_q, table, positions=None, q_gain=None, k=None, d_k=None, k_positions=None,
@@ -746,46 +789,72 @@ def norm_rotary_heads_backward(q, d_q, table, positions=None, q_gain=None, k=Non
     d_k_gain, device_status)."""
     if (k is None) != (d_k is None):
         raise InvalidArgumentError(CLI_INVALID_ARGUMENT, "norm_rotary_heads_backward: k and d_k go together")
-    xq, xk = _out(out, "d_q", q), None if k is None else _out(out, "d_k", k)
+    dtype, dim = q.dtype, _states(q, "q")[2]
+    xq, xk, st = _out(out, "d_q", q), None if k is None else _out(out, "d_k", k), _status(device_status, q)
     gq = None if q_gain is None else _out(out, "d_q_gain", q_gain)
     gk = None if k is None or k_gain is None else _out(out, "d_k_gain", k_gain)
-    st = _rotary_call("norm_rotary_heads_backward",
-                      (dict(x=q, d_y=d_q, d_x=xq), None if k is None else dict(x=k, d_y=d_k, d_x=xk)), table,
-                      (positions, k_positions), (q_gain, k_gain), (gq, gk), interleaved, epsilon, workspace,
-                      device_status, stream)
-    return dict(d_q=xq, d_q_gain=gq, d_k=xk, d_k_gain=gk, device_status=st)
+    if workspace is None and (gq is not None or gk is not None):
+        workspace = _ws(lib.norm_rotary_heads_backward_workspace_bytes(dim), q.device)
+    _rotary_call("norm_rotary_heads_backward", q, _part("q", q, positions, q, None, d_q, xq, q_gain, gq, dtype, dim),
+                 _NO_PART if k is None else _part("k", k, k_positions, k, None, d_k, xk, k_gain, gk, dtype, dim),
+                 table, interleaved, epsilon, workspace, st, stream)
+    return {"d_q": xq, "d_q_gain": gq, "d_k": xk, "d_k_gain": gk, "device_status": st}
 
 
-def _attention_args(verb, q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_rows, max_key_rows):
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _check_cuda(t, name, q.dtype)
-        if t.dim() != 3:
-            raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: {name} must be [rows, heads, head_dim]")
-    if q.dtype not in DTYPES:
-        raise UnsupportedError(CLI_UNSUPPORTED, f"{verb}: {q.dtype}")
-    rows_q, hq, dim = q.shape
-    rows_k, hk, _ = k.shape
-    _check_cuda(k_offsets, "k_offsets", torch.int64)
-    _check_cuda(q_offsets, "q_offsets", torch.int64)
+def _mask(key_mask, rows):
+    if key_mask is None:
+        return 0
+    if key_mask.dtype not in (torch.uint8, torch.bool):
+        raise InvalidArgumentError(CLI_INVALID_ARGUMENT, "key_mask must be torch.uint8 or torch.bool")
+    return _vector(key_mask, "key_mask", rows, key_mask.dtype)
+
+
+def _attention_sizes(q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_rows, max_key_rows):
+    """The struct's words up to `v`, and the number of items."""
+    q_shape, k_shape, dtype = _states(q, "q"), _states(k, "k"), q.dtype
+    (rows_q, hq, dim), (rows_k, hk, _) = q_shape, k_shape
     items = k_offsets.numel() - 1
-    if not k_offsets.is_contiguous() or (q_offsets is not None and (q_offsets.numel() != items + 1 or
-                                                                    not q_offsets.is_contiguous())):
-        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: offsets must be [items + 1] each, packed")
-    if key_mask is not None:
-        _check_cuda(key_mask, "key_mask")
-        if key_mask.dtype not in (torch.uint8, torch.bool):
-            raise InvalidArgumentError(CLI_INVALID_ARGUMENT, "key_mask must be torch.uint8 or torch.bool")
-        if key_mask.numel() != rows_k or not key_mask.is_contiguous():
-            raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: key_mask must be [{rows_k}], packed")
-    if min(rows_q if max_query_rows is None else max_query_rows, rows_k if max_key_rows is None else max_key_rows) < 0:
-        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: max_query_rows and max_key_rows must be >= 0")
-    return AttentionArgs(
-        dtype=DTYPES[q.dtype], items=max(items, 0), query_rows=rows_q, key_rows=rows_k, query_offsets=_ptr(q_offsets),
-        key_offsets=k_offsets.data_ptr(), max_query_rows=rows_q if max_query_rows is None else max_query_rows,
-        max_key_rows=rows_k if max_key_rows is None else max_key_rows, query_heads=hq, key_heads=hk, head_dim=dim,
-        scale=dim ** -0.5 if scale is None else scale, key_mask=_ptr(key_mask),
-        q=_heads(q, "q", rows_q, hq, dim, q.dtype), k=_heads(k, "k", rows_k, hk, dim, q.dtype),
-        v=_heads(v, "v", rows_k, hk, dim, q.dtype))
+    max_q = rows_q if max_query_rows is None else max_query_rows
+    max_k = rows_k if max_key_rows is None else max_key_rows
+    if items < 0 or max_q < 0 or max_k < 0:
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, "offsets must be [items + 1], maxima at least 0")
+    k_shape = (rows_k, hk, dim)
+    return (DTYPES[dtype], items, rows_q, rows_k, _vector(q_offsets, "q_offsets", items + 1, torch.int64),
+            _vector(k_offsets, "k_offsets", items + 1, torch.int64), max_q, max_k, hq, hk, dim,
+            dim ** -0.5 if scale is None else scale, _mask(key_mask, rows_k), *_heads(q, "q", q_shape, dtype),
+            *_heads(k, "k", k_shape, dtype), *_heads(v, "v", k_shape, dtype)), items
+
+
+def _attention_call(verb, head, tail, workspace, like, status, stream):
+    call, workspace_bytes = _ATTENTION[verb]
+    stream = _raw_stream(stream, like)
+    if workspace is None:
+        need = workspace_bytes(_pack_attention.pack(*head, *tail, 0, 0, 0, 0))
+        workspace = _ws(need, like.device) if need else None
+    ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    rc = call(_pack_attention.pack(*head, *tail, ws, ws_bytes, status.data_ptr(), stream))
+    if rc:
+        raise_for(rc, verb)
+
+
+def cross_attention_workspace_bytes(q, q_offsets, k, v, k_offsets, key_mask=None, max_query_rows=None,
+                                    max_key_rows=None):
+    """Workspace bytes for cross_attention of these arguments (their sizes alone count)."""
+    head, _ = _attention_sizes(q, q_offsets, k, v, k_offsets, key_mask, 1.0, max_query_rows, max_key_rows)
+    return int(_ATTENTION["cross_attention"][1](_pack_attention.pack(*head, *(0,) * 16, 0, 0, 0, 0)))
+
+
+def cross_attention_backward_workspace_bytes(q, q_offsets, k, v, k_offsets, key_mask=None, max_query_rows=None,
+                                             max_key_rows=None):
+    """Workspace bytes for cross_attention_backward of these arguments (their sizes alone count)."""
+    head, _ = _attention_sizes(q, q_offsets, k, v, k_offsets, key_mask, 1.0, max_query_rows, max_key_rows)
+    return int(_ATTENTION["cross_attention_backward"][1](_pack_attention.pack(*head, *(0,) * 16, 0, 0, 0, 0)))
+
+
+def _lse_ptr(lse, rows, heads):
+    if list(lse.shape) != [rows, heads]:
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"lse must be [{rows}, {heads}], packed")
+    return _vector(lse, "lse", rows * heads, torch.float32)
 
 
 def cross_attention(q, q_offsets, k, v, k_offsets, key_mask=None, scale=None, max_query_rows=None, max_key_rows=None,
@@ -795,40 +864,22 @@ def cross_attention(q, q_offsets, k, v, k_offsets, key_mask=None, scale=None, ma
     the outputs have items * rows rows.  `key_mask` (uint8 or bool [states]) drops states where it is 0; `scale`
     defaults to dim^-0.5; the two maxima bound the items' rows (default: the tapes').  bf16 or fp16.  Returns
     dict(output, lse, device_status), lse fp32 [output rows, heads] or None."""
-    args = _attention_args("cross_attention", q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_rows,
-                           max_key_rows)
-    dev = q.device
-    rows = q.shape[0] if q_offsets is not None else q.shape[0] * args.items
-    o = _out(out, "output", q, rows)
-    args.output = _heads(o, "output", rows, q.shape[1], q.shape[2], q.dtype)
-    lse = None
+    head, items = _attention_sizes(q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_rows, max_key_rows)
+    rows_q, hq, dim = q.shape
+    shape = (rows_q if q_offsets is not None else rows_q * items, hq, dim)
+    o = out.get("output") if out else None
+    if o is None:
+        o = torch.empty(shape, dtype=q.dtype, device=q.device)
+    lse, lse_ptr = None, 0
     if want_lse:
         lse = out.get("lse") if out else None
         if lse is None:
-            lse = torch.empty(rows, q.shape[1], device=dev)
-        _check_lse(lse, rows, q.shape[1], "cross_attention")
-        args.lse = lse.data_ptr()
-    st = _status(device_status, dev)
-    _attention_call("cross_attention", args, workspace, st, dev, stream)
-    return dict(output=o, lse=lse, device_status=st)
-
-
-def _check_lse(lse, rows, heads, verb):
-    _check_cuda(lse, "lse", torch.float32)
-    if list(lse.shape) != [rows, heads] or not lse.is_contiguous():
-        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: lse must be [{rows}, {heads}], packed")
-
-
-def _attention_call(verb, args, workspace, status, device, stream):
-    ws = workspace
-    if ws is None:
-        need = getattr(lib, verb + "_workspace_bytes")(ctypes.byref(args))
-        ws = _ws(need, device) if need else None
-    args.workspace = _ptr(ws)
-    args.workspace_bytes = 0 if ws is None else ws.numel()
-    args.device_status = status.data_ptr()
-    args.stream = _stream(stream)
-    raise_for(getattr(lib, verb)(ctypes.byref(args)), verb)
+            lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+        lse_ptr = _lse_ptr(lse, *shape[:2])
+    st = _status(device_status, q)
+    _attention_call("cross_attention", head, (*_heads(o, "output", shape, q.dtype), lse_ptr, *_NO_HEADS, *_NO_HEADS,
+                                              *_NO_HEADS, *_NO_HEADS), workspace, q, st, stream)
+    return {"output": o, "lse": lse, "device_status": st}
 
 
 def cross_attention_backward(q, q_offsets, k, v, k_offsets, output, lse, d_output, key_mask=None, scale=None,
@@ -836,18 +887,12 @@ def cross_attention_backward(q, q_offsets, k, v, k_offsets, output, lse, d_outpu
                              stream=None):
     """The gradients of cross_attention for `q`, `k` and `v`, given its `output` and `lse` and the output's gradient;
     the rest as there.  Returns dict(d_q, d_k, d_v, device_status)."""
-    verb = "cross_attention_backward"
-    args = _attention_args(verb, q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_rows, max_key_rows)
-    dev, (rows_q, hq, dim), (rows_k, hk, _) = q.device, q.shape, k.shape
-    rows = rows_q if q_offsets is not None else rows_q * args.items
-    _check_lse(lse, rows, hq, verb)
-    dq, dk, dv = _out(out, "d_q", q), _out(out, "d_k", k), _out(out, "d_v", v)
-    args.output = _heads(output, "output", rows, hq, dim, q.dtype)
-    args.lse = lse.data_ptr()
-    args.d_output = _heads(d_output, "d_output", rows, hq, dim, q.dtype)
-    args.d_q = _heads(dq, "d_q", rows_q, hq, dim, q.dtype)
-    args.d_k = _heads(dk, "d_k", rows_k, hk, dim, q.dtype)
-    args.d_v = _heads(dv, "d_v", rows_k, hk, dim, q.dtype)
-    st = _status(device_status, dev)
-    _attention_call(verb, args, workspace, st, dev, stream)
-    return dict(d_q=dq, d_k=dk, d_v=dv, device_status=st)
+    head, items = _attention_sizes(q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_rows, max_key_rows)
+    (rows_q, hq, dim), dtype = q.shape, q.dtype
+    shape = (rows_q if q_offsets is not None else rows_q * items, hq, dim)
+    dq, dk, dv, st = _out(out, "d_q", q), _out(out, "d_k", k), _out(out, "d_v", v), _status(device_status, q)
+    tail = (*_heads(output, "output", shape, dtype), _lse_ptr(lse, *shape[:2]),
+            *_heads(d_output, "d_output", shape, dtype), *_heads(dq, "d_q", q.shape, dtype),
+            *_heads(dk, "d_k", k.shape, dtype), *_heads(dv, "d_v", v.shape, dtype))
+    _attention_call("cross_attention_backward", head, tail, workspace, q, st, stream)
+    return {"d_q": dq, "d_k": dk, "d_v": dv, "device_status": st}

@@ -117,22 +117,45 @@ __device__ __forceinline__ uint32_t round16(int n) { return static_cast<uint32_t
 constexpr uint32_t kTileRows = 128;
 constexpr uint32_t kBoxBytes = kTileRows * 128;
 
-// D (+)= A B^T over `dim` elements, A and B K-major tiles of rows of heads.
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, int dim) {
-    const int steps = (dim + 15) / 16;
-    for (int k = 0; k < steps; ++k) {
-        const uint32_t at = (k >> 2) * kBoxBytes + (k & 3) * 32;
-        mma_bf16(d, sdesc_sw128(a + at, 16, 1024), sdesc_sw128(b + at, 16, 1024), idesc, k != 0);
+// Descriptors of a tile: rows of heads as a K-major operand, and as the
+// MN-major operand of a product that sums over the rows.  The address field
+// counts 16 bytes, so a step within a tile is an addition to the descriptor.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t tile) { return sdesc_sw128(tile, 16, 1024); }
+__device__ __forceinline__ uint64_t desc_sum(uint32_t tile) { return sdesc_sw128(tile, kBoxBytes, 1024); }
+constexpr uint64_t desc_bytes(uint32_t bytes) { return bytes >> 4; }
+
+// Hides where a descriptor came from.  Without it the compiler (nvcc 13.0)
+// folds the steps below into bases that several calls share, and the products
+// of the backward then came out wrong on every input.
+__device__ __forceinline__ uint64_t opaque(uint64_t d) {
+    asm volatile("" : "+l"(d));
+    return d;
+}
+
+// D = A B^T over `steps` times 16 elements of the heads.  Unrolled: one thread
+// issues the products, and an instruction or two each is what keeps it ahead
+// of the tensor core (64 cycles a product; a loop that built its descriptors
+// took about 150).
+template <int BOXES>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int steps) {
+    a = opaque(a);
+    b = opaque(b);
+#pragma unroll
+    for (int k = 0; k < 4 * BOXES; ++k) {
+        const uint64_t at = desc_bytes((k >> 2) * kBoxBytes + (k & 3) * 32);
+        if (k < steps) mma_bf16(d, a + at, b + at, idesc, k != 0);
     }
 }
 
-// D (+)= A B over `rows` rows of B, A in TMEM (16-bit pairs), B a tile of rows
-// of heads read MN-major.
-__device__ __forceinline__ void mma_pairs(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, int rows,
+// D (+)= A B over `rows` rows of B, at most 16 STEPS; A in TMEM (16-bit pairs), B a tile
+// of rows of heads.
+template <int STEPS>
+__device__ __forceinline__ void mma_pairs(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int rows,
                                           bool accumulate) {
-    const int steps = (rows + 15) / 16;
-    for (int k = 0; k < steps; ++k)
-        mma_ts(d, a + k * 8, sdesc_sw128(b + k * 2048, kBoxBytes, 1024), idesc, accumulate || k != 0);
+    b = opaque(b);
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k)
+        if (16 * k < rows) mma_ts(d, a + k * 8, b + desc_bytes(k * 2048), idesc, k != 0 || accumulate);
 }
 
 // Zeroes rows of a tile of `boxes` boxes: those of the first `rows` whose bit

@@ -261,18 +261,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t entry = 0, held = 0, j_all = 0;
         bool ok = true;
         Work w;
-        const uint32_t k_at = smem_u32(sm.held[0]), v_at = smem_u32(sm.held[1]);
+        const uint64_t held_desc = desc_rows(smem_u32(sm.held[0])), ring_desc = desc_rows(smem_u32(sm.ring[0][0]));
+        const uint64_t sum_desc = desc_sum(smem_u32(sm.ring[0][0]));
+        constexpr uint64_t kTile = desc_bytes(BOXES * kBoxBytes);
+        const int steps = (dim + 15) / 16;
         for (uint32_t it = 0; ok && next_work(sm, L, it, w); ++it) {
             const int blocks = q_blocks(w);
             if (lane == 0 && blocks) {
                 // A 16-bit TMEM operand whose halves lie 64 columns apart.
-                auto sum = [&](uint32_t d, uint32_t a, uint32_t b, int rows, bool more) {
-                    mma_pairs(d, a, b, idesc_d, min(rows, 64), more);
-                    if (rows > 64) mma_pairs(d, a + 64, b + 4 * 2048, idesc_d, rows - 64, true);
+                auto sum = [&](uint32_t d, uint32_t a, uint64_t b, int rows, bool more) {
+                    mma_pairs<4>(d, a, b, idesc_d, rows, more);
+                    mma_pairs<4>(d, a + 64, b + desc_bytes(4 * 2048), idesc_d, rows - 64, true);
                 };
                 auto scores = [&](int j, uint32_t e, int which) {
                     const uint32_t n = round16(q_rows(w, j));
-                    mma_rows(tmem + which * 128, which ? v_at : k_at, smem_u32(sm.ring[e & 1][which]), idesc_s | (n >> 3) << 17, dim);
+                    mma_rows<BOXES>(tmem + which * 128, held_desc + which * kTile, ring_desc + ((e & 1) * 2 + which) * kTile,
+                                    idesc_s | (n >> 3) << 17, steps);
                     mma_commit(which ? &sm.dp_full : &sm.s_full[0]);
                 };
                 ok = wait(&sm.held_full, held & 1) && wait(&sm.ring_ready[entry & 1], (entry >> 1) & 1);
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t e = entry + j, en = e + 1;
                     if (!wait(&sm.p_ready, j_all & 1)) { ok = false; break; }
                     tc_fence_after();
-                    sum(tmem + 256, tmem, smem_u32(sm.ring[e & 1][1]), q_rows(w, j), j != 0);
+                    sum(tmem + 256, tmem, sum_desc + ((e & 1) * 2 + 1) * kTile, q_rows(w, j), j != 0);
                     if (j + 1 < blocks) {
                         if (!wait(&sm.ring_ready[en & 1], (en >> 1) & 1)) { ok = false; break; }
                         tc_fence_after();
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (!wait(&sm.ds_ready[0], j_all & 1)) { ok = false; break; }
                     tc_fence_after();
-                    sum(tmem + 384, tmem + 128, smem_u32(sm.ring[e & 1][0]), q_rows(w, j), j != 0);
+                    sum(tmem + 384, tmem + 128, sum_desc + (e & 1) * 2 * kTile, q_rows(w, j), j != 0);
                     mma_commit(&sm.ring_empty[e & 1]);
                     if (j + 1 < blocks) {
                         scores(j + 1, en, 1);
@@ -488,6 +492,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         const uint32_t idesc_s = idesc_16bit(Type<T>::bf16, 128, 0, 0, 0);
         const uint32_t idesc_d = idesc_16bit(Type<T>::bf16, 128, round16(dim), 0, 1);
+        const uint64_t held_desc = desc_rows(smem_u32(sm.held[0])), ring_desc = desc_rows(smem_u32(sm.ring[0][0]));
+        const uint64_t sum_desc = desc_sum(smem_u32(sm.ring[0][0]));
+        constexpr uint64_t kTile = desc_bytes(BOXES * kBoxBytes);
+        const int steps = (dim + 15) / 16;
         uint32_t entry = 0, held = 0, j_all = 0;
         bool ok = true;
         Work w;
@@ -497,7 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto scores = [&](int j, uint32_t e, int which) {
                     const uint32_t n = round16(min(128, w.nk - 128 * j));
                     const uint32_t d = which ? tmem + 256 : tmem + (e & 1) * 128;
-                    mma_rows(d, smem_u32(sm.held[which]), smem_u32(sm.ring[e & 1][which]), idesc_s | (n >> 3) << 17, dim);
+                    mma_rows<BOXES>(d, held_desc + which * kTile, ring_desc + ((e & 1) * 2 + which) * kTile,
+                                    idesc_s | (n >> 3) << 17, steps);
                     mma_commit(which ? &sm.dp_full : &sm.s_full[e & 1]);
                 };
                 ok = wait(&sm.held_full, held & 1) && wait(&sm.ring_ready[entry & 1], (entry >> 1) & 1);
@@ -524,9 +533,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!wait(&sm.ds_ready[j_all & 1], (j_all >> 1) & 1)) { ok = false; break; }
                     tc_fence_after();
                     const int n = min(128, w.nk - 128 * j);
-                    const uint32_t a = tmem + (e & 1) * 128, b = smem_u32(sm.ring[e & 1][0]);
-                    mma_pairs(tmem + 384, a, b, idesc_d, min(n, 64), j != 0);
-                    if (n > 64) mma_pairs(tmem + 384, a + 64, b + 4 * 2048, idesc_d, n - 64, true);
+                    const uint32_t a = tmem + (e & 1) * 128;
+                    const uint64_t b = sum_desc + (e & 1) * 2 * kTile;
+                    mma_pairs<4>(tmem + 384, a, b, idesc_d, n, j != 0);
+                    mma_pairs<4>(tmem + 384, a + 64, b + desc_bytes(4 * 2048), idesc_d, n - 64, true);
                     mma_commit(&sm.ring_empty[e & 1]);
                     if (j + 1 == blocks) mma_commit(&sm.sum_full);
                 }

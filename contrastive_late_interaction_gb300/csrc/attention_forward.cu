@@ -179,6 +179,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ products
         const uint32_t idesc_s = idesc_16bit(Type<T>::bf16, 128, 0, 0, 0);   // N by block
         const uint32_t idesc_o = idesc_16bit(Type<T>::bf16, 128, round16(dim), 0, 1);
+        const uint64_t q_desc = desc_rows(smem_u32(sm.q[0])), k_desc = desc_rows(smem_u32(sm.kv[0]));
+        const uint64_t v_desc = desc_sum(smem_u32(sm.kv[0]));
+        constexpr uint64_t kTile = desc_bytes(BOXES * kBoxBytes);
+        const int steps = (dim + 15) / 16;
         uint32_t entry = 0, q_phase = 0, p_phase = 0;
         bool ok = true;
         Pair p;
@@ -187,7 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0 && blocks) {
                 auto scores = [&](int t, int j, uint32_t e) {
                     const uint32_t n = round16(min(128, p.nk - 128 * j));
-                    mma_rows(tmem + t * 128, smem_u32(sm.q[t]), smem_u32(sm.kv[e % kStages]), idesc_s | (n >> 3) << 17, dim);
+                    mma_rows<BOXES>(tmem + t * 128, q_desc + t * kTile, k_desc + (e % kStages) * kTile, idesc_s | (n >> 3) << 17,
+                                    steps);
                     mma_commit(&sm.s_full[t]);
                     if (j + 1 == blocks) mma_commit(&sm.q_empty[t]);
                 };
@@ -207,8 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!wait(&sm.p_ready[t], (p_phase >> t) & 1)) { ok = false; break; }
                         p_phase ^= 1u << t;
                         tc_fence_after();
-                        mma_pairs(tmem + 256 + t * 128, tmem + t * 128, smem_u32(sm.kv[ev % kStages]), idesc_o,
-                                  min(128, p.nk - 128 * j), j != 0);
+                        mma_pairs<8>(tmem + 256 + t * 128, tmem + t * 128, v_desc + (ev % kStages) * kTile, idesc_o,
+                                     min(128, p.nk - 128 * j), j != 0);
                         if (j + 1 == blocks) {
                             mma_commit(&sm.o_full[t]);
                         } else {
