@@ -294,68 +294,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 phase ^= 1;
                 tc_fence_after();
                 const int n = min(128, p.nk - 128 * j);
-                uint32_t r[4][32];
-                float top;
-                if (n == 128 && !L.key_mask && sign > 0.0f) {
-                    float t0, t1, t2, t3;
-                    tmem_ld32_max_async(s_at, r[0], t0);
-                    tmem_ld32_max_async(s_at + 32, r[1], t1);
-                    tmem_ld32_max_async(s_at + 64, r[2], t2);
-                    tmem_ld32_max_async(s_at + 96, r[3], t3);
-                    tmem_wait_ld();
-                    tmem_regs_ready(r[0], t0);
-                    tmem_regs_ready(r[1], t1);
-                    tmem_regs_ready(r[2], t2);
-                    tmem_regs_ready(r[3], t3);
-                    top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
-                } else {
-                    if (L.key_mask && !wait(&sm.bits_full[block % kBits], (block / kBits) & 1)) { ok = false; break; }
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) tmem_ld32_async(s_at + 32 * w, r[w]);
-                    tmem_wait_ld();
-                    top = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        tmem_regs_ready(r[w]);
-                        const uint32_t keep = L.key_mask ? sm.bits[block % kBits][w] : first_bits(n, w);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float v = (keep >> i) & 1u ? sign * __uint_as_float(r[w][i]) : -INFINITY;
-                            r[w][i] = __float_as_uint(v);
-                            top = fmaxf(top, v);
-                        }
-                    }
-                }
-                // The reference follows the maximum only when that has grown past 2^8.
-                if (__any_sync(0xffffffffu, top > m + lazy || (m == -INFINITY && top > m))) {
-                    const float m1 = fmaxf(m, top);
-                    const float c = m1 > m ? ex2((m - m1) * sl2) : 1.0f;
-                    m = m1;
-                    l *= c;
-                    if (j > 0) {   // S of this block is ready, so the product before it is done
-#pragma unroll 1
-                        for (int x = 0; x < BOXES * 64; x += 16) {
-                            uint32_t o[16];
-                            tmem_ld16_async(o_at + x, o);
-                            tmem_wait_ld();
-                            tmem_regs_ready_n(o);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
-                            tmem_st16(o_at + x, o);
-                            tmem_wait_st();
-                        }
-                    }
-                }
-                const float shift = m == -INFINITY ? 0.0f : -m * sl2;
-                const float2 shift2 = make_float2(shift, shift);
+                const bool plain = n == 128 && !L.key_mask && sign > 0.0f;
                 float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    uint32_t packed[16];
+                float2 shift = make_float2(-m * sl2, -m * sl2);
+                // The exponentials of 32 scores, packed, and added to the sums.
+                auto weights = [&](const uint32_t (&r)[32], uint32_t (&packed)[16]) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
-                        float2 a = __ffma2_rn(make_float2(__uint_as_float(r[w][i]), __uint_as_float(r[w][i + 1])), sl22, shift2);
-                        float2 b = __ffma2_rn(make_float2(__uint_as_float(r[w][i + 2]), __uint_as_float(r[w][i + 3])), sl22, shift2);
+                        float2 a = __ffma2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), sl22, shift);
+                        float2 b = __ffma2_rn(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), sl22, shift);
                         a = make_float2(ex2(a.x), ex2(a.y));
                         b = make_float2(ex2(b.x), ex2(b.y));
                         sum = __fadd2_rn(sum, a);
@@ -363,7 +310,93 @@ __global__ void __launch_bounds__(kThreads, 1)
                         packed[i / 2] = Type<T>::pack(a.x, a.y);
                         packed[i / 2 + 1] = Type<T>::pack(b.x, b.y);
                     }
-                    tmem_st16(s_at + 16 * w, packed);
+                };
+                bool again = !plain || m == -INFINITY;
+                if (!__any_sync(0xffffffffu, again)) {
+                    // Nearly always the reference still serves: the weights are taken as the scores arrive, and
+                    // thrown away in the rare block whose maximum turns out to be past it.
+                    uint32_t a[32], b[32], packed[4][16];
+                    float t0, t1, t2, t3;
+                    tmem_ld32_max_async(s_at, a, t0);
+                    tmem_ld32_max_async(s_at + 32, b, t1);
+                    tmem_wait_ld();
+                    tmem_regs_ready(a, t0);
+                    tmem_regs_ready(b, t1);
+                    weights(a, packed[0]);
+                    tmem_ld32_max_async(s_at + 64, a, t2);
+                    weights(b, packed[1]);
+                    tmem_wait_ld();
+                    tmem_regs_ready(a, t2);
+                    tmem_ld32_max_async(s_at + 96, b, t3);
+                    weights(a, packed[2]);
+                    tmem_wait_ld();
+                    tmem_regs_ready(b, t3);
+                    weights(b, packed[3]);
+                    again = __any_sync(0xffffffffu, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) > m + lazy);
+                    if (!again) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) tmem_st16(s_at + 16 * w, packed[w]);
+                    }
+                }
+                if (__any_sync(0xffffffffu, again)) {
+                    // The maximum first, then the weights: an item's first block, blocks with states to leave out.
+                    if (L.key_mask && !wait(&sm.bits_full[block % kBits], (block / kBits) & 1)) { ok = false; break; }
+                    auto left_out = [&](uint32_t (&r)[32], int w) {
+                        const uint32_t keep = L.key_mask ? sm.bits[block % kBits][w] : first_bits(n, w);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            r[i] = __float_as_uint((keep >> i) & 1u ? sign * __uint_as_float(r[i]) : -INFINITY);
+                    };
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        if (32 * w >= n) continue;
+                        uint32_t r[32];
+                        float t0;
+                        tmem_ld32_max_async(s_at + 32 * w, r, t0);
+                        tmem_wait_ld();
+                        tmem_regs_ready(r, t0);
+                        if (!plain) {
+                            left_out(r, w);
+                            t0 = -INFINITY;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) t0 = fmax3(t0, __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+                        }
+                        top = fmaxf(top, t0);
+                    }
+                    // The reference follows the maximum only when that has grown past 2^8.
+                    if (__any_sync(0xffffffffu, top > m + lazy || (m == -INFINITY && top > m))) {
+                        const float m1 = fmaxf(m, top);
+                        const float c = m1 > m ? ex2((m - m1) * sl2) : 1.0f;
+                        m = m1;
+                        l *= c;
+                        if (j > 0) {   // S of this block is ready, so the product before it is done
+#pragma unroll 1
+                            for (int x = 0; x < BOXES * 64; x += 32) {
+                                uint32_t o[32];
+                                tmem_ld32_async(o_at + x, o);
+                                tmem_wait_ld();
+                                tmem_regs_ready(o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
+                                tmem_st32(o_at + x, o);
+                                tmem_wait_st();
+                            }
+                        }
+                    }
+                    shift.x = shift.y = m == -INFINITY ? 0.0f : -m * sl2;
+                    sum = sum1 = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {   // P's words stay behind the scores still to be read
+                        if (32 * w >= n) continue;
+                        uint32_t r[32], packed[16];
+                        tmem_ld32_async(s_at + 32 * w, r);
+                        tmem_wait_ld();
+                        tmem_regs_ready(r);
+                        if (!plain) left_out(r, w);
+                        weights(r, packed);
+                        tmem_st16(s_at + 16 * w, packed);
+                    }
                 }
                 l += (sum.x + sum1.x) + (sum.y + sum1.y);
                 tmem_wait_st();
