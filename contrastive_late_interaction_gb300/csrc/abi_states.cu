@@ -292,7 +292,6 @@ cli_status_t attention_call(const cli_attention_t *a, bool backward) {
     L.workspace = static_cast<uint8_t *>(a->workspace);
     L.status = a->device_status;
     cudaStream_t stream = static_cast<cudaStream_t>(a->stream);
-    if (cudaMemsetAsync(a->device_status, 0, sizeof(int32_t), stream) != cudaSuccess) return CLI_DEVICE;
     const cudaError_t e = backward ? launch_attention_backward(L, stream) : launch_attention(L, stream);
     return e == cudaSuccess ? CLI_OK : CLI_DEVICE;
 }

@@ -62,8 +62,8 @@ __device__ __forceinline__ void check_items(const AttentionLaunch &L, long long 
 // and is its block x - first(i): an item of n rows has ceil(n / span) blocks
 // and at least that many slots, since floor((o + n) / span) - floor(o / span)
 // + 1 >= ceil(n / span); at most one slot per item stays empty.  So the slots
-// (rows / span + items of them) need no table and no scan: a warp finds the
-// item by a 32-way search over the offsets.
+// (rows / span + items of them) need no table and no scan: a search over the
+// offsets finds the item.  A warp searches 32 ways:
 __device__ __forceinline__ int find_item(const uint64_t *off, int items, unsigned span, long long x, int lane) {
     int lo = 0, n = items;   // the item is one of lo .. lo + n - 1
     while (n > 1) {
@@ -78,6 +78,75 @@ __device__ __forceinline__ int find_item(const uint64_t *off, int items, unsigne
     }
     return lo;
 }
+
+// A thread on its own, in halves.
+__device__ __forceinline__ int find_item(const uint64_t *off, int items, unsigned span, long long x) {
+    int lo = 0, hi = items;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (static_cast<long long>(off[mid] / span) + mid <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// Block `x` of a tape cut into blocks of `span` rows, or of shared queries
+// (off NULL) with `per_item` blocks an item: its item and the row it starts
+// at; false where the slot is empty.
+__device__ __forceinline__ bool find_block(const AttentionLaunch &L, const uint64_t *off, unsigned span, int per_item,
+                                           bool of_keys, long long x, Item &t, int &r0) {
+    int i;
+    long long block;
+    if (off) {
+        i = find_item(off, L.items, span, x);
+        block = x - (static_cast<long long>(off[i] / span) + i);
+    } else {
+        i = static_cast<int>(x / per_item);
+        block = x - static_cast<long long>(i) * per_item;
+    }
+    t = load_item(L, i);
+    const long long at = block * span;
+    r0 = static_cast<int>(at);
+    return t.ok && block >= 0 && at < (of_keys ? t.nk : t.nq);
+}
+
+// The tensor-core kernels hand out their blocks from a counter, a batch at a
+// time: items differ in length, and every other slot may be empty.  A warp
+// looks up a batch at once, one block a lane, so that the search costs each
+// block little, and enough batches are left to even out the CTAs.
+__device__ __forceinline__ int batch_of(long long tiles) {
+    const long long b = tiles / (static_cast<long long>(gridDim.x) * 8);
+    return b < 1 ? 1 : b > 32 ? 32 : static_cast<int>(b);
+}
+
+// The first kernel of a call: the status and the counters start at 0.
+static __global__ void begin_kernel(int32_t *status, unsigned long long *counters) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) *status = 0;
+    if (threadIdx.x < 4) counters[threadIdx.x] = 0;
+}
+
+// Waits for the kernels before this one on the stream, which may still run
+// when it starts (launch_after).
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches a kernel that may start before the one before it has ended; it
+// calls after_previous() before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+constexpr size_t kCounterBytes = 256;   // at the start of the workspace
 
 template <typename T> struct Type;
 template <> struct Type<__nv_bfloat16> {

@@ -29,7 +29,8 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kReaders = 10;   // of a published work item: warp 1, warp 2, eight arithmetic warps
+constexpr int kWorks = 4;
+constexpr int kReaders = 11;   // of a published work item: warps 0 to 2, eight arithmetic warps
 
 // What the scores' rows need in the backward, one entry per output row and
 // head at stat_at: lse in powers of two (+infinity where the row kept no
@@ -42,6 +43,8 @@ __device__ __forceinline__ long long stat_at(const AttentionLaunch &L, int out_r
 template <typename T>
 __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ AttentionLaunch L, int out_rows,
                                                     float2 *stats) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    after_previous();
     check_items(L, static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, static_cast<long long>(gridDim.x) * 256);
     const int lane = threadIdx.x & 15;
     const long long cells = static_cast<long long>(out_rows) * L.query_heads;
@@ -85,8 +88,8 @@ struct Storage {
     alignas(1024) uint8_t ring[2][2][BOXES * kBoxBytes];   // stages of (Q, dO), or of (K, V)
     alignas(16) float stat[2][2][128];                      // dkv: lse and delta of a stage's rows
     uint32_t bits[4][4];                                    // dq: a block's kept states
-    Work work[2];
-    uint64_t work_full[2], work_empty[2];
+    Work work[kWorks];
+    uint64_t work_full[kWorks], work_empty[kWorks];
     uint64_t held_full, held_empty, ring_full[2], ring_empty[2], ring_ready[2];
     uint64_t s_full[2], dp_full, p_ready, ds_ready[2], sum_full, done;   // the dkv kernel uses the first of two
     uint32_t tmem_base;
@@ -101,13 +104,15 @@ template <typename Smem>
 __device__ __forceinline__ uint32_t begin(Smem &sm, const Maps &M) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.work_full[i], 1);
-            mbar_init(&sm.work_empty[i], kReaders);
             mbar_init(&sm.ring_full[i], 1);
             mbar_init(&sm.ring_empty[i], 1);
             mbar_init(&sm.ring_ready[i], 1);
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.ds_ready[i], 8);
+        }
+        for (int i = 0; i < kWorks; ++i) {
+            mbar_init(&sm.work_full[i], 1);
+            mbar_init(&sm.work_empty[i], kReaders);
         }
         mbar_init(&sm.held_full, 1);
         mbar_init(&sm.held_empty, 1);
@@ -126,34 +131,69 @@ __device__ __forceinline__ uint32_t begin(Smem &sm, const Maps &M) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    after_previous();
     return sm.tmem_base;
 }
 
 template <typename Smem>
 __device__ __forceinline__ bool next_work(Smem &sm, const AttentionLaunch &L, uint32_t it, Work &w) {
-    if (!mbar_wait(&sm.work_full[it & 1], (it >> 1) & 1, &sm.abort_flag, L.status)) return false;
-    w = sm.work[it & 1];
+    if (!mbar_wait(&sm.work_full[it % kWorks], (it / kWorks) & 1, &sm.abort_flag, L.status)) return false;
+    w = sm.work[it % kWorks];
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.work_empty[it & 1]);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.work_empty[it % kWorks]);
     return w.head >= 0;
 }
 
-// The TMA producer's side: publishes work and loads its tiles.
+// Hands out the work: blocks of `span` states (of_keys) or queries.
+template <typename Smem>
+__device__ __forceinline__ void hand_out(Smem &sm, const AttentionLaunch &L, bool of_keys, int span, long long slots,
+                                         long long tiles, unsigned long long *counter) {
+    const int lane = threadIdx.x & 31, batch = batch_of(tiles);
+    const uint64_t *off = of_keys ? L.k_off : L.q_off;
+    const int per_item = off ? 0 : (L.query_rows + span - 1) / span;
+    uint32_t it = 0;
+    bool ok = true;
+    auto publish = [&](const Work &w) {
+        if (!mbar_wait(&sm.work_empty[it % kWorks], ((it / kWorks) & 1) ^ 1, &sm.abort_flag, L.status)) return false;
+        if (lane == 0) {
+            sm.work[it % kWorks] = w;
+            mbar_arrive(&sm.work_full[it % kWorks]);
+        }
+        ++it;
+        return true;
+    };
+    while (ok) {
+        unsigned long long base = 0;
+        if (lane == 0) base = atomicAdd(counter, static_cast<unsigned long long>(batch));
+        base = __shfl_sync(0xffffffffu, base, 0);
+        if (base >= static_cast<unsigned long long>(tiles)) break;
+        const long long id = static_cast<long long>(base) + lane;
+        Item t;
+        int r0 = 0;
+        const bool on = lane < batch && id < tiles && find_block(L, off, span, per_item, of_keys, id % slots, t, r0);
+        for (uint32_t left = __ballot_sync(0xffffffffu, on); left && ok; left &= left - 1) {
+            const int from = __ffs(left) - 1;
+            Work w = of_keys ? Work{t.q0, t.o0, t.nq, t.k0 + r0, min(span, t.nk - r0), static_cast<int>(id / slots)}
+                             : Work{t.q0 + r0, t.o0 + r0, min(span, t.nq - r0), t.k0, t.nk, static_cast<int>(id / slots)};
+            w.q0 = __shfl_sync(0xffffffffu, w.q0, from);
+            w.o0 = __shfl_sync(0xffffffffu, w.o0, from);
+            w.nq = __shfl_sync(0xffffffffu, w.nq, from);
+            w.k0 = __shfl_sync(0xffffffffu, w.k0, from);
+            w.nk = __shfl_sync(0xffffffffu, w.nk, from);
+            w.head = __shfl_sync(0xffffffffu, w.head, from);
+            ok = publish(w);
+        }
+    }
+    if (ok) publish({0, 0, 0, 0, 0, -1});
+}
+
+// The TMA producer's side.
 template <int BOXES, typename Smem>
 struct Producer {
     Smem &sm;
     const AttentionLaunch &L;
-    uint32_t it = 0, entry = 0, held = 0;
+    uint32_t entry = 0, held = 0;
     __device__ bool wait(uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, &sm.abort_flag, L.status); }
-    __device__ bool publish(const Work &w) {
-        if (!wait(&sm.work_empty[it & 1], ((it >> 1) & 1) ^ 1)) return false;
-        if ((threadIdx.x & 31) == 0) {
-            sm.work[it & 1] = w;
-            mbar_arrive(&sm.work_full[it & 1]);
-        }
-        ++it;
-        return true;
-    }
     __device__ void load(uint8_t *dst, const CUtensorMap *map, uint64_t *bar, int head, int row) {
 #pragma unroll
         for (int b = 0; b < BOXES; ++b) tma_load_3d(dst + b * kBoxBytes, map, bar, 64 * b, head, row);
@@ -220,7 +260,7 @@ __device__ __forceinline__ void store_sums(uint32_t at, int dim, float scale, bo
 template <typename T, int BOXES>
 __global__ void __launch_bounds__(kThreads, 1)
     dkv_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
-               int out_rows, const float2 *stats, long long slots, long long tiles) {
+               int out_rows, const float2 *stats, long long slots, long long tiles, unsigned long long *counter) {
     extern __shared__ uint8_t smem_raw[];
     using Smem = Storage<BOXES>;
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -235,18 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         Producer<BOXES, Smem> P{sm, L};
         const uint32_t q_bytes = BOXES * static_cast<uint32_t>(rows_per_tile * group) * 128u;
         bool ok = true;
-        for (long long id = blockIdx.x; ok; id += gridDim.x) {
-            Work w = {0, 0, 0, 0, 0, -1};
-            if (id < tiles) {
-                const long long x = id % slots;
-                const int i = find_item(L.k_off, L.items, 128, x, lane);
-                const long long block = x - (static_cast<long long>(L.k_off[i] / 128) + i);
-                const Item t = load_item(L, i);
-                if (!t.ok || block < 0 || block * 128 >= t.nk) continue;   // an empty slot
-                const int r0 = static_cast<int>(block) * 128;
-                w = {t.q0, t.o0, t.nq, t.k0 + r0, min(128, t.nk - r0), static_cast<int>(id / slots)};
-            }
-            if (!P.publish(w) || w.head < 0) break;
+        Work w;
+        for (uint32_t it = 0; ok && next_work(sm, L, it, w); ++it) {
             if (lane == 0 && w.nq) {
                 ok = P.hold(&M.k, &M.v, BOXES * kBoxBytes, w.head, w.k0, w.k0);
                 for (int j = 0; j < q_blocks(w) && ok; ++j)
@@ -347,7 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&sm.ring_ready[s]);
             }
         }
-    } else if (warp >= 4) {
+    } else if (warp == 3) {
+        hand_out(sm, L, true, 128, slots, tiles, counter);
+    } else {
         const int side = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t s_at = tmem + lanes + side * 64, dp_at = s_at + 128;
@@ -448,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename T, int BOXES>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
-              int out_rows, const float2 *stats, float *partials, long long slots, long long tiles) {
+              int out_rows, const float2 *stats, float *partials, long long slots, long long tiles, unsigned long long *counter) {
     extern __shared__ uint8_t smem_raw[];
     using Smem = Storage<BOXES>;
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -460,27 +492,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         Producer<BOXES, Smem> P{sm, L};
         const uint32_t q_bytes = BOXES * static_cast<uint32_t>(rows_per_tile * group) * 128u;
-        const int per_item = L.q_off ? 0 : (L.query_rows + rows_per_tile - 1) / rows_per_tile;
         bool ok = true;
-        for (long long id = blockIdx.x; ok; id += gridDim.x) {
-            Work w = {0, 0, 0, 0, 0, -1};
-            if (id < tiles) {
-                const long long x = id % slots;
-                int i;
-                long long block;
-                if (L.q_off) {
-                    i = find_item(L.q_off, L.items, rows_per_tile, x, lane);
-                    block = x - (static_cast<long long>(L.q_off[i] / rows_per_tile) + i);
-                } else {
-                    i = static_cast<int>(x / per_item);
-                    block = x - static_cast<long long>(i) * per_item;
-                }
-                const Item t = load_item(L, i);
-                if (!t.ok || block < 0 || block * rows_per_tile >= t.nq) continue;   // an empty slot
-                const int r0 = static_cast<int>(block) * rows_per_tile;
-                w = {t.q0 + r0, t.o0 + r0, min(rows_per_tile, t.nq - r0), t.k0, t.nk, static_cast<int>(id / slots)};
-            }
-            if (!P.publish(w) || w.head < 0) break;
+        Work w;
+        for (uint32_t it = 0; ok && next_work(sm, L, it, w); ++it) {
             if (lane == 0 && w.nk) {
                 ok = P.hold(&M.q, &M.d_o, q_bytes, w.head * group, w.q0, w.o0);
                 for (int j = 0; j < (w.nk + 127) / 128 && ok; ++j)
@@ -578,7 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&sm.ring_ready[s]);
             }
         }
-    } else if (warp >= 4) {
+    } else if (warp == 3) {
+        hand_out(sm, L, false, rows_per_tile, slots, tiles, counter);
+    } else {
         const int side = (warp - 4) >> 2, quad = warp & 3, m_row = quad * 32 + lane;
         const int r_in = m_row / group, head_in = m_row - r_in * group;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
@@ -716,8 +732,9 @@ template <typename T, int BOXES>
 cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
     const int rows_per_tile = 128 / L.group;
     const int out_rows = L.query_rows * (L.q_off ? 1 : L.items);
-    float2 *stats = reinterpret_cast<float2 *>(L.workspace);
-    float *partials = L.q_off ? nullptr : reinterpret_cast<float *>(L.workspace + stats_bytes(L));
+    unsigned long long *counters = reinterpret_cast<unsigned long long *>(L.workspace);
+    float2 *stats = reinterpret_cast<float2 *>(L.workspace + kCounterBytes);
+    float *partials = L.q_off ? nullptr : reinterpret_cast<float *>(L.workspace + kCounterBytes + stats_bytes(L));
     Maps M;
     const bool bf16 = Type<T>::bf16;
     if (!encode_heads_tiles(&M.q, L.q, bf16, L.head_dim, L.query_heads, L.query_rows, L.group, rows_per_tile) ||
@@ -727,21 +744,26 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     const long long cells = static_cast<long long>(out_rows) * L.query_heads;
     const long long blocks = (cells + 15) / 16, most = 16ll * L.sm_count;
-    stats_kernel<T><<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, stream>>>(L, out_rows, stats);
+    begin_kernel<<<1, 32, 0, stream>>>(L.status, counters);
+    cudaError_t e = launch_after(stats_kernel<T>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, stream, L,
+                                 out_rows, stats);
+    if (e != cudaSuccess) return e;
 
     const size_t smem = sizeof(Storage<BOXES>) + 1024;
     auto dkv = dkv_kernel<T, BOXES>;
     auto dq = dq_kernel<T, BOXES>;
-    cudaError_t e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e == cudaSuccess) e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     auto grid = [&](long long tiles) { return static_cast<unsigned>(tiles < L.sm_count ? tiles : L.sm_count); };
     const long long k_slots = L.key_rows / 128 + L.items, k_tiles = k_slots * L.key_heads;
-    dkv<<<grid(k_tiles), kThreads, smem, stream>>>(L, M, rows_per_tile, out_rows, stats, k_slots, k_tiles);
+    e = launch_after(dkv, dim3(grid(k_tiles)), kThreads, smem, stream, L, M, rows_per_tile, out_rows, stats, k_slots, k_tiles,
+                     counters);
+    if (e != cudaSuccess) return e;
     const long long q_slots = L.q_off ? static_cast<long long>(L.query_rows) / rows_per_tile + L.items
                                       : static_cast<long long>(L.items) * ((L.query_rows + rows_per_tile - 1) / rows_per_tile);
     const long long q_tiles = q_slots * L.key_heads;
-    dq<<<grid(q_tiles), kThreads, smem, stream>>>(L, M, rows_per_tile, out_rows, stats, partials, q_slots, q_tiles);
+    dq<<<grid(q_tiles), kThreads, smem, stream>>>(L, M, rows_per_tile, out_rows, stats, partials, q_slots, q_tiles, counters + 1);
     if (partials) {
         const long long all = static_cast<long long>(L.query_rows) * L.query_heads * L.head_dim;
         dq_sum_kernel<T><<<static_cast<unsigned>((all / 8 + 255) / 256), 256, 0, stream>>>(L, partials);
@@ -754,7 +776,7 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
 size_t backward_tiles_workspace(const AttentionLaunch &L) {
     const size_t partials = L.q_off ? 0
                                     : static_cast<size_t>(L.items) * L.query_rows * L.query_heads * L.head_dim * sizeof(float);
-    return stats_bytes(L) + align256(partials);
+    return kCounterBytes + stats_bytes(L) + align256(partials);
 }
 
 // Needs at least one query row and one state (the tensor maps have no empty form).

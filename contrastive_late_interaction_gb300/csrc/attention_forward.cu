@@ -14,15 +14,16 @@
 // share a key head are packed next to one another, so K and V are read once
 // for all of them.  A CTA takes two tiles at a time against blocks of 128
 // states, one persistent CTA per SM.  Warp roles:
-//   0      finds the next pair of tiles (find_item) and issues the TMA loads:
-//          Q, and K and V blocks through a ring of four stages;
+//   0      issues the TMA loads: Q, and K and V blocks through a ring of four
+//          stages;
 //   1      issues the products: S = Q K^T into TMEM, then O += P V with P read
 //          from TMEM, alternating between the two tiles so that one tile's
 //          softmax runs under the other's products;
 //   2      makes V blocks safe: rows past the item's end and dropped rows are
 //          zeroed (0 x NaN would reach the output through the product), and
 //          the dropped states' bits are gathered;
-//   3      checks the offsets of every item;
+//   3      hands out the pairs of tiles, some ahead, and checks the offsets of
+//          every item;
 //   4..11  softmax, four warps a tile, one row a thread: S from TMEM, P back
 //          over the same columns, and at the end O / l to global memory.
 // TMEM: S0 | S1 | O0 | O1, 128 columns each.
@@ -38,7 +39,8 @@ namespace {
 constexpr int kStages = 4;   // even: K blocks in the even stages, V blocks in the odd ones
 constexpr int kThreads = 384;
 constexpr int kBits = 4;
-constexpr int kReaders = 10;   // of a published pair: warp 1, warp 2, eight softmax warps
+constexpr int kPairs = 4;
+constexpr int kReaders = 11;   // of a published pair: warps 0 to 2, eight softmax warps
 
 struct Pair {
     int q0, o0, rows, k0, nk, head;   // rows < 0: no more work
@@ -49,8 +51,8 @@ struct Storage {
     alignas(1024) uint8_t q[2][BOXES * kBoxBytes];
     alignas(1024) uint8_t kv[kStages][BOXES * kBoxBytes];
     uint32_t bits[kBits][4];
-    Pair pair[2];
-    uint64_t pair_full[2], pair_empty[2];
+    Pair pair[kPairs];
+    uint64_t pair_full[kPairs], pair_empty[kPairs];
     uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages], v_ready[kStages], bits_full[kBits];
     uint64_t s_full[2], p_ready[2], o_full[2], done;
     uint32_t tmem_base;
@@ -64,15 +66,13 @@ struct Maps {
 template <typename T, int BOXES>
 __global__ void __launch_bounds__(kThreads, 1)
     forward_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
-                   long long slots, long long tiles) {
+                   long long slots, long long tiles, unsigned long long *counter) {
     extern __shared__ uint8_t smem_raw[];
     using Smem = Storage<BOXES>;
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.pair_full[i], 1);
-            mbar_init(&sm.pair_empty[i], kReaders);
             mbar_init(&sm.q_full[i], 1);
             mbar_init(&sm.q_empty[i], 1);
             mbar_init(&sm.s_full[i], 1);
@@ -85,6 +85,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.v_ready[i], 1);
         }
         for (int i = 0; i < kBits; ++i) mbar_init(&sm.bits_full[i], 1);
+        for (int i = 0; i < kPairs; ++i) {
+            mbar_init(&sm.pair_full[i], 1);
+            mbar_init(&sm.pair_empty[i], kReaders);
+        }
         mbar_init(&sm.done, 1);
         sm.abort_flag = 0;
         fence_mbar_init();
@@ -96,50 +100,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    after_previous();
     const uint32_t tmem = sm.tmem_base;
     volatile int *abort_flag = &sm.abort_flag;
     const int group = L.group, dim = L.head_dim, span = 2 * rows_per_tile;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, L.status); };
     // The next published pair, for a reader; false where there is none or the CTA gave up.
     auto next_pair = [&](uint32_t it, Pair &p) {
-        if (!wait(&sm.pair_full[it & 1], (it >> 1) & 1)) return false;
-        p = sm.pair[it & 1];
+        if (!wait(&sm.pair_full[it % kPairs], (it / kPairs) & 1)) return false;
+        p = sm.pair[it % kPairs];
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.pair_empty[it & 1]);
+        if (lane == 0) mbar_arrive(&sm.pair_empty[it % kPairs]);
         return p.rows >= 0;
     };
 
     if (warp == 0) {
-        // ------------------------------------------------------------ work and TMA
-        uint32_t it = 0, entry = 0, q_phase = 0;
+        // ------------------------------------------------------------ TMA
+        uint32_t entry = 0, q_phase = 0;
         bool ok = true;
         const uint32_t q_bytes = BOXES * static_cast<uint32_t>(rows_per_tile * group) * 128u;
-        const int per_item = L.q_off ? 0 : (L.query_rows + span - 1) / span;
-        for (long long id = blockIdx.x; ok; id += gridDim.x) {
-            Pair p = {0, 0, -1, 0, 0, 0};
-            if (id < tiles) {
-                const long long x = id % slots;
-                int i;
-                long long block;
-                if (L.q_off) {
-                    i = find_item(L.q_off, L.items, span, x, lane);
-                    block = x - (static_cast<long long>(L.q_off[i] / span) + i);
-                } else {
-                    i = static_cast<int>(x / per_item);
-                    block = x - static_cast<long long>(i) * per_item;
-                }
-                const Item t = load_item(L, i);
-                if (!t.ok || block < 0 || block * span >= t.nq) continue;   // an empty slot
-                const int r0 = static_cast<int>(block) * span;
-                p = {t.q0 + r0, t.o0 + r0, min(span, t.nq - r0), t.k0, t.nk, static_cast<int>(id / slots)};
-            }
-            if (!wait(&sm.pair_empty[it & 1], ((it >> 1) & 1) ^ 1)) break;
-            if (lane == 0) {
-                sm.pair[it & 1] = p;
-                mbar_arrive(&sm.pair_full[it & 1]);
-            }
-            ++it;
-            if (p.rows < 0) break;
+        Pair p;
+        for (uint32_t it = 0; ok && next_pair(it, p); ++it) {
             const int blocks = (p.nk + 127) / 128, nt = p.rows > rows_per_tile ? 2 : 1;
             if (lane == 0 && blocks) {
                 auto load = [&](uint8_t *dst, const CUtensorMap *map, uint64_t *bar, int head, int row) {
@@ -267,6 +248,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 3) {
+        // ------------------------------------------------------------ work
+        const int per_item = L.q_off ? 0 : (L.query_rows + span - 1) / span, batch = batch_of(tiles);
+        uint32_t it = 0;
+        bool ok = true;
+        auto publish = [&](const Pair &p) {
+            if (!wait(&sm.pair_empty[it % kPairs], ((it / kPairs) & 1) ^ 1)) return false;
+            if (lane == 0) {
+                sm.pair[it % kPairs] = p;
+                mbar_arrive(&sm.pair_full[it % kPairs]);
+            }
+            ++it;
+            return true;
+        };
+        while (ok) {
+            unsigned long long base = 0;
+            if (lane == 0) base = atomicAdd(counter, static_cast<unsigned long long>(batch));
+            base = __shfl_sync(0xffffffffu, base, 0);
+            if (base >= static_cast<unsigned long long>(tiles)) break;
+            const long long id = static_cast<long long>(base) + lane;
+            Item t;
+            int r0 = 0;
+            const bool on = lane < batch && id < tiles &&
+                            find_block(L, L.q_off, span, per_item, false, id % slots, t, r0);
+            for (uint32_t left = __ballot_sync(0xffffffffu, on); left && ok; left &= left - 1) {
+                const int from = __ffs(left) - 1;
+                Pair p = {t.q0 + r0, t.o0 + r0, min(span, t.nq - r0), t.k0, t.nk, static_cast<int>(id / slots)};
+                p.q0 = __shfl_sync(0xffffffffu, p.q0, from);
+                p.o0 = __shfl_sync(0xffffffffu, p.o0, from);
+                p.rows = __shfl_sync(0xffffffffu, p.rows, from);
+                p.k0 = __shfl_sync(0xffffffffu, p.k0, from);
+                p.nk = __shfl_sync(0xffffffffu, p.nk, from);
+                p.head = __shfl_sync(0xffffffffu, p.head, from);
+                ok = publish(p);
+            }
+        }
+        if (ok) publish({0, 0, -1, 0, 0, 0});
         check_items(L, static_cast<long long>(blockIdx.x) * 32 + lane, static_cast<long long>(gridDim.x) * 32);
     } else {
         // ------------------------------------------------------------ softmax
@@ -463,8 +480,9 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(tiles < L.sm_count ? tiles : L.sm_count);
-    kernel<<<grid, kThreads, smem, stream>>>(L, M, rows_per_tile, slots, tiles);
-    return cudaGetLastError();
+    unsigned long long *counters = reinterpret_cast<unsigned long long *>(L.workspace);
+    begin_kernel<<<1, 32, 0, stream>>>(L.status, counters);
+    return launch_after(kernel, dim3(grid), kThreads, smem, stream, L, M, rows_per_tile, slots, tiles, counters);
 }
 
 }  // namespace

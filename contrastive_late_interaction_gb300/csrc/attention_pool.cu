@@ -707,7 +707,8 @@ bool few_rows(const AttentionLaunch &L) { return static_cast<long long>(L.max_q)
 
 size_t attention_workspace(const AttentionLaunch &L) {
     using namespace attn;
-    if (!L.query_rows || !L.key_rows || !few_rows(L)) return 0;
+    if (!L.query_rows || !L.key_rows) return 0;
+    if (!few_rows(L)) return kCounterBytes;
     const Cut c = cut_of(L);
     if (c.chunk >= L.max_k) return 0;
     return part_bytes(L, c.slots, c) + align256(static_cast<size_t>(c.slots) * L.key_heads * c.rows * sizeof(float2));
@@ -723,24 +724,28 @@ size_t attention_backward_workspace(const AttentionLaunch &L) {
 
 cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t stream) {
     using namespace attn;
+    if (L.query_rows && L.key_rows && !few_rows(L)) return launch_forward_tiles(L, stream);
+    const cudaError_t e = cudaMemsetAsync(L.status, 0, sizeof(int32_t), stream);
+    if (e != cudaSuccess) return e;
     const long long out_rows = static_cast<long long>(L.query_rows) * (L.q_off ? 1 : L.items);
     if (!L.query_rows || !L.key_rows) {
         empty(L, L.o, out_rows, L.query_heads, L.lse, stream);
         return cudaGetLastError();
     }
-    if (!few_rows(L)) return launch_forward_tiles(L, stream);
     return L.dtype == CLI_BF16 ? dispatch<__nv_bfloat16>(L, false, stream) : dispatch<__half>(L, false, stream);
 }
 
 cudaError_t launch_attention_backward(const AttentionLaunch &L, cudaStream_t stream) {
     using namespace attn;
+    if (L.query_rows && L.key_rows && !few_rows(L)) return launch_backward_tiles(L, stream);
+    const cudaError_t e = cudaMemsetAsync(L.status, 0, sizeof(int32_t), stream);
+    if (e != cudaSuccess) return e;
     if (!L.query_rows || !L.key_rows) {
         empty(L, L.d_q, L.query_rows, L.query_heads, nullptr, stream);
         empty(L, L.d_k, L.key_rows, L.key_heads, nullptr, stream);
         empty(L, L.d_v, L.key_rows, L.key_heads, nullptr, stream);
         return cudaGetLastError();
     }
-    if (!few_rows(L)) return launch_backward_tiles(L, stream);
     return L.dtype == CLI_BF16 ? dispatch<__nv_bfloat16>(L, true, stream) : dispatch<__half>(L, true, stream);
 }
 
