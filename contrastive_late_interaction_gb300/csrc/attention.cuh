@@ -179,6 +179,17 @@ __device__ __forceinline__ uint32_t first_bits(int n, int w) {
     return left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
 }
 
+// The kept ones of the n states (at most 128) from k0, as bits.  One warp.
+__device__ __forceinline__ void kept_bits(const AttentionLaunch &L, int k0, int n, int lane, uint32_t (&keep)[4]) {
+    uint8_t byte[4];
+    if (L.key_mask) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) byte[w] = 32 * w + lane < n ? L.key_mask[k0 + 32 * w + lane] : 0;
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) keep[w] = L.key_mask ? __ballot_sync(0xffffffffu, byte[w] != 0) : first_bits(n, w);
+}
+
 __device__ __forceinline__ uint32_t round16(int n) { return static_cast<uint32_t>((n + 15) & ~15); }
 
 // Shared-memory tiles: rows of 64 elements (128 bytes, 128-byte swizzle), one
@@ -201,43 +212,142 @@ __device__ __forceinline__ uint64_t opaque(uint64_t d) {
     return d;
 }
 
-// D = A B^T over `steps` times 16 elements of the heads.  Unrolled: one thread
-// issues the products, and an instruction or two each is what keeps it ahead
-// of the tensor core (64 cycles a product; a loop that built its descriptors
-// took about 150).
+// Products are issued by one thread, but by code that the whole warp runs
+// along: the descriptors then are uniform values, which is where the
+// instruction wants them.  Issued from a branch of one thread, each product
+// first moved its operands there and took 97 cycles in the place of 64.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+__device__ __forceinline__ void issue_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        " .reg .pred p, q;\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void issue_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        " .reg .pred p, q;\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+// Arrives on `bar` when the products issued so far are complete.
+__device__ __forceinline__ void issue_commit(uint32_t leader, uint64_t *bar) {
+    asm volatile(
+        "{\n"
+        " .reg .pred q;\n"
+        " setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+        "}\n" ::"r"(smem_u32(bar)),
+        "r"(leader)
+        : "memory");
+}
+
+// D = A B^T over `steps` times 16 elements of the heads.
 template <int BOXES>
-__device__ __forceinline__ void mma_rows(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int steps) {
+__device__ __forceinline__ void mma_rows(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int steps) {
     a = opaque(a);
     b = opaque(b);
 #pragma unroll
     for (int k = 0; k < 4 * BOXES; ++k) {
         const uint64_t at = desc_bytes((k >> 2) * kBoxBytes + (k & 3) * 32);
-        if (k < steps) mma_bf16(d, a + at, b + at, idesc, k != 0);
+        if (k < steps) issue_ss(leader, d, a + at, b + at, idesc, k != 0);
     }
 }
 
 // D (+)= A B over `rows` rows of B, at most 16 STEPS; A in TMEM (16-bit pairs), B a tile
 // of rows of heads.
 template <int STEPS>
-__device__ __forceinline__ void mma_pairs(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int rows,
+__device__ __forceinline__ void mma_pairs(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int rows,
                                           bool accumulate) {
     b = opaque(b);
 #pragma unroll
     for (int k = 0; k < STEPS; ++k)
-        if (16 * k < rows) mma_ts(d, a + k * 8, b + desc_bytes(k * 2048), idesc, k != 0 || accumulate);
+        if (16 * k < rows) issue_ts(leader, d, a + k * 8, b + desc_bytes(k * 2048), idesc, k != 0 || accumulate);
 }
 
-// Zeroes rows of a tile of `boxes` boxes: those of the first `rows` whose bit
-// in `keep` (one word per 32 rows) is 0.  One warp.
-__device__ __forceinline__ void zero_rows(uint32_t tile, int boxes, int rows, const uint32_t (&keep)[4], int lane) {
-    const int sub = lane >> 3, chunk = lane & 7;
+// Rows of TMEM to global memory.  A thread has a row there, and rows lie apart
+// in memory: stored as they come, each 16 bytes are a request of their own
+// (5000 cycles for two tiles of 128 rows).  So 64 bytes of each of a warp's
+// rows go through 2 KB of shared memory, and a request covers 8 rows of them.
+constexpr uint32_t kRowStage = 32 * 64;   // bytes a warp
+
+// `words` gives 16 bytes (chunk c of 4) of this thread's row for the 64 bytes
+// at `at`; `out` is the row's address, `bytes` its length.
+template <typename Words>
+__device__ __forceinline__ void store_rows(uint32_t stage, bool mine, uint8_t *out, int bytes, Words &&words) {
+    const int lane = threadIdx.x & 31;
+    const unsigned long long to = mine ? reinterpret_cast<unsigned long long>(out) : 0ull;
+#pragma unroll 1
+    for (int at = 0; at < bytes; at += 64) {
+        uint4 w[4];
+        words(at, w);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            st_shared_v4(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), w[c].x, w[c].y, w[c].z, w[c].w);
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int row = 8 * x + (lane >> 2), c = lane & 3;
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(stage + row * 64 + ((c ^ ((row >> 1) & 3)) << 4))
+                         : "memory");
+            const unsigned long long p = __shfl_sync(0xffffffffu, to, row);
+            if (p && at + 16 * c < bytes) *reinterpret_cast<uint4 *>(p + at + 16 * c) = v;
+        }
+        __syncwarp();
+    }
+}
+
+// 16-bit rows of `dim` sums at `sums` in TMEM times `scale`; zeros where there are none.
+template <typename T>
+__device__ __forceinline__ void store_sums(uint32_t stage, uint32_t sums, int dim, float scale, bool have, bool mine, T *out) {
+    store_rows(stage, mine, reinterpret_cast<uint8_t *>(out), dim * 2, [&](int at, uint4 (&w)[4]) {
+        uint32_t r[32];
+        if (have) {
+            tmem_ld32_async(sums + at / 2, r);
+            tmem_wait_ld();
+            tmem_regs_ready(r);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = have && scale != 0.0f ? Type<T>::pack(__uint_as_float(r[8 * c + 2 * i]) * scale,
+                                                             __uint_as_float(r[8 * c + 2 * i + 1]) * scale)
+                                             : 0u;
+            w[c] = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    });
+}
+
+// Zeroes rows of a tile: those of the first `rows` whose bit in `keep` (one
+// word per 32 rows) is 0.  One warp, a row a lane; the lanes' chunks are
+// staggered so that they fall into different banks.
+template <int BOXES>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int rows, const uint32_t (&keep)[4], int lane) {
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-        if (32 * w >= rows || keep[w] == 0xffffffffu) continue;
-        for (int r = sub; r < 32 && 32 * w + r < rows; r += 4)
-            if (!((keep[w] >> r) & 1u))
-                for (int x = 0; x < boxes; ++x)
-                    st_shared_v4(tile + x * kBoxBytes + (32 * w + r) * 128 + chunk * 16, 0, 0, 0, 0);
+        const bool drop = !((keep[w] >> lane) & 1u) && 32 * w + lane < rows;
+        if (!__any_sync(0xffffffffu, drop)) continue;
+        if (drop)
+#pragma unroll
+            for (int i = 0; i < 8 * BOXES; ++i)
+                st_shared_v4(tile + (i >> 3) * kBoxBytes + (32 * w + lane) * 128 + (((i + lane) & 7) << 4), 0, 0, 0, 0);
     }
 }
 

@@ -86,6 +86,7 @@ template <int BOXES>
 struct Storage {
     alignas(1024) uint8_t held[2][BOXES * kBoxBytes];      // K and V, or Q and dO
     alignas(1024) uint8_t ring[2][2][BOXES * kBoxBytes];   // stages of (Q, dO), or of (K, V)
+    alignas(16) uint8_t rows[8][kRowStage];                 // an arithmetic warp's rows on their way out
     alignas(16) float stat[2][2][128];                      // dkv: lse and delta of a stage's rows
     uint32_t bits[4][4];                                    // dq: a block's kept states
     Work work[kWorks];
@@ -224,31 +225,6 @@ struct Producer {
     }
 };
 
-// A row of sums from TMEM, scaled, to `out`.
-template <typename T>
-__device__ __forceinline__ void store_sums(uint32_t at, int dim, float scale, bool have, bool mine, T *out) {
-#pragma unroll 1
-    for (int x = 0; x < dim; x += 16) {
-        uint32_t o[16];
-        if (have) {
-            tmem_ld16_async(at + x, o);
-            tmem_wait_ld();
-            tmem_regs_ready_n(o);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (!mine || x + 8 * h >= dim) continue;
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = have ? Type<T>::pack(__uint_as_float(o[8 * h + 2 * i]) * scale,
-                                            __uint_as_float(o[8 * h + 2 * i + 1]) * scale)
-                            : 0u;
-            *reinterpret_cast<uint4 *>(out + x + 8 * h) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-    }
-}
-
 // ----------------------------------------------------------------------------
 // dK, dV
 // ----------------------------------------------------------------------------
@@ -264,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     using Smem = Storage<BOXES>;
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t tmem = begin(sm, M);
     const int group = L.group, dim = L.head_dim;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, &sm.abort_flag, L.status); };
@@ -286,66 +262,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) P.drain();
     } else if (warp == 1) {
-        const uint32_t idesc_s = idesc_16bit(Type<T>::bf16, 128, 0, 0, 0);
+        const uint32_t idesc_s = idesc_16bit(Type<T>::bf16, 128, 0, 0, 0);   // N by block
         const uint32_t idesc_d = idesc_16bit(Type<T>::bf16, 128, round16(dim), 0, 1);
-        uint32_t entry = 0, held = 0, j_all = 0;
-        bool ok = true;
-        Work w;
         const uint64_t held_desc = desc_rows(smem_u32(sm.held[0])), ring_desc = desc_rows(smem_u32(sm.ring[0][0]));
         const uint64_t sum_desc = desc_sum(smem_u32(sm.ring[0][0]));
         constexpr uint64_t kTile = desc_bytes(BOXES * kBoxBytes);
         const int steps = (dim + 15) / 16;
-        for (uint32_t it = 0; ok && next_work(sm, L, it, w); ++it) {
+        const uint32_t leader = lane == 0, tm = uniform(tmem);
+        uint32_t entry = 0, held = 0, j_all = 0;
+        bool ok = true;
+        auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+        Work w;
+        for (uint32_t it = 0; ok && __all_sync(0xffffffffu, next_work(sm, L, it, w)); ++it) {
+            w.nq = static_cast<int>(uniform(w.nq));
             const int blocks = q_blocks(w);
-            if (lane == 0 && blocks) {
-                // A 16-bit TMEM operand whose halves lie 64 columns apart.
-                auto sum = [&](uint32_t d, uint32_t a, uint64_t b, int rows, bool more) {
-                    mma_pairs<4>(d, a, b, idesc_d, rows, more);
-                    mma_pairs<4>(d, a + 64, b + desc_bytes(4 * 2048), idesc_d, rows - 64, true);
-                };
-                auto scores = [&](int j, uint32_t e, int which) {
-                    const uint32_t n = round16(q_rows(w, j));
-                    mma_rows<BOXES>(tmem + which * 128, held_desc + which * kTile, ring_desc + ((e & 1) * 2 + which) * kTile,
-                                    idesc_s | (n >> 3) << 17, steps);
-                    mma_commit(which ? &sm.dp_full : &sm.s_full[0]);
-                };
-                ok = wait(&sm.held_full, held & 1) && wait(&sm.ring_ready[entry & 1], (entry >> 1) & 1);
-                ++held;
-                tc_fence_after();
-                if (ok) {
-                    scores(0, entry, 0);
-                    scores(0, entry, 1);
-                    if (blocks == 1) mma_commit(&sm.held_empty);
-                }
-                for (int j = 0; j < blocks && ok; ++j, ++j_all) {
-                    const uint32_t e = entry + j, en = e + 1;
-                    if (!wait(&sm.p_ready, j_all & 1)) { ok = false; break; }
-                    tc_fence_after();
-                    sum(tmem + 256, tmem, sum_desc + ((e & 1) * 2 + 1) * kTile, q_rows(w, j), j != 0);
-                    if (j + 1 < blocks) {
-                        if (!wait(&sm.ring_ready[en & 1], (en >> 1) & 1)) { ok = false; break; }
-                        tc_fence_after();
-                        scores(j + 1, en, 0);
-                    }
-                    if (!wait(&sm.ds_ready[0], j_all & 1)) { ok = false; break; }
-                    tc_fence_after();
-                    sum(tmem + 384, tmem + 128, sum_desc + (e & 1) * 2 * kTile, q_rows(w, j), j != 0);
-                    mma_commit(&sm.ring_empty[e & 1]);
-                    if (j + 1 < blocks) {
-                        scores(j + 1, en, 1);
-                        if (j + 2 == blocks) mma_commit(&sm.held_empty);
-                    } else {
-                        mma_commit(&sm.sum_full);
-                    }
-                }
-                entry += blocks;
+            if (blocks == 0) continue;
+            // A 16-bit TMEM operand whose halves lie 64 columns apart.
+            auto sum = [&](uint32_t d, uint32_t a, uint64_t b, int rows, bool more) {
+                mma_pairs<4>(leader, d, a, b, idesc_d, rows, more);
+                mma_pairs<4>(leader, d, a + 64, b + desc_bytes(4 * 2048), idesc_d, rows - 64, true);
+            };
+            auto scores = [&](int j, uint32_t e, int which) {
+                const uint32_t n = round16(q_rows(w, j));
+                mma_rows<BOXES>(leader, tm + which * 128, held_desc + which * kTile, ring_desc + ((e & 1) * 2 + which) * kTile,
+                                idesc_s | (n >> 3) << 17, steps);
+                issue_commit(leader, which ? &sm.dp_full : &sm.s_full[0]);
+            };
+            ok = wait_all(&sm.held_full, held & 1) && wait_all(&sm.ring_ready[entry & 1], (entry >> 1) & 1);
+            ++held;
+            tc_fence_after();
+            if (ok) {
+                scores(0, entry, 0);
+                scores(0, entry, 1);
+                if (blocks == 1) issue_commit(leader, &sm.held_empty);
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            for (int j = 0; j < blocks && ok; ++j, ++j_all) {
+                const uint32_t e = entry + j, en = e + 1;
+                if (!wait_all(&sm.p_ready, j_all & 1)) { ok = false; break; }
+                tc_fence_after();
+                sum(tm + 256, tm, sum_desc + ((e & 1) * 2 + 1) * kTile, q_rows(w, j), j != 0);
+                if (j + 1 < blocks) {
+                    if (!wait_all(&sm.ring_ready[en & 1], (en >> 1) & 1)) { ok = false; break; }
+                    tc_fence_after();
+                    scores(j + 1, en, 0);
+                }
+                if (!wait_all(&sm.ds_ready[0], j_all & 1)) { ok = false; break; }
+                tc_fence_after();
+                sum(tm + 384, tm + 128, sum_desc + (e & 1) * 2 * kTile, q_rows(w, j), j != 0);
+                issue_commit(leader, &sm.ring_empty[e & 1]);
+                if (j + 1 < blocks) {
+                    scores(j + 1, en, 1);
+                    if (j + 2 == blocks) issue_commit(leader, &sm.held_empty);
+                } else {
+                    issue_commit(leader, &sm.sum_full);
+                }
+            }
+            entry += blocks;
         }
-        if (lane == 0) {
-            mma_commit(&sm.done);
-            wait(&sm.done, 0);
-        }
+        issue_commit(leader, &sm.done);
+        wait(&sm.done, 0);
     } else if (warp == 2) {
         // Rows past the item's end are zeroed (they are summed over), and the rows' lse and delta staged.
         uint32_t entry = 0;
@@ -370,8 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sm.stat[s][1][32 * i + lane] = f[i].y;
                 }
                 const uint32_t keep[4] = {first_bits(n, 0), first_bits(n, 1), first_bits(n, 2), first_bits(n, 3)};
-                zero_rows(smem_u32(sm.ring[s][0]), BOXES, round16(n), keep, lane);
-                zero_rows(smem_u32(sm.ring[s][1]), BOXES, round16(n), keep, lane);
+                zero_rows<BOXES>(smem_u32(sm.ring[s][0]), round16(n), keep, lane);
+                zero_rows<BOXES>(smem_u32(sm.ring[s][1]), round16(n), keep, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.ring_ready[s]);
@@ -459,7 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const HeadsView &v = side ? L.d_k : L.d_v;
             T *out = static_cast<T *>(v.data) + (static_cast<long long>(w.k0) + row) * v.row + w.head * v.head;
-            store_sums<T>(tmem + lanes + 256 + side * 128, dim, side ? L.scale : 1.0f, blocks != 0, mine, out);
+            store_sums<T>(smem_u32(sm.rows[warp - 4]), tmem + lanes + 256 + side * 128, dim, side ? L.scale : 1.0f, blocks != 0, mine,
+                          out);
             tc_fence_before();
         }
     }
@@ -484,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     using Smem = Storage<BOXES>;
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t tmem = begin(sm, M);
     const int group = L.group, dim = L.head_dim;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, &sm.abort_flag, L.status); };
@@ -504,64 +480,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) P.drain();
     } else if (warp == 1) {
-        const uint32_t idesc_s = idesc_16bit(Type<T>::bf16, 128, 0, 0, 0);
+        const uint32_t idesc_s = idesc_16bit(Type<T>::bf16, 128, 0, 0, 0);   // N by block
         const uint32_t idesc_d = idesc_16bit(Type<T>::bf16, 128, round16(dim), 0, 1);
         const uint64_t held_desc = desc_rows(smem_u32(sm.held[0])), ring_desc = desc_rows(smem_u32(sm.ring[0][0]));
         const uint64_t sum_desc = desc_sum(smem_u32(sm.ring[0][0]));
         constexpr uint64_t kTile = desc_bytes(BOXES * kBoxBytes);
         const int steps = (dim + 15) / 16;
+        const uint32_t leader = lane == 0, tm = uniform(tmem);
         uint32_t entry = 0, held = 0, j_all = 0;
         bool ok = true;
+        auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
         Work w;
-        for (uint32_t it = 0; ok && next_work(sm, L, it, w); ++it) {
-            const int blocks = (w.nk + 127) / 128;
-            if (lane == 0 && blocks) {
-                auto scores = [&](int j, uint32_t e, int which) {
-                    const uint32_t n = round16(min(128, w.nk - 128 * j));
-                    const uint32_t d = which ? tmem + 256 : tmem + (e & 1) * 128;
-                    mma_rows<BOXES>(d, held_desc + which * kTile, ring_desc + ((e & 1) * 2 + which) * kTile,
-                                    idesc_s | (n >> 3) << 17, steps);
-                    mma_commit(which ? &sm.dp_full : &sm.s_full[e & 1]);
-                };
-                ok = wait(&sm.held_full, held & 1) && wait(&sm.ring_ready[entry & 1], (entry >> 1) & 1);
-                ++held;
-                tc_fence_after();
-                if (ok) {
-                    scores(0, entry, 0);
-                    scores(0, entry, 1);
-                    if (blocks == 1) mma_commit(&sm.held_empty);
-                }
-                for (int j = 0; j < blocks && ok; ++j, ++j_all) {
-                    const uint32_t e = entry + j, en = e + 1;
-                    if (j + 1 < blocks) {
-                        if (!wait(&sm.ring_ready[en & 1], (en >> 1) & 1)) { ok = false; break; }
-                        tc_fence_after();
-                        scores(j + 1, en, 0);
-                    }
-                    if (!wait(&sm.p_ready, j_all & 1)) { ok = false; break; }
-                    tc_fence_after();
-                    if (j + 1 < blocks) {
-                        scores(j + 1, en, 1);
-                        if (j + 2 == blocks) mma_commit(&sm.held_empty);
-                    }
-                    if (!wait(&sm.ds_ready[j_all & 1], (j_all >> 1) & 1)) { ok = false; break; }
-                    tc_fence_after();
-                    const int n = min(128, w.nk - 128 * j);
-                    const uint32_t a = tmem + (e & 1) * 128;
-                    const uint64_t b = sum_desc + (e & 1) * 2 * kTile;
-                    mma_pairs<4>(tmem + 384, a, b, idesc_d, n, j != 0);
-                    mma_pairs<4>(tmem + 384, a + 64, b + desc_bytes(4 * 2048), idesc_d, n - 64, true);
-                    mma_commit(&sm.ring_empty[e & 1]);
-                    if (j + 1 == blocks) mma_commit(&sm.sum_full);
-                }
-                entry += blocks;
+        for (uint32_t it = 0; ok && __all_sync(0xffffffffu, next_work(sm, L, it, w)); ++it) {
+            const int nk = static_cast<int>(uniform(w.nk)), blocks = (nk + 127) / 128;
+            if (blocks == 0) continue;
+            auto scores = [&](int j, uint32_t e, int which) {
+                const uint32_t n = round16(min(128, nk - 128 * j));
+                const uint32_t d = which ? tm + 256 : tm + (e & 1) * 128;
+                mma_rows<BOXES>(leader, d, held_desc + which * kTile, ring_desc + ((e & 1) * 2 + which) * kTile,
+                                idesc_s | (n >> 3) << 17, steps);
+                issue_commit(leader, which ? &sm.dp_full : &sm.s_full[e & 1]);
+            };
+            ok = wait_all(&sm.held_full, held & 1) && wait_all(&sm.ring_ready[entry & 1], (entry >> 1) & 1);
+            ++held;
+            tc_fence_after();
+            if (ok) {
+                scores(0, entry, 0);
+                scores(0, entry, 1);
+                if (blocks == 1) issue_commit(leader, &sm.held_empty);
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            for (int j = 0; j < blocks && ok; ++j, ++j_all) {
+                const uint32_t e = entry + j, en = e + 1;
+                if (j + 1 < blocks) {
+                    if (!wait_all(&sm.ring_ready[en & 1], (en >> 1) & 1)) { ok = false; break; }
+                    tc_fence_after();
+                    scores(j + 1, en, 0);
+                }
+                if (!wait_all(&sm.p_ready, j_all & 1)) { ok = false; break; }
+                tc_fence_after();
+                if (j + 1 < blocks) {
+                    scores(j + 1, en, 1);
+                    if (j + 2 == blocks) issue_commit(leader, &sm.held_empty);
+                }
+                if (!wait_all(&sm.ds_ready[j_all & 1], (j_all >> 1) & 1)) { ok = false; break; }
+                tc_fence_after();
+                const int n = min(128, nk - 128 * j);
+                const uint32_t a = tm + (e & 1) * 128;
+                const uint64_t b = sum_desc + (e & 1) * 2 * kTile;
+                mma_pairs<4>(leader, tm + 384, a, b, idesc_d, n, j != 0);
+                mma_pairs<4>(leader, tm + 384, a + 64, b + desc_bytes(4 * 2048), idesc_d, n - 64, true);
+                issue_commit(leader, &sm.ring_empty[e & 1]);
+                if (j + 1 == blocks) issue_commit(leader, &sm.sum_full);
+            }
+            entry += blocks;
         }
-        if (lane == 0) {
-            mma_commit(&sm.done);
-            wait(&sm.done, 0);
-        }
+        issue_commit(leader, &sm.done);
+        wait(&sm.done, 0);
     } else if (warp == 2) {
         // Dropped states and those past the item's end: their K rows are zeroed (they are summed over), and
         // their bits staged.  V's rows only reach their own columns of dP, which are not used.
@@ -573,20 +547,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < blocks; ++j, ++entry) {
                 const int n = min(128, w.nk - 128 * j);
                 uint32_t keep[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int at = 32 * k + lane;
-                    keep[k] = first_bits(n, k);
-                    if (L.key_mask)
-                        keep[k] = __ballot_sync(0xffffffffu, at < n && L.key_mask[w.k0 + 128 * j + at] != 0);
-                }
+                kept_bits(L, w.k0 + 128 * j, n, lane, keep);
                 const uint32_t s = entry & 1;
                 if (!wait(&sm.ring_full[s], (entry >> 1) & 1)) { ok = false; break; }
                 if (lane == 0) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) sm.bits[entry & 3][k] = keep[k];
                 }
-                zero_rows(smem_u32(sm.ring[s][0]), BOXES, round16(n), keep, lane);
+                zero_rows<BOXES>(smem_u32(sm.ring[s][0]), round16(n), keep, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.ring_ready[s]);
@@ -671,27 +639,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
             }
             const int head = w.head * group + head_in;
-            if (side == 0) {
-                if (partials) {
-                    float *out = partials + ((static_cast<long long>(w.o0) + r_in) * L.query_heads + head) * dim;
-#pragma unroll 1
-                    for (int x = 0; x < dim; x += 16) {
-                        uint32_t o[16];
-                        if (blocks) {
-                            tmem_ld16_async(tmem + lanes + 384 + x, o);
-                            tmem_wait_ld();
-                            tmem_regs_ready_n(o);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4)
-                            if (mine && x + i < dim)
-                                *reinterpret_cast<uint4 *>(out + x + i) =
-                                    blocks ? make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]) : make_uint4(0, 0, 0, 0);
+            // The sides take half of the row's columns each (of whole 64 bytes).
+            const uint32_t stage = smem_u32(sm.rows[warp - 4]);
+            const int half = partials ? (dim / 2 + 15) & ~15 : (dim / 2 + 31) & ~31;
+            const int first = side ? half : 0, count = max(0, side ? dim - half : min(half, dim));
+            const uint32_t sums = tmem + lanes + 384 + first;
+            if (partials) {
+                float *out = partials + ((static_cast<long long>(w.o0) + r_in) * L.query_heads + head) * dim + first;
+                store_rows(stage, mine, reinterpret_cast<uint8_t *>(out), count * 4, [&](int at, uint4 (&v)[4]) {
+                    uint32_t o[16] = {};
+                    if (blocks) {
+                        tmem_ld16_async(sums + at / 4, o);
+                        tmem_wait_ld();
+                        tmem_regs_ready_n(o);
                     }
-                } else {
-                    T *out = static_cast<T *>(L.d_q.data) + (static_cast<long long>(w.q0) + r_in) * L.d_q.row + head * L.d_q.head;
-                    store_sums<T>(tmem + lanes + 384, dim, L.scale, blocks != 0, mine, out);
-                }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                });
+            } else {
+                T *out = static_cast<T *>(L.d_q.data) + (static_cast<long long>(w.q0) + r_in) * L.d_q.row + head * L.d_q.head + first;
+                store_sums<T>(stage, sums, count, L.scale, blocks != 0, mine, out);
             }
             tc_fence_before();
         }

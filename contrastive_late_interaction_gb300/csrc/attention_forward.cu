@@ -19,9 +19,10 @@
 //   1      issues the products: S = Q K^T into TMEM, then O += P V with P read
 //          from TMEM, alternating between the two tiles so that one tile's
 //          softmax runs under the other's products;
-//   2      makes V blocks safe: rows past the item's end and dropped rows are
-//          zeroed (0 x NaN would reach the output through the product), and
-//          the dropped states' bits are gathered;
+//   2      makes the blocks safe: V's rows past the item's end and dropped
+//          rows of K and V are zeroed (0 x NaN would reach the output through
+//          the product), and the dropped states are listed, as bits and as
+//          what is added to a score: 0 or -infinity;
 //   3      hands out the pairs of tiles, some ahead, and checks the offsets of
 //          every item;
 //   4..11  softmax, four warps a tile, one row a thread: S from TMEM, P back
@@ -50,10 +51,12 @@ template <int BOXES>
 struct Storage {
     alignas(1024) uint8_t q[2][BOXES * kBoxBytes];
     alignas(1024) uint8_t kv[kStages][BOXES * kBoxBytes];
+    alignas(16) uint8_t rows[8][kRowStage];   // a softmax warp's rows on their way out
+    alignas(16) float bias[kBits][128];
     uint32_t bits[kBits][4];
     Pair pair[kPairs];
     uint64_t pair_full[kPairs], pair_empty[kPairs];
-    uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages], v_ready[kStages], bits_full[kBits];
+    uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages], ready[kStages], bits_full[kBits];
     uint64_t s_full[2], p_ready[2], o_full[2], done;
     uint32_t tmem_base;
     int abort_flag;
@@ -70,7 +73,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     using Smem = Storage<BOXES>;
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_full[i], 1);
@@ -82,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sm.kv_full[i], 1);
             mbar_init(&sm.kv_empty[i], 1);
-            mbar_init(&sm.v_ready[i], 1);
+            mbar_init(&sm.ready[i], 1);
         }
         for (int i = 0; i < kBits; ++i) mbar_init(&sm.bits_full[i], 1);
         for (int i = 0; i < kPairs; ++i) {
@@ -164,59 +167,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t v_desc = desc_sum(smem_u32(sm.kv[0]));
         constexpr uint64_t kTile = desc_bytes(BOXES * kBoxBytes);
         const int steps = (dim + 15) / 16;
+        uint64_t *k_bars = L.key_mask ? sm.ready : sm.kv_full;
+        const uint32_t leader = lane == 0, tm = uniform(tmem);
         uint32_t entry = 0, q_phase = 0, p_phase = 0;
         bool ok = true;
+        auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
         Pair p;
-        for (uint32_t it = 0; ok && next_pair(it, p); ++it) {
-            const int blocks = (p.nk + 127) / 128, nt = p.rows > rows_per_tile ? 2 : 1;
-            if (lane == 0 && blocks) {
-                auto scores = [&](int t, int j, uint32_t e) {
-                    const uint32_t n = round16(min(128, p.nk - 128 * j));
-                    mma_rows<BOXES>(tmem + t * 128, q_desc + t * kTile, k_desc + (e % kStages) * kTile, idesc_s | (n >> 3) << 17,
-                                    steps);
-                    mma_commit(&sm.s_full[t]);
-                    if (j + 1 == blocks) mma_commit(&sm.q_empty[t]);
-                };
-                ok = wait(&sm.kv_full[entry % kStages], (entry / kStages) & 1);
-                for (int t = 0; t < nt && ok; ++t) {
-                    ok = wait(&sm.q_full[t], (q_phase >> t) & 1);
-                    if (!ok) break;
-                    q_phase ^= 1u << t;
-                    tc_fence_after();
-                    scores(t, 0, entry);
-                }
-                if (ok) mma_commit(&sm.kv_empty[entry % kStages]);
-                for (int j = 0; j < blocks && ok; ++j) {
-                    const uint32_t ev = entry + 2 * j + 1, ek = ev + 1;
-                    ok = wait(&sm.v_ready[ev % kStages], (ev / kStages) & 1);
-                    for (int t = 0; t < nt && ok; ++t) {
-                        if (!wait(&sm.p_ready[t], (p_phase >> t) & 1)) { ok = false; break; }
-                        p_phase ^= 1u << t;
-                        tc_fence_after();
-                        mma_pairs<8>(tmem + 256 + t * 128, tmem + t * 128, v_desc + (ev % kStages) * kTile, idesc_o,
-                                     min(128, p.nk - 128 * j), j != 0);
-                        if (j + 1 == blocks) {
-                            mma_commit(&sm.o_full[t]);
-                        } else {
-                            if (t == 0 && !wait(&sm.kv_full[ek % kStages], (ek / kStages) & 1)) { ok = false; break; }
-                            tc_fence_after();
-                            scores(t, j + 1, ek);
-                        }
-                    }
-                    if (!ok) break;
-                    mma_commit(&sm.kv_empty[ev % kStages]);
-                    if (j + 1 < blocks) mma_commit(&sm.kv_empty[ek % kStages]);
-                }
-                entry += 2 * blocks;
+        for (uint32_t it = 0; ok && __all_sync(0xffffffffu, next_pair(it, p)); ++it) {
+            const int nk = static_cast<int>(uniform(p.nk)), rows = static_cast<int>(uniform(p.rows));
+            const int blocks = (nk + 127) / 128, nt = rows > rows_per_tile ? 2 : 1;
+            if (blocks == 0) continue;
+            auto scores = [&](int t, int j, uint32_t e) {
+                const uint32_t n = round16(min(128, nk - 128 * j));
+                mma_rows<BOXES>(leader, tm + t * 128, q_desc + t * kTile, k_desc + (e % kStages) * kTile,
+                                idesc_s | (n >> 3) << 17, steps);
+                issue_commit(leader, &sm.s_full[t]);
+                if (j + 1 == blocks) issue_commit(leader, &sm.q_empty[t]);
+            };
+            ok = wait_all(&k_bars[entry % kStages], (entry / kStages) & 1);
+            for (int t = 0; t < nt && ok; ++t) {
+                ok = wait_all(&sm.q_full[t], (q_phase >> t) & 1);
+                if (!ok) break;
+                q_phase ^= 1u << t;
+                tc_fence_after();
+                scores(t, 0, entry);
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (ok) issue_commit(leader, &sm.kv_empty[entry % kStages]);
+            for (int j = 0; j < blocks && ok; ++j) {
+                const uint32_t ev = entry + 2 * j + 1, ek = ev + 1;
+                ok = wait_all(&sm.ready[ev % kStages], (ev / kStages) & 1);
+                for (int t = 0; t < nt && ok; ++t) {
+                    if (!wait_all(&sm.p_ready[t], (p_phase >> t) & 1)) { ok = false; break; }
+                    p_phase ^= 1u << t;
+                    tc_fence_after();
+                    mma_pairs<8>(leader, tm + 256 + t * 128, tm + t * 128, v_desc + (ev % kStages) * kTile, idesc_o,
+                                 min(128, nk - 128 * j), j != 0);
+                    if (j + 1 == blocks) {
+                        issue_commit(leader, &sm.o_full[t]);
+                    } else {
+                        if (t == 0 && !wait_all(&k_bars[ek % kStages], (ek / kStages) & 1)) { ok = false; break; }
+                        tc_fence_after();
+                        scores(t, j + 1, ek);
+                    }
+                }
+                if (!ok) break;
+                issue_commit(leader, &sm.kv_empty[ev % kStages]);
+                if (j + 1 < blocks) issue_commit(leader, &sm.kv_empty[ek % kStages]);
+            }
+            entry += 2 * blocks;
         }
-        if (lane == 0) {
-            mma_commit(&sm.done);
-            wait(&sm.done, 0);
-        }
+        issue_commit(leader, &sm.done);
+        wait(&sm.done, 0);
     } else if (warp == 2) {
-        // ------------------------------------------------------------ V blocks made safe, dropped states
+        // ------------------------------------------------------------ blocks made safe, dropped states
         uint32_t entry = 0, block = 0;
         bool ok = true;
         Pair p;
@@ -225,26 +228,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < blocks && ok; ++j, ++block, entry += 2) {
                 const int n = min(128, p.nk - 128 * j);
                 uint32_t keep[4];
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const int at = 32 * w + lane;
-                    keep[w] = first_bits(n, w);
-                    if (L.key_mask)
-                        keep[w] = __ballot_sync(0xffffffffu, at < n && L.key_mask[p.k0 + 128 * j + at] != 0);
-                }
+                kept_bits(L, p.k0 + 128 * j, n, lane, keep);
+                const uint32_t sk = entry % kStages, sv = (entry + 1) % kStages;
                 if (L.key_mask) {
-                    if (lane == 0) {
+                    const uint32_t x = block % kBits;
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) sm.bits[block % kBits][w] = keep[w];
-                        mbar_arrive(&sm.bits_full[block % kBits]);
+                    for (int w = 0; w < 4; ++w) {
+                        sm.bias[x][32 * w + lane] = (keep[w] >> lane) & 1u ? 0.0f : -INFINITY;
+                        if (lane == 0) sm.bits[x][w] = keep[w];
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.bits_full[x]);
+                    if (!wait(&sm.kv_full[sk], (entry / kStages) & 1)) { ok = false; break; }
+                    zero_rows<BOXES>(smem_u32(sm.kv[sk]), round16(n), keep, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.ready[sk]);
                 }
-                const uint32_t e = entry + 1, s = e % kStages;
-                if (!wait(&sm.kv_full[s], (e / kStages) & 1)) { ok = false; break; }
-                zero_rows(smem_u32(sm.kv[s]), BOXES, round16(n), keep, lane);
+                if (!wait(&sm.kv_full[sv], ((entry + 1) / kStages) & 1)) { ok = false; break; }
+                zero_rows<BOXES>(smem_u32(sm.kv[sv]), round16(n), keep, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.v_ready[s]);
+                if (lane == 0) mbar_arrive(&sm.ready[sv]);
             }
         }
     } else if (warp == 3) {
@@ -311,15 +316,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 phase ^= 1;
                 tc_fence_after();
                 const int n = min(128, p.nk - 128 * j);
-                const bool plain = n == 128 && !L.key_mask && sign > 0.0f;
+                const bool whole = n == 128 && sign > 0.0f, plain = whole && !L.key_mask;
+                if (L.key_mask && !wait(&sm.bits_full[block % kBits], (block / kBits) & 1)) { ok = false; break; }
+                const float4 *bias = reinterpret_cast<const float4 *>(sm.bias[block % kBits]);
                 float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
                 float2 shift = make_float2(-m * sl2, -m * sl2);
-                // The exponentials of 32 scores, packed, and added to the sums.
-                auto weights = [&](const uint32_t (&r)[32], uint32_t (&packed)[16]) {
+                // The exponentials of the 32 scores of chunk w, packed, and added to the sums.
+                auto weights = [&](const uint32_t (&r)[32], uint32_t (&packed)[16], int w, bool add) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
                         float2 a = __ffma2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), sl22, shift);
                         float2 b = __ffma2_rn(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), sl22, shift);
+                        if (add) {   // a dropped state's score is finite (its row of K is zero)
+                            const float4 x = bias[8 * w + i / 4];
+                            a = __fadd2_rn(a, make_float2(x.x, x.y));
+                            b = __fadd2_rn(b, make_float2(x.z, x.w));
+                        }
                         a = make_float2(ex2(a.x), ex2(a.y));
                         b = make_float2(ex2(b.x), ex2(b.y));
                         sum = __fadd2_rn(sum, a);
@@ -328,10 +340,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         packed[i / 2 + 1] = Type<T>::pack(b.x, b.y);
                     }
                 };
-                bool again = !plain || m == -INFINITY;
-                if (!__any_sync(0xffffffffu, again)) {
+                auto at_once = [&](bool add) {
                     // Nearly always the reference still serves: the weights are taken as the scores arrive, and
                     // thrown away in the rare block whose maximum turns out to be past it.
+                    // (A dropped state's score of 0 may be past it too: no harm, the block is done again.)
                     uint32_t a[32], b[32], packed[4][16];
                     float t0, t1, t2, t3;
                     tmem_ld32_max_async(s_at, a, t0);
@@ -339,25 +351,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_ld();
                     tmem_regs_ready(a, t0);
                     tmem_regs_ready(b, t1);
-                    weights(a, packed[0]);
+                    weights(a, packed[0], 0, add);
                     tmem_ld32_max_async(s_at + 64, a, t2);
-                    weights(b, packed[1]);
+                    weights(b, packed[1], 1, add);
                     tmem_wait_ld();
                     tmem_regs_ready(a, t2);
                     tmem_ld32_max_async(s_at + 96, b, t3);
-                    weights(a, packed[2]);
+                    weights(a, packed[2], 2, add);
                     tmem_wait_ld();
                     tmem_regs_ready(b, t3);
-                    weights(b, packed[3]);
-                    again = __any_sync(0xffffffffu, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) > m + lazy);
-                    if (!again) {
+                    weights(b, packed[3], 3, add);
+                    if (__any_sync(0xffffffffu, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) > m + lazy)) return false;
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) tmem_st16(s_at + 16 * w, packed[w]);
-                    }
-                }
-                if (__any_sync(0xffffffffu, again)) {
+                    for (int w = 0; w < 4; ++w) tmem_st16(s_at + 16 * w, packed[w]);
+                    return true;
+                };
+                bool again = !whole || __any_sync(0xffffffffu, m == -INFINITY);
+                if (!again) again = L.key_mask ? !at_once(true) : !at_once(false);
+                if (again) {
                     // The maximum first, then the weights: an item's first block, blocks with states to leave out.
-                    if (L.key_mask && !wait(&sm.bits_full[block % kBits], (block / kBits) & 1)) { ok = false; break; }
                     auto left_out = [&](uint32_t (&r)[32], int w) {
                         const uint32_t keep = L.key_mask ? sm.bits[block % kBits][w] : first_bits(n, w);
 #pragma unroll
@@ -411,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_ld();
                         tmem_regs_ready(r);
                         if (!plain) left_out(r, w);
-                        weights(r, packed);
+                        weights(r, packed, w, false);
                         tmem_st16(s_at + 16 * w, packed);
                     }
                 }
@@ -429,28 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int row = t * rows_per_tile + r_in, head = p.head * group + head_in;
             const bool mine = in_tile && row < p.rows;
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // no kept state: zero
             T *out = static_cast<T *>(L.o.data) + (static_cast<long long>(p.o0) + row) * L.o.row + head * L.o.head;
-#pragma unroll 1
-            for (int x = 0; x < dim; x += 16) {
-                uint32_t o[16];
-                if (blocks) {
-                    tmem_ld16_async(o_at + x, o);
-                    tmem_wait_ld();
-                    tmem_regs_ready_n(o);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!mine || x + 8 * h >= dim) continue;
-                    uint32_t w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        w[i] = l == 0.0f ? 0u
-                                         : Type<T>::pack(__uint_as_float(o[8 * h + 2 * i]) * inv,
-                                                         __uint_as_float(o[8 * h + 2 * i + 1]) * inv);
-                    *reinterpret_cast<uint4 *>(out + x + 8 * h) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
+            // no kept state: zero
+            store_sums<T>(smem_u32(sm.rows[warp - 4]), o_at, dim, l == 0.0f ? 0.0f : 1.0f / l, blocks != 0, mine, out);
             if (L.lse && mine)
                 L.lse[(static_cast<long long>(p.o0) + row) * L.query_heads + head] =
                     l == 0.0f ? -INFINITY : m * (sl2 * kLn2) + logf(l);
