@@ -287,28 +287,36 @@ constexpr uint32_t kRowStage = 32 * 64;   // bytes a warp
 // at `at`; `out` is the row's address, `bytes` its length.
 template <typename Words>
 __device__ __forceinline__ void store_rows(uint32_t stage, bool mine, uint8_t *out, int bytes, Words &&words) {
-    const int lane = threadIdx.x & 31;
-    const unsigned long long to = mine ? reinterpret_cast<unsigned long long>(out) : 0ull;
+    const int lane = threadIdx.x & 31, c = lane & 3;
+    const unsigned long long own = mine ? reinterpret_cast<unsigned long long>(out) : 0ull;
+    unsigned long long to[4];   // where this lane's chunk of rows lane / 4, 8 + lane / 4, ... goes
+    uint32_t from[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int row = 8 * x + (lane >> 2);
+        to[x] = __shfl_sync(0xffffffffu, own, row);
+        from[x] = stage + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+    }
 #pragma unroll 1
     for (int at = 0; at < bytes; at += 64) {
         uint4 w[4];
         words(at, w);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            st_shared_v4(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), w[c].x, w[c].y, w[c].z, w[c].w);
+        for (int i = 0; i < 4; ++i)
+            st_shared_v4(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), w[i].x, w[i].y, w[i].z, w[i].w);
         __syncwarp();
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int row = 8 * x + (lane >> 2), c = lane & 3;
-            uint4 v;
+        for (int x = 0; x < 4; ++x)
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "r"(stage + row * 64 + ((c ^ ((row >> 1) & 3)) << 4))
-                         : "memory");
-            const unsigned long long p = __shfl_sync(0xffffffffu, to, row);
-            if (p && at + 16 * c < bytes) *reinterpret_cast<uint4 *>(p + at + 16 * c) = v;
-        }
+                         : "=r"(w[x].x), "=r"(w[x].y), "=r"(w[x].z), "=r"(w[x].w)
+                         : "r"(from[x]));
         __syncwarp();
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (to[x] && at + 16 * c < bytes)
+                asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(to[x] + at + 16 * c), "r"(w[x].x),
+                             "r"(w[x].y), "r"(w[x].z), "r"(w[x].w)
+                             : "memory");
     }
 }
 
