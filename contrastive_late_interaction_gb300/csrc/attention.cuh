@@ -254,15 +254,22 @@ __device__ __forceinline__ void issue_commit(uint32_t leader, uint64_t *bar) {
         : "memory");
 }
 
-// D = A B^T over `steps` times 16 elements of the heads.
+// D = A B^T over `steps` times 16 elements of the heads.  The usual count has
+// code without conditions: one before each product costs as much as the product.
 template <int BOXES>
 __device__ __forceinline__ void mma_rows(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int steps) {
     a = opaque(a);
     b = opaque(b);
-#pragma unroll
-    for (int k = 0; k < 4 * BOXES; ++k) {
+    auto step = [&](int k) {
         const uint64_t at = desc_bytes((k >> 2) * kBoxBytes + (k & 3) * 32);
-        if (k < steps) issue_ss(leader, d, a + at, b + at, idesc, k != 0);
+        issue_ss(leader, d, a + at, b + at, idesc, k != 0);
+    };
+    if (steps == 4 * BOXES) {
+#pragma unroll
+        for (int k = 0; k < 4 * BOXES; ++k) step(k);
+    } else {
+#pragma unroll 1
+        for (int k = 0; k < steps; ++k) step(k);
     }
 }
 
@@ -272,9 +279,16 @@ template <int STEPS>
 __device__ __forceinline__ void mma_pairs(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int rows,
                                           bool accumulate) {
     b = opaque(b);
+    const uint32_t first = accumulate;
+    if (rows > 16 * (STEPS - 1)) {
+        issue_ts(leader, d, a, b, idesc, first);
 #pragma unroll
-    for (int k = 0; k < STEPS; ++k)
-        if (16 * k < rows) issue_ts(leader, d, a + k * 8, b + desc_bytes(k * 2048), idesc, k != 0 || accumulate);
+        for (int k = 1; k < STEPS; ++k) issue_ts(leader, d, a + k * 8, b + desc_bytes(k * 2048), idesc, 1);
+    } else {
+#pragma unroll 1
+        for (int k = 0; 16 * k < rows; ++k)
+            issue_ts(leader, d, a + k * 8, b + desc_bytes(k * 2048), idesc, k != 0 ? 1 : first);
+    }
 }
 
 // Rows of TMEM to global memory.  A thread has a row there, and rows lie apart
