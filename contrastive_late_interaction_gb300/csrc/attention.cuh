@@ -258,8 +258,6 @@ __device__ __forceinline__ void issue_commit(uint32_t leader, uint64_t *bar) {
 // code without conditions: one before each product costs as much as the product.
 template <int BOXES>
 __device__ __forceinline__ void mma_rows(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int steps) {
-    a = opaque(a);
-    b = opaque(b);
     auto step = [&](int k) {
         const uint64_t at = desc_bytes((k >> 2) * kBoxBytes + (k & 3) * 32);
         issue_ss(leader, d, a + at, b + at, idesc, k != 0);
@@ -278,7 +276,6 @@ __device__ __forceinline__ void mma_rows(uint32_t leader, uint32_t d, uint64_t a
 template <int STEPS>
 __device__ __forceinline__ void mma_pairs(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int rows,
                                           bool accumulate) {
-    b = opaque(b);
     const uint32_t first = accumulate;
     if (rows > 16 * (STEPS - 1)) {
         issue_ts(leader, d, a, b, idesc, first);
