@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t sum_desc = desc_sum(smem_u32(sm.ring[0][0]));
         constexpr uint64_t kTile = desc_bytes(BOXES * kBoxBytes);
         const int steps = (dim + 15) / 16;
-        const uint32_t leader = lane == 0, tm = uniform(tmem);
+        const uint32_t leader = elected(), tm = uniform(tmem);
         uint32_t entry = 0, held = 0, j_all = 0;
         bool ok = true;
         auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t sum_desc = desc_sum(smem_u32(sm.ring[0][0]));
         constexpr uint64_t kTile = desc_bytes(BOXES * kBoxBytes);
         const int steps = (dim + 15) / 16;
-        const uint32_t leader = lane == 0, tm = uniform(tmem);
+        const uint32_t leader = elected(), tm = uniform(tmem);
         uint32_t entry = 0, held = 0, j_all = 0;
         bool ok = true;
         auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };

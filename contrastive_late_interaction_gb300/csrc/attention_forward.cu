@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint64_t kTile = desc_bytes(BOXES * kBoxBytes);
         const int steps = (dim + 15) / 16;
         uint64_t *k_bars = L.key_mask ? sm.ready : sm.kv_full;
-        const uint32_t leader = lane == 0, tm = uniform(tmem);
+        const uint32_t leader = elected(), tm = uniform(tmem);
         uint32_t entry = 0, q_phase = 0, p_phase = 0;
         bool ok = true;
         auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
