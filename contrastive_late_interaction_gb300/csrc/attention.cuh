@@ -109,6 +109,12 @@ __device__ __forceinline__ bool find_block(const AttentionLaunch &L, const uint6
     return t.ok && block >= 0 && at < (of_keys ? t.nk : t.nq);
 }
 
+// A wait of a whole warp, whose lanes come out of it together and agree on
+// whether it was given up.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status)) != 0;
+}
+
 // The tensor-core kernels hand out their blocks from a counter, a batch at a
 // time: items differ in length, and every other slot may be empty.  A warp
 // looks up a batch at once, one block a lane, so that the search costs each
@@ -287,70 +293,45 @@ __device__ __forceinline__ void mma_pairs(uint32_t leader, uint32_t d, uint32_t 
     }
 }
 
-// Rows of TMEM to global memory.  A thread has a row there, and rows lie apart
-// in memory: stored as they come, each 16 bytes are a request of their own
-// (5000 cycles for two tiles of 128 rows).  So 64 bytes of each of a warp's
-// rows go through 2 KB of shared memory, and a request covers 8 rows of them.
-constexpr uint32_t kRowStage = 32 * 64;   // bytes a warp
-
-// `words` gives 16 bytes (chunk c of 4) of this thread's row for the 64 bytes
-// at `at`; `out` is the row's address, `bytes` its length.
-template <typename Words>
-__device__ __forceinline__ void store_rows(uint32_t stage, bool mine, uint8_t *out, int bytes, Words &&words) {
-    const int lane = threadIdx.x & 31, c = lane & 3;
-    const unsigned long long own = mine ? reinterpret_cast<unsigned long long>(out) : 0ull;
-    unsigned long long to[4];   // where this lane's chunk of rows lane / 4, 8 + lane / 4, ... goes
-    uint32_t from[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        const int row = 8 * x + (lane >> 2);
-        to[x] = __shfl_sync(0xffffffffu, own, row);
-        from[x] = stage + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-    }
-#pragma unroll 1
-    for (int at = 0; at < bytes; at += 64) {
-        uint4 w[4];
-        words(at, w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            st_shared_v4(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), w[i].x, w[i].y, w[i].z, w[i].w);
-        __syncwarp();
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[x].x), "=r"(w[x].y), "=r"(w[x].z), "=r"(w[x].w)
-                         : "r"(from[x]));
-        __syncwarp();
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-            if (to[x] && at + 16 * c < bytes)
-                asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(to[x] + at + 16 * c), "r"(w[x].x),
-                             "r"(w[x].y), "r"(w[x].z), "r"(w[x].w)
-                             : "memory");
+// 32 bytes to global memory, in one request where the address allows it.
+__device__ __forceinline__ void store_32(void *p, bool wide, const uint32_t (&v)[8]) {
+    if (wide)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
     }
 }
 
-// 16-bit rows of `dim` sums at `sums` in TMEM times `scale`; zeros where there are none.
+// A row of `dim` sums (a multiple of 8) at `sums` in TMEM, times `scale`, as
+// 16-bit values to `out`; zeros where `zero`, or where the warp has no sums.  A thread writes its own row, whole
+// sectors at a time; going through shared memory for contiguous requests was
+// no faster, since the products' operands keep that busy.
 template <typename T>
-__device__ __forceinline__ void store_sums(uint32_t stage, uint32_t sums, int dim, float scale, bool have, bool mine, T *out) {
-    store_rows(stage, mine, reinterpret_cast<uint8_t *>(out), dim * 2, [&](int at, uint4 (&w)[4]) {
-        uint32_t r[32];
-        if (have) {
-            tmem_ld32_async(sums + at / 2, r);
+__device__ __forceinline__ void store_sums(uint32_t sums, int dim, float scale, bool warp_has, bool zero, bool mine, T *out) {
+    const bool wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;
+#pragma unroll 1
+    for (int x = 0; x < dim; x += 16) {
+        uint32_t r[16], v[8];
+        if (warp_has) {   // the same for the whole warp, as the load demands
+            tmem_ld16_async(sums + x, r);
             tmem_wait_ld();
-            tmem_regs_ready(r);
+            tmem_regs_ready_n(r);
         }
+        if (mine) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = have && scale != 0.0f ? Type<T>::pack(__uint_as_float(r[8 * c + 2 * i]) * scale,
-                                                             __uint_as_float(r[8 * c + 2 * i + 1]) * scale)
-                                             : 0u;
-            w[c] = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int i = 0; i < 8; ++i)
+                v[i] = warp_has && !zero ? Type<T>::pack(__uint_as_float(r[2 * i]) * scale, __uint_as_float(r[2 * i + 1]) * scale)
+                                        : 0u;
+            if (x + 16 <= dim)
+                store_32(out + x, wide, v);
+            else
+                *reinterpret_cast<uint4 *>(out + x) = make_uint4(v[0], v[1], v[2], v[3]);
         }
-    });
+        __syncwarp();   // the loads above are the whole warp's
+    }
 }
 
 // Zeroes rows of a tile: those of the first `rows` whose bit in `keep` (one

@@ -86,7 +86,6 @@ template <int BOXES>
 struct Storage {
     alignas(1024) uint8_t held[2][BOXES * kBoxBytes];      // K and V, or Q and dO
     alignas(1024) uint8_t ring[2][2][BOXES * kBoxBytes];   // stages of (Q, dO), or of (K, V)
-    alignas(16) uint8_t rows[8][kRowStage];                 // an arithmetic warp's rows on their way out
     alignas(16) float stat[2][2][128];                      // dkv: lse and delta of a stage's rows
     uint32_t bits[4][4];                                    // dq: a block's kept states
     Work work[kWorks];
@@ -138,7 +137,7 @@ __device__ __forceinline__ uint32_t begin(Smem &sm, const Maps &M) {
 
 template <typename Smem>
 __device__ __forceinline__ bool next_work(Smem &sm, const AttentionLaunch &L, uint32_t it, Work &w) {
-    if (!mbar_wait(&sm.work_full[it % kWorks], (it / kWorks) & 1, &sm.abort_flag, L.status)) return false;
+    if (!wait_warp(&sm.work_full[it % kWorks], (it / kWorks) & 1, &sm.abort_flag, L.status)) return false;
     w = sm.work[it % kWorks];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.work_empty[it % kWorks]);
@@ -155,7 +154,7 @@ __device__ __forceinline__ void hand_out(Smem &sm, const AttentionLaunch &L, boo
     uint32_t it = 0;
     bool ok = true;
     auto publish = [&](const Work &w) {
-        if (!mbar_wait(&sm.work_empty[it % kWorks], ((it / kWorks) & 1) ^ 1, &sm.abort_flag, L.status)) return false;
+        if (!wait_warp(&sm.work_empty[it % kWorks], ((it / kWorks) & 1) ^ 1, &sm.abort_flag, L.status)) return false;
         if (lane == 0) {
             sm.work[it % kWorks] = w;
             mbar_arrive(&sm.work_full[it % kWorks]);
@@ -243,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t tmem = begin(sm, M);
     const int group = L.group, dim = L.head_dim;
-    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, &sm.abort_flag, L.status); };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, &sm.abort_flag, L.status); };
     auto q_blocks = [&](const Work &w) { return (w.nq + rows_per_tile - 1) / rows_per_tile; };
     auto q_rows = [&](const Work &w, int j) { return min(rows_per_tile, w.nq - j * rows_per_tile) * group; };
 
@@ -271,9 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t leader = elected(), tm = uniform(tmem);
         uint32_t entry = 0, held = 0, j_all = 0;
         bool ok = true;
-        auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
         Work w;
-        for (uint32_t it = 0; ok && __all_sync(0xffffffffu, next_work(sm, L, it, w)); ++it) {
+        for (uint32_t it = 0; ok && next_work(sm, L, it, w); ++it) {
             w.nq = static_cast<int>(uniform(w.nq));
             const int blocks = q_blocks(w);
             if (blocks == 0) continue;
@@ -288,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 idesc_s | (n >> 3) << 17, steps);
                 issue_commit(leader, which ? &sm.dp_full : &sm.s_full[0]);
             };
-            ok = wait_all(&sm.held_full, held & 1) && wait_all(&sm.ring_ready[entry & 1], (entry >> 1) & 1);
+            ok = wait(&sm.held_full, held & 1) && wait(&sm.ring_ready[entry & 1], (entry >> 1) & 1);
             ++held;
             tc_fence_after();
             if (ok) {
@@ -298,15 +296,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int j = 0; j < blocks && ok; ++j, ++j_all) {
                 const uint32_t e = entry + j, en = e + 1;
-                if (!wait_all(&sm.p_ready, j_all & 1)) { ok = false; break; }
+                if (!wait(&sm.p_ready, j_all & 1)) { ok = false; break; }
                 tc_fence_after();
                 sum(tm + 256, tm, sum_desc + ((e & 1) * 2 + 1) * kTile, q_rows(w, j), j != 0);
                 if (j + 1 < blocks) {
-                    if (!wait_all(&sm.ring_ready[en & 1], (en >> 1) & 1)) { ok = false; break; }
+                    if (!wait(&sm.ring_ready[en & 1], (en >> 1) & 1)) { ok = false; break; }
                     tc_fence_after();
                     scores(j + 1, en, 0);
                 }
-                if (!wait_all(&sm.ds_ready[0], j_all & 1)) { ok = false; break; }
+                if (!wait(&sm.ds_ready[0], j_all & 1)) { ok = false; break; }
                 tc_fence_after();
                 sum(tm + 384, tm + 128, sum_desc + (e & 1) * 2 * kTile, q_rows(w, j), j != 0);
                 issue_commit(leader, &sm.ring_empty[e & 1]);
@@ -434,8 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const HeadsView &v = side ? L.d_k : L.d_v;
             T *out = static_cast<T *>(v.data) + (static_cast<long long>(w.k0) + row) * v.row + w.head * v.head;
-            store_sums<T>(smem_u32(sm.rows[warp - 4]), tmem + lanes + 256 + side * 128, dim, side ? L.scale : 1.0f, blocks != 0, mine,
-                          out);
+            store_sums<T>(tmem + lanes + 256 + side * 128, dim, side ? L.scale : 1.0f, blocks != 0, false, mine, out);
             tc_fence_before();
         }
     }
@@ -463,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t tmem = begin(sm, M);
     const int group = L.group, dim = L.head_dim;
-    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, &sm.abort_flag, L.status); };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, &sm.abort_flag, L.status); };
 
     if (warp == 0) {
         Producer<BOXES, Smem> P{sm, L};
@@ -489,9 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t leader = elected(), tm = uniform(tmem);
         uint32_t entry = 0, held = 0, j_all = 0;
         bool ok = true;
-        auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
         Work w;
-        for (uint32_t it = 0; ok && __all_sync(0xffffffffu, next_work(sm, L, it, w)); ++it) {
+        for (uint32_t it = 0; ok && next_work(sm, L, it, w); ++it) {
             const int nk = static_cast<int>(uniform(w.nk)), blocks = (nk + 127) / 128;
             if (blocks == 0) continue;
             auto scores = [&](int j, uint32_t e, int which) {
@@ -501,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 idesc_s | (n >> 3) << 17, steps);
                 issue_commit(leader, which ? &sm.dp_full : &sm.s_full[e & 1]);
             };
-            ok = wait_all(&sm.held_full, held & 1) && wait_all(&sm.ring_ready[entry & 1], (entry >> 1) & 1);
+            ok = wait(&sm.held_full, held & 1) && wait(&sm.ring_ready[entry & 1], (entry >> 1) & 1);
             ++held;
             tc_fence_after();
             if (ok) {
@@ -512,17 +508,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < blocks && ok; ++j, ++j_all) {
                 const uint32_t e = entry + j, en = e + 1;
                 if (j + 1 < blocks) {
-                    if (!wait_all(&sm.ring_ready[en & 1], (en >> 1) & 1)) { ok = false; break; }
+                    if (!wait(&sm.ring_ready[en & 1], (en >> 1) & 1)) { ok = false; break; }
                     tc_fence_after();
                     scores(j + 1, en, 0);
                 }
-                if (!wait_all(&sm.p_ready, j_all & 1)) { ok = false; break; }
+                if (!wait(&sm.p_ready, j_all & 1)) { ok = false; break; }
                 tc_fence_after();
                 if (j + 1 < blocks) {
                     scores(j + 1, en, 1);
                     if (j + 2 == blocks) issue_commit(leader, &sm.held_empty);
                 }
-                if (!wait_all(&sm.ds_ready[j_all & 1], (j_all >> 1) & 1)) { ok = false; break; }
+                if (!wait(&sm.ds_ready[j_all & 1], (j_all >> 1) & 1)) { ok = false; break; }
                 tc_fence_after();
                 const int n = min(128, nk - 128 * j);
                 const uint32_t a = tm + (e & 1) * 128;
@@ -639,26 +635,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
             }
             const int head = w.head * group + head_in;
-            // The sides take half of the row's columns each (of whole 64 bytes).
-            const uint32_t stage = smem_u32(sm.rows[warp - 4]);
-            const int half = partials ? (dim / 2 + 15) & ~15 : (dim / 2 + 31) & ~31;
-            const int first = side ? half : 0, count = max(0, side ? dim - half : min(half, dim));
+            // The sides take half of the row's columns each, in whole 16s.
+            const int half = (dim / 2 + 15) & ~15;
+            const int first = side ? half : 0, count = side ? dim - half : min(half, dim);
             const uint32_t sums = tmem + lanes + 384 + first;
             if (partials) {
                 float *out = partials + ((static_cast<long long>(w.o0) + r_in) * L.query_heads + head) * dim + first;
-                store_rows(stage, mine, reinterpret_cast<uint8_t *>(out), count * 4, [&](int at, uint4 (&v)[4]) {
-                    uint32_t o[16] = {};
+#pragma unroll 1
+                for (int x = 0; x < count; x += 8) {
+                    uint32_t o[8] = {};
                     if (blocks) {
-                        tmem_ld16_async(sums + at / 4, o);
+                        tmem_ld8_async(sums + x, o);
                         tmem_wait_ld();
                         tmem_regs_ready_n(o);
                     }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) v[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-                });
+                    if (mine) store_32(out + x, true, o);
+                    __syncwarp();
+                }
             } else {
                 T *out = static_cast<T *>(L.d_q.data) + (static_cast<long long>(w.q0) + r_in) * L.d_q.row + head * L.d_q.head + first;
-                store_sums<T>(stage, sums, count, L.scale, blocks != 0, mine, out);
+                store_sums<T>(sums, count, L.scale, blocks != 0, false, mine, out);
             }
             tc_fence_before();
         }

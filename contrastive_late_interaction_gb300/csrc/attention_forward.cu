@@ -21,8 +21,8 @@
 //          softmax runs under the other's products;
 //   2      makes the blocks safe: V's rows past the item's end and dropped
 //          rows of K and V are zeroed (0 x NaN would reach the output through
-//          the product), and the dropped states are listed, as bits and as
-//          what is added to a score: 0 or -infinity;
+//          the product), and for the states to leave out -infinity is put
+//          down, to be added to their scores;
 //   3      hands out the pairs of tiles, some ahead, and checks the offsets of
 //          every item;
 //   4..11  softmax, four warps a tile, one row a thread: S from TMEM, P back
@@ -30,6 +30,8 @@
 // TMEM: S0 | S1 | O0 | O1, 128 columns each.
 
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "attention.cuh"
 
@@ -39,7 +41,7 @@ namespace {
 
 constexpr int kStages = 4;   // even: K blocks in the even stages, V blocks in the odd ones
 constexpr int kThreads = 384;
-constexpr int kBits = 4;
+constexpr int kBias = 4;
 constexpr int kPairs = 4;
 constexpr int kReaders = 11;   // of a published pair: warps 0 to 2, eight softmax warps
 
@@ -51,12 +53,10 @@ template <int BOXES>
 struct Storage {
     alignas(1024) uint8_t q[2][BOXES * kBoxBytes];
     alignas(1024) uint8_t kv[kStages][BOXES * kBoxBytes];
-    alignas(16) uint8_t rows[8][kRowStage];   // a softmax warp's rows on their way out
-    alignas(16) float bias[kBits][128];
-    uint32_t bits[kBits][4];
+    alignas(16) float bias[kBias][128];
     Pair pair[kPairs];
     uint64_t pair_full[kPairs], pair_empty[kPairs];
-    uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages], ready[kStages], bits_full[kBits];
+    uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages], ready[kStages], bias_full[kBias];
     uint64_t s_full[2], p_ready[2], o_full[2], done;
     uint32_t tmem_base;
     int abort_flag;
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.kv_empty[i], 1);
             mbar_init(&sm.ready[i], 1);
         }
-        for (int i = 0; i < kBits; ++i) mbar_init(&sm.bits_full[i], 1);
+        for (int i = 0; i < kBias; ++i) mbar_init(&sm.bias_full[i], 1);
         for (int i = 0; i < kPairs; ++i) {
             mbar_init(&sm.pair_full[i], 1);
             mbar_init(&sm.pair_empty[i], kReaders);
@@ -107,7 +107,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = sm.tmem_base;
     volatile int *abort_flag = &sm.abort_flag;
     const int group = L.group, dim = L.head_dim, span = 2 * rows_per_tile;
-    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, L.status); };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, abort_flag, L.status); };
+    auto wait_one = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, L.status); };   // a thread's
     // The next published pair, for a reader; false where there is none or the CTA gave up.
     auto next_pair = [&](uint32_t it, Pair &p) {
         if (!wait(&sm.pair_full[it % kPairs], (it / kPairs) & 1)) return false;
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int b = 0; b < BOXES; ++b) tma_load_3d(dst + b * kBoxBytes, map, bar, 64 * b, head, row);
                 };
                 auto load_q = [&](int t) {
-                    if (!wait(&sm.q_empty[t], ((q_phase >> t) & 1) ^ 1)) return false;
+                    if (!wait_one(&sm.q_empty[t], ((q_phase >> t) & 1) ^ 1)) return false;
                     q_phase ^= 1u << t;
                     mbar_arrive_expect_tx(&sm.q_full[t], q_bytes);
                     load(sm.q[t], &M.q, &sm.q_full[t], p.head * group, p.q0 + t * rows_per_tile);
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 auto load_kv = [&](const CUtensorMap *map, int j) {
                     const uint32_t s = entry % kStages;
-                    if (!wait(&sm.kv_empty[s], ((entry / kStages) & 1) ^ 1)) return false;
+                    if (!wait_one(&sm.kv_empty[s], ((entry / kStages) & 1) ^ 1)) return false;
                     mbar_arrive_expect_tx(&sm.kv_full[s], BOXES * kBoxBytes);
                     load(sm.kv[s], map, &sm.kv_full[s], p.head, p.k0 + 128 * j);
                     ++entry;
@@ -156,37 +157,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the last use of stage s: entry - 1 - ((entry - 1 - s) mod kStages), where there is one
                 if (entry > static_cast<uint32_t>(s)) {
                     const uint32_t last = (entry - 1 - s) / kStages;
-                    wait(&sm.kv_empty[s], last & 1);
+                    wait_one(&sm.kv_empty[s], last & 1);
                 }
             }
     } else if (warp == 1) {
         // ------------------------------------------------------------ products
-        const uint32_t idesc_s = idesc_16bit(Type<T>::bf16, 128, 0, 0, 0);   // N by block
+        // N by block; with a negative scale the scores are negated here, so that their maximum is the row's
+        const uint32_t idesc_s = idesc_16bit(Type<T>::bf16, 128, 0, 0, 0) | (L.scale < 0.0f ? kIdescNegateA : 0u);
         const uint32_t idesc_o = idesc_16bit(Type<T>::bf16, 128, round16(dim), 0, 1);
         const uint64_t q_desc = desc_rows(smem_u32(sm.q[0])), k_desc = desc_rows(smem_u32(sm.kv[0]));
         const uint64_t v_desc = desc_sum(smem_u32(sm.kv[0]));
         constexpr uint64_t kTile = desc_bytes(BOXES * kBoxBytes);
         const int steps = (dim + 15) / 16;
-        uint64_t *k_bars = L.key_mask ? sm.ready : sm.kv_full;
         const uint32_t leader = elected(), tm = uniform(tmem);
         uint32_t entry = 0, q_phase = 0, p_phase = 0;
         bool ok = true;
-        auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
         Pair p;
-        for (uint32_t it = 0; ok && __all_sync(0xffffffffu, next_pair(it, p)); ++it) {
+        for (uint32_t it = 0; ok && next_pair(it, p); ++it) {
             const int nk = static_cast<int>(uniform(p.nk)), rows = static_cast<int>(uniform(p.rows));
             const int blocks = (nk + 127) / 128, nt = rows > rows_per_tile ? 2 : 1;
             if (blocks == 0) continue;
             auto scores = [&](int t, int j, uint32_t e) {
-                const uint32_t n = round16(min(128, nk - 128 * j));
+                const uint32_t n = (min(128, nk - 128 * j) + 31) & ~31;
                 mma_rows<BOXES>(leader, tm + t * 128, q_desc + t * kTile, k_desc + (e % kStages) * kTile,
                                 idesc_s | (n >> 3) << 17, steps);
                 issue_commit(leader, &sm.s_full[t]);
                 if (j + 1 == blocks) issue_commit(leader, &sm.q_empty[t]);
             };
-            ok = wait_all(&k_bars[entry % kStages], (entry / kStages) & 1);
+            ok = wait(&sm.ready[entry % kStages], (entry / kStages) & 1);
             for (int t = 0; t < nt && ok; ++t) {
-                ok = wait_all(&sm.q_full[t], (q_phase >> t) & 1);
+                ok = wait(&sm.q_full[t], (q_phase >> t) & 1);
                 if (!ok) break;
                 q_phase ^= 1u << t;
                 tc_fence_after();
@@ -195,9 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) issue_commit(leader, &sm.kv_empty[entry % kStages]);
             for (int j = 0; j < blocks && ok; ++j) {
                 const uint32_t ev = entry + 2 * j + 1, ek = ev + 1;
-                ok = wait_all(&sm.ready[ev % kStages], (ev / kStages) & 1);
+                ok = wait(&sm.ready[ev % kStages], (ev / kStages) & 1);
                 for (int t = 0; t < nt && ok; ++t) {
-                    if (!wait_all(&sm.p_ready[t], (p_phase >> t) & 1)) { ok = false; break; }
+                    if (!wait(&sm.p_ready[t], (p_phase >> t) & 1)) { ok = false; break; }
                     p_phase ^= 1u << t;
                     tc_fence_after();
                     mma_pairs<8>(leader, tm + 256 + t * 128, tm + t * 128, v_desc + (ev % kStages) * kTile, idesc_o,
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j + 1 == blocks) {
                         issue_commit(leader, &sm.o_full[t]);
                     } else {
-                        if (t == 0 && !wait_all(&k_bars[ek % kStages], (ek / kStages) & 1)) { ok = false; break; }
+                        if (t == 0 && !wait(&sm.ready[ek % kStages], (ek / kStages) & 1)) { ok = false; break; }
                         tc_fence_after();
                         scores(t, j + 1, ek);
                     }
@@ -230,23 +230,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t keep[4];
                 kept_bits(L, p.k0 + 128 * j, n, lane, keep);
                 const uint32_t sk = entry % kStages, sv = (entry + 1) % kStages;
-                if (L.key_mask) {
-                    const uint32_t x = block % kBits;
+                if (L.key_mask || n < 128) {
+                    const uint32_t x = block % kBias;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        sm.bias[x][32 * w + lane] = (keep[w] >> lane) & 1u ? 0.0f : -INFINITY;
-                        if (lane == 0) sm.bits[x][w] = keep[w];
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.bits_full[x]);
-                    if (!wait(&sm.kv_full[sk], (entry / kStages) & 1)) { ok = false; break; }
-                    zero_rows<BOXES>(smem_u32(sm.kv[sk]), round16(n), keep, lane);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.ready[sk]);
+                    for (int w = 0; w < 4; ++w) sm.bias[x][32 * w + lane] = (keep[w] >> lane) & 1u ? 0.0f : -INFINITY;
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.bias_full[block % kBias]);
+                // Scores are taken 32 at a time: the rows up to there have to be numbers.
+                if (!wait(&sm.kv_full[sk], (entry / kStages) & 1)) { ok = false; break; }
+                zero_rows<BOXES>(smem_u32(sm.kv[sk]), (n + 31) & ~31, keep, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.ready[sk]);
                 if (!wait(&sm.kv_full[sv], ((entry + 1) / kStages) & 1)) { ok = false; break; }
-                zero_rows<BOXES>(smem_u32(sm.kv[sv]), round16(n), keep, lane);
+                zero_rows<BOXES>(smem_u32(sm.kv[sv]), (n + 31) & ~31, keep, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.ready[sv]);
@@ -298,7 +296,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * 128;
         const float sl2 = fmaxf(fabsf(L.scale) * kLog2e, 1e-30f);   // above 0, so that -infinity stays that
-        const float sign = L.scale < 0.0f ? -1.0f : 1.0f;
         const float lazy = 8.0f / sl2;   // in units of a raw score
         const float2 sl22 = make_float2(sl2, sl2);
         uint32_t phase = 0, o_phase = 0, block = 0;
@@ -316,85 +313,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                 phase ^= 1;
                 tc_fence_after();
                 const int n = min(128, p.nk - 128 * j);
-                const bool whole = n == 128 && sign > 0.0f, plain = whole && !L.key_mask;
-                if (L.key_mask && !wait(&sm.bits_full[block % kBits], (block / kBits) & 1)) { ok = false; break; }
-                const float4 *bias = reinterpret_cast<const float4 *>(sm.bias[block % kBits]);
-                float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
-                float2 shift = make_float2(-m * sl2, -m * sl2);
-                // The exponentials of the 32 scores of chunk w, packed, and added to the sums.
-                auto weights = [&](const uint32_t (&r)[32], uint32_t (&packed)[16], int w, bool add) {
+                const bool add = n < 128 || L.key_mask;   // states to leave out: their scores are 0 here
+                const float4 *bias = reinterpret_cast<const float4 *>(sm.bias[block % kBias]);
+                if (add && !wait(&sm.bias_full[block % kBias], (block / kBias) & 1)) { ok = false; break; }
+                // The maximum of the scores, the first two chunks of 32 staying in registers.
+                uint32_t a[32], b[32];
+                float top = -INFINITY, top1 = -INFINITY;
+                if (n > 64) {
+                    tmem_ld32_max_async(s_at + 64, a, top);
+                    if (n > 96) tmem_ld32_max_async(s_at + 96, b, top1);
+                    tmem_wait_ld();
+                    tmem_regs_ready(a, top);
+                    tmem_regs_ready(b, top1);
+                    top = fmaxf(top, top1);
+                    top1 = -INFINITY;
+                }
+                {
+                    float top2;
+                    tmem_ld32_max_async(s_at, a, top2);
+                    if (n > 32) tmem_ld32_max_async(s_at + 32, b, top1);
+                    tmem_wait_ld();
+                    tmem_regs_ready(a, top2);
+                    tmem_regs_ready(b, top1);
+                    top = fmaxf(fmaxf(top, top1), top2);
+                }
+                // The reference follows the maximum only when that has grown past 2^8.
+                auto past = [&]() { return __any_sync(0xffffffffu, top > m + lazy || (m == -INFINITY && top > m)); };
+                if (past()) {
+                    if (add) {   // of the kept ones alone
+                        top = -INFINITY;
+#pragma unroll 1
+                        for (int w = 0; 32 * w < n; ++w) {
+                            uint32_t r[32];
+                            tmem_ld32_async(s_at + 32 * w, r);
+                            tmem_wait_ld();
+                            tmem_regs_ready(r);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        float2 a = __ffma2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), sl22, shift);
-                        float2 b = __ffma2_rn(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), sl22, shift);
-                        if (add) {   // a dropped state's score is finite (its row of K is zero)
-                            const float4 x = bias[8 * w + i / 4];
-                            a = __fadd2_rn(a, make_float2(x.x, x.y));
-                            b = __fadd2_rn(b, make_float2(x.z, x.w));
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 x = bias[8 * w + i / 4];
+                                top = fmax3(top, __uint_as_float(r[i]) + x.x, __uint_as_float(r[i + 1]) + x.y);
+                                top = fmax3(top, __uint_as_float(r[i + 2]) + x.z, __uint_as_float(r[i + 3]) + x.w);
+                            }
                         }
-                        a = make_float2(ex2(a.x), ex2(a.y));
-                        b = make_float2(ex2(b.x), ex2(b.y));
-                        sum = __fadd2_rn(sum, a);
-                        sum1 = __fadd2_rn(sum1, b);
-                        packed[i / 2] = Type<T>::pack(a.x, a.y);
-                        packed[i / 2 + 1] = Type<T>::pack(b.x, b.y);
                     }
-                };
-                auto at_once = [&](bool add) {
-                    // Nearly always the reference still serves: the weights are taken as the scores arrive, and
-                    // thrown away in the rare block whose maximum turns out to be past it.
-                    // (A dropped state's score of 0 may be past it too: no harm, the block is done again.)
-                    uint32_t a[32], b[32], packed[4][16];
-                    float t0, t1, t2, t3;
-                    tmem_ld32_max_async(s_at, a, t0);
-                    tmem_ld32_max_async(s_at + 32, b, t1);
-                    tmem_wait_ld();
-                    tmem_regs_ready(a, t0);
-                    tmem_regs_ready(b, t1);
-                    weights(a, packed[0], 0, add);
-                    tmem_ld32_max_async(s_at + 64, a, t2);
-                    weights(b, packed[1], 1, add);
-                    tmem_wait_ld();
-                    tmem_regs_ready(a, t2);
-                    tmem_ld32_max_async(s_at + 96, b, t3);
-                    weights(a, packed[2], 2, add);
-                    tmem_wait_ld();
-                    tmem_regs_ready(b, t3);
-                    weights(b, packed[3], 3, add);
-                    if (__any_sync(0xffffffffu, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) > m + lazy)) return false;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) tmem_st16(s_at + 16 * w, packed[w]);
-                    return true;
-                };
-                bool again = !whole || __any_sync(0xffffffffu, m == -INFINITY);
-                if (!again) again = L.key_mask ? !at_once(true) : !at_once(false);
-                if (again) {
-                    // The maximum first, then the weights: an item's first block, blocks with states to leave out.
-                    auto left_out = [&](uint32_t (&r)[32], int w) {
-                        const uint32_t keep = L.key_mask ? sm.bits[block % kBits][w] : first_bits(n, w);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            r[i] = __float_as_uint((keep >> i) & 1u ? sign * __uint_as_float(r[i]) : -INFINITY);
-                    };
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        if (32 * w >= n) continue;
-                        uint32_t r[32];
-                        float t0;
-                        tmem_ld32_max_async(s_at + 32 * w, r, t0);
-                        tmem_wait_ld();
-                        tmem_regs_ready(r, t0);
-                        if (!plain) {
-                            left_out(r, w);
-                            t0 = -INFINITY;
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) t0 = fmax3(t0, __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
-                        }
-                        top = fmaxf(top, t0);
-                    }
-                    // The reference follows the maximum only when that has grown past 2^8.
-                    if (__any_sync(0xffffffffu, top > m + lazy || (m == -INFINITY && top > m))) {
+                    if (!add || past()) {
                         const float m1 = fmaxf(m, top);
                         const float c = m1 > m ? ex2((m - m1) * sl2) : 1.0f;
                         m = m1;
@@ -413,20 +375,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    shift.x = shift.y = m == -INFINITY ? 0.0f : -m * sl2;
-                    sum = sum1 = make_float2(0.0f, 0.0f);
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {   // P's words stay behind the scores still to be read
-                        if (32 * w >= n) continue;
-                        uint32_t r[32], packed[16];
-                        tmem_ld32_async(s_at + 32 * w, r);
-                        tmem_wait_ld();
-                        tmem_regs_ready(r);
-                        if (!plain) left_out(r, w);
-                        weights(r, packed, w, false);
-                        tmem_st16(s_at + 16 * w, packed);
-                    }
                 }
+                // The weights, stored over the scores as these are done with: chunk w's 16 words end before
+                // chunk w + 1's scores begin.
+                const float at0 = m == -INFINITY ? 0.0f : -m * sl2;
+                const float2 shift = make_float2(at0, at0);
+                float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
+                auto weights = [&](const uint32_t (&r)[32], int w, auto with_bias) {
+                    uint32_t packed[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        float2 x = __ffma2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), sl22, shift);
+                        float2 y = __ffma2_rn(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), sl22, shift);
+                        if constexpr (decltype(with_bias)::value) {
+                            const float4 z = bias[8 * w + i / 4];
+                            x = __fadd2_rn(x, make_float2(z.x, z.y));
+                            y = __fadd2_rn(y, make_float2(z.z, z.w));
+                        }
+                        x = make_float2(ex2(x.x), ex2(x.y));
+                        y = make_float2(ex2(y.x), ex2(y.y));
+                        sum = __fadd2_rn(sum, x);
+                        sum1 = __fadd2_rn(sum1, y);
+                        packed[i / 2] = Type<T>::pack(x.x, x.y);
+                        packed[i / 2 + 1] = Type<T>::pack(y.x, y.y);
+                    }
+                    tmem_st16(s_at + 16 * w, packed);
+                };
+                auto all = [&](auto with_bias) {
+                    weights(a, 0, with_bias);
+                    if (n > 64) tmem_ld32_async(s_at + 64, a);
+                    if (n > 32) weights(b, 1, with_bias);
+                    if (n > 64) {
+                        tmem_wait_ld();
+                        tmem_regs_ready(a);
+                        if (n > 96) tmem_ld32_async(s_at + 96, b);
+                        weights(a, 2, with_bias);
+                    }
+                    if (n > 96) {
+                        tmem_wait_ld();
+                        tmem_regs_ready(b);
+                        weights(b, 3, with_bias);
+                    }
+                };
+                if (add) all(std::true_type()); else all(std::false_type());
                 l += (sum.x + sum1.x) + (sum.y + sum1.y);
                 tmem_wait_st();
                 tc_fence_before();
@@ -442,8 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = t * rows_per_tile + r_in, head = p.head * group + head_in;
             const bool mine = in_tile && row < p.rows;
             T *out = static_cast<T *>(L.o.data) + (static_cast<long long>(p.o0) + row) * L.o.row + head * L.o.head;
-            // no kept state: zero
-            store_sums<T>(smem_u32(sm.rows[warp - 4]), o_at, dim, l == 0.0f ? 0.0f : 1.0f / l, blocks != 0, mine, out);
+            __syncwarp();
+            store_sums<T>(o_at, dim, 1.0f / l, blocks != 0, l == 0.0f, mine, out);   // no kept state: zero
             if (L.lse && mine)
                 L.lse[(static_cast<long long>(p.o0) + row) * L.query_heads + head] =
                     l == 0.0f ? -INFINITY : m * (sl2 * kLn2) + logf(l);

@@ -294,6 +294,14 @@ def test_attention_of_flat_and_sharp_rows(cli, q_len, k_len, q_scale):
     check(*attend(cli, q_len, k_len, 4, 2, 64, BF16, 400, shared=isinstance(q_len, int), q_scale=q_scale))
 
 
+@pytest.mark.parametrize("q_len, k_len", [([200, 30], [400, 77]), ([2], [700]), (1, [300, 40])])
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1.0])
+@pytest.mark.parametrize("mask", [None, 0.3])
+def test_attention_scales(cli, q_len, k_len, scale, mask):
+    """Scores that are negated, all equal, or not shrunk."""
+    check(*attend(cli, q_len, k_len, 4, 2, 64, BF16, 500, mask, shared=isinstance(q_len, int), scale=scale))
+
+
 @pytest.mark.parametrize("q_len, k_len", [([150, 3], [260, 130]), ([1, 1], [260, 130])])
 def test_states_past_an_item_do_not_reach_it(cli, q_len, k_len):
     """Neighbouring items' rows, whatever they hold, change nothing: not in the tile that an item ends in."""
