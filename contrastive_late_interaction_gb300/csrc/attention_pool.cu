@@ -141,6 +141,7 @@ template <typename T, int DP, int NT>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
     forward_kernel(const __grid_constant__ AttentionLaunch L, int chunk, long long slots, float *part_o, float2 *part_ml) {
     constexpr int KC = DP / 32, VB = DP / 64, KG = 128 / DP, kStep = 16 * KG;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel, if there is one
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const long long id = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     if (chunk < L.max_k)
@@ -306,13 +307,16 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
         }
 }
 
-// Joins the parts of each row: one warp a row, four elements a lane.
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32)
+// Joins the parts of each row, four elements a lane.  W warps a row: one where
+// items have a few parts, eight where they have many (one item of 4096 states
+// in chunks of 32: 128 parts took one warp 30 us).
+template <typename T, int W>
+__global__ void __launch_bounds__(256)
     join_kernel(const __grid_constant__ AttentionLaunch L, int chunk, const float *part_o, const float2 *part_ml) {
-    const int lane = threadIdx.x & 31;
+    after_previous();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long most = static_cast<long long>(L.max_q) * L.group;   // rows of an item and key head
-    const long long id = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const long long id = W == 8 ? blockIdx.x : static_cast<long long>(blockIdx.x) * 8 + warp;
     if (id >= static_cast<long long>(L.items) * L.key_heads * most) return;
     const int row = static_cast<int>(id % most), head = static_cast<int>(id / most % L.key_heads);
     const int i = static_cast<int>(id / (most * L.key_heads));
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     const long long first = static_cast<long long>(L.k_off[i] / chunk) + i;
     const int parts = max(1, (u.item.nk + chunk - 1) / chunk);
     const long long step = L.key_heads * most, at = (first * L.key_heads + head) * most + row;
-    // The largest reference, then the sums at it; a lane takes every 32nd part's (m, l).
+    // The largest reference, then the sums at it.
     float m = -INFINITY, l = 0.0f;
     for (int p = lane; p < parts; p += 32) m = fmaxf(m, part_ml[at + p * step].x);
     for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
@@ -331,13 +335,26 @@ __global__ void __launch_bounds__(kWarps * 32)
     const int dim = L.head_dim, d = 4 * lane;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
+    for (int p = W == 8 ? warp : 0; p < parts; p += W) {
         const float2 ml = part_ml[at + p * step];
         const float c = ex2_full(ml.x - ref);
         l = fmaf(ml.y, c, l);
         if (d < dim) {
             const float4 v = *reinterpret_cast<const float4 *>(part_o + (at + p * step) * dim + d);
             o.x = fmaf(v.x, c, o.x), o.y = fmaf(v.y, c, o.y), o.z = fmaf(v.z, c, o.z), o.w = fmaf(v.w, c, o.w);
+        }
+    }
+    if constexpr (W == 8) {
+        __shared__ float4 sum_o[8][32];
+        __shared__ float sum_l[8];
+        sum_o[warp][lane] = o;
+        if (lane == 0) sum_l[warp] = l;
+        __syncthreads();
+        if (warp != 0) return;
+        for (int w = 1; w < 8; ++w) {
+            const float4 v = sum_o[w][lane];
+            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+            l += sum_l[w];
         }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -673,9 +690,11 @@ cudaError_t forward(const AttentionLaunch &L, cudaStream_t stream) {
     float *part_o = split ? reinterpret_cast<float *>(L.workspace) : nullptr;
     float2 *part_ml = split ? reinterpret_cast<float2 *>(L.workspace + part_bytes(L, c.slots, c)) : nullptr;
     forward_kernel<T, DP, NT><<<blocks_of(c.slots * L.key_heads, kWarps), kWarps * 32, 0, stream>>>(L, c.chunk, c.slots, part_o, part_ml);
-    if (split)
-        join_kernel<T><<<blocks_of(L.items * L.key_heads * c.rows, kWarps), kWarps * 32, 0, stream>>>(L, c.chunk, part_o, part_ml);
-    return cudaGetLastError();
+    if (!split) return cudaGetLastError();
+    const long long rows = L.items * L.key_heads * c.rows;
+    if (L.max_k > 8 * c.chunk)
+        return launch_after(join_kernel<T, 8>, dim3(static_cast<unsigned>(rows)), 256, 0, stream, L, c.chunk, part_o, part_ml);
+    return launch_after(join_kernel<T, 1>, dim3(blocks_of(rows, 8)), 256, 0, stream, L, c.chunk, part_o, part_ml);
 }
 
 template <typename T, int DP, int NT>
