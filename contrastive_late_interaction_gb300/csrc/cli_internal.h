@@ -206,11 +206,12 @@ struct RotaryLaunch {
     int table_rows;
     float epsilon, inv_dim, sin_sign;
     RotaryPartLaunch part[2];
+    int q_blocks;   // the first blocks of the grid take part 0
     int32_t *status;
     int sm_count;
 };
 
-// The most blocks a part's grid has.
+// The most blocks a call has.
 inline int rotary_blocks(int sm_count) { return sm_count * 8; }
 cudaError_t launch_rotary(RotaryLaunch L, cudaStream_t stream);
 cudaError_t launch_rotary_table(float *table, long long positions, int half, const double *frequencies,
