@@ -33,8 +33,8 @@ constexpr int kWorks = 4;
 constexpr int kReaders = 11;   // of a published work item: warps 0 to 2, eight arithmetic warps
 
 // What the scores' rows need in the backward, one entry per output row and
-// head at stat_at: lse in powers of two (+infinity where the row kept no
-// state, so that p is 0) and delta.
+// head at stat_at: -lse in powers of two (-infinity where the row kept no
+// state, so that p is 0) and -delta, to be added.
 __device__ __forceinline__ long long stat_at(const AttentionLaunch &L, int out_rows, int key_head, long long row) {
     return (static_cast<long long>(key_head) * out_rows + row) * L.group;
 }
@@ -48,31 +48,41 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ Atte
     check_items(L, static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, static_cast<long long>(gridDim.x) * 256);
     const int lane = threadIdx.x & 15;
     const long long cells = static_cast<long long>(out_rows) * L.query_heads;
-    for (long long c = static_cast<long long>(blockIdx.x) * 16 + (threadIdx.x >> 4); c - (threadIdx.x >> 4) < cells;
-         c += static_cast<long long>(gridDim.x) * 16) {
-        const bool on = c < cells;
-        const long long row = on ? c / L.query_heads : 0;
-        const int head = on ? static_cast<int>(c - row * L.query_heads) : 0;
-        float d = 0.0f;
-        if (on && 8 * lane < L.head_dim) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const T *>(L.o.data) + row * L.o.row +
-                                                             head * L.o.head + 8 * lane);
-            const uint4 b = *reinterpret_cast<const uint4 *>(static_cast<const T *>(L.d_o.data) + row * L.d_o.row +
-                                                             head * L.d_o.head + 8 * lane);
-            const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+    constexpr int kAtOnce = 4;   // cells of a group of lanes: their loads are under way together
+    for (long long base = static_cast<long long>(blockIdx.x) * 16 * kAtOnce; base < cells; base += static_cast<long long>(gridDim.x) * 16 * kAtOnce) {
+        uint4 a[kAtOnce], b[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 x = Type<T>::unpack(wa[i]), y = Type<T>::unpack(wb[i]);
-                d = fmaf(x.x, y.x, fmaf(x.y, y.y, d));
+        for (int x = 0; x < kAtOnce; ++x) {
+            const long long c = base + x * 16 + (threadIdx.x >> 4);
+            a[x] = b[x] = make_uint4(0, 0, 0, 0);
+            if (c < cells && 8 * lane < L.head_dim) {
+                const long long row = c / L.query_heads;
+                const int head = static_cast<int>(c - row * L.query_heads);
+                a[x] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(L.o.data) + row * L.o.row +
+                                                              head * L.o.head + 8 * lane));
+                b[x] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(L.d_o.data) + row * L.d_o.row +
+                                                        head * L.d_o.head + 8 * lane);
             }
         }
 #pragma unroll
-        for (int o = 8; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-        if (on && lane == 0) {
-            const float lse = L.lse[c];
-            const int kh = head / L.group;
-            stats[stat_at(L, out_rows, kh, row) + head - kh * L.group] =
-                make_float2(lse == -INFINITY ? INFINITY : lse * kLog2e, d);
+        for (int x = 0; x < kAtOnce; ++x) {
+            const long long c = base + x * 16 + (threadIdx.x >> 4);
+            const uint32_t wa[4] = {a[x].x, a[x].y, a[x].z, a[x].w}, wb[4] = {b[x].x, b[x].y, b[x].z, b[x].w};
+            float d = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 u = Type<T>::unpack(wa[i]), v = Type<T>::unpack(wb[i]);
+                d = fmaf(u.x, v.x, fmaf(u.y, v.y, d));
+            }
+#pragma unroll
+            for (int o = 8; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+            if (c < cells && lane == 0) {
+                const long long row = c / L.query_heads;
+                const int head = static_cast<int>(c - row * L.query_heads), kh = head / L.group;
+                const float lse = L.lse[c];
+                stats[stat_at(L, out_rows, kh, row) + head - kh * L.group] =
+                    make_float2(lse == -INFINITY ? -INFINITY : -lse * kLog2e, -d);
+            }
         }
     }
 }
@@ -82,15 +92,22 @@ struct Work {
     int q0, o0, nq, k0, nk, head;   // nq, nk: rows of the item to walk, or of the tile; head < 0: no more work
 };
 
+// The walked tiles come through two rings.  Those of A (Q, or K) are held
+// longest, from the scores of a block to the last product of it, while the
+// next block's scores are already wanted: they need three stages (with two,
+// the products waited 1100 of 3900 cycles a block).  Those of B (dO, or V) are
+// done with earlier.
 template <int BOXES>
 struct Storage {
+    static constexpr uint32_t kA = BOXES == 2 ? 3 : 4, kB = BOXES == 2 ? 2 : 3;
     alignas(1024) uint8_t held[2][BOXES * kBoxBytes];      // K and V, or Q and dO
-    alignas(1024) uint8_t ring[2][2][BOXES * kBoxBytes];   // stages of (Q, dO), or of (K, V)
-    alignas(16) float stat[2][2][128];                      // dkv: lse and delta of a stage's rows
+    alignas(1024) uint8_t ring_a[kA][BOXES * kBoxBytes];
+    alignas(1024) uint8_t ring_b[kB][BOXES * kBoxBytes];
+    alignas(16) float lse[kB][128], delta[kA][128];        // dkv: of a stage's rows, negated; lse is done with when dO is
     uint32_t bits[4][4];                                    // dq: a block's kept states
     Work work[kWorks];
     uint64_t work_full[kWorks], work_empty[kWorks];
-    uint64_t held_full, held_empty, ring_full[2], ring_empty[2], ring_ready[2];
+    uint64_t held_full, held_empty, a_full[kA], a_empty[kA], a_ready[kA], b_full[kB], b_empty[kB], b_ready[kB];
     uint64_t s_full[2], dp_full, p_ready, ds_ready[2], sum_full, done;   // the dkv kernel uses the first of two
     uint32_t tmem_base;
     int abort_flag;
@@ -101,14 +118,21 @@ struct Maps {
 };
 
 template <typename Smem>
-__device__ __forceinline__ uint32_t begin(Smem &sm, const Maps &M) {
+__device__ __forceinline__ uint32_t begin(Smem &sm, const Maps &M, int32_t *status) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.ring_full[i], 1);
-            mbar_init(&sm.ring_empty[i], 1);
-            mbar_init(&sm.ring_ready[i], 1);
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.ds_ready[i], 8);
+        }
+        for (uint32_t i = 0; i < Smem::kA; ++i) {
+            mbar_init(&sm.a_full[i], 1);
+            mbar_init(&sm.a_empty[i], 1);
+            mbar_init(&sm.a_ready[i], 1);
+        }
+        for (uint32_t i = 0; i < Smem::kB; ++i) {
+            mbar_init(&sm.b_full[i], 1);
+            mbar_init(&sm.b_empty[i], 1);
+            mbar_init(&sm.b_ready[i], 1);
         }
         for (int i = 0; i < kWorks; ++i) {
             mbar_init(&sm.work_full[i], 1);
@@ -120,7 +144,9 @@ __device__ __forceinline__ uint32_t begin(Smem &sm, const Maps &M) {
         mbar_init(&sm.p_ready, 8);
         mbar_init(&sm.sum_full, 1);
         mbar_init(&sm.done, 1);
-        sm.abort_flag = 0;
+        // The tiles use every byte there is, so the array has to start on 1024, as it asks for.
+        sm.abort_flag = smem_u32(&sm) % 1024 != 0;
+        if (sm.abort_flag) report(status, CLI_INTERNAL);
         fence_mbar_init();
         prefetch_tmap(&M.q);
         prefetch_tmap(&M.k);
@@ -208,18 +234,23 @@ struct Producer {
         return true;
     }
     __device__ bool stage(const CUtensorMap *a, const CUtensorMap *b, uint32_t bytes, int head, int row_a, int row_b) {
-        const uint32_t s = entry & 1;
-        if (!wait(&sm.ring_empty[s], ((entry >> 1) & 1) ^ 1)) return false;
+        constexpr uint32_t kA = Smem::kA, kB = Smem::kB;
+        const uint32_t x = entry % kA, y = entry % kB;
+        if (!wait(&sm.a_empty[x], ((entry / kA) & 1) ^ 1)) return false;
+        mbar_arrive_expect_tx(&sm.a_full[x], bytes);
+        load(sm.ring_a[x], a, &sm.a_full[x], head, row_a);
+        if (!wait(&sm.b_empty[y], ((entry / kB) & 1) ^ 1)) return false;
+        mbar_arrive_expect_tx(&sm.b_full[y], bytes);
+        load(sm.ring_b[y], b, &sm.b_full[y], head, row_b);
         ++entry;
-        mbar_arrive_expect_tx(&sm.ring_full[s], 2 * bytes);
-        load(sm.ring[s][0], a, &sm.ring_full[s], head, row_a);
-        load(sm.ring[s][1], b, &sm.ring_full[s], head, row_b);
         return true;
     }
     // Lets the loads in flight land before the CTA can exit.
     __device__ void drain() {
-        for (uint32_t s = 0; s < 2; ++s)
-            if (entry > s) wait(&sm.ring_empty[s], ((entry - 1 - s) >> 1) & 1);
+        for (uint32_t s = 0; s < Smem::kA; ++s)
+            if (entry > s) wait(&sm.a_empty[s], ((entry - 1 - s) / Smem::kA) & 1);
+        for (uint32_t s = 0; s < Smem::kB; ++s)
+            if (entry > s) wait(&sm.b_empty[s], ((entry - 1 - s) / Smem::kB) & 1);
         if (held) wait(&sm.held_empty, (held - 1) & 1);
     }
 };
@@ -236,11 +267,11 @@ template <typename T, int BOXES>
 __global__ void __launch_bounds__(kThreads, 1)
     dkv_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
                int out_rows, const float2 *stats, long long slots, long long tiles, unsigned long long *counter) {
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     using Smem = Storage<BOXES>;
-    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const uint32_t tmem = begin(sm, M);
+    const uint32_t tmem = begin(sm, M, L.status);
     const int group = L.group, dim = L.head_dim;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, &sm.abort_flag, L.status); };
     auto q_blocks = [&](const Work &w) { return (w.nq + rows_per_tile - 1) / rows_per_tile; };
@@ -263,8 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         const uint32_t idesc_s = idesc_16bit(Type<T>::bf16, 128, 0, 0, 0);   // N by block
         const uint32_t idesc_d = idesc_16bit(Type<T>::bf16, 128, round16(dim), 0, 1);
-        const uint64_t held_desc = desc_rows(smem_u32(sm.held[0])), ring_desc = desc_rows(smem_u32(sm.ring[0][0]));
-        const uint64_t sum_desc = desc_sum(smem_u32(sm.ring[0][0]));
+        constexpr uint32_t kA = Smem::kA, kB = Smem::kB;
+        const uint64_t held_desc = desc_rows(smem_u32(sm.held[0]));
+        const uint64_t a_rows = desc_rows(smem_u32(sm.ring_a[0])), b_rows = desc_rows(smem_u32(sm.ring_b[0]));
+        const uint64_t a_sum = desc_sum(smem_u32(sm.ring_a[0])), b_sum = desc_sum(smem_u32(sm.ring_b[0]));
         constexpr uint64_t kTile = desc_bytes(BOXES * kBoxBytes);
         const int steps = (dim + 15) / 16;
         const uint32_t leader = elected(), tm = uniform(tmem);
@@ -282,15 +315,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto scores = [&](int j, uint32_t e, int which) {
                 const uint32_t n = round16(q_rows(w, j));
-                mma_rows<BOXES>(leader, tm + which * 128, held_desc + which * kTile, ring_desc + ((e & 1) * 2 + which) * kTile,
-                                idesc_s | (n >> 3) << 17, steps);
+                mma_rows<BOXES>(leader, tm + which * 128, held_desc + which * kTile,
+                                which ? b_rows + e % kB * kTile : a_rows + e % kA * kTile, idesc_s | (n >> 3) << 17, steps);
                 issue_commit(leader, which ? &sm.dp_full : &sm.s_full[0]);
             };
-            ok = wait(&sm.held_full, held & 1) && wait(&sm.ring_ready[entry & 1], (entry >> 1) & 1);
+            auto a_there = [&](uint32_t e) { return wait(&sm.a_ready[e % kA], (e / kA) & 1); };
+            auto b_there = [&](uint32_t e) { return wait(&sm.b_ready[e % kB], (e / kB) & 1); };
+            ok = wait(&sm.held_full, held & 1) && a_there(entry);
             ++held;
             tc_fence_after();
             if (ok) {
                 scores(0, entry, 0);
+                ok = b_there(entry);
+            }
+            if (ok) {
+                tc_fence_after();
                 scores(0, entry, 1);
                 if (blocks == 1) issue_commit(leader, &sm.held_empty);
             }
@@ -298,17 +337,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t e = entry + j, en = e + 1;
                 if (!wait(&sm.p_ready, j_all & 1)) { ok = false; break; }
                 tc_fence_after();
-                sum(tm + 256, tm, sum_desc + ((e & 1) * 2 + 1) * kTile, q_rows(w, j), j != 0);
+                sum(tm + 256, tm, b_sum + e % kB * kTile, q_rows(w, j), j != 0);
+                issue_commit(leader, &sm.b_empty[e % kB]);
                 if (j + 1 < blocks) {
-                    if (!wait(&sm.ring_ready[en & 1], (en >> 1) & 1)) { ok = false; break; }
+                    if (!a_there(en)) { ok = false; break; }
                     tc_fence_after();
                     scores(j + 1, en, 0);
                 }
                 if (!wait(&sm.ds_ready[0], j_all & 1)) { ok = false; break; }
                 tc_fence_after();
-                sum(tm + 384, tm + 128, sum_desc + (e & 1) * 2 * kTile, q_rows(w, j), j != 0);
-                issue_commit(leader, &sm.ring_empty[e & 1]);
+                sum(tm + 384, tm + 128, a_sum + e % kA * kTile, q_rows(w, j), j != 0);
+                issue_commit(leader, &sm.a_empty[e % kA]);
                 if (j + 1 < blocks) {
+                    if (!b_there(en)) { ok = false; break; }
+                    tc_fence_after();
                     scores(j + 1, en, 1);
                     if (j + 2 == blocks) issue_commit(leader, &sm.held_empty);
                 } else {
@@ -333,21 +375,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int at = 32 * i + lane;
-                    f[i] = at < n ? src[at] : make_float2(INFINITY, 0.0f);
+                    f[i] = at < n ? src[at] : make_float2(-INFINITY, 0.0f);
                 }
-                const uint32_t s = entry & 1;
-                if (!wait(&sm.ring_full[s], (entry >> 1) & 1)) { ok = false; break; }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    sm.stat[s][0][32 * i + lane] = f[i].x;
-                    sm.stat[s][1][32 * i + lane] = f[i].y;
-                }
+                const uint32_t s = entry % Smem::kA, sb = entry % Smem::kB;
+                if (!wait(&sm.a_full[s], (entry / Smem::kA) & 1)) { ok = false; break; }
                 const uint32_t keep[4] = {first_bits(n, 0), first_bits(n, 1), first_bits(n, 2), first_bits(n, 3)};
-                zero_rows<BOXES>(smem_u32(sm.ring[s][0]), round16(n), keep, lane);
-                zero_rows<BOXES>(smem_u32(sm.ring[s][1]), round16(n), keep, lane);
+                zero_rows<BOXES>(smem_u32(sm.ring_a[s]), round16(n), keep, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.ring_ready[s]);
+                if (lane == 0) mbar_arrive(&sm.a_ready[s]);
+                if (!wait(&sm.b_full[sb], (entry / Smem::kB) & 1)) { ok = false; break; }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sm.lse[sb][32 * i + lane] = f[i].x;
+                    sm.delta[s][32 * i + lane] = f[i].y;
+                }
+                zero_rows<BOXES>(smem_u32(sm.ring_b[sb]), round16(n), keep, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.b_ready[sb]);
             }
         }
     } else if (warp == 3) {
@@ -356,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int side = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t s_at = tmem + lanes + side * 64, dp_at = s_at + 128;
-        const float sl2 = L.scale * kLog2e;
+        const float2 sl22 = make_float2(L.scale * kLog2e, L.scale * kLog2e);
         uint32_t j_all = 0, works = 0;
         bool ok = true;
         Work w;
@@ -365,11 +411,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool mine = row < w.nk, live = mine && (!L.key_mask || L.key_mask[w.k0 + row] != 0);
             for (int j = 0; j < blocks; ++j, ++j_all) {
                 const int n = round16(q_rows(w, j)) - side * 64;   // columns of this side
-                const uint32_t s = j_all & 1, ph = (j_all >> 1) & 1;
-                if (!wait(&sm.ring_ready[s], ph) || !wait(&sm.s_full[0], j_all & 1)) { ok = false; break; }
+                const uint32_t sb = j_all % Smem::kB;
+                if (!wait(&sm.b_ready[sb], (j_all / Smem::kB) & 1) || !wait(&sm.s_full[0], j_all & 1)) { ok = false; break; }
                 tc_fence_after();
-                const float *lse = sm.stat[s][0] + side * 64, *delta = sm.stat[s][1] + side * 64;
-                float p[64];
+                // A dropped state's row of scores may be anything; so is its row of P and dS then, which reaches
+                // its own row of the sums alone, and that is not written.
+                const float4 *lse = reinterpret_cast<const float4 *>(sm.lse[sb] + side * 64);
+                const float4 *delta = reinterpret_cast<const float4 *>(sm.delta[j_all % Smem::kA] + side * 64);
+                float2 p[32];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     if (32 * c >= n) continue;
@@ -379,15 +428,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_regs_ready(r);
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
-                        const float4 l = *reinterpret_cast<const float4 *>(lse + 32 * c + i);
-                        const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float e = ex2(fmaf(__uint_as_float(r[i + k]), sl2, -lv[k]));
-                            p[32 * c + i + k] = live ? e : 0.0f;
-                        }
-                        packed[i / 2] = Type<T>::pack(p[32 * c + i], p[32 * c + i + 1]);
-                        packed[i / 2 + 1] = Type<T>::pack(p[32 * c + i + 2], p[32 * c + i + 3]);
+                        const float4 l = lse[8 * c + i / 4];
+                        float2 x = __ffma2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), sl22, make_float2(l.x, l.y));
+                        float2 y = __ffma2_rn(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), sl22, make_float2(l.z, l.w));
+                        x = make_float2(ex2(x.x), ex2(x.y));
+                        y = make_float2(ex2(y.x), ex2(y.y));
+                        p[16 * c + i / 2] = x;
+                        p[16 * c + i / 2 + 1] = y;
+                        packed[i / 2] = Type<T>::pack(x.x, x.y);
+                        packed[i / 2 + 1] = Type<T>::pack(y.x, y.y);
                     }
                     tmem_st16(s_at + 16 * c, packed);
                 }
@@ -406,16 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_regs_ready(r);
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
-                        const float4 dl = *reinterpret_cast<const float4 *>(delta + 32 * c + i);
-                        const float dv[4] = {dl.x, dl.y, dl.z, dl.w};
-                        float ds[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float d = p[32 * c + i + k] * (__uint_as_float(r[i + k]) - dv[k]);
-                            ds[k] = live ? d : 0.0f;
-                        }
-                        packed[i / 2] = Type<T>::pack(ds[0], ds[1]);
-                        packed[i / 2 + 1] = Type<T>::pack(ds[2], ds[3]);
+                        const float4 d = delta[8 * c + i / 4];
+                        float2 x = __fadd2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(d.x, d.y));
+                        float2 y = __fadd2_rn(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), make_float2(d.z, d.w));
+                        x = __fmul2_rn(p[16 * c + i / 2], x);
+                        y = __fmul2_rn(p[16 * c + i / 2 + 1], y);
+                        packed[i / 2] = Type<T>::pack(x.x, x.y);
+                        packed[i / 2 + 1] = Type<T>::pack(y.x, y.y);
                     }
                     tmem_st16(dp_at + 16 * c, packed);
                 }
@@ -432,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const HeadsView &v = side ? L.d_k : L.d_v;
             T *out = static_cast<T *>(v.data) + (static_cast<long long>(w.k0) + row) * v.row + w.head * v.head;
-            store_sums<T>(tmem + lanes + 256 + side * 128, dim, side ? L.scale : 1.0f, blocks != 0, false, mine, out);
+            store_sums<T>(tmem + lanes + 256 + side * 128, dim, side ? L.scale : 1.0f, blocks != 0, !live, mine, out);
             tc_fence_before();
         }
     }
@@ -454,11 +500,11 @@ template <typename T, int BOXES>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
               int out_rows, const float2 *stats, float *partials, long long slots, long long tiles, unsigned long long *counter) {
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     using Smem = Storage<BOXES>;
-    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const uint32_t tmem = begin(sm, M);
+    const uint32_t tmem = begin(sm, M, L.status);
     const int group = L.group, dim = L.head_dim;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, &sm.abort_flag, L.status); };
 
@@ -479,8 +525,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         const uint32_t idesc_s = idesc_16bit(Type<T>::bf16, 128, 0, 0, 0);   // N by block
         const uint32_t idesc_d = idesc_16bit(Type<T>::bf16, 128, round16(dim), 0, 1);
-        const uint64_t held_desc = desc_rows(smem_u32(sm.held[0])), ring_desc = desc_rows(smem_u32(sm.ring[0][0]));
-        const uint64_t sum_desc = desc_sum(smem_u32(sm.ring[0][0]));
+        constexpr uint32_t kA = Smem::kA, kB = Smem::kB;
+        const uint64_t held_desc = desc_rows(smem_u32(sm.held[0]));
+        const uint64_t a_rows = desc_rows(smem_u32(sm.ring_a[0])), b_rows = desc_rows(smem_u32(sm.ring_b[0]));
+        const uint64_t a_sum = desc_sum(smem_u32(sm.ring_a[0])), b_sum = desc_sum(smem_u32(sm.ring_b[0]));
         constexpr uint64_t kTile = desc_bytes(BOXES * kBoxBytes);
         const int steps = (dim + 15) / 16;
         const uint32_t leader = elected(), tm = uniform(tmem);
@@ -493,28 +541,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto scores = [&](int j, uint32_t e, int which) {
                 const uint32_t n = round16(min(128, nk - 128 * j));
                 const uint32_t d = which ? tm + 256 : tm + (e & 1) * 128;
-                mma_rows<BOXES>(leader, d, held_desc + which * kTile, ring_desc + ((e & 1) * 2 + which) * kTile,
+                mma_rows<BOXES>(leader, d, held_desc + which * kTile, which ? b_rows + e % kB * kTile : a_rows + e % kA * kTile,
                                 idesc_s | (n >> 3) << 17, steps);
+                if (which) issue_commit(leader, &sm.b_empty[e % kB]);
                 issue_commit(leader, which ? &sm.dp_full : &sm.s_full[e & 1]);
             };
-            ok = wait(&sm.held_full, held & 1) && wait(&sm.ring_ready[entry & 1], (entry >> 1) & 1);
+            auto a_there = [&](uint32_t e) { return wait(&sm.a_ready[e % kA], (e / kA) & 1); };
+            auto b_there = [&](uint32_t e) { return wait(&sm.b_full[e % kB], (e / kB) & 1); };
+            ok = wait(&sm.held_full, held & 1) && a_there(entry);
             ++held;
             tc_fence_after();
             if (ok) {
                 scores(0, entry, 0);
+                ok = b_there(entry);
+            }
+            if (ok) {
+                tc_fence_after();
                 scores(0, entry, 1);
                 if (blocks == 1) issue_commit(leader, &sm.held_empty);
             }
             for (int j = 0; j < blocks && ok; ++j, ++j_all) {
                 const uint32_t e = entry + j, en = e + 1;
                 if (j + 1 < blocks) {
-                    if (!wait(&sm.ring_ready[en & 1], (en >> 1) & 1)) { ok = false; break; }
+                    if (!a_there(en)) { ok = false; break; }
                     tc_fence_after();
                     scores(j + 1, en, 0);
                 }
                 if (!wait(&sm.p_ready, j_all & 1)) { ok = false; break; }
                 tc_fence_after();
                 if (j + 1 < blocks) {
+                    if (!b_there(en)) { ok = false; break; }
+                    tc_fence_after();
                     scores(j + 1, en, 1);
                     if (j + 2 == blocks) issue_commit(leader, &sm.held_empty);
                 }
@@ -522,10 +579,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const int n = min(128, nk - 128 * j);
                 const uint32_t a = tm + (e & 1) * 128;
-                const uint64_t b = sum_desc + (e & 1) * 2 * kTile;
+                const uint64_t b = a_sum + e % kA * kTile;
                 mma_pairs<4>(leader, tm + 384, a, b, idesc_d, n, j != 0);
                 mma_pairs<4>(leader, tm + 384, a + 64, b + desc_bytes(4 * 2048), idesc_d, n - 64, true);
-                issue_commit(leader, &sm.ring_empty[e & 1]);
+                issue_commit(leader, &sm.a_empty[e % kA]);
                 if (j + 1 == blocks) issue_commit(leader, &sm.sum_full);
             }
             entry += blocks;
@@ -544,16 +601,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int n = min(128, w.nk - 128 * j);
                 uint32_t keep[4];
                 kept_bits(L, w.k0 + 128 * j, n, lane, keep);
-                const uint32_t s = entry & 1;
-                if (!wait(&sm.ring_full[s], (entry >> 1) & 1)) { ok = false; break; }
+                const uint32_t s = entry % Smem::kA;
+                if (!wait(&sm.a_full[s], (entry / Smem::kA) & 1)) { ok = false; break; }
                 if (lane == 0) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) sm.bits[entry & 3][k] = keep[k];
                 }
-                zero_rows<BOXES>(smem_u32(sm.ring[s][0]), round16(n), keep, lane);
+                zero_rows<BOXES>(smem_u32(sm.ring_a[s]), round16(n), keep, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.ring_ready[s]);
+                if (lane == 0) mbar_arrive(&sm.a_ready[s]);
             }
         }
     } else if (warp == 3) {
@@ -570,17 +627,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t it = 0; ok && next_work(sm, L, it, w); ++it) {
             const int blocks = (w.nk + 127) / 128;
             const bool mine = r_in < w.nq && m_row < rows_per_tile * group;
-            float2 st = make_float2(INFINITY, 0.0f);
+            float2 st = make_float2(-INFINITY, 0.0f);
             if (mine)
                 st = stats[stat_at(L, out_rows, w.head, static_cast<long long>(w.o0) + r_in) + head_in];
-            const float2 sl22 = make_float2(sl2, sl2), shift = make_float2(-st.x, -st.x);
+            const float2 sl22 = make_float2(sl2, sl2), shift = make_float2(st.x, st.x), delta = make_float2(st.y, st.y);
             for (int j = 0; j < blocks; ++j, ++j_all) {
                 const int n = min(128, w.nk - 128 * j) - side * 64;   // columns of this side
                 const bool whole = !L.key_mask && n >= 64;
                 const uint32_t s_at = tmem + lanes + (j_all & 1) * 128 + side * 64;
-                if (!wait(&sm.ring_ready[j_all & 1], (j_all >> 1) & 1) || !wait(&sm.s_full[j_all & 1], (j_all >> 1) & 1)) { ok = false; break; }
+                if (!wait(&sm.a_ready[j_all % Smem::kA], (j_all / Smem::kA) & 1) || !wait(&sm.s_full[j_all & 1], (j_all >> 1) & 1)) { ok = false; break; }
                 tc_fence_after();
-                float p[64];
+                float2 p[32];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     if (32 * c >= n) continue;
@@ -591,8 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), sl22, shift);
-                        p[32 * c + i] = ex2(x.x);
-                        p[32 * c + i + 1] = ex2(x.y);
+                        p[16 * c + i / 2] = make_float2(ex2(x.x), ex2(x.y));
                     }
                 }
                 if (!wait(&sm.dp_full, j_all & 1)) { ok = false; break; }
@@ -608,13 +664,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t keep = whole ? 0xffffffffu : sm.bits[j_all & 3][2 * side + c];
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
-                        float a = p[32 * c + i] * (__uint_as_float(r[i]) - st.y);
-                        float b = p[32 * c + i + 1] * (__uint_as_float(r[i + 1]) - st.y);
+                        float2 x = __fadd2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), delta);
+                        x = __fmul2_rn(p[16 * c + i / 2], x);
                         if (!whole) {
-                            a = (keep >> i) & 1u ? a : 0.0f;
-                            b = (keep >> (i + 1)) & 1u ? b : 0.0f;
+                            x.x = (keep >> i) & 1u ? x.x : 0.0f;
+                            x.y = (keep >> (i + 1)) & 1u ? x.y : 0.0f;
                         }
-                        packed[c][i / 2] = Type<T>::pack(a, b);
+                        packed[c][i / 2] = Type<T>::pack(x.x, x.y);
                     }
                 }
                 tc_fence_before();
@@ -706,13 +762,14 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
         !encode_heads_tiles(&M.v, L.v, bf16, L.head_dim, L.key_heads, L.key_rows, 1, kTileRows))
         return cudaErrorInvalidValue;
     const long long cells = static_cast<long long>(out_rows) * L.query_heads;
-    const long long blocks = (cells + 15) / 16, most = 16ll * L.sm_count;
+    const long long blocks = (cells + 63) / 64, most = 16ll * L.sm_count;
     begin_kernel<<<1, 32, 0, stream>>>(L.status, counters);
     cudaError_t e = launch_after(stats_kernel<T>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, stream, L,
                                  out_rows, stats);
     if (e != cudaSuccess) return e;
 
-    const size_t smem = sizeof(Storage<BOXES>) + 1024;
+    const size_t smem = sizeof(Storage<BOXES>);
+    static_assert(sizeof(Storage<BOXES>) <= 227 * 1024, "shared memory per CTA");
     auto dkv = dkv_kernel<T, BOXES>;
     auto dq = dq_kernel<T, BOXES>;
     e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));

@@ -486,8 +486,10 @@ __global__ void __launch_bounds__(1024) gain_sum_kernel(const __grid_constant__ 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
     __shared__ float sums[32][33];
     float t = 0.0f;
-    if (i < P.head_dim)
+    if (i < P.head_dim) {
+#pragma unroll 8
         for (int b = warp; b < blocks; b += 32) t += part.gain_partials[static_cast<size_t>(b) * P.head_dim + i];
+    }
     sums[warp][lane] = t;
     __syncthreads();
     if (warp == 0 && i < P.head_dim) {
