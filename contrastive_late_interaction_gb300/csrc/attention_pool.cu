@@ -50,18 +50,6 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <typename T>
-__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-    if constexpr (Type<T>::bf16)
-        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(b0));
-    else
-        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(b0));
-}
-
 // Element (row g, columns 2 t, 2 t + 1) of an 8 x 8 matrix of 16-bit values -> (row g, ...) of its transpose.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     uint32_t r;
@@ -77,6 +65,16 @@ __device__ __forceinline__ float ex2_full(float x) {
 }
 
 __device__ __forceinline__ uint4 load16(const void *p) { return __ldcs(static_cast<const uint4 *>(p)); }
+
+// Two values as a pair of 16-bit pairs that add up to them to twice the type's
+// digits.  HBM bounds these kernels, so weights go into the products as both
+// halves: their rounding would be half of the results' error.
+template <typename T>
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = Type<T>::pack(a, b);
+    const float2 h = Type<T>::unpack(hi);
+    lo = Type<T>::pack(a - h.x, b - h.y);
+}
 
 // The 16 bytes at p where `on`, else zeros.
 __device__ __forceinline__ void load_if(bool on, const void *p, uint32_t (&r)[4]) {
@@ -241,7 +239,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
         }
 #pragma unroll
         for (int x = 0; x < KG; ++x) {
-            uint32_t p[NT][2];
+            uint32_t p[NT][4];   // high halves, then low ones
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float e[4];
@@ -251,8 +249,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
                     e[i] = ex2_full(s[x][n][i] - ref);
                     l[n][i & 1] += e[i];
                 }
-                p[n][0] = transpose8(Type<T>::pack(e[0], e[1]));
-                p[n][1] = transpose8(Type<T>::pack(e[2], e[3]));
+                split_pair<T>(e[0], e[1], p[n][0], p[n][2]);
+                split_pair<T>(e[2], e[3], p[n][1], p[n][3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[n][i] = transpose8(p[n][i]);
             }
 #pragma unroll
             for (int b = 0; b < VB; ++b)
@@ -263,7 +263,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
                     const uint32_t a2 = __byte_perm(vr[x][2][b][i], vr[x][3][b][i], 0x5410);
                     const uint32_t a3 = __byte_perm(vr[x][2][b][i], vr[x][3][b][i], 0x7632);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16<T>(o[b][i][n], a0, a1, a2, a3, p[n][0], p[n][1]);
+                    for (int n = 0; n < NT; ++n) {
+                        mma16<T>(o[b][i][n], a0, a1, a2, a3, p[n][0], p[n][1]);
+                        mma16<T>(o[b][i][n], a0, a1, a2, a3, p[n][2], p[n][3]);
+                    }
                 }
         }
     }
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
                     load_if(on, vbase + row * L.v.row + 32 * c, vr[y][c]);
                 }
             }
-            uint32_t p[NT][2], ds[NT][2];   // of states g and g + 8
+            uint32_t p[NT][4], ds[NT][4];   // of states g and g + 8: high halves, then low ones
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -516,10 +519,10 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
                     pe[i] = on ? ex2_full(fmaf(s4[i], sl2, -lse[n][i & 1])) : 0.0f;
                     de[i] = on ? pe[i] * (d4[i] - delta[n][i & 1]) : 0.0f;
                 }
-                p[n][0] = Type<T>::pack(pe[0], pe[1]);
-                p[n][1] = Type<T>::pack(pe[2], pe[3]);
-                ds[n][0] = Type<T>::pack(de[0], de[1]);
-                ds[n][1] = Type<T>::pack(de[2], de[3]);
+                split_pair<T>(pe[0], pe[1], p[n][0], p[n][2]);
+                split_pair<T>(pe[2], pe[3], p[n][1], p[n][3]);
+                split_pair<T>(de[0], de[1], ds[n][0], ds[n][2]);
+                split_pair<T>(de[2], de[3], ds[n][1], ds[n][3]);
             }
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
@@ -533,8 +536,9 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
                     const uint32_t qi[4] = {q.x, q.y, q.z, q.w}, di[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        mma8<T>(av[i], p[n][0], p[n][1], di[i]);
-                        mma8<T>(ak[i], ds[n][0], ds[n][1], qi[i]);
+                        // 8 rows twice: against the high halves and against the low ones
+                        mma16<T>(av[i], p[n][0], p[n][1], p[n][2], p[n][3], di[i], di[i]);
+                        mma16<T>(ak[i], ds[n][0], ds[n][1], ds[n][2], ds[n][3], qi[i], qi[i]);
                     }
                 }
                 if (32 * c + 8 * t < dim) {
@@ -553,12 +557,11 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
                     }
                 }
             }
-            uint32_t bs[NT][2];
+            uint32_t bs[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                bs[n][0] = transpose8(ds[n][0]);
-                bs[n][1] = transpose8(ds[n][1]);
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) bs[n][i] = transpose8(ds[n][i]);
 #pragma unroll
             for (int c = 0; c < KC; ++c)
 #pragma unroll
@@ -566,7 +569,10 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
                     const uint32_t a0 = transpose8(kr[0][c][2 * i]), a1 = transpose8(kr[0][c][2 * i + 1]);
                     const uint32_t a2 = transpose8(kr[1][c][2 * i]), a3 = transpose8(kr[1][c][2 * i + 1]);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16<T>(dq[c][i][n], a0, a1, a2, a3, bs[n][0], bs[n][1]);
+                    for (int n = 0; n < NT; ++n) {
+                        mma16<T>(dq[c][i][n], a0, a1, a2, a3, bs[n][0], bs[n][1]);
+                        mma16<T>(dq[c][i][n], a0, a1, a2, a3, bs[n][2], bs[n][3]);
+                    }
                 }
         }
         __syncwarp();
