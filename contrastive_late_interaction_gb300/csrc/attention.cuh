@@ -157,6 +157,7 @@ constexpr size_t kCounterBytes = 256;   // at the start of the workspace
 template <typename T> struct Type;
 template <> struct Type<__nv_bfloat16> {
     static constexpr bool bf16 = true;
+    static constexpr uint16_t one = 0x3F80, infinity = 0x7F80;
     static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_bf16x2(a, b); }
     static __device__ __forceinline__ float2 unpack(uint32_t v) {
         return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
@@ -164,6 +165,7 @@ template <> struct Type<__nv_bfloat16> {
 };
 template <> struct Type<__half> {
     static constexpr bool bf16 = false;
+    static constexpr uint16_t one = 0x3C00, infinity = 0x7C00;
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         const __half2 h = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&h);
@@ -259,6 +261,15 @@ __device__ __forceinline__ void issue_commit(uint32_t leader, uint64_t *bar) {
         : "memory");
 }
 
+// Descriptor of a K-major operand of 16 elements a row without a swizzle: 8
+// rows of 16 bytes are 128 bytes in a row, 8-row groups follow one another,
+// the second 8 elements lie 2 KB on.
+constexpr uint32_t kColumnBytes = 4096;
+__device__ __forceinline__ uint64_t desc_column(uint32_t at) {
+    return static_cast<uint64_t>((at & 0x3FFFFu) >> 4) | static_cast<uint64_t>(2048 >> 4) << 16 |
+           static_cast<uint64_t>(128 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
+}
+
 // D = A B^T over `steps` times 16 elements of the heads.  The usual count has
 // code without conditions: one before each product costs as much as the product.
 template <int BOXES>
@@ -313,22 +324,29 @@ template <typename T>
 __device__ __forceinline__ void store_sums(uint32_t sums, int dim, float scale, bool warp_has, bool zero, bool mine, T *out) {
     const bool wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;
 #pragma unroll 1
-    for (int x = 0; x < dim; x += 16) {
-        uint32_t r[16], v[8];
+    for (int x = 0; x < dim; x += 32) {
+        uint32_t r[32];
         if (warp_has) {   // the same for the whole warp, as the load demands
-            tmem_ld16_async(sums + x, r);
+            tmem_ld32_async(sums + x, r);
             tmem_wait_ld();
-            tmem_regs_ready_n(r);
+            tmem_regs_ready(r);
         }
         if (mine) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = warp_has && !zero ? Type<T>::pack(__uint_as_float(r[2 * i]) * scale, __uint_as_float(r[2 * i + 1]) * scale)
-                                        : 0u;
-            if (x + 16 <= dim)
-                store_32(out + x, wide, v);
-            else
-                *reinterpret_cast<uint4 *>(out + x) = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int i = 0; i < 32; ++i)
+                r[i] = warp_has && !zero ? __float_as_uint(__uint_as_float(r[i]) * scale) : 0u;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                uint32_t v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = Type<T>::pack(__uint_as_float(r[16 * y + 2 * i]), __uint_as_float(r[16 * y + 2 * i + 1]));
+                const int at = x + 16 * y;
+                if (at + 16 <= dim)
+                    store_32(out + at, wide, v);
+                else if (at < dim)
+                    *reinterpret_cast<uint4 *>(out + at) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
         }
         __syncwarp();   // the loads above are the whole warp's
     }

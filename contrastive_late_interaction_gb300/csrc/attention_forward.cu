@@ -21,8 +21,10 @@
 //          softmax runs under the other's products;
 //   2      makes the blocks safe: V's rows past the item's end and dropped
 //          rows of K and V are zeroed (0 x NaN would reach the output through
-//          the product), and for the states to leave out -infinity is put
-//          down, to be added to their scores;
+//          the product), and for the states to leave out -infinity is added
+//          to their scores by the product itself: one more step of 16
+//          elements, a column of ones against a column of 0 or -infinity, so
+//          that the softmax knows nothing of them;
 //   3      hands out the pairs of tiles, some ahead, and checks the offsets of
 //          every item;
 //   4..11  softmax, four warps a tile, one row a thread: S from TMEM, P back
@@ -30,8 +32,6 @@
 // TMEM: S0 | S1 | O0 | O1, 128 columns each.
 
 #include <cuda.h>
-
-#include <type_traits>
 
 #include "attention.cuh"
 
@@ -41,7 +41,6 @@ namespace {
 
 constexpr int kStages = 4;   // even: K blocks in the even stages, V blocks in the odd ones
 constexpr int kThreads = 384;
-constexpr int kBias = 4;
 constexpr int kPairs = 4;
 constexpr int kReaders = 11;   // of a published pair: warps 0 to 2, eight softmax warps
 
@@ -53,10 +52,11 @@ template <int BOXES>
 struct Storage {
     alignas(1024) uint8_t q[2][BOXES * kBoxBytes];
     alignas(1024) uint8_t kv[kStages][BOXES * kBoxBytes];
-    alignas(16) float bias[kBias][128];
+    alignas(128) uint8_t ones[kColumnBytes];             // a 1, and 15 zeros, for each of 128 rows
+    alignas(128) uint8_t left_out[kStages / 2][kColumnBytes];   // 0 or an infinity, and 15 zeros, for each state of a K stage
     Pair pair[kPairs];
     uint64_t pair_full[kPairs], pair_empty[kPairs];
-    uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages], ready[kStages], bias_full[kBias];
+    uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages], ready[kStages];
     uint64_t s_full[2], p_ready[2], o_full[2], done;
     uint32_t tmem_base;
     int abort_flag;
@@ -87,7 +87,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.kv_empty[i], 1);
             mbar_init(&sm.ready[i], 1);
         }
-        for (int i = 0; i < kBias; ++i) mbar_init(&sm.bias_full[i], 1);
         for (int i = 0; i < kPairs; ++i) {
             mbar_init(&sm.pair_full[i], 1);
             mbar_init(&sm.pair_empty[i], kReaders);
@@ -100,6 +99,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&M.v);
     }
     if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+    for (uint32_t i = threadIdx.x; i < kColumnBytes / 16; i += kThreads) {
+        const uint32_t at = i * 16;
+        st_shared_v4(smem_u32(sm.ones) + at, at < 2048 ? Type<T>::one : 0u, 0, 0, 0);
+        for (int k = 0; k < kStages / 2; ++k) st_shared_v4(smem_u32(sm.left_out[k]) + at, 0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -167,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t idesc_o = idesc_16bit(Type<T>::bf16, 128, round16(dim), 0, 1);
         const uint64_t q_desc = desc_rows(smem_u32(sm.q[0])), k_desc = desc_rows(smem_u32(sm.kv[0]));
         const uint64_t v_desc = desc_sum(smem_u32(sm.kv[0]));
+        const uint64_t ones_desc = desc_column(smem_u32(sm.ones)), out_desc = desc_column(smem_u32(sm.left_out[0]));
         constexpr uint64_t kTile = desc_bytes(BOXES * kBoxBytes);
         const int steps = (dim + 15) / 16;
         const uint32_t leader = elected(), tm = uniform(tmem);
@@ -181,6 +187,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t n = (min(128, nk - 128 * j) + 31) & ~31;
                 mma_rows<BOXES>(leader, tm + t * 128, q_desc + t * kTile, k_desc + (e % kStages) * kTile,
                                 idesc_s | (n >> 3) << 17, steps);
+                if (L.key_mask || nk - 128 * j < 128)
+                    issue_ss(leader, tm + t * 128, ones_desc, out_desc + (e % kStages) / 2 * desc_bytes(kColumnBytes),
+                             idesc_s | (n >> 3) << 17, 1);
                 issue_commit(leader, &sm.s_full[t]);
                 if (j + 1 == blocks) issue_commit(leader, &sm.q_empty[t]);
             };
@@ -220,25 +229,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&sm.done, 0);
     } else if (warp == 2) {
         // ------------------------------------------------------------ blocks made safe, dropped states
-        uint32_t entry = 0, block = 0;
+        uint32_t entry = 0;
         bool ok = true;
+        // -infinity, or its negative where the scores' product is negated
+        const uint16_t infinity = Type<T>::infinity | (L.scale < 0.0f ? 0u : 0x8000u);
         Pair p;
         for (uint32_t it = 0; ok && next_pair(it, p); ++it) {
             const int blocks = (p.nk + 127) / 128;
-            for (int j = 0; j < blocks && ok; ++j, ++block, entry += 2) {
+            for (int j = 0; j < blocks && ok; ++j, entry += 2) {
                 const int n = min(128, p.nk - 128 * j);
                 uint32_t keep[4];
                 kept_bits(L, p.k0 + 128 * j, n, lane, keep);
                 const uint32_t sk = entry % kStages, sv = (entry + 1) % kStages;
-                if (L.key_mask || n < 128) {
-                    const uint32_t x = block % kBias;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) sm.bias[x][32 * w + lane] = (keep[w] >> lane) & 1u ? 0.0f : -INFINITY;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.bias_full[block % kBias]);
                 // Scores are taken 32 at a time: the rows up to there have to be numbers.
                 if (!wait(&sm.kv_full[sk], (entry / kStages) & 1)) { ok = false; break; }
+                if (L.key_mask || n < 128) {   // the products that read this column last are done: the stage was free
+                    const uint32_t column = smem_u32(sm.left_out[sk / 2]);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint16_t v = (keep[w] >> lane) & 1u ? 0 : infinity;
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(column + (32 * w + lane) * 16), "h"(v) : "memory");
+                    }
+                }
                 zero_rows<BOXES>(smem_u32(sm.kv[sk]), (n + 31) & ~31, keep, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -298,24 +310,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sl2 = fmaxf(fabsf(L.scale) * kLog2e, 1e-30f);   // above 0, so that -infinity stays that
         const float lazy = 8.0f / sl2;   // in units of a raw score
         const float2 sl22 = make_float2(sl2, sl2);
-        uint32_t phase = 0, o_phase = 0, block = 0;
+        uint32_t phase = 0, o_phase = 0;
         bool ok = true;
         Pair p;
         for (uint32_t it = 0; ok && next_pair(it, p); ++it) {
             const int blocks = (p.nk + 127) / 128;
-            if (t * rows_per_tile >= p.rows) {
-                block += blocks;
-                continue;
-            }
+            if (t * rows_per_tile >= p.rows) continue;
             float m = -INFINITY, l = 0.0f;
-            for (int j = 0; j < blocks; ++j, ++block) {
+            for (int j = 0; j < blocks; ++j) {
                 if (!wait(&sm.s_full[t], phase)) { ok = false; break; }
                 phase ^= 1;
                 tc_fence_after();
                 const int n = min(128, p.nk - 128 * j);
-                const bool add = n < 128 || L.key_mask;   // states to leave out: their scores are 0 here
-                const float4 *bias = reinterpret_cast<const float4 *>(sm.bias[block % kBias]);
-                if (add && !wait(&sm.bias_full[block % kBias], (block / kBias) & 1)) { ok = false; break; }
                 // The maximum of the scores, the first two chunks of 32 staying in registers.
                 uint32_t a[32], b[32];
                 float top = -INFINITY, top1 = -INFINITY;
@@ -338,41 +344,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     top = fmaxf(fmaxf(top, top1), top2);
                 }
                 // The reference follows the maximum only when that has grown past 2^8.
-                auto past = [&]() { return __any_sync(0xffffffffu, top > m + lazy || (m == -INFINITY && top > m)); };
-                if (past()) {
-                    if (add) {   // of the kept ones alone
-                        top = -INFINITY;
+                if (__any_sync(0xffffffffu, top > m + lazy || (m == -INFINITY && top > m))) {
+                    const float m1 = fmaxf(m, top);
+                    const float c = m1 > m ? ex2((m - m1) * sl2) : 1.0f;
+                    m = m1;
+                    l *= c;
+                    if (j > 0) {   // S of this block is ready, so the product before it is done
 #pragma unroll 1
-                        for (int w = 0; 32 * w < n; ++w) {
-                            uint32_t r[32];
-                            tmem_ld32_async(s_at + 32 * w, r);
+                        for (int x = 0; x < BOXES * 64; x += 32) {
+                            uint32_t o[32];
+                            tmem_ld32_async(o_at + x, o);
                             tmem_wait_ld();
-                            tmem_regs_ready(r);
+                            tmem_regs_ready(o);
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 x = bias[8 * w + i / 4];
-                                top = fmax3(top, __uint_as_float(r[i]) + x.x, __uint_as_float(r[i + 1]) + x.y);
-                                top = fmax3(top, __uint_as_float(r[i + 2]) + x.z, __uint_as_float(r[i + 3]) + x.w);
-                            }
-                        }
-                    }
-                    if (!add || past()) {
-                        const float m1 = fmaxf(m, top);
-                        const float c = m1 > m ? ex2((m - m1) * sl2) : 1.0f;
-                        m = m1;
-                        l *= c;
-                        if (j > 0) {   // S of this block is ready, so the product before it is done
-#pragma unroll 1
-                            for (int x = 0; x < BOXES * 64; x += 32) {
-                                uint32_t o[32];
-                                tmem_ld32_async(o_at + x, o);
-                                tmem_wait_ld();
-                                tmem_regs_ready(o);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
-                                tmem_st32(o_at + x, o);
-                                tmem_wait_st();
-                            }
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
+                            tmem_st32(o_at + x, o);
+                            tmem_wait_st();
                         }
                     }
                 }
@@ -381,17 +368,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float at0 = m == -INFINITY ? 0.0f : -m * sl2;
                 const float2 shift = make_float2(at0, at0);
                 float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
-                auto weights = [&](const uint32_t (&r)[32], int w, auto with_bias) {
+                auto weights = [&](const uint32_t (&r)[32], int w) {
                     uint32_t packed[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
                         float2 x = __ffma2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), sl22, shift);
                         float2 y = __ffma2_rn(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), sl22, shift);
-                        if constexpr (decltype(with_bias)::value) {
-                            const float4 z = bias[8 * w + i / 4];
-                            x = __fadd2_rn(x, make_float2(z.x, z.y));
-                            y = __fadd2_rn(y, make_float2(z.z, z.w));
-                        }
                         x = make_float2(ex2(x.x), ex2(x.y));
                         y = make_float2(ex2(y.x), ex2(y.y));
                         sum = __fadd2_rn(sum, x);
@@ -401,23 +383,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tmem_st16(s_at + 16 * w, packed);
                 };
-                auto all = [&](auto with_bias) {
-                    weights(a, 0, with_bias);
-                    if (n > 64) tmem_ld32_async(s_at + 64, a);
-                    if (n > 32) weights(b, 1, with_bias);
-                    if (n > 64) {
-                        tmem_wait_ld();
-                        tmem_regs_ready(a);
-                        if (n > 96) tmem_ld32_async(s_at + 96, b);
-                        weights(a, 2, with_bias);
-                    }
-                    if (n > 96) {
-                        tmem_wait_ld();
-                        tmem_regs_ready(b);
-                        weights(b, 3, with_bias);
-                    }
-                };
-                if (add) all(std::true_type()); else all(std::false_type());
+                weights(a, 0);
+                if (n > 64) tmem_ld32_async(s_at + 64, a);
+                if (n > 32) weights(b, 1);
+                if (n > 64) {
+                    tmem_wait_ld();
+                    tmem_regs_ready(a);
+                    if (n > 96) tmem_ld32_async(s_at + 96, b);
+                    weights(a, 2);
+                }
+                if (n > 96) {
+                    tmem_wait_ld();
+                    tmem_regs_ready(b);
+                    weights(b, 3);
+                }
                 l += (sum.x + sum1.x) + (sum.y + sum1.y);
                 tmem_wait_st();
                 tc_fence_before();
