@@ -324,29 +324,22 @@ template <typename T>
 __device__ __forceinline__ void store_sums(uint32_t sums, int dim, float scale, bool warp_has, bool zero, bool mine, T *out) {
     const bool wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;
 #pragma unroll 1
-    for (int x = 0; x < dim; x += 32) {
-        uint32_t r[32];
+    for (int x = 0; x < dim; x += 16) {
+        uint32_t r[16], v[8];
         if (warp_has) {   // the same for the whole warp, as the load demands
-            tmem_ld32_async(sums + x, r);
+            tmem_ld16_async(sums + x, r);
             tmem_wait_ld();
-            tmem_regs_ready(r);
+            tmem_regs_ready_n(r);
         }
         if (mine) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                r[i] = warp_has && !zero ? __float_as_uint(__uint_as_float(r[i]) * scale) : 0u;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                uint32_t v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] = Type<T>::pack(__uint_as_float(r[16 * y + 2 * i]), __uint_as_float(r[16 * y + 2 * i + 1]));
-                const int at = x + 16 * y;
-                if (at + 16 <= dim)
-                    store_32(out + at, wide, v);
-                else if (at < dim)
-                    *reinterpret_cast<uint4 *>(out + at) = make_uint4(v[0], v[1], v[2], v[3]);
-            }
+            for (int i = 0; i < 8; ++i)
+                v[i] = warp_has && !zero ? Type<T>::pack(__uint_as_float(r[2 * i]) * scale, __uint_as_float(r[2 * i + 1]) * scale)
+                                        : 0u;
+            if (x + 16 <= dim)
+                store_32(out + x, wide, v);
+            else
+                *reinterpret_cast<uint4 *>(out + x) = make_uint4(v[0], v[1], v[2], v[3]);
         }
         __syncwarp();   // the loads above are the whole warp's
     }

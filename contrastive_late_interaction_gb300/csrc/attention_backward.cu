@@ -39,49 +39,56 @@ __device__ __forceinline__ long long stat_at(const AttentionLaunch &L, int out_r
     return (static_cast<long long>(key_head) * out_rows + row) * L.group;
 }
 
-// A group of 16 lanes per (output row, head): 8 elements a lane.
+// A warp a row, 16 lanes a head, 8 elements a lane, the loads of eight heads
+// under way together.
 template <typename T>
 __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ AttentionLaunch L, int out_rows,
                                                     float2 *stats) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     after_previous();
     check_items(L, static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, static_cast<long long>(gridDim.x) * 256);
-    const int lane = threadIdx.x & 15;
-    const long long cells = static_cast<long long>(out_rows) * L.query_heads;
-    constexpr int kAtOnce = 4;   // cells of a group of lanes: their loads are under way together
-    for (long long base = static_cast<long long>(blockIdx.x) * 16 * kAtOnce; base < cells; base += static_cast<long long>(gridDim.x) * 16 * kAtOnce) {
-        uint4 a[kAtOnce], b[kAtOnce];
+    const int lane = threadIdx.x & 15, side = (threadIdx.x >> 4) & 1;
+    const bool in = 8 * lane < L.head_dim;
+    constexpr int kAtOnce = 4;
+    for (long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < out_rows;
+         row += static_cast<long long>(gridDim.x) * 8) {
+        const T *o = static_cast<const T *>(L.o.data) + row * L.o.row + 8 * lane;
+        const T *d_o = static_cast<const T *>(L.d_o.data) + row * L.d_o.row + 8 * lane;
+        for (int h0 = side; h0 - side < L.query_heads; h0 += 2 * kAtOnce) {
+            uint4 a[kAtOnce], b[kAtOnce];
 #pragma unroll
-        for (int x = 0; x < kAtOnce; ++x) {
-            const long long c = base + x * 16 + (threadIdx.x >> 4);
-            a[x] = b[x] = make_uint4(0, 0, 0, 0);
-            if (c < cells && 8 * lane < L.head_dim) {
-                const long long row = c / L.query_heads;
-                const int head = static_cast<int>(c - row * L.query_heads);
-                a[x] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(L.o.data) + row * L.o.row +
-                                                              head * L.o.head + 8 * lane));
-                b[x] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(L.d_o.data) + row * L.d_o.row +
-                                                        head * L.d_o.head + 8 * lane);
+            for (int x = 0; x < kAtOnce; ++x) {
+                const int h = h0 + 2 * x;
+                a[x] = b[x] = make_uint4(0, 0, 0, 0);
+                if (in && h < L.query_heads) {
+                    a[x] = __ldcs(reinterpret_cast<const uint4 *>(o + h * L.o.head));
+                    b[x] = __ldg(reinterpret_cast<const uint4 *>(d_o + h * L.d_o.head));
+                }
             }
-        }
+            float d[kAtOnce];
 #pragma unroll
-        for (int x = 0; x < kAtOnce; ++x) {
-            const long long c = base + x * 16 + (threadIdx.x >> 4);
-            const uint32_t wa[4] = {a[x].x, a[x].y, a[x].z, a[x].w}, wb[4] = {b[x].x, b[x].y, b[x].z, b[x].w};
-            float d = 0.0f;
+            for (int x = 0; x < kAtOnce; ++x) {
+                const uint32_t wa[4] = {a[x].x, a[x].y, a[x].z, a[x].w}, wb[4] = {b[x].x, b[x].y, b[x].z, b[x].w};
+                d[x] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 u = Type<T>::unpack(wa[i]), v = Type<T>::unpack(wb[i]);
-                d = fmaf(u.x, v.x, fmaf(u.y, v.y, d));
+                for (int i = 0; i < 4; ++i) {
+                    const float2 u = Type<T>::unpack(wa[i]), v = Type<T>::unpack(wb[i]);
+                    d[x] = fmaf(u.x, v.x, fmaf(u.y, v.y, d[x]));
+                }
+#pragma unroll
+                for (int s = 8; s; s >>= 1) d[x] += __shfl_xor_sync(0xffffffffu, d[x], s);
             }
+            if (lane < kAtOnce) {
+                float mine = d[0];
 #pragma unroll
-            for (int o = 8; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-            if (c < cells && lane == 0) {
-                const long long row = c / L.query_heads;
-                const int head = static_cast<int>(c - row * L.query_heads), kh = head / L.group;
-                const float lse = L.lse[c];
-                stats[stat_at(L, out_rows, kh, row) + head - kh * L.group] =
-                    make_float2(lse == -INFINITY ? -INFINITY : -lse * kLog2e, -d);
+                for (int x = 1; x < kAtOnce; ++x) mine = lane == x ? d[x] : mine;
+                const int h = h0 + 2 * lane;
+                if (h < L.query_heads) {
+                    const int kh = h / L.group;
+                    const float lse = L.lse[row * L.query_heads + h];
+                    stats[stat_at(L, out_rows, kh, row) + h - kh * L.group] =
+                        make_float2(lse == -INFINITY ? -INFINITY : -lse * kLog2e, -mine);
+                }
             }
         }
     }
@@ -761,8 +768,7 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
         !encode_heads_tiles(&M.k, L.k, bf16, L.head_dim, L.key_heads, L.key_rows, 1, kTileRows) ||
         !encode_heads_tiles(&M.v, L.v, bf16, L.head_dim, L.key_heads, L.key_rows, 1, kTileRows))
         return cudaErrorInvalidValue;
-    const long long cells = static_cast<long long>(out_rows) * L.query_heads;
-    const long long blocks = (cells + 63) / 64, most = 16ll * L.sm_count;
+    const long long blocks = (static_cast<long long>(out_rows) + 7) / 8, most = 8ll * L.sm_count;
     begin_kernel<<<1, 32, 0, stream>>>(L.status, counters);
     cudaError_t e = launch_after(stats_kernel<T>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, stream, L,
                                  out_rows, stats);

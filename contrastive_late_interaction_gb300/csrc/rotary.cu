@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, MODE == kNormGrad ? 4 : 6)
     const int lph = 1 << P.lph_log2, sub = lane & (lph - 1), group = lane >> P.lph_log2, groups = 32 >> P.lph_log2;
     const int half = P.rotary_dim >> 1, D = P.head_dim;
     const size_t warp_bytes = kStages * S::kStageBytes + (kStages + 1) * static_cast<size_t>(half) * 8;
-    const uint32_t stage0 = smem_u32(smem) + static_cast<uint32_t>(warp * warp_bytes) + lane * 16;
+    const uint32_t stage0 = smem_u32(smem) + static_cast<uint32_t>(warp * warp_bytes);
     const uint32_t angle0 = smem_u32(smem) + static_cast<uint32_t>(warp * warp_bytes) + kStages * S::kStageBytes;
 
     // This lane's two chunks (-1: none) and the first of its pairs (-1: not rotated).
@@ -259,6 +259,19 @@ __global__ void __launch_bounds__(kStreamWarps * 32, MODE == kNormGrad ? 4 : 6)
         a_at = sub < turned ? 8 * sub : rest < D ? rest : -1;
         b_at = sub < turned ? half + 8 * sub : rest + 8 < D ? rest + 8 : -1;
         pair = sub < turned ? 8 * sub : -1;
+    }
+    // What it copies of a step.  Its own chunks, where the lanes' chunks are neighbours (16-bit halves); elsewhere
+    // every 32nd 16 bytes of the step's heads, so that a request still covers whole lines (36 -> 31 us for 20011
+    // rows of fp32 pairs), at the price of a head's address for each copy (371 -> 443 us for 270336 rows of halves).
+    constexpr bool kOwn = !INTER && sizeof(T) == 2;
+    constexpr int kCopies = 2 * kUnits;
+    const int head_units = D * static_cast<int>(sizeof(T)) / 16;
+    int copy_head[kCopies], copy_at[kCopies];
+#pragma unroll
+    for (int i = 0; i < kCopies && !kOwn; ++i) {
+        const int u = lane + 32 * i;
+        copy_head[i] = u < groups * head_units ? u / head_units : 1 << 30;
+        copy_at[i] = u % head_units * (16 / static_cast<int>(sizeof(T)));
     }
     float gain[2 * N], dg[2 * N];
     if constexpr (MODE != kRotate) {
@@ -302,21 +315,29 @@ __global__ void __launch_bounds__(kStreamWarps * 32, MODE == kNormGrad ? 4 : 6)
                 const uint32_t to = angle0 + static_cast<uint32_t>(at_row % (kStages + 1)) * half * 8;
                 for (int i = 2 * lane; i < half; i += 64) copy16(to + i * 8, from + i);
             }
-            const int h = at_head * groups + group;
-            if (h < part.heads) {
-                const T *in = static_cast<const T *>(part.in) + row * part.in_row + h * part.in_head;
-                const T *x = static_cast<const T *>(part.x) + row * part.x_row + h * part.x_head;
-                const uint32_t to = stage0 + stage * S::kStageBytes;
+            const uint32_t to = stage0 + stage * S::kStageBytes + lane * 16;
+            if constexpr (kOwn) {
+                const int h = at_head * groups + group;
+                if (h < part.heads) {
+                    const T *in = static_cast<const T *>(part.in) + row * part.in_row + h * part.in_head;
+                    const T *x = static_cast<const T *>(part.x) + row * part.x_row + h * part.x_head;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int e = c ? b_at : a_at;
-                    if (e < 0) continue;
-#pragma unroll
-                    for (int u = 0; u < kUnits; ++u) {
-                        copy16(to + (c * kUnits + u) * 512, in + e + u * (16 / sizeof(T)));
-                        if constexpr (MODE == kNormGrad)
-                            copy16(to + ((2 + c) * kUnits + u) * 512, x + e + u * (16 / sizeof(T)));
+                    for (int c = 0; c < 2; ++c) {
+                        const int e = c ? b_at : a_at;
+                        if (e < 0) continue;
+                        copy16(to + c * 512, in + e);
+                        if constexpr (MODE == kNormGrad) copy16(to + (2 + c) * 512, x + e);
                     }
+                }
+            } else {
+                const T *in = static_cast<const T *>(part.in) + row * part.in_row;
+                const T *x = static_cast<const T *>(part.x) + row * part.x_row;
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i) {
+                    const int h = at_head * groups + copy_head[i];
+                    if (h >= part.heads) continue;
+                    copy16(to + i * 512, in + h * part.in_head + copy_at[i]);
+                    if constexpr (MODE == kNormGrad) copy16(to + (kCopies + i) * 512, x + h * part.x_head + copy_at[i]);
                 }
             }
             if (++at_head == head_steps) at_head = 0, ++at_row;
@@ -330,7 +351,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, MODE == kNormGrad ? 4 : 6)
     int row_k = 0, head_k = 0, stage = 0;
     for (long long t = 0; t < steps; ++t) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-        __syncwarp();   // the angles are copied by all lanes
+        __syncwarp();   // what a lane reads is copied by others
         if (head_k == 0) {
             const uint32_t from = angle0 + static_cast<uint32_t>(row_k % (kStages + 1)) * half * 8 + pair * 8;
 #pragma unroll
@@ -344,17 +365,19 @@ __global__ void __launch_bounds__(kStreamWarps * 32, MODE == kNormGrad ? 4 : 6)
         const int h = head_k * groups + group;
         const bool on = h < part.heads;
         float v[2 * N], x[MODE == kNormGrad ? 2 * N : 1];
-        const uint32_t from = stage0 + stage * S::kStageBytes;
+        const uint32_t from = stage0 + stage * S::kStageBytes + (kOwn ? lane : group * head_units) * 16;
 #pragma unroll
         for (int k = 0; k < 2 * S::kTensors; ++k) {
             float *to = k < 2 ? v + 8 * k : x + 8 * (k - 2);
+            const int e = k & 1 ? b_at : a_at;
             uint4 u[kUnits];
 #pragma unroll
             for (int i = 0; i < kUnits; ++i)
-                u[i] = on && (k & 1 ? b_at : a_at) >= 0 ? shared16(from + (k * kUnits + i) * 512) : make_uint4(0, 0, 0, 0);
+                u[i] = on && e >= 0 ? shared16(from + (kOwn ? k * 512 : (k >> 1) * kCopies * 512 + e * static_cast<int>(sizeof(T)) + i * 16))
+                                    : make_uint4(0, 0, 0, 0);
             floats_of<T>(u, to);
         }
-        // Every lane has read its stage (its own part of it) and its angles: the copies go on.
+        // Every lane has read its part of the stage and its angles: the copies go on.
         __syncwarp();
         int next = stage + kStages - 1;
         copy_step(next >= kStages ? next - kStages : next);
