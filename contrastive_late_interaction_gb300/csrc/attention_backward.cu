@@ -164,7 +164,6 @@ __device__ __forceinline__ uint32_t begin(Smem &sm, const Maps &M, int32_t *stat
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    after_previous();
     return sm.tmem_base;
 }
 
@@ -279,6 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t tmem = begin(sm, M, L.status);
+    after_previous();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // dq_kernel, once the statistics are there
     const int group = L.group, dim = L.head_dim;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, &sm.abort_flag, L.status); };
     auto q_blocks = [&](const Work &w) { return (w.nq + rows_per_tile - 1) / rows_per_tile; };
@@ -503,6 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ds_ready alternate: the scores of block j + 1 are issued before block j's
 // are waited for, and dP of block j + 1 before ds of block j is, so with one
 // barrier each a phase could pass unseen.
+// It reads nothing that dkv_kernel writes, and starts on the SMs that kernel
+// leaves: launched as its dependent, it waits for it only at its own end.
 template <typename T, int BOXES>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool mine = r_in < w.nq && m_row < rows_per_tile * group;
             float2 st = make_float2(-INFINITY, 0.0f);
             if (mine)
-                st = stats[stat_at(L, out_rows, w.head, static_cast<long long>(w.o0) + r_in) + head_in];
+                st = __ldcg(stats + stat_at(L, out_rows, w.head, static_cast<long long>(w.o0) + r_in) + head_in);
             const float2 sl22 = make_float2(sl2, sl2), shift = make_float2(st.x, st.x), delta = make_float2(st.y, st.y);
             for (int j = 0; j < blocks; ++j, ++j_all) {
                 const int n = min(128, w.nk - 128 * j) - side * 64;   // columns of this side
@@ -725,6 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
+    after_previous();   // what follows on the stream waits for this kernel alone
 }
 
 // dQ of shared queries: the items' sums, in their order, eight elements a thread.
@@ -789,7 +793,9 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
     const long long q_slots = L.q_off ? static_cast<long long>(L.query_rows) / rows_per_tile + L.items
                                       : static_cast<long long>(L.items) * ((L.query_rows + rows_per_tile - 1) / rows_per_tile);
     const long long q_tiles = q_slots * L.key_heads;
-    dq<<<grid(q_tiles), kThreads, smem, stream>>>(L, M, rows_per_tile, out_rows, stats, partials, q_slots, q_tiles, counters + 1);
+    e = launch_after(dq, dim3(grid(q_tiles)), kThreads, smem, stream, L, M, rows_per_tile, out_rows, stats, partials, q_slots,
+                     q_tiles, counters + 1);
+    if (e != cudaSuccess) return e;
     if (partials) {
         const long long all = static_cast<long long>(L.query_rows) * L.query_heads * L.head_dim;
         dq_sum_kernel<T><<<static_cast<unsigned>((all / 8 + 255) / 256), 256, 0, stream>>>(L, partials);

@@ -14,7 +14,7 @@
 // have enough on its way: a warp that loads a row, looks its position up,
 // loads its angles, computes and stores, waits most of the time (3.2 TB/s for
 // the gradients).  stream_kernel, which takes every call whose rotated halves
-// start on a multiple of 8, copies what a warp needs three steps from now into
+// start on a multiple of 8, copies what a warp needs two steps from now into
 // shared memory (cp.async; a step is 32 / (lanes per head) heads of a row), so
 // some 100 KB an SM are under way; the rest go through heads_kernel.
 //
@@ -227,7 +227,7 @@ template <typename T, Mode MODE>
 struct Stream {
     static constexpr int kUnits = sizeof(T) / 2;                        // 16 bytes each, of a chunk
     static constexpr int kTensors = MODE == kNormGrad ? 2 : 1;
-    static constexpr int kStages = sizeof(T) == 4 ? 3 : 4;
+    static constexpr int kStages = 3;   // 2: 396 us where 3 takes 355, 4: 358, 6: 385
     static constexpr int kStageBytes = 2 * kTensors * kUnits * 32 * 16;
     // a warp's stages, and the angles of as many rows as may be under way
     static size_t warp_bytes(int half) { return kStages * kStageBytes + (kStages + 1) * static_cast<size_t>(half) * 8; }

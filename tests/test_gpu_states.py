@@ -414,3 +414,80 @@ def test_offsets_past_32_bits(cli):
         within(b["d_v"][-n:], *want["d_v"], "d_v")
         assert not b["d_k"][:5].any() and not b["d_k"][rows - n - 5:rows - n].any()
         del b
+
+
+def test_calls_in_a_captured_graph(cli):
+    """A captured step (tiles and few rows, forward and backward, rotation before it) replays on new contents."""
+    g = gen(21)
+    tab = ref.table(512, 64).cuda()
+    k_len = [300, 45, 128]
+    ko = offsets(k_len)
+    k, v = rand(g, sum(k_len), 2, 64, dtype=BF16), rand(g, sum(k_len), 2, 64, dtype=BF16)
+
+    def step(q, qo, d_o, most):
+        n = cli.rotary_heads(q, tab, k=k)
+        f = cli.cross_attention(n["q"], qo, n["k"], v, ko, max_query_rows=most, max_key_rows=300)
+        b = cli.cross_attention_backward(n["q"], qo, n["k"], v, ko, f["output"], f["lse"], d_o, max_query_rows=most,
+                                         max_key_rows=300)
+        return [f["output"], f["lse"], b["d_q"], b["d_k"], b["d_v"], f["device_status"], b["device_status"]]
+    for q_len in ([70, 3, 200], [1, 2, 1]):
+        qo = offsets(q_len)
+        q, d_o = rand(g, sum(q_len), 8, 64, dtype=BF16), rand(g, sum(q_len), 8, 64, dtype=BF16)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step(q, qo, d_o, max(q_len))
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step(q, qo, d_o, max(q_len))
+        for seed in (22, 23):
+            g2 = gen(seed)
+            q.copy_(rand(g2, *q.shape, dtype=BF16))
+            k.copy_(rand(g2, *k.shape, dtype=BF16))
+            graph.replay()
+            torch.cuda.synchronize()
+            got = [t.clone() for t in out]
+            for a, b in zip(got, step(q, qo, d_o, max(q_len))):
+                assert torch.equal(a, b)
+
+
+def test_outputs_workspace_and_status_are_the_callers(cli):
+    g = gen(31)
+    q_len, k_len = [70, 9], [140, 200]
+    qo, ko = offsets(q_len), offsets(k_len)
+    q, d_o = rand(g, 79, 4, 64, dtype=BF16), rand(g, 79, 4, 64, dtype=BF16)
+    k, v = rand(g, 340, 2, 64, dtype=BF16), rand(g, 340, 2, 64, dtype=BF16)
+    kw = dict(max_query_rows=70, max_key_rows=200)
+    a = cli.cross_attention(q, qo, k, v, ko, **kw)
+    b = cli.cross_attention_backward(q, qo, k, v, ko, a["output"], a["lse"], d_o, **kw)
+    for names, call, need, want in (
+            (("output", "lse"), lambda **o: cli.cross_attention(q, qo, k, v, ko, **kw, **o),
+             cli.cross_attention_workspace_bytes(q, qo, k, v, ko, **kw), a),
+            (("d_q", "d_k", "d_v"), lambda **o: cli.cross_attention_backward(q, qo, k, v, ko, a["output"], a["lse"], d_o,
+                                                                             **kw, **o),
+             cli.cross_attention_backward_workspace_bytes(q, qo, k, v, ko, **kw), b)):
+        out = {n: torch.full_like(want[n], 9.0) for n in names}
+        ws = torch.full((need + 256,), 0xAB, dtype=torch.uint8, device="cuda")
+        st = torch.full((1,), 77, dtype=torch.int32, device="cuda")
+        r = call(out=out, workspace=ws[:need], device_status=st)
+        assert int(st.item()) == 0 and (ws[need:] == 0xAB).all()
+        for n in names:
+            assert r[n] is out[n] and torch.equal(out[n], want[n]), n
+        with pytest.raises(cli.InvalidArgumentError):
+            call(workspace=ws[:need - 1])
+
+
+def test_pooling_example_learns():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "pool_states.py")
+    spec = importlib.util.spec_from_file_location("pool_states", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    losses = m.train(items=64, heads=4, dim=64, steps=20, say=lambda s: None)
+    assert all(np_isfinite(x) for x in losses) and losses[-1] < 0.8 * losses[0], losses
+
+
+def np_isfinite(x):
+    return x == x and abs(x) != float("inf")
