@@ -683,6 +683,18 @@ def _out(out, name, like):
                                                                            device=like.device)
 
 
+def _result(out, name, like, shape):
+    """(tensor, its words in the struct): as `_out`; one made here needs no checks."""
+    t = out.get(name) if out else None
+    if t is not None:
+        return t, _heads(t, "out " + name, shape, like.dtype)
+    if like.is_contiguous():
+        t = torch.empty_like(like)
+    else:
+        t = torch.empty(shape, dtype=like.dtype, device=like.device)
+    return t, (t.data_ptr(), shape[1] * shape[2], shape[2])
+
+
 def _status(device_status, like):
     if device_status is None:
         return torch.empty(1, dtype=torch.int32, device=like.device)   # the call writes it
@@ -710,18 +722,14 @@ def rotary_table(positions, rotary_dim, base=10000.0, scaling="plain", factor=1.
     return dict(table=t)
 
 
-def _part(name, lead, positions, x, y, d_y, d_x, gain, d_gain, dtype, dim):
-    """One part of a rotation call, as the struct's 17 words; the matrices given have the shape of `lead`."""
-    shape = lead.shape
+def _part(name, t, positions, gain, dim, dtype):
+    """What the parts of the rotation verbs share: the shape of `t`, and its words, rows' positions and gain."""
+    shape = t.shape
     if len(shape) != 3 or shape[2] != dim:
         raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name} must be [rows, heads, {dim}], not {list(shape)}")
-    rows, heads, _ = shape
-    return (rows, heads, _vector(positions, name + " positions", rows, torch.int32),
-            *(_NO_HEADS if x is None else _heads(x, name, shape, dtype)),
-            *(_NO_HEADS if y is None else _heads(y, "out " + name, shape, dtype)),
-            *(_NO_HEADS if d_y is None else _heads(d_y, "d_" + name, shape, dtype)),
-            *(_NO_HEADS if d_x is None else _heads(d_x, "out d_" + name, shape, dtype)),
-            _vector(gain, name + "_gain", dim, torch.float32), _vector(d_gain, f"d_{name}_gain", dim, torch.float32))
+    return (shape, _heads(t, name, shape, dtype), 0 if positions is None else
+            _vector(positions, name + " positions", shape[0], torch.int32),
+            0 if gain is None else _vector(gain, name + "_gain", dim, torch.float32))
 
 
 _NO_PART = (0,) * 17
@@ -741,16 +749,27 @@ def _rotary_call(verb, lead, q_part, k_part, table, interleaved, epsilon, worksp
         raise_for(rc, verb)
 
 
+def _rotate_part(out, name, t, positions, gain, dim, dtype, back):
+    """(result, the part's 17 words) of a verb with one input and one output."""
+    if t is None:
+        return None, _NO_PART
+    shape, given, pos, g = _part(name, t, positions, gain, dim, dtype)
+    y, made = _result(out, name, t, shape)
+    if back:
+        return y, (shape[0], shape[1], pos, 0, 0, 0, 0, 0, 0, *given, *made, g, 0)
+    return y, (shape[0], shape[1], pos, *given, *made, 0, 0, 0, 0, 0, 0, g, 0)
+
+
 def rotary_heads(q, table, positions=None, k=None, k_positions=None, interleaved=False, out=None, device_status=None,
                  stream=None):
     """Rotates queries [rows, heads, dim] (and keys, of their own rows and heads) by their rows' positions (int32;
     None: row r is at position r), over the first 2 * table.shape[1] elements of each head.  bf16, fp16 or fp32.
     Returns dict(q, k, device_status); out['q'] may be `q` itself."""
     dtype, dim = q.dtype, _states(q, "q")[2]
-    yq, yk, st = _out(out, "q", q), None if k is None else _out(out, "k", k), _status(device_status, q)
-    _rotary_call("rotary_heads", q, _part("q", q, positions, q, yq, None, None, None, None, dtype, dim),
-                 _NO_PART if k is None else _part("k", k, k_positions, k, yk, None, None, None, None, dtype, dim),
-                 table, interleaved, 0.0, None, st, stream)
+    yq, q_part = _rotate_part(out, "q", q, positions, None, dim, dtype, False)
+    yk, k_part = _rotate_part(out, "k", k, k_positions, None, dim, dtype, False)
+    st = _status(device_status, q)
+    _rotary_call("rotary_heads", q, q_part, k_part, table, interleaved, 0.0, None, st, stream)
     return {"q": yq, "k": yk, "device_status": st}
 
 
@@ -758,10 +777,10 @@ def rotary_heads_backward(d_q, table, positions=None, d_k=None, k_positions=None
                           device_status=None, stream=None):
     """The gradient of rotary_heads for its inputs.  Returns dict(d_q, d_k, device_status)."""
     dtype, dim = d_q.dtype, _states(d_q, "d_q")[2]
-    xq, xk, st = _out(out, "d_q", d_q), None if d_k is None else _out(out, "d_k", d_k), _status(device_status, d_q)
-    _rotary_call("rotary_heads_backward", d_q, _part("q", d_q, positions, None, None, d_q, xq, None, None, dtype, dim),
-                 _NO_PART if d_k is None else _part("k", d_k, k_positions, None, None, d_k, xk, None, None, dtype, dim),
-                 table, interleaved, 0.0, None, st, stream)
+    xq, q_part = _rotate_part(out, "d_q", d_q, positions, None, dim, dtype, True)
+    xk, k_part = _rotate_part(out, "d_k", d_k, k_positions, None, dim, dtype, True)
+    st = _status(device_status, d_q)
+    _rotary_call("rotary_heads_backward", d_q, q_part, k_part, table, interleaved, 0.0, None, st, stream)
     return {"d_q": xq, "d_k": xk, "device_status": st}
 
 
@@ -770,10 +789,10 @@ def norm_rotary_heads(q, table, positions=None, q_gain=None, k=None, k_positions
     """Normalises each head, rotate(gain * x / sqrt(mean(x^2) + epsilon)), of queries and keys in one pass.  Gains
     are fp32 [dim] (None: ones); the rest as in rotary_heads.  Returns dict(q, k, device_status)."""
     dtype, dim = q.dtype, _states(q, "q")[2]
-    yq, yk, st = _out(out, "q", q), None if k is None else _out(out, "k", k), _status(device_status, q)
-    _rotary_call("norm_rotary_heads", q, _part("q", q, positions, q, yq, None, None, q_gain, None, dtype, dim),
-                 _NO_PART if k is None else _part("k", k, k_positions, k, yk, None, None, k_gain, None, dtype, dim),
-                 table, interleaved, epsilon, None, st, stream)
+    yq, q_part = _rotate_part(out, "q", q, positions, q_gain, dim, dtype, False)
+    yk, k_part = _rotate_part(out, "k", k, k_positions, k_gain, dim, dtype, False)
+    st = _status(device_status, q)
+    _rotary_call("norm_rotary_heads", q, q_part, k_part, table, interleaved, epsilon, None, st, stream)
     return {"q": yq, "k": yk, "device_status": st}
 
 
@@ -790,15 +809,29 @@ def norm_rotary_heads_backward(q, d_q, table, positions=None, q_gain=None, k=Non
     if (k is None) != (d_k is None):
         raise InvalidArgumentError(CLI_INVALID_ARGUMENT, "norm_rotary_heads_backward: k and d_k go together")
     dtype, dim = q.dtype, _states(q, "q")[2]
-    xq, xk, st = _out(out, "d_q", q), None if k is None else _out(out, "d_k", k), _status(device_status, q)
-    gq = None if q_gain is None else _out(out, "d_q_gain", q_gain)
-    gk = None if k is None or k_gain is None else _out(out, "d_k_gain", k_gain)
+    xq, q_part, gq = _norm_grad_part(out, "q", q, d_q, positions, q_gain, dim, dtype)
+    xk, k_part, gk = _norm_grad_part(out, "k", k, d_k, k_positions, k_gain, dim, dtype)
+    st = _status(device_status, q)
     if workspace is None and (gq is not None or gk is not None):
         workspace = _ws(lib.norm_rotary_heads_backward_workspace_bytes(dim), q.device)
-    _rotary_call("norm_rotary_heads_backward", q, _part("q", q, positions, q, None, d_q, xq, q_gain, gq, dtype, dim),
-                 _NO_PART if k is None else _part("k", k, k_positions, k, None, d_k, xk, k_gain, gk, dtype, dim),
-                 table, interleaved, epsilon, workspace, st, stream)
+    _rotary_call("norm_rotary_heads_backward", q, q_part, k_part, table, interleaved, epsilon, workspace, st, stream)
     return {"d_q": xq, "d_q_gain": gq, "d_k": xk, "d_k_gain": gk, "device_status": st}
+
+
+def _norm_grad_part(out, name, x, d_y, positions, gain, dim, dtype):
+    """(d_x, the part's 17 words, the gain's gradient or None)."""
+    if x is None:
+        return None, _NO_PART, None
+    shape, given, pos, g = _part(name, x, positions, gain, dim, dtype)
+    dy = _heads(d_y, "d_" + name, shape, dtype)
+    dx, made = _result(out, "d_" + name, x, shape)
+    d_gain, dg = None, 0
+    if gain is not None:
+        d_gain = out.get(f"d_{name}_gain") if out else None
+        if d_gain is None:
+            d_gain = torch.empty_like(gain)
+        dg = _vector(d_gain, f"d_{name}_gain", dim, torch.float32)
+    return dx, (shape[0], shape[1], pos, *given, 0, 0, 0, *dy, *made, g, dg), d_gain
 
 
 def _mask(key_mask, rows):

@@ -185,7 +185,6 @@ cli_status_t rotary_call(const cli_rotary_t *a, bool norm, bool backward) {
         if (L.part[p].d_gain) L.part[p].gain_partials = partials + p * static_cast<size_t>(rotary_blocks(sms)) * d;
     if (want_gain && 2ull * rotary_blocks(sms) * d * 4 > ws_bytes) return CLI_UNSUPPORTED;
     cudaStream_t stream = static_cast<cudaStream_t>(a->stream);
-    if (cudaMemsetAsync(a->device_status, 0, sizeof(int32_t), stream) != cudaSuccess) return CLI_DEVICE;
     return launch_rotary(L, stream) == cudaSuccess ? CLI_OK : CLI_DEVICE;
 }
 

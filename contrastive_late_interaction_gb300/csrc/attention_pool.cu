@@ -64,8 +64,6 @@ __device__ __forceinline__ float ex2_full(float x) {
     return y;
 }
 
-__device__ __forceinline__ uint4 load16(const void *p) { return __ldcs(static_cast<const uint4 *>(p)); }
-
 // Two values as a pair of 16-bit pairs that add up to them to twice the type's
 // digits.  HBM bounds these kernels, so weights go into the products as both
 // halves: their rounding would be half of the results' error.
@@ -76,10 +74,20 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint3
     lo = Type<T>::pack(a - h.x, b - h.y);
 }
 
-// The 16 bytes at p where `on`, else zeros.
+// The 16 bytes at p where `on`, else zeros.  Volatile, as the products are: a
+// step's loads then all go out before its first product, however the compiler
+// would like to save registers (the kernel below ran at 5.8 or at 6.5 TB/s as
+// it chose).
 __device__ __forceinline__ void load_if(bool on, const void *p, uint32_t (&r)[4]) {
-    const uint4 v = on ? load16(p) : make_uint4(0, 0, 0, 0);
-    r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " setp.ne.u32 p, %5, 0;\n"
+        " mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n mov.u32 %3, 0;\n"
+        " @p ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+        "}\n"
+        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3])
+        : "l"(p), "r"(static_cast<uint32_t>(on)));
 }
 
 // A warp's unit: states k0 .. k0 + n - 1 of an item for one key head.
@@ -116,6 +124,23 @@ __device__ __forceinline__ Unit find_unit(const AttentionLaunch &L, int chunk, l
     return u;
 }
 
+// A call on few items has no memset of the status before it: block 0 checks
+// every item and writes the word (what others report until then is what it
+// will find).  With more items the grid shares the checks.
+constexpr int kFewItems = 256;
+__device__ __forceinline__ void check_all(const AttentionLaunch &L, bool reached) {
+    if (L.items > kFewItems) {
+        if (!reached)   // a unit looks at its item anyway, where each item has one
+            check_items(L, static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x,
+                        static_cast<long long>(gridDim.x) * blockDim.x);
+    } else if (blockIdx.x == 0) {
+        bool bad = false;
+        for (int i = threadIdx.x; i < L.items; i += blockDim.x) bad |= !load_item(L, i).ok;
+        bad = __syncthreads_or(bad);
+        if (threadIdx.x == 0) *L.status = bad ? CLI_MALFORMED : CLI_OK;
+    }
+}
+
 // The kept states among the `count` (at most 32) from k0, as bits.
 __device__ __forceinline__ uint32_t kept(const AttentionLaunch &L, int k0, int count, int lane) {
     if (!L.key_mask) return count >= 32 ? 0xffffffffu : (1u << count) - 1u;
@@ -142,9 +167,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel, if there is one
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const long long id = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (chunk < L.max_k)
-        check_items(L, static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x,
-                    static_cast<long long>(gridDim.x) * blockDim.x);
+    check_all(L, chunk >= L.max_k);
     if (id >= slots * L.key_heads) return;
     const Unit u = find_unit(L, chunk, id / L.key_heads, static_cast<int>(id % L.key_heads), lane);
     if (u.rows == 0) return;
@@ -388,8 +411,7 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     // [warp][Q, dO, Q^T, dO^T][tile][chunk][lane]
     __shared__ uint4 frag[kWarps / NT][4][NT][KC][32];
-    check_items(L, static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x,
-                static_cast<long long>(gridDim.x) * blockDim.x);
+    check_all(L, false);
     const long long id = static_cast<long long>(blockIdx.x) * (kWarps / NT) + warp;
     if (id >= stride * L.key_heads) return;
     const int head = static_cast<int>(id % L.key_heads), dim = L.head_dim;
@@ -750,10 +772,13 @@ size_t attention_backward_workspace(const AttentionLaunch &L) {
 cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t stream) {
     using namespace attn;
     if (L.query_rows && L.key_rows && !few_rows(L)) return launch_forward_tiles(L, stream);
-    const cudaError_t e = cudaMemsetAsync(L.status, 0, sizeof(int32_t), stream);
-    if (e != cudaSuccess) return e;
+    const bool none = !L.query_rows || !L.key_rows;
+    if (none || L.items > kFewItems) {
+        const cudaError_t e = cudaMemsetAsync(L.status, 0, sizeof(int32_t), stream);
+        if (e != cudaSuccess) return e;
+    }
     const long long out_rows = static_cast<long long>(L.query_rows) * (L.q_off ? 1 : L.items);
-    if (!L.query_rows || !L.key_rows) {
+    if (none) {
         empty(L, L.o, out_rows, L.query_heads, L.lse, stream);
         return cudaGetLastError();
     }
@@ -763,9 +788,12 @@ cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t stream) {
 cudaError_t launch_attention_backward(const AttentionLaunch &L, cudaStream_t stream) {
     using namespace attn;
     if (L.query_rows && L.key_rows && !few_rows(L)) return launch_backward_tiles(L, stream);
-    const cudaError_t e = cudaMemsetAsync(L.status, 0, sizeof(int32_t), stream);
-    if (e != cudaSuccess) return e;
-    if (!L.query_rows || !L.key_rows) {
+    const bool none = !L.query_rows || !L.key_rows;
+    if (none || L.items > kFewItems) {
+        const cudaError_t e = cudaMemsetAsync(L.status, 0, sizeof(int32_t), stream);
+        if (e != cudaSuccess) return e;
+    }
+    if (none) {
         empty(L, L.d_q, L.query_rows, L.query_heads, nullptr, stream);
         empty(L, L.d_k, L.key_rows, L.key_heads, nullptr, stream);
         empty(L, L.d_v, L.key_rows, L.key_heads, nullptr, stream);

@@ -168,6 +168,31 @@ __device__ __forceinline__ Share share_of(const RotaryLaunch &P) {
     return b < P.q_blocks ? Share{0, b, P.q_blocks} : Share{1, b - P.q_blocks, static_cast<int>(gridDim.x) - P.q_blocks};
 }
 
+// A call on few rows has no memset of the status before it: block 0 looks at
+// every position and writes the word, and nobody else reports.
+constexpr int kFewRows = 1024;
+__device__ __forceinline__ bool few_rows(const RotaryLaunch &P) { return static_cast<long long>(P.part[0].rows) + P.part[1].rows <= kFewRows; }
+
+__device__ __forceinline__ void write_status(const RotaryLaunch &P) {
+    if (blockIdx.x != 0 || !few_rows(P)) return;   // the same for the block
+    bool bad = false;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const RotaryPartLaunch &part = P.part[p];
+        if (!part.positions) {
+            bad |= part.rows > P.table_rows;
+            continue;
+        }
+#pragma unroll 8
+        for (int r = threadIdx.x; r < part.rows; r += blockDim.x) {
+            const int pos = part.positions[r];
+            bad |= pos < 0 || pos >= P.table_rows;
+        }
+    }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *P.status = bad ? CLI_MALFORMED : CLI_OK;
+}
+
 // One row of partials of the gain's gradient: the block's lanes add up in a fixed order.
 template <int N, int VEC, int WARPS>
 __device__ __forceinline__ void gain_partial(const RotaryLaunch &P, float *to, const int *a_at, const int *b_at,
@@ -239,6 +264,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, MODE == kNormGrad ? 4 : 6)
     using S = Stream<T, MODE>;
     constexpr int N = 8, kStages = S::kStages, kUnits = S::kUnits;
     extern __shared__ __align__(16) uint8_t smem[];
+    write_status(P);
     const Share share = share_of(P);
     const RotaryPartLaunch &part = P.part[share.part];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -297,7 +323,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, MODE == kNormGrad ? 4 : 6)
         if (mine < my_rows) {
             p = part.positions ? part.positions[row_of(mine)] : static_cast<int>(row_of(mine));
             if (p < 0 || p >= P.table_rows) {
-                report(P.status, CLI_MALFORMED);
+                if (!few_rows(P)) report(P.status, CLI_MALFORMED);
                 p = 0;
             }
         }
@@ -411,6 +437,7 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
     constexpr int SPL = VEC >= 4 ? 1 : 4 / VEC;
     constexpr int N = VEC * SPL;   // pairs of a lane
     using C = Chunk<T, VEC>;
+    write_status(P);
     const Share share = share_of(P);
     const RotaryPartLaunch &part = P.part[share.part];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -448,7 +475,7 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
     for (long long row = share.block * kWarps + warp; row < part.rows; row += share.blocks * kWarps) {
         const int pos = part.positions ? part.positions[row] : static_cast<int>(row);
         if (pos < 0 || pos >= P.table_rows) {    // the same for the warp
-            if (lane == 0) report(P.status, CLI_MALFORMED);
+            if (lane == 0 && !few_rows(P)) report(P.status, CLI_MALFORMED);
             continue;
         }
         float c[N], s[N];
@@ -567,8 +594,10 @@ cudaError_t launch_layout(RotaryLaunch L, int vec, int &blocks, cudaStream_t str
         const int fit = static_cast<int>(200 * 1024 / smem), cap = MODE == kNormGrad ? 4 : 6;
         split(L, kStreamWarps, L.sm_count * (fit < cap ? fit : cap), blocks);
         auto kernel = L.interleaved ? stream_kernel<T, true, MODE> : stream_kernel<T, false, MODE>;
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
+        if (smem > 48 * 1024) {   // more than a kernel has without asking
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            if (e != cudaSuccess) return e;
+        }
         kernel<<<blocks, kStreamWarps * 32, smem, stream>>>(L);
     } else {
         split(L, kWarps, rotary_blocks(L.sm_count), blocks);
@@ -615,6 +644,10 @@ cudaError_t launch_rotary(RotaryLaunch L, cudaStream_t stream) {
     const int spl = vec >= 4 ? 1 : 4 / vec;
     L.lph_log2 = 0;
     while ((spl << L.lph_log2) < slots) ++L.lph_log2;
+    if (static_cast<long long>(L.part[0].rows) + L.part[1].rows > kFewRows) {
+        const cudaError_t e = cudaMemsetAsync(L.status, 0, sizeof(int32_t), stream);
+        if (e != cudaSuccess) return e;
+    }
     int blocks = 0;
     if (L.dtype == CLI_BF16) return launch_mode<__nv_bfloat16>(L, vec, blocks, stream);
     if (L.dtype == CLI_F16) return launch_mode<__half>(L, vec, blocks, stream);
