@@ -202,11 +202,11 @@ __device__ __forceinline__ void hand_out(Smem &sm, const AttentionLaunch &L, boo
         const long long id = static_cast<long long>(base) + lane;
         Item t;
         int r0 = 0;
-        const bool on = lane < batch && id < tiles && find_block(L, off, span, per_item, of_keys, id % slots, t, r0);
+        const bool on = lane < batch && id < tiles && find_block(L, off, span, per_item, of_keys, id / L.key_heads, t, r0);
         for (uint32_t left = __ballot_sync(0xffffffffu, on); left && ok; left &= left - 1) {
             const int from = __ffs(left) - 1;
-            Work w = of_keys ? Work{t.q0, t.o0, t.nq, t.k0 + r0, min(span, t.nk - r0), static_cast<int>(id / slots)}
-                             : Work{t.q0 + r0, t.o0 + r0, min(span, t.nq - r0), t.k0, t.nk, static_cast<int>(id / slots)};
+            Work w = of_keys ? Work{t.q0, t.o0, t.nq, t.k0 + r0, min(span, t.nk - r0), static_cast<int>(id % L.key_heads)}
+                             : Work{t.q0 + r0, t.o0 + r0, min(span, t.nq - r0), t.k0, t.nk, static_cast<int>(id % L.key_heads)};
             w.q0 = __shfl_sync(0xffffffffu, w.q0, from);
             w.o0 = __shfl_sync(0xffffffffu, w.o0, from);
             w.nq = __shfl_sync(0xffffffffu, w.nq, from);

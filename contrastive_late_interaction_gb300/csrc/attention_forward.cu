@@ -12,9 +12,11 @@
 //
 // Work.  A tile is 128 rows of (query row, head of the group): the heads that
 // share a key head are packed next to one another, so K and V are read once
-// for all of them.  A CTA takes two tiles at a time against blocks of 128
-// states, one persistent CTA per SM.  Warp roles:
-//   0      issues the TMA loads: Q, and K and V blocks through a ring of four
+// for all of them.  A persistent CTA takes two tiles at a time (or one, see
+// dispatch) against blocks of 128 states; key heads are handed out before
+// items, so that the lines that hold several heads are read together (64 x 4096
+// rows, 8 heads of 128: 240 -> 198 us).  Warp roles:
+//   0      issues the TMA loads: Q, and K and V blocks through a ring of
 //          stages;
 //   1      issues the products: S = Q K^T into TMEM, then O += P V with P read
 //          from TMEM, alternating between the two tiles so that one tile's
@@ -30,6 +32,12 @@
 //   4..11  softmax, four warps a tile, one row a thread: S from TMEM, P back
 //          over the same columns, and at the end O / l to global memory.
 // TMEM: S0 | S1 | O0 | O1, 128 columns each.
+//
+// Bound: 8 items of 2048 x 4096 rows, 16 heads of 128, run at 1400 TFLOP/s (75%
+// of measured), where the two tiles' softmax (about 1700 cycles a block of each,
+// half of it exponentials) and products (2100 for both) take turns; 2048 x
+// 1024 at 1280, the rest being the rows' way out at every item's end; 64 x 4096
+// at 5.5 TB/s, bound by HBM.
 
 #include <cuda.h>
 
@@ -39,25 +47,25 @@ namespace cli {
 namespace attn {
 namespace {
 
-constexpr int kStages = 4;   // even: K blocks in the even stages, V blocks in the odd ones
-constexpr int kThreads = 384;
 constexpr int kPairs = 4;
-constexpr int kReaders = 11;   // of a published pair: warps 0 to 2, eight softmax warps
 
 struct Pair {
     int q0, o0, rows, k0, nk, head;   // rows < 0: no more work
 };
 
-template <int BOXES>
+// TILES: tiles that a CTA works on at a time.
+template <int BOXES, int TILES>
 struct Storage {
-    alignas(1024) uint8_t q[2][BOXES * kBoxBytes];
+    // K blocks in the even stages, V blocks in the odd ones.
+    static constexpr int kStages = TILES == 1 && BOXES == 2 ? 2 : 4;
+    alignas(1024) uint8_t q[TILES][BOXES * kBoxBytes];
     alignas(1024) uint8_t kv[kStages][BOXES * kBoxBytes];
     alignas(128) uint8_t ones[kColumnBytes];             // a 1, and 15 zeros, for each of 128 rows
     alignas(128) uint8_t left_out[kStages / 2][kColumnBytes];   // 0 or an infinity, and 15 zeros, for each state of a K stage
     Pair pair[kPairs];
     uint64_t pair_full[kPairs], pair_empty[kPairs];
-    uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages], ready[kStages];
-    uint64_t s_full[2], p_ready[2], o_full[2], done;
+    uint64_t q_full[TILES], q_empty[TILES], kv_full[kStages], kv_empty[kStages], ready[kStages];
+    uint64_t s_full[TILES], p_ready[TILES], o_full[TILES], done;
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -66,16 +74,18 @@ struct Maps {
     CUtensorMap q, k, v;
 };
 
-template <typename T, int BOXES>
-__global__ void __launch_bounds__(kThreads, 1)
+template <typename T, int BOXES, int TILES>
+__global__ void __launch_bounds__(128 + 128 * TILES, 3 - TILES)
     forward_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
                    long long slots, long long tiles, unsigned long long *counter) {
     extern __shared__ uint8_t smem_raw[];
-    using Smem = Storage<BOXES>;
+    using Smem = Storage<BOXES, TILES>;
+    constexpr int kStages = Smem::kStages, kThreads = 128 + 128 * TILES;
+    constexpr uint32_t kColumns = TILES * 256, kO = TILES * 128;   // of TMEM: the tiles' scores, then their sums
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < TILES; ++i) {
             mbar_init(&sm.q_full[i], 1);
             mbar_init(&sm.q_empty[i], 1);
             mbar_init(&sm.s_full[i], 1);
@@ -89,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kPairs; ++i) {
             mbar_init(&sm.pair_full[i], 1);
-            mbar_init(&sm.pair_empty[i], kReaders);
+            mbar_init(&sm.pair_empty[i], 3 + 4 * TILES);   // warps 0 to 2 and the softmax warps read it
         }
         mbar_init(&sm.done, 1);
         sm.abort_flag = 0;
@@ -98,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&M.k);
         prefetch_tmap(&M.v);
     }
-    if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+    if (warp == 1) tmem_alloc(&sm.tmem_base, kColumns);
     for (uint32_t i = threadIdx.x; i < kColumnBytes / 16; i += kThreads) {
         const uint32_t at = i * 16;
         st_shared_v4(smem_u32(sm.ones) + at, at < 2048 ? Type<T>::one : 0u, 0, 0, 0);
@@ -111,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     after_previous();
     const uint32_t tmem = sm.tmem_base;
     volatile int *abort_flag = &sm.abort_flag;
-    const int group = L.group, dim = L.head_dim, span = 2 * rows_per_tile;
+    const int group = L.group, dim = L.head_dim, span = TILES * rows_per_tile;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, abort_flag, L.status); };
     auto wait_one = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, L.status); };   // a thread's
     // The next published pair, for a reader; false where there is none or the CTA gave up.
@@ -130,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t q_bytes = BOXES * static_cast<uint32_t>(rows_per_tile * group) * 128u;
         Pair p;
         for (uint32_t it = 0; ok && next_pair(it, p); ++it) {
-            const int blocks = (p.nk + 127) / 128, nt = p.rows > rows_per_tile ? 2 : 1;
+            const int blocks = (p.nk + 127) / 128, nt = TILES == 2 && p.rows > rows_per_tile ? 2 : 1;
             if (lane == 0 && blocks) {
                 auto load = [&](uint8_t *dst, const CUtensorMap *map, uint64_t *bar, int head, int row) {
 #pragma unroll
@@ -181,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Pair p;
         for (uint32_t it = 0; ok && next_pair(it, p); ++it) {
             const int nk = static_cast<int>(uniform(p.nk)), rows = static_cast<int>(uniform(p.rows));
-            const int blocks = (nk + 127) / 128, nt = rows > rows_per_tile ? 2 : 1;
+            const int blocks = (nk + 127) / 128, nt = TILES == 2 && rows > rows_per_tile ? 2 : 1;
             if (blocks == 0) continue;
             auto scores = [&](int t, int j, uint32_t e) {
                 const uint32_t n = (min(128, nk - 128 * j) + 31) & ~31;
@@ -209,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!wait(&sm.p_ready[t], (p_phase >> t) & 1)) { ok = false; break; }
                     p_phase ^= 1u << t;
                     tc_fence_after();
-                    mma_pairs<8>(leader, tm + 256 + t * 128, tm + t * 128, v_desc + (ev % kStages) * kTile, idesc_o,
+                    mma_pairs<8>(leader, tm + kO + t * 128, tm + t * 128, v_desc + (ev % kStages) * kTile, idesc_o,
                                  min(128, nk - 128 * j), j != 0);
                     if (j + 1 == blocks) {
                         issue_commit(leader, &sm.o_full[t]);
@@ -285,10 +295,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             Item t;
             int r0 = 0;
             const bool on = lane < batch && id < tiles &&
-                            find_block(L, L.q_off, span, per_item, false, id % slots, t, r0);
+                            find_block(L, L.q_off, span, per_item, false, id / L.key_heads, t, r0);
             for (uint32_t left = __ballot_sync(0xffffffffu, on); left && ok; left &= left - 1) {
                 const int from = __ffs(left) - 1;
-                Pair p = {t.q0 + r0, t.o0 + r0, min(span, t.nq - r0), t.k0, t.nk, static_cast<int>(id / slots)};
+                Pair p = {t.q0 + r0, t.o0 + r0, min(span, t.nq - r0), t.k0, t.nk, static_cast<int>(id % L.key_heads)};
                 p.q0 = __shfl_sync(0xffffffffu, p.q0, from);
                 p.o0 = __shfl_sync(0xffffffffu, p.o0, from);
                 p.rows = __shfl_sync(0xffffffffu, p.rows, from);
@@ -306,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r_in = m_row / group, head_in = m_row - r_in * group;
         const bool in_tile = r_in < rows_per_tile;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-        const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * 128;
+        const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + kO + t * 128;
         const float sl2 = fmaxf(fabsf(L.scale) * kLog2e, 1e-30f);   // above 0, so that -infinity stays that
         const float lazy = 8.0f / sl2;   // in units of a raw score
         const float2 sl22 = make_float2(sl2, sl2);
@@ -422,13 +432,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 512);
+    if (warp == 1) tmem_dealloc(tmem, kColumns);
 }
 
-template <typename T, int BOXES>
+template <typename T, int BOXES, int TILES>
 cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
     const int rows_per_tile = 128 / L.group;
-    const long long span = 2 * rows_per_tile;
+    const long long span = TILES * rows_per_tile;
     const long long slots = L.q_off ? L.query_rows / span + L.items
                                     : static_cast<long long>(L.items) * ((L.query_rows + span - 1) / span);
     const long long tiles = slots * L.key_heads;
@@ -438,23 +448,38 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
         !encode_heads_tiles(&M.k, L.k, bf16, L.head_dim, L.key_heads, L.key_rows, 1, kTileRows) ||
         !encode_heads_tiles(&M.v, L.v, bf16, L.head_dim, L.key_heads, L.key_rows, 1, kTileRows))
         return cudaErrorInvalidValue;
-    const size_t smem = sizeof(Storage<BOXES>) + 1024;
-    auto kernel = forward_kernel<T, BOXES>;
+    const size_t smem = sizeof(Storage<BOXES, TILES>) + 1024;
+    auto kernel = forward_kernel<T, BOXES, TILES>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(tiles < L.sm_count ? tiles : L.sm_count);
+    const long long ctas = static_cast<long long>(L.sm_count) * (3 - TILES);
     unsigned long long *counters = reinterpret_cast<unsigned long long *>(L.workspace);
     begin_kernel<<<1, 32, 0, stream>>>(L.status, counters);
-    return launch_after(kernel, dim3(grid), kThreads, smem, stream, L, M, rows_per_tile, slots, tiles, counters);
+    return launch_after(kernel, dim3(static_cast<unsigned>(tiles < ctas ? tiles : ctas)), 128 + 128 * TILES, smem, stream, L, M,
+                        rows_per_tile, slots, tiles, counters);
+}
+
+// Two tiles a CTA share K and V, which is what long queries need (2048 x 1024
+// rows, 16 heads of 128: 431 us against 521 with one tile a CTA, two CTAs an
+// SM).  One tile a CTA serves calls whose items fill no second one, with
+// narrow heads, for which two CTAs of the full ring fit an SM (64 x 256 rows, 8
+// heads of 64: 90 us against 117; at heads of 128 the short ring loses what
+// the second CTA gains), and calls with less than a pair for every other SM
+// (2048 x 2048 rows, 2 heads: 35 us against 38).
+template <typename T>
+cudaError_t dispatch(const AttentionLaunch &L, cudaStream_t stream) {
+    const bool one = static_cast<long long>(L.max_q) * L.group <= 128;
+    const long long rows = static_cast<long long>(L.query_rows) * (L.q_off ? 1 : L.items);
+    const bool small = (rows * L.group / 256 + 1) * L.key_heads <= L.sm_count / 2;
+    if (L.head_dim > 64) return small ? launch<T, 2, 1>(L, stream) : launch<T, 2, 2>(L, stream);
+    return one || small ? launch<T, 1, 1>(L, stream) : launch<T, 1, 2>(L, stream);
 }
 
 }  // namespace
 
 // Needs at least one query row and one state (the tensor maps have no empty form).
 cudaError_t launch_forward_tiles(const AttentionLaunch &L, cudaStream_t stream) {
-    const bool wide = L.head_dim > 64;
-    if (L.dtype == CLI_BF16) return wide ? launch<__nv_bfloat16, 2>(L, stream) : launch<__nv_bfloat16, 1>(L, stream);
-    return wide ? launch<__half, 2>(L, stream) : launch<__half, 1>(L, stream);
+    return L.dtype == CLI_BF16 ? dispatch<__nv_bfloat16>(L, stream) : dispatch<__half>(L, stream);
 }
 
 }  // namespace attn
