@@ -42,7 +42,7 @@ __device__ __forceinline__ long long stat_at(const AttentionLaunch &L, int out_r
 // A warp a row, 16 lanes a head, 8 elements a lane, the loads of eight heads
 // under way together.
 template <typename T>
-__global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ AttentionLaunch L, int out_rows,
+__global__ void __launch_bounds__(256, 4) stats_kernel(const __grid_constant__ AttentionLaunch L, int out_rows,
                                                     float2 *stats) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     after_previous();

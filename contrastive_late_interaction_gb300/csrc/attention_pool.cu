@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(256)
 // backward
 // ----------------------------------------------------------------------------
 
-// One step takes 16 states: S^T = K Q^T and dP^T = V dO^T, then
+// A step loads 8 KB and takes 16 states at a time: S^T = K Q^T and dP^T = V dO^T, then
 // dV = P^T dO and dK = dS^T Q of these states (the inner index is the row, P^T
 // and dS^T are A operands as they come out of the first products), and
 // dQ^T += K^T dS^T.  The fragments of Q and dO, as B operands of the first
@@ -407,7 +407,7 @@ template <typename T, int DP, int NT>
 __global__ void __launch_bounds__(kWarps / NT * 32, 3)
     backward_kernel(const __grid_constant__ AttentionLaunch L, int chunk, long long slots, long long stride,
                     float *part_dq) {
-    constexpr int KC = DP / 32;
+    constexpr int KC = DP / 32, KG = 128 / DP;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     // [warp][Q, dO, Q^T, dO^T][tile][chunk][lane]
     __shared__ uint4 frag[kWarps / NT][4][NT][KC][32];
@@ -507,66 +507,71 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
         const T *vbase = static_cast<const T *>(L.v.data) + head * L.v.head + 8 * t;
         T *dkbase = static_cast<T *>(L.d_k.data) + head * L.d_k.head + 8 * t;
         T *dvbase = static_cast<T *>(L.d_v.data) + head * L.d_v.head + 8 * t;
-        for (int j = 0; j < u.n; j += 16) {
-            const int count = min(16, u.n - j);
-            const uint32_t keep = kept(L, u.k0 + j, count, lane);
-            uint32_t kr[2][KC][4], vr[2][KC][4];
+        for (int j0 = 0; j0 < u.n; j0 += 16 * KG) {
+            const uint32_t keep0 = kept(L, u.k0 + j0, min(16 * KG, u.n - j0), lane);
+            uint32_t kr0[KG][2][KC][4], vr0[KG][2][KC][4];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int s = 8 * y + g;
-                const long long row = u.k0 + j + s;
+            for (int x = 0; x < KG; ++x)
 #pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    const bool on = ((keep >> s) & 1u) && 32 * c + 8 * t < dim;
-                    load_if(on, kbase + row * L.k.row + 32 * c, kr[y][c]);
-                    load_if(on, vbase + row * L.v.row + 32 * c, vr[y][c]);
-                }
-            }
-            uint32_t p[NT][4], ds[NT][4];   // of states g and g + 8: high halves, then low ones
+                for (int y = 0; y < 2; ++y) {
+                    const int s = 16 * x + 8 * y + g;
+                    const long long row = u.k0 + j0 + s;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    const uint4 q = frag[warp][0][n][c][lane], d = frag[warp][1][n][c][lane];
-                    mma16<T>(s4, kr[0][c][0], kr[1][c][0], kr[0][c][1], kr[1][c][1], q.x, q.y);
-                    mma16<T>(s4, kr[0][c][2], kr[1][c][2], kr[0][c][3], kr[1][c][3], q.z, q.w);
-                    mma16<T>(d4, vr[0][c][0], vr[1][c][0], vr[0][c][1], vr[1][c][1], d.x, d.y);
-                    mma16<T>(d4, vr[0][c][2], vr[1][c][2], vr[0][c][3], vr[1][c][3], d.z, d.w);
-                }
-                float pe[4], de[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool on = (keep >> (8 * (i >> 1) + g)) & 1u;
-                    pe[i] = on ? ex2_full(fmaf(s4[i], sl2, -lse[n][i & 1])) : 0.0f;
-                    de[i] = on ? pe[i] * (d4[i] - delta[n][i & 1]) : 0.0f;
-                }
-                split_pair<T>(pe[0], pe[1], p[n][0], p[n][2]);
-                split_pair<T>(pe[2], pe[3], p[n][1], p[n][3]);
-                split_pair<T>(de[0], de[1], ds[n][0], ds[n][2]);
-                split_pair<T>(de[2], de[3], ds[n][1], ds[n][3]);
-            }
-#pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                float av[4][4], ak[4][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    av[i][0] = av[i][1] = av[i][2] = av[i][3] = ak[i][0] = ak[i][1] = ak[i][2] = ak[i][3] = 0.0f;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 q = frag[warp][2][n][c][lane], d = frag[warp][3][n][c][lane];
-                    const uint32_t qi[4] = {q.x, q.y, q.z, q.w}, di[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        // 8 rows twice: against the high halves and against the low ones
-                        mma16<T>(av[i], p[n][0], p[n][1], p[n][2], p[n][3], di[i], di[i]);
-                        mma16<T>(ak[i], ds[n][0], ds[n][1], ds[n][2], ds[n][3], qi[i], qi[i]);
+                    for (int c = 0; c < KC; ++c) {
+                        const bool on = ((keep0 >> s) & 1u) && 32 * c + 8 * t < dim;
+                        load_if(on, kbase + row * L.k.row + 32 * c, kr0[x][y][c]);
+                        load_if(on, vbase + row * L.v.row + 32 * c, vr0[x][y][c]);
                     }
                 }
-                if (32 * c + 8 * t < dim) {
+#pragma unroll
+            for (int x = 0; x < KG; ++x) {
+                const int j = j0 + 16 * x, count = min(16, u.n - j);
+                const uint32_t keep = keep0 >> (16 * x);
+                auto &kr = kr0[x];
+                auto &vr = vr0[x];
+                uint32_t p[NT][4], ds[NT][4];   // of states g and g + 8: high halves, then low ones
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int c = 0; c < KC; ++c) {
+                        const uint4 q = frag[warp][0][n][c][lane], d = frag[warp][1][n][c][lane];
+                        mma16<T>(s4, kr[0][c][0], kr[1][c][0], kr[0][c][1], kr[1][c][1], q.x, q.y);
+                        mma16<T>(s4, kr[0][c][2], kr[1][c][2], kr[0][c][3], kr[1][c][3], q.z, q.w);
+                        mma16<T>(d4, vr[0][c][0], vr[1][c][0], vr[0][c][1], vr[1][c][1], d.x, d.y);
+                        mma16<T>(d4, vr[0][c][2], vr[1][c][2], vr[0][c][3], vr[1][c][3], d.z, d.w);
+                    }
+                    float pe[4], de[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool on = (keep >> (8 * (i >> 1) + g)) & 1u;
+                        pe[i] = on ? ex2_full(fmaf(s4[i], sl2, -lse[n][i & 1])) : 0.0f;
+                        de[i] = on ? pe[i] * (d4[i] - delta[n][i & 1]) : 0.0f;
+                    }
+                    split_pair<T>(pe[0], pe[1], p[n][0], p[n][2]);
+                    split_pair<T>(pe[2], pe[3], p[n][1], p[n][3]);
+                    split_pair<T>(de[0], de[1], ds[n][0], ds[n][2]);
+                    split_pair<T>(de[2], de[3], ds[n][1], ds[n][3]);
+                }
+#pragma unroll
+                for (int c = 0; c < KC; ++c) {
+                    float av[4][4], ak[4][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        av[i][0] = av[i][1] = av[i][2] = av[i][3] = ak[i][0] = ak[i][1] = ak[i][2] = ak[i][3] = 0.0f;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const uint4 q = frag[warp][2][n][c][lane], d = frag[warp][3][n][c][lane];
+                        const uint32_t qi[4] = {q.x, q.y, q.z, q.w}, di[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            // 8 rows twice: against the high halves and against the low ones
+                            mma16<T>(av[i], p[n][0], p[n][1], p[n][2], p[n][3], di[i], di[i]);
+                            mma16<T>(ak[i], ds[n][0], ds[n][1], ds[n][2], ds[n][3], qi[i], qi[i]);
+                        }
+                    }
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        if (8 * y + g >= count) continue;
                         const long long row = u.k0 + j + 8 * y + g;
                         uint32_t wv[4], wk[4];
 #pragma unroll
@@ -574,28 +579,31 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
                             wv[i] = Type<T>::pack(av[i][2 * y], av[i][2 * y + 1]);
                             wk[i] = Type<T>::pack(ak[i][2 * y] * L.scale, ak[i][2 * y + 1] * L.scale);
                         }
-                        __stcs(reinterpret_cast<uint4 *>(dvbase + row * L.d_v.row + 32 * c), make_uint4(wv[0], wv[1], wv[2], wv[3]));
-                        __stcs(reinterpret_cast<uint4 *>(dkbase + row * L.d_k.row + 32 * c), make_uint4(wk[0], wk[1], wk[2], wk[3]));
+                        if (32 * c + 8 * t < dim && 8 * y + g < count) {
+                            __stcs(reinterpret_cast<uint4 *>(dvbase + row * L.d_v.row + 32 * c), make_uint4(wv[0], wv[1], wv[2], wv[3]));
+                            __stcs(reinterpret_cast<uint4 *>(dkbase + row * L.d_k.row + 32 * c), make_uint4(wk[0], wk[1], wk[2], wk[3]));
+                        }
                     }
+                    __syncwarp();   // the products that follow are the whole warp's
                 }
+                uint32_t bs[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) bs[n][i] = transpose8(ds[n][i]);
+#pragma unroll
+                for (int c = 0; c < KC; ++c)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t a0 = transpose8(kr[0][c][2 * i]), a1 = transpose8(kr[0][c][2 * i + 1]);
+                        const uint32_t a2 = transpose8(kr[1][c][2 * i]), a3 = transpose8(kr[1][c][2 * i + 1]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma16<T>(dq[c][i][n], a0, a1, a2, a3, bs[n][0], bs[n][1]);
+                            mma16<T>(dq[c][i][n], a0, a1, a2, a3, bs[n][2], bs[n][3]);
+                        }
+                    }
             }
-            uint32_t bs[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) bs[n][i] = transpose8(ds[n][i]);
-#pragma unroll
-            for (int c = 0; c < KC; ++c)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t a0 = transpose8(kr[0][c][2 * i]), a1 = transpose8(kr[0][c][2 * i + 1]);
-                    const uint32_t a2 = transpose8(kr[1][c][2 * i]), a3 = transpose8(kr[1][c][2 * i + 1]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma16<T>(dq[c][i][n], a0, a1, a2, a3, bs[n][0], bs[n][1]);
-                        mma16<T>(dq[c][i][n], a0, a1, a2, a3, bs[n][2], bs[n][3]);
-                    }
-                }
         }
         __syncwarp();
         if (L.q_off) {
