@@ -15,6 +15,7 @@ namespace cli {
 namespace {
 
 constexpr size_t kRowsLimit = 1ull << 31;
+constexpr size_t kTapeLimit = kRowsLimit - 4096;   // of attention: blocks of states are rounded up in 32 bits
 
 size_t dtype_bytes(int dtype) { return dtype == CLI_F32 ? 4 : 2; }
 
@@ -191,7 +192,7 @@ cli_status_t rotary_call(const cli_rotary_t *a, bool norm, bool backward) {
 // The sizes of an attention call, checked; `L` receives them.
 cli_status_t attention_sizes(const cli_attention_t *a, AttentionLaunch &L) {
     if (a->dtype != CLI_BF16 && a->dtype != CLI_F16) return CLI_UNSUPPORTED;
-    if (a->items == 0 || a->items >= kRowsLimit || a->query_rows >= kRowsLimit || a->key_rows >= kRowsLimit)
+    if (a->items == 0 || a->items >= kRowsLimit || a->query_rows >= kTapeLimit || a->key_rows >= kTapeLimit)
         return CLI_SHAPE_MISMATCH;
     if (a->head_dim == 0 || a->head_dim % 8 != 0) return CLI_SHAPE_MISMATCH;
     if (a->head_dim > 128) return CLI_UNSUPPORTED;

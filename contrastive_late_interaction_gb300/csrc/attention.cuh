@@ -345,6 +345,42 @@ __device__ __forceinline__ void store_sums(uint32_t sums, int dim, float scale, 
     }
 }
 
+// The same as 32-bit sums; `out` on 32 bytes.
+__device__ __forceinline__ void store_partials(uint32_t sums, int dim, bool warp_has, bool mine, float *out) {
+#pragma unroll 1
+    for (int x = 0; x < dim; x += 8) {
+        uint32_t r[8] = {};
+        if (warp_has) {
+            tmem_ld8_async(sums + x, r);
+            tmem_wait_ld();
+            tmem_regs_ready_n(r);
+        }
+        if (mine) store_32(out + x, true, r);
+        __syncwarp();
+    }
+}
+
+// How a call's items are cut along their states where there are too few blocks
+// of queries to go round: `parts` chunks of `chunk` states (a multiple of 128)
+// each, as many as give `ctas` CTAs a block, of about `least` states at least.
+struct Split {
+    int parts, chunk;
+};
+inline Split split_of(const AttentionLaunch &L, long long blocks, long long ctas, long long least) {
+    const long long most = (L.max_k + least - 1) / least;
+    long long parts = blocks > 0 ? ctas / blocks : 1;
+    if (parts > most) parts = most;
+    if (parts > 32) parts = 32;
+    if (parts < 1) parts = 1;
+    return {static_cast<int>(parts), static_cast<int>(((L.max_k + parts - 1) / parts + 127) / 128 * 128)};
+}
+// The states of item t in part `part`.
+__device__ __forceinline__ void part_of(const Split &s, int part, Item &t) {
+    const int from = static_cast<int>(min(static_cast<long long>(t.nk), static_cast<long long>(part) * s.chunk));
+    t.k0 += from;
+    t.nk = min(s.chunk, t.nk - from);
+}
+
 // Zeroes rows of a tile: those of the first `rows` whose bit in `keep` (one
 // word per 32 rows) is 0.  One warp, a row a lane; the lanes' chunks are
 // staggered so that they fall into different banks.

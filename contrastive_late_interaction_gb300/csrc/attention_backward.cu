@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(256, 4) stats_kernel(const __grid_constant__ A
 }
 
 // One CTA's current work: a tile of 128 states or of 128 packed rows.
-struct Work {
-    int q0, o0, nq, k0, nk, head;   // nq, nk: rows of the item to walk, or of the tile; head < 0: no more work
+struct alignas(16) Work {
+    int q0, o0, nq, k0, nk, head, part;   // nq, nk: rows of the item to walk, or of the tile; head < 0: no more work
 };
 
 // The walked tiles come through two rings.  Those of A (Q, or K) are held
@@ -178,8 +178,8 @@ __device__ __forceinline__ bool next_work(Smem &sm, const AttentionLaunch &L, ui
 
 // Hands out the work: blocks of `span` states (of_keys) or queries.
 template <typename Smem>
-__device__ __forceinline__ void hand_out(Smem &sm, const AttentionLaunch &L, bool of_keys, int span, long long slots,
-                                         long long tiles, unsigned long long *counter) {
+__device__ __forceinline__ void hand_out(Smem &sm, const AttentionLaunch &L, bool of_keys, int span, long long tiles,
+                                         const Split &cut, unsigned long long *counter) {
     const int lane = threadIdx.x & 31, batch = batch_of(tiles);
     const uint64_t *off = of_keys ? L.k_off : L.q_off;
     const int per_item = off ? 0 : (L.query_rows + span - 1) / span;
@@ -202,21 +202,31 @@ __device__ __forceinline__ void hand_out(Smem &sm, const AttentionLaunch &L, boo
         const long long id = static_cast<long long>(base) + lane;
         Item t;
         int r0 = 0;
-        const bool on = lane < batch && id < tiles && find_block(L, off, span, per_item, of_keys, id / L.key_heads, t, r0);
+        long long block = id / L.key_heads;
+        const int head = static_cast<int>(id - block * L.key_heads);
+        int part = 0;
+        if (cut.parts > 1) {
+            const long long whole = block / cut.parts;
+            part = static_cast<int>(block - whole * cut.parts);
+            block = whole;
+        }
+        const bool on = lane < batch && id < tiles && find_block(L, off, span, per_item, of_keys, block, t, r0);
+        if (on && cut.parts > 1) part_of(cut, part, t);
         for (uint32_t left = __ballot_sync(0xffffffffu, on); left && ok; left &= left - 1) {
             const int from = __ffs(left) - 1;
-            Work w = of_keys ? Work{t.q0, t.o0, t.nq, t.k0 + r0, min(span, t.nk - r0), static_cast<int>(id % L.key_heads)}
-                             : Work{t.q0 + r0, t.o0 + r0, min(span, t.nq - r0), t.k0, t.nk, static_cast<int>(id % L.key_heads)};
+            Work w = of_keys ? Work{t.q0, t.o0, t.nq, t.k0 + r0, min(span, t.nk - r0), head, part}
+                             : Work{t.q0 + r0, t.o0 + r0, min(span, t.nq - r0), t.k0, t.nk, head, part};
             w.q0 = __shfl_sync(0xffffffffu, w.q0, from);
             w.o0 = __shfl_sync(0xffffffffu, w.o0, from);
             w.nq = __shfl_sync(0xffffffffu, w.nq, from);
             w.k0 = __shfl_sync(0xffffffffu, w.k0, from);
             w.nk = __shfl_sync(0xffffffffu, w.nk, from);
             w.head = __shfl_sync(0xffffffffu, w.head, from);
+            w.part = __shfl_sync(0xffffffffu, w.part, from);
             ok = publish(w);
         }
     }
-    if (ok) publish({0, 0, 0, 0, 0, -1});
+    if (ok) publish({0, 0, 0, 0, 0, -1, 0});
 }
 
 // The TMA producer's side.
@@ -272,7 +282,7 @@ struct Producer {
 template <typename T, int BOXES>
 __global__ void __launch_bounds__(kThreads, 1)
     dkv_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
-               int out_rows, const float2 *stats, long long slots, long long tiles, unsigned long long *counter) {
+               int out_rows, const float2 *stats, long long tiles, unsigned long long *counter) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     using Smem = Storage<BOXES>;
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
@@ -405,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 3) {
-        hand_out(sm, L, true, 128, slots, tiles, counter);
+        hand_out(sm, L, true, 128, tiles, {1, 0}, counter);
     } else {
         const int side = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
@@ -509,7 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename T, int BOXES>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
-              int out_rows, const float2 *stats, float *partials, long long slots, long long tiles, unsigned long long *counter) {
+              int out_rows, const float2 *stats, float *partials, long long tiles, Split cut,
+              unsigned long long *counter) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     using Smem = Storage<BOXES>;
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
@@ -624,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 3) {
-        hand_out(sm, L, false, rows_per_tile, slots, tiles, counter);
+        hand_out(sm, L, false, rows_per_tile, tiles, cut, counter);
     } else {
         const int side = (warp - 4) >> 2, quad = warp & 3, m_row = quad * 32 + lane;
         const int r_in = m_row / group, head_in = m_row - r_in * group;
@@ -706,18 +717,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int first = side ? half : 0, count = side ? dim - half : min(half, dim);
             const uint32_t sums = tmem + lanes + 384 + first;
             if (partials) {
-                float *out = partials + ((static_cast<long long>(w.o0) + r_in) * L.query_heads + head) * dim + first;
-#pragma unroll 1
-                for (int x = 0; x < count; x += 8) {
-                    uint32_t o[8] = {};
-                    if (blocks) {
-                        tmem_ld8_async(sums + x, o);
-                        tmem_wait_ld();
-                        tmem_regs_ready_n(o);
-                    }
-                    if (mine) store_32(out + x, true, o);
-                    __syncwarp();
-                }
+                float *out = partials + ((static_cast<long long>(w.part) * out_rows + w.o0 + r_in) * L.query_heads + head) * dim + first;
+                store_partials(sums, count, blocks != 0, mine, out);
             } else {
                 T *out = static_cast<T *>(L.d_q.data) + (static_cast<long long>(w.q0) + r_in) * L.d_q.row + head * L.d_q.head + first;
                 store_sums<T>(sums, count, L.scale, blocks != 0, false, mine, out);
@@ -731,31 +732,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     after_previous();   // what follows on the stream waits for this kernel alone
 }
 
-// dQ of shared queries: the items' sums, in their order, eight elements a thread.
+// dQ of shared queries, and of items cut into parts: the sums of all, in a
+// fixed order.  A block takes 128 elements, four a lane; its warps take an
+// eighth of the sums each, so that many small items do not make one long chain
+// of loads (512 items of 17 rows, 16 heads of 64: 144 us with a thread walking
+// all of them).
+constexpr int kSumElems = 128;
 template <typename T>
-__global__ void __launch_bounds__(256) dq_sum_kernel(const __grid_constant__ AttentionLaunch L, const float *partials) {
+__global__ void __launch_bounds__(256) dq_sum_kernel(const __grid_constant__ AttentionLaunch L, int sums, const float *partials) {
+    __shared__ float4 part[8][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long row_elems = static_cast<long long>(L.query_heads) * L.head_dim, all = row_elems * L.query_rows;
-    const long long at = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 8;
-    if (at >= all) return;
-    float s[8] = {};
-    for (int i = 0; i < L.items; ++i) {
-        const float4 *src = reinterpret_cast<const float4 *>(partials + i * all + at);
-        const float4 a = src[0], b = src[1];
-        s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;
-        s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
+    const long long at = static_cast<long long>(blockIdx.x) * kSumElems + lane * 4;
+    const int per = (sums + 7) / 8, from = min(sums, warp * per), to = min(sums, from + per);
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](const float4 &v) { s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w; };
+    if (at < all) {
+#pragma unroll 8
+        for (int i = from; i < to; ++i) add(__ldcs(reinterpret_cast<const float4 *>(partials + i * all + at)));
     }
+    part[warp][lane] = s;
+    __syncthreads();
+    if (warp || at >= all) return;
+    for (int w = 1; w < 8; ++w) add(part[w][lane]);
     const long long row = at / row_elems;
     const int in_row = static_cast<int>(at - row * row_elems), head = in_row / L.head_dim;
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = Type<T>::pack(s[2 * i] * L.scale, s[2 * i + 1] * L.scale);
-    *reinterpret_cast<uint4 *>(static_cast<T *>(L.d_q.data) + row * L.d_q.row + head * L.d_q.head + in_row -
-                               head * L.head_dim) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint2 *>(static_cast<T *>(L.d_q.data) + row * L.d_q.row + head * L.d_q.head + in_row - head * L.head_dim) =
+        make_uint2(Type<T>::pack(s.x * L.scale, s.y * L.scale), Type<T>::pack(s.z * L.scale, s.w * L.scale));
 }
 
 size_t stats_bytes(const AttentionLaunch &L) {
     const size_t out_rows = static_cast<size_t>(L.query_rows) * (L.q_off ? 1 : L.items);
     return align256(out_rows * L.query_heads * sizeof(float2));
+}
+
+// dq_kernel's work: slots of tiles of queries, parts along the states, and the sums that this leaves for each row.
+struct Cut {
+    long long slots;
+    Split split;
+    int sums;   // 1: none, dQ is stored at once
+};
+Cut cut_of(const AttentionLaunch &L) {
+    const int rows_per_tile = 128 / L.group;
+    Cut c;
+    c.slots = L.q_off ? static_cast<long long>(L.query_rows) / rows_per_tile + L.items
+                      : static_cast<long long>(L.items) * ((L.query_rows + rows_per_tile - 1) / rows_per_tile);
+    const long long filled = L.q_off ? (L.query_rows + rows_per_tile - 1) / rows_per_tile : c.slots;
+    const long long blocks = (filled > L.items ? filled : L.items) * L.key_heads;
+    // dkv_kernel runs beside, with a CTA for each of its blocks while they last: parts shorter than what those
+    // walk end no sooner, and a second wave behind them later than whole items (200 x 2048 rows, 8 heads: 31 us
+    // in parts, 25 whole).
+    const long long left = 152 - (static_cast<long long>(L.key_rows) + 127) / 128 * L.key_heads;
+    const long long walk = static_cast<long long>(L.max_q) * L.group;
+    c.split = split_of(L, blocks, left >= blocks ? left : 152, walk > 512 ? walk : 512);
+    c.sums = (L.q_off ? 1 : L.items) * c.split.parts;
+    return c;
 }
 
 template <typename T, int BOXES>
@@ -764,7 +795,8 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
     const int out_rows = L.query_rows * (L.q_off ? 1 : L.items);
     unsigned long long *counters = reinterpret_cast<unsigned long long *>(L.workspace);
     float2 *stats = reinterpret_cast<float2 *>(L.workspace + kCounterBytes);
-    float *partials = L.q_off ? nullptr : reinterpret_cast<float *>(L.workspace + kCounterBytes + stats_bytes(L));
+    const Cut c = cut_of(L);
+    float *partials = L.q_off && c.sums == 1 ? nullptr : reinterpret_cast<float *>(L.workspace + kCounterBytes + stats_bytes(L));
     Maps M;
     const bool bf16 = Type<T>::bf16;
     if (!encode_heads_tiles(&M.q, L.q, bf16, L.head_dim, L.query_heads, L.query_rows, L.group, rows_per_tile) ||
@@ -786,19 +818,17 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     auto grid = [&](long long tiles) { return static_cast<unsigned>(tiles < L.sm_count ? tiles : L.sm_count); };
-    const long long k_slots = L.key_rows / 128 + L.items, k_tiles = k_slots * L.key_heads;
-    e = launch_after(dkv, dim3(grid(k_tiles)), kThreads, smem, stream, L, M, rows_per_tile, out_rows, stats, k_slots, k_tiles,
+    const long long k_tiles = (static_cast<long long>(L.key_rows) / 128 + L.items) * L.key_heads;
+    e = launch_after(dkv, dim3(grid(k_tiles)), kThreads, smem, stream, L, M, rows_per_tile, out_rows, stats, k_tiles,
                      counters);
     if (e != cudaSuccess) return e;
-    const long long q_slots = L.q_off ? static_cast<long long>(L.query_rows) / rows_per_tile + L.items
-                                      : static_cast<long long>(L.items) * ((L.query_rows + rows_per_tile - 1) / rows_per_tile);
-    const long long q_tiles = q_slots * L.key_heads;
-    e = launch_after(dq, dim3(grid(q_tiles)), kThreads, smem, stream, L, M, rows_per_tile, out_rows, stats, partials, q_slots,
-                     q_tiles, counters + 1);
+    const long long q_tiles = c.slots * c.split.parts * L.key_heads;
+    e = launch_after(dq, dim3(grid(q_tiles)), kThreads, smem, stream, L, M, rows_per_tile, out_rows, stats, partials, q_tiles,
+                     c.split, counters + 1);
     if (e != cudaSuccess) return e;
     if (partials) {
         const long long all = static_cast<long long>(L.query_rows) * L.query_heads * L.head_dim;
-        dq_sum_kernel<T><<<static_cast<unsigned>((all / 8 + 255) / 256), 256, 0, stream>>>(L, partials);
+        dq_sum_kernel<T><<<static_cast<unsigned>((all + kSumElems - 1) / kSumElems), 256, 0, stream>>>(L, c.sums, partials);
     }
     return cudaGetLastError();
 }
@@ -806,8 +836,9 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
 }  // namespace
 
 size_t backward_tiles_workspace(const AttentionLaunch &L) {
-    const size_t partials = L.q_off ? 0
-                                    : static_cast<size_t>(L.items) * L.query_rows * L.query_heads * L.head_dim * sizeof(float);
+    const Cut c = cut_of(L);
+    const size_t rows = L.q_off && c.sums == 1 ? 0 : static_cast<size_t>(c.sums) * L.query_rows;
+    const size_t partials = rows * L.query_heads * L.head_dim * sizeof(float);
     return kCounterBytes + stats_bytes(L) + align256(partials);
 }
 

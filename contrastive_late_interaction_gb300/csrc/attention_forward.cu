@@ -50,7 +50,7 @@ namespace {
 constexpr int kPairs = 4;
 
 struct Pair {
-    int q0, o0, rows, k0, nk, head;   // rows < 0: no more work
+    int q0, o0, rows, k0, nk, head;   // o0: output row, or with parts the partials' row; rows < 0: no more work
 };
 
 // TILES: tiles that a CTA works on at a time.
@@ -74,10 +74,12 @@ struct Maps {
     CUtensorMap q, k, v;
 };
 
-template <typename T, int BOXES, int TILES>
+// CUT: items are cut along their states, and the sums joined afterwards (as a
+// branch in the one kernel this cost whole items 2%).
+template <typename T, int BOXES, int TILES, bool CUT>
 __global__ void __launch_bounds__(128 + 128 * TILES, 3 - TILES)
     forward_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
-                   long long slots, long long tiles, unsigned long long *counter) {
+                   long long tiles, unsigned long long *counter, Split cut, int out_rows, float *part_o, float2 *part_ml) {
     extern __shared__ uint8_t smem_raw[];
     using Smem = Storage<BOXES, TILES>;
     constexpr int kStages = Smem::kStages, kThreads = 128 + 128 * TILES;
@@ -294,11 +296,21 @@ __global__ void __launch_bounds__(128 + 128 * TILES, 3 - TILES)
             const long long id = static_cast<long long>(base) + lane;
             Item t;
             int r0 = 0;
-            const bool on = lane < batch && id < tiles &&
-                            find_block(L, L.q_off, span, per_item, false, id / L.key_heads, t, r0);
+            long long block = id / L.key_heads;
+            const int head = static_cast<int>(id - block * L.key_heads);
+            int part = 0;
+            if constexpr (CUT) {
+                const long long whole = block / cut.parts;
+                part = static_cast<int>(block - whole * cut.parts);
+                block = whole;
+            }
+            const bool on = lane < batch && id < tiles && find_block(L, L.q_off, span, per_item, false, block, t, r0);
+            if constexpr (CUT) {
+                if (on) part_of(cut, part, t);
+            }
             for (uint32_t left = __ballot_sync(0xffffffffu, on); left && ok; left &= left - 1) {
                 const int from = __ffs(left) - 1;
-                Pair p = {t.q0 + r0, t.o0 + r0, min(span, t.nq - r0), t.k0, t.nk, static_cast<int>(id % L.key_heads)};
+                Pair p = {t.q0 + r0, part * out_rows + t.o0 + r0, min(span, t.nq - r0), t.k0, t.nk, head};
                 p.q0 = __shfl_sync(0xffffffffu, p.q0, from);
                 p.o0 = __shfl_sync(0xffffffffu, p.o0, from);
                 p.rows = __shfl_sync(0xffffffffu, p.rows, from);
@@ -421,12 +433,18 @@ __global__ void __launch_bounds__(128 + 128 * TILES, 3 - TILES)
             }
             const int row = t * rows_per_tile + r_in, head = p.head * group + head_in;
             const bool mine = in_tile && row < p.rows;
-            T *out = static_cast<T *>(L.o.data) + (static_cast<long long>(p.o0) + row) * L.o.row + head * L.o.head;
             __syncwarp();
-            store_sums<T>(o_at, dim, 1.0f / l, blocks != 0, l == 0.0f, mine, out);   // no kept state: zero
-            if (L.lse && mine)
-                L.lse[(static_cast<long long>(p.o0) + row) * L.query_heads + head] =
-                    l == 0.0f ? -INFINITY : m * (sl2 * kLn2) + logf(l);
+            if constexpr (CUT) {   // the sums as they are, and what they are relative to
+                const long long cell = (static_cast<long long>(p.o0) + row) * L.query_heads + head;
+                store_partials(o_at, dim, blocks != 0, mine, part_o + cell * dim);
+                if (mine) part_ml[cell] = make_float2(m * sl2, l);
+            } else {
+                T *out = static_cast<T *>(L.o.data) + (static_cast<long long>(p.o0) + row) * L.o.row + head * L.o.head;
+                store_sums<T>(o_at, dim, 1.0f / l, blocks != 0, l == 0.0f, mine, out);   // no kept state: zero
+                if (L.lse && mine)
+                    L.lse[(static_cast<long long>(p.o0) + row) * L.query_heads + head] =
+                        l == 0.0f ? -INFINITY : m * (sl2 * kLn2) + logf(l);
+            }
             tc_fence_before();
         }
     }
@@ -435,29 +453,47 @@ __global__ void __launch_bounds__(128 + 128 * TILES, 3 - TILES)
     if (warp == 1) tmem_dealloc(tmem, kColumns);
 }
 
-template <typename T, int BOXES, int TILES>
-cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
-    const int rows_per_tile = 128 / L.group;
-    const long long span = TILES * rows_per_tile;
-    const long long slots = L.q_off ? L.query_rows / span + L.items
-                                    : static_cast<long long>(L.items) * ((L.query_rows + span - 1) / span);
-    const long long tiles = slots * L.key_heads;
-    Maps M;
-    const bool bf16 = Type<T>::bf16;
-    if (!encode_heads_tiles(&M.q, L.q, bf16, L.head_dim, L.query_heads, L.query_rows, L.group, rows_per_tile) ||
-        !encode_heads_tiles(&M.k, L.k, bf16, L.head_dim, L.key_heads, L.key_rows, 1, kTileRows) ||
-        !encode_heads_tiles(&M.v, L.v, bf16, L.head_dim, L.key_heads, L.key_rows, 1, kTileRows))
-        return cudaErrorInvalidValue;
-    const size_t smem = sizeof(Storage<BOXES, TILES>) + 1024;
-    auto kernel = forward_kernel<T, BOXES, TILES>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    const long long ctas = static_cast<long long>(L.sm_count) * (3 - TILES);
-    unsigned long long *counters = reinterpret_cast<unsigned long long *>(L.workspace);
-    begin_kernel<<<1, 32, 0, stream>>>(L.status, counters);
-    return launch_after(kernel, dim3(static_cast<unsigned>(tiles < ctas ? tiles : ctas)), 128 + 128 * TILES, smem, stream, L, M,
-                        rows_per_tile, slots, tiles, counters);
+// Joins the parts of each row in their order: a warp a row and head.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    join_parts_kernel(const __grid_constant__ AttentionLaunch L, int parts, int out_rows, const float *part_o, const float2 *part_ml) {
+    after_previous();
+    const long long cells = static_cast<long long>(out_rows) * L.query_heads;
+    const long long cell = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, dim = L.head_dim, d = 4 * lane;
+    if (cell >= cells) return;
+    const float2 mine = lane < parts ? part_ml[lane * cells + cell] : make_float2(-INFINITY, 0.0f);
+    float m = mine.x;
+    for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+    const float c = lane < parts ? ex2(mine.x - (m == -INFINITY ? 0.0f : m)) : 0.0f;
+    float l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+        const float cp = __shfl_sync(0xffffffffu, c, p), lp = __shfl_sync(0xffffffffu, mine.y, p);
+        l = fmaf(lp, cp, l);
+        if (d < dim) {
+            const float4 v = *reinterpret_cast<const float4 *>(part_o + (p * cells + cell) * dim + d);
+            o.x = fmaf(v.x, cp, o.x), o.y = fmaf(v.y, cp, o.y), o.z = fmaf(v.z, cp, o.z), o.w = fmaf(v.w, cp, o.w);
+        }
+    }
+    const long long row = cell / L.query_heads;
+    const int head = static_cast<int>(cell - row * L.query_heads);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // no kept state: zero
+    if (d < dim)
+        *reinterpret_cast<uint2 *>(static_cast<T *>(L.o.data) + row * L.o.row + head * L.o.head + d) =
+            make_uint2(Type<T>::pack(o.x * inv, o.y * inv), Type<T>::pack(o.z * inv, o.w * inv));
+    if (L.lse && lane == 0) L.lse[cell] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
+
+int output_rows(const AttentionLaunch &L) { return L.query_rows * (L.q_off ? 1 : L.items); }
+
+// How a call is cut: tiles a CTA, slots of blocks of queries, parts along the states.
+struct Cut {
+    int tiles;
+    long long slots;
+    Split split;
+};
 
 // Two tiles a CTA share K and V, which is what long queries need (2048 x 1024
 // rows, 16 heads of 128: 431 us against 521 with one tile a CTA, two CTAs an
@@ -466,16 +502,70 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
 // heads of 64: 90 us against 117; at heads of 128 the short ring loses what
 // the second CTA gains), and calls with less than a pair for every other SM
 // (2048 x 2048 rows, 2 heads: 35 us against 38).
+Cut cut_of(const AttentionLaunch &L) {
+    const bool one = static_cast<long long>(L.max_q) * L.group <= 128 && L.head_dim <= 64;
+    const bool small = (static_cast<long long>(output_rows(L)) * L.group / 256 + 1) * L.key_heads <= 76;
+    Cut c;
+    c.tiles = one || small ? 1 : 2;
+    const long long span = c.tiles * (128 / L.group);
+    c.slots = L.q_off ? L.query_rows / span + L.items : static_cast<long long>(L.items) * ((L.query_rows + span - 1) / span);
+    // at least so many blocks are there: half of the slots may be empty
+    const long long filled = (output_rows(L) + span - 1) / span;
+    c.split = split_of(L, (filled > L.items ? filled : L.items) * L.key_heads, 152 * (3 - c.tiles), 512);
+    return c;
+}
+
+size_t part_bytes(const AttentionLaunch &L, const Cut &c) {
+    return align256(static_cast<size_t>(c.split.parts) * output_rows(L) * L.query_heads * L.head_dim * sizeof(float));
+}
+
+template <typename T, int BOXES, int TILES, bool CUT>
+cudaError_t launch(const AttentionLaunch &L, const Cut &c, cudaStream_t stream) {
+    const int rows_per_tile = 128 / L.group, out_rows = output_rows(L);
+    const long long tiles = c.slots * c.split.parts * L.key_heads;
+    Maps M;
+    const bool bf16 = Type<T>::bf16;
+    if (!encode_heads_tiles(&M.q, L.q, bf16, L.head_dim, L.query_heads, L.query_rows, L.group, rows_per_tile) ||
+        !encode_heads_tiles(&M.k, L.k, bf16, L.head_dim, L.key_heads, L.key_rows, 1, kTileRows) ||
+        !encode_heads_tiles(&M.v, L.v, bf16, L.head_dim, L.key_heads, L.key_rows, 1, kTileRows))
+        return cudaErrorInvalidValue;
+    const size_t smem = sizeof(Storage<BOXES, TILES>) + 1024;
+    auto kernel = forward_kernel<T, BOXES, TILES, CUT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const long long ctas = static_cast<long long>(L.sm_count) * (3 - TILES);
+    unsigned long long *counters = reinterpret_cast<unsigned long long *>(L.workspace);
+    float *part_o = reinterpret_cast<float *>(L.workspace + kCounterBytes);
+    float2 *part_ml = reinterpret_cast<float2 *>(L.workspace + kCounterBytes + part_bytes(L, c));
+    begin_kernel<<<1, 32, 0, stream>>>(L.status, counters);
+    e = launch_after(kernel, dim3(static_cast<unsigned>(tiles < ctas ? tiles : ctas)), 128 + 128 * TILES, smem, stream, L, M,
+                     rows_per_tile, tiles, counters, c.split, out_rows, part_o, part_ml);
+    if (e != cudaSuccess || !CUT) return e;
+    const long long cells = static_cast<long long>(out_rows) * L.query_heads;
+    return launch_after(join_parts_kernel<T>, dim3(static_cast<unsigned>((cells + 7) / 8)), 256, 0, stream, L, c.split.parts,
+                        out_rows, part_o, part_ml);
+}
+
+template <typename T, int BOXES, int TILES>
+cudaError_t launch(const AttentionLaunch &L, const Cut &c, cudaStream_t stream) {
+    return c.split.parts > 1 ? launch<T, BOXES, TILES, true>(L, c, stream) : launch<T, BOXES, TILES, false>(L, c, stream);
+}
+
 template <typename T>
 cudaError_t dispatch(const AttentionLaunch &L, cudaStream_t stream) {
-    const bool one = static_cast<long long>(L.max_q) * L.group <= 128;
-    const long long rows = static_cast<long long>(L.query_rows) * (L.q_off ? 1 : L.items);
-    const bool small = (rows * L.group / 256 + 1) * L.key_heads <= L.sm_count / 2;
-    if (L.head_dim > 64) return small ? launch<T, 2, 1>(L, stream) : launch<T, 2, 2>(L, stream);
-    return one || small ? launch<T, 1, 1>(L, stream) : launch<T, 1, 2>(L, stream);
+    const Cut c = cut_of(L);
+    if (L.head_dim > 64) return c.tiles == 1 ? launch<T, 2, 1>(L, c, stream) : launch<T, 2, 2>(L, c, stream);
+    return c.tiles == 1 ? launch<T, 1, 1>(L, c, stream) : launch<T, 1, 2>(L, c, stream);
 }
 
 }  // namespace
+
+size_t forward_tiles_workspace(const AttentionLaunch &L) {
+    const Cut c = cut_of(L);
+    if (c.split.parts == 1) return kCounterBytes;
+    return kCounterBytes + part_bytes(L, c) +
+           align256(static_cast<size_t>(c.split.parts) * output_rows(L) * L.query_heads * sizeof(float2));
+}
 
 // Needs at least one query row and one state (the tensor maps have no empty form).
 cudaError_t launch_forward_tiles(const AttentionLaunch &L, cudaStream_t stream) {

@@ -333,9 +333,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
         }
 }
 
-// Joins the parts of each row, four elements a lane.  W warps a row: one where
-// items have a few parts, eight where they have many (one item of 4096 states
-// in chunks of 32: 128 parts took one warp 30 us).
+// Joins the parts of each row, four elements a lane, by W warps a row.
 template <typename T, int W>
 __global__ void __launch_bounds__(256)
     join_kernel(const __grid_constant__ AttentionLaunch L, int chunk, const float *part_o, const float2 *part_ml) {
@@ -614,25 +612,20 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
     if (!L.q_off) write(worker, L.query_rows * L.group);
 }
 
-// dQ: the sum of a row's parts in their order, times the scale.  Shared
-// queries sum over all workers: a block of 8 warps takes 32 elements x 4.
-template <typename T>
+// dQ: the sum of a row's parts in a fixed order, times the scale; of shared
+// queries the sum over all workers.  W warps a row, four elements a lane.
+template <typename T, int W>
 __global__ void __launch_bounds__(256)
     dq_join_kernel(const __grid_constant__ AttentionLaunch L, int chunk, long long workers, const float *part_dq) {
+    after_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long most = static_cast<long long>(L.max_q) * L.group;
     const int dim = L.head_dim, d = 4 * lane;
-    __shared__ float4 sums[8][32];
     Unit u;
-    long long id, first, parts;
-    int i = 0;
-    if (L.q_off) {   // a warp a row
-        id = static_cast<long long>(blockIdx.x) * 8 + warp;
-        if (id >= static_cast<long long>(L.items) * L.key_heads * most) return;
-        i = static_cast<int>(id / (most * L.key_heads));
-    } else {         // a block a row
-        id = blockIdx.x;
-    }
+    long long first, parts;
+    const long long id = W == 8 ? blockIdx.x : static_cast<long long>(blockIdx.x) * 8 + warp;
+    if (id >= (L.q_off ? static_cast<long long>(L.items) : 1) * L.key_heads * most) return;
+    const int i = static_cast<int>(id / (most * L.key_heads));
     const int row = static_cast<int>(id % most), head = static_cast<int>(id / most % L.key_heads);
     u.head = head;
     if (L.q_off) {
@@ -650,12 +643,13 @@ __global__ void __launch_bounds__(256)
         const float *src = part_dq + ((first * L.key_heads + head) * most + row) * dim + d;
         const long long step = L.key_heads * most * dim;
 #pragma unroll 4
-        for (long long p = L.q_off ? 0 : warp; p < parts; p += L.q_off ? 1 : 8) {
+        for (long long p = W == 8 ? warp : 0; p < parts; p += W) {
             const float4 v = *reinterpret_cast<const float4 *>(src + p * step);
             s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
         }
     }
-    if (!L.q_off) {
+    if constexpr (W == 8) {
+        __shared__ float4 sums[8][32];
         sums[warp][lane] = s;
         __syncthreads();
         if (warp != 0) return;
@@ -713,6 +707,13 @@ Cut cut_of(const AttentionLaunch &L) {
     return c;
 }
 
+// Eight warps a row join many parts of few rows sooner (1 x 8192 states, 8 heads
+// of 64: the backward 17 us against 60), one warp a row the parts of many (64 x
+// 4096, 16 rows: 244 us against 260).
+bool wide_join(const AttentionLaunch &L, const Cut &c, long long rows) {
+    return L.max_k > 8 * static_cast<long long>(c.chunk) && rows <= 152 * 8;
+}
+
 size_t part_bytes(const AttentionLaunch &L, long long slots, const Cut &c) {
     return align256(static_cast<size_t>(slots) * L.key_heads * c.rows * L.head_dim * sizeof(float));
 }
@@ -728,7 +729,7 @@ cudaError_t forward(const AttentionLaunch &L, cudaStream_t stream) {
     forward_kernel<T, DP, NT><<<blocks_of(c.slots * L.key_heads, kWarps), kWarps * 32, 0, stream>>>(L, c.chunk, c.slots, part_o, part_ml);
     if (!split) return cudaGetLastError();
     const long long rows = L.items * L.key_heads * c.rows;
-    if (L.max_k > 8 * c.chunk)
+    if (wide_join(L, c, rows))
         return launch_after(join_kernel<T, 8>, dim3(static_cast<unsigned>(rows)), 256, 0, stream, L, c.chunk, part_o, part_ml);
     return launch_after(join_kernel<T, 1>, dim3(blocks_of(rows, 8)), 256, 0, stream, L, c.chunk, part_o, part_ml);
 }
@@ -739,8 +740,9 @@ cudaError_t backward(const AttentionLaunch &L, cudaStream_t stream) {
     float *part_dq = reinterpret_cast<float *>(L.workspace);
     backward_kernel<T, DP, NT><<<blocks_of(c.workers * L.key_heads, kWarps / NT), kWarps / NT * 32, 0, stream>>>(L, c.chunk, c.slots, c.workers, part_dq);
     const long long rows = L.q_off ? L.items * L.key_heads * c.rows : L.key_heads * c.rows;
-    dq_join_kernel<T><<<blocks_of(rows, L.q_off ? 8 : 1), 256, 0, stream>>>(L, c.chunk, c.workers, part_dq);
-    return cudaGetLastError();
+    if (!L.q_off || wide_join(L, c, rows))
+        return launch_after(dq_join_kernel<T, 8>, dim3(static_cast<unsigned>(rows)), 256, 0, stream, L, c.chunk, c.workers, part_dq);
+    return launch_after(dq_join_kernel<T, 1>, dim3(blocks_of(rows, 8)), 256, 0, stream, L, c.chunk, c.workers, part_dq);
 }
 
 template <typename T>
@@ -754,8 +756,16 @@ cudaError_t dispatch(const AttentionLaunch &L, bool back, cudaStream_t stream) {
     return two ? forward<T, 64, 2>(L, stream) : forward<T, 64, 1>(L, stream);
 }
 
-// Few rows: an item's packed rows fill at most two tiles of 8.
-bool few_rows(const AttentionLaunch &L) { return static_cast<long long>(L.max_q) * L.group <= 16; }
+// Few rows: an item's packed rows fill at most two tiles of 8.  With two of them
+// the forward's tensor cores are ahead from some states on (16 rows, 8 heads of
+// 128: 1 x 4096 states 13.8 us here and 16.3 there, 1 x 8192 27 and 18; 32 x
+// 256 of 64: 16.6 and 11.6; 32 x 2048: 60 and 34; 512 x 32 to 1024 shared, 16
+// heads of 64: 301 and 290; with 9 rows, 260).  The backward is ahead here (the
+// last: 624 us and 875; 32 x 2048, 8 heads of 64: 83 and 125).
+bool few_rows(const AttentionLaunch &L, bool back) {
+    const long long rows = static_cast<long long>(L.max_q) * L.group;
+    return rows <= 8 || (rows <= 16 && (back || static_cast<long long>(L.key_rows) * L.key_heads <= 32768));
+}
 
 }  // namespace
 }  // namespace attn
@@ -763,7 +773,7 @@ bool few_rows(const AttentionLaunch &L) { return static_cast<long long>(L.max_q)
 size_t attention_workspace(const AttentionLaunch &L) {
     using namespace attn;
     if (!L.query_rows || !L.key_rows) return 0;
-    if (!few_rows(L)) return kCounterBytes;
+    if (!few_rows(L, false)) return forward_tiles_workspace(L);
     const Cut c = cut_of(L);
     if (c.chunk >= L.max_k) return 0;
     return part_bytes(L, c.slots, c) + align256(static_cast<size_t>(c.slots) * L.key_heads * c.rows * sizeof(float2));
@@ -772,14 +782,14 @@ size_t attention_workspace(const AttentionLaunch &L) {
 size_t attention_backward_workspace(const AttentionLaunch &L) {
     using namespace attn;
     if (!L.query_rows || !L.key_rows) return 0;
-    if (!few_rows(L)) return backward_tiles_workspace(L);
+    if (!few_rows(L, true)) return backward_tiles_workspace(L);
     const Cut c = cut_of(L);
     return part_bytes(L, c.workers, c);
 }
 
 cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t stream) {
     using namespace attn;
-    if (L.query_rows && L.key_rows && !few_rows(L)) return launch_forward_tiles(L, stream);
+    if (L.query_rows && L.key_rows && !few_rows(L, false)) return launch_forward_tiles(L, stream);
     const bool none = !L.query_rows || !L.key_rows;
     if (none || L.items > kFewItems) {
         const cudaError_t e = cudaMemsetAsync(L.status, 0, sizeof(int32_t), stream);
@@ -795,7 +805,7 @@ cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t stream) {
 
 cudaError_t launch_attention_backward(const AttentionLaunch &L, cudaStream_t stream) {
     using namespace attn;
-    if (L.query_rows && L.key_rows && !few_rows(L)) return launch_backward_tiles(L, stream);
+    if (L.query_rows && L.key_rows && !few_rows(L, true)) return launch_backward_tiles(L, stream);
     const bool none = !L.query_rows || !L.key_rows;
     if (none || L.items > kFewItems) {
         const cudaError_t e = cudaMemsetAsync(L.status, 0, sizeof(int32_t), stream);

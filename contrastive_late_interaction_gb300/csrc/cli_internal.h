@@ -247,6 +247,7 @@ size_t attention_workspace(const AttentionLaunch &L);
 size_t attention_backward_workspace(const AttentionLaunch &L);
 namespace attn {
 cudaError_t launch_forward_tiles(const AttentionLaunch &L, cudaStream_t stream);
+size_t forward_tiles_workspace(const AttentionLaunch &L);
 cudaError_t launch_backward_tiles(const AttentionLaunch &L, cudaStream_t stream);
 size_t backward_tiles_workspace(const AttentionLaunch &L);
 }

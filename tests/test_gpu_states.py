@@ -280,6 +280,15 @@ def test_attention_and_its_gradient(cli, case, mask, dtype):
     check(*attend(cli, q_len, k_len, hq, hk, d, dtype, 100 + case, mask, shared=isinstance(q_len, int)))
 
 
+@pytest.mark.parametrize("mask", [None, 0.3])
+@pytest.mark.parametrize("q_len, k_len, h, d", [
+    ([200], [9000], 2, 128), ([40, 3, 0, 17], [5000, 700, 6000, 0], 3, 72), (20, [4000, 100, 1537], 2, 64),
+    ([130], [512 * 5 + 1], 1, 8), ([16] * 40, [70, 130] * 20, 4, 128), (10, [33, 0, 257] * 60, 1, 96),
+])
+def test_attention_cut_along_the_states_or_into_many_items(cli, q_len, k_len, h, d, mask):
+    check(*attend(cli, q_len, k_len, h, h, d, BF16, 310, mask, shared=isinstance(q_len, int)))
+
+
 @pytest.mark.parametrize("layout", ["padded", "heads_first", "packed_kv"])
 @pytest.mark.parametrize("case", [3, 11, 13, 20, 22])
 def test_attention_layouts(cli, case, layout):
