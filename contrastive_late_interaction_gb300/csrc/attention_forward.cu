@@ -33,6 +33,13 @@
 //          over the same columns, and at the end O / l to global memory.
 // TMEM: S0 | S1 | O0 | O1, 128 columns each.
 //
+// Where the blocks of queries do not fill the SMs, items are also cut along their
+// states, and join_parts_kernel adds the parts: 1 x 64 x 8192 rows, 8 heads of
+// 128, take 18 us instead of 97.
+//
+// P is rounded to 16 bits because the product takes it so; l sums the weights
+// before that.
+//
 // Bound: 8 items of 2048 x 4096 rows, 16 heads of 128, run at 1400 TFLOP/s (75%
 // of measured), where the two tiles' softmax (about 1700 cycles a block of each,
 // half of it exponentials) and products (2100 for both) take turns; 2048 x
@@ -495,15 +502,16 @@ struct Cut {
     Split split;
 };
 
-// Two tiles a CTA share K and V, which is what long queries need (2048 x 1024
-// rows, 16 heads of 128: 431 us against 521 with one tile a CTA, two CTAs an
-// SM).  One tile a CTA serves calls whose items fill no second one, with
-// narrow heads, for which two CTAs of the full ring fit an SM (64 x 256 rows, 8
-// heads of 64: 90 us against 117; at heads of 128 the short ring loses what
-// the second CTA gains), and calls with less than a pair for every other SM
-// (2048 x 2048 rows, 2 heads: 35 us against 38).
+// Two tiles a CTA share K and V, which is what long queries need (32 x 2048 x
+// 1024 rows, 16 heads of 128: 431 us against 521 with one tile a CTA, two CTAs
+// an SM; 64 x 512 x 1024, 8 heads of 64: 99 against 106).  One tile a CTA serves
+// narrow heads, for which two CTAs of the full ring fit an SM, in items of two
+// tiles or less (64 x 200 x 1024, 8 heads of 64: 72 us against 80; 64 x 256: 78
+// against 81; at heads of 128 the short ring loses what the second CTA gains),
+// and calls with less than a pair for every other SM (1 x 2048 x 2048 rows, 2
+// heads: 35 us against 38, whole).
 Cut cut_of(const AttentionLaunch &L) {
-    const bool one = static_cast<long long>(L.max_q) * L.group <= 128 && L.head_dim <= 64;
+    const bool one = static_cast<long long>(L.max_q) * L.group <= 256 && L.head_dim <= 64;
     const bool small = (static_cast<long long>(output_rows(L)) * L.group / 256 + 1) * L.key_heads <= 76;
     Cut c;
     c.tiles = one || small ? 1 : 2;

@@ -1,8 +1,8 @@
 /*
  * cli.h -- in-batch contrastive scoring on one GB300 (sm_103a): a stateless C ABI.
  *
- * Two operations of a multi-modal byte-encoder trainer's contrastive step, as
- * the UForm 4 documentation pages describe them:
+ * Operations of a multi-modal byte-encoder trainer's contrastive step, as the
+ * UForm 4 documentation pages describe them:
  *
  *   1. the pooled pair loss in SigLIP's `sigmoid` form over N pooled
  *      embeddings, with a learnable inverse temperature t and bias b and
@@ -13,7 +13,9 @@
  *   2. ColBERT-style hard MaxSim between query and document token vectors held
  *      in Arrow-style ragged tapes, with a backward pass routed through the
  *      argmax ("UForm", section "ColBERT-Style Late-Interaction Rerankers";
- *      "Arenas", section "Rows and Tapes").
+ *      "Arenas", section "Rows and Tapes");
+ *   3. what makes those vectors from a tower's token states: rotary positions,
+ *      head norms and cross attention over tapes, with their gradients.
  *
  * Conventions, after the pages' C API ("Arenas"; "Training"):
  *   - Callers lend memory and never a way to allocate it: every input, output
@@ -487,8 +489,9 @@ typedef struct {
  *   CLI_ROTARY_YARN     pairs that turn more than 32 times over
  *                       `trained_positions` keep f_i, those that turn less
  *                       than once take f_i / factor, those between them a
- *                       blend linear in i; amplitude 0.1 ln(factor) + 1
- *                       (Peng, Quesnelle, Fan, Shippole 2023)
+ *                       blend linear in i between the first pair, rounded
+ *                       down, and the last, rounded up; amplitude
+ *                       0.1 ln(factor) + 1 (Peng, Quesnelle, Fan, Shippole 2023)
  *
  *   positions      rows of the table, 1 .. 2^31 - 1
  *   rotary_dim     even, 2 .. 256
@@ -528,7 +531,8 @@ cli_status_t rotary_table(const cli_rotary_table_t *args);
  *   head_dim        a multiple of 8, 8 .. 256
  *   rotary_dim      even, 2 .. head_dim
  *   table           device fp32 [table_rows][rotary_dim / 2][2] from
- *                   rotary_table, 8-byte aligned
+ *                   rotary_table, 8-byte aligned (16-byte aligned ones are
+ *                   read faster)
  *   epsilon         > 0 (the norm verbs)
  *   rows, heads     of a part; rows < 2^31 (0 is a call on no rows), heads at most 65535
  *   positions       device int32 [rows], row r's position; NULL: r itself.  One
@@ -615,9 +619,9 @@ size_t norm_rotary_heads_backward_workspace_bytes(size_t head_dim);
  *                    contents on entry are ignored; may be NULL where that is 0
  *   device_status    device int32 (written: 0 or a cli_status_t)
  *
- * P and dS are rounded to `dtype` as operands of the tensor cores; everything
- * else between input and output is in 32 bits.  Results are bit-reproducible:
- * no sum depends on the order in which blocks run.
+ * P and dS enter the products as `dtype`, or as the sum of two such where an
+ * item has few rows; everything else between input and output is in 32 bits.
+ * Results are bit-reproducible: no sum depends on the order in which blocks run.
  */
 typedef struct {
     int dtype;
