@@ -625,11 +625,13 @@ def _fast(name):
 _PART = "17Q"       # rows, heads, positions, x, y, d_y, d_x, gain, d_gain
 _pack_rotary = struct.Struct("@2i4Qf4x" + _PART + _PART + "4Q")
 _pack_attention = struct.Struct("@i4x10Qf4x" + "Q12QQ12Q" + "4Q")
+_pack_last = struct.Struct("@4Q")   # workspace, workspace_bytes, device_status, stream
+_ATTENTION_LAST = _pack_attention.size - _pack_last.size
 assert _pack_rotary.size == ctypes.sizeof(RotaryArgs) and _pack_attention.size == ctypes.sizeof(AttentionArgs)
 _ROTARY = {v: _fast(v) for v in ("rotary_heads", "rotary_heads_backward", "norm_rotary_heads",
                                  "norm_rotary_heads_backward")}
 _ATTENTION = {v: (_fast(v), _fast(v + "_workspace_bytes")) for v in ("cross_attention", "cross_attention_backward")}
-_NO_HEADS = (0, 0, 0)
+_NO_GRADIENTS = (0,) * 12   # d_output, d_q, d_k, d_v
 
 
 def _raw_stream(stream, tensor):
@@ -674,21 +676,13 @@ def _states(t, name):
     return t.shape
 
 
-def _out(out, name, like):
-    """The caller's output `name`, or a new packed one of the shape of `like`."""
-    t = out.get(name) if out else None
-    if t is not None:
-        return t
-    return torch.empty_like(like) if like.is_contiguous() else torch.empty(like.shape, dtype=like.dtype,
-                                                                           device=like.device)
-
-
 def _result(out, name, like, shape):
-    """(tensor, its words in the struct): as `_out`; one made here needs no checks."""
+    """The caller's output `name`, or a new packed one of `shape`, and its words in the struct: one made here needs no
+    checks."""
     t = out.get(name) if out else None
     if t is not None:
         return t, _heads(t, "out " + name, shape, like.dtype)
-    if like.is_contiguous():
+    if shape == like.shape and like.is_contiguous():
         t = torch.empty_like(like)
     else:
         t = torch.empty(shape, dtype=like.dtype, device=like.device)
@@ -830,7 +824,9 @@ def _norm_grad_part(out, name, x, d_y, positions, gain, dim, dtype):
         d_gain = out.get(f"d_{name}_gain") if out else None
         if d_gain is None:
             d_gain = torch.empty_like(gain)
-        dg = _vector(d_gain, f"d_{name}_gain", dim, torch.float32)
+            dg = d_gain.data_ptr()
+        else:
+            dg = _vector(d_gain, f"d_{name}_gain", dim, torch.float32)
     return dx, (shape[0], shape[1], pos, *given, 0, 0, 0, *dy, *made, g, dg), d_gain
 
 
@@ -860,12 +856,15 @@ def _attention_sizes(q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_r
 
 def _attention_call(verb, head, tail, workspace, like, status, stream):
     call, workspace_bytes = _ATTENTION[verb]
-    stream = _raw_stream(stream, like)
-    if workspace is None:
-        need = workspace_bytes(_pack_attention.pack(*head, *tail, 0, 0, 0, 0))
-        workspace = _ws(need, like.device) if need else None
     ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    rc = call(_pack_attention.pack(*head, *tail, ws, ws_bytes, status.data_ptr(), stream))
+    last = status.data_ptr(), _raw_stream(stream, like)
+    args = _pack_attention.pack(*head, *tail, ws, ws_bytes, *last)
+    if workspace is None:
+        need = workspace_bytes(args)
+        if need:
+            workspace = _ws(need, like.device)
+            args = args[:_ATTENTION_LAST] + _pack_last.pack(workspace.data_ptr(), need, *last)
+    rc = call(args)
     if rc:
         raise_for(rc, verb)
 
@@ -900,18 +899,17 @@ def cross_attention(q, q_offsets, k, v, k_offsets, key_mask=None, scale=None, ma
     head, items = _attention_sizes(q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_rows, max_key_rows)
     rows_q, hq, dim = q.shape
     shape = (rows_q if q_offsets is not None else rows_q * items, hq, dim)
-    o = out.get("output") if out else None
-    if o is None:
-        o = torch.empty(shape, dtype=q.dtype, device=q.device)
+    o, made = _result(out, "output", q, shape)
     lse, lse_ptr = None, 0
     if want_lse:
         lse = out.get("lse") if out else None
         if lse is None:
             lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
-        lse_ptr = _lse_ptr(lse, *shape[:2])
+            lse_ptr = lse.data_ptr()
+        else:
+            lse_ptr = _lse_ptr(lse, *shape[:2])
     st = _status(device_status, q)
-    _attention_call("cross_attention", head, (*_heads(o, "output", shape, q.dtype), lse_ptr, *_NO_HEADS, *_NO_HEADS,
-                                              *_NO_HEADS, *_NO_HEADS), workspace, q, st, stream)
+    _attention_call("cross_attention", head, (*made, lse_ptr, *_NO_GRADIENTS), workspace, q, st, stream)
     return {"output": o, "lse": lse, "device_status": st}
 
 
@@ -923,9 +921,10 @@ def cross_attention_backward(q, q_offsets, k, v, k_offsets, output, lse, d_outpu
     head, items = _attention_sizes(q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_rows, max_key_rows)
     (rows_q, hq, dim), dtype = q.shape, q.dtype
     shape = (rows_q if q_offsets is not None else rows_q * items, hq, dim)
-    dq, dk, dv, st = _out(out, "d_q", q), _out(out, "d_k", k), _out(out, "d_v", v), _status(device_status, q)
+    (dq, q_made), (dk, k_made), (dv, v_made) = (_result(out, n, t, t.shape)
+                                                for n, t in (("d_q", q), ("d_k", k), ("d_v", v)))
+    st = _status(device_status, q)
     tail = (*_heads(output, "output", shape, dtype), _lse_ptr(lse, *shape[:2]),
-            *_heads(d_output, "d_output", shape, dtype), *_heads(dq, "d_q", q.shape, dtype),
-            *_heads(dk, "d_k", k.shape, dtype), *_heads(dv, "d_v", v.shape, dtype))
+            *_heads(d_output, "d_output", shape, dtype), *q_made, *k_made, *v_made)
     _attention_call("cross_attention_backward", head, tail, workspace, q, st, stream)
     return {"d_q": dq, "d_k": dk, "d_v": dv, "device_status": st}
