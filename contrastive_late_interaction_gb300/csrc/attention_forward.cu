@@ -506,12 +506,14 @@ struct Cut {
 // 1024 rows, 16 heads of 128: 431 us against 521 with one tile a CTA, two CTAs
 // an SM; 64 x 512 x 1024, 8 heads of 64: 99 against 106).  One tile a CTA serves
 // narrow heads, for which two CTAs of the full ring fit an SM, in items of two
-// tiles or less (64 x 200 x 1024, 8 heads of 64: 72 us against 80; 64 x 256: 78
-// against 81; at heads of 128 the short ring loses what the second CTA gains),
+// and a half tiles or less on average (64 x 200 x 1024, 8 heads of 64: 72 us
+// against 80; 64 x 300: 88 against 92; 64 of 1 to 512 x 1 to 1024: 62 against
+// 66, of 1 to 700: 73 against 72; at heads of 128 the short ring loses what the
+// second CTA gains: 64 of 1 to 512: 90 against 78),
 // and calls with less than a pair for every other SM (1 x 2048 x 2048 rows, 2
 // heads: 35 us against 38, whole).
 Cut cut_of(const AttentionLaunch &L) {
-    const bool one = static_cast<long long>(L.max_q) * L.group <= 256 && L.head_dim <= 64;
+    const bool one = static_cast<long long>(output_rows(L)) * L.group <= 320ll * L.items && L.head_dim <= 64;
     const bool small = (static_cast<long long>(output_rows(L)) * L.group / 256 + 1) * L.key_heads <= 76;
     Cut c;
     c.tiles = one || small ? 1 : 2;
