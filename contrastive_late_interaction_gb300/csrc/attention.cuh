@@ -91,13 +91,14 @@ __device__ __forceinline__ int find_item(const uint64_t *off, int items, unsigne
 
 // Block `x` of a tape cut into blocks of `span` rows, or of shared queries
 // (off NULL) with `per_item` blocks an item: its item and the row it starts
-// at; false where the slot is empty.
+// at; false where the slot is empty.  `known` is the item where the warp has
+// searched for it, and -1 where it has not.
 __device__ __forceinline__ bool find_block(const AttentionLaunch &L, const uint64_t *off, unsigned span, int per_item,
-                                           bool of_keys, long long x, Item &t, int &r0) {
+                                           bool of_keys, long long x, Item &t, int &r0, int known = -1) {
     int i;
     long long block;
     if (off) {
-        i = find_item(off, L.items, span, x);
+        i = known >= 0 ? known : find_item(off, L.items, span, x);
         block = x - (static_cast<long long>(off[i] / span) + i);
     } else {
         i = static_cast<int>(x / per_item);

@@ -295,12 +295,8 @@ __global__ void __launch_bounds__(128 + 128 * TILES, 3 - TILES)
             ++it;
             return true;
         };
-        while (ok) {
-            unsigned long long base = 0;
-            if (lane == 0) base = atomicAdd(counter, static_cast<unsigned long long>(batch));
-            base = __shfl_sync(0xffffffffu, base, 0);
-            if (base >= static_cast<unsigned long long>(tiles)) break;
-            const long long id = static_cast<long long>(base) + lane;
+        auto hand_out = [&](long long base, int known) {
+            const long long id = base + lane;
             Item t;
             int r0 = 0;
             long long block = id / L.key_heads;
@@ -311,7 +307,7 @@ __global__ void __launch_bounds__(128 + 128 * TILES, 3 - TILES)
                 part = static_cast<int>(block - whole * cut.parts);
                 block = whole;
             }
-            const bool on = lane < batch && id < tiles && find_block(L, L.q_off, span, per_item, false, block, t, r0);
+            const bool on = lane < batch && id < tiles && find_block(L, L.q_off, span, per_item, false, block, t, r0, known);
             if constexpr (CUT) {
                 if (on) part_of(cut, part, t);
             }
@@ -326,6 +322,19 @@ __global__ void __launch_bounds__(128 + 128 * TILES, 3 - TILES)
                 p.head = __shfl_sync(0xffffffffu, p.head, from);
                 ok = publish(p);
             }
+        };
+        auto more = [&]() {
+            unsigned long long base = 0;
+            if (lane == 0) base = atomicAdd(counter, static_cast<unsigned long long>(batch));
+            return static_cast<long long>(__shfl_sync(0xffffffffu, base, 0));
+        };
+        if (batch == 1) {
+            // Few pairs a CTA: the way to its first product counts.  The first is its own, without the counter, and
+            // the warp searches together (512 items of 32 x 512 rows, 4 key heads of 64: 95 -> 83 us).
+            for (long long base = blockIdx.x; ok && base < tiles; base = more() + gridDim.x)
+                hand_out(base, L.q_off ? find_item(L.q_off, L.items, span, base / L.key_heads / (CUT ? cut.parts : 1), lane) : -1);
+        } else {
+            for (long long base = more(); ok && base < tiles; base = more()) hand_out(base, -1);
         }
         if (ok) publish({0, 0, -1, 0, 0, 0});
         check_items(L, static_cast<long long>(blockIdx.x) * 32 + lane, static_cast<long long>(gridDim.x) * 32);
