@@ -29,7 +29,8 @@
 //
 // Bound: HBM.  2048 items of 64 to 512 states, one shared query, 16 heads of
 // 64: 357 us (6.8 TB/s); 512 of 32 to 1024, 8 heads of 128: 185 us (6.1 TB/s)
-// and 407 for the backward (5.4 TB/s, reads and writes mixed).  One row against
+// and 440 for the backward (5.0 TB/s, reads and writes mixed; 17 of it are the
+// joins and mends).  One row against
 // 4096 states, 8 heads on 2: 4.8 us and 4.5 for the join, both latency.
 
 #include "attention.cuh"
@@ -39,6 +40,7 @@ namespace attn {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kMostChunk = 512, kSteps = kMostChunk / 16;   // states of a unit; 16 are taken at a time
 
 template <typename T>
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -406,10 +408,28 @@ __global__ void __launch_bounds__(256)
 // dQ^T += K^T dS^T.  The fragments of Q and dO, as B operands of the first
 // products and transposed as those of the second, stay in shared memory.
 // With shared queries a warp keeps one dQ for all the units it takes.
+//
+// delta is taken from the output, which is rounded.  Where one state has most
+// of a row's weight, its ds = p (dp - delta) is a small difference of large
+// terms, and that rounding shows: an element of dK was off by as much as the
+// root mean square of all of dK.  So the sums of ds are kept too: over a whole
+// row sum p (dp - delta) is 0, and what it is instead is delta's error.  States
+// with a weight of kLarge or more in some row (at most 1 / kLarge a row) are
+// noted, and mend() computes their dK again with the right delta.
+constexpr float kLarge = 1.0f / 16;
+
+// What the backward leaves for mend(): of each unit, the sums of ds of its
+// rows, the steps of 16 states with noted ones, and which they are: bit 4 g of
+// a step's word is state g, bit 4 g + 1 state g + 8.
+struct Notes {
+    float *sums;
+    uint32_t *steps, *states;
+};
+
 template <typename T, int DP, int NT>
 __global__ void __launch_bounds__(kWarps / NT * 32, 3)
     backward_kernel(const __grid_constant__ AttentionLaunch L, int chunk, long long slots, long long stride,
-                    float *part_dq) {
+                    float *part_dq, Notes notes) {
     constexpr int KC = DP / 32, KG = 128 / DP;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     // [warp][Q, dO, Q^T, dO^T][tile][chunk][lane]
@@ -453,7 +473,9 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
     clear();
     for (long long slot = worker; slot < slots; slot += stride) {
         const Unit u = find_unit(L, chunk, slot, head, lane);
+        const long long unit = slot * L.key_heads + head;
         if (u.rows == 0) {
+            if (lane == 0) notes.steps[unit] = 0;
             // an item without queries still has gradients to write, of zero
             if (u.item.ok && u.n > 0) {
                 for (int s = g; s < u.n; s += 8)
@@ -506,6 +528,8 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
             }
         }
         __syncwarp();
+        uint32_t noted = 0;
+        float ds_sum[NT][2] = {};
         const T *kbase = static_cast<const T *>(L.k.data) + head * L.k.head + 8 * t;
         const T *vbase = static_cast<const T *>(L.v.data) + head * L.v.head + 8 * t;
         T *dkbase = static_cast<T *>(L.d_k.data) + head * L.d_k.head + 8 * t;
@@ -533,6 +557,7 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
                 auto &kr = kr0[x];
                 auto &vr = vr0[x];
                 uint32_t p[NT][4], ds[NT][4];   // of states g and g + 8: high halves, then low ones
+                bool large0 = false, large1 = false;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -551,10 +576,21 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
                         pe[i] = on ? ex2_full(fmaf(s4[i], sl2, -lse[n][i & 1])) : 0.0f;
                         de[i] = on ? pe[i] * (d4[i] - delta[n][i & 1]) : 0.0f;
                     }
+                    ds_sum[n][0] += de[0] + de[2];
+                    ds_sum[n][1] += de[1] + de[3];
+                    large0 |= fmaxf(pe[0], pe[1]) >= kLarge;
+                    large1 |= fmaxf(pe[2], pe[3]) >= kLarge;
                     split_pair<T>(pe[0], pe[1], p[n][0], p[n][2]);
                     split_pair<T>(pe[2], pe[3], p[n][1], p[n][3]);
                     split_pair<T>(de[0], de[1], ds[n][0], ds[n][2]);
                     split_pair<T>(de[2], de[3], ds[n][1], ds[n][3]);
+                }
+                if (__any_sync(0xffffffffu, large0 || large1)) {   // fold the four lanes of a state
+                    uint32_t m0 = __ballot_sync(0xffffffffu, large0), m1 = __ballot_sync(0xffffffffu, large1);
+                    m0 |= m0 >> 1, m1 |= m1 >> 1;
+                    m0 |= m0 >> 2, m1 |= m1 >> 2;
+                    if (lane == 0) notes.states[unit * kSteps + (j >> 4)] = (m0 & 0x11111111u) | (m1 & 0x11111111u) << 1;
+                    noted |= 1u << (j >> 4);
                 }
 #pragma unroll
                 for (int c = 0; c < KC; ++c) {
@@ -609,6 +645,16 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
             }
         }
         __syncwarp();
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float e = ds_sum[n][r];
+                for (int w = 4; w < 32; w <<= 1) e += __shfl_xor_sync(0xffffffffu, e, w);
+                const int row = 8 * n + 2 * t + r;
+                if (g == 0 && row < u.rows) notes.sums[unit * (static_cast<long long>(L.max_q) * L.group) + row] = e;
+            }
+        if (lane == 0) notes.steps[unit] = noted;
         if (L.q_off) {
             write(slot, u.rows);
             clear();
@@ -620,9 +666,7 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
 // dQ: the sum of a row's parts in a fixed order, times the scale; of shared
 // queries the sum over all workers.  W warps a row, four elements a lane.
 template <typename T, int W>
-__global__ void __launch_bounds__(256)
-    dq_join_kernel(const __grid_constant__ AttentionLaunch L, int chunk, long long workers, const float *part_dq) {
-    after_previous();
+__device__ __forceinline__ void join_dq(const AttentionLaunch &L, int chunk, long long workers, const float *part_dq) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long most = static_cast<long long>(L.max_q) * L.group;
     const int dim = L.head_dim, d = 4 * lane;
@@ -668,6 +712,80 @@ __global__ void __launch_bounds__(256)
             make_uint2(Type<T>::pack(s.x * L.scale, s.y * L.scale), Type<T>::pack(s.z * L.scale, s.w * L.scale));
 }
 
+// The dK of a unit's noted states, with delta corrected by the row's sum of ds
+// over the item's units, in their order.  A warp a unit, four elements a lane.
+template <typename T>
+__device__ __forceinline__ void mend(const AttentionLaunch &L, int chunk, long long slots, long long unit, const Notes &notes) {
+    if (unit >= slots * L.key_heads) return;
+    uint32_t steps = notes.steps[unit];
+    if (!steps) return;
+    const int lane = threadIdx.x & 31, head = static_cast<int>(unit % L.key_heads), dim = L.head_dim, d = 4 * lane;
+    const Unit u = find_unit(L, chunk, unit / L.key_heads, head, lane);
+    const long long most = static_cast<long long>(L.max_q) * L.group;
+    const long long first = u.slot - (u.k0 - u.item.k0) / chunk;
+    const int parts = max(1, (u.item.nk + chunk - 1) / chunk);
+    const bool in = d < dim;
+    auto load = [&](const T *p, float (&v)[4]) {
+        const uint2 w = in ? *reinterpret_cast<const uint2 *>(p + d) : make_uint2(0, 0);
+        const float2 a = Type<T>::unpack(w.x), b = Type<T>::unpack(w.y);
+        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+    };
+    auto dot = [&](const float (&a)[4], const float (&b)[4]) {
+        float x = fmaf(a[0], b[0], fmaf(a[1], b[1], fmaf(a[2], b[2], a[3] * b[3])));
+        for (int w = 16; w; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+        return x;
+    };
+    // Row r's delta and lse (in powers of two) in lane r.
+    float delta = 0.0f, lse = 0.0f;
+    for (int r = 0; r < u.rows; ++r) {
+        float a[4], b[4];
+        load(row_ptr<T>(L, L.d_o, u, u.item.o0, r), a);
+        load(row_ptr<T>(L, L.o, u, u.item.o0, r), b);
+        const float x = dot(a, b);
+        if (lane == r) delta = x;
+    }
+    if (lane < u.rows) {
+        const int rr = lane / L.group, h = head * L.group + lane - rr * L.group;
+        const float e = L.lse[static_cast<long long>(u.item.o0 + rr) * L.query_heads + h];
+        lse = e == -INFINITY ? INFINITY : e * kLog2e;
+        for (int p = 0; p < parts; ++p) delta += notes.sums[((first + p) * L.key_heads + head) * most + lane];
+    }
+    for (; steps; steps &= steps - 1) {
+        const int step = __ffs(steps) - 1;
+        for (uint32_t left = notes.states[unit * kSteps + step]; left; left &= left - 1) {
+            const int bit = __ffs(left) - 1;
+            const long long row = u.k0 + 16 * step + (bit >> 2) + 8 * (bit & 1);
+            float k[4], v[4], dk[4] = {};
+            load(static_cast<const T *>(L.k.data) + row * L.k.row + head * L.k.head, k);
+            load(static_cast<const T *>(L.v.data) + row * L.v.row + head * L.v.head, v);
+#pragma unroll 4
+            for (int r = 0; r < u.rows; ++r) {
+                float q[4], o[4];
+                load(row_ptr<T>(L, L.q, u, u.item.q0, r), q);
+                load(row_ptr<T>(L, L.d_o, u, u.item.o0, r), o);
+                const float p = ex2_full(fmaf(dot(q, k), L.scale * kLog2e, -__shfl_sync(0xffffffffu, lse, r)));
+                const float ds = p * (dot(o, v) - __shfl_sync(0xffffffffu, delta, r));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dk[i] = fmaf(ds, q[i], dk[i]);
+            }
+            if (in)
+                *reinterpret_cast<uint2 *>(static_cast<T *>(L.d_k.data) + row * L.d_k.row + head * L.d_k.head + d) =
+                    make_uint2(Type<T>::pack(dk[0] * L.scale, dk[1] * L.scale), Type<T>::pack(dk[2] * L.scale, dk[3] * L.scale));
+        }
+    }
+}
+
+template <typename T, int W>
+__global__ void __launch_bounds__(256)
+    finish_kernel(const __grid_constant__ AttentionLaunch L, int chunk, long long slots, long long workers, unsigned joins,
+                  const float *part_dq, Notes notes) {
+    after_previous();
+    if (blockIdx.x < joins)
+        join_dq<T, W>(L, chunk, workers, part_dq);
+    else
+        mend<T>(L, chunk, slots, static_cast<long long>(blockIdx.x - joins) * 8 + (threadIdx.x >> 5), notes);
+}
+
 // ----------------------------------------------------------------------------
 // calls without states or without queries
 // ----------------------------------------------------------------------------
@@ -704,7 +822,7 @@ Cut cut_of(const AttentionLaunch &L) {
     Cut c;
     long long want = static_cast<long long>(L.key_rows) * L.key_heads / (152 * 16 * 4);
     want = (want + 31) / 32 * 32;
-    c.chunk = static_cast<int>(want < 32 ? 32 : want > 512 ? 512 : want);
+    c.chunk = static_cast<int>(want < 32 ? 32 : want > kMostChunk ? kMostChunk : want);
     c.slots = c.chunk >= L.max_k ? L.items : L.key_rows / c.chunk + static_cast<long long>(L.items);
     const long long warps = 152 * 12 / L.key_heads;
     c.workers = L.q_off ? c.slots : warps < 1 ? 1 : warps < c.slots ? warps : c.slots;
@@ -739,15 +857,32 @@ cudaError_t forward(const AttentionLaunch &L, cudaStream_t stream) {
     return launch_after(join_kernel<T, 1>, dim3(blocks_of(rows, 8)), 256, 0, stream, L, c.chunk, part_o, part_ml);
 }
 
+// The backward's workspace: dQ's parts, then the notes.
+size_t notes_sums_bytes(const AttentionLaunch &L, const Cut &c) {
+    return align256(static_cast<size_t>(c.slots) * L.key_heads * c.rows * sizeof(float));
+}
+size_t notes_steps_bytes(const AttentionLaunch &L, const Cut &c) {
+    return align256(static_cast<size_t>(c.slots) * L.key_heads * sizeof(uint32_t));
+}
+
 template <typename T, int DP, int NT>
 cudaError_t backward(const AttentionLaunch &L, cudaStream_t stream) {
     const Cut c = cut_of(L);
     float *part_dq = reinterpret_cast<float *>(L.workspace);
-    backward_kernel<T, DP, NT><<<blocks_of(c.workers * L.key_heads, kWarps / NT), kWarps / NT * 32, 0, stream>>>(L, c.chunk, c.slots, c.workers, part_dq);
-    const long long rows = L.q_off ? L.items * L.key_heads * c.rows : L.key_heads * c.rows;
+    char *at = reinterpret_cast<char *>(L.workspace) + part_bytes(L, c.workers, c);
+    Notes notes;
+    notes.sums = reinterpret_cast<float *>(at);
+    notes.steps = reinterpret_cast<uint32_t *>(at + notes_sums_bytes(L, c));
+    notes.states = reinterpret_cast<uint32_t *>(at + notes_sums_bytes(L, c) + notes_steps_bytes(L, c));
+    backward_kernel<T, DP, NT><<<blocks_of(c.workers * L.key_heads, kWarps / NT), kWarps / NT * 32, 0, stream>>>(
+        L, c.chunk, c.slots, c.workers, part_dq, notes);
+    const long long rows = (L.q_off ? static_cast<long long>(L.items) : 1) * L.key_heads * c.rows;
+    const unsigned mends = blocks_of(c.slots * L.key_heads, 8);
     if (!L.q_off || wide_join(L, c, rows))
-        return launch_after(dq_join_kernel<T, 8>, dim3(static_cast<unsigned>(rows)), 256, 0, stream, L, c.chunk, c.workers, part_dq);
-    return launch_after(dq_join_kernel<T, 1>, dim3(blocks_of(rows, 8)), 256, 0, stream, L, c.chunk, c.workers, part_dq);
+        return launch_after(finish_kernel<T, 8>, dim3(static_cast<unsigned>(rows) + mends), 256, 0, stream, L, c.chunk, c.slots,
+                            c.workers, static_cast<unsigned>(rows), part_dq, notes);
+    return launch_after(finish_kernel<T, 1>, dim3(blocks_of(rows, 8) + mends), 256, 0, stream, L, c.chunk, c.slots, c.workers,
+                        blocks_of(rows, 8), part_dq, notes);
 }
 
 template <typename T>
@@ -789,7 +924,8 @@ size_t attention_backward_workspace(const AttentionLaunch &L) {
     if (!L.query_rows || !L.key_rows) return 0;
     if (!few_rows(L, true)) return backward_tiles_workspace(L);
     const Cut c = cut_of(L);
-    return part_bytes(L, c.workers, c);
+    return part_bytes(L, c.workers, c) + notes_sums_bytes(L, c) + notes_steps_bytes(L, c) +
+           static_cast<size_t>(c.slots) * L.key_heads * kSteps * sizeof(uint32_t);
 }
 
 cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t stream) {

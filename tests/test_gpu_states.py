@@ -347,6 +347,48 @@ def test_attention_is_repeatable_and_stream_ordered(cli, q_len, k_len, hq):
         assert torch.equal(a[name], b[name]), name
 
 
+@pytest.mark.parametrize("q_len, k_len, hq, hk, d, shared", [
+    (1, [200, 37, 1024, 700, 0, 3] * 8, 8, 8, 128, True), ([1, 3, 2], [5000, 90, 400], 8, 2, 64, False),
+    ([4], [700], 12, 3, 72, False),
+])
+def test_gradient_of_a_state_that_has_most_of_a_row(cli, q_len, k_len, hq, hk, d, shared):
+    """dK in bf16 where ds = p (dp - delta) is a small difference: with delta from the rounded output alone it is off by up to
+    u scale p sum |dO O| |q|, u the type's unit roundoff.  Of that at most a sixteenth may be left (a state with a
+    weight above it is computed with delta from 32-bit sums), beside dK's own rounding, two roundings' worth of the
+    16-bit halves (u^2) and the sums in 32 bits (2^-15 of their terms, as p and delta take part in all of them)."""
+    g, dtype = gen(77), BF16
+    rows_q, rows_k = (q_len if shared else sum(q_len)), sum(k_len)
+    out_rows = rows_q * len(k_len) if shared else rows_q
+    q, k, v = rand(g, rows_q, hq, d, dtype=dtype, scale=4.0), rand(g, rows_k, hk, d, dtype=dtype), rand(g, rows_k, hk, d, dtype=dtype)
+    d_o = rand(g, out_rows, hq, d, dtype=dtype)
+    qo = None if shared else offsets(q_len)
+    kw = dict(max_query_rows=rows_q if shared else max(q_len), max_key_rows=max(k_len))
+    f = cli.cross_attention(q, qo, k, v, offsets(k_len), **kw)
+    got = cli.cross_attention_backward(q, qo, k, v, offsets(k_len), f["output"], f["lse"], d_o, **kw)["d_k"].double()
+    u, scale = 2.0 ** -8, d ** -0.5
+    ka = qa = 0
+    largest = 0.0
+    for i, nk in enumerate(k_len):
+        nq = rows_q if shared else q_len[i]
+        qi = q[:nq] if shared else q[qa:qa + nq]
+        wide = lambda t: t.double().repeat_interleave(hq // hk, 1)  # noqa: E731
+        qi, oi, ki, vi = qi.double(), d_o[qa:qa + nq].double(), wide(k[ka:ka + nk]), wide(v[ka:ka + nk])
+        p = (torch.einsum("qhd,khd->hqk", qi, ki) * scale).softmax(-1)
+        o = torch.einsum("hqk,khd->qhd", p, vi)
+        delta = (oi * o).sum(-1).T[:, :, None]
+        ds = p * (torch.einsum("qhd,khd->hqk", oi, vi) - delta)
+        terms = p * (torch.einsum("qhd,khd->hqk", oi.abs(), vi.abs()) + (oi * o).abs().sum(-1).T[:, :, None])
+        spread = p.clamp(max=1 / 16) * u * (oi * o).abs().sum(-1).T[:, :, None] + (2.0 ** -15 + u * u) * terms
+        fold = lambda t: t.view(nk, hk, hq // hk, d).sum(2)  # noqa: E731
+        want = scale * fold(torch.einsum("hqk,qhd->khd", ds, qi))
+        bound = u * want.abs() + scale * fold(torch.einsum("hqk,qhd->khd", spread, qi.abs())) + ref.TINY[dtype]
+        if nk:
+            largest = max(largest, p.max().item())
+            assert ((got[ka:ka + nk] - want).abs() <= bound).all()
+        ka, qa = ka + nk, qa + nq
+    assert largest > 0.9
+
+
 def test_attention_without_lse_and_with_loose_maxima(cli):
     g = gen(12)
     q_len, k_len = [1, 1, 1], [40, 500, 7]
