@@ -735,20 +735,25 @@ __device__ __forceinline__ void mend(const AttentionLaunch &L, int chunk, long l
         for (int w = 16; w; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
         return x;
     };
-    // Row r's delta and lse (in powers of two) in lane r.
+    // Row r's delta and lse (in powers of two) in lane r and lane r + 16, which share its sums.
     float delta = 0.0f, lse = 0.0f;
+    const int row_of = lane & 15;
+    if (row_of < u.rows) {
+        const int rr = row_of / L.group, h = head * L.group + row_of - rr * L.group;
+        const float e = L.lse[static_cast<long long>(u.item.o0 + rr) * L.query_heads + h];
+        lse = e == -INFINITY ? INFINITY : e * kLog2e;
+        const float *sums = notes.sums + (first * L.key_heads + head) * most + row_of;
+#pragma unroll 8
+        for (int p = lane >> 4; p < parts; p += 2) delta += sums[p * (L.key_heads * most)];
+    }
+    delta += __shfl_xor_sync(0xffffffffu, delta, 16);
+#pragma unroll 8
     for (int r = 0; r < u.rows; ++r) {
         float a[4], b[4];
         load(row_ptr<T>(L, L.d_o, u, u.item.o0, r), a);
         load(row_ptr<T>(L, L.o, u, u.item.o0, r), b);
         const float x = dot(a, b);
-        if (lane == r) delta = x;
-    }
-    if (lane < u.rows) {
-        const int rr = lane / L.group, h = head * L.group + lane - rr * L.group;
-        const float e = L.lse[static_cast<long long>(u.item.o0 + rr) * L.query_heads + h];
-        lse = e == -INFINITY ? INFINITY : e * kLog2e;
-        for (int p = 0; p < parts; ++p) delta += notes.sums[((first + p) * L.key_heads + head) * most + lane];
+        if (row_of == r) delta += x;
     }
     for (; steps; steps &= steps - 1) {
         const int step = __ffs(steps) - 1;
@@ -758,7 +763,7 @@ __device__ __forceinline__ void mend(const AttentionLaunch &L, int chunk, long l
             float k[4], v[4], dk[4] = {};
             load(static_cast<const T *>(L.k.data) + row * L.k.row + head * L.k.head, k);
             load(static_cast<const T *>(L.v.data) + row * L.v.row + head * L.v.head, v);
-#pragma unroll 4
+#pragma unroll 8
             for (int r = 0; r < u.rows; ++r) {
                 float q[4], o[4];
                 load(row_ptr<T>(L, L.q, u, u.item.q0, r), q);
