@@ -713,26 +713,34 @@ __device__ __forceinline__ void join_dq(const AttentionLaunch &L, int chunk, lon
 }
 
 // The dK of a unit's noted states, with delta corrected by the row's sum of ds
-// over the item's units, in their order.  A warp a unit, four elements a lane.
+// over the item's units, in a fixed order.  A warp a unit: half a warp a row,
+// eight elements a lane.
 template <typename T>
 __device__ __forceinline__ void mend(const AttentionLaunch &L, int chunk, long long slots, long long unit, const Notes &notes) {
     if (unit >= slots * L.key_heads) return;
     uint32_t steps = notes.steps[unit];
     if (!steps) return;
-    const int lane = threadIdx.x & 31, head = static_cast<int>(unit % L.key_heads), dim = L.head_dim, d = 4 * lane;
+    const int lane = threadIdx.x & 31, head = static_cast<int>(unit % L.key_heads), dim = L.head_dim, d = 8 * (lane & 15);
+    const int half = lane >> 4;
     const Unit u = find_unit(L, chunk, unit / L.key_heads, head, lane);
     const long long most = static_cast<long long>(L.max_q) * L.group;
     const long long first = u.slot - (u.k0 - u.item.k0) / chunk;
     const int parts = max(1, (u.item.nk + chunk - 1) / chunk);
     const bool in = d < dim;
-    auto load = [&](const T *p, float (&v)[4]) {
-        const uint2 w = in ? *reinterpret_cast<const uint2 *>(p + d) : make_uint2(0, 0);
-        const float2 a = Type<T>::unpack(w.x), b = Type<T>::unpack(w.y);
-        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+    auto load = [&](const T *p, bool on, float (&v)[8]) {
+        const uint4 w = in && on ? *reinterpret_cast<const uint4 *>(p + d) : make_uint4(0, 0, 0, 0);
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 y = Type<T>::unpack(x[i]);
+            v[2 * i] = y.x, v[2 * i + 1] = y.y;
+        }
     };
-    auto dot = [&](const float (&a)[4], const float (&b)[4]) {
-        float x = fmaf(a[0], b[0], fmaf(a[1], b[1], fmaf(a[2], b[2], a[3] * b[3])));
-        for (int w = 16; w; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+    auto dot = [&](const float (&a)[8], const float (&b)[8]) {   // each half's
+        float x = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x = fmaf(a[i], b[i], x);
+        for (int w = 8; w; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
         return x;
     };
     // Row r's delta and lse (in powers of two) in lane r and lane r + 16, which share its sums.
@@ -747,35 +755,44 @@ __device__ __forceinline__ void mend(const AttentionLaunch &L, int chunk, long l
         for (int p = lane >> 4; p < parts; p += 2) delta += sums[p * (L.key_heads * most)];
     }
     delta += __shfl_xor_sync(0xffffffffu, delta, 16);
-#pragma unroll 8
-    for (int r = 0; r < u.rows; ++r) {
-        float a[4], b[4];
-        load(row_ptr<T>(L, L.d_o, u, u.item.o0, r), a);
-        load(row_ptr<T>(L, L.o, u, u.item.o0, r), b);
-        const float x = dot(a, b);
-        if (row_of == r) delta += x;
+#pragma unroll 4
+    for (int r0 = 0; r0 < u.rows; r0 += 2) {
+        const int r = r0 + half;
+        const bool on = r < u.rows;
+        float a[8], b[8];
+        load(row_ptr<T>(L, L.d_o, u, u.item.o0, on ? r : 0), on, a);
+        load(row_ptr<T>(L, L.o, u, u.item.o0, on ? r : 0), on, b);
+        const float x = dot(a, b), other = __shfl_xor_sync(0xffffffffu, x, 16);
+        if ((row_of & ~1) == r0) delta += (row_of & 1) == half ? x : other;
     }
     for (; steps; steps &= steps - 1) {
         const int step = __ffs(steps) - 1;
         for (uint32_t left = notes.states[unit * kSteps + step]; left; left &= left - 1) {
             const int bit = __ffs(left) - 1;
             const long long row = u.k0 + 16 * step + (bit >> 2) + 8 * (bit & 1);
-            float k[4], v[4], dk[4] = {};
-            load(static_cast<const T *>(L.k.data) + row * L.k.row + head * L.k.head, k);
-            load(static_cast<const T *>(L.v.data) + row * L.v.row + head * L.v.head, v);
-#pragma unroll 8
-            for (int r = 0; r < u.rows; ++r) {
-                float q[4], o[4];
-                load(row_ptr<T>(L, L.q, u, u.item.q0, r), q);
-                load(row_ptr<T>(L, L.d_o, u, u.item.o0, r), o);
-                const float p = ex2_full(fmaf(dot(q, k), L.scale * kLog2e, -__shfl_sync(0xffffffffu, lse, r)));
-                const float ds = p * (dot(o, v) - __shfl_sync(0xffffffffu, delta, r));
+            float k[8], v[8], dk[8] = {};
+            load(static_cast<const T *>(L.k.data) + row * L.k.row + head * L.k.head, true, k);
+            load(static_cast<const T *>(L.v.data) + row * L.v.row + head * L.v.head, true, v);
+#pragma unroll 4
+            for (int r0 = 0; r0 < u.rows; r0 += 2) {
+                const int r = r0 + half;
+                const bool on = r < u.rows;
+                float q[8], o[8];
+                load(row_ptr<T>(L, L.q, u, u.item.q0, on ? r : 0), on, q);
+                load(row_ptr<T>(L, L.d_o, u, u.item.o0, on ? r : 0), on, o);
+                const float p = ex2_full(fmaf(dot(q, k), L.scale * kLog2e, -__shfl_sync(0xffffffffu, lse, r & 15)));
+                const float ds = p * (dot(o, v) - __shfl_sync(0xffffffffu, delta, r & 15));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) dk[i] = fmaf(ds, q[i], dk[i]);
+                for (int i = 0; i < 8; ++i) dk[i] = on ? fmaf(ds, q[i], dk[i]) : dk[i];
             }
-            if (in)
-                *reinterpret_cast<uint2 *>(static_cast<T *>(L.d_k.data) + row * L.d_k.row + head * L.d_k.head + d) =
-                    make_uint2(Type<T>::pack(dk[0] * L.scale, dk[1] * L.scale), Type<T>::pack(dk[2] * L.scale, dk[3] * L.scale));
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dk[i] = (dk[i] + __shfl_xor_sync(0xffffffffu, dk[i], 16)) * L.scale;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = Type<T>::pack(dk[2 * i], dk[2 * i + 1]);
+            if (in && half == 0)
+                *reinterpret_cast<uint4 *>(static_cast<T *>(L.d_k.data) + row * L.d_k.row + head * L.d_k.head + d) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 }
