@@ -413,10 +413,12 @@ __global__ void __launch_bounds__(256)
 // of a row's weight, its ds = p (dp - delta) is a small difference of large
 // terms, and that rounding shows: an element of dK was off by as much as the
 // root mean square of all of dK.  So the sums of ds are kept too: over a whole
-// row sum p (dp - delta) is 0, and what it is instead is delta's error.  States
-// with a weight of kLarge or more in some row (at most 1 / kLarge a row) are
-// noted, and mend() computes their dK again with the right delta.
-constexpr float kLarge = 1.0f / 16;
+// row sum p (dp - delta) is 0, and what it is instead is delta's error.
+// States with a weight of 1/8 or more in some row, or 1/4 with more than 8 rows,
+// whose share of an element is less, are noted, and mend() computes their dK
+// again with the right delta (with 1/16 for all, 512 x 32 to 1024 states, 16
+// rows, 16 heads of 64 took 1287 us, twice what they take without).
+constexpr float large_weight(int tiles) { return tiles == 1 ? 0.125f : 0.25f; }
 
 // What the backward leaves for mend(): of each unit, the sums of ds of its
 // rows, the steps of 16 states with noted ones, and which they are: bit 4 g of
@@ -432,6 +434,7 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
                     float *part_dq, Notes notes) {
     constexpr int KC = DP / 32, KG = 128 / DP;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    constexpr float kLarge = large_weight(NT);
     // [warp][Q, dO, Q^T, dO^T][tile][chunk][lane]
     __shared__ uint4 frag[kWarps / NT][4][NT][KC][32];
     check_all(L, false);
@@ -922,8 +925,9 @@ cudaError_t dispatch(const AttentionLaunch &L, bool back, cudaStream_t stream) {
 // the forward's tensor cores are ahead from some states on (16 rows, 8 heads of
 // 128: 1 x 4096 states 13.8 us here and 16.3 there, 1 x 8192 27 and 18; 32 x
 // 256 of 64: 16.6 and 11.6; 32 x 2048: 60 and 34; 512 x 32 to 1024 shared, 16
-// heads of 64: 301 and 290; with 9 rows, 260).  The backward is ahead here (the
-// last: 624 us and 875; 32 x 2048, 8 heads of 64: 83 and 125).
+// heads of 64: 301 and 290; with 9 rows, 260).  The backward is ahead here in
+// long items (64 x 4096, 8 heads of 64: 320 us and 434; 32 x 2048: 110 and 126)
+// and behind in short ones (the last: 925 us and 875).
 bool few_rows(const AttentionLaunch &L, bool back) {
     const long long rows = static_cast<long long>(L.max_q) * L.group;
     return rows <= 8 || (rows <= 16 && (back || static_cast<long long>(L.key_rows) * L.key_heads <= 32768));

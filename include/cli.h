@@ -622,7 +622,7 @@ size_t norm_rotary_heads_backward_workspace_bytes(size_t head_dim);
  * P and dS enter the products as `dtype`, or as the sum of two such where an
  * item has few rows; everything else between input and output is in 32 bits,
  * but for D, which the rounded output gives (with few rows, states that have a
- * sixteenth or more of a row's weight get theirs from 32-bit sums).
+ * quarter or more of a row's weight get theirs from 32-bit sums).
  * Results are bit-reproducible: no sum depends on the order in which blocks run.
  */
 typedef struct {
