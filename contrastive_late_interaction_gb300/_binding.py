@@ -5,6 +5,11 @@ already live on the GPU, calls the exported C symbol of the same name, and
 turns a non-OK status into an exception.  All arithmetic happens in the CUDA
 library; if it is missing, importing this module raises.  PyTorch is used only
 for device memory and streams.
+
+A verb runs on the current stream, or on `stream` where one is given.  Its
+inputs have to be ready on that stream, and they and any buffers lent to it
+have to stay alive until it has passed them; what the verb makes itself is
+ordered by it.
 """
 
 from __future__ import annotations
@@ -240,9 +245,8 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream():
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
 def _check_cuda(t, name, dtype=None):
@@ -296,16 +300,34 @@ def _ws(nbytes, device):
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
+def _on(stream, verb, arguments):
+    """verb(**arguments) with `stream` as the current stream.  What the verb allocates or fills comes from that
+    stream's pool, in its order: a workspace that the verb drops is not handed to the caller's stream while kernels
+    still use it, and a result is not made of memory that the caller's stream still reads.  Results dropped by the
+    caller wait for the caller's stream.  The verb's inputs, and buffers lent to it, are the caller's to keep and to
+    order."""
+    caller = torch.cuda.current_stream()
+    arguments["stream"] = None
+    with torch.cuda.stream(stream):
+        made = verb(**arguments)
+    for t in made.values():
+        if t is not None:
+            t.record_stream(caller)
+    return made
+
+
 def selftest_bounded_wait(limit_us=20000, device_status=None, gave_up=None, stream=None):
     """Runs the failure path of the kernels' bounded waits (one CTA waiting on a barrier nothing arrives
     at, giving up after `limit_us`).  Returns dict(device_status, gave_up) of device int32 tensors; the
     status reads CLI_INTERNAL and gave_up the number of threads (64) once the stream reaches them."""
+    if stream is not None:
+        return _on(stream, selftest_bounded_wait, locals())
     dev = torch.device("cuda", torch.cuda.current_device())
     st = device_status if device_status is not None else torch.zeros(1, dtype=torch.int32, device=dev)
     gu = gave_up if gave_up is not None else torch.zeros(1, dtype=torch.int32, device=dev)
     _check_cuda(st, "device_status", torch.int32)
     _check_cuda(gu, "gave_up", torch.int32)
-    raise_for(lib.cli_selftest_bounded_wait(_ptr(st), _ptr(gu), int(limit_us), _stream(stream)),
+    raise_for(lib.cli_selftest_bounded_wait(_ptr(st), _ptr(gu), int(limit_us), _stream()),
               "cli_selftest_bounded_wait")
     return dict(device_status=st, gave_up=gu)
 
@@ -330,6 +352,8 @@ def pair_loss_sigmoid_fwd_bwd(embeddings, inverse_temperature, bias, attract, re
     unless `out['width']` narrows it).  Returns dict(loss, d_embeddings, d_inverse_temperature, d_bias,
     device_status) of device tensors; the device status is not synchronised here.  `band` = (row_begin,
     row_count) scores only the anchors in those rows: the results are that band's shares of the whole call's."""
+    if stream is not None:
+        return _on(stream, pair_loss_sigmoid_fwd_bwd, locals())
     _check_cuda(embeddings, "embeddings", torch.bfloat16)
     _check_cuda(inverse_temperature, "inverse_temperature", torch.float32)
     _check_cuda(bias, "bias", torch.float32)
@@ -352,7 +376,7 @@ def pair_loss_sigmoid_fwd_bwd(embeddings, inverse_temperature, bias, attract, re
         relations=Relations(A, R, I, int(bool(negatives_named)), float(ambient_weight)),
         loss=_ptr(loss), d_embeddings=_ptr(de), ld_d_embeddings=de.stride(0),
         d_inverse_temperature=_ptr(dt), d_bias=_ptr(db), workspace=_ptr(ws), workspace_bytes=ws.numel(),
-        device_status=_ptr(st), stream=_stream(stream), **_band(band))
+        device_status=_ptr(st), stream=_stream(), **_band(band))
     raise_for(lib.pair_loss_sigmoid_fwd_bwd(ctypes.byref(args)), "pair_loss_sigmoid_fwd_bwd")
     return dict(loss=loss, d_embeddings=de, d_inverse_temperature=dt, d_bias=db, device_status=st)
 
@@ -363,6 +387,8 @@ def pair_loss_sigmoid_groups_fwd_bwd(embeddings, groups, inverse_temperature, bi
     """The pooled sigmoid pair loss with temperature groups: `groups` (int32 [N]) selects each item's pair of
     `inverse_temperature`, `bias` (fp32 [G]) and a cell takes its anchor's.  Returns dict(loss, d_embeddings,
     d_inverse_temperature [G], d_bias [G], device_status) of device tensors."""
+    if stream is not None:
+        return _on(stream, pair_loss_sigmoid_groups_fwd_bwd, locals())
     _check_cuda(embeddings, "embeddings", torch.bfloat16)
     _check_cuda(groups, "groups", torch.int32)
     _check_cuda(inverse_temperature, "inverse_temperature", torch.float32)
@@ -389,7 +415,7 @@ def pair_loss_sigmoid_groups_fwd_bwd(embeddings, groups, inverse_temperature, bi
         relations=Relations(A, R, I, int(bool(negatives_named)), float(ambient_weight)),
         loss=_ptr(loss), d_embeddings=_ptr(de), ld_d_embeddings=de.stride(0),
         d_inverse_temperature=_ptr(dt), d_bias=_ptr(db), workspace=_ptr(ws), workspace_bytes=ws.numel(),
-        device_status=_ptr(st), stream=_stream(stream), **_band(band))
+        device_status=_ptr(st), stream=_stream(), **_band(band))
     args = PairLossGroupsArgs(base=base, groups=_ptr(groups), group_count=g)
     raise_for(lib.pair_loss_sigmoid_groups_fwd_bwd(ctypes.byref(args)), "pair_loss_sigmoid_groups_fwd_bwd")
     return dict(loss=loss, d_embeddings=de, d_inverse_temperature=dt, d_bias=db, device_status=st)
@@ -405,6 +431,8 @@ def pair_loss_sigmoid_matryoshka_fwd_bwd(embeddings, prefix_widths, inverse_temp
     """The pooled sigmoid pair loss summed over the normalised prefixes `prefix_widths` of bf16 embeddings
     [N, ld] (first `width` = embeddings.shape[1] columns unless `out['width']` narrows it).  Returns
     dict(loss, d_embeddings, d_inverse_temperature, d_bias, prefix_loss, device_status) of device tensors."""
+    if stream is not None:
+        return _on(stream, pair_loss_sigmoid_matryoshka_fwd_bwd, locals())
     _check_cuda(embeddings, "embeddings", torch.bfloat16)
     _check_cuda(inverse_temperature, "inverse_temperature", torch.float32)
     _check_cuda(bias, "bias", torch.float32)
@@ -430,7 +458,7 @@ def pair_loss_sigmoid_matryoshka_fwd_bwd(embeddings, prefix_widths, inverse_temp
         relations=Relations(A, R, I, int(bool(negatives_named)), float(ambient_weight)),
         loss=_ptr(loss), d_embeddings=_ptr(de), ld_d_embeddings=de.stride(0),
         d_inverse_temperature=_ptr(dt), d_bias=_ptr(db), workspace=_ptr(ws), workspace_bytes=ws.numel(),
-        device_status=_ptr(st), stream=_stream(stream), **_band(band))
+        device_status=_ptr(st), stream=_stream(), **_band(band))
     args = PairLossMatryoshkaArgs(base=base, prefix_widths=ctypes.cast(widths, c_void_p),
                                   prefix_count=len(prefix_widths), prefix_loss=_ptr(pl))
     raise_for(lib.pair_loss_sigmoid_matryoshka_fwd_bwd(ctypes.byref(args)), "pair_loss_sigmoid_matryoshka_fwd_bwd")
@@ -445,6 +473,8 @@ def pair_loss_sigmoid_scores_fwd_bwd(scores, inverse_temperature, bias, attract,
                                      sides=None, negatives_named=False, ambient_weight=1.0, out=None,
                                      workspace=None, device_status=None, stream=None):
     """Sigmoid pair loss over an fp32 score matrix [rows, cols]."""
+    if stream is not None:
+        return _on(stream, pair_loss_sigmoid_scores_fwd_bwd, locals())
     _check_cuda(scores, "scores", torch.float32)
     _check_cuda(sides, "sides", torch.uint8)
     rows, cols = scores.shape
@@ -462,7 +492,7 @@ def pair_loss_sigmoid_scores_fwd_bwd(scores, inverse_temperature, bias, attract,
         bias=_ptr(bias), relations=Relations(A, R, I, int(bool(negatives_named)), float(ambient_weight)),
         sides=_ptr(sides), loss=_ptr(loss), d_scores=_ptr(ds), ld_d_scores=ds.stride(0),
         d_inverse_temperature=_ptr(dt), d_bias=_ptr(db), workspace=_ptr(ws), workspace_bytes=ws.numel(),
-        device_status=_ptr(st), stream=_stream(stream))
+        device_status=_ptr(st), stream=_stream())
     raise_for(lib.pair_loss_sigmoid_scores_fwd_bwd(ctypes.byref(args)), "pair_loss_sigmoid_scores_fwd_bwd")
     return dict(loss=loss, d_scores=ds, d_inverse_temperature=dt, d_bias=db, device_status=st)
 
@@ -475,6 +505,8 @@ def pair_loss_scores_fwd_bwd(form, scores, inverse_temperature, bias, attract, r
                              negatives_named=False, ambient_weight=1.0, out=None, workspace=None, device_status=None,
                              stream=None):
     """Pair loss of form 'balanced', 'ranked' or 'sigmoid' over an fp32 score matrix [rows, cols]."""
+    if stream is not None:
+        return _on(stream, pair_loss_scores_fwd_bwd, locals())
     _check_cuda(scores, "scores", torch.float32)
     _check_cuda(sides, "sides", torch.uint8)
     rows, cols = scores.shape
@@ -492,7 +524,7 @@ def pair_loss_scores_fwd_bwd(form, scores, inverse_temperature, bias, attract, r
         bias=_ptr(bias), relations=Relations(A, R, I, int(bool(negatives_named)), float(ambient_weight)),
         sides=_ptr(sides), loss=_ptr(loss), d_scores=_ptr(ds), ld_d_scores=ds.stride(0),
         d_inverse_temperature=_ptr(dt), d_bias=_ptr(db), workspace=_ptr(ws), workspace_bytes=ws.numel(),
-        device_status=_ptr(st), stream=_stream(stream))
+        device_status=_ptr(st), stream=_stream())
     args = PairLossScoresArgs(form=FORMS[form], args=inner)
     raise_for(lib.pair_loss_scores_fwd_bwd(ctypes.byref(args)), "pair_loss_scores_fwd_bwd")
     return dict(loss=loss, d_scores=ds, d_inverse_temperature=dt, d_bias=db, device_status=st)
@@ -516,6 +548,8 @@ def maxsim_scores(q_data, q_offsets, d_data, d_offsets, mean=False, out=None, wo
                   stream=None):
     """Hard MaxSim of every query against every document.  Returns dict(scores [nq, nd] fp32,
     argmax [nd, rows_q] int32 (document-major), device_status)."""
+    if stream is not None:
+        return _on(stream, maxsim_scores, locals())
     Q, D = _tape(q_data, q_offsets), _tape(d_data, d_offsets)
     width = q_data.shape[1]
     if d_data.shape[1] != width:
@@ -530,7 +564,7 @@ def maxsim_scores(q_data, q_offsets, d_data, d_offsets, mean=False, out=None, wo
                                                      dev)
     args = MaxSimArgs(queries=Q, documents=D, width=width, mean=int(bool(mean)), scores=_ptr(scores),
                       ld_scores=scores.stride(0), argmax=_ptr(argmax), ld_argmax=argmax.stride(0),
-                      workspace=_ptr(ws), workspace_bytes=ws.numel(), device_status=_ptr(st), stream=_stream(stream))
+                      workspace=_ptr(ws), workspace_bytes=ws.numel(), device_status=_ptr(st), stream=_stream())
     raise_for(lib.maxsim_scores(ctypes.byref(args)), "maxsim_scores")
     return dict(scores=scores, argmax=argmax, device_status=st)
 
@@ -544,6 +578,8 @@ def maxsim_scores_named(q_data, q_offsets, d_data, d_offsets, pairs, mean=False,
     """Hard MaxSim of each query against the documents `pairs` names (a CSR over the queries, as from
     `device_edges`).  Returns dict(scores [nq, nd] fp32, zero for pairs not named, argmax [nd, rows_q] int32,
     a valid row of the document for pairs not named, device_status)."""
+    if stream is not None:
+        return _on(stream, maxsim_scores_named, locals())
     Q, D = _tape(q_data, q_offsets), _tape(d_data, d_offsets)
     width = q_data.shape[1]
     if d_data.shape[1] != width:
@@ -558,7 +594,7 @@ def maxsim_scores_named(q_data, q_offsets, d_data, d_offsets, pairs, mean=False,
         maxsim_named_workspace_bytes(Q.count, D.count, Q.rows, D.rows, width), dev)
     base = MaxSimArgs(queries=Q, documents=D, width=width, mean=int(bool(mean)), scores=_ptr(scores),
                       ld_scores=scores.stride(0), argmax=_ptr(argmax), ld_argmax=argmax.stride(0),
-                      workspace=_ptr(ws), workspace_bytes=ws.numel(), device_status=_ptr(st), stream=_stream(stream))
+                      workspace=_ptr(ws), workspace_bytes=ws.numel(), device_status=_ptr(st), stream=_stream())
     args = MaxSimNamedArgs(base=base, pairs=_edges(pairs, Q.count))
     raise_for(lib.maxsim_scores_named(ctypes.byref(args)), "maxsim_scores_named")
     return dict(scores=scores, argmax=argmax, device_status=st)
@@ -567,6 +603,8 @@ def maxsim_scores_named(q_data, q_offsets, d_data, d_offsets, pairs, mean=False,
 def maxsim_backward(q_data, q_offsets, d_data, d_offsets, argmax, d_scores, mean=False, out=None, workspace=None,
                     device_status=None, stream=None):
     """Gradient through the argmax.  Returns dict(d_queries, d_documents, device_status)."""
+    if stream is not None:
+        return _on(stream, maxsim_backward, locals())
     Q, D = _tape(q_data, q_offsets), _tape(d_data, d_offsets)
     _check_cuda(argmax, "argmax", torch.int32)
     _check_cuda(d_scores, "d_scores", torch.float32)
@@ -581,7 +619,7 @@ def maxsim_backward(q_data, q_offsets, d_data, d_offsets, argmax, d_scores, mean
     args = MaxSimBackwardArgs(queries=Q, documents=D, width=width, mean=int(bool(mean)), argmax=_ptr(argmax),
                               ld_argmax=argmax.stride(0), d_scores=_ptr(d_scores), ld_d_scores=d_scores.stride(0),
                               d_queries=_ptr(dq), d_documents=_ptr(dd), workspace=_ptr(ws),
-                              workspace_bytes=ws.numel(), device_status=_ptr(st), stream=_stream(stream))
+                              workspace_bytes=ws.numel(), device_status=_ptr(st), stream=_stream())
     raise_for(lib.maxsim_backward(ctypes.byref(args)), "maxsim_backward")
     return dict(d_queries=dq, d_documents=dd, device_status=st)
 
@@ -590,6 +628,8 @@ def maxsim_backward_named(q_data, q_offsets, d_data, d_offsets, argmax, d_scores
                           device_status=None, stream=None):
     """Gradient through the argmax of the named pairs only (`pairs` as for maxsim_scores_named).  Returns
     dict(d_queries, d_documents, device_status)."""
+    if stream is not None:
+        return _on(stream, maxsim_backward_named, locals())
     Q, D = _tape(q_data, q_offsets), _tape(d_data, d_offsets)
     _check_cuda(argmax, "argmax", torch.int32)
     _check_cuda(d_scores, "d_scores", torch.float32)
@@ -602,7 +642,7 @@ def maxsim_backward_named(q_data, q_offsets, d_data, d_offsets, argmax, d_scores
     base = MaxSimBackwardArgs(queries=Q, documents=D, width=width, mean=int(bool(mean)), argmax=_ptr(argmax),
                               ld_argmax=argmax.stride(0), d_scores=_ptr(d_scores), ld_d_scores=d_scores.stride(0),
                               d_queries=_ptr(dq), d_documents=_ptr(dd), workspace=None, workspace_bytes=0,
-                              device_status=_ptr(st), stream=_stream(stream))
+                              device_status=_ptr(st), stream=_stream())
     args = MaxSimBackwardNamedArgs(base=base, pairs=_edges(pairs, Q.count))
     raise_for(lib.maxsim_backward_named(ctypes.byref(args)), "maxsim_backward_named")
     return dict(d_queries=dq, d_documents=dd, device_status=st)
@@ -634,13 +674,13 @@ _ATTENTION = {v: (_fast(v), _fast(v + "_workspace_bytes")) for v in ("cross_atte
 _NO_GRADIENTS = (0,) * 12   # d_output, d_q, d_k, d_v
 
 
-def _raw_stream(stream, tensor):
-    return (stream if stream is not None else torch.cuda.current_stream(tensor.device)).cuda_stream
+def _raw_stream(tensor):
+    return torch.cuda.current_stream(tensor.device).cuda_stream
 
 
 if hasattr(torch._C, "_cuda_getCurrentRawStream"):   # the same without building a Stream object
-    def _raw_stream(stream, tensor):   # noqa: F811
-        return torch._C._cuda_getCurrentRawStream(tensor.get_device()) if stream is None else stream.cuda_stream
+    def _raw_stream(tensor):   # noqa: F811
+        return torch._C._cuda_getCurrentRawStream(tensor.get_device())
 
 
 def _heads(t, name, shape, dtype):
@@ -700,6 +740,8 @@ def rotary_table(positions, rotary_dim, base=10000.0, scaling="plain", factor=1.
                  device="cuda", stream=None):
     """The (cos, sin) table [positions, rotary_dim / 2, 2] fp32 that the rotation verbs read.  `scaling` is 'plain',
     'linear', 'ntk' or 'yarn' for contexts `factor` times the trained one.  Returns dict(table)."""
+    if stream is not None:
+        return _on(stream, rotary_table, locals())
     if scaling not in ROTARY_SCALINGS:
         raise UnsupportedError(CLI_UNSUPPORTED, f"rotary_table: scaling {scaling!r}")
     if positions < 0 or rotary_dim < 0 or trained_positions < 0:
@@ -711,7 +753,7 @@ def rotary_table(positions, rotary_dim, base=10000.0, scaling="plain", factor=1.
     if list(t.shape) != [positions, rotary_dim // 2, 2] or not t.is_contiguous():
         raise ShapeMismatchError(CLI_SHAPE_MISMATCH, "rotary_table: table must be [positions, rotary_dim / 2, 2], packed")
     args = RotaryTableArgs(positions=positions, rotary_dim=rotary_dim, base=base, scaling=ROTARY_SCALINGS[scaling],
-                           factor=factor, trained_positions=trained_positions, table=_ptr(t), stream=_stream(stream))
+                           factor=factor, trained_positions=trained_positions, table=_ptr(t), stream=_stream())
     raise_for(lib.rotary_table(ctypes.byref(args)), "rotary_table")
     return dict(table=t)
 
@@ -729,7 +771,7 @@ def _part(name, t, positions, gain, dim, dtype):
 _NO_PART = (0,) * 17
 
 
-def _rotary_call(verb, lead, q_part, k_part, table, interleaved, epsilon, workspace, status, stream):
+def _rotary_call(verb, lead, q_part, k_part, table, interleaved, epsilon, workspace, status):
     if table.dtype is not torch.float32 or not table.is_cuda:
         _check_cuda(table, "table", torch.float32)
     shape = table.shape
@@ -738,7 +780,7 @@ def _rotary_call(verb, lead, q_part, k_part, table, interleaved, epsilon, worksp
     ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     rc = _ROTARY[verb](_pack_rotary.pack(DTYPES[lead.dtype], 1 if interleaved else 0, lead.shape[2], 2 * shape[1],
                                          table.data_ptr(), shape[0], epsilon, *q_part, *k_part, ws, ws_bytes,
-                                         status.data_ptr(), _raw_stream(stream, lead)))
+                                         status.data_ptr(), _raw_stream(lead)))
     if rc:
         raise_for(rc, verb)
 
@@ -759,22 +801,26 @@ def rotary_heads(q, table, positions=None, k=None, k_positions=None, interleaved
     """Rotates queries [rows, heads, dim] (and keys, of their own rows and heads) by their rows' positions (int32;
     None: row r is at position r), over the first 2 * table.shape[1] elements of each head.  bf16, fp16 or fp32.
     Returns dict(q, k, device_status); out['q'] may be `q` itself."""
+    if stream is not None:
+        return _on(stream, rotary_heads, locals())
     dtype, dim = q.dtype, _states(q, "q")[2]
     yq, q_part = _rotate_part(out, "q", q, positions, None, dim, dtype, False)
     yk, k_part = _rotate_part(out, "k", k, k_positions, None, dim, dtype, False)
     st = _status(device_status, q)
-    _rotary_call("rotary_heads", q, q_part, k_part, table, interleaved, 0.0, None, st, stream)
+    _rotary_call("rotary_heads", q, q_part, k_part, table, interleaved, 0.0, None, st)
     return {"q": yq, "k": yk, "device_status": st}
 
 
 def rotary_heads_backward(d_q, table, positions=None, d_k=None, k_positions=None, interleaved=False, out=None,
                           device_status=None, stream=None):
     """The gradient of rotary_heads for its inputs.  Returns dict(d_q, d_k, device_status)."""
+    if stream is not None:
+        return _on(stream, rotary_heads_backward, locals())
     dtype, dim = d_q.dtype, _states(d_q, "d_q")[2]
     xq, q_part = _rotate_part(out, "d_q", d_q, positions, None, dim, dtype, True)
     xk, k_part = _rotate_part(out, "d_k", d_k, k_positions, None, dim, dtype, True)
     st = _status(device_status, d_q)
-    _rotary_call("rotary_heads_backward", d_q, q_part, k_part, table, interleaved, 0.0, None, st, stream)
+    _rotary_call("rotary_heads_backward", d_q, q_part, k_part, table, interleaved, 0.0, None, st)
     return {"d_q": xq, "d_k": xk, "device_status": st}
 
 
@@ -782,11 +828,13 @@ def norm_rotary_heads(q, table, positions=None, q_gain=None, k=None, k_positions
                       epsilon=1e-6, out=None, device_status=None, stream=None):
     """Normalises each head, rotate(gain * x / sqrt(mean(x^2) + epsilon)), of queries and keys in one pass.  Gains
     are fp32 [dim] (None: ones); the rest as in rotary_heads.  Returns dict(q, k, device_status)."""
+    if stream is not None:
+        return _on(stream, norm_rotary_heads, locals())
     dtype, dim = q.dtype, _states(q, "q")[2]
     yq, q_part = _rotate_part(out, "q", q, positions, q_gain, dim, dtype, False)
     yk, k_part = _rotate_part(out, "k", k, k_positions, k_gain, dim, dtype, False)
     st = _status(device_status, q)
-    _rotary_call("norm_rotary_heads", q, q_part, k_part, table, interleaved, epsilon, None, st, stream)
+    _rotary_call("norm_rotary_heads", q, q_part, k_part, table, interleaved, epsilon, None, st)
     return {"q": yq, "k": yk, "device_status": st}
 
 
@@ -800,6 +848,8 @@ def norm_rotary_heads_backward(q, d_q, table, positions=None, q_gain=None, k=Non
     """The gradients of norm_rotary_heads for its inputs `q`, `k` and its gains, given those of its outputs, `d_q`
     and `d_k`.  A gain's gradient (fp32 [dim]) is None where the gain is.  Returns dict(d_q, d_q_gain, d_k,
     d_k_gain, device_status)."""
+    if stream is not None:
+        return _on(stream, norm_rotary_heads_backward, locals())
     if (k is None) != (d_k is None):
         raise InvalidArgumentError(CLI_INVALID_ARGUMENT, "norm_rotary_heads_backward: k and d_k go together")
     dtype, dim = q.dtype, _states(q, "q")[2]
@@ -808,7 +858,7 @@ def norm_rotary_heads_backward(q, d_q, table, positions=None, q_gain=None, k=Non
     st = _status(device_status, q)
     if workspace is None and (gq is not None or gk is not None):
         workspace = _ws(lib.norm_rotary_heads_backward_workspace_bytes(dim), q.device)
-    _rotary_call("norm_rotary_heads_backward", q, q_part, k_part, table, interleaved, epsilon, workspace, st, stream)
+    _rotary_call("norm_rotary_heads_backward", q, q_part, k_part, table, interleaved, epsilon, workspace, st)
     return {"d_q": xq, "d_q_gain": gq, "d_k": xk, "d_k_gain": gk, "device_status": st}
 
 
@@ -854,10 +904,10 @@ def _attention_sizes(q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_r
             *_heads(k, "k", k_shape, dtype), *_heads(v, "v", k_shape, dtype)), items
 
 
-def _attention_call(verb, head, tail, workspace, like, status, stream):
+def _attention_call(verb, head, tail, workspace, like, status):
     call, workspace_bytes = _ATTENTION[verb]
     ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    last = status.data_ptr(), _raw_stream(stream, like)
+    last = status.data_ptr(), _raw_stream(like)
     args = _pack_attention.pack(*head, *tail, ws, ws_bytes, *last)
     if workspace is None:
         need = workspace_bytes(args)
@@ -896,6 +946,8 @@ def cross_attention(q, q_offsets, k, v, k_offsets, key_mask=None, scale=None, ma
     the outputs have items * rows rows.  `key_mask` (uint8 or bool [states]) drops states where it is 0; `scale`
     defaults to dim^-0.5; the two maxima bound the items' rows (default: the tapes').  bf16 or fp16.  Returns
     dict(output, lse, device_status), lse fp32 [output rows, heads] or None."""
+    if stream is not None:
+        return _on(stream, cross_attention, locals())
     head, items = _attention_sizes(q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_rows, max_key_rows)
     rows_q, hq, dim = q.shape
     shape = (rows_q if q_offsets is not None else rows_q * items, hq, dim)
@@ -909,7 +961,7 @@ def cross_attention(q, q_offsets, k, v, k_offsets, key_mask=None, scale=None, ma
         else:
             lse_ptr = _lse_ptr(lse, *shape[:2])
     st = _status(device_status, q)
-    _attention_call("cross_attention", head, (*made, lse_ptr, *_NO_GRADIENTS), workspace, q, st, stream)
+    _attention_call("cross_attention", head, (*made, lse_ptr, *_NO_GRADIENTS), workspace, q, st)
     return {"output": o, "lse": lse, "device_status": st}
 
 
@@ -918,6 +970,8 @@ def cross_attention_backward(q, q_offsets, k, v, k_offsets, output, lse, d_outpu
                              stream=None):
     """The gradients of cross_attention for `q`, `k` and `v`, given its `output` and `lse` and the output's gradient;
     the rest as there.  Returns dict(d_q, d_k, d_v, device_status)."""
+    if stream is not None:
+        return _on(stream, cross_attention_backward, locals())
     head, items = _attention_sizes(q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_rows, max_key_rows)
     (rows_q, hq, dim), dtype = q.shape, q.dtype
     shape = (rows_q if q_offsets is not None else rows_q * items, hq, dim)
@@ -926,5 +980,5 @@ def cross_attention_backward(q, q_offsets, k, v, k_offsets, output, lse, d_outpu
     st = _status(device_status, q)
     tail = (*_heads(output, "output", shape, dtype), _lse_ptr(lse, *shape[:2]),
             *_heads(d_output, "d_output", shape, dtype), *q_made, *k_made, *v_made)
-    _attention_call("cross_attention_backward", head, tail, workspace, q, st, stream)
+    _attention_call("cross_attention_backward", head, tail, workspace, q, st)
     return {"d_q": dq, "d_k": dk, "d_v": dv, "device_status": st}
