@@ -300,6 +300,25 @@ def _ws(nbytes, device):
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
+def _lent(workspace):
+    """(address, bytes) of a lent workspace; (0, 0) for None."""
+    if workspace is None:
+        return 0, 0
+    _check_cuda(workspace, "workspace")
+    if not workspace.is_contiguous():
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, "workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _check_lent(out, workspace, device_status):
+    """What a caller lends a verb to write: device memory."""
+    for name, t in (out or {}).items():
+        if isinstance(t, torch.Tensor):
+            _check_cuda(t, "out " + name)
+    _check_cuda(device_status, "device_status", torch.int32)
+    _lent(workspace)
+
+
 def _on(stream, verb, arguments):
     """verb(**arguments) with `stream` as the current stream.  What the verb allocates or fills comes from that
     stream's pool, in its order: a workspace that the verb drops is not handed to the caller's stream while kernels
@@ -361,6 +380,7 @@ def pair_loss_sigmoid_fwd_bwd(embeddings, inverse_temperature, bias, attract, re
     width = (out or {}).get("width", ld)
     dev = embeddings.device
     out = dict(out or {})
+    _check_lent(out, workspace, device_status)
     loss = out.get("loss") if out.get("loss") is not None else torch.empty(1, device=dev)
     de = out.get("d_embeddings") if out.get("d_embeddings") is not None else torch.empty(n, width, device=dev)
     dt = out.get("d_inverse_temperature") if out.get("d_inverse_temperature") is not None else torch.empty(1, device=dev)
@@ -375,7 +395,7 @@ def pair_loss_sigmoid_fwd_bwd(embeddings, inverse_temperature, bias, attract, re
         inverse_temperature=_ptr(inverse_temperature), bias=_ptr(bias),
         relations=Relations(A, R, I, int(bool(negatives_named)), float(ambient_weight)),
         loss=_ptr(loss), d_embeddings=_ptr(de), ld_d_embeddings=de.stride(0),
-        d_inverse_temperature=_ptr(dt), d_bias=_ptr(db), workspace=_ptr(ws), workspace_bytes=ws.numel(),
+        d_inverse_temperature=_ptr(dt), d_bias=_ptr(db), workspace=_ptr(ws), workspace_bytes=_lent(ws)[1],
         device_status=_ptr(st), stream=_stream(), **_band(band))
     raise_for(lib.pair_loss_sigmoid_fwd_bwd(ctypes.byref(args)), "pair_loss_sigmoid_fwd_bwd")
     return dict(loss=loss, d_embeddings=de, d_inverse_temperature=dt, d_bias=db, device_status=st)
@@ -400,6 +420,7 @@ def pair_loss_sigmoid_groups_fwd_bwd(embeddings, groups, inverse_temperature, bi
     width = (out or {}).get("width", ld)
     dev = embeddings.device
     out = dict(out or {})
+    _check_lent(out, workspace, device_status)
     loss = out.get("loss") if out.get("loss") is not None else torch.empty(1, device=dev)
     de = out.get("d_embeddings") if out.get("d_embeddings") is not None else torch.empty(n, width, device=dev)
     dt = out.get("d_inverse_temperature") if out.get("d_inverse_temperature") is not None else torch.empty(g, device=dev)
@@ -414,7 +435,7 @@ def pair_loss_sigmoid_groups_fwd_bwd(embeddings, groups, inverse_temperature, bi
         inverse_temperature=_ptr(inverse_temperature), bias=_ptr(bias),
         relations=Relations(A, R, I, int(bool(negatives_named)), float(ambient_weight)),
         loss=_ptr(loss), d_embeddings=_ptr(de), ld_d_embeddings=de.stride(0),
-        d_inverse_temperature=_ptr(dt), d_bias=_ptr(db), workspace=_ptr(ws), workspace_bytes=ws.numel(),
+        d_inverse_temperature=_ptr(dt), d_bias=_ptr(db), workspace=_ptr(ws), workspace_bytes=_lent(ws)[1],
         device_status=_ptr(st), stream=_stream(), **_band(band))
     args = PairLossGroupsArgs(base=base, groups=_ptr(groups), group_count=g)
     raise_for(lib.pair_loss_sigmoid_groups_fwd_bwd(ctypes.byref(args)), "pair_loss_sigmoid_groups_fwd_bwd")
@@ -440,6 +461,7 @@ def pair_loss_sigmoid_matryoshka_fwd_bwd(embeddings, prefix_widths, inverse_temp
     width = (out or {}).get("width", ld)
     dev = embeddings.device
     out = dict(out or {})
+    _check_lent(out, workspace, device_status)
     widths = (c_size_t * len(prefix_widths))(*[int(p) for p in prefix_widths])
     loss = out.get("loss") if out.get("loss") is not None else torch.empty(1, device=dev)
     de = out.get("d_embeddings") if out.get("d_embeddings") is not None else torch.empty(n, width, device=dev)
@@ -457,7 +479,7 @@ def pair_loss_sigmoid_matryoshka_fwd_bwd(embeddings, prefix_widths, inverse_temp
         inverse_temperature=_ptr(inverse_temperature), bias=_ptr(bias),
         relations=Relations(A, R, I, int(bool(negatives_named)), float(ambient_weight)),
         loss=_ptr(loss), d_embeddings=_ptr(de), ld_d_embeddings=de.stride(0),
-        d_inverse_temperature=_ptr(dt), d_bias=_ptr(db), workspace=_ptr(ws), workspace_bytes=ws.numel(),
+        d_inverse_temperature=_ptr(dt), d_bias=_ptr(db), workspace=_ptr(ws), workspace_bytes=_lent(ws)[1],
         device_status=_ptr(st), stream=_stream(), **_band(band))
     args = PairLossMatryoshkaArgs(base=base, prefix_widths=ctypes.cast(widths, c_void_p),
                                   prefix_count=len(prefix_widths), prefix_loss=_ptr(pl))
@@ -480,6 +502,7 @@ def pair_loss_sigmoid_scores_fwd_bwd(scores, inverse_temperature, bias, attract,
     rows, cols = scores.shape
     dev = scores.device
     out = dict(out or {})
+    _check_lent(out, workspace, device_status)
     loss = out.get("loss") if out.get("loss") is not None else torch.empty(1, device=dev)
     ds = out.get("d_scores") if out.get("d_scores") is not None else torch.empty(rows, cols, device=dev)
     dt = out.get("d_inverse_temperature") if out.get("d_inverse_temperature") is not None else torch.empty(1, device=dev)
@@ -491,7 +514,7 @@ def pair_loss_sigmoid_scores_fwd_bwd(scores, inverse_temperature, bias, attract,
         rows=rows, cols=cols, ld=scores.stride(0), scores=_ptr(scores), inverse_temperature=_ptr(inverse_temperature),
         bias=_ptr(bias), relations=Relations(A, R, I, int(bool(negatives_named)), float(ambient_weight)),
         sides=_ptr(sides), loss=_ptr(loss), d_scores=_ptr(ds), ld_d_scores=ds.stride(0),
-        d_inverse_temperature=_ptr(dt), d_bias=_ptr(db), workspace=_ptr(ws), workspace_bytes=ws.numel(),
+        d_inverse_temperature=_ptr(dt), d_bias=_ptr(db), workspace=_ptr(ws), workspace_bytes=_lent(ws)[1],
         device_status=_ptr(st), stream=_stream())
     raise_for(lib.pair_loss_sigmoid_scores_fwd_bwd(ctypes.byref(args)), "pair_loss_sigmoid_scores_fwd_bwd")
     return dict(loss=loss, d_scores=ds, d_inverse_temperature=dt, d_bias=db, device_status=st)
@@ -512,6 +535,7 @@ def pair_loss_scores_fwd_bwd(form, scores, inverse_temperature, bias, attract, r
     rows, cols = scores.shape
     dev = scores.device
     out = dict(out or {})
+    _check_lent(out, workspace, device_status)
     loss = out.get("loss") if out.get("loss") is not None else torch.empty(1, device=dev)
     ds = out.get("d_scores") if out.get("d_scores") is not None else torch.empty(rows, cols, device=dev)
     dt = out.get("d_inverse_temperature") if out.get("d_inverse_temperature") is not None else torch.empty(1, device=dev)
@@ -523,7 +547,7 @@ def pair_loss_scores_fwd_bwd(form, scores, inverse_temperature, bias, attract, r
         rows=rows, cols=cols, ld=scores.stride(0), scores=_ptr(scores), inverse_temperature=_ptr(inverse_temperature),
         bias=_ptr(bias), relations=Relations(A, R, I, int(bool(negatives_named)), float(ambient_weight)),
         sides=_ptr(sides), loss=_ptr(loss), d_scores=_ptr(ds), ld_d_scores=ds.stride(0),
-        d_inverse_temperature=_ptr(dt), d_bias=_ptr(db), workspace=_ptr(ws), workspace_bytes=ws.numel(),
+        d_inverse_temperature=_ptr(dt), d_bias=_ptr(db), workspace=_ptr(ws), workspace_bytes=_lent(ws)[1],
         device_status=_ptr(st), stream=_stream())
     args = PairLossScoresArgs(form=FORMS[form], args=inner)
     raise_for(lib.pair_loss_scores_fwd_bwd(ctypes.byref(args)), "pair_loss_scores_fwd_bwd")
@@ -556,6 +580,7 @@ def maxsim_scores(q_data, q_offsets, d_data, d_offsets, mean=False, out=None, wo
         raise ShapeMismatchError(CLI_SHAPE_MISMATCH, "maxsim_scores: query and document widths differ")
     dev = q_data.device
     out = dict(out or {})
+    _check_lent(out, workspace, device_status)
     scores = out.get("scores") if out.get("scores") is not None else torch.empty(Q.count, D.count, device=dev)
     argmax = out.get("argmax") if out.get("argmax") is not None else torch.empty(D.count, Q.rows, dtype=torch.int32,
                                                                                   device=dev)
@@ -564,7 +589,7 @@ def maxsim_scores(q_data, q_offsets, d_data, d_offsets, mean=False, out=None, wo
                                                      dev)
     args = MaxSimArgs(queries=Q, documents=D, width=width, mean=int(bool(mean)), scores=_ptr(scores),
                       ld_scores=scores.stride(0), argmax=_ptr(argmax), ld_argmax=argmax.stride(0),
-                      workspace=_ptr(ws), workspace_bytes=ws.numel(), device_status=_ptr(st), stream=_stream())
+                      workspace=_ptr(ws), workspace_bytes=_lent(ws)[1], device_status=_ptr(st), stream=_stream())
     raise_for(lib.maxsim_scores(ctypes.byref(args)), "maxsim_scores")
     return dict(scores=scores, argmax=argmax, device_status=st)
 
@@ -586,6 +611,7 @@ def maxsim_scores_named(q_data, q_offsets, d_data, d_offsets, pairs, mean=False,
         raise ShapeMismatchError(CLI_SHAPE_MISMATCH, "maxsim_scores_named: query and document widths differ")
     dev = q_data.device
     out = dict(out or {})
+    _check_lent(out, workspace, device_status)
     scores = out.get("scores") if out.get("scores") is not None else torch.empty(Q.count, D.count, device=dev)
     argmax = out.get("argmax") if out.get("argmax") is not None else torch.empty(D.count, Q.rows, dtype=torch.int32,
                                                                                   device=dev)
@@ -594,7 +620,7 @@ def maxsim_scores_named(q_data, q_offsets, d_data, d_offsets, pairs, mean=False,
         maxsim_named_workspace_bytes(Q.count, D.count, Q.rows, D.rows, width), dev)
     base = MaxSimArgs(queries=Q, documents=D, width=width, mean=int(bool(mean)), scores=_ptr(scores),
                       ld_scores=scores.stride(0), argmax=_ptr(argmax), ld_argmax=argmax.stride(0),
-                      workspace=_ptr(ws), workspace_bytes=ws.numel(), device_status=_ptr(st), stream=_stream())
+                      workspace=_ptr(ws), workspace_bytes=_lent(ws)[1], device_status=_ptr(st), stream=_stream())
     args = MaxSimNamedArgs(base=base, pairs=_edges(pairs, Q.count))
     raise_for(lib.maxsim_scores_named(ctypes.byref(args)), "maxsim_scores_named")
     return dict(scores=scores, argmax=argmax, device_status=st)
@@ -611,6 +637,7 @@ def maxsim_backward(q_data, q_offsets, d_data, d_offsets, argmax, d_scores, mean
     width = q_data.shape[1]
     dev = q_data.device
     out = dict(out or {})
+    _check_lent(out, workspace, device_status)
     dq = out.get("d_queries") if out.get("d_queries") is not None else torch.empty(Q.rows, width, device=dev)
     dd = out.get("d_documents") if out.get("d_documents") is not None else torch.empty(D.rows, width, device=dev)
     st = device_status if device_status is not None else torch.zeros(1, dtype=torch.int32, device=dev)
@@ -619,7 +646,7 @@ def maxsim_backward(q_data, q_offsets, d_data, d_offsets, argmax, d_scores, mean
     args = MaxSimBackwardArgs(queries=Q, documents=D, width=width, mean=int(bool(mean)), argmax=_ptr(argmax),
                               ld_argmax=argmax.stride(0), d_scores=_ptr(d_scores), ld_d_scores=d_scores.stride(0),
                               d_queries=_ptr(dq), d_documents=_ptr(dd), workspace=_ptr(ws),
-                              workspace_bytes=ws.numel(), device_status=_ptr(st), stream=_stream())
+                              workspace_bytes=_lent(ws)[1], device_status=_ptr(st), stream=_stream())
     raise_for(lib.maxsim_backward(ctypes.byref(args)), "maxsim_backward")
     return dict(d_queries=dq, d_documents=dd, device_status=st)
 
@@ -636,6 +663,7 @@ def maxsim_backward_named(q_data, q_offsets, d_data, d_offsets, argmax, d_scores
     width = q_data.shape[1]
     dev = q_data.device
     out = dict(out or {})
+    _check_lent(out, None, device_status)
     dq = out.get("d_queries") if out.get("d_queries") is not None else torch.empty(Q.rows, width, device=dev)
     dd = out.get("d_documents") if out.get("d_documents") is not None else torch.empty(D.rows, width, device=dev)
     st = device_status if device_status is not None else torch.zeros(1, dtype=torch.int32, device=dev)
@@ -777,7 +805,7 @@ def _rotary_call(verb, lead, q_part, k_part, table, interleaved, epsilon, worksp
     shape = table.shape
     if len(shape) != 3 or shape[2] != 2 or not table.is_contiguous():
         raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: table must be [positions, rotary_dim / 2, 2], packed")
-    ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    ws, ws_bytes = _lent(workspace)
     rc = _ROTARY[verb](_pack_rotary.pack(DTYPES[lead.dtype], 1 if interleaved else 0, lead.shape[2], 2 * shape[1],
                                          table.data_ptr(), shape[0], epsilon, *q_part, *k_part, ws, ws_bytes,
                                          status.data_ptr(), _raw_stream(lead)))
@@ -906,7 +934,7 @@ def _attention_sizes(q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_r
 
 def _attention_call(verb, head, tail, workspace, like, status):
     call, workspace_bytes = _ATTENTION[verb]
-    ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    ws, ws_bytes = _lent(workspace)
     last = status.data_ptr(), _raw_stream(like)
     args = _pack_attention.pack(*head, *tail, ws, ws_bytes, *last)
     if workspace is None:

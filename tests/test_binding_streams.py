@@ -1,4 +1,4 @@
-"""Where the binding's memory comes from when a verb is given a stream: no GPU, with a stand-in for the library, the
+"""What the binding does with streams, and with buffers that are lent to it: no GPU, with a stand-in for the library, the
 streams and the allocator that notes which stream was current."""
 
 import contextlib
@@ -57,6 +57,8 @@ def box(monkeypatch):
             def call(*args):
                 if name.endswith("_workspace_bytes"):
                     return 4096
+                if name == "cli_status_name":
+                    return b"refused"
                 a = args[0]._obj if hasattr(args[0], "_obj") else None
                 while a is not None and not hasattr(a, "stream"):
                     a = getattr(a, "base", None) or a.args
@@ -140,3 +142,37 @@ def test_memory_of_a_call_without_a_stream_is_the_current_ones(box):
         getattr(box.b, name)(*c.get("a", ()), **c.get("k", {}))
         assert box.launched == [11], name
         assert box.made and all(s is box.caller for s, _ in box.made), name
+
+
+def test_lent_buffers_are_device_memory(box):
+    """A workspace, a status or an output in host memory, or a workspace with gaps, is refused before the launch."""
+    b = box.b
+    host, gaps = torch.ones(8192, dtype=torch.uint8), tensor(16384, dtype=torch.uint8)[::2]
+    for name, c in calls(b).items():
+        takes = inspect.signature(getattr(b, name)).parameters
+        call = lambda **kw: getattr(b, name)(*c.get("a", ()), **c.get("k", {}), **kw)  # noqa: E731
+        box.launched.clear()
+        if "workspace" in takes:
+            with pytest.raises(b.InvalidArgumentError, match="workspace"):
+                call(workspace=host)
+            with pytest.raises(b.ShapeMismatchError, match="workspace"):
+                call(workspace=gaps)
+        if "device_status" in takes:
+            with pytest.raises(b.InvalidArgumentError, match="device_status"):
+                call(device_status=torch.ones(1, dtype=torch.int32))
+        if "out" in takes:
+            for key, t in call().items():
+                if t is not None and key != "device_status":
+                    with pytest.raises(b.InvalidArgumentError):
+                        call(out={key: torch.ones(*t.shape, dtype=t.dtype)})
+            box.launched.clear()
+        assert not box.launched, name
+
+
+def test_a_lent_workspace_counts_in_bytes(box):
+    b = box.b
+    q, off = tensor(4, 2, 8, dtype=BF16), tensor(3, dtype=I64)
+    seen = []
+    b._ATTENTION["cross_attention"] = (lambda a: seen.append(int.from_bytes(a[-24:-16], "little")) or 0, lambda a: 0)
+    b.cross_attention(q, off, q, q, off, workspace=tensor(512))
+    assert seen == [2048]
