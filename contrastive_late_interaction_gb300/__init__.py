@@ -24,6 +24,5 @@ _BINDING_NAMES = {
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import _binding
-        value = globals()[name] = getattr(_binding, name)   # the next look-up finds it without this function
-        return value
+        return getattr(_binding, name)
     raise AttributeError(name)

@@ -176,3 +176,12 @@ def test_a_lent_workspace_counts_in_bytes(box):
     b._ATTENTION["cross_attention"] = (lambda a: seen.append(int.from_bytes(a[-24:-16], "little")) or 0, lambda a: 0)
     b.cross_attention(q, off, q, q, off, workspace=tensor(512))
     assert seen == [2048]
+
+
+def test_the_packages_names_follow_the_binding(box, monkeypatch):
+    """A name replaced in the binding is the package's too, whether it was looked up before or not."""
+    import contrastive_late_interaction_gb300 as cli
+    assert cli.rotary_table is box.b.rotary_table
+    other = lambda *a: None  # noqa: E731
+    monkeypatch.setattr(box.b, "rotary_table", other)
+    assert cli.rotary_table is other
