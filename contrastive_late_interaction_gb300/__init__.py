@@ -23,6 +23,8 @@ _BINDING_NAMES = {
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
-        from . import _binding
-        return getattr(_binding, name)
+        binding = globals().get("_binding")   # there once it has been imported
+        if binding is None:
+            from . import _binding as binding
+        return getattr(binding, name)
     raise AttributeError(name)
