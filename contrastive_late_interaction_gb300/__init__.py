@@ -6,6 +6,9 @@ The compute path is the CUDA library built from `csrc/` (C ABI in `include/cli.h
 so `synth` imports without a built library.
 """
 
+import sys
+import types
+
 _BINDING_NAMES = {
     "CliError", "DeviceError", "InternalError", "InvalidArgumentError", "MalformedError", "ShapeMismatchError",
     "UnsupportedError", "check_device_status", "device_edges", "maxsim_backward", "maxsim_backward_workspace_bytes",
@@ -21,10 +24,21 @@ _BINDING_NAMES = {
 }
 
 
-def __getattr__(name):
-    if name in _BINDING_NAMES:
-        binding = globals().get("_binding")   # there once it has been imported
+class _Name:
+    """A name of the binding, looked up there each time: cheaper than a module's __getattr__, and a name that is set on the
+    package itself still comes first."""
+
+    def __init__(self, name):
+        self.name = name
+
+    def __get__(self, module, kind=None):
+        binding = _loaded.get("binding")
         if binding is None:
             from . import _binding as binding
-        return getattr(binding, name)
-    raise AttributeError(name)
+            _loaded["binding"] = binding
+        return getattr(binding, self.name)
+
+
+_loaded = {}
+_Package = type("_Package", (types.ModuleType,), {name: _Name(name) for name in _BINDING_NAMES})
+sys.modules[__name__].__class__ = _Package
