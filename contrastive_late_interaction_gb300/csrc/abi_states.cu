@@ -190,7 +190,7 @@ cli_status_t rotary_call(const cli_rotary_t *a, bool norm, bool backward) {
 }
 
 // The sizes of an attention call, checked; `L` receives them.
-cli_status_t attention_sizes(const cli_attention_t *a, AttentionLaunch &L) {
+cli_status_t attention_sizes(const cli_attention_t *a, bool backward, AttentionLaunch &L) {
     if (a->dtype != CLI_BF16 && a->dtype != CLI_F16) return CLI_UNSUPPORTED;
     if (a->items == 0 || a->items >= kRowsLimit || a->query_rows >= kTapeLimit || a->key_rows >= kTapeLimit)
         return CLI_SHAPE_MISMATCH;
@@ -215,13 +215,13 @@ cli_status_t attention_sizes(const cli_attention_t *a, AttentionLaunch &L) {
     L.key_heads = static_cast<int>(a->key_heads);
     L.group = L.query_heads / L.key_heads;
     L.head_dim = static_cast<int>(a->head_dim);
-    return CLI_OK;
+    return attention_grids_fit(L, backward) ? CLI_OK : CLI_SHAPE_MISMATCH;
 }
 
 cli_status_t attention_call(const cli_attention_t *a, bool backward) {
     if (!a) return CLI_INVALID_ARGUMENT;
     AttentionLaunch L = {};
-    cli_status_t st = attention_sizes(a, L);
+    cli_status_t st = attention_sizes(a, backward, L);
     if (st != CLI_OK) return st;
     if (!a->key_offsets || !a->device_status || !std::isfinite(a->scale)) return CLI_INVALID_ARGUMENT;
     if (!aligned(a->key_offsets, 8) || !aligned(a->query_offsets, 8) || !aligned(a->device_status, 4) ||
@@ -299,7 +299,7 @@ cli_status_t attention_call(const cli_attention_t *a, bool backward) {
 size_t attention_bytes(const cli_attention_t *a, bool backward) {
     if (!a) return 0;
     AttentionLaunch L = {};
-    if (attention_sizes(a, L) != CLI_OK) return 0;
+    if (attention_sizes(a, backward, L) != CLI_OK) return 0;
     return backward ? attention_backward_workspace(L) : attention_workspace(L);
 }
 

@@ -803,6 +803,10 @@ Cut cut_of(const AttentionLaunch &L) {
     return c;
 }
 
+long long joins_of(const AttentionLaunch &L) {
+    return (static_cast<long long>(L.query_rows) * L.query_heads * L.head_dim + kSumElems - 1) / kSumElems;
+}
+
 template <typename T, int BOXES>
 cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
     const int rows_per_tile = 128 / L.group;
@@ -840,14 +844,13 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
     e = launch_after(dq, dim3(grid(q_tiles)), kThreads, smem, stream, L, M, rows_per_tile, out_rows, stats, partials, q_tiles,
                      c.split, counters + 1);
     if (e != cudaSuccess) return e;
-    if (partials) {
-        const long long all = static_cast<long long>(L.query_rows) * L.query_heads * L.head_dim;
-        dq_sum_kernel<T><<<static_cast<unsigned>((all + kSumElems - 1) / kSumElems), 256, 0, stream>>>(L, c.sums, partials);
-    }
+    if (partials) dq_sum_kernel<T><<<static_cast<unsigned>(joins_of(L)), 256, 0, stream>>>(L, c.sums, partials);
     return cudaGetLastError();
 }
 
 }  // namespace
+
+long long backward_tiles_joins(const AttentionLaunch &L) { return L.q_off && cut_of(L).sums == 1 ? 0 : joins_of(L); }
 
 size_t backward_tiles_workspace(const AttentionLaunch &L) {
     const Cut c = cut_of(L);

@@ -538,6 +538,8 @@ size_t part_bytes(const AttentionLaunch &L, const Cut &c) {
     return align256(static_cast<size_t>(c.split.parts) * output_rows(L) * L.query_heads * L.head_dim * sizeof(float));
 }
 
+long long joins_of(const AttentionLaunch &L) { return (static_cast<long long>(output_rows(L)) * L.query_heads + 7) / 8; }
+
 template <typename T, int BOXES, int TILES, bool CUT>
 cudaError_t launch(const AttentionLaunch &L, const Cut &c, cudaStream_t stream) {
     const int rows_per_tile = 128 / L.group, out_rows = output_rows(L);
@@ -560,8 +562,7 @@ cudaError_t launch(const AttentionLaunch &L, const Cut &c, cudaStream_t stream) 
     e = launch_after(kernel, dim3(static_cast<unsigned>(tiles < ctas ? tiles : ctas)), 128 + 128 * TILES, smem, stream, L, M,
                      rows_per_tile, tiles, counters, c.split, out_rows, part_o, part_ml);
     if (e != cudaSuccess || !CUT) return e;
-    const long long cells = static_cast<long long>(out_rows) * L.query_heads;
-    return launch_after(join_parts_kernel<T>, dim3(static_cast<unsigned>((cells + 7) / 8)), 256, 0, stream, L, c.split.parts,
+    return launch_after(join_parts_kernel<T>, dim3(static_cast<unsigned>(joins_of(L))), 256, 0, stream, L, c.split.parts,
                         out_rows, part_o, part_ml);
 }
 
@@ -578,6 +579,8 @@ cudaError_t dispatch(const AttentionLaunch &L, cudaStream_t stream) {
 }
 
 }  // namespace
+
+long long forward_tiles_joins(const AttentionLaunch &L) { return cut_of(L).split.parts == 1 ? 0 : joins_of(L); }
 
 size_t forward_tiles_workspace(const AttentionLaunch &L) {
     const Cut c = cut_of(L);

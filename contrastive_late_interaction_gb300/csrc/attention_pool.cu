@@ -866,7 +866,22 @@ size_t part_bytes(const AttentionLaunch &L, long long slots, const Cut &c) {
     return align256(static_cast<size_t>(slots) * L.key_heads * c.rows * L.head_dim * sizeof(float));
 }
 
-unsigned blocks_of(long long n, int per) { return static_cast<unsigned>((n + per - 1) / per); }
+// A call's two grids: the pass over the states, and what joins its parts (and
+// mends, in the backward).  Items times heads pass 32 bits.
+struct Grids {
+    long long first, joins, mends;
+    bool wide;   // eight warps a row join
+};
+Grids grids_of(const AttentionLaunch &L, const Cut &c, bool back) {
+    const long long of_rows = L.q_off || !back ? L.items : 1, rows = of_rows * L.key_heads * c.rows;
+    const int warps = back && c.rows > 8 ? kWarps / 2 : kWarps;
+    Grids g;
+    g.first = ((back ? c.workers : c.slots) * L.key_heads + warps - 1) / warps;
+    g.wide = (back && !L.q_off) || wide_join(L, c, rows);
+    g.joins = !back && c.chunk >= L.max_k ? 0 : g.wide ? rows : (rows + 7) / 8;
+    g.mends = back ? (c.slots * L.key_heads + 7) / 8 : 0;
+    return g;
+}
 
 template <typename T, int DP, int NT>
 cudaError_t forward(const AttentionLaunch &L, cudaStream_t stream) {
@@ -874,12 +889,12 @@ cudaError_t forward(const AttentionLaunch &L, cudaStream_t stream) {
     const bool split = c.chunk < L.max_k;
     float *part_o = split ? reinterpret_cast<float *>(L.workspace) : nullptr;
     float2 *part_ml = split ? reinterpret_cast<float2 *>(L.workspace + part_bytes(L, c.slots, c)) : nullptr;
-    forward_kernel<T, DP, NT><<<blocks_of(c.slots * L.key_heads, kWarps), kWarps * 32, 0, stream>>>(L, c.chunk, c.slots, part_o, part_ml);
+    const Grids g = grids_of(L, c, false);
+    forward_kernel<T, DP, NT><<<static_cast<unsigned>(g.first), kWarps * 32, 0, stream>>>(L, c.chunk, c.slots, part_o, part_ml);
     if (!split) return cudaGetLastError();
-    const long long rows = L.items * L.key_heads * c.rows;
-    if (wide_join(L, c, rows))
-        return launch_after(join_kernel<T, 8>, dim3(static_cast<unsigned>(rows)), 256, 0, stream, L, c.chunk, part_o, part_ml);
-    return launch_after(join_kernel<T, 1>, dim3(blocks_of(rows, 8)), 256, 0, stream, L, c.chunk, part_o, part_ml);
+    const dim3 joins(static_cast<unsigned>(g.joins));
+    if (g.wide) return launch_after(join_kernel<T, 8>, joins, 256, 0, stream, L, c.chunk, part_o, part_ml);
+    return launch_after(join_kernel<T, 1>, joins, 256, 0, stream, L, c.chunk, part_o, part_ml);
 }
 
 // The backward's workspace: dQ's parts, then the notes.
@@ -899,15 +914,14 @@ cudaError_t backward(const AttentionLaunch &L, cudaStream_t stream) {
     notes.sums = reinterpret_cast<float *>(at);
     notes.steps = reinterpret_cast<uint32_t *>(at + notes_sums_bytes(L, c));
     notes.states = reinterpret_cast<uint32_t *>(at + notes_sums_bytes(L, c) + notes_steps_bytes(L, c));
-    backward_kernel<T, DP, NT><<<blocks_of(c.workers * L.key_heads, kWarps / NT), kWarps / NT * 32, 0, stream>>>(
-        L, c.chunk, c.slots, c.workers, part_dq, notes);
-    const long long rows = (L.q_off ? static_cast<long long>(L.items) : 1) * L.key_heads * c.rows;
-    const unsigned mends = blocks_of(c.slots * L.key_heads, 8);
-    if (!L.q_off || wide_join(L, c, rows))
-        return launch_after(finish_kernel<T, 8>, dim3(static_cast<unsigned>(rows) + mends), 256, 0, stream, L, c.chunk, c.slots,
-                            c.workers, static_cast<unsigned>(rows), part_dq, notes);
-    return launch_after(finish_kernel<T, 1>, dim3(blocks_of(rows, 8) + mends), 256, 0, stream, L, c.chunk, c.slots, c.workers,
-                        blocks_of(rows, 8), part_dq, notes);
+    const Grids g = grids_of(L, c, true);
+    backward_kernel<T, DP, NT><<<static_cast<unsigned>(g.first), kWarps / NT * 32, 0, stream>>>(L, c.chunk, c.slots, c.workers,
+                                                                                               part_dq, notes);
+    const dim3 grid(static_cast<unsigned>(g.joins + g.mends));
+    const unsigned joins = static_cast<unsigned>(g.joins);
+    if (g.wide)
+        return launch_after(finish_kernel<T, 8>, grid, 256, 0, stream, L, c.chunk, c.slots, c.workers, joins, part_dq, notes);
+    return launch_after(finish_kernel<T, 1>, grid, 256, 0, stream, L, c.chunk, c.slots, c.workers, joins, part_dq, notes);
 }
 
 template <typename T>
@@ -935,6 +949,15 @@ bool few_rows(const AttentionLaunch &L, bool back) {
 
 }  // namespace
 }  // namespace attn
+
+bool attention_grids_fit(const AttentionLaunch &L, bool back) {
+    using namespace attn;
+    constexpr long long kMost = (1ll << 31) - 1;
+    if (!L.query_rows || !L.key_rows) return true;   // a grid of their own size
+    if (!few_rows(L, back)) return (back ? backward_tiles_joins(L) : forward_tiles_joins(L)) <= kMost;
+    const Grids g = grids_of(L, cut_of(L), back);
+    return g.first <= kMost && g.joins + g.mends <= kMost;
+}
 
 size_t attention_workspace(const AttentionLaunch &L) {
     using namespace attn;

@@ -243,13 +243,17 @@ struct AttentionLaunch {
     int sm_count;
 };
 
+// False where a kernel of the call would need more blocks than a grid has.
+bool attention_grids_fit(const AttentionLaunch &L, bool backward);
 size_t attention_workspace(const AttentionLaunch &L);
 size_t attention_backward_workspace(const AttentionLaunch &L);
 namespace attn {
 cudaError_t launch_forward_tiles(const AttentionLaunch &L, cudaStream_t stream);
 size_t forward_tiles_workspace(const AttentionLaunch &L);
+long long forward_tiles_joins(const AttentionLaunch &L);   // blocks of the grid that depends on the call's size
 cudaError_t launch_backward_tiles(const AttentionLaunch &L, cudaStream_t stream);
 size_t backward_tiles_workspace(const AttentionLaunch &L);
+long long backward_tiles_joins(const AttentionLaunch &L);
 }
 cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t stream);
 cudaError_t launch_attention_backward(const AttentionLaunch &L, cudaStream_t stream);

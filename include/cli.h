@@ -596,7 +596,8 @@ size_t norm_rotary_heads_backward_workspace_bytes(size_t head_dim);
  *   head_dim         a multiple of 8, 8 .. 128
  *   query_heads      a multiple of key_heads, at most 128 times it; both
  *                    1 .. 65535
- *   items            1 .. 2^31 - 1
+ *   items            1 .. 2^31 - 1; a call whose items times heads would need more
+ *                    than 2^31 - 1 blocks is refused (CLI_SHAPE_MISMATCH)
  *   query_rows, key_rows   rows of the tapes, < 2^31 - 4096 (key_rows may be 0, as may
  *                    query_rows); outputs' rows < 2^31 too
  *   query_offsets, key_offsets   device uint64 [items + 1]; malformed ones set
