@@ -83,6 +83,14 @@ bool same_place(const Heads &a, const Heads &b) {
     return a.at == b.at && a.row == b.row && a.head == b.head;
 }
 
+// What a launch came to.  A failed one leaves its error with the runtime, where the caller's next check of its own
+// would find it.
+cli_status_t launched(cudaError_t e) {
+    if (e == cudaSuccess) return CLI_OK;
+    cudaGetLastError();
+    return CLI_DEVICE;
+}
+
 HeadsView view_of(const cli_heads_t &h) {
     return {h.data, static_cast<long long>(h.row_stride), static_cast<long long>(h.head_stride)};
 }
@@ -186,7 +194,7 @@ cli_status_t rotary_call(const cli_rotary_t *a, bool norm, bool backward) {
         if (L.part[p].d_gain) L.part[p].gain_partials = partials + p * static_cast<size_t>(rotary_blocks(sms)) * d;
     if (want_gain && 2ull * rotary_blocks(sms) * d * 4 > ws_bytes) return CLI_UNSUPPORTED;
     cudaStream_t stream = static_cast<cudaStream_t>(a->stream);
-    return launch_rotary(L, stream) == cudaSuccess ? CLI_OK : CLI_DEVICE;
+    return launched(launch_rotary(L, stream));
 }
 
 // The sizes of an attention call, checked; `L` receives them.
@@ -292,8 +300,7 @@ cli_status_t attention_call(const cli_attention_t *a, bool backward) {
     L.workspace = static_cast<uint8_t *>(a->workspace);
     L.status = a->device_status;
     cudaStream_t stream = static_cast<cudaStream_t>(a->stream);
-    const cudaError_t e = backward ? launch_attention_backward(L, stream) : launch_attention(L, stream);
-    return e == cudaSuccess ? CLI_OK : CLI_DEVICE;
+    return launched(backward ? launch_attention_backward(L, stream) : launch_attention(L, stream));
 }
 
 size_t attention_bytes(const cli_attention_t *a, bool backward) {
@@ -343,10 +350,8 @@ cli_status_t rotary_table(const cli_rotary_table_t *a) {
             f[i] = f[i] * (1.0 - blend) + f[i] / a->factor * blend;
         }
     }
-    return launch_rotary_table(a->table, static_cast<long long>(a->positions), half, f, amplitude,
-                               static_cast<cudaStream_t>(a->stream)) == cudaSuccess
-               ? CLI_OK
-               : CLI_DEVICE;
+    return launched(launch_rotary_table(a->table, static_cast<long long>(a->positions), half, f, amplitude,
+                                        static_cast<cudaStream_t>(a->stream)));
 }
 
 cli_status_t rotary_heads(const cli_rotary_t *a) { return rotary_call(a, false, false); }

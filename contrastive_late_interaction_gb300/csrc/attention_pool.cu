@@ -891,7 +891,7 @@ cudaError_t forward(const AttentionLaunch &L, cudaStream_t stream) {
     float2 *part_ml = split ? reinterpret_cast<float2 *>(L.workspace + part_bytes(L, c.slots, c)) : nullptr;
     const Grids g = grids_of(L, c, false);
     forward_kernel<T, DP, NT><<<static_cast<unsigned>(g.first), kWarps * 32, 0, stream>>>(L, c.chunk, c.slots, part_o, part_ml);
-    if (!split) return cudaGetLastError();
+    if (g.joins == 0) return cudaGetLastError();   // whole items, or none that may have rows
     const dim3 joins(static_cast<unsigned>(g.joins));
     if (g.wide) return launch_after(join_kernel<T, 8>, joins, 256, 0, stream, L, c.chunk, part_o, part_ml);
     return launch_after(join_kernel<T, 1>, joins, 256, 0, stream, L, c.chunk, part_o, part_ml);

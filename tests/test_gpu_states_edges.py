@@ -64,3 +64,23 @@ def test_scratch_of_a_call_on_another_stream_is_not_handed_out(cli, q_len, k_len
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     del fill
+
+
+# ----------------------------------------------------------------------------
+# maxima, offsets and positions that do not fit
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("maxima", [dict(max_query_rows=0), dict(max_key_rows=0), dict(max_query_rows=0, max_key_rows=0),
+                                    dict(max_query_rows=0, max_key_rows=300)])
+@pytest.mark.parametrize("k_len", [[20, 30], [9000, 700]])
+def test_maxima_of_nothing_are_reported_as_malformed(cli, k_len, maxima):
+    """Rows longer than a maximum of 0 are the device's to report, whatever the call is cut into."""
+    q, k = rand(gen(1), 3, 2, 64), rand(gen(2), sum(k_len), 2, 64)
+    qo, ko = offsets([2, 1]), offsets(k_len)
+    f = cli.cross_attention(q, qo, k, k, ko, **maxima)
+    with pytest.raises(cli.MalformedError):
+        cli.check_device_status(f["device_status"])
+    b = cli.cross_attention_backward(q, qo, k, k, ko, torch.zeros_like(q), torch.zeros(3, 2, device="cuda"), q, **maxima)
+    with pytest.raises(cli.MalformedError):
+        cli.check_device_status(b["device_status"])
+    assert not q.isnan().any()   # and PyTorch's own launches find no error of the call's
