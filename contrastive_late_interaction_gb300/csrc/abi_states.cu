@@ -25,10 +25,12 @@ struct Heads {
     size_t rows, heads, inner, row, head;   // inner: bytes of a head; row, head: strides in bytes
     Heads(const cli_heads_t &h, size_t rows_, size_t heads_, size_t dim, size_t esize)
         : at(reinterpret_cast<uintptr_t>(h.data)), rows(rows_), heads(heads_), inner(dim * esize),
-          row(h.row_stride * esize), head(h.head_stride * esize) {
+          row(bytes_of(h.row_stride, esize)), head(bytes_of(h.head_stride, esize)) {
         if (rows <= 1) row = 0;
         if (heads <= 1) head = 0;
     }
+    // past 2^40 elements it is more than heads_ok takes, and stays so
+    static size_t bytes_of(size_t stride, size_t esize) { return (stride >> 40 ? 1ull << 40 : stride) * esize; }
     bool empty() const { return rows == 0 || heads == 0; }
     size_t span() const { return empty() ? 0 : (rows - 1) * row + (heads - 1) * head + inner; }
     Range range() const { return {at, at + span()}; }
@@ -41,6 +43,7 @@ cli_status_t heads_ok(const Heads &h) {
     if (!h.at || h.at % 16 != 0) return CLI_INVALID_ARGUMENT;
     if (h.row % 16 != 0 || h.head % 16 != 0) return CLI_SHAPE_MISMATCH;
     if (h.row >= (1ull << 40) || h.head >= (1ull << 40)) return CLI_SHAPE_MISMATCH;
+    if (h.row && h.rows - 1 > (1ull << 61) / h.row) return CLI_SHAPE_MISMATCH;   // heads: 2^16 times 2^40 at most
     return CLI_OK;
 }
 

@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from test_states_reference import A, attention_args, heads
+from test_states_reference import A, attention_args, heads, rotary_args
 from test_states_reference import b as _b
 
 b = _b   # the fixture
@@ -25,3 +25,13 @@ def test_attention_refuses_more_blocks_than_a_grid_has(b, over):
 def test_attention_sizes_below_that_are_taken(b):
     args = attention_args(b, items=1 << 26, query_heads=64, key_heads=64, max_query_rows=1, max_key_rows=32)
     assert b.lib.cross_attention(ctypes.byref(args)) != b.CLI_SHAPE_MISMATCH
+
+
+def test_matrices_past_the_address_space_are_refused(b):
+    """Strides and spans that wrap in 64 bits: the overlap checks would look at another place."""
+    H = b.HeadsArgs
+    for rows, row, head in ((1 << 30, 1 << 38, 64), (100, (1 << 63) + 256, 64), (100, 256, (1 << 63) + 64)):
+        part = dict(rows=rows, x=H(A * 4, row, head), y=heads(b, 5, rows, 4, 64))
+        assert b.lib.rotary_heads(ctypes.byref(rotary_args(b, part=part))) == b.CLI_SHAPE_MISMATCH
+        args = attention_args(b, key_rows=rows, max_key_rows=300, k=H(A * 4, row, head))
+        assert b.lib.cross_attention(ctypes.byref(args)) == b.CLI_SHAPE_MISMATCH
