@@ -477,10 +477,10 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
     }
 
     for (long long row = share.block * kWarps + warp; row < part.rows; row += share.blocks * kWarps) {
-        const int pos = part.positions ? part.positions[row] : static_cast<int>(row);
-        if (pos < 0 || pos >= P.table_rows) {    // the same for the warp
+        int pos = part.positions ? part.positions[row] : static_cast<int>(row);
+        if (pos < 0 || pos >= P.table_rows) {    // reported and read as 0, as above; the same for the warp
             if (lane == 0 && !few_rows(P)) report(P.status, CLI_MALFORMED);
-            continue;
+            pos = 0;
         }
         float c[N], s[N];
         const float2 *cs = P.table + static_cast<long long>(pos) * half;

@@ -536,7 +536,8 @@ cli_status_t rotary_table(const cli_rotary_table_t *args);
  *   epsilon         > 0 (the norm verbs)
  *   rows, heads     of a part; rows < 2^31 (0 is a call on no rows), heads at most 65535
  *   positions       device int32 [rows], row r's position; NULL: r itself.  One
- *                   outside [0, table_rows) sets CLI_MALFORMED
+ *                   outside [0, table_rows) sets CLI_MALFORMED, and its row is
+ *                   rotated as one at 0
  *   x, y, d_y, d_x  rotary_heads reads x and writes y; rotary_heads_backward
  *                   reads d_y and writes d_x; norm_rotary_heads reads x and
  *                   writes y; norm_rotary_heads_backward reads x and d_y and

@@ -84,3 +84,69 @@ def test_maxima_of_nothing_are_reported_as_malformed(cli, k_len, maxima):
     with pytest.raises(cli.MalformedError):
         cli.check_device_status(b["device_status"])
     assert not q.isnan().any()   # and PyTorch's own launches find no error of the call's
+
+
+@pytest.mark.parametrize("rotary_dim", [64, 36, 34])    # half a multiple of 8, of 2, odd
+@pytest.mark.parametrize("rows", [40, 3000])            # one block looks at every position, or every warp at its own
+@pytest.mark.parametrize("part", ["q", "k"])
+@pytest.mark.parametrize("bad", [-1, 50, -2 ** 31])
+def test_a_row_outside_the_table_is_reported_and_rotated_as_at_0(cli, bad, part, rows, rotary_dim):
+    g, tab = gen(rows), ref.table(50, rotary_dim).cuda()
+    x = {"q": rand(g, rows, 3, 64), "k": rand(g, rows + 7, 2, 64)}
+    gain = 1 + 0.1 * rand(g, 64, dtype=F32)
+    good = {n: torch.randint(0, 50, (t.shape[0],), generator=g, device="cuda", dtype=torch.int32) for n, t in x.items()}
+    good[part][rows // 2] = 0
+    wrong = {n: p.clone() for n, p in good.items()}
+    wrong[part][rows // 2] = bad
+
+    def both(pos):
+        out = {n: torch.full_like(t, 9.0) for n, t in x.items()}
+        f = cli.norm_rotary_heads(x["q"], tab, pos["q"], q_gain=gain, k=x["k"], k_positions=pos["k"], k_gain=gain, out=out)
+        out = {"d_" + n: torch.full_like(t, 9.0) for n, t in x.items()}
+        b = cli.norm_rotary_heads_backward(x["q"], x["q"], tab, pos["q"], q_gain=gain, k=x["k"], d_k=x["k"],
+                                           k_positions=pos["k"], k_gain=gain, out=out)
+        r = cli.rotary_heads(x["q"], tab, pos["q"], k=x["k"], k_positions=pos["k"])
+        return f, b, r
+    for a, w in zip(both(good), both(wrong)):
+        cli.check_device_status(a["device_status"])
+        with pytest.raises(cli.MalformedError):
+            cli.check_device_status(w["device_status"])
+        for name in a:
+            if name != "device_status":
+                assert torch.equal(a[name], w[name]), name
+
+
+def test_rotation_of_a_packed_projection_in_place(cli):
+    """Queries and keys of one [rows, 3, heads, dim] tensor, in place: the same values, and the values left alone."""
+    g, tab = gen(6), ref.table(4096, 64).cuda()
+    packed = rand(g, 1500, 3, 6, 64)
+    want = cli.rotary_heads(packed[:, 0].contiguous(), tab, k=packed[:, 1].contiguous())
+    values = packed[:, 2].clone()
+    r = cli.rotary_heads(packed[:, 0], tab, k=packed[:, 1], out={"q": packed[:, 0], "k": packed[:, 1]})
+    cli.check_device_status(r["device_status"])
+    assert torch.equal(packed[:, 0], want["q"]) and torch.equal(packed[:, 1], want["k"])
+    assert torch.equal(packed[:, 2], values)
+
+
+@pytest.mark.parametrize("items", [3, 300])              # one block checks every item, or the grid shares them
+@pytest.mark.parametrize("states", [20, 1500])           # whole items, and items cut along their states
+@pytest.mark.parametrize("rows", [1, 40])                # few rows, and tiles
+@pytest.mark.parametrize("which", ["k", "q"])
+@pytest.mark.parametrize("how", ["down", "first", "last", "past"])
+def test_malformed_offsets_are_reported_whatever_the_call_is_cut_into(cli, how, which, rows, states, items):
+    q, k = torch.zeros(rows * items, 2, 64, dtype=BF16, device="cuda"), torch.zeros(states * items, 2, 64, dtype=BF16, device="cuda")
+    n = {"q": rows, "k": states}[which]
+    bad = offsets([n] * items)
+    at, value = {"down": (items // 2, 0), "first": (0, 1), "last": (items, n * items - 1), "past": (items - 1, 2 ** 62)}[how]
+    bad[at] = value
+    off = {"q": offsets([rows] * items), "k": offsets([states] * items), which: bad}
+    kw = dict(max_query_rows=rows, max_key_rows=states)
+    if how == "down" and items // 2 == 1:
+        kw["max_" + ("query" if which == "q" else "key") + "_rows"] = 2 * n   # 0, 0, 2n, 3n is a tape of its own
+        off[which] = torch.tensor([0, 2 * n, n, 3 * n], device="cuda")
+    f = cli.cross_attention(q, off["q"], k, k, off["k"], **kw)
+    with pytest.raises(cli.MalformedError):
+        cli.check_device_status(f["device_status"])
+    b = cli.cross_attention_backward(q, off["q"], k, k, off["k"], q, torch.zeros(rows * items, 2, device="cuda"), q, **kw)
+    with pytest.raises(cli.MalformedError):
+        cli.check_device_status(b["device_status"])
