@@ -615,11 +615,12 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const long long row = u.k0 + j + 8 * y + g;
+                        const bool live = (keep >> (8 * y + g)) & 1u;   // a dropped state's are 0 times whatever the rows hold
                         uint32_t wv[4], wk[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            wv[i] = Type<T>::pack(av[i][2 * y], av[i][2 * y + 1]);
-                            wk[i] = Type<T>::pack(ak[i][2 * y] * L.scale, ak[i][2 * y + 1] * L.scale);
+                            wv[i] = live ? Type<T>::pack(av[i][2 * y], av[i][2 * y + 1]) : 0u;
+                            wk[i] = live ? Type<T>::pack(ak[i][2 * y] * L.scale, ak[i][2 * y + 1] * L.scale) : 0u;
                         }
                         if (32 * c + 8 * t < dim && 8 * y + g < count) {
                             __stcs(reinterpret_cast<uint4 *>(dvbase + row * L.d_v.row + 32 * c), make_uint4(wv[0], wv[1], wv[2], wv[3]));

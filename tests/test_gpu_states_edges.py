@@ -150,3 +150,27 @@ def test_malformed_offsets_are_reported_whatever_the_call_is_cut_into(cli, how, 
     b = cli.cross_attention_backward(q, off["q"], k, k, off["k"], q, torch.zeros(rows * items, 2, device="cuda"), q, **kw)
     with pytest.raises(cli.MalformedError):
         cli.check_device_status(b["device_status"])
+
+
+# ----------------------------------------------------------------------------
+# values that only some rows hold
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("q_len", [[2, 1, 3], [3, 40, 2]])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_dropped_states_have_no_gradient_whatever_the_rows_hold(cli, bad, q_len, dtype):
+    g = gen(51)
+    k_len = [70, 300, 33]
+    q, d_o = rand(g, sum(q_len), 4, 64, dtype=dtype), rand(g, sum(q_len), 4, 64, dtype=dtype)
+    k, v = rand(g, sum(k_len), 2, 64, dtype=dtype), rand(g, sum(k_len), 2, 64, dtype=dtype)
+    q[0, :, 3], d_o[q_len[0] - 1, :, 5] = bad, bad     # of the first item
+    keep = (torch.rand(sum(k_len), generator=g, device="cuda") >= 0.4).to(torch.uint8)
+    keep[-k_len[2]:] = 0
+    kw = dict(key_mask=keep, max_query_rows=max(q_len), max_key_rows=max(k_len))
+    f = cli.cross_attention(q, offsets(q_len), k, v, offsets(k_len), **kw)
+    b = cli.cross_attention_backward(q, offsets(q_len), k, v, offsets(k_len), f["output"], f["lse"], d_o, **kw)
+    for name in ("d_k", "d_v"):
+        assert not b[name][keep == 0].any(), name
+        assert b[name][k_len[0]:].isfinite().all(), name
+    assert b["d_q"][q_len[0]:].isfinite().all()
