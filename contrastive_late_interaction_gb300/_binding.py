@@ -806,13 +806,9 @@ def _rotary_call(verb, lead, q_part, k_part, table, interleaved, epsilon, worksp
     if len(shape) != 3 or shape[2] != 2 or not table.is_contiguous():
         raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: table must be [positions, rotary_dim / 2, 2], packed")
     ws, ws_bytes = _lent(workspace)
-    try:
-        args = _pack_rotary.pack(DTYPES[lead.dtype], 1 if interleaved else 0, lead.shape[2], 2 * shape[1],
-                                 table.data_ptr(), shape[0], epsilon, *q_part, *k_part, ws, ws_bytes,
-                                 status.data_ptr(), _raw_stream(lead))
-    except (OverflowError, struct.error) as e:
-        raise InvalidArgumentError(CLI_INVALID_ARGUMENT, f"{verb}: {e}") from None
-    rc = _ROTARY[verb](args)
+    rc = _ROTARY[verb](_pack_rotary.pack(DTYPES[lead.dtype], 1 if interleaved else 0, lead.shape[2], 2 * shape[1],
+                                         table.data_ptr(), shape[0], epsilon, *q_part, *k_part, ws, ws_bytes,
+                                         status.data_ptr(), _raw_stream(lead)))
     if rc:
         raise_for(rc, verb)
 
@@ -940,10 +936,7 @@ def _attention_call(verb, head, tail, workspace, like, status):
     call, workspace_bytes = _ATTENTION[verb]
     ws, ws_bytes = _lent(workspace)
     last = status.data_ptr(), _raw_stream(like)
-    try:
-        args = _pack_attention.pack(*head, *tail, ws, ws_bytes, *last)
-    except (OverflowError, struct.error) as e:
-        raise InvalidArgumentError(CLI_INVALID_ARGUMENT, f"{verb}: {e}") from None
+    args = _pack_attention.pack(*head, *tail, ws, ws_bytes, *last)
     if workspace is None:
         need = workspace_bytes(args)
         if need:

@@ -185,16 +185,3 @@ def test_the_packages_names_follow_the_binding(box, monkeypatch):
     other = lambda *a: None  # noqa: E731
     monkeypatch.setattr(box.b, "rotary_table", other)
     assert cli.rotary_table is other
-
-
-def test_numbers_that_the_arguments_cannot_hold_are_refused_as_arguments(box):
-    b = box.b
-    q, off, table = tensor(4, 2, 8, dtype=BF16), tensor(3, dtype=I64), tensor(9, 4, 2)
-    for bad in (1e39, -1e39, "1"):
-        with pytest.raises(b.InvalidArgumentError, match="cross_attention"):
-            b.cross_attention(q, off, q, q, off, scale=bad)
-        with pytest.raises(b.InvalidArgumentError, match="norm_rotary_heads"):
-            b.norm_rotary_heads(q, table, epsilon=bad)
-    with pytest.raises(b.InvalidArgumentError, match="cross_attention"):
-        b.cross_attention(q, off, q, q, off, max_query_rows=2.5)
-    assert not box.launched
