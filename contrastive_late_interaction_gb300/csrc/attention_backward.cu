@@ -20,19 +20,28 @@
 // those of the forward, with eight warps for the tiles' arithmetic: each
 // thread has one row of TMEM and half of its columns.
 //
-// Rounding.  P and dS are rounded to 16 bits as operands, and delta is taken
-// from the rounded output; sums are in 32 bits.  Each adds about as much to dQ
-// and dK as the rounding of the result itself: their error against 64 bits is
-// 1.6 times what one rounding at the end leaves (bf16: 0.0026 of the norm, not
-// 0.0017).  Doubling the operands would double the products.
+// Delta.  The output is rounded, so delta_r from it is off by up to u <|dO_r|,
+// |O_r|>.  That hardly shows in dQ_r, but where one state has most of a row's
+// weight, its ds is a small difference of large terms and an element of dK was
+// off by 0.3 to 0.7 of the root mean square of all of dK in items of few rows.
+// So dq_kernel runs first, with that delta, and sums each row's ds in 32 bits:
+// the sum over a row is 0 but for delta's error, and dkv_kernel takes delta
+// with it.  The order costs the time that dq_kernel used to fill at the other's
+// end: 32 items of 512 to 2048 x 512 to 1024 rows, 690 -> 783 us.
+//
+// Rounding.  P and dS are rounded to 16 bits as operands; sums are in 32 bits.
+// The error of dV and dK against 64 bits is 1.4 times what one rounding at the
+// end leaves (bf16: 0.0023 of the norm, not 0.0017), that of dQ, which has the
+// first delta, 1.6 to 2.3 times (0.0027 to 0.0038).  Doubling the operands
+// would double the products.
 //
 // Bound: 32 items of 512 to 2048 x 512 to 1024 rows, 16 heads of 128 in groups
-// of 4, take 782 us: stats 63 (HBM: dO and O, 5.3 TB/s), dkv 587 and dq, which
-// fills the SMs that leaves, 548; the products are at 70% and 59% of the tensor
-// pipe, the rest is the arithmetic between them, for which a block has only
-// two products to hide under, and the items' ends.  Short items (96 of 1 to 300
-// x 0 to 700 rows) are bound by the chain of loads, products and stores of a
-// tile of four or five blocks: 125 us.
+// of 4, take 783 us: stats 54 (HBM: dO and O), dq 311, dkv 419, of which some
+// 80 are its end, where CTAs wait for the last units of up to 64 blocks.  The
+// rest is the arithmetic between products, for which a block has only two
+// products to hide under, and the items' ends.  Short items (96 of 1 to 300 x 0
+// to 700 rows) are bound by the chain of loads, products and stores of a tile
+// of four or five blocks: 119 us.
 
 #include <cuda.h>
 
@@ -48,7 +57,7 @@ constexpr int kReaders = 11;   // of a published work item: warps 0 to 2, eight 
 
 // What the scores' rows need in the backward, one entry per output row and
 // head at stat_at: -lse in powers of two (-infinity where the row kept no
-// state, so that p is 0) and -delta, to be added.
+// state, so that p is 0) and -delta of the rounded output, to be added.
 __device__ __forceinline__ long long stat_at(const AttentionLaunch &L, int out_rows, int key_head, long long row) {
     return (static_cast<long long>(key_head) * out_rows + row) * L.group;
 }
@@ -296,14 +305,13 @@ struct Producer {
 template <typename T, int BOXES>
 __global__ void __launch_bounds__(kThreads, 1)
     dkv_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
-               int out_rows, const float2 *stats, long long tiles, unsigned long long *counter) {
+               int out_rows, const float2 *stats, const float *ds_sums, long long tiles, unsigned long long *counter) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     using Smem = Storage<BOXES>;
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t tmem = begin(sm, M, L.status);
     after_previous();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // dq_kernel, once the statistics are there
     const int group = L.group, dim = L.head_dim;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, &sm.abort_flag, L.status); };
     auto q_blocks = [&](const Work &w) { return (w.nq + rows_per_tile - 1) / rows_per_tile; };
@@ -394,7 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         issue_commit(leader, &sm.done);
         wait(&sm.done, 0);
     } else if (warp == 2) {
-        // Rows past the item's end are zeroed (they are summed over), and the rows' lse and delta staged.
+        // Rows past the item's end are zeroed (they are summed over), and the rows' lse and corrected delta staged.
+        const long long cells = static_cast<long long>(out_rows) * L.query_heads;
         uint32_t entry = 0;
         bool ok = true;
         Work w;
@@ -402,12 +411,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int blocks = q_blocks(w);
             for (int j = 0; j < blocks; ++j, ++entry) {
                 const int n = q_rows(w, j);
-                const float2 *src = stats + stat_at(L, out_rows, w.head, static_cast<long long>(w.o0) + j * rows_per_tile);
-                float2 f[4];
+                const long long first = stat_at(L, out_rows, w.head, static_cast<long long>(w.o0) + j * rows_per_tile);
+                float2 f[4], more[4];   // all on their way together: one after another they held up every block
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int at = 32 * i + lane;
-                    f[i] = at < n ? src[at] : make_float2(-INFINITY, 0.0f);
+                    f[i] = make_float2(-INFINITY, 0.0f), more[i] = make_float2(0.0f, 0.0f);
+                    if (at < n) {
+                        f[i] = stats[first + at];
+                        more[i] = make_float2(ds_sums[first + at], ds_sums[cells + first + at]);
+                    }
                 }
                 const uint32_t s = entry % Smem::kA, sb = entry % Smem::kB;
                 if (!wait(&sm.a_full[s], (entry / Smem::kA) & 1)) { ok = false; break; }
@@ -420,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     sm.lse[sb][32 * i + lane] = f[i].x;
-                    sm.delta[s][32 * i + lane] = f[i].y;
+                    sm.delta[s][32 * i + lane] = f[i].y - (more[i].x + more[i].y);
                 }
                 zero_rows<BOXES>(smem_u32(sm.ring_b[sb]), round16(n), keep, lane);
                 fence_proxy_async_smem();
@@ -528,18 +541,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ds_ready alternate: the scores of block j + 1 are issued before block j's
 // are waited for, and dP of block j + 1 before ds of block j is, so with one
 // barrier each a phase could pass unseen.
-// It reads nothing that dkv_kernel writes, and starts on the SMs that kernel
-// leaves: launched as its dependent, it waits for it only at its own end.
+// It runs first: each row's sum of ds, which the two sides' threads leave in
+// slots 2 part and 2 part + 1 of `ds_sums`, is what dkv_kernel corrects delta by.
 template <typename T, int BOXES>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
-              int out_rows, const float2 *stats, float *partials, long long tiles, Split cut,
+              int out_rows, const float2 *stats, float *ds_sums, float *partials, long long tiles, Split cut,
               unsigned long long *counter) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     using Smem = Storage<BOXES>;
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t tmem = begin(sm, M, L.status);
+    after_previous();
+    // dkv_kernel may set up on the SMs that this one leaves, where it waits for all of this one.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int group = L.group, dim = L.head_dim;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, &sm.abort_flag, L.status); };
 
@@ -666,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (mine)
                 st = __ldcg(stats + stat_at(L, out_rows, w.head, static_cast<long long>(w.o0) + r_in) + head_in);
             const float2 sl22 = make_float2(sl2, sl2), shift = make_float2(st.x, st.x), delta = make_float2(st.y, st.y);
+            float2 ds_sum = make_float2(0.0f, 0.0f);
             for (int j = 0; j < blocks; ++j, ++j_all) {
                 const int n = min(128, w.nk - 128 * j) - side * 64;   // columns of this side
                 const bool whole = !L.key_mask && n >= 64;
@@ -705,6 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             x.x = (keep >> i) & 1u ? x.x : 0.0f;
                             x.y = (keep >> (i + 1)) & 1u ? x.y : 0.0f;
                         }
+                        ds_sum = __fadd2_rn(ds_sum, x);
                         packed[c][i / 2] = Type<T>::pack(x.x, x.y);
                     }
                 }
@@ -726,6 +744,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
             }
             const int head = w.head * group + head_in;
+            if (mine)
+                ds_sums[static_cast<long long>(2 * w.part + side) * out_rows * L.query_heads +
+                        stat_at(L, out_rows, w.head, static_cast<long long>(w.o0) + r_in) + head_in] = ds_sum.x + ds_sum.y;
             // The sides take half of the row's columns each, in whole 16s.
             const int half = (dim / 2 + 15) & ~15;
             const int first = side ? half : 0, count = side ? dim - half : min(half, dim);
@@ -743,7 +764,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
-    after_previous();   // what follows on the stream waits for this kernel alone
+}
+
+// Where items are cut into parts: the rows' sums of ds of all parts, in a fixed
+// order, become those of the first.
+__global__ void __launch_bounds__(256) ds_sum_kernel(float *ds_sums, long long cells, int parts) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    after_previous();
+    const long long at = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;   // of both sides' cells
+    if (at >= 2 * cells) return;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) s += ds_sums[2 * cells * p + at];
+    ds_sums[at] = s;
 }
 
 // dQ of shared queries, and of items cut into parts: the sums of all, in a
@@ -775,10 +808,10 @@ __global__ void __launch_bounds__(256) dq_sum_kernel(const __grid_constant__ Att
         make_uint2(Type<T>::pack(s.x * L.scale, s.y * L.scale), Type<T>::pack(s.z * L.scale, s.w * L.scale));
 }
 
-size_t stats_bytes(const AttentionLaunch &L) {
-    const size_t out_rows = static_cast<size_t>(L.query_rows) * (L.q_off ? 1 : L.items);
-    return align256(out_rows * L.query_heads * sizeof(float2));
+long long cells_of(const AttentionLaunch &L) {
+    return static_cast<long long>(L.query_rows) * (L.q_off ? 1 : L.items) * L.query_heads;
 }
+size_t stats_bytes(const AttentionLaunch &L) { return align256(static_cast<size_t>(cells_of(L)) * sizeof(float2)); }
 
 // dq_kernel's work: slots of tiles of queries, parts along the states, and the sums that this leaves for each row.
 struct Cut {
@@ -786,6 +819,7 @@ struct Cut {
     Split split;
     int sums;   // 1: none, dQ is stored at once
 };
+constexpr long long kLeastPart = 512;
 Cut cut_of(const AttentionLaunch &L) {
     const int rows_per_tile = 128 / L.group;
     Cut c;
@@ -793,12 +827,7 @@ Cut cut_of(const AttentionLaunch &L) {
                       : static_cast<long long>(L.items) * ((L.query_rows + rows_per_tile - 1) / rows_per_tile);
     const long long filled = L.q_off ? (L.query_rows + rows_per_tile - 1) / rows_per_tile : c.slots;
     const long long blocks = (filled > L.items ? filled : L.items) * L.key_heads;
-    // dkv_kernel runs beside, with a CTA for each of its blocks while they last: parts shorter than what those
-    // walk end no sooner, and a second wave behind them later than whole items (200 x 2048 rows, 8 heads: 31 us
-    // in parts, 25 whole).
-    const long long left = 152 - (static_cast<long long>(L.key_rows) + 127) / 128 * L.key_heads;
-    const long long walk = static_cast<long long>(L.max_q) * L.group;
-    c.split = split_of(L, blocks, left >= blocks ? left : 152, walk > 512 ? walk : 512);
+    c.split = split_of(L, blocks, 152, kLeastPart);
     c.sums = (L.q_off ? 1 : L.items) * c.split.parts;
     return c;
 }
@@ -807,14 +836,19 @@ long long joins_of(const AttentionLaunch &L) {
     return (static_cast<long long>(L.query_rows) * L.query_heads * L.head_dim + kSumElems - 1) / kSumElems;
 }
 
+// Two slots of a float a part.
+size_t ds_sums_bytes(const AttentionLaunch &L, const Cut &c) { return c.split.parts * stats_bytes(L); }
+
 template <typename T, int BOXES>
 cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
     const int rows_per_tile = 128 / L.group;
     const int out_rows = L.query_rows * (L.q_off ? 1 : L.items);
     unsigned long long *counters = reinterpret_cast<unsigned long long *>(L.workspace);
-    float2 *stats = reinterpret_cast<float2 *>(L.workspace + kCounterBytes);
     const Cut c = cut_of(L);
-    float *partials = L.q_off && c.sums == 1 ? nullptr : reinterpret_cast<float *>(L.workspace + kCounterBytes + stats_bytes(L));
+    uint8_t *at = L.workspace + kCounterBytes;
+    float2 *stats = reinterpret_cast<float2 *>(at);
+    float *ds_sums = reinterpret_cast<float *>(at += stats_bytes(L));
+    float *partials = L.q_off && c.sums == 1 ? nullptr : reinterpret_cast<float *>(at + ds_sums_bytes(L, c));
     Maps M;
     const bool bf16 = Type<T>::bf16;
     if (!encode_heads_tiles(&M.q, L.q, bf16, L.head_dim, L.query_heads, L.query_rows, L.group, rows_per_tile) ||
@@ -836,13 +870,18 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     auto grid = [&](long long tiles) { return static_cast<unsigned>(tiles < L.sm_count ? tiles : L.sm_count); };
-    const long long k_tiles = (static_cast<long long>(L.key_rows) / 128 + L.items) * L.key_heads;
-    e = launch_after(dkv, dim3(grid(k_tiles)), kThreads, smem, stream, L, M, rows_per_tile, out_rows, stats, k_tiles,
-                     counters);
-    if (e != cudaSuccess) return e;
     const long long q_tiles = c.slots * c.split.parts * L.key_heads;
-    e = launch_after(dq, dim3(grid(q_tiles)), kThreads, smem, stream, L, M, rows_per_tile, out_rows, stats, partials, q_tiles,
-                     c.split, counters + 1);
+    e = launch_after(dq, dim3(grid(q_tiles)), kThreads, smem, stream, L, M, rows_per_tile, out_rows, stats, ds_sums, partials,
+                     q_tiles, c.split, counters);
+    if (e != cudaSuccess) return e;
+    if (c.split.parts > 1) {
+        e = launch_after(ds_sum_kernel, dim3(static_cast<unsigned>((2 * cells_of(L) + 255) / 256)), 256, 0, stream, ds_sums,
+                         cells_of(L), c.split.parts);
+        if (e != cudaSuccess) return e;
+    }
+    const long long k_tiles = (static_cast<long long>(L.key_rows) / 128 + L.items) * L.key_heads;
+    e = launch_after(dkv, dim3(grid(k_tiles)), kThreads, smem, stream, L, M, rows_per_tile, out_rows, stats, ds_sums, k_tiles,
+                     counters + 1);
     if (e != cudaSuccess) return e;
     if (partials) dq_sum_kernel<T><<<static_cast<unsigned>(joins_of(L)), 256, 0, stream>>>(L, c.sums, partials);
     return cudaGetLastError();
@@ -850,13 +889,18 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
 
 }  // namespace
 
-long long backward_tiles_joins(const AttentionLaunch &L) { return L.q_off && cut_of(L).sums == 1 ? 0 : joins_of(L); }
+long long backward_tiles_joins(const AttentionLaunch &L) {
+    const Cut c = cut_of(L);
+    const long long folds = c.split.parts > 1 ? (2 * cells_of(L) + 255) / 256 : 0;
+    const long long joins = L.q_off && c.sums == 1 ? 0 : joins_of(L);
+    return folds > joins ? folds : joins;
+}
 
 size_t backward_tiles_workspace(const AttentionLaunch &L) {
     const Cut c = cut_of(L);
     const size_t rows = L.q_off && c.sums == 1 ? 0 : static_cast<size_t>(c.sums) * L.query_rows;
     const size_t partials = rows * L.query_heads * L.head_dim * sizeof(float);
-    return kCounterBytes + stats_bytes(L) + align256(partials);
+    return kCounterBytes + stats_bytes(L) + ds_sums_bytes(L, c) + align256(partials);
 }
 
 // Needs at least one query row and one state (the tensor maps have no empty form).

@@ -623,8 +623,9 @@ size_t norm_rotary_heads_backward_workspace_bytes(size_t head_dim);
  *
  * P and dS enter the products as `dtype`, or as the sum of two such where an
  * item has few rows; everything else between input and output is in 32 bits,
- * but for D, which the rounded output gives (with few rows, states that have a
- * quarter or more of a row's weight get theirs from 32-bit sums).
+ * but for D, which the rounded output gives.  For dK, D is corrected by a row's
+ * sum of dS in 32 bits (with few rows, for the states that have an eighth or
+ * more of some row's weight, a quarter with more than 8 rows).
  * Results are bit-reproducible: no sum depends on the order in which blocks run.
  */
 typedef struct {

@@ -174,3 +174,64 @@ def test_dropped_states_have_no_gradient_whatever_the_rows_hold(cli, bad, q_len,
         assert not b[name][keep == 0].any(), name
         assert b[name][k_len[0]:].isfinite().all(), name
     assert b["d_q"][q_len[0]:].isfinite().all()
+
+
+def exact_backward(q, k, v, d_o, q_len, k_len, scale, shared=False):
+    """Of each item, in 64 bits: (p, dP, delta, ds) [heads, rows, states], its slices of the tapes, and wide k, v."""
+    group = q.shape[1] // k.shape[1]
+    qa = oa = ka = 0
+    for i, nk in enumerate(k_len):
+        nq = q.shape[0] if shared else q_len[i]
+        qi, oi = q[qa:qa + nq].double(), d_o[oa:oa + nq].double()
+        ki, vi = (t[ka:ka + nk].double().repeat_interleave(group, 1) for t in (k, v))
+        if nk and nq:
+            p = (torch.einsum("qhd,khd->hqk", qi, ki) * scale).softmax(-1)
+            dp = torch.einsum("qhd,khd->hqk", oi, vi)
+            delta = (p * dp).sum(-1, keepdim=True)
+            yield slice(qa, qa + nq), slice(ka, ka + nk), qi, oi, ki, vi, p, dp, delta, p * (dp - delta)
+        oa, ka = oa + nq, ka + nk
+        qa += 0 if shared else nq
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("q_len, k_len, hq, hk, d, shared", [
+    ([1] * 60 + [20], [300, 37, 900] * 20 + [500], 4, 4, 128, False),   # short items in a long call
+    ([1, 300, 2], [700, 400, 90], 4, 2, 64, False), ([17, 5], [9000, 700], 2, 2, 128, False),
+    (20, [400, 60, 1300], 2, 2, 72, True),
+])
+def test_gradient_of_a_dominating_state_on_tiles(cli, q_len, k_len, hq, hk, d, shared, dtype):
+    """dK of the calls that go through tiles, where ds = p (dp - delta) is a small difference of large terms.  delta comes
+    from sums in 32 bits, so what is left of a state's ds is: its rounding as an operand (u |ds|, or half the smallest
+    subnormal), p's relative error r (of ds, and of every state's ds through delta), and the 32-bit sums of dP and of the
+    row (e (d + 4) and e n of their terms).  r is as in the reference: 2 es + 2^-20 + e |s|."""
+    g = gen(78)
+    u, e, tiny = ref.UNIT[dtype], ref.E, ref.TINY[dtype]
+    rows_q, rows_k = (q_len if shared else sum(q_len)), sum(k_len)
+    out_rows = rows_q * len(k_len) if shared else rows_q
+    q, k, v = rand(g, rows_q, hq, d, dtype=dtype, scale=4.0), rand(g, rows_k, hk, d, dtype=dtype), rand(g, rows_k, hk, d, dtype=dtype)
+    d_o = rand(g, out_rows, hq, d, dtype=dtype)
+    qo, scale = None if shared else offsets(q_len), d ** -0.5
+    kw = dict(max_query_rows=rows_q if shared else max(q_len), max_key_rows=max(k_len))
+    f = cli.cross_attention(q, qo, k, v, offsets(k_len), **kw)
+    got = cli.cross_attention_backward(q, qo, k, v, offsets(k_len), f["output"], f["lse"], d_o, **kw)["d_k"].double()
+    largest = 0.0
+    for _, ks, qi, oi, ki, vi, p, dp, delta, ds in exact_backward(q, k, v, d_o, q_len, k_len, scale, shared):
+        es = (d + 4) * e * scale * torch.einsum("qhd,khd->hqk", qi.abs(), ki.abs()).amax(-1, keepdim=True)
+        s = scale * torch.einsum("qhd,khd->hqk", qi, ki).abs().amax(-1, keepdim=True)
+        r = 2 * es + 2.0 ** -20 + e * s
+        mag = torch.einsum("qhd,khd->hqk", oi.abs(), vi.abs())
+        # of delta: the row's ds with p's error, its dP sums, and the sum over n states of ds with the first delta, which
+        # is off by u sum |dO O| at most
+        first = u * torch.einsum("qhd,hqd->hq", oi.abs(), torch.einsum("hqk,khd->hqd", p, vi).abs())[..., None]
+        nk = p.shape[2]
+        b_delta = (r * ds.abs() + (d + 4) * e * p * mag + nk * e * (ds.abs() + p * first)).sum(-1, keepdim=True) + r * first
+        b = (u + r) * ds.abs() + tiny + p * ((d + 4) * e * mag + b_delta)
+        fold = lambda t: t.view(nk, hk, hq // hk, d).sum(2)  # noqa: E731
+        want = scale * fold(torch.einsum("hqk,qhd->khd", ds, qi))
+        sums = fold(torch.einsum("hqk,qhd->khd", ds.abs(), qi.abs()))
+        bound = (u + 2.0 ** -20) * want.abs() + scale * fold(torch.einsum("hqk,qhd->khd", b, qi.abs())) + \
+            scale * (p.shape[1] * hq // hk + 4) * e * sums + tiny
+        largest = max(largest, p.max().item())
+        bad = (got[ks] - want).abs() > bound
+        assert not bad.any(), (int(bad.sum()), ((got[ks] - want).abs() / bound).max().item())
+    assert largest > 0.9
