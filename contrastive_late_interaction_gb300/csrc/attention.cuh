@@ -125,11 +125,14 @@ __device__ __forceinline__ int batch_of(long long tiles) {
     return b < 1 ? 1 : b > 32 ? 32 : static_cast<int>(b);
 }
 
-// The first kernel of a call: the status and the counters start at 0.
+constexpr size_t kCounterBytes = 256;   // at the start of the workspace: the counters, and from word kBoundsAt on bounds
+constexpr int kBoundsAt = 16;
+
+// The first kernel of a call: the status, the counters and the bounds start at 0.
 static __global__ void begin_kernel(int32_t *status, unsigned long long *counters) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) *status = 0;
-    if (threadIdx.x < 4) counters[threadIdx.x] = 0;
+    if (threadIdx.x < kCounterBytes / 8) counters[threadIdx.x] = 0;
 }
 
 // Waits for the kernels before this one on the stream, which may still run
@@ -153,8 +156,6 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
-constexpr size_t kCounterBytes = 256;   // at the start of the workspace
-
 template <typename T> struct Type;
 template <> struct Type<__nv_bfloat16> {
     static constexpr bool bf16 = true;
@@ -175,6 +176,19 @@ template <> struct Type<__half> {
         return __half22float2(*reinterpret_cast<const __half2 *>(&v));
     }
 };
+
+// fp16 as the type of P and dS, whose products' gradients may be of any size:
+// P goes in times 2^14, and dS times a power of two that brings it below 2^15,
+// so that neither leaves the type's normal range downwards while the other end
+// holds (in their own size dQ and dK had 6 times the error at output gradients
+// of 0.001, and infinities at 10^5).  In bf16 both stay as they are.
+template <typename T> __host__ __device__ constexpr float weight_shift() { return Type<T>::bf16 ? 0.0f : 14.0f; }
+template <typename T> __host__ __device__ constexpr float weight_unit() { return Type<T>::bf16 ? 1.0f : 1.0f / 16384.0f; }
+
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+// The e of a positive normal number's 2^e <= x < 2^(e + 1).
+__device__ __forceinline__ int exponent_of(float x) { return static_cast<int>(__float_as_uint(x) >> 23) - 127; }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -347,7 +361,7 @@ __device__ __forceinline__ void store_sums(uint32_t sums, int dim, float scale, 
 }
 
 // The same as 32-bit sums; `out` on 32 bytes.
-__device__ __forceinline__ void store_partials(uint32_t sums, int dim, bool warp_has, bool mine, float *out) {
+__device__ __forceinline__ void store_partials(uint32_t sums, int dim, float scale, bool warp_has, bool mine, float *out) {
 #pragma unroll 1
     for (int x = 0; x < dim; x += 8) {
         uint32_t r[8] = {};
@@ -355,6 +369,8 @@ __device__ __forceinline__ void store_partials(uint32_t sums, int dim, bool warp
             tmem_ld8_async(sums + x, r);
             tmem_wait_ld();
             tmem_regs_ready_n(r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * scale);
         }
         if (mine) store_32(out + x, true, r);
         __syncwarp();

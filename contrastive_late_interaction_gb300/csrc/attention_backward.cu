@@ -62,17 +62,61 @@ __device__ __forceinline__ long long stat_at(const AttentionLaunch &L, int out_r
     return (static_cast<long long>(key_head) * out_rows + row) * L.group;
 }
 
+// fp16: the largest square of a norm among the output gradient's rows of heads,
+// and among the kept values', as the bits of a float.  Rows that are not
+// finite are left out: their own gradients are not finite either.
+struct Bounds {
+    uint32_t d_o, v;
+};
+// The largest of a block's threads, in whatever order the blocks come: one request a block, as they all go to one address.
+__device__ __forceinline__ void raise_bounds(Bounds *bounds, float d_o, float v) {
+    __shared__ float most[2][8];
+    for (int w = 16; w; w >>= 1) {
+        d_o = fmaxf(d_o, __shfl_xor_sync(0xffffffffu, d_o, w));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, w));
+    }
+    if ((threadIdx.x & 31) == 0) most[0][threadIdx.x >> 5] = d_o, most[1][threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x > 1) return;
+    float mine = 0.0f;
+    for (int w = 0; w < 8; ++w) mine = fmaxf(mine, most[threadIdx.x][w]);
+    atomicMax(threadIdx.x ? &bounds->v : &bounds->d_o, __float_as_uint(mine));
+}
+
+// What dS is multiplied by beside P's 2^14: |dS| <= p (|dP| + |delta|) <= 2 |dO| |v| < 2^(e + 1), and 2^14 2^-e times
+// that is below 2^15.
+template <typename T>
+__device__ __forceinline__ float ds_scale(const Bounds *bounds) {
+    if constexpr (Type<T>::bf16) return 1.0f;
+    const float most = 2.001f * sqrtf(__uint_as_float(__ldcg(&bounds->d_o))) * sqrtf(__uint_as_float(__ldcg(&bounds->v)));
+    return most > 0.0f ? power_of_two(-exponent_of(most)) : 1.0f;
+}
+
+// The larger of `most` and the square of the norm of a row of a head, 8 elements a lane of 16.
+__device__ __forceinline__ float larger_square(float most, const uint32_t (&w)[4]) {
+    float sq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = Type<__half>::unpack(w[i]);
+        sq = fmaf(v.x, v.x, fmaf(v.y, v.y, sq));
+    }
+#pragma unroll
+    for (int s = 8; s; s >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, s);
+    return sq < INFINITY ? fmaxf(most, sq) : most;   // not infinite, and not a NaN
+}
+
 // A warp a row, 16 lanes a head, 8 elements a lane, the loads of eight heads
 // under way together.
 template <typename T>
 __global__ void __launch_bounds__(256, 4) stats_kernel(const __grid_constant__ AttentionLaunch L, int out_rows,
-                                                    float2 *stats) {
+                                                    float2 *stats, Bounds *bounds) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     after_previous();
     check_items(L, static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, static_cast<long long>(gridDim.x) * 256);
     const int lane = threadIdx.x & 15, side = (threadIdx.x >> 4) & 1;
     const bool in = 8 * lane < L.head_dim;
     constexpr int kAtOnce = 4;
+    float most = 0.0f, most_v = 0.0f;
     for (long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < out_rows;
          row += static_cast<long long>(gridDim.x) * 8) {
         const T *o = static_cast<const T *>(L.o.data) + row * L.o.row + 8 * lane;
@@ -98,6 +142,7 @@ __global__ void __launch_bounds__(256, 4) stats_kernel(const __grid_constant__ A
                     const float2 u = Type<T>::unpack(wa[i]), v = Type<T>::unpack(wb[i]);
                     d[x] = fmaf(u.x, v.x, fmaf(u.y, v.y, d[x]));
                 }
+                if constexpr (!Type<T>::bf16) most = larger_square(most, wb);
 #pragma unroll
                 for (int s = 8; s; s >>= 1) d[x] += __shfl_xor_sync(0xffffffffu, d[x], s);
             }
@@ -115,6 +160,37 @@ __global__ void __launch_bounds__(256, 4) stats_kernel(const __grid_constant__ A
             }
         }
     }
+    if constexpr (!Type<T>::bf16) {
+        const long long cells = static_cast<long long>(L.key_rows) * L.key_heads;
+        for (long long c0 = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * 2 * kAtOnce; c0 < cells;
+             c0 += static_cast<long long>(gridDim.x) * 16 * kAtOnce) {
+            uint4 a[kAtOnce];
+            bool kept[kAtOnce];
+#pragma unroll
+            for (int x = 0; x < kAtOnce; ++x) {
+                const long long cell = c0 + 2 * x + side, row = cell / L.key_heads;
+                a[x] = make_uint4(0, 0, 0, 0), kept[x] = false;
+                if (cell >= cells) continue;
+                kept[x] = !L.key_mask || L.key_mask[row] != 0;
+                if (in)
+                    a[x] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(L.v.data) + row * L.v.row +
+                                                                 (cell - row * L.key_heads) * L.v.head + 8 * lane));
+            }
+#pragma unroll
+            for (int x = 0; x < kAtOnce; ++x) {
+                const uint32_t w[4] = {a[x].x, a[x].y, a[x].z, a[x].w};
+                const float with = larger_square(most_v, w);
+                most_v = kept[x] ? with : most_v;
+            }
+        }
+        raise_bounds(bounds, most, most_v);
+    }
+}
+
+// dP - delta, both times the scale of dS (delta has it already).
+template <typename T>
+__device__ __forceinline__ float2 centred(float2 dp, float2 unit, float2 minus_delta) {
+    return Type<T>::bf16 ? __fadd2_rn(dp, minus_delta) : __ffma2_rn(dp, unit, minus_delta);
 }
 
 // One CTA's current work: a tile of 128 states or of 128 packed rows.
@@ -305,7 +381,8 @@ struct Producer {
 template <typename T, int BOXES>
 __global__ void __launch_bounds__(kThreads, 1)
     dkv_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
-               int out_rows, const float2 *stats, const float *ds_sums, long long tiles, unsigned long long *counter) {
+               int out_rows, const float2 *stats, const float *ds_sums, const Bounds *bounds, long long tiles,
+               unsigned long long *counter) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     using Smem = Storage<BOXES>;
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
@@ -404,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 2) {
         // Rows past the item's end are zeroed (they are summed over), and the rows' lse and corrected delta staged.
         const long long cells = static_cast<long long>(out_rows) * L.query_heads;
+        const float ds_unit = ds_scale<T>(bounds);
         uint32_t entry = 0;
         bool ok = true;
         Work w;
@@ -432,8 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(&sm.b_full[sb], (entry / Smem::kB) & 1)) { ok = false; break; }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    sm.lse[sb][32 * i + lane] = f[i].x;
-                    sm.delta[s][32 * i + lane] = f[i].y - (more[i].x + more[i].y);
+                    sm.lse[sb][32 * i + lane] = f[i].x + weight_shift<T>();
+                    sm.delta[s][32 * i + lane] = (f[i].y - (more[i].x + more[i].y)) * ds_unit;
                 }
                 zero_rows<BOXES>(smem_u32(sm.ring_b[sb]), round16(n), keep, lane);
                 fence_proxy_async_smem();
@@ -448,6 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t s_at = tmem + lanes + side * 64, dp_at = s_at + 128;
         const float2 sl22 = make_float2(L.scale * kLog2e, L.scale * kLog2e);
+        const float ds_unit = ds_scale<T>(bounds);
+        const float2 ds_unit2 = make_float2(ds_unit, ds_unit);
         uint32_t j_all = 0, works = 0;
         bool ok = true;
         Work w;
@@ -501,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
                         const float4 d = delta[8 * c + i / 4];
-                        float2 x = __fadd2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(d.x, d.y));
-                        float2 y = __fadd2_rn(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), make_float2(d.z, d.w));
+                        float2 x = centred<T>(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), ds_unit2, make_float2(d.x, d.y));
+                        float2 y = centred<T>(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), ds_unit2, make_float2(d.z, d.w));
                         x = __fmul2_rn(p[16 * c + i / 2], x);
                         y = __fmul2_rn(p[16 * c + i / 2 + 1], y);
                         packed[i / 2] = Type<T>::pack(x.x, x.y);
@@ -523,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const HeadsView &v = side ? L.d_k : L.d_v;
             T *out = static_cast<T *>(v.data) + (static_cast<long long>(w.k0) + row) * v.row + w.head * v.head;
-            store_sums<T>(tmem + lanes + 256 + side * 128, dim, side ? L.scale : 1.0f, blocks != 0, !live, mine, out);
+            store_sums<T>(tmem + lanes + 256 + side * 128, dim, weight_unit<T>() * (side ? L.scale / ds_unit : 1.0f), blocks != 0, !live, mine, out);
             tc_fence_before();
         }
     }
@@ -546,8 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename T, int BOXES>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ AttentionLaunch L, const __grid_constant__ Maps M, int rows_per_tile,
-              int out_rows, const float2 *stats, float *ds_sums, float *partials, long long tiles, Split cut,
-              unsigned long long *counter) {
+              int out_rows, const float2 *stats, float *ds_sums, const Bounds *bounds, float *partials, long long tiles,
+              Split cut, unsigned long long *counter) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     using Smem = Storage<BOXES>;
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
@@ -671,7 +751,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r_in = m_row / group, head_in = m_row - r_in * group;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t dp_at = tmem + lanes + 256 + side * 64;
-        const float sl2 = L.scale * kLog2e;
+        const float sl2 = L.scale * kLog2e, ds_unit = ds_scale<T>(bounds);
+        const float2 ds_unit2 = make_float2(ds_unit, ds_unit);
         uint32_t j_all = 0, works = 0;
         bool ok = true;
         Work w;
@@ -681,6 +762,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float2 st = make_float2(-INFINITY, 0.0f);
             if (mine)
                 st = __ldcg(stats + stat_at(L, out_rows, w.head, static_cast<long long>(w.o0) + r_in) + head_in);
+            st.x += weight_shift<T>();
+            st.y *= ds_unit;
             const float2 sl22 = make_float2(sl2, sl2), shift = make_float2(st.x, st.x), delta = make_float2(st.y, st.y);
             float2 ds_sum = make_float2(0.0f, 0.0f);
             for (int j = 0; j < blocks; ++j, ++j_all) {
@@ -716,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t keep = whole ? 0xffffffffu : sm.bits[j_all & 3][2 * side + c];
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
-                        float2 x = __fadd2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), delta);
+                        float2 x = centred<T>(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), ds_unit2, delta);
                         x = __fmul2_rn(p[16 * c + i / 2], x);
                         if (!whole) {
                             x.x = (keep >> i) & 1u ? x.x : 0.0f;
@@ -746,17 +829,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int head = w.head * group + head_in;
             if (mine)
                 ds_sums[static_cast<long long>(2 * w.part + side) * out_rows * L.query_heads +
-                        stat_at(L, out_rows, w.head, static_cast<long long>(w.o0) + r_in) + head_in] = ds_sum.x + ds_sum.y;
+                        stat_at(L, out_rows, w.head, static_cast<long long>(w.o0) + r_in) + head_in] =
+                    (ds_sum.x + ds_sum.y) * (weight_unit<T>() / ds_unit);
             // The sides take half of the row's columns each, in whole 16s.
             const int half = (dim / 2 + 15) & ~15;
             const int first = side ? half : 0, count = side ? dim - half : min(half, dim);
             const uint32_t sums = tmem + lanes + 384 + first;
             if (partials) {
                 float *out = partials + ((static_cast<long long>(w.part) * out_rows + w.o0 + r_in) * L.query_heads + head) * dim + first;
-                store_partials(sums, count, blocks != 0, mine, out);
+                store_partials(sums, count, weight_unit<T>() / ds_unit, blocks != 0, mine, out);
             } else {
                 T *out = static_cast<T *>(L.d_q.data) + (static_cast<long long>(w.q0) + r_in) * L.d_q.row + head * L.d_q.head + first;
-                store_sums<T>(sums, count, L.scale, blocks != 0, false, mine, out);
+                store_sums<T>(sums, count, weight_unit<T>() * (L.scale / ds_unit), blocks != 0, false, mine, out);
             }
             tc_fence_before();
         }
@@ -844,6 +928,7 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
     const int rows_per_tile = 128 / L.group;
     const int out_rows = L.query_rows * (L.q_off ? 1 : L.items);
     unsigned long long *counters = reinterpret_cast<unsigned long long *>(L.workspace);
+    Bounds *bounds = reinterpret_cast<Bounds *>(reinterpret_cast<uint32_t *>(L.workspace) + kBoundsAt);
     const Cut c = cut_of(L);
     uint8_t *at = L.workspace + kCounterBytes;
     float2 *stats = reinterpret_cast<float2 *>(at);
@@ -859,7 +944,7 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
     const long long blocks = (static_cast<long long>(out_rows) + 7) / 8, most = 8ll * L.sm_count;
     begin_kernel<<<1, 32, 0, stream>>>(L.status, counters);
     cudaError_t e = launch_after(stats_kernel<T>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, stream, L,
-                                 out_rows, stats);
+                                 out_rows, stats, bounds);
     if (e != cudaSuccess) return e;
 
     const size_t smem = sizeof(Storage<BOXES>);
@@ -871,8 +956,8 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     auto grid = [&](long long tiles) { return static_cast<unsigned>(tiles < L.sm_count ? tiles : L.sm_count); };
     const long long q_tiles = c.slots * c.split.parts * L.key_heads;
-    e = launch_after(dq, dim3(grid(q_tiles)), kThreads, smem, stream, L, M, rows_per_tile, out_rows, stats, ds_sums, partials,
-                     q_tiles, c.split, counters);
+    e = launch_after(dq, dim3(grid(q_tiles)), kThreads, smem, stream, L, M, rows_per_tile, out_rows, stats, ds_sums, bounds,
+                     partials, q_tiles, c.split, counters);
     if (e != cudaSuccess) return e;
     if (c.split.parts > 1) {
         e = launch_after(ds_sum_kernel, dim3(static_cast<unsigned>((2 * cells_of(L) + 255) / 256)), 256, 0, stream, ds_sums,
@@ -880,8 +965,8 @@ cudaError_t launch(const AttentionLaunch &L, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     const long long k_tiles = (static_cast<long long>(L.key_rows) / 128 + L.items) * L.key_heads;
-    e = launch_after(dkv, dim3(grid(k_tiles)), kThreads, smem, stream, L, M, rows_per_tile, out_rows, stats, ds_sums, k_tiles,
-                     counters + 1);
+    e = launch_after(dkv, dim3(grid(k_tiles)), kThreads, smem, stream, L, M, rows_per_tile, out_rows, stats, ds_sums, bounds,
+                     k_tiles, counters + 1);
     if (e != cudaSuccess) return e;
     if (partials) dq_sum_kernel<T><<<static_cast<unsigned>(joins_of(L)), 256, 0, stream>>>(L, c.sums, partials);
     return cudaGetLastError();

@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(128 + 128 * TILES, 3 - TILES)
             __syncwarp();
             if constexpr (CUT) {   // the sums as they are, and what they are relative to
                 const long long cell = (static_cast<long long>(p.o0) + row) * L.query_heads + head;
-                store_partials(o_at, dim, blocks != 0, mine, part_o + cell * dim);
+                store_partials(o_at, dim, 1.0f, blocks != 0, mine, part_o + cell * dim);
                 if (mine) part_ml[cell] = make_float2(m * sl2, l);
             } else {
                 T *out = static_cast<T *>(L.o.data) + (static_cast<long long>(p.o0) + row) * L.o.row + head * L.o.head;

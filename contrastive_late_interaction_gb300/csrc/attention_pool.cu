@@ -443,6 +443,9 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
     const int head = static_cast<int>(id % L.key_heads), dim = L.head_dim;
     const long long worker = id / L.key_heads;
     const float sl2 = L.scale * kLog2e;
+    // fp16: what dS is multiplied by on its way through the products, P's 2^14 among it.  A power of two that follows the
+    // largest dS that the warp has met: that goes in between 2^7 and 2^15.
+    float unit = weight_unit<T>() == 1.0f ? 1.0f : 0.0f;   // 0: none met yet
     float dq[KC][2][NT][4];
     auto clear = [&]() {
 #pragma unroll
@@ -454,6 +457,7 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
     };
     // dq[c][i][n]: elements 32 c + 8 (g / 2) + 4 i + (g % 2), and two further on, of rows 8 n + 2 t, 2 t + 1.
     auto write = [&](long long slot, int rows) {
+        const float back = unit == 0.0f ? 1.0f : weight_unit<T>() / unit;
         const long long at = (slot * L.key_heads + head) * (static_cast<long long>(L.max_q) * L.group);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -467,8 +471,8 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
                     if (32 * c + 8 * (g >> 1) >= dim) continue;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        p[32 * c + 4 * i] = dq[c][i][n][r];
-                        p[32 * c + 4 * i + 2] = dq[c][i][n][r + 2];
+                        p[32 * c + 4 * i] = dq[c][i][n][r] * back;
+                        p[32 * c + 4 * i + 2] = dq[c][i][n][r + 2] * back;
                     }
                 }
             }
@@ -476,9 +480,9 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
     clear();
     for (long long slot = worker; slot < slots; slot += stride) {
         const Unit u = find_unit(L, chunk, slot, head, lane);
-        const long long unit = slot * L.key_heads + head;
+        const long long slot_unit = slot * L.key_heads + head;
         if (u.rows == 0) {
-            if (lane == 0) notes.steps[unit] = 0;
+            if (lane == 0) notes.steps[slot_unit] = 0;
             // an item without queries still has gradients to write, of zero
             if (u.item.ok && u.n > 0) {
                 for (int s = g; s < u.n; s += 8)
@@ -523,7 +527,7 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
             d += __shfl_xor_sync(0xffffffffu, d, 2);
             const int rr = row / L.group, h = head * L.group + row - rr * L.group;
             const float e = on ? L.lse[static_cast<long long>(u.item.o0 + rr) * L.query_heads + h] : -INFINITY;
-            const float e2 = e == -INFINITY ? INFINITY : e * kLog2e;   // no kept state: p is 0
+            const float e2 = e == -INFINITY ? INFINITY : e * kLog2e - weight_shift<T>();   // no kept state: p is 0
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 lse[n][r] = __shfl_sync(0xffffffffu, e2, 4 * (2 * t + r));
@@ -561,6 +565,7 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
                 auto &vr = vr0[x];
                 uint32_t p[NT][4], ds[NT][4];   // of states g and g + 8: high halves, then low ones
                 bool large0 = false, large1 = false;
+                float met = 0.0f, des[NT][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -581,18 +586,45 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
                     }
                     ds_sum[n][0] += de[0] + de[2];
                     ds_sum[n][1] += de[1] + de[3];
-                    large0 |= fmaxf(pe[0], pe[1]) >= kLarge;
-                    large1 |= fmaxf(pe[2], pe[3]) >= kLarge;
+                    large0 |= fmaxf(pe[0], pe[1]) >= kLarge / weight_unit<T>();
+                    large1 |= fmaxf(pe[2], pe[3]) >= kLarge / weight_unit<T>();
                     split_pair<T>(pe[0], pe[1], p[n][0], p[n][2]);
                     split_pair<T>(pe[2], pe[3], p[n][1], p[n][3]);
-                    split_pair<T>(de[0], de[1], ds[n][0], ds[n][2]);
-                    split_pair<T>(de[2], de[3], ds[n][1], ds[n][3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        des[n][i] = de[i];
+                        if constexpr (!Type<T>::bf16) met = fmaxf(met, fabsf(de[i]));
+                    }
+                }
+                if constexpr (!Type<T>::bf16) {
+                    const bool grow = met * unit > 32768.0f, first = unit == 0.0f && met > 0.0f;
+                    if (__any_sync(0xffffffffu, (grow || first) && met < INFINITY)) {
+                        if (!(met < INFINITY)) met = 0.0f;   // its results are not finite anyway
+                        for (int w = 16; w; w >>= 1) met = fmaxf(met, __shfl_xor_sync(0xffffffffu, met, w));
+                        const int e = max(min(7 - exponent_of(met), 100), -100);
+                        const float now = power_of_two(e), change = unit == 0.0f ? 1.0f : now / unit;
+                        unit = now;
+#pragma unroll
+                        for (int c = 0; c < KC; ++c)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                    for (int r = 0; r < 4; ++r) dq[c][i][n][r] *= change;
+                    }
+                }
+                const float back = unit == 0.0f ? 1.0f : weight_unit<T>() / unit;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    split_pair<T>(des[n][0] * unit, des[n][1] * unit, ds[n][0], ds[n][2]);
+                    split_pair<T>(des[n][2] * unit, des[n][3] * unit, ds[n][1], ds[n][3]);
                 }
                 if (__any_sync(0xffffffffu, large0 || large1)) {   // fold the four lanes of a state
                     uint32_t m0 = __ballot_sync(0xffffffffu, large0), m1 = __ballot_sync(0xffffffffu, large1);
                     m0 |= m0 >> 1, m1 |= m1 >> 1;
                     m0 |= m0 >> 2, m1 |= m1 >> 2;
-                    if (lane == 0) notes.states[unit * kSteps + (j >> 4)] = (m0 & 0x11111111u) | (m1 & 0x11111111u) << 1;
+                    if (lane == 0) notes.states[slot_unit * kSteps + (j >> 4)] = (m0 & 0x11111111u) | (m1 & 0x11111111u) << 1;
                     noted |= 1u << (j >> 4);
                 }
 #pragma unroll
@@ -619,8 +651,8 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
                         uint32_t wv[4], wk[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            wv[i] = live ? Type<T>::pack(av[i][2 * y], av[i][2 * y + 1]) : 0u;
-                            wk[i] = live ? Type<T>::pack(ak[i][2 * y] * L.scale, ak[i][2 * y + 1] * L.scale) : 0u;
+                            wv[i] = live ? Type<T>::pack(av[i][2 * y] * weight_unit<T>(), av[i][2 * y + 1] * weight_unit<T>()) : 0u;
+                            wk[i] = live ? Type<T>::pack(ak[i][2 * y] * (L.scale * back), ak[i][2 * y + 1] * (L.scale * back)) : 0u;
                         }
                         if (32 * c + 8 * t < dim && 8 * y + g < count) {
                             __stcs(reinterpret_cast<uint4 *>(dvbase + row * L.d_v.row + 32 * c), make_uint4(wv[0], wv[1], wv[2], wv[3]));
@@ -656,9 +688,10 @@ __global__ void __launch_bounds__(kWarps / NT * 32, 3)
                 float e = ds_sum[n][r];
                 for (int w = 4; w < 32; w <<= 1) e += __shfl_xor_sync(0xffffffffu, e, w);
                 const int row = 8 * n + 2 * t + r;
-                if (g == 0 && row < u.rows) notes.sums[unit * (static_cast<long long>(L.max_q) * L.group) + row] = e;
+                if (g == 0 && row < u.rows)
+                    notes.sums[slot_unit * (static_cast<long long>(L.max_q) * L.group) + row] = e * weight_unit<T>();
             }
-        if (lane == 0) notes.steps[unit] = noted;
+        if (lane == 0) notes.steps[slot_unit] = noted;
         if (L.q_off) {
             write(slot, u.rows);
             clear();

@@ -235,3 +235,50 @@ def test_gradient_of_a_dominating_state_on_tiles(cli, q_len, k_len, hq, hk, d, s
         bad = (got[ks] - want).abs() > bound
         assert not bad.any(), (int(bad.sum()), ((got[ks] - want).abs() / bound).max().item())
     assert largest > 0.9
+
+
+def half_case(q_len, k_len, hq, hk, d, shared, seed, q_scale, k_scale, v_scale):
+    g = gen(seed)
+    rows_q, rows_k = (q_len if shared else sum(q_len)), sum(k_len)
+    q, k, v = (rand(g, n, h, d, dtype=F16, scale=s) for n, h, s in ((rows_q, hq, q_scale), (rows_k, hk, k_scale), (rows_k, hk, v_scale)))
+    d_o = torch.randn(rows_q * len(k_len) if shared else rows_q, hq, d, generator=g, device="cuda")
+    qo, ko = None if shared else offsets(q_len), offsets(k_len)
+    kw = dict(max_query_rows=rows_q if shared else max(q_len), max_key_rows=max(k_len))
+    return q, qo, k, v, ko, d_o, kw
+
+
+HALVES = [([200], [4096], 2, 2, 64, False), ([40, 3, 300], [700, 1000, 90], 4, 2, 72, False),
+          (30, [500, 129], 2, 2, 128, True), ([1, 2], [4096, 300], 2, 2, 64, False), ([4] * 8, [900] * 8, 12, 4, 128, False),
+          (1, [3000, 40] * 4, 8, 8, 64, True)]
+
+
+@pytest.mark.parametrize("case", range(len(HALVES)))
+def test_half_precision_gradients_scale_with_the_output_gradient(cli, case):
+    """Gradients are linear in d_output.  A power of two in it changes no sum's digits, so that the results differ by
+    their own rounding alone: u of themselves, or half the smallest subnormal, on either side."""
+    q, qo, k, v, ko, d_o, kw = half_case(*HALVES[case], 90 + case, 2.0, 1.0, 1.0)
+    small = (d_o * 2.0 ** -12).to(F16)
+    f = cli.cross_attention(q, qo, k, v, ko, **kw)
+    a = cli.cross_attention_backward(q, qo, k, v, ko, f["output"], f["lse"], small, **kw)
+    b = cli.cross_attention_backward(q, qo, k, v, ko, f["output"], f["lse"], small * 2.0 ** 12, **kw)
+    u, tiny = ref.UNIT[F16], ref.TINY[F16]
+    for name in ("d_q", "d_k", "d_v"):
+        x, y = a[name].double(), b[name].double() * 2.0 ** -12
+        bound = u * (1 + u) * (x.abs() + y.abs()) + tiny * (1 + 2.0 ** -12)
+        bad = (x - y).abs() > bound
+        assert y.abs().max() > 0 and not bad.any(), (name, int(bad.sum()), ((x - y).abs() / bound).max().item())
+
+
+@pytest.mark.parametrize("q_len, shared", [([200, 30], False), ([1, 2], False), (1, True), (40, True)])
+def test_half_precision_gradients_of_large_values(cli, q_len, shared):
+    """Weights' gradients past the type's range, between inputs and results within it."""
+    k_len = [40, 25]
+    q, qo, k, v, ko, d_o, kw = half_case(q_len, k_len, 4, 2, 64, shared, 99, 1e-3, 1e-3, 1e4)
+    d_o = (60 * d_o).to(F16)
+    f = cli.cross_attention(q, qo, k, v, ko, **kw)
+    b = cli.cross_attention_backward(q, qo, k, v, ko, f["output"], f["lse"], d_o, **kw)
+    want = ref.attention(q, k, v, None if shared else q_len, k_len, 0.125, d_o=d_o, shared=shared, dtype=F16)
+    for name in ("d_q", "d_k", "d_v"):
+        value, bound = want[name]
+        assert value.abs().max() < 65504
+        assert ((b[name].double() - value).abs() <= bound).all() and b[name].isfinite().all(), name
