@@ -4,6 +4,7 @@ positions, values that only some rows hold."""
 import pytest
 import torch
 
+import states_delta as sd
 import states_reference as ref
 
 pytestmark = pytest.mark.gpu
@@ -282,3 +283,31 @@ def test_half_precision_gradients_of_large_values(cli, q_len, shared):
         value, bound = want[name]
         assert value.abs().max() < 65504
         assert ((b[name].double() - value).abs() <= bound).all() and b[name].isfinite().all(), name
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("group", [1, 4])
+@pytest.mark.parametrize("case", range(len(sd.CASES)))
+def test_few_rows_notes_the_states_that_it_says(cli, case, group, dtype):
+    """dK where a state's share of delta's error is kept up to the weight at which states are noted, and not above it."""
+    rows, k_len, d = sd.CASES[case]
+    if rows % group:
+        pytest.skip("no whole query rows")
+    g, nq, hk = gen(500 + case), rows // group, 2
+    q_len = [nq] * len(k_len)
+    q, d_o = (rand(g, sum(q_len), hk * group, d, dtype=dtype, scale=s) for s in (4.0, 1.0))
+    k, v = (rand(g, sum(k_len), hk, d, dtype=dtype) for _ in range(2))
+    kw = dict(max_query_rows=nq, max_key_rows=max(k_len))
+    f = cli.cross_attention(q, offsets(q_len), k, v, offsets(k_len), **kw)
+    got = cli.cross_attention_backward(q, offsets(q_len), k, v, offsets(k_len), f["output"], f["lse"], d_o, **kw)["d_k"].double()
+    ka, largest = 0, 0.0
+    for i, n in enumerate(k_len):
+        for h in range(hk):
+            rows_of = lambda t: t[i * nq:(i + 1) * nq, h * group:(h + 1) * group].double().reshape(rows, d)  # noqa: E731
+            ki, vi = k[ka:ka + n, h].double(), v[ka:ka + n, h].double()
+            want, bound, _ = sd.item(rows_of(q), ki, vi, rows_of(d_o), rows_of(f["output"]), d ** -0.5, sd.large_weight(rows), dtype)
+            ratio = ((got[ka:ka + n, h] - want).abs() / bound).max().item()
+            assert ratio <= 1, (i, h, ratio)
+            largest = max(largest, ((got[ka:ka + n, h] - want).abs().max() / want.pow(2).mean().sqrt()).item())
+        ka += n
+    print(f"largest error {largest:.3f} of the root mean square")
