@@ -920,6 +920,8 @@ def _attention_sizes(q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_r
     """The struct's words up to `v`, and the number of items."""
     q_shape, k_shape, dtype = _states(q, "q"), _states(k, "k"), q.dtype
     (rows_q, hq, dim), (rows_k, hk, _) = q_shape, k_shape
+    if k_offsets is None:
+        raise InvalidArgumentError(CLI_INVALID_ARGUMENT, "k_offsets are needed")
     items = k_offsets.numel() - 1
     max_q = rows_q if max_query_rows is None else max_query_rows
     max_k = rows_k if max_key_rows is None else max_key_rows
@@ -962,6 +964,8 @@ def cross_attention_backward_workspace_bytes(q, q_offsets, k, v, k_offsets, key_
 
 
 def _lse_ptr(lse, rows, heads):
+    if lse is None:
+        raise InvalidArgumentError(CLI_INVALID_ARGUMENT, "lse is needed: the forward's, with want_lse")
     if list(lse.shape) != [rows, heads]:
         raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"lse must be [{rows}, {heads}], packed")
     return _vector(lse, "lse", rows * heads, torch.float32)

@@ -185,3 +185,13 @@ def test_the_packages_names_follow_the_binding(box, monkeypatch):
     other = lambda *a: None  # noqa: E731
     monkeypatch.setattr(box.b, "rotary_table", other)
     assert cli.rotary_table is other
+
+
+def test_what_a_call_cannot_do_without_is_asked_for(box):
+    b = box.b
+    q, off = tensor(4, 2, 8, dtype=BF16), tensor(3, dtype=I64)
+    with pytest.raises(b.InvalidArgumentError):
+        b.cross_attention_backward(q, off, q, q, off, q, None, q)     # a forward without want_lse gives None
+    with pytest.raises(b.InvalidArgumentError):
+        b.cross_attention(q, off, q, q, None)
+    assert not box.launched
