@@ -797,17 +797,17 @@ def _part(name, t, positions, gain, dim, dtype):
 
 
 _NO_PART = (0,) * 17
+_NO_WORKSPACE = 0, 0
 
 
-def _rotary_call(verb, lead, q_part, k_part, table, interleaved, epsilon, workspace, status):
+def _rotary_call(verb, lead, q_part, k_part, table, interleaved, epsilon, lent, status):
     if table.dtype is not torch.float32 or not table.is_cuda:
         _check_cuda(table, "table", torch.float32)
     shape = table.shape
     if len(shape) != 3 or shape[2] != 2 or not table.is_contiguous():
         raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{verb}: table must be [positions, rotary_dim / 2, 2], packed")
-    ws, ws_bytes = _lent(workspace)
     rc = _ROTARY[verb](_pack_rotary.pack(DTYPES[lead.dtype], 1 if interleaved else 0, lead.shape[2], 2 * shape[1],
-                                         table.data_ptr(), shape[0], epsilon, *q_part, *k_part, ws, ws_bytes,
+                                         table.data_ptr(), shape[0], epsilon, *q_part, *k_part, *lent,
                                          status.data_ptr(), _raw_stream(lead)))
     if rc:
         raise_for(rc, verb)
@@ -835,7 +835,7 @@ def rotary_heads(q, table, positions=None, k=None, k_positions=None, interleaved
     yq, q_part = _rotate_part(out, "q", q, positions, None, dim, dtype, False)
     yk, k_part = _rotate_part(out, "k", k, k_positions, None, dim, dtype, False)
     st = _status(device_status, q)
-    _rotary_call("rotary_heads", q, q_part, k_part, table, interleaved, 0.0, None, st)
+    _rotary_call("rotary_heads", q, q_part, k_part, table, interleaved, 0.0, _NO_WORKSPACE, st)
     return {"q": yq, "k": yk, "device_status": st}
 
 
@@ -848,7 +848,7 @@ def rotary_heads_backward(d_q, table, positions=None, d_k=None, k_positions=None
     xq, q_part = _rotate_part(out, "d_q", d_q, positions, None, dim, dtype, True)
     xk, k_part = _rotate_part(out, "d_k", d_k, k_positions, None, dim, dtype, True)
     st = _status(device_status, d_q)
-    _rotary_call("rotary_heads_backward", d_q, q_part, k_part, table, interleaved, 0.0, None, st)
+    _rotary_call("rotary_heads_backward", d_q, q_part, k_part, table, interleaved, 0.0, _NO_WORKSPACE, st)
     return {"d_q": xq, "d_k": xk, "device_status": st}
 
 
@@ -862,7 +862,7 @@ def norm_rotary_heads(q, table, positions=None, q_gain=None, k=None, k_positions
     yq, q_part = _rotate_part(out, "q", q, positions, q_gain, dim, dtype, False)
     yk, k_part = _rotate_part(out, "k", k, k_positions, k_gain, dim, dtype, False)
     st = _status(device_status, q)
-    _rotary_call("norm_rotary_heads", q, q_part, k_part, table, interleaved, epsilon, None, st)
+    _rotary_call("norm_rotary_heads", q, q_part, k_part, table, interleaved, epsilon, _NO_WORKSPACE, st)
     return {"q": yq, "k": yk, "device_status": st}
 
 
@@ -885,8 +885,12 @@ def norm_rotary_heads_backward(q, d_q, table, positions=None, q_gain=None, k=Non
     xk, k_part, gk = _norm_grad_part(out, "k", k, d_k, k_positions, k_gain, dim, dtype)
     st = _status(device_status, q)
     if workspace is None and (gq is not None or gk is not None):
-        workspace = _ws(lib.norm_rotary_heads_backward_workspace_bytes(dim), q.device)
-    _rotary_call("norm_rotary_heads_backward", q, q_part, k_part, table, interleaved, epsilon, workspace, st)
+        need = lib.norm_rotary_heads_backward_workspace_bytes(dim)
+        workspace = _ws(need, q.device)
+        lent = workspace.data_ptr(), need
+    else:
+        lent = _lent(workspace)
+    _rotary_call("norm_rotary_heads_backward", q, q_part, k_part, table, interleaved, epsilon, lent, st)
     return {"d_q": xq, "d_q_gain": gq, "d_k": xk, "d_k_gain": gk, "device_status": st}
 
 
@@ -976,8 +980,10 @@ def cross_attention(q, q_offsets, k, v, k_offsets, key_mask=None, scale=None, ma
     """Every query row of `q` [rows, heads, dim] attends to the states `k`, `v` [states, key_heads, dim] of its item
     on the tapes `q_offsets`, `k_offsets` (int64 [items + 1]).  q_offsets None: all of `q` belongs to every item, and
     the outputs have items * rows rows.  `key_mask` (uint8 or bool [states]) drops states where it is 0; `scale`
-    defaults to dim^-0.5; the two maxima bound the items' rows (default: the tapes').  bf16 or fp16.  Returns
-    dict(output, lse, device_status), lse fp32 [output rows, heads] or None."""
+    defaults to dim^-0.5; the two maxima bound the items' rows.  They choose the kernels, and their default, the tapes'
+    rows, chooses those for long items: pass the longest item's where items are short (2048 items of one query each go
+    through tiles of 128 rows otherwise).  bf16 or fp16.  Returns dict(output, lse, device_status), lse fp32 [output
+    rows, heads] or None."""
     if stream is not None:
         return _on(stream, cross_attention, locals())
     head, items = _attention_sizes(q, q_offsets, k, v, k_offsets, key_mask, scale, max_query_rows, max_key_rows)
