@@ -377,6 +377,9 @@ __device__ __forceinline__ void store_partials(uint32_t sums, int dim, float sca
     }
 }
 
+// The cuts go by the 152 SMs of a GB300 rather than by the device's own count, so that the sizers, which are asked without a
+// device, come to the same as the launches; on fewer SMs they are right and only larger than they need to be.
+//
 // How a call's items are cut along their states where there are too few blocks
 // of queries to go round: `parts` chunks of `chunk` states (a multiple of 128)
 // each, as many as give `ctas` CTAs a block, of about `least` states at least.

@@ -40,11 +40,11 @@
 // P is rounded to 16 bits because the product takes it so; l sums the weights
 // before that.
 //
-// Bound: 8 items of 2048 x 4096 rows, 16 heads of 128, run at 1400 TFLOP/s (75%
+// Bound: 8 items of 2048 x 4096 rows, 16 heads of 128, run at 1460 TFLOP/s (75%
 // of measured), where the two tiles' softmax (about 1700 cycles a block of each,
 // half of it exponentials) and products (2100 for both) take turns; 2048 x
 // 1024 at 1280, the rest being the rows' way out at every item's end; 64 x 4096
-// at 5.5 TB/s, bound by HBM.
+// at 4.9 TB/s, bound by HBM.
 
 #include <cuda.h>
 

@@ -28,10 +28,10 @@
 // parts in a fixed order; results do not depend on the order of execution.
 //
 // Bound: HBM.  2048 items of 64 to 512 states, one shared query, 16 heads of
-// 64: 357 us (6.8 TB/s); 512 of 32 to 1024, 8 heads of 128: 185 us (6.1 TB/s)
-// and 440 for the backward (5.0 TB/s, reads and writes mixed; 17 of it are the
-// joins and mends).  One row against
-// 4096 states, 8 heads on 2: 4.8 us and 4.5 for the join, both latency.
+// 64: 364 us (6.6 TB/s); 512 of 32 to 1024, 8 heads of 128: 185 us (6.0 TB/s)
+// and 432 for the backward (5.1 TB/s, reads and writes mixed; 413 without the
+// noting and mending of dK).  One row against 4096 states, 8 heads on 2: 12 us in two
+// launches, both latency.
 
 #include "attention.cuh"
 
@@ -416,8 +416,10 @@ __global__ void __launch_bounds__(256)
 // row sum p (dp - delta) is 0, and what it is instead is delta's error.
 // States with a weight of 1/8 or more in some row, or 1/4 with more than 8 rows,
 // whose share of an element is less, are noted, and mend() computes their dK
-// again with the right delta (with 1/16 for all, 512 x 32 to 1024 states, 16
-// rows, 16 heads of 64 took 1287 us, twice what they take without).
+// again with the right delta (512 x 32 to 1024 states, 16 rows, 16 heads of 64:
+// 873 us, 848 without; with 1/16 for all 976).  dQ keeps the first delta: its
+// error is up to twice that of one rounding (0.0028 to 0.0033 of the norm in
+// bf16, with sharp rows).
 constexpr float large_weight(int tiles) { return tiles == 1 ? 0.125f : 0.25f; }
 
 // What the backward leaves for mend(): of each unit, the sums of ds of its
@@ -973,9 +975,10 @@ cudaError_t dispatch(const AttentionLaunch &L, bool back, cudaStream_t stream) {
 // the forward's tensor cores are ahead from some states on (16 rows, 8 heads of
 // 128: 1 x 4096 states 13.8 us here and 16.3 there, 1 x 8192 27 and 18; 32 x
 // 256 of 64: 16.6 and 11.6; 32 x 2048: 60 and 34; 512 x 32 to 1024 shared, 16
-// heads of 64: 301 and 290; with 9 rows, 260).  The backward is ahead here in
-// long items (64 x 4096, 8 heads of 64: 320 us and 434; 32 x 2048: 110 and 126)
-// and behind in short ones (the last: 925 us and 875).
+// heads of 64: 301 and 290; with 9 rows, 260).  The backward is ahead here (1 x
+// 4096, 8 heads of 128: 18.5 us and 32.8; 8 heads of 64: 32 x 256 28.5 and 37,
+// 64 x 4096 288 and 416; 512 x 32 to 1024, 16 heads of 64: 863 and 977, 725 and
+// 972 with rows of their own).
 bool few_rows(const AttentionLaunch &L, bool back) {
     const long long rows = static_cast<long long>(L.max_q) * L.group;
     return rows <= 8 || (rows <= 16 && (back || static_cast<long long>(L.key_rows) * L.key_heads <= 32768));

@@ -18,9 +18,13 @@
 // shared memory (cp.async; a step is 32 / (lanes per head) heads of a row), so
 // some 100 KB an SM are under way; the rest go through heads_kernel.  Measured
 // in bf16: the norm with rotation of 270336 rows, 32 heads of 64, 355 us (6.2
-// TB/s), the gradient of 131072 rows, 16 heads of 128, 271 us (5.9 TB/s); in fp32
-// the rotation of 20011 rows, 10 heads of 80, 31 us (4.3 TB/s: too short a call
-// to fill and drain).
+// TB/s), the gradient of 131072 rows, 16 heads of 128, 279 us (5.8 TB/s).  A step
+// does not span rows, so a part with few heads leaves lanes idle: in fp32 the
+// rotation of 20011 rows, 8 + 2 heads of 80 (four a step), takes 34 us (3.7
+// TB/s), the norm with rotation of 100000 rows, 8 + 1 heads of 64 (eight a
+// step), 184 us (1.3 TB/s).  heads_kernel: 131072 rows, 16 heads of 128, 100 of
+// each rotated, 251 us (4.3 TB/s), the gradient 700 (2.3 TB/s); 102 rotated, in
+// chunks of one, 326 us.
 //
 // The gain's gradient: a lane sums its slots over the heads and rows it sees
 // in registers, a block adds its lanes' sums in a fixed order into one row of
@@ -567,7 +571,10 @@ __global__ void __launch_bounds__(256) table_kernel(float2 *table, long long cel
     }
 }
 
-// Blocks of the parts, in proportion to what they move, at least one each.
+// Blocks of the parts, in proportion to the heads that they move, at least one
+// each.  A warp's time goes by its steps, rows * ceil(heads / heads a step), so
+// that a part whose heads do not fill a step has too few blocks (20011 rows, 8 + 2
+// heads of 80: 28 steps a warp for the keys, 14 for the queries).
 void split(RotaryLaunch &L, int rows_a_block, int most, int &blocks) {
     long long work[2], want[2];
     for (int p = 0; p < 2; ++p) {

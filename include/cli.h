@@ -603,17 +603,19 @@ size_t norm_rotary_heads_backward_workspace_bytes(size_t head_dim);
  *                    query_rows); outputs' rows < 2^31 too
  *   query_offsets, key_offsets   device uint64 [items + 1]; malformed ones set
  *                    CLI_MALFORMED, as does an item longer than the two below
- *   max_query_rows, max_key_rows   at least the longest item's rows: they choose
- *                    the kernel and the split of long items (the tape's rows
- *                    always do)
+ *   max_query_rows, max_key_rows   at least the longest item's rows.  They choose
+ *                    the kernel and the split of long items: the tape's rows
+ *                    always do as a bound, but with them a call on items of one
+ *                    row each takes the kernels for tiles of 128
  *   key_mask         device uint8 [key_rows], 0 drops a state (its k and v may
  *                    hold anything, NaN included); NULL keeps all
  *   scale            finite
- *   q, k, v          row strides of at least head_dim; see cli_heads_t
+ *   q, k, v, d_output   row and head strides of at least head_dim (no broadcast
+ *                    rows or heads); see cli_heads_t
  *   output           written by the forward, read by the backward
  *   lse              device fp32 [output rows][query_heads], packed; written by
  *                    the forward (NULL: not wanted), read by the backward
- *   d_output         read by the backward
+ *   d_output         read by the backward; as an output of the forward's rows
  *   d_q, d_k, d_v    written by the backward: the inputs' type, sums in 32 bits
  *                    rounded once; zeros for dropped states
  *   workspace        device, >= the verb's *_workspace_bytes of the same
