@@ -354,6 +354,8 @@ __global__ void __launch_bounds__(128 + 128 * TILES, 3 - TILES)
         for (uint32_t it = 0; ok && next_pair(it, p); ++it) {
             const int blocks = (p.nk + 127) / 128;
             if (t * rows_per_tile >= p.rows) continue;
+            const int row = t * rows_per_tile + r_in;
+            const bool mine = in_tile && row < p.rows;
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < blocks; ++j) {
                 if (!wait(&sm.s_full[t], phase)) { ok = false; break; }
@@ -381,8 +383,9 @@ __global__ void __launch_bounds__(128 + 128 * TILES, 3 - TILES)
                     tmem_regs_ready(b, top1);
                     top = fmaxf(fmaxf(top, top1), top2);
                 }
-                // The reference follows the maximum only when that has grown past 2^8.
-                if (__any_sync(0xffffffffu, top > m + lazy || (m == -INFINITY && top > m))) {
+                // The reference follows the maximum only when that has grown past 2^8, in some row of the item's: rows of
+                // the tile that are another's, or hold what was there before, have no say in it.
+                if (__any_sync(0xffffffffu, mine && (top > m + lazy || (m == -INFINITY && top > m)))) {
                     const float m1 = fmaxf(m, top);
                     const float c = m1 > m ? ex2((m - m1) * sl2) : 1.0f;
                     m = m1;
@@ -447,8 +450,7 @@ __global__ void __launch_bounds__(128 + 128 * TILES, 3 - TILES)
                 o_phase ^= 1;
                 tc_fence_after();
             }
-            const int row = t * rows_per_tile + r_in, head = p.head * group + head_in;
-            const bool mine = in_tile && row < p.rows;
+            const int head = p.head * group + head_in;
             __syncwarp();
             if constexpr (CUT) {   // the sums as they are, and what they are relative to
                 const long long cell = (static_cast<long long>(p.o0) + row) * L.query_heads + head;

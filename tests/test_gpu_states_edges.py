@@ -311,3 +311,50 @@ def test_few_rows_notes_the_states_that_it_says(cli, case, group, dtype):
             largest = max(largest, ((got[ka:ka + n, h] - want).abs().max() / want.pow(2).mean().sqrt()).item())
         ka += n
     print(f"largest error {largest:.3f} of the root mean square")
+
+
+# ----------------------------------------------------------------------------
+# rows that share a tile
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("q_len, k_len, group", [([45, 20], [700, 300], 9), ([150, 3], [260, 900], 1), ([33, 70], [2100, 64], 3),
+                                                 ([1, 2], [700, 300], 5), ([60, 5], [9000, 300], 1)])
+def test_an_items_bits_do_not_depend_on_the_rows_beside_it(cli, q_len, k_len, group, dtype):
+    """The second item's rows lie in the tiles that the first one's end in: large or small, they change no bit of it."""
+    g, hk = gen(61), 2
+    q, d_o = (rand(g, sum(q_len), hk * group, 64, dtype=dtype) for _ in range(2))
+    k, v = (rand(g, sum(k_len), hk, 64, dtype=dtype) for _ in range(2))
+    kw = dict(max_query_rows=max(q_len), max_key_rows=max(k_len))
+
+    def first(scale):
+        x, y = q.clone(), d_o.clone()
+        x[q_len[0]:] *= scale
+        f = cli.cross_attention(x, offsets(q_len), k, v, offsets(k_len), **kw)
+        b = cli.cross_attention_backward(x, offsets(q_len), k, v, offsets(k_len), f["output"], f["lse"], y, **kw)
+        return [t[:q_len[0]] for t in (f["output"], f["lse"], b["d_q"])] + [t[:k_len[0]] for t in (b["d_k"], b["d_v"])]
+    want = first(1.0)
+    for scale in (30.0, 1e-3):
+        for a, b in zip(want, first(scale)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("q_len, k_len, group", [([45, 40], [700, 300], 9), ([60], [3000], 7), ([200, 3], [400, 260], 3)])
+def test_results_do_not_depend_on_what_ran_before(cli, q_len, k_len, group):
+    """Groups that do not divide 128 leave rows of a tile without queries, which hold whatever was there."""
+    g, hk = gen(62), 2
+    q, d_o = (rand(g, sum(q_len), hk * group, 96) for _ in range(2))
+    k, v = (rand(g, sum(k_len), hk, 96) for _ in range(2))
+    kw = dict(max_query_rows=max(q_len), max_key_rows=max(k_len))
+
+    def both(q):
+        f = cli.cross_attention(q, offsets(q_len), k, v, offsets(k_len), **kw)
+        b = cli.cross_attention_backward(q, offsets(q_len), k, v, offsets(k_len), f["output"], f["lse"], d_o, **kw)
+        return [f["output"], f["lse"], b["d_q"], b["d_k"], b["d_v"]]
+    other = rand(g, 600, 4, 128)
+    want = both(q)
+    for scale in (100.0, 1e-3, 3e4):    # a call whose tiles are full, with large and small rows
+        x = (scale * other).to(BF16)
+        cli.cross_attention(x, offsets([600]), x, x, offsets([600]), max_query_rows=600)
+        for a, b in zip(want, both(q)):
+            assert torch.equal(a, b)
