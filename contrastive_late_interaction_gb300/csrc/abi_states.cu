@@ -126,7 +126,7 @@ cli_status_t rotary_call(const cli_rotary_t *a, bool norm, bool backward) {
         const cli_rotary_part_t &s = *parts[p];
         if (p == 1 && s.heads == 0) continue;
         if (s.rows >= kRowsLimit || s.heads == 0 || s.heads > 65535) return CLI_SHAPE_MISMATCH;
-        if (!aligned(s.positions, 4) || (norm && !aligned(s.gain, 4))) return CLI_INVALID_ARGUMENT;
+        if (!aligned(s.positions, 4) || (norm && !aligned(s.gain, 4)) || (grads && !aligned(s.d_gain, 4))) return CLI_INVALID_ARGUMENT;
         const cli_heads_t &in = backward ? s.d_y : s.x, &out = backward ? s.d_x : s.y;
         const Heads hin(in, s.rows, s.heads, d, es), hout(out, s.rows, s.heads, d, es);
         const Heads hx(grads ? s.x : cli_heads_t{}, grads ? s.rows : 0, s.heads, d, es);

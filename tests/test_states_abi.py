@@ -35,3 +35,19 @@ def test_matrices_past_the_address_space_are_refused(b):
         assert b.lib.rotary_heads(ctypes.byref(rotary_args(b, part=part))) == b.CLI_SHAPE_MISMATCH
         args = attention_args(b, key_rows=rows, max_key_rows=300, k=H(A * 4, row, head))
         assert b.lib.cross_attention(ctypes.byref(args)) == b.CLI_SHAPE_MISMATCH
+
+
+@pytest.mark.parametrize("field", ["gain", "d_gain", "positions"])
+def test_misaligned_vectors_are_refused(b, field):
+    """32-bit values at an odd address: the kernel's access would fault."""
+    for off in (1, 2, 3):
+        part = {field: A * 20 + off}
+        args = rotary_args(b, part=part)
+        assert b.lib.norm_rotary_heads_backward(ctypes.byref(args)) == b.CLI_INVALID_ARGUMENT
+
+
+def test_misaligned_attention_vectors_are_refused(b):
+    for name, off in (("lse", 2), ("key_offsets", 4), ("query_offsets", 4), ("device_status", 2)):
+        for verb in ("cross_attention", "cross_attention_backward"):
+            args = attention_args(b, **{name: A * 20 + off})
+            assert getattr(b.lib, verb)(ctypes.byref(args)) == b.CLI_INVALID_ARGUMENT, name
