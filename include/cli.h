@@ -624,7 +624,8 @@ size_t norm_rotary_heads_backward_workspace_bytes(size_t head_dim);
  *   device_status    device int32 (written: 0 or a cli_status_t)
  *
  * P and dS enter the products as `dtype`, or as the sum of two such where an
- * item has few rows; everything else between input and output is in 32 bits,
+ * item has few rows (in fp16 times powers of two that keep them in its range,
+ * dS by the largest values of the call); everything else between input and output is in 32 bits,
  * but for D, which the rounded output gives.  For dK, D is corrected by a row's
  * sum of dS in 32 bits (with few rows, for the states that have an eighth or
  * more of some row's weight, a quarter with more than 8 rows).
