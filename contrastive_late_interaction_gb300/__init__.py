@@ -1,11 +1,13 @@
 """In-batch contrastive scoring on one GB300: the fused SigLIP sigmoid pair loss and hard MaxSim.
 
 The compute path is the CUDA library built from `csrc/` (C ABI in `include/cli.h`);
-`_binding` only marshals arguments to it and raises if the library is missing.
-`synth` draws the seeded inputs.  The binding's names are re-exported lazily,
-so `synth` imports without a built library.
+`_binding` and, for what stands between a tower's blocks, `_norms` only marshal
+arguments to it and raise if the library is missing.  `synth` draws the seeded
+inputs.  The binding's names are re-exported lazily, so `synth` imports without
+a built library.
 """
 
+import importlib
 import sys
 import types
 
@@ -23,22 +25,27 @@ _BINDING_NAMES = {
     "norm_rotary_heads_backward_workspace_bytes",
 }
 
+_NORM_NAMES = {
+    "layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_bytes", "dropout", "dropout_backward",
+    "dropout_layer_norm", "dropout_layer_norm_backward",
+}
+
 
 class _Name:
     """A name of the binding, looked up there each time: cheaper than a module's __getattr__, and a name that is set on the
     package itself still comes first."""
 
-    def __init__(self, name):
-        self.name = name
+    def __init__(self, name, module):
+        self.name, self.module = name, module
 
-    def __get__(self, module, kind=None):
-        binding = _loaded.get("binding")
+    def __get__(self, package, kind=None):
+        binding = _loaded.get(self.module)
         if binding is None:
-            from . import _binding as binding
-            _loaded["binding"] = binding
+            binding = _loaded[self.module] = importlib.import_module(self.module, __name__)
         return getattr(binding, self.name)
 
 
 _loaded = {}
-_Package = type("_Package", (types.ModuleType,), {name: _Name(name) for name in _BINDING_NAMES})
+_Package = type("_Package", (types.ModuleType,), {name: _Name(name, module) for names, module in (
+    (_BINDING_NAMES, "._binding"), (_NORM_NAMES, "._norms")) for name in names})
 sys.modules[__name__].__class__ = _Package

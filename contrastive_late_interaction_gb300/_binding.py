@@ -178,6 +178,34 @@ class AttentionArgs(ctypes.Structure):
                 ("stream", c_void_p)]
 
 
+class RowsArgs(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("row_stride", c_size_t)]
+
+
+class DropoutMaskArgs(ctypes.Structure):
+    _fields_ = [("rate", ctypes.c_double), ("seed", c_void_p), ("site", ctypes.c_uint32)]
+
+
+class LayerNormArgs(ctypes.Structure):
+    _fields_ = [("x_dtype", c_int), ("y_dtype", c_int), ("rows", c_size_t), ("width", c_size_t), ("x", RowsArgs),
+                ("y", RowsArgs), ("d_y", RowsArgs), ("d_x", RowsArgs), ("gain", c_void_p), ("bias", c_void_p),
+                ("d_gain", c_void_p), ("d_bias", c_void_p), ("epsilon", c_float), ("workspace", c_void_p),
+                ("workspace_bytes", c_size_t), ("stream", c_void_p)]
+
+
+class DropoutArgs(ctypes.Structure):
+    _fields_ = [("dtype", c_int), ("rows", c_size_t), ("width", c_size_t), ("x", RowsArgs), ("y", RowsArgs),
+                ("d_y", RowsArgs), ("d_x", RowsArgs), ("mask", DropoutMaskArgs), ("stream", c_void_p)]
+
+
+class DropoutLayerNormArgs(ctypes.Structure):
+    _fields_ = [("dtype", c_int), ("stream_dtype", c_int), ("rows", c_size_t), ("width", c_size_t), ("x", RowsArgs),
+                ("residual", RowsArgs), ("sum", RowsArgs), ("y", RowsArgs), ("d_y", RowsArgs), ("d_sum", RowsArgs),
+                ("d_residual", RowsArgs), ("d_x", RowsArgs), ("mask", DropoutMaskArgs), ("gain", c_void_p),
+                ("bias", c_void_p), ("d_gain", c_void_p), ("d_bias", c_void_p), ("epsilon", c_float),
+                ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("stream", c_void_p)]
+
+
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # cli_dtype_t
 ROTARY_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -211,6 +239,13 @@ EXPORTS = {
     "cross_attention_workspace_bytes": (c_size_t, [ctypes.POINTER(AttentionArgs)]),
     "cross_attention_backward": (c_int, [ctypes.POINTER(AttentionArgs)]),
     "cross_attention_backward_workspace_bytes": (c_size_t, [ctypes.POINTER(AttentionArgs)]),
+    "layer_norm": (c_int, [ctypes.POINTER(LayerNormArgs)]),
+    "layer_norm_backward": (c_int, [ctypes.POINTER(LayerNormArgs)]),
+    "layer_norm_backward_workspace_bytes": (c_size_t, [c_size_t, c_size_t]),
+    "dropout": (c_int, [ctypes.POINTER(DropoutArgs)]),
+    "dropout_backward": (c_int, [ctypes.POINTER(DropoutArgs)]),
+    "dropout_layer_norm": (c_int, [ctypes.POINTER(DropoutLayerNormArgs)]),
+    "dropout_layer_norm_backward": (c_int, [ctypes.POINTER(DropoutLayerNormArgs)]),
     "cli_selftest_bounded_wait": (c_int, [c_void_p, c_void_p, ctypes.c_uint32, c_void_p]),
 }
 NO_ALLOC_MAX_QUERY_ROWS = 262144   # CLI_MAXSIM_NO_ALLOC_MAX_QUERY_ROWS in include/cli.h

@@ -10,6 +10,7 @@
 
 #include "cli_device.cuh"
 #include "cli_internal.h"
+#include "launch.cuh"
 
 namespace cli {
 namespace attn {
@@ -133,27 +134,6 @@ static __global__ void begin_kernel(int32_t *status, unsigned long long *counter
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) *status = 0;
     if (threadIdx.x < kCounterBytes / 8) counters[threadIdx.x] = 0;
-}
-
-// Waits for the kernels before this one on the stream, which may still run
-// when it starts (launch_after).
-__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// Launches a kernel that may start before the one before it has ended; it
-// calls after_previous() before it touches memory.
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, A &&...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
 template <typename T> struct Type;

@@ -258,4 +258,53 @@ long long backward_tiles_joins(const AttentionLaunch &L);
 cudaError_t launch_attention(const AttentionLaunch &L, cudaStream_t stream);
 cudaError_t launch_attention_backward(const AttentionLaunch &L, cudaStream_t stream);
 
+// ----------------------------------------------------------------------------
+// rows: layer norm, dropout, the residual join (norm*.cu, dropout.cu)
+// ----------------------------------------------------------------------------
+
+// A dropout mask: an element is kept where its word is at least `least` (0:
+// all are), times `scale`.  `seed`: device [2], the key and the step.
+struct MaskLaunch {
+    const uint64_t *seed;
+    uint32_t site, least;
+    float scale;
+};
+
+// Rows of a norm call, strides in elements.  In the stream's type: `in` (what
+// is normalised, or the residual a branch joins; the sum in a backward call),
+// `sum`, `d_sum`, `d_in`; in the other one `branch`, `out`, `d_out`, `d_branch`.
+struct NormLaunch {
+    int dtype, stream_dtype, backward, join;
+    long long rows;
+    int width, lanes;   // lanes: of a team
+    bool whole;         // chunks of 4 are aligned
+    float inv_width, epsilon;
+    const void *in, *branch, *d_out, *d_sum;
+    void *sum, *out, *d_in, *d_branch;
+    long long in_row, branch_row, sum_row, out_row, d_out_row, d_sum_row, d_in_row, d_branch_row;
+    const float *gain, *bias;
+    float *d_gain, *d_bias, *partials;   // partials: [2][blocks][width], or NULL
+    MaskLaunch mask;
+    int sm_count;
+    bool wide;          // chunks of 8 are whole and aligned
+};
+
+constexpr size_t kMaxRowWidth = 16384;
+// The most blocks of a backward call, each of which has a row of partial sums.
+inline long long norm_blocks(long long rows, int sm_count) { return rows < 4ll * sm_count ? (rows < 1 ? 1 : rows) : 4ll * sm_count; }
+cudaError_t launch_norm(const NormLaunch &L, cudaStream_t stream);
+
+struct DropoutLaunch {
+    int dtype;
+    long long rows;
+    int width;
+    bool whole, wide;
+    const void *in;
+    void *out;
+    long long in_row, out_row;
+    MaskLaunch mask;
+    int sm_count;
+};
+cudaError_t launch_dropout(const DropoutLaunch &L, cudaStream_t stream);
+
 }  // namespace cli

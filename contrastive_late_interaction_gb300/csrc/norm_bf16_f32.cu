@@ -1,0 +1,9 @@
+// Layer norm and the residual join: bf16 rows beside an fp32 stream.
+
+#include "norm.cuh"
+
+namespace cli {
+namespace norm {
+template cudaError_t launch_types<__nv_bfloat16, float>(const NormLaunch &L, cudaStream_t stream);
+}
+}  // namespace cli

@@ -653,6 +653,139 @@ size_t cross_attention_workspace_bytes(const cli_attention_t *args);
 cli_status_t cross_attention_backward(const cli_attention_t *args);
 size_t cross_attention_backward_workspace_bytes(const cli_attention_t *args);
 
+/* ---------------------------------------------------------------------------
+ * Between a tower's blocks: layer norm, dropout and the residual join.
+ *
+ * Rows of `width` elements, 1 .. 16384 (wider ones: CLI_UNSUPPORTED), rows
+ * < 2^31 (0 is a call on no rows).  Types are cli_dtype_t.  Arithmetic is in 32
+ * bits, rounded once at the end.  Sums run in a fixed order, so every result
+ * is bit-reproducible, and a row's results do not depend on the other rows
+ * (but for d_gain and d_bias, which sum over them in an order that goes by the
+ * sizes, the matrices' alignment and the device).
+ * ------------------------------------------------------------------------- */
+
+/* A matrix in device memory: element i of row r is data[r * row_stride + i].
+ * `data` is aligned to an element; the stride, in elements, is any (one row's
+ * is not read), but an output's rows may not overlap one another.  Matrices
+ * whose width and strides are multiples of 8 elements and that start on one
+ * are moved 16 bytes at a time, those of 4 in halves of that (16-bit types),
+ * others element by element.  An output may be an input in place (the same
+ * data, stride and type); it overlaps no other input or output otherwise. */
+typedef struct {
+    void *data;
+    size_t row_stride;
+} cli_rows_t;
+
+/*
+ * layer_norm -- normalises each row:
+ *     n = (x - mean x) / sqrt(mean (x - mean x)^2 + epsilon),  y = gain n + bias.
+ * layer_norm_backward -- its gradients: with t = gain d_y,
+ *     d_x = (t - mean t - n mean(t n)) / sqrt(mean (x - mean x)^2 + epsilon),
+ *     d_gain = sum over rows of d_y n,  d_bias = sum over rows of d_y.
+ *
+ *   x_dtype         of x and d_x: y_dtype, or CLI_F32 beside 16-bit outputs
+ *   y_dtype         of y and d_y
+ *   x, y, d_y, d_x  layer_norm reads x and writes y; layer_norm_backward reads x
+ *                   and d_y and writes d_x
+ *   gain, bias      device fp32 [width]; NULL: ones, zeros (the backward does not
+ *                   read the bias)
+ *   d_gain, d_bias  device fp32 [width] (written by the backward); NULL: not wanted
+ *   epsilon         > 0
+ *   workspace       layer_norm_backward with a d_gain or d_bias alone: device, >=
+ *                   layer_norm_backward_workspace_bytes(rows, width), 256-byte
+ *                   aligned; contents on entry are ignored
+ */
+typedef struct {
+    int x_dtype, y_dtype;
+    size_t rows, width;
+    cli_rows_t x, y, d_y, d_x;
+    const float *gain, *bias;
+    float *d_gain, *d_bias;
+    float epsilon;
+    void *workspace;
+    size_t workspace_bytes;
+    void *stream;
+} cli_layer_norm_t;
+
+cli_status_t layer_norm(const cli_layer_norm_t *args);
+cli_status_t layer_norm_backward(const cli_layer_norm_t *args);
+size_t layer_norm_backward_workspace_bytes(size_t rows, size_t width);
+
+/*
+ * A dropout mask, which is never stored: both directions draw it from a
+ * counter-based generator, Philox 4x32 of ten rounds (Salmon, Moraes, Dror,
+ * Shaw 2011).  The element at (row, column) has word column % 4 of the block
+ * with the key (seed, low word first) and the counter
+ *     (column / 4 + 2^16 site, row, step, low word first),
+ * and is kept where that word is at least D = floor(rate 2^32), times
+ * 2^32 / (2^32 - D).  A dropped element is 0 whatever the input holds there.
+ * The same seed, step and site give the same mask, however the rows lie.
+ *
+ *   rate            0 <= rate < 1; with 0 nothing is dropped and the seed not read
+ *   seed            device uint64 [2], (seed, step), 8-byte aligned, read when the
+ *                   call's kernels run: a captured call draws the step that is
+ *                   there at each replay
+ *   site            0 .. 65535, the call's place among those of one step
+ */
+typedef struct {
+    double rate;
+    const uint64_t *seed;
+    uint32_t site;
+} cli_dropout_mask_t;
+
+/*
+ * dropout -- y = x through the mask.
+ * dropout_backward -- its gradient, d_x = d_y through the same mask.
+ *
+ *   dtype           of every matrix
+ *   x, y, d_y, d_x  dropout reads x and writes y; dropout_backward reads d_y and
+ *                   writes d_x
+ */
+typedef struct {
+    int dtype;
+    size_t rows, width;
+    cli_rows_t x, y, d_y, d_x;
+    cli_dropout_mask_t mask;
+    void *stream;
+} cli_dropout_t;
+
+cli_status_t dropout(const cli_dropout_t *args);
+cli_status_t dropout_backward(const cli_dropout_t *args);
+
+/*
+ * dropout_layer_norm -- a branch joins the residual stream, and the norm of
+ * that, in one pass:
+ *     sum = residual + x through the mask,  y = layer_norm(sum),
+ * y being the norm of the sum before it is rounded to its type.
+ * dropout_layer_norm_backward -- its gradients, of the sum as it was stored:
+ *     d_residual = d_sum + layer_norm_backward(sum, d_y),
+ *     d_x = d_residual (before it is rounded) through the mask.
+ *
+ *   dtype           of x, y, d_y and d_x
+ *   stream_dtype    of residual, sum, d_sum and d_residual: dtype, or CLI_F32
+ *                   beside a 16-bit branch
+ *   sum             written by the forward (data NULL: not wanted), read by the
+ *                   backward
+ *   d_sum           the gradient that comes back along the stream (data NULL: none)
+ *   d_residual, d_x   written by the backward (d_x: data NULL: not wanted)
+ *   the rest        as above; workspace as for layer_norm_backward
+ */
+typedef struct {
+    int dtype, stream_dtype;
+    size_t rows, width;
+    cli_rows_t x, residual, sum, y, d_y, d_sum, d_residual, d_x;
+    cli_dropout_mask_t mask;
+    const float *gain, *bias;
+    float *d_gain, *d_bias;
+    float epsilon;
+    void *workspace;
+    size_t workspace_bytes;
+    void *stream;
+} cli_dropout_layer_norm_t;
+
+cli_status_t dropout_layer_norm(const cli_dropout_layer_norm_t *args);
+cli_status_t dropout_layer_norm_backward(const cli_dropout_layer_norm_t *args);
+
 /*
  * cli_selftest_bounded_wait -- runs the failure path of the kernels' bounded
  * waits, faulting nothing.  Every wait of the tensor-core kernels gives up
