@@ -38,9 +38,8 @@ struct Rows {
         if (row >= (1ull << 40) || (row && rows - 1 > (1ull << 61) / row)) return CLI_SHAPE_MISMATCH;
         return CLI_OK;
     }
-    bool chunks(size_t elements) const {   // rows of whole, aligned chunks
-        return empty() || (at % (16 < elements * element ? 16 : elements * element) == 0 && row % (elements * element) == 0 &&
-                           inner % (elements * element) == 0);
+    bool pieces(size_t bytes) const {   // rows of whole, aligned pieces
+        return empty() || (at % bytes == 0 && row % bytes == 0 && inner % bytes == 0);
     }
 };
 
@@ -87,12 +86,21 @@ struct Call {
         }
         return CLI_OK;
     }
-    bool chunks(size_t elements) const {
+    template <typename F>
+    bool all(F f) const {
         for (const Rows &r : in)
-            if (!r.chunks(elements)) return false;
+            if (!f(r)) return false;
         for (const Rows &r : out)
-            if (!r.chunks(elements)) return false;
+            if (!f(r)) return false;
         return true;
+    }
+    // How the call's chunks of 4 can be moved, and whether chunks of 8 are 16 bytes each.
+    int moves() const {
+        if (all([](const Rows &r) { return r.pieces(4 * r.element); })) return 0;   // kWhole
+        return all([](const Rows &r) { return r.pieces(4); }) ? 1 : 2;              // kWords, kHalves
+    }
+    bool wide() const {
+        return all([](const Rows &r) { return r.empty() || (r.element == 2 && r.pieces(16)); });
     }
 };
 
@@ -183,8 +191,8 @@ cli_status_t norm_call(const Norm &a) {
     L.join = a.join;
     L.rows = static_cast<long long>(a.rows);
     L.width = static_cast<int>(a.width);
-    L.wide = c.chunks(8);
-    L.whole = L.wide || c.chunks(4);
+    L.wide = c.wide();
+    L.moves = c.moves();
     L.inv_width = 1.0f / static_cast<float>(a.width);
     L.epsilon = a.epsilon;
     L.in = a.in.data, L.in_row = stride_of(a.in);
@@ -253,8 +261,8 @@ cli_status_t dropout_call(const cli_dropout_t *a, bool backward) {
     L.dtype = a->dtype;
     L.rows = static_cast<long long>(a->rows);
     L.width = static_cast<int>(a->width);
-    L.wide = c.chunks(8);
-    L.whole = L.wide || c.chunks(4);
+    L.wide = c.wide();
+    L.moves = c.moves();
     L.in = in.data, L.in_row = stride_of(in);
     L.out = out.data, L.out_row = stride_of(out);
     return launched(launch_dropout(L, static_cast<cudaStream_t>(a->stream)));

@@ -277,7 +277,7 @@ struct NormLaunch {
     int dtype, stream_dtype, backward, join;
     long long rows;
     int width, lanes;   // lanes: of a team
-    bool whole;         // chunks of 4 are aligned
+    int moves;          // how chunks of 4 can be moved (rows.cuh)
     float inv_width, epsilon;
     const void *in, *branch, *d_out, *d_sum;
     void *sum, *out, *d_in, *d_branch;
@@ -286,7 +286,7 @@ struct NormLaunch {
     float *d_gain, *d_bias, *partials;   // partials: [2][blocks][width], or NULL
     MaskLaunch mask;
     int sm_count;
-    bool wide;          // chunks of 8 are whole and aligned
+    bool wide;          // chunks of 8 are whole, in 16-bit types
 };
 
 constexpr size_t kMaxRowWidth = 16384;
@@ -298,7 +298,8 @@ struct DropoutLaunch {
     int dtype;
     long long rows;
     int width;
-    bool whole, wide;
+    int moves;
+    bool wide;
     const void *in;
     void *out;
     long long in_row, out_row;

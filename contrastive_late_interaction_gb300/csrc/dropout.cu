@@ -16,7 +16,7 @@ constexpr int kThreads = 256, kUnroll = 4;
 
 // The rows' chunks, counted through: a block takes kThreads * kUnroll of them at a time.  magic: 2^32 / chunks of a row,
 // rounded up (0 for one chunk); next_row, next_chunk: how far the grid is across.
-template <typename T, int E>
+template <typename T, int E, int MOVES>
 __global__ void __launch_bounds__(kThreads)
     dropout_kernel(const __grid_constant__ DropoutLaunch P, uint32_t chunks, uint32_t magic, long long next_row, uint32_t next_chunk) {
     constexpr uint32_t kTile = kThreads * kUnroll;
@@ -39,33 +39,37 @@ __global__ void __launch_bounds__(kThreads)
             row[u] = row0 + down;
             at[u] = static_cast<int>(k - down * chunks) * E;
             n[u] = row[u] < P.rows ? min(E, P.width - at[u]) : 0;
-            take(c[u], static_cast<const T *>(P.in) + row[u] * P.in_row + at[u], n[u], P.whole);
+            take<MOVES>(c[u], static_cast<const T *>(P.in) + row[u] * P.in_row + at[u], n[u]);
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            float v[E];
+            float2 v[E / 2];
             c[u].floats(v);
             mask.apply<E>(v, static_cast<uint32_t>(row[u]), at[u]);
             c[u].set(v);
-            put(c[u], static_cast<T *>(P.out) + row[u] * P.out_row + at[u], n[u], P.whole);
+            put<MOVES>(c[u], static_cast<T *>(P.out) + row[u] * P.out_row + at[u], n[u]);
         }
     }
 }
 
-template <typename T, int E>
+template <typename T, int E, int MOVES>
 cudaError_t launch(const DropoutLaunch &L, cudaStream_t stream) {
     constexpr long long kTile = kThreads * kUnroll;
     const long long chunks = (L.width + E - 1) / E, tiles = (L.rows * chunks + kTile - 1) / kTile;
     const long long most = 8ll * L.sm_count, blocks = tiles < most ? tiles : most;
     const uint32_t magic = chunks == 1 ? 0 : static_cast<uint32_t>(((1ull << 32) + chunks - 1) / chunks);
-    dropout_kernel<T, E><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
+    dropout_kernel<T, E, MOVES><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
         L, static_cast<uint32_t>(chunks), magic, blocks * kTile / chunks, static_cast<uint32_t>(blocks * kTile % chunks));
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch(const DropoutLaunch &L, cudaStream_t stream) {
-    return L.wide ? launch<T, 8>(L, stream) : launch<T, 4>(L, stream);
+    if constexpr (sizeof(T) == 2) {
+        if (L.wide) return launch<T, 8, kWhole>(L, stream);
+        if (L.moves == kHalves) return launch<T, 4, kHalves>(L, stream);
+    }
+    return L.moves == kWhole ? launch<T, 4, kWhole>(L, stream) : launch<T, 4, kWords>(L, stream);
 }
 
 }  // namespace

@@ -1,5 +1,6 @@
 // Kernels of layer norm over rows of 1 to 16384 elements, alone and where a
-// dropped-out branch joins a residual stream; norm.cu launches them.
+// dropped-out branch joins a residual stream, and their launches for one pair
+// of types (norm_*.cu).
 //
 // Mathematics (see include/cli.h).  A row z is x itself, or residual + the
 // branch through its mask.  The mean m comes from one sum, and the variance
@@ -7,6 +8,11 @@
 // e = mean d, n = (d - e) r and v = mean d^2 - e^2, so that a mean far from 0
 // costs no digits of the spread around it.  The gradient, t = gain d_y:
 //     d_z = r (t - mean t - n mean(t n)),  d_gain = sum d_y n,  d_bias = sum d_y.
+//
+// Work.  A team takes a row, or R of them: 2^k lanes of a warp, or whole
+// warps, each thread NE elements of a row in chunks of E.  Teams walk the rows
+// at the grid's stride, and what a thread needs some steps from now is on its
+// way into its own places in shared memory (rows.cuh).
 #pragma once
 
 #include "rows.cuh"
@@ -16,11 +22,14 @@ namespace norm {
 
 using namespace rows;
 
-// Where a thread's chunks of a row lie, and how many elements of each there are.
-template <int E>
-__device__ __forceinline__ int column_of(const Team &team, int j) { return (j * team.lanes + team.lane) * E; }
-template <int E>
-__device__ __forceinline__ int elements_of(int at, int width) { return min(max(width - at, 0), E); }
+constexpr int kThreads = 512;   // the most of a block: one team of the widest rows
+
+// Where a thread's chunk j of a row lies: neighbours with NE = 8, whose team is a part of a warp, else the warp's chunks
+// j side by side, so that the chunks of a thread are a constant apart.
+template <int E, int NE>
+__device__ __forceinline__ int column_of(const Team &team, int j) {
+    return NE == 8 ? team.lane * 8 + j * E : (team.lane >> 5) * (32 * NE) + (team.lane & 31) * E + j * (32 * E);
+}
 
 // 1 / sqrt(variance + epsilon) of `width` deviations that sum to `sum` and whose squares sum to `squares`; e: their mean.
 __device__ __forceinline__ float deviation(float sum, float squares, float inv_width, float epsilon, float &e) {
@@ -28,227 +37,343 @@ __device__ __forceinline__ float deviation(float sum, float squares, float inv_w
     return rsqrtf(fmaxf(squares * inv_width - e * e, 0.0f) + epsilon);
 }
 
-// The most threads of a block: one team of the widest rows where it has several warps.
-template <int E, int C> constexpr int kForwardThreads = C < 4 ? 256 : static_cast<int>(kMaxRowWidth) / (E * C);
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// v - m for the n elements of a chunk that there are; the others are 0 and stay so.
+template <int E, int MOVES>
+__device__ __forceinline__ void deviations(float2 (&v)[E / 2], float m, int n) {
+    if constexpr (MOVES == kWhole) {
+        const float2 shift = both(n > 0 ? -m : 0.0f);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) v[i] = __fadd2_rn(v[i], shift);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i)
+            v[i] = __fadd2_rn(v[i], make_float2(2 * i < n ? -m : 0.0f, 2 * i + 1 < n ? -m : 0.0f));
+    }
+}
+
+// Stages of a thread's places, `bytes` a step: up to 400 bytes in all, so that 512 threads' fit an SM.
+constexpr int stages_of(int bytes) { return bytes > 200 ? 1 : bytes >= 100 ? 400 / bytes : 4; }
+static_assert(stages_of(64) == 4 && stages_of(128) == 3 && stages_of(192) == 2 && stages_of(384) == 1, "");
+
+template <typename T, typename S, int E, int NE, int R, bool BRANCH>
+struct Forward {
+    static constexpr int kChunks = NE / E * R, kBytes = NE * R * static_cast<int>(sizeof(S) + (BRANCH ? sizeof(T) : 0));
+    static constexpr int kStages = stages_of(kBytes);
+};
 
 // T: type of the branch and the output.  S: the stream's.  E: elements of a
-// chunk; C: chunks of a row that a thread has; R: rows that a team takes at a
-// time.  BRANCH: a branch joins.
-template <typename T, typename S, int E, int C, int R, bool BRANCH>
-__global__ void __launch_bounds__(kForwardThreads<E, C>) forward_kernel(const __grid_constant__ NormLaunch P) {
-    extern __shared__ float scratch[];   // teams of several warps: two of 64 floats each
+// chunk; NE: of a row that a thread has; R: rows that a team takes at a time.
+// BRANCH: a branch joins.
+template <typename T, typename S, int E, int NE, int R, bool BRANCH, int MOVES>
+__global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant__ NormLaunch P) {
+    using F = Forward<T, S, E, NE, R, BRANCH>;
+    constexpr int C = NE / E, kStages = F::kStages;
+    constexpr bool kHold = NE <= 16;   // the gain and the bias stay in registers
+    extern __shared__ __align__(16) float scratch[];   // teams of several warps: R * 48 floats each; then the feeds
     const Team team(P.lanes);
-    const int width = P.width;
-    const bool whole = P.whole;
-    float *sums = scratch + team.id * 128;
+    float *sums = scratch + team.id * R * 48;
+    const uint32_t places = smem_u32(scratch) + (team.lanes > 32 ? team.in_block * R * 192 : 0);
+    Feed<S, E, C * R, MOVES> in(places, kStages);
+    Feed<T, E, C * R, MOVES> branch(places + (BRANCH ? kStages * C * R * E * static_cast<int>(sizeof(S)) * blockDim.x : 0), BRANCH ? kStages : 0);
     const Mask mask(P.mask);
-    const int first = team.lanes < 32 ? team.index - (threadIdx.x & 31) / team.lanes : team.index;   // of the warp
-    for (long long base = 0; base + static_cast<long long>(first) * R < P.rows; base += static_cast<long long>(team.count) * R) {
-        const long long row0 = base + static_cast<long long>(team.index) * R;
-        float v[R][C][E];
-        {
-            Chunk<S, E> in[R][C];
-            Chunk<T, E> x[BRANCH ? R : 1][C];
+    const int column = column_of<E, NE>(team, 0);
+    constexpr int kNext = NE == 8 ? E : 32 * E;   // from a chunk to the next
+    int there[C];   // elements of each chunk
+    float2 gain[kHold ? C : 1][E / 2], bias[kHold ? C : 1][E / 2];
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int j = 0; j < C; ++j) {
-                    const int at = column_of<E>(team, j), n = row0 + r < P.rows ? elements_of<E>(at, width) : 0;
-                    take(in[r][j], static_cast<const S *>(P.in) + (row0 + r) * P.in_row + at, n, whole);
-                    if constexpr (BRANCH) take(x[r][j], static_cast<const T *>(P.branch) + (row0 + r) * P.branch_row + at, n, whole);
-                }
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int j = 0; j < C; ++j) {
-                    in[r][j].floats(v[r][j]);
-                    if constexpr (BRANCH) {
-                        const int at = column_of<E>(team, j), n = row0 + r < P.rows ? elements_of<E>(at, width) : 0;
-                        float f[E];
-                        x[r][j].floats(f);
-                        mask.apply<E>(f, static_cast<uint32_t>(row0 + r), at);
-#pragma unroll
-                        for (int i = 0; i < E; ++i) v[r][j][i] += f[i];
-                        if (P.sum) {
-                            Chunk<S, E> c;
-                            c.set(v[r][j]);
-                            put(c, static_cast<S *>(P.sum) + (row0 + r) * P.sum_row + at, n, whole);
-                        }
-                    }
-                }
+    for (int j = 0; j < C; ++j) {
+        const int at = column + j * kNext;
+        there[j] = min(max(P.width - at, 0), E);
+        if constexpr (kHold) {
+            vector_of<E>(P.gain, at, P.width, 1.0f, gain[j]);
+            vector_of<E>(P.bias, at, P.width, 0.0f, bias[j]);
         }
+    }
+    const uint32_t rows = static_cast<uint32_t>(P.rows), stride = team.count * R, mine = team.index * R;
+    const uint32_t first = team.first * R;   // of the warp
+
+    // The copies of a step, rows base + mine to base + mine + R - 1.
+    auto copy = [&](uint32_t base, int stage) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint32_t row = base + mine + r;
+            const bool on = row < rows;
+            const S *from = static_cast<const S *>(P.in) + row * P.in_row + column;
+            const T *x = static_cast<const T *>(P.branch) + row * P.branch_row + column;
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                in.copy(stage, r * C + j, from + j * kNext, on ? there[j] : 0);
+                if constexpr (BRANCH) branch.copy(stage, r * C + j, x + j * kNext, on ? there[j] : 0);
+            }
+        }
+    };
+    auto settle = [&](int stage) {
+        in.settle(stage);
+        if constexpr (BRANCH) branch.settle(stage);
+    };
+    constexpr bool kHeld = MOVES == kHalves && (BRANCH || sizeof(S) == 2);
+    constexpr int kAhead = kHeld && kStages > 1 ? 1 : kStages - 1;   // steps
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        copy(k * stride, k);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    if constexpr (kHeld && kAhead) settle(0);
+    int stage = 0;
+    for (uint32_t base = 0; base + first < rows; base += stride) {
+        const int next = stage + kAhead >= kStages ? stage + kAhead - kStages : stage + kAhead;
+        copy(base + kAhead * stride, next);   // what was there was used up a step ago
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+        if constexpr (kHeld && !kAhead) settle(stage);
+        float2 v[R][C][E / 2];
         float s[R], s2[2 * R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            s[r] = 0.0f;
+            const uint32_t row = base + mine + r;
+            const bool on = row < rows;
+            S *total = static_cast<S *>(P.sum) + row * P.sum_row + column;
+            float2 sum = both(0.0f);
 #pragma unroll
-            for (int j = 0; j < C; ++j)
+            for (int j = 0; j < C; ++j) {
+                in.floats(stage, r * C + j, v[r][j]);
+                if constexpr (BRANCH) {
+                    float2 f[E / 2];
+                    branch.floats(stage, r * C + j, f);
+                    mask.apply<E>(f, row, column + j * kNext);
 #pragma unroll
-                for (int i = 0; i < E; ++i) s[r] += v[r][j][i];   // 0 past the row's end
+                    for (int i = 0; i < E / 2; ++i) v[r][j][i] = __fadd2_rn(v[r][j][i], f[i]);
+                    if (P.sum) {
+                        Chunk<S, E> c;
+                        c.set(v[r][j]);
+                        put<MOVES>(c, total + j * kNext, on ? there[j] : 0);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) sum = __fadd2_rn(sum, v[r][j][i]);   // 0 past the row's end
+            }
+            s[r] = sum.x + sum.y;
         }
-        team.sum<R>(s, sums);
+        team.sum<R, (NE > 8)>(s, sums);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const float m = s[r] * P.inv_width;
-            s2[2 * r] = s2[2 * r + 1] = 0.0f;
+            float2 sum = both(0.0f), squares = sum;
 #pragma unroll
             for (int j = 0; j < C; ++j) {
-                const int n = elements_of<E>(column_of<E>(team, j), width);
+                deviations<E, MOVES>(v[r][j], m, there[j]);
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const float d = (E == 8 ? n > 0 : i < n) ? v[r][j][i] - m : 0.0f;
-                    v[r][j][i] = d;
-                    s2[2 * r] += d;
-                    s2[2 * r + 1] = fmaf(d, d, s2[2 * r + 1]);
+                for (int i = 0; i < E / 2; ++i) {
+                    sum = __fadd2_rn(sum, v[r][j][i]);
+                    squares = __ffma2_rn(v[r][j][i], v[r][j][i], squares);
                 }
             }
+            s2[2 * r] = sum.x + sum.y;
+            s2[2 * r + 1] = squares.x + squares.y;
         }
-        team.sum<2 * R>(s2, sums + 64);
+        team.sum<2 * R, (NE > 8)>(s2, sums + R * 16);
 #pragma unroll
         for (int r = 0; r < R; ++r) s[r] = deviation(s2[2 * r], s2[2 * r + 1], P.inv_width, P.epsilon, s2[2 * r]);
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-            const int at = column_of<E>(team, j);
-            float gain[E], bias[E];
-            vector_of<E>(P.gain, at, width, 1.0f, gain);
-            vector_of<E>(P.bias, at, width, 0.0f, bias);
+            if constexpr (!kHold) {
+                vector_of<E>(P.gain, column + j * kNext, P.width, 1.0f, gain[0]);
+                vector_of<E>(P.bias, column + j * kNext, P.width, 0.0f, bias[0]);
+            }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int n = row0 + r < P.rows ? elements_of<E>(at, width) : 0;
-                float y[E];
+                const uint32_t row = base + mine + r;
+                const float2 scale = both(s[r]), shift = both(-s2[2 * r] * s[r]);
+                float2 y[E / 2];
 #pragma unroll
-                for (int i = 0; i < E; ++i) y[i] = fmaf((v[r][j][i] - s2[2 * r]) * s[r], gain[i], bias[i]);
+                for (int i = 0; i < E / 2; ++i)
+                    y[i] = __ffma2_rn(__ffma2_rn(v[r][j][i], scale, shift), gain[kHold ? j : 0][i], bias[kHold ? j : 0][i]);
                 Chunk<T, E> c;
                 c.set(y);
-                put(c, static_cast<T *>(P.out) + (row0 + r) * P.out_row + at, n, whole);
+                put<MOVES>(c, static_cast<T *>(P.out) + row * P.out_row + column + j * kNext, row < rows ? there[j] : 0);
             }
         }
+        if constexpr (kHeld && kAhead) settle(next);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// THREADS: the most of a block.
-template <typename T, typename S, int E, int C, int THREADS, bool BRANCH>
-__global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant__ NormLaunch P) {
-    extern __shared__ float scratch[];   // teams of several warps: two of 128 floats each; then the block's sums
+template <typename T, typename S, int NE, bool BRANCH>
+struct Backward {
+    static constexpr int kBytes = NE * static_cast<int>(sizeof(S) * (BRANCH ? 2 : 1) + sizeof(T));
+    static constexpr int kStages = stages_of(kBytes);
+};
+
+template <typename T, typename S, int E, int NE, bool BRANCH, int MOVES>
+__global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ NormLaunch P) {
+    using B = Backward<T, S, NE, BRANCH>;
+    constexpr int C = NE / E, kStages = B::kStages;
+    constexpr bool kHold = NE <= 16;   // the gain and the row's deviations stay in registers
+    extern __shared__ __align__(16) float scratch[];   // teams of several warps: 80 floats each; then the feeds.  At the end, the block's sums
     const Team team(P.lanes);
-    const int width = P.width;
-    const bool whole = P.whole;
-    float *sums = scratch + team.id * 256;
+    float *sums = scratch + team.id * 80;
+    uint32_t places = smem_u32(scratch) + (team.lanes > 32 ? team.in_block * 320 : 0);
+    Feed<S, E, C, MOVES> in(places, kStages);
+    places += kStages * NE * static_cast<int>(sizeof(S)) * blockDim.x;
+    Feed<T, E, C, MOVES> d_out(places, kStages);
+    places += kStages * NE * static_cast<int>(sizeof(T)) * blockDim.x;
+    Feed<S, E, C, MOVES> d_sum(places, BRANCH ? kStages : 0);
     const Mask mask(P.mask);
-    float gain[C][E], d_gain[C][E], d_bias[C][E];
+    const int column = column_of<E, NE>(team, 0);
+    constexpr int kNext = NE == 8 ? E : 32 * E;   // from a chunk to the next
+    int there[C];   // elements of each chunk
+    float2 gain[kHold ? C : 1][E / 2], d_gain[C][E / 2], d_bias[C][E / 2];
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-        vector_of<E>(P.gain, column_of<E>(team, j), width, 1.0f, gain[j]);
+        const int at = column + j * kNext;
+        there[j] = min(max(P.width - at, 0), E);
+        if constexpr (kHold) vector_of<E>(P.gain, at, P.width, 1.0f, gain[j]);
 #pragma unroll
-        for (int i = 0; i < E; ++i) d_gain[j][i] = d_bias[j][i] = 0.0f;
+        for (int i = 0; i < E / 2; ++i) d_gain[j][i] = d_bias[j][i] = both(0.0f);
     }
-    const int first = team.lanes < 32 ? team.index - (threadIdx.x & 31) / team.lanes : team.index;   // of the warp
-    for (long long base = 0; base + first < P.rows; base += team.count) {
-        const long long row = base + team.index;
-        const bool on = row < P.rows;
-        Chunk<S, E> z[C], d_sum[BRANCH ? C : 1];
-        Chunk<T, E> d_y[C];
+    const uint32_t rows = static_cast<uint32_t>(P.rows), stride = team.count, mine = team.index, first = team.first;
+
+    auto copy = [&](uint32_t base, int stage) {
+        const uint32_t row = base + mine;
+        const bool on = row < rows;
+        const S *z = static_cast<const S *>(P.in) + row * P.in_row + column;
+        const T *g = static_cast<const T *>(P.d_out) + row * P.d_out_row + column;
+        const S *more = static_cast<const S *>(P.d_sum) + row * P.d_sum_row + column;
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-            const int at = column_of<E>(team, j), n = on ? elements_of<E>(at, width) : 0;
-            take(z[j], static_cast<const S *>(P.in) + row * P.in_row + at, n, whole);
-            take(d_y[j], static_cast<const T *>(P.d_out) + row * P.d_out_row + at, n, whole);
-            if constexpr (BRANCH) {
-                if (P.d_sum)
-                    take(d_sum[j], static_cast<const S *>(P.d_sum) + row * P.d_sum_row + at, n, whole);
-                else
-                    d_sum[j].clear();
+            const int n = on ? there[j] : 0;
+            in.copy(stage, j, z + j * kNext, n);
+            d_out.copy(stage, j, g + j * kNext, n);
+            if constexpr (BRANCH) d_sum.copy(stage, j, more + j * kNext, P.d_sum ? n : 0);   // none: its places stay 0
+        }
+    };
+    auto settle = [&](int stage) {
+        in.settle(stage);
+        d_out.settle(stage);
+        if constexpr (BRANCH) d_sum.settle(stage);
+    };
+    constexpr bool kHeld = MOVES == kHalves;
+    constexpr int kAhead = kHeld && kStages > 1 ? 1 : kStages - 1;   // steps
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        copy(k * stride, k);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    if constexpr (kHeld && kAhead) settle(0);
+    int stage = 0;
+    for (uint32_t base = 0; base + first < rows; base += stride) {
+        const int next = stage + kAhead >= kStages ? stage + kAhead - kStages : stage + kAhead;
+        copy(base + kAhead * stride, next);   // what was there was used up a step ago
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+        if constexpr (kHeld && !kAhead) settle(stage);
+        const uint32_t row = base + mine;
+        const bool on = row < rows;
+        float2 d[kHold ? C : 1][E / 2];
+        Chunk<T, E> dy[kHold ? C : 1];
+        float s[1], s4[4];
+        {
+            float2 sum = both(0.0f);
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                float2 (&v)[E / 2] = d[kHold ? j : 0];
+                in.floats(stage, j, v);
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) sum = __fadd2_rn(sum, v[i]);   // 0 past the row's end
             }
+            s[0] = sum.x + sum.y;
         }
-        float s[1] = {0.0f}, s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            float v[E];
-            z[j].floats(v);
-#pragma unroll
-            for (int i = 0; i < E; ++i) s[0] += v[i];
-        }
-        team.sum<1>(s, sums);
+        team.sum<1, (NE > 8)>(s, sums);
         const float m = s[0] * P.inv_width;
+        // A chunk's deviations and gradient: kept with kHold, else computed again where they are used.
+        auto load = [&](int j) {
+            if constexpr (!kHold) in.floats(stage, j, d[0]);
+            deviations<E, MOVES>(d[kHold ? j : 0], m, there[j]);
+            dy[kHold ? j : 0] = d_out.chunk(stage, j);
+            if constexpr (!kHold) vector_of<E>(P.gain, column + j * kNext, P.width, 1.0f, gain[0]);
+        };
+        {
+            float2 sum = both(0.0f), squares = sum, sum_t = sum, sum_td = sum;
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
-            const int n = elements_of<E>(column_of<E>(team, j), width);
-            float v[E], g[E];
-            z[j].floats(v);
-            d_y[j].floats(g);
+            for (int j = 0; j < C; ++j) {
+                load(j);
+                const int k = kHold ? j : 0;
+                float2 g[E / 2];
+                dy[k].floats(g);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float d = (E == 8 ? n > 0 : i < n) ? v[i] - m : 0.0f, t = g[i] * gain[j][i];
-                s4[0] += d;
-                s4[1] = fmaf(d, d, s4[1]);
-                s4[2] += t;
-                s4[3] = fmaf(t, d, s4[3]);
+                for (int i = 0; i < E / 2; ++i) {
+                    const float2 t = __fmul2_rn(g[i], gain[k][i]);
+                    sum = __fadd2_rn(sum, d[k][i]);
+                    squares = __ffma2_rn(d[k][i], d[k][i], squares);
+                    sum_t = __fadd2_rn(sum_t, t);
+                    sum_td = __ffma2_rn(t, d[k][i], sum_td);
+                }
             }
+            s4[0] = sum.x + sum.y, s4[1] = squares.x + squares.y, s4[2] = sum_t.x + sum_t.y, s4[3] = sum_td.x + sum_td.y;
         }
-        team.sum<4>(s4, sums + 128);
+        team.sum<4, (NE > 8)>(s4, sums + 16);
         float e;
         const float r = deviation(s4[0], s4[1], P.inv_width, P.epsilon, e);
         const float mean_t = s4[2] * P.inv_width, mean_tn = (s4[3] * P.inv_width - e * mean_t) * r;
+        const float2 scale = both(r), shift = both(-e * r), less = both(-r * mean_t), less_n = both(-r * mean_tn);
+        if (on) {
+            S *to = static_cast<S *>(P.d_in) + row * P.d_in_row + column;
+            T *to_x = static_cast<T *>(P.d_branch) + row * P.d_branch_row + column;
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
-            const int at = column_of<E>(team, j), n = on ? elements_of<E>(at, width) : 0;
-            float v[E], g[E], dz[E];
-            z[j].floats(v);
-            d_y[j].floats(g);
+            for (int j = 0; j < C; ++j) {
+                if constexpr (!kHold) load(j);
+                const int k = kHold ? j : 0;
+                float2 v[E / 2], g[E / 2];
+                dy[k].floats(g);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float norm = ((v[i] - m) - e) * r;
-                if (on) {
-                    d_gain[j][i] = fmaf(g[i], norm, d_gain[j][i]);
-                    d_bias[j][i] += g[i];
+                for (int i = 0; i < E / 2; ++i) {
+                    const float2 norm = __ffma2_rn(d[k][i], scale, shift);
+                    d_gain[j][i] = __ffma2_rn(g[i], norm, d_gain[j][i]);
+                    d_bias[j][i] = __fadd2_rn(d_bias[j][i], g[i]);
+                    v[i] = __ffma2_rn(__fmul2_rn(g[i], gain[k][i]), scale, __ffma2_rn(norm, less_n, less));
                 }
-                dz[i] = r * (g[i] * gain[j][i] - mean_t - norm * mean_tn);
-            }
-            if constexpr (BRANCH) {
-                float more[E];
-                d_sum[j].floats(more);
+                if constexpr (BRANCH) {
+                    d_sum.floats(stage, j, g);
 #pragma unroll
-                for (int i = 0; i < E; ++i) dz[i] += more[i];
-            }
-            Chunk<S, E> c;
-            c.set(dz);
-            put(c, static_cast<S *>(P.d_in) + row * P.d_in_row + at, n, whole);
-            if constexpr (BRANCH) {
-                if (P.d_branch) {
-                    mask.apply<E>(dz, static_cast<uint32_t>(row), at);
-                    Chunk<T, E> b;
-                    b.set(dz);
-                    put(b, static_cast<T *>(P.d_branch) + row * P.d_branch_row + at, n, whole);
+                    for (int i = 0; i < E / 2; ++i) v[i] = __fadd2_rn(v[i], g[i]);
+                }
+                Chunk<S, E> c;
+                c.set(v);
+                put<MOVES>(c, to + j * kNext, there[j]);
+                if constexpr (BRANCH) {
+                    if (P.d_branch) {
+                        mask.apply<E>(v, row, column + j * kNext);
+                        Chunk<T, E> b;
+                        b.set(v);
+                        put<MOVES>(b, to_x + j * kNext, there[j]);
+                    }
                 }
             }
         }
+        if constexpr (kHeld && kAhead) settle(next);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!P.partials) return;
     // The block's sums: its teams' in their order.
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-        float *to = P.partials + (static_cast<size_t>(which) * gridDim.x + blockIdx.x) * width;
-        if (team.in_block > 1) {
-            __syncthreads();
-            const int slot = C * E * team.lanes;   // of a team
+        float *to = P.partials + (static_cast<size_t>(which) * gridDim.x + blockIdx.x) * P.width;
+        const int slot = NE * team.lanes;   // of a team
+        __syncthreads();
 #pragma unroll
-            for (int j = 0; j < C; ++j)
+        for (int j = 0; j < C; ++j)
 #pragma unroll
-                for (int i = 0; i < E; ++i) scratch[team.id * slot + column_of<E>(team, j) + i] = which ? d_bias[j][i] : d_gain[j][i];
-            __syncthreads();
-            for (int c = threadIdx.x; c < width; c += blockDim.x) {
-                float t = 0.0f;
-                for (int k = 0; k < team.in_block; ++k) t += scratch[k * slot + c];
-                to[c] = t;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < C; ++j)
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const int c = column_of<E>(team, j) + i;
-                    if (c < width) to[c] = which ? d_bias[j][i] : d_gain[j][i];
-                }
+            for (int i = 0; i < E / 2; ++i)
+                *reinterpret_cast<float2 *>(scratch + team.id * slot + column + j * kNext + 2 * i) = which ? d_bias[j][i] : d_gain[j][i];
+        __syncthreads();
+        for (int c = threadIdx.x; c < P.width; c += blockDim.x) {
+            float t = 0.0f;
+            for (int k = 0; k < team.in_block; ++k) t += scratch[k * slot + c];
+            to[c] = t;
         }
     }
 }
@@ -279,70 +404,89 @@ static __global__ void __launch_bounds__(1024) gain_kernel(const __grid_constant
 // launches of one pair of types
 // ----------------------------------------------------------------------------
 
-inline int lanes_of(int chunks, int each) {   // of a team whose lanes have `each` chunks at most
-    const int need = (chunks + each - 1) / each;
+inline int lanes_of(int width, int each) {   // of a team whose lanes have `each` elements at most
+    const int need = (width + each - 1) / each;
     if (need > 32) return (need + 31) / 32 * 32;
     int lanes = 1;
     while (lanes < need) lanes *= 2;
     return lanes;
 }
 
-template <typename T, typename S, int E, int C, int R, bool BRANCH>
+// Blocks of `threads` with `smem` bytes each that an SM of 227 KB holds, given 128 registers a thread.
+inline int resident(int threads, size_t smem) {
+    const int by_threads = 512 / threads, by_smem = static_cast<int>(226 * 1024 / (smem + 1024));
+    return by_threads < by_smem ? by_threads : by_smem < 1 ? 1 : by_smem;
+}
+
+template <typename K>
+cudaError_t allow(K kernel, size_t smem) {   // more shared memory than a kernel has without asking
+    return smem > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) : cudaSuccess;
+}
+
+template <typename T, typename S, int E, int NE, int R, bool BRANCH, int MOVES>
 cudaError_t forward(NormLaunch L, cudaStream_t stream) {
-    L.lanes = lanes_of((L.width + E - 1) / E, C);
+    using F = Forward<T, S, E, NE, R, BRANCH>;
+    L.lanes = lanes_of(L.width, NE);
     const int threads = L.lanes > 256 ? L.lanes : 256 / L.lanes * L.lanes, teams = threads / L.lanes;
+    const size_t smem = (L.lanes > 32 ? teams * R * 192 : 0) + static_cast<size_t>(F::kStages) * F::kBytes * threads;
     const long long want = (L.rows + static_cast<long long>(teams) * R - 1) / (static_cast<long long>(teams) * R);
-    const long long most = 8ll * L.sm_count;
-    const size_t smem = L.lanes > 32 ? teams * 128 * sizeof(float) : 0;
-    forward_kernel<T, S, E, C, R, BRANCH><<<static_cast<unsigned>(want < most ? want : most), threads, smem, stream>>>(L);
+    const long long most = static_cast<long long>(resident(threads, smem)) * L.sm_count;
+    auto kernel = forward_kernel<T, S, E, NE, R, BRANCH, MOVES>;
+    const cudaError_t e = allow(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>(want < most ? want : most), threads, smem, stream>>>(L);
     return cudaGetLastError();
 }
 
-template <typename T, typename S, int E, bool BRANCH>
-cudaError_t forward(const NormLaunch &L, cudaStream_t stream) {
-    const int chunks = (L.width + E - 1) / E;
-    if (chunks <= 32) return forward<T, S, E, 1, 4, BRANCH>(L, stream);
-    if (chunks <= 64) return forward<T, S, E, 2, 2, BRANCH>(L, stream);
-    return forward<T, S, E, 4, 1, BRANCH>(L, stream);
-}
-
-template <typename T, typename S, int E, int C, int THREADS, bool BRANCH>
-cudaError_t backward_of(NormLaunch L, cudaStream_t stream) {
-    L.lanes = lanes_of((L.width + E - 1) / E, C);
+template <typename T, typename S, int E, int NE, bool BRANCH, int MOVES>
+cudaError_t backward(NormLaunch L, cudaStream_t stream) {
+    using B = Backward<T, S, NE, BRANCH>;
+    L.lanes = lanes_of(L.width, NE);
     const int threads = L.lanes > 256 ? L.lanes : 256 / L.lanes * L.lanes, teams = threads / L.lanes;
-    long long blocks = (L.rows + teams - 1) / teams, most = 2ll * L.sm_count;
+    size_t smem = (L.lanes > 32 ? teams * 320 : 0) + static_cast<size_t>(B::kStages) * B::kBytes * threads;
+    const size_t sums = static_cast<size_t>(threads) * NE * sizeof(float);
+    if (smem < sums) smem = sums;
+    long long blocks = (L.rows + teams - 1) / teams;
+    const long long most = static_cast<long long>(resident(threads, smem)) * L.sm_count;
     blocks = blocks < 1 ? 1 : blocks < most ? blocks : most;
-    size_t smem = L.lanes > 32 ? teams * 256 * sizeof(float) : 0;
-    if (teams > 1) {
-        const size_t sums = static_cast<size_t>(threads) * C * E * sizeof(float);
-        smem = smem > sums ? smem : sums;
-    }
-    backward_kernel<T, S, E, C, THREADS, BRANCH><<<static_cast<unsigned>(blocks), threads, smem, stream>>>(L);
-    if (!L.partials) return cudaGetLastError();
-    const cudaError_t e = cudaGetLastError();
+    auto kernel = backward_kernel<T, S, E, NE, BRANCH, MOVES>;
+    cudaError_t e = allow(kernel, smem);
     if (e != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>(blocks), threads, smem, stream>>>(L);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !L.partials) return e;
     return launch_after(gain_kernel, dim3((L.width + 31) / 32, 2), 1024, 0, stream, L, static_cast<int>(blocks));
 }
 
-template <typename T, typename S, int E, bool BRANCH>
-cudaError_t backward_of(const NormLaunch &L, cudaStream_t stream) {
-    constexpr int kEach = 16 / E;   // chunks of a thread
-    const int chunks = (L.width + E - 1) / E;
-    if (chunks <= 32) return backward_of<T, S, E, 1, 256, BRANCH>(L, stream);
-    if (chunks <= 512 * kEach) return backward_of<T, S, E, kEach, 512, BRANCH>(L, stream);
-    return backward_of<T, S, E, kEach, 1024, BRANCH>(L, stream);
+template <typename T, typename S, int E, bool BRANCH, int MOVES>
+cudaError_t launch_widths(const NormLaunch &L, cudaStream_t stream) {
+    if (L.backward) {
+        if (L.width <= 256) return backward<T, S, E, 8, BRANCH, MOVES>(L, stream);
+        if (L.width <= 8192) return backward<T, S, E, 16, BRANCH, MOVES>(L, stream);
+        return backward<T, S, E, 32, BRANCH, MOVES>(L, stream);
+    }
+    constexpr int kRows = sizeof(S) + (BRANCH ? sizeof(T) : 0) > 6 ? 1 : 2;   // what leaves room for two stages
+    if (L.width <= 256) return forward<T, S, E, 8, 2 * kRows, BRANCH, MOVES>(L, stream);
+    if (L.width <= 8192) return forward<T, S, E, 16, kRows, BRANCH, MOVES>(L, stream);
+    return forward<T, S, E, 32, 1, BRANCH, MOVES>(L, stream);
 }
 
-template <typename T, typename S, int E>
-cudaError_t launch_chunks(const NormLaunch &L, cudaStream_t stream) {
-    if (L.backward) return L.join ? backward_of<T, S, E, true>(L, stream) : backward_of<T, S, E, false>(L, stream);
-    return L.join ? forward<T, S, E, true>(L, stream) : forward<T, S, E, false>(L, stream);
+template <typename T, typename S, int E, int MOVES>
+cudaError_t launch_branch(const NormLaunch &L, cudaStream_t stream) {
+    return L.join ? launch_widths<T, S, E, true, MOVES>(L, stream) : launch_widths<T, S, E, false, MOVES>(L, stream);
 }
 
-// One pair of types a source file (norm_*.cu).
+// Chunks of 8 for rows of 16-bit types alone, whose 16 bytes are one access; beside fp32 rows, and where rows are not
+// aligned to that, chunks of 4.
 template <typename T, typename S>
 cudaError_t launch_types(const NormLaunch &L, cudaStream_t stream) {
-    return L.wide ? launch_chunks<T, S, 8>(L, stream) : launch_chunks<T, S, 4>(L, stream);
+    if constexpr (sizeof(S) == 2) {
+        if (L.wide) return launch_branch<T, S, 8, kWhole>(L, stream);
+    }
+    if constexpr (sizeof(T) == 2) {
+        if (L.moves == kHalves) return launch_branch<T, S, 4, kHalves>(L, stream);
+    }
+    return L.moves == kWhole ? launch_branch<T, S, 4, kWhole>(L, stream) : launch_branch<T, S, 4, kWords>(L, stream);
 }
 
 }  // namespace norm

@@ -33,122 +33,179 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) 
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
+// How a call's chunks can be moved: whole (aligned to their size, and the rows
+// a multiple of it), else by the widest pieces that their alignment allows,
+// words of 4 bytes or halves of 2.
+enum Moves { kWhole = 0, kWords = 1, kHalves = 2 };
+
 template <typename T, int E>
 struct Chunk {
-    static constexpr int kWords = E * static_cast<int>(sizeof(T)) / 4;
-    uint32_t w[kWords];
+    static constexpr int kBytes = E * static_cast<int>(sizeof(T)), kWords4 = kBytes / 4;
+    static_assert(kBytes == 8 || kBytes == 16, "a chunk is one access");
+    uint32_t w[kWords4];
 
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) w[i] = 0u;
-    }
-
-    // All E elements at p, which is aligned to E elements (32 bytes are taken as two halves).
     __device__ __forceinline__ void load(const T *p) {
-        if constexpr (kWords == 2) {
+        if constexpr (kBytes == 8) {
             const uint2 u = *reinterpret_cast<const uint2 *>(p);
             w[0] = u.x, w[1] = u.y;
         } else {
-#pragma unroll
-            for (int i = 0; i < kWords; i += 4) {
-                const uint4 u = reinterpret_cast<const uint4 *>(p)[i / 4];
-                w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
-            }
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
         }
     }
     __device__ __forceinline__ void store(T *p) const {
-        if constexpr (kWords == 2) {
+        if constexpr (kBytes == 8)
             *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWords; i += 4)
-                reinterpret_cast<uint4 *>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-        }
+        else
+            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 
-    // The first n elements at p, which is aligned to one; the others are 0.
+    // The first n elements at p, the others 0, in words or halves.
+    template <int MOVES>
     __device__ __forceinline__ void load_some(const T *p, int n) {
-        if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < E; ++i) w[i] = i < n ? reinterpret_cast<const uint32_t *>(p)[i] : 0u;
-        } else {
+        if constexpr (sizeof(T) == 2 && MOVES == kHalves) {
 #pragma unroll
             for (int i = 0; i < E; i += 2) {
                 const uint32_t lo = i < n ? reinterpret_cast<const uint16_t *>(p)[i] : 0u;
                 const uint32_t hi = i + 1 < n ? reinterpret_cast<const uint16_t *>(p)[i + 1] : 0u;
                 w[i / 2] = lo | hi << 16;
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords4; ++i) w[i] = i * E < n * kWords4 ? reinterpret_cast<const uint32_t *>(p)[i] : 0u;
         }
     }
+    template <int MOVES>
     __device__ __forceinline__ void store_some(T *p, int n) const {
+        if constexpr (sizeof(T) == 2 && MOVES == kHalves) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if (i >= n) continue;
-            if constexpr (sizeof(T) == 4)
-                reinterpret_cast<uint32_t *>(p)[i] = w[i];
-            else
-                reinterpret_cast<uint16_t *>(p)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+            for (int i = 0; i < E; ++i)
+                if (i < n) reinterpret_cast<uint16_t *>(p)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords4; ++i)
+                if (i * E < n * kWords4) reinterpret_cast<uint32_t *>(p)[i] = w[i];
         }
     }
 
-    __device__ __forceinline__ void floats(float (&v)[E]) const {
+    __device__ __forceinline__ void floats(float2 (&v)[E / 2]) const {
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) v[i] = __uint_as_float(w[i]);
+            for (int i = 0; i < E / 2; ++i) v[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
         } else {
 #pragma unroll
-            for (int i = 0; i < E; i += 2) {
-                const float2 f = unpack2<T>(w[i / 2]);
-                v[i] = f.x, v[i + 1] = f.y;
-            }
+            for (int i = 0; i < E / 2; ++i) v[i] = unpack2<T>(w[i]);
         }
     }
-    __device__ __forceinline__ void set(const float (&v)[E]) {
+    __device__ __forceinline__ void set(const float2 (&v)[E / 2]) {
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) w[i] = __float_as_uint(v[i]);
+            for (int i = 0; i < E / 2; ++i) w[2 * i] = __float_as_uint(v[i].x), w[2 * i + 1] = __float_as_uint(v[i].y);
         } else {
 #pragma unroll
-            for (int i = 0; i < E; i += 2) w[i / 2] = pack2<T>(v[i], v[i + 1]);
+            for (int i = 0; i < E / 2; ++i) w[i] = pack2<T>(v[i].x, v[i].y);
         }
     }
 };
 
-// A chunk's elements, of which there are n, moved as the call's alignment
-// allows: E = 8 takes calls whose every matrix has rows of whole, aligned
-// chunks, E = 4 the others, whole and aligned or element by element.
-template <typename T, int E>
-__device__ __forceinline__ void take(Chunk<T, E> &c, const T *p, int n, bool whole) {
-    if (E == 8 || whole) {
-        if (n > 0) c.load(p); else c.clear();
+// The n elements of a chunk that are there, from and to global memory.
+template <int MOVES, typename T, int E>
+__device__ __forceinline__ void take(Chunk<T, E> &c, const T *p, int n) {
+    if constexpr (MOVES == kWhole) {
+        if (n > 0) c.load(p);
     } else {
-        c.load_some(p, n);
+        c.template load_some<MOVES>(p, n);
     }
 }
-template <typename T, int E>
-__device__ __forceinline__ void put(const Chunk<T, E> &c, T *p, int n, bool whole) {
-    if (E == 8 || whole) {
+template <int MOVES, typename T, int E>
+__device__ __forceinline__ void put(const Chunk<T, E> &c, T *p, int n) {
+    if constexpr (MOVES == kWhole) {
         if (n > 0) c.store(p);
     } else {
-        c.store_some(p, n);
+        c.template store_some<MOVES>(p, n);
     }
 }
 
-// E consecutive floats of a vector of `width`, aligned to 4 bytes alone; what lies past it, or the vector's absence, is
-// `otherwise`.
+// E consecutive floats of a vector of `width` from `at` (a multiple of 4); the vector is aligned to 4 bytes alone.  What
+// lies past it, or the vector's absence, is `otherwise`.
 template <int E>
-__device__ __forceinline__ void vector_of(const float *p, int at, int width, float otherwise, float (&v)[E]) {
-    if (p && at + E <= width && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {   // at is a multiple of 4
+__device__ __forceinline__ void vector_of(const float *p, int at, int width, float otherwise, float2 (&v)[E / 2]) {
+    if (p && at + E <= width && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
 #pragma unroll
         for (int i = 0; i < E; i += 4) {
             const float4 f = __ldg(reinterpret_cast<const float4 *>(p + at + i));
-            v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+            v[i / 2] = make_float2(f.x, f.y), v[i / 2 + 1] = make_float2(f.z, f.w);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) v[i] = p && at + i < width ? __ldg(p + at + i) : otherwise;
+        for (int i = 0; i < E; i += 2)
+            v[i / 2] = make_float2(p && at + i < width ? __ldg(p + at + i) : otherwise,
+                                   p && at + i + 1 < width ? __ldg(p + at + i + 1) : otherwise);
     }
 }
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void *from) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
+}
+
+// A thread's chunks of one matrix, N a step, on their way to it through its own
+// places in shared memory.  No other thread reads those, so that the thread's
+// own wait for its copies is all that a step needs.  Halves, which no
+// asynchronous copy takes, wait in registers for one step.
+template <typename T, int E, int N, int MOVES>
+struct Feed {
+    static constexpr int kUnit = Chunk<T, E>::kBytes;
+    static constexpr bool kHeld = MOVES == kHalves && sizeof(T) == 2;
+    uint32_t at;   // of chunk 0 of stage 0
+    Chunk<T, E> held[kHeld ? N : 1];
+
+    // `base`: where the block's places for this matrix start, [stages][N][threads] units.  Places that no copy writes,
+    // those past a row's end, are 0.
+    __device__ __forceinline__ Feed(uint32_t base, int stages) {
+        at = base + threadIdx.x * kUnit;
+        for (int i = 0; i < stages * N; ++i) {
+            if constexpr (kUnit == 16)
+                st_shared_v4(at + i * blockDim.x * kUnit, 0, 0, 0, 0);
+            else
+                asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(at + i * blockDim.x * kUnit), "r"(0) : "memory");
+        }
+    }
+    __device__ __forceinline__ uint32_t place(int stage, int i) const { return at + (stage * N + i) * blockDim.x * kUnit; }
+    __device__ __forceinline__ void copy(int stage, int i, const T *p, int n) {
+        const uint32_t to = place(stage, i);
+        if constexpr (kHeld) {
+            held[i].template load_some<MOVES>(p, n);
+        } else if constexpr (MOVES == kWhole) {
+            if (n > 0) copy_async<kUnit>(to, p);
+        } else {
+            constexpr int kWords4 = kUnit / 4;
+#pragma unroll
+            for (int k = 0; k < kWords4; ++k)
+                if (k * E < n * kWords4) copy_async<4>(to + 4 * k, reinterpret_cast<const uint32_t *>(p) + k);
+        }
+    }
+    // What is held, to its stage.
+    __device__ __forceinline__ void settle(int stage) {
+        if constexpr (kHeld) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(place(stage, i)), "r"(held[i].w[0]), "r"(held[i].w[1]) : "memory");
+        }
+    }
+    __device__ __forceinline__ Chunk<T, E> chunk(int stage, int i) const {
+        Chunk<T, E> c;
+        if constexpr (kUnit == 16)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(c.w[0]), "=r"(c.w[1]), "=r"(c.w[2]), "=r"(c.w[3]) : "r"(place(stage, i)) : "memory");
+        else
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(c.w[0]), "=r"(c.w[1]) : "r"(place(stage, i)) : "memory");
+        return c;
+    }
+    __device__ __forceinline__ void floats(int stage, int i, float2 (&v)[E / 2]) const { chunk(stage, i).floats(v); }
+};
 
 // ----------------------------------------------------------------------------
 // dropout
@@ -175,20 +232,23 @@ struct Mask {
         : k0(0), k1(0), step0(0), step1(0), site(m.site << 16), least(m.least), scale(m.scale) {
         if (least) {
             const uint2 key = *reinterpret_cast<const uint2 *>(m.seed), step = *reinterpret_cast<const uint2 *>(m.seed + 1);
-            k0 = key.x, k1 = key.y, step0 = step.x, step1 = step.y;
+            // through a shuffle, which tells the compiler that these are the warp's: the rounds' keys are then added up
+            // beside the other arithmetic
+            k0 = __shfl_sync(0xffffffffu, key.x, 0), k1 = __shfl_sync(0xffffffffu, key.y, 0);
+            step0 = __shfl_sync(0xffffffffu, step.x, 0), step1 = __shfl_sync(0xffffffffu, step.y, 0);
         }
     }
     // E elements of row `row` from column `at` (a multiple of 4): kept ones times scale, the others 0 whatever they hold.
     template <int E>
-    __device__ __forceinline__ void apply(float (&v)[E], uint32_t row, int at) const {
+    __device__ __forceinline__ void apply(float2 (&v)[E / 2], uint32_t row, int at) const {
         if (!least) return;
 #pragma unroll
-        for (int i = 0; i < E; i += 4) {
-            const uint4 r = philox(make_uint4(static_cast<uint32_t>((at + i) >> 2) | site, row, step0, step1), k0, k1);
-            v[i] = r.x >= least ? v[i] * scale : 0.0f;
-            v[i + 1] = r.y >= least ? v[i + 1] * scale : 0.0f;
-            v[i + 2] = r.z >= least ? v[i + 2] * scale : 0.0f;
-            v[i + 3] = r.w >= least ? v[i + 3] * scale : 0.0f;
+        for (int i = 0; i < E / 2; i += 2) {
+            const uint4 r = philox(make_uint4(static_cast<uint32_t>((at + 2 * i) >> 2) | site, row, step0, step1), k0, k1);
+            v[i].x = r.x >= least ? v[i].x * scale : 0.0f;
+            v[i].y = r.y >= least ? v[i].y * scale : 0.0f;
+            v[i + 1].x = r.z >= least ? v[i + 1].x * scale : 0.0f;
+            v[i + 1].y = r.w >= least ? v[i + 1].y * scale : 0.0f;
         }
     }
 };
@@ -197,10 +257,40 @@ struct Mask {
 // teams
 // ----------------------------------------------------------------------------
 
+// Sums over a warp of N values (1, 2 or 4), the same in each lane: with several, halves of the warp take some of them each
+// and hand them round at the end, 9 shuffles for four sums instead of 20.
+template <int N>
+__device__ __forceinline__ void warp_sum(float (&v)[N]) {
+    const uint32_t lane = threadIdx.x;
+    auto swap = [](float x, int o) { return __shfl_xor_sync(0xffffffffu, x, o); };
+    if constexpr (N == 1) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v[0] += swap(v[0], o);
+    } else if constexpr (N == 2) {
+        const bool upper = lane & 16;
+        float t = (upper ? v[1] : v[0]) + swap(upper ? v[0] : v[1], 16);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) t += swap(t, o);
+        const float u = swap(t, 16);
+        v[0] = upper ? u : t, v[1] = upper ? t : u;
+    } else {
+        static_assert(N == 4, "");
+        const bool upper = lane & 16, odd = lane & 8;
+        const float a = (upper ? v[2] : v[0]) + swap(upper ? v[0] : v[2], 16);
+        const float b = (upper ? v[3] : v[1]) + swap(upper ? v[1] : v[3], 16);
+        float t = (odd ? b : a) + swap(odd ? a : b, 8);
+#pragma unroll
+        for (int o = 4; o; o >>= 1) t += swap(t, o);
+        const float u = swap(t, 8), lo = odd ? u : t, hi = odd ? t : u, lo2 = swap(lo, 16), hi2 = swap(hi, 16);
+        v[0] = upper ? lo2 : lo, v[1] = upper ? hi2 : hi, v[2] = upper ? lo : lo2, v[3] = upper ? hi : hi2;
+    }
+}
+
 // The lanes that take a row together: 2^k lanes of a warp, or whole warps.
 struct Team {
     int lane, lanes;      // this thread's place, the team's size
     int index, count;     // the team's place among the grid's
+    int first;            // the index of the warp's first team
     int id, in_block;     // its place in the block, the block's teams
     __device__ __forceinline__ explicit Team(int lanes_) : lanes(lanes_) {
         id = threadIdx.x / lanes;
@@ -208,28 +298,34 @@ struct Team {
         in_block = blockDim.x / lanes;
         index = blockIdx.x * in_block + id;
         count = gridDim.x * in_block;
+        first = lanes < 32 ? index - (threadIdx.x & 31) / lanes : index;
     }
-    // Sums of N values over the team, the same in each lane, in a fixed order.  `scratch`: N * 32 floats of the team's own
-    // in shared memory, of two that calls alternate between (a team of several warps needs one barrier a sum, then).
-    template <int N>
+    // Sums of N values over the team, the same in each lane, in a fixed order.  `scratch`: 16 * N floats of the team's own
+    // in shared memory, 16-byte aligned, of two that calls alternate between (a team of several warps needs one barrier a
+    // sum, then).  WARPS: the team is one warp or more.
+    template <int N, bool WARPS>
     __device__ __forceinline__ void sum(float (&v)[N], float *scratch) const {
-        const int within = lanes < 32 ? lanes : 32;
-        for (int o = 1; o < within; o <<= 1) {
+        if constexpr (!WARPS) {
+            for (int o = 1; o < lanes; o <<= 1) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-        }
-        if (lanes > 32) {
-            const int warps = lanes >> 5;
-            if ((lane & 31) == 0) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) scratch[i * 32 + (lane >> 5)] = v[i];
+                for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
             }
-            named_barrier_sync(1 + id, lanes);
+        } else {
+            warp_sum(v);
+            if (lanes > 32) {
+                const int warps = lanes >> 5;
+                if ((lane & 31) == 0) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                float t = 0.0f;
-                for (int w = 0; w < warps; ++w) t += scratch[i * 32 + w];
-                v[i] = t;
+                    for (int i = 0; i < N; ++i) scratch[(lane >> 5) * N + i] = v[i];
+                }
+                named_barrier_sync(1 + id, lanes);
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = scratch[i];
+#pragma unroll 1
+                for (int w = 1; w < warps; ++w) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) v[i] += scratch[w * N + i];
+                }
             }
         }
     }
