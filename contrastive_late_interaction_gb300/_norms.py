@@ -25,114 +25,127 @@ _pack_join = struct.Struct("@2i2Q16QdQI4x4Qf4x3Q")
 assert _pack_norm.size == _b.ctypes.sizeof(_b.LayerNormArgs)
 assert _pack_dropout.size == _b.ctypes.sizeof(_b.DropoutArgs)
 assert _pack_join.size == _b.ctypes.sizeof(_b.DropoutLayerNormArgs)
-_VERBS = {v: _b._fast(v) for v in ("layer_norm", "layer_norm_backward", "dropout", "dropout_backward",
-                                   "dropout_layer_norm", "dropout_layer_norm_backward")}
+_VERBS = {v: (_b._fast(v), p.pack) for p, verbs in (
+    (_pack_norm, ("layer_norm", "layer_norm_backward")), (_pack_dropout, ("dropout", "dropout_backward")),
+    (_pack_join, ("dropout_layer_norm", "dropout_layer_norm_backward"))) for v in verbs}
 _NONE = 0, 0
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_F32, _I64 = torch.float32, torch.int64
 
 
-def _call(verb, lead, pack, *words):
-    """The verb on `lead`'s device and that device's current stream, or raises."""
-    device = lead.get_device()
+def _call(verb, lead, device, args):
+    """The verb on `device`, that of `lead`, and its current stream, or raises.  `args`: the struct up to the stream."""
+    call, pack = _VERBS[verb]
     if device >= 0 and device != _current_device():
         with torch.cuda.device(device):
-            rc = _VERBS[verb](pack(*words, _b._raw_stream(lead)))
+            rc = call(pack(*args, _b._raw_stream(lead)))
     else:
-        rc = _VERBS[verb](pack(*words, _b._raw_stream(lead)))
+        rc = call(pack(*args, _b._raw_stream(lead)))
     if rc:
         _b.raise_for(rc, verb)
 
 
+# The checks below ask a tensor for little: each question costs a tenth of a microsecond.
+
 def _first(t, name):
-    """The shape of the call's first matrix [rows, width]."""
+    """(shape, data type, device) of the call's first matrix [rows, width]."""
     if not t.is_cuda:
         _b._check_cuda(t, name)
     if t.dim() != 2:
         raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name} must be [rows, width], not {list(t.shape)}")
-    if t.dtype not in DTYPES:
-        raise UnsupportedError(CLI_UNSUPPORTED, f"{name}: {t.dtype}")
-    return t.shape
+    dtype = t.dtype
+    if dtype not in DTYPES:
+        raise UnsupportedError(CLI_UNSUPPORTED, f"{name}: {dtype}")
+    return t.shape, dtype, t.get_device()
 
 
-def _matrix(t, name, shape, dtype, lead):
-    """(data, row stride) of a matrix of `shape` whose rows' elements are adjacent, on lead's device."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
-        _b._check_cuda(t, name, dtype)
+def _matrix(t, name, shape, dtype, device):
+    """(data, row stride) of a matrix of `shape` on `device` whose rows' elements are adjacent."""
+    if t.get_device() != device:
+        _elsewhere(t, name)
+    if t.dtype is not dtype:
+        raise InvalidArgumentError(CLI_INVALID_ARGUMENT, f"{name} must be {dtype}")
+    if t.shape != shape:
         raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name} must be {list(shape)}, not {list(t.shape)}")
-    _same_device(t, name, lead)
     row, inner = t.stride()
     if inner != 1 and shape[1] > 1:
         raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name}: the elements of a row must be adjacent")
     return t.data_ptr(), row
 
 
-def _same_device(t, name, lead):
-    if t.get_device() != lead.get_device():
-        raise InvalidArgumentError(CLI_INVALID_ARGUMENT, f"{name} is on another device than the call's first matrix")
+def _elsewhere(t, name):
+    _b._check_cuda(t, name)
+    raise InvalidArgumentError(CLI_INVALID_ARGUMENT, f"{name} is on another device than the call's first matrix")
 
 
-def _vector(t, name, n, lead):
+def _vector(t, name, n, device, dtype=_F32):
+    """The address of a packed vector of n elements on `device`, 0 for None."""
     if t is None:
         return 0
-    at = _b._vector(t, name, n, torch.float32)
-    _same_device(t, name, lead)
-    return at
+    if t.get_device() != device:
+        _elsewhere(t, name)
+    if t.dtype is not dtype:
+        raise InvalidArgumentError(CLI_INVALID_ARGUMENT, f"{name} must be {dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name} must be [{n}], packed")
+    return t.data_ptr()
 
 
-def _result(out, name, shape, dtype, lead):
+def _result(out, name, shape, dtype, like, device):
     """The caller's output `name`, or a new packed one, and its (data, row stride)."""
     t = out.get(name) if out else None
     if t is not None:
-        return t, _matrix(t, "out " + name, shape, dtype, lead)
-    t = torch.empty(shape, dtype=dtype, device=lead.device)
+        return t, _matrix(t, "out " + name, shape, dtype, device)
+    if dtype is like.dtype and like.is_contiguous():
+        t = torch.empty_like(like)
+    else:
+        t = torch.empty(shape, dtype=dtype, device=like.device)
     return t, (t.data_ptr(), shape[1])
 
 
-def _gradient(out, name, of, lead):
+def _gradient(out, name, of, device):
     """The gradient of a vector: the caller's or a new one, and its address; None where the vector is."""
     if of is None:
         return None, 0
     t = out.get(name) if out else None
     if t is not None:
-        return t, _vector(t, "out " + name, of.numel(), lead)
+        return t, _vector(t, "out " + name, of.numel(), device)
     t = torch.empty_like(of)
     return t, t.data_ptr()
 
 
-def _other(dtype, lead, what):
-    """A type that goes with lead's stream type: the same, or a 16-bit one beside fp32."""
-    if dtype is None:
-        return lead.dtype
-    if dtype not in DTYPES or (dtype is not lead.dtype and lead.dtype is not torch.float32):
-        raise UnsupportedError(CLI_UNSUPPORTED, f"{what}: {dtype} beside {lead.dtype}")
+def _other(dtype, stream, what):
+    """A type that goes with the stream's: the same, or a 16-bit one beside fp32."""
+    if dtype is None or dtype is stream:
+        return stream
+    if dtype not in DTYPES or stream is not _F32:
+        raise UnsupportedError(CLI_UNSUPPORTED, f"{what}: {dtype} beside {stream}")
     return dtype
 
 
-def _mask(rate, seed, site, lead):
+def _mask(rate, seed, site, device):
     """The mask's words in a struct."""
     if not 0 <= site <= 65535:
         raise InvalidArgumentError(CLI_INVALID_ARGUMENT, "site must be 0 .. 65535")
-    if seed is None:
-        return rate, 0, site   # refused by the library unless the rate is 0
-    at = _b._vector(seed, "seed", 2, torch.int64)
-    _same_device(seed, "seed", lead)
-    return rate, at, site
+    # without a seed it is refused by the library unless the rate is 0
+    return rate, _vector(seed, "seed", 2, device, _I64), site
 
 
 def layer_norm_backward_workspace_bytes(rows, width):
     return int(_b.lib.layer_norm_backward_workspace_bytes(rows, width))
 
 
-def _workspace(workspace, wanted, rows, width, lead):
+def _workspace(workspace, wanted, shape, like, device):
     """(tensor to keep until the call is made, address, bytes)"""
     if workspace is not None:
         lent = _b._lent(workspace)
-        _same_device(workspace, "workspace", lead)
+        if workspace.get_device() != device:
+            _elsewhere(workspace, "workspace")
         return workspace, *lent
     if not wanted:
         return None, 0, 0
-    need = _b.lib.layer_norm_backward_workspace_bytes(rows, width)
-    workspace = _b._ws(need, lead.device)
+    need = _b.lib.layer_norm_backward_workspace_bytes(*shape)
+    workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
     return workspace, workspace.data_ptr(), need
 
 
@@ -142,13 +155,13 @@ def layer_norm(x, gain=None, bias=None, epsilon=1e-5, dtype=None, out=None, stre
     fp32 `x` if wanted.  Returns dict(output); out['output'] may be `x` itself."""
     if stream is not None:
         return _b._on(stream, layer_norm, locals())
-    shape = _first(x, "x")
-    to = _other(dtype, x, "dtype")
-    given = _matrix(x, "x", shape, x.dtype, x)
-    g, b = _vector(gain, "gain", shape[1], x), _vector(bias, "bias", shape[1], x)
-    y, made = _result(out, "output", shape, to, x)
-    _call("layer_norm", x, _pack_norm.pack, DTYPES[x.dtype], DTYPES[to], *shape, *given, *made, *_NONE, *_NONE, g, b, 0, 0,
-          epsilon, 0, 0)
+    shape, stream_dtype, device = _first(x, "x")
+    to = _other(dtype, stream_dtype, "dtype")
+    given = _matrix(x, "x", shape, stream_dtype, device)
+    g, b = _vector(gain, "gain", shape[1], device), _vector(bias, "bias", shape[1], device)
+    y, made = _result(out, "output", shape, to, x, device)
+    _call("layer_norm", x, device, (DTYPES[stream_dtype], DTYPES[to], *shape, *given, *made, 0, 0, 0, 0, g, b, 0, 0, epsilon,
+                                    0, 0))
     return {"output": y}
 
 
@@ -158,18 +171,17 @@ def layer_norm_backward(x, d_output, gain=None, bias=None, epsilon=1e-5, out=Non
     type with it, `d_output`."""
     if stream is not None:
         return _b._on(stream, layer_norm_backward, locals())
-    shape = _first(x, "x")
-    _first(d_output, "d_output")
-    to = _other(d_output.dtype, x, "d_output")
-    given, dy = _matrix(x, "x", shape, x.dtype, x), _matrix(d_output, "d_output", shape, to, x)
-    g = _vector(gain, "gain", shape[1], x)
-    _vector(bias, "bias", shape[1], x)
-    dx, made = _result(out, "d_x", shape, x.dtype, x)
-    d_gain, dg = _gradient(out, "d_gain", gain, x)
-    d_bias, db = _gradient(out, "d_bias", bias, x)
-    workspace, *lent = _workspace(workspace, dg or db, *shape, x)
-    _call("layer_norm_backward", x, _pack_norm.pack, DTYPES[x.dtype], DTYPES[to], *shape, *given, *_NONE, *dy, *made, g, 0,
-          dg, db, epsilon, *lent)
+    shape, stream_dtype, device = _first(x, "x")
+    to = _other(d_output.dtype, stream_dtype, "d_output")
+    given, dy = _matrix(x, "x", shape, stream_dtype, device), _matrix(d_output, "d_output", shape, to, device)
+    g = _vector(gain, "gain", shape[1], device)
+    _vector(bias, "bias", shape[1], device)
+    dx, made = _result(out, "d_x", shape, stream_dtype, x, device)
+    d_gain, dg = _gradient(out, "d_gain", gain, device)
+    d_bias, db = _gradient(out, "d_bias", bias, device)
+    workspace, *lent = _workspace(workspace, dg or db, shape, x, device)
+    _call("layer_norm_backward", x, device, (DTYPES[stream_dtype], DTYPES[to], *shape, *given, 0, 0, *dy, *made, g, 0, dg, db,
+                                             epsilon, *lent))
     return {"d_x": dx, "d_gain": d_gain, "d_bias": d_bias}
 
 
@@ -179,11 +191,11 @@ def dropout(x, rate, seed, site=0, out=None, stream=None):
     may be `x` itself."""
     if stream is not None:
         return _b._on(stream, dropout, locals())
-    shape = _first(x, "x")
-    given = _matrix(x, "x", shape, x.dtype, x)
-    mask = _mask(rate, seed, site, x)
-    y, made = _result(out, "output", shape, x.dtype, x)
-    _call("dropout", x, _pack_dropout.pack, DTYPES[x.dtype], *shape, *given, *made, *_NONE, *_NONE, *mask)
+    shape, dtype, device = _first(x, "x")
+    given = _matrix(x, "x", shape, dtype, device)
+    mask = _mask(rate, seed, site, device)
+    y, made = _result(out, "output", shape, dtype, x, device)
+    _call("dropout", x, device, (DTYPES[dtype], *shape, *given, *made, 0, 0, 0, 0, *mask))
     return {"output": y}
 
 
@@ -191,12 +203,11 @@ def dropout_backward(d_output, rate, seed, site=0, out=None, stream=None):
     """The gradient of dropout for its input: `d_output` through the same mask.  Returns dict(d_x)."""
     if stream is not None:
         return _b._on(stream, dropout_backward, locals())
-    shape = _first(d_output, "d_output")
-    given = _matrix(d_output, "d_output", shape, d_output.dtype, d_output)
-    mask = _mask(rate, seed, site, d_output)
-    dx, made = _result(out, "d_x", shape, d_output.dtype, d_output)
-    _call("dropout_backward", d_output, _pack_dropout.pack, DTYPES[d_output.dtype], *shape, *_NONE, *_NONE, *given, *made,
-          *mask)
+    shape, dtype, device = _first(d_output, "d_output")
+    given = _matrix(d_output, "d_output", shape, dtype, device)
+    mask = _mask(rate, seed, site, device)
+    dx, made = _result(out, "d_x", shape, dtype, d_output, device)
+    _call("dropout_backward", d_output, device, (DTYPES[dtype], *shape, 0, 0, 0, 0, *given, *made, *mask))
     return {"d_x": dx}
 
 
@@ -208,16 +219,16 @@ def dropout_layer_norm(x, residual, rate, seed, site=0, gain=None, bias=None, ep
     `residual` and out['output'] `x`."""
     if stream is not None:
         return _b._on(stream, dropout_layer_norm, locals())
-    shape = _first(x, "x")
-    _first(residual, "residual")
-    _other(x.dtype, residual, "x")
-    given, stay = _matrix(x, "x", shape, x.dtype, x), _matrix(residual, "residual", shape, residual.dtype, x)
-    mask = _mask(rate, seed, site, x)
-    g, b = _vector(gain, "gain", shape[1], x), _vector(bias, "bias", shape[1], x)
-    total, total_made = _result(out, "sum", shape, residual.dtype, x) if want_sum else (None, _NONE)
-    y, made = _result(out, "output", shape, x.dtype, x)
-    _call("dropout_layer_norm", x, _pack_join.pack, DTYPES[x.dtype], DTYPES[residual.dtype], *shape, *given, *stay,
-          *total_made, *made, *_NONE, *_NONE, *_NONE, *_NONE, *mask, g, b, 0, 0, epsilon, 0, 0)
+    shape, dtype, device = _first(x, "x")
+    stream_dtype = residual.dtype
+    _other(dtype, stream_dtype, "x")
+    given, stay = _matrix(x, "x", shape, dtype, device), _matrix(residual, "residual", shape, stream_dtype, device)
+    mask = _mask(rate, seed, site, device)
+    g, b = _vector(gain, "gain", shape[1], device), _vector(bias, "bias", shape[1], device)
+    total, total_made = _result(out, "sum", shape, stream_dtype, residual, device) if want_sum else (None, _NONE)
+    y, made = _result(out, "output", shape, dtype, x, device)
+    _call("dropout_layer_norm", x, device, (DTYPES[dtype], DTYPES[stream_dtype], *shape, *given, *stay, *total_made, *made,
+                                            0, 0, 0, 0, 0, 0, 0, 0, *mask, g, b, 0, 0, epsilon, 0, 0))
     return {"sum": total, "output": y}
 
 
@@ -229,19 +240,19 @@ def dropout_layer_norm_backward(sum, d_output, rate, seed, site=0, d_sum=None, g
     d_x, d_gain, d_bias); out['d_residual'] may be `d_sum` or `sum`, and out['d_x'] `d_output`."""
     if stream is not None:
         return _b._on(stream, dropout_layer_norm_backward, locals())
-    shape = _first(sum, "sum")
-    _first(d_output, "d_output")
-    to = _other(d_output.dtype, sum, "d_output")
-    given, dy = _matrix(sum, "sum", shape, sum.dtype, sum), _matrix(d_output, "d_output", shape, to, sum)
-    onward = _NONE if d_sum is None else _matrix(d_sum, "d_sum", shape, sum.dtype, sum)
-    mask = _mask(rate, seed, site, sum)
-    g = _vector(gain, "gain", shape[1], sum)
-    _vector(bias, "bias", shape[1], sum)
-    stay, stay_made = _result(out, "d_residual", shape, sum.dtype, sum)
-    dx, made = _result(out, "d_x", shape, to, sum) if want_d_x else (None, _NONE)
-    d_gain, dg = _gradient(out, "d_gain", gain, sum)
-    d_bias, db = _gradient(out, "d_bias", bias, sum)
-    workspace, *lent = _workspace(workspace, dg or db, *shape, sum)
-    _call("dropout_layer_norm_backward", sum, _pack_join.pack, DTYPES[to], DTYPES[sum.dtype], *shape, *_NONE, *_NONE,
-          *given, *_NONE, *dy, *onward, *stay_made, *made, *mask, g, 0, dg, db, epsilon, *lent)
+    shape, stream_dtype, device = _first(sum, "sum")
+    to = _other(d_output.dtype, stream_dtype, "d_output")
+    given, dy = _matrix(sum, "sum", shape, stream_dtype, device), _matrix(d_output, "d_output", shape, to, device)
+    onward = _NONE if d_sum is None else _matrix(d_sum, "d_sum", shape, stream_dtype, device)
+    mask = _mask(rate, seed, site, device)
+    g = _vector(gain, "gain", shape[1], device)
+    _vector(bias, "bias", shape[1], device)
+    stay, stay_made = _result(out, "d_residual", shape, stream_dtype, sum, device)
+    dx, made = _result(out, "d_x", shape, to, d_output, device) if want_d_x else (None, _NONE)
+    d_gain, dg = _gradient(out, "d_gain", gain, device)
+    d_bias, db = _gradient(out, "d_bias", bias, device)
+    workspace, *lent = _workspace(workspace, dg or db, shape, sum, device)
+    _call("dropout_layer_norm_backward", sum, device, (
+        DTYPES[to], DTYPES[stream_dtype], *shape, 0, 0, 0, 0, *given, 0, 0, *dy, *onward, *stay_made, *made, *mask, g, 0, dg,
+        db, epsilon, *lent))
     return {"d_residual": stay, "d_x": dx, "d_gain": d_gain, "d_bias": d_bias}

@@ -5,6 +5,10 @@
 // least rate * 2^32, else 0, with scale = 1 / P(kept).  The word depends on the
 // seed, the step, the call's site, the row and the column alone, so the
 // backward draws it again and no mask is stored.
+//
+// Work.  A thread has a chunk of one row in every few, always the same columns:
+// what the generator's first rounds make of those and of the step is worked out
+// once.  It takes kUnroll rows at a time, the next ones on their way.
 
 #include "rows.cuh"
 
@@ -12,54 +16,88 @@ namespace cli {
 namespace rows {
 namespace {
 
-constexpr int kThreads = 256, kUnroll = 4;
+constexpr int kUnroll = 4;
 
-// The rows' chunks, counted through: a block takes kThreads * kUnroll of them at a time.  magic: 2^32 / chunks of a row,
-// rounded up (0 for one chunk); next_row, next_chunk: how far the grid is across.
+// The rounds' keys in registers: 18 additions a row less.  They come by way of shared memory, or the compiler would add
+// them up again in each row.
+struct HeldKeys {
+    uint32_t k[20];
+    __device__ __forceinline__ uint32_t a(int i) const { return k[i]; }
+    __device__ __forceinline__ uint32_t b(int i) const { return k[10 + i]; }
+    __device__ __forceinline__ explicit HeldKeys(const Mask &mask) {
+        __shared__ uint32_t keys[20];
+        const int i = threadIdx.x;
+        if (i < 20) keys[i] = i < 10 ? mask.k0 + i * kWeyl0 : mask.k1 + (i - 10) * kWeyl1;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 20; ++j) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(k[j]) : "r"(smem_u32(keys + j)));
+    }
+};
+
+// Lanes whose chunks make a span: whole chunks stand for themselves; pieces of 16 lanes are 32 bytes at least.
+template <int MOVES> constexpr int kPart = MOVES == kWhole ? 1 : 16;
+
+// spans: that the block has of each row; height: rows that it takes side by side.
 template <typename T, int E, int MOVES>
-__global__ void __launch_bounds__(kThreads)
-    dropout_kernel(const __grid_constant__ DropoutLaunch P, uint32_t chunks, uint32_t magic, long long next_row, uint32_t next_chunk) {
-    constexpr uint32_t kTile = kThreads * kUnroll;
+__global__ void __launch_bounds__(512) dropout_kernel(const __grid_constant__ DropoutLaunch P, int spans, int height) {
+    constexpr int part = kPart<MOVES>;
+    using L = Layout<T, E, MOVES, part>;
     const Mask mask(P.mask);
-    const unsigned long long start = static_cast<unsigned long long>(blockIdx.x) * kTile;
-    long long row0 = static_cast<long long>(start / chunks);
-    uint32_t chunk0 = static_cast<uint32_t>(start % chunks);
-    for (; row0 < P.rows; row0 += next_row, chunk0 += next_chunk) {
-        if (chunk0 >= chunks) {
-            chunk0 -= chunks;
-            if (++row0 >= P.rows) break;
-        }
-        Chunk<T, E> c[kUnroll];
-        long long row[kUnroll];
-        int at[kUnroll], n[kUnroll];
+    const int group = threadIdx.x / part, span = blockIdx.y * spans + group % spans, down = group / spans;
+    const L layout(part, threadIdx.x - group * part, span * part * E);
+    const uint32_t rows = static_cast<uint32_t>(P.rows), stride = gridDim.x * height;
+    const uint32_t there = down < height ? layout.template there<1>(P.width) : 0u;
+    const HeldKeys keys(mask);
+    const Block blocks[2] = {{keys, mask.block_of(layout.first_of(0, 0)), mask.step0, mask.step1},
+                             {keys, mask.block_of(layout.first_of(0, E == 8 ? 1 : 0)), mask.step0, mask.step1}};
+    const uint32_t row_word = product(kMul1, mask.step0).y ^ keys.a(0);
+    const T *in = static_cast<const T *>(P.in) + layout.column;
+    T *out = static_cast<T *>(P.out) + layout.column;
+    Chunk<T, E> next[kUnroll];
+    auto load = [&](uint32_t row) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const uint32_t k = chunk0 + threadIdx.x + u * kThreads;   // k * chunks < 2^32: the quotient is exact
-            const uint32_t down = magic ? __umulhi(k, magic) : k;
-            row[u] = row0 + down;
-            at[u] = static_cast<int>(k - down * chunks) * E;
-            n[u] = row[u] < P.rows ? min(E, P.width - at[u]) : 0;
-            take<MOVES>(c[u], static_cast<const T *>(P.in) + row[u] * P.in_row + at[u], n[u]);
-        }
+        for (int u = 0; u < kUnroll; ++u, row += stride)
+            layout.load(next[u], in + row * P.in_row, row < rows ? there : 0u);
+    };
+    uint32_t base = blockIdx.x * height;   // of the block
+    load(base + down);
+    for (; base < rows; base += kUnroll * stride) {
+        uint32_t row = base + down;
+        Chunk<T, E> now[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < kUnroll; ++u) now[u] = next[u];
+        load(row + kUnroll * stride);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u, row += stride) {
             float2 v[E / 2];
-            c[u].floats(v);
-            mask.apply<E>(v, static_cast<uint32_t>(row[u]), at[u]);
-            c[u].set(v);
-            put<MOVES>(c[u], static_cast<T *>(P.out) + row[u] * P.out_row + at[u], n[u]);
+            now[u].floats(v);
+            if (mask.least) {
+                const uint2 p = product(kMul0, row ^ row_word);
+                mask.apply<E>(layout, v, [&](int i) { return blocks[i].words(keys, p); });
+            }
+            now[u].set(v);
+            layout.store(now[u], out + row * P.out_row, row < rows ? there : 0u);
         }
     }
 }
 
 template <typename T, int E, int MOVES>
 cudaError_t launch(const DropoutLaunch &L, cudaStream_t stream) {
-    constexpr long long kTile = kThreads * kUnroll;
-    const long long chunks = (L.width + E - 1) / E, tiles = (L.rows * chunks + kTile - 1) / kTile;
-    const long long most = 8ll * L.sm_count, blocks = tiles < most ? tiles : most;
-    const uint32_t magic = chunks == 1 ? 0 : static_cast<uint32_t>(((1ull << 32) + chunks - 1) / chunks);
-    dropout_kernel<T, E, MOVES><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
-        L, static_cast<uint32_t>(chunks), magic, blocks * kTile / chunks, static_cast<uint32_t>(blocks * kTile % chunks));
+    constexpr int part = kPart<MOVES>;
+    const int all = (L.width + part * E - 1) / (part * E);   // spans of a row
+    const int pieces = (all * part + 511) / 512, spans = (all + pieces - 1) / pieces;
+    // Rows side by side: of the blocks of 256 threads and more the one that wastes least of its last warp.
+    int height = 1, threads = 0;
+    double best = 0.0;
+    for (int h = 1; h * spans * part <= 512; ++h) {
+        const int t = (h * spans * part + 31) / 32 * 32;
+        const double used = static_cast<double>(h * spans * part) / t;
+        if (!threads || t <= 256 || used > best) height = h, threads = t, best = used;
+    }
+    const long long want = (L.rows + height - 1) / height;
+    const long long most = static_cast<long long>(L.sm_count) * (1024 / threads);
+    long long across = want < most ? want : most;
+    dropout_kernel<T, E, MOVES><<<dim3(static_cast<unsigned>(across), pieces), threads, 0, stream>>>(L, spans, height);
     return cudaGetLastError();
 }
 

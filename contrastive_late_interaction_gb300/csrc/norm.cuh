@@ -24,11 +24,12 @@ using namespace rows;
 
 constexpr int kThreads = 512;   // the most of a block: one team of the widest rows
 
-// Where a thread's chunk j of a row lies: neighbours with NE = 8, whose team is a part of a warp, else the warp's chunks
-// j side by side, so that the chunks of a thread are a constant apart.
-template <int E, int NE>
-__device__ __forceinline__ int column_of(const Team &team, int j) {
-    return NE == 8 ? team.lane * 8 + j * E : (team.lane >> 5) * (32 * NE) + (team.lane & 31) * E + j * (32 * E);
+// A thread's chunks lie a constant apart where its team is whole warps (NE > 8).
+template <typename T, int E, int NE, int MOVES>
+using RowLayout = Layout<T, E, MOVES, NE == 8 ? 0 : 32>;
+template <typename L, int NE>
+__device__ __forceinline__ L layout_of(const Team &team) {
+    return NE == 8 ? L(team.lanes, team.lane, 0) : L(32, team.lane & 31, (team.lane >> 5) * (32 * NE));
 }
 
 // 1 / sqrt(variance + epsilon) of `width` deviations that sum to `sum` and whose squares sum to `squares`; e: their mean.
@@ -39,18 +40,12 @@ __device__ __forceinline__ float deviation(float sum, float squares, float inv_w
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// v - m for the n elements of a chunk that there are; the others are 0 and stay so.
-template <int E, int MOVES>
-__device__ __forceinline__ void deviations(float2 (&v)[E / 2], float m, int n) {
-    if constexpr (MOVES == kWhole) {
-        const float2 shift = both(n > 0 ? -m : 0.0f);
+// v - m for a chunk's elements that are there; the others are 0 and stay so.
+template <int E, typename L>
+__device__ __forceinline__ void deviations(float2 (&v)[E / 2], float m, uint32_t there) {
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) v[i] = __fadd2_rn(v[i], shift);
-    } else {
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i)
-            v[i] = __fadd2_rn(v[i], make_float2(2 * i < n ? -m : 0.0f, 2 * i + 1 < n ? -m : 0.0f));
-    }
+    for (int i = 0; i < E; i += 2)
+        v[i / 2] = __fadd2_rn(v[i / 2], make_float2(there >> (i / L::kPiece) & 1u ? -m : 0.0f, there >> ((i + 1) / L::kPiece) & 1u ? -m : 0.0f));
 }
 
 // Stages of a thread's places, `bytes` a step: up to 400 bytes in all, so that 512 threads' fit an SM.
@@ -78,18 +73,14 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
     Feed<S, E, C * R, MOVES> in(places, kStages);
     Feed<T, E, C * R, MOVES> branch(places + (BRANCH ? kStages * C * R * E * static_cast<int>(sizeof(S)) * blockDim.x : 0), BRANCH ? kStages : 0);
     const Mask mask(P.mask);
-    const int column = column_of<E, NE>(team, 0);
-    constexpr int kNext = NE == 8 ? E : 32 * E;   // from a chunk to the next
-    int there[C];   // elements of each chunk
+    using L = RowLayout<T, E, NE, MOVES>;
+    const L layout = layout_of<L, NE>(team);
+    const uint32_t there = layout.template there<C>(P.width);
     float2 gain[kHold ? C : 1][E / 2], bias[kHold ? C : 1][E / 2];
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-        const int at = column + j * kNext;
-        there[j] = min(max(P.width - at, 0), E);
-        if constexpr (kHold) {
-            vector_of<E>(P.gain, at, P.width, 1.0f, gain[j]);
-            vector_of<E>(P.bias, at, P.width, 0.0f, bias[j]);
-        }
+    for (int j = 0; j < C && kHold; ++j) {
+        layout.vector(P.gain, j, P.width, 1.0f, gain[j]);
+        layout.vector(P.bias, j, P.width, 0.0f, bias[j]);
     }
     const uint32_t rows = static_cast<uint32_t>(P.rows), stride = team.count * R, mine = team.index * R;
     const uint32_t first = team.first * R;   // of the warp
@@ -99,13 +90,13 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const uint32_t row = base + mine + r;
-            const bool on = row < rows;
-            const S *from = static_cast<const S *>(P.in) + row * P.in_row + column;
-            const T *x = static_cast<const T *>(P.branch) + row * P.branch_row + column;
+            const uint32_t on = row < rows ? there : 0u;
+            const S *from = static_cast<const S *>(P.in) + row * P.in_row + layout.column;
+            const T *x = static_cast<const T *>(P.branch) + row * P.branch_row + layout.column;
 #pragma unroll
             for (int j = 0; j < C; ++j) {
-                in.copy(stage, r * C + j, from + j * kNext, on ? there[j] : 0);
-                if constexpr (BRANCH) branch.copy(stage, r * C + j, x + j * kNext, on ? there[j] : 0);
+                in.copy(layout, stage, r * C + j, from + layout.chunk(j), on >> (j * L::kPieces));
+                if constexpr (BRANCH) branch.copy(layout, stage, r * C + j, x + layout.chunk(j), on >> (j * L::kPieces));
             }
         }
     };
@@ -133,8 +124,8 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const uint32_t row = base + mine + r;
-            const bool on = row < rows;
-            S *total = static_cast<S *>(P.sum) + row * P.sum_row + column;
+            const uint32_t on = row < rows ? there : 0u;
+            S *total = static_cast<S *>(P.sum) + row * P.sum_row + layout.column;
             float2 sum = both(0.0f);
 #pragma unroll
             for (int j = 0; j < C; ++j) {
@@ -142,13 +133,13 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
                 if constexpr (BRANCH) {
                     float2 f[E / 2];
                     branch.floats(stage, r * C + j, f);
-                    mask.apply<E>(f, row, column + j * kNext);
+                    mask.apply<E>(layout, f, row, j);
 #pragma unroll
                     for (int i = 0; i < E / 2; ++i) v[r][j][i] = __fadd2_rn(v[r][j][i], f[i]);
                     if (P.sum) {
                         Chunk<S, E> c;
                         c.set(v[r][j]);
-                        put<MOVES>(c, total + j * kNext, on ? there[j] : 0);
+                        layout.store(c, total + layout.chunk(j), on >> (j * L::kPieces));
                     }
                 }
 #pragma unroll
@@ -163,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
             float2 sum = both(0.0f), squares = sum;
 #pragma unroll
             for (int j = 0; j < C; ++j) {
-                deviations<E, MOVES>(v[r][j], m, there[j]);
+                deviations<E, L>(v[r][j], m, there >> (j * L::kPieces));
 #pragma unroll
                 for (int i = 0; i < E / 2; ++i) {
                     sum = __fadd2_rn(sum, v[r][j][i]);
@@ -179,8 +170,8 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             if constexpr (!kHold) {
-                vector_of<E>(P.gain, column + j * kNext, P.width, 1.0f, gain[0]);
-                vector_of<E>(P.bias, column + j * kNext, P.width, 0.0f, bias[0]);
+                layout.vector(P.gain, j, P.width, 1.0f, gain[0]);
+                layout.vector(P.bias, j, P.width, 0.0f, bias[0]);
             }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -192,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
                     y[i] = __ffma2_rn(__ffma2_rn(v[r][j][i], scale, shift), gain[kHold ? j : 0][i], bias[kHold ? j : 0][i]);
                 Chunk<T, E> c;
                 c.set(y);
-                put<MOVES>(c, static_cast<T *>(P.out) + row * P.out_row + column + j * kNext, row < rows ? there[j] : 0);
+                layout.store(c, static_cast<T *>(P.out) + row * P.out_row + layout.column + layout.chunk(j), row < rows ? there >> (j * L::kPieces) : 0u);
             }
         }
         if constexpr (kHeld && kAhead) settle(next);
@@ -222,15 +213,13 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
     places += kStages * NE * static_cast<int>(sizeof(T)) * blockDim.x;
     Feed<S, E, C, MOVES> d_sum(places, BRANCH ? kStages : 0);
     const Mask mask(P.mask);
-    const int column = column_of<E, NE>(team, 0);
-    constexpr int kNext = NE == 8 ? E : 32 * E;   // from a chunk to the next
-    int there[C];   // elements of each chunk
+    using L = RowLayout<T, E, NE, MOVES>;
+    const L layout = layout_of<L, NE>(team);
+    const uint32_t there = layout.template there<C>(P.width);
     float2 gain[kHold ? C : 1][E / 2], d_gain[C][E / 2], d_bias[C][E / 2];
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-        const int at = column + j * kNext;
-        there[j] = min(max(P.width - at, 0), E);
-        if constexpr (kHold) vector_of<E>(P.gain, at, P.width, 1.0f, gain[j]);
+        if constexpr (kHold) layout.vector(P.gain, j, P.width, 1.0f, gain[j]);
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) d_gain[j][i] = d_bias[j][i] = both(0.0f);
     }
@@ -238,16 +227,16 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
 
     auto copy = [&](uint32_t base, int stage) {
         const uint32_t row = base + mine;
-        const bool on = row < rows;
-        const S *z = static_cast<const S *>(P.in) + row * P.in_row + column;
-        const T *g = static_cast<const T *>(P.d_out) + row * P.d_out_row + column;
-        const S *more = static_cast<const S *>(P.d_sum) + row * P.d_sum_row + column;
+        const uint32_t on = row < rows ? there : 0u;
+        const S *z = static_cast<const S *>(P.in) + row * P.in_row + layout.column;
+        const T *g = static_cast<const T *>(P.d_out) + row * P.d_out_row + layout.column;
+        const S *more = static_cast<const S *>(P.d_sum) + row * P.d_sum_row + layout.column;
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-            const int n = on ? there[j] : 0;
-            in.copy(stage, j, z + j * kNext, n);
-            d_out.copy(stage, j, g + j * kNext, n);
-            if constexpr (BRANCH) d_sum.copy(stage, j, more + j * kNext, P.d_sum ? n : 0);   // none: its places stay 0
+            const uint32_t pieces = on >> (j * L::kPieces);
+            in.copy(layout, stage, j, z + layout.chunk(j), pieces);
+            d_out.copy(layout, stage, j, g + layout.chunk(j), pieces);
+            if constexpr (BRANCH) d_sum.copy(layout, stage, j, more + layout.chunk(j), P.d_sum ? pieces : 0u);   // none: its places stay 0
         }
     };
     auto settle = [&](int stage) {
@@ -291,9 +280,9 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
         // A chunk's deviations and gradient: kept with kHold, else computed again where they are used.
         auto load = [&](int j) {
             if constexpr (!kHold) in.floats(stage, j, d[0]);
-            deviations<E, MOVES>(d[kHold ? j : 0], m, there[j]);
+            deviations<E, L>(d[kHold ? j : 0], m, there >> (j * L::kPieces));
             dy[kHold ? j : 0] = d_out.chunk(stage, j);
-            if constexpr (!kHold) vector_of<E>(P.gain, column + j * kNext, P.width, 1.0f, gain[0]);
+            if constexpr (!kHold) layout.vector(P.gain, j, P.width, 1.0f, gain[0]);
         };
         {
             float2 sum = both(0.0f), squares = sum, sum_t = sum, sum_td = sum;
@@ -319,20 +308,23 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
         const float r = deviation(s4[0], s4[1], P.inv_width, P.epsilon, e);
         const float mean_t = s4[2] * P.inv_width, mean_tn = (s4[3] * P.inv_width - e * mean_t) * r;
         const float2 scale = both(r), shift = both(-e * r), less = both(-r * mean_t), less_n = both(-r * mean_tn);
-        if (on) {
-            S *to = static_cast<S *>(P.d_in) + row * P.d_in_row + column;
-            T *to_x = static_cast<T *>(P.d_branch) + row * P.d_branch_row + column;
+        if (NE == 8 || on) {   // of a warp with several teams all lanes go on together, for the mask
+            S *to = static_cast<S *>(P.d_in) + row * P.d_in_row + layout.column;
+            T *to_x = static_cast<T *>(P.d_branch) + row * P.d_branch_row + layout.column;
 #pragma unroll
             for (int j = 0; j < C; ++j) {
                 if constexpr (!kHold) load(j);
                 const int k = kHold ? j : 0;
+                const uint32_t pieces = on ? there >> (j * L::kPieces) : 0u;
                 float2 v[E / 2], g[E / 2];
                 dy[k].floats(g);
 #pragma unroll
                 for (int i = 0; i < E / 2; ++i) {
                     const float2 norm = __ffma2_rn(d[k][i], scale, shift);
-                    d_gain[j][i] = __ffma2_rn(g[i], norm, d_gain[j][i]);
-                    d_bias[j][i] = __fadd2_rn(d_bias[j][i], g[i]);
+                    if (on) {
+                        d_gain[j][i] = __ffma2_rn(g[i], norm, d_gain[j][i]);
+                        d_bias[j][i] = __fadd2_rn(d_bias[j][i], g[i]);
+                    }
                     v[i] = __ffma2_rn(__fmul2_rn(g[i], gain[k][i]), scale, __ffma2_rn(norm, less_n, less));
                 }
                 if constexpr (BRANCH) {
@@ -342,13 +334,13 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
                 }
                 Chunk<S, E> c;
                 c.set(v);
-                put<MOVES>(c, to + j * kNext, there[j]);
+                layout.store(c, to + layout.chunk(j), pieces);
                 if constexpr (BRANCH) {
-                    if (P.d_branch) {
-                        mask.apply<E>(v, row, column + j * kNext);
+                    if (P.d_branch && (L::kPiece != E || pieces)) {   // warps whose lanes have none are spared the mask
+                        mask.apply<E>(layout, v, row, j);
                         Chunk<T, E> b;
                         b.set(v);
-                        put<MOVES>(b, to_x + j * kNext, there[j]);
+                        layout.store(b, to_x + layout.chunk(j), pieces);
                     }
                 }
             }
@@ -358,17 +350,22 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!P.partials) return;
-    // The block's sums: its teams' in their order.
+    // The block's sums: its teams' in their order.  A block by itself has the gradients.
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         float *to = P.partials + (static_cast<size_t>(which) * gridDim.x + blockIdx.x) * P.width;
+        if (gridDim.x == 1) to = which ? P.d_bias : P.d_gain;
+        if (!to) continue;
         const int slot = NE * team.lanes;   // of a team
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < C; ++j)
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i)
-                *reinterpret_cast<float2 *>(scratch + team.id * slot + column + j * kNext + 2 * i) = which ? d_bias[j][i] : d_gain[j][i];
+            for (int i = 0; i < E / 2; ++i) {
+                const float2 v = which ? d_bias[j][i] : d_gain[j][i];
+                scratch[team.id * slot + layout.element(j, 2 * i)] = v.x;
+                scratch[team.id * slot + layout.element(j, 2 * i + 1)] = v.y;
+            }
         __syncthreads();
         for (int c = threadIdx.x; c < P.width; c += blockDim.x) {
             float t = 0.0f;
@@ -404,10 +401,10 @@ static __global__ void __launch_bounds__(1024) gain_kernel(const __grid_constant
 // launches of one pair of types
 // ----------------------------------------------------------------------------
 
-inline int lanes_of(int width, int each) {   // of a team whose lanes have `each` elements at most
+inline int lanes_of(int width, int each) {   // of a team whose lanes have `each` elements at most: whole groups of 4
     const int need = (width + each - 1) / each;
     if (need > 32) return (need + 31) / 32 * 32;
-    int lanes = 1;
+    int lanes = 4;
     while (lanes < need) lanes *= 2;
     return lanes;
 }
@@ -438,6 +435,9 @@ cudaError_t forward(NormLaunch L, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+// With so few rows a team and gradients over them one block takes them all, and no second kernel adds its sums up.
+constexpr int kFewRows = 4;
+
 template <typename T, typename S, int E, int NE, bool BRANCH, int MOVES>
 cudaError_t backward(NormLaunch L, cudaStream_t stream) {
     using B = Backward<T, S, NE, BRANCH>;
@@ -449,26 +449,41 @@ cudaError_t backward(NormLaunch L, cudaStream_t stream) {
     long long blocks = (L.rows + teams - 1) / teams;
     const long long most = static_cast<long long>(resident(threads, smem)) * L.sm_count;
     blocks = blocks < 1 ? 1 : blocks < most ? blocks : most;
+    if (L.partials && L.rows <= kFewRows * teams) blocks = 1;
     auto kernel = backward_kernel<T, S, E, NE, BRANCH, MOVES>;
     cudaError_t e = allow(kernel, smem);
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(blocks), threads, smem, stream>>>(L);
     e = cudaGetLastError();
-    if (e != cudaSuccess || !L.partials) return e;
+    if (e != cudaSuccess || !L.partials || blocks == 1) return e;
     return launch_after(gain_kernel, dim3((L.width + 31) / 32, 2), 1024, 0, stream, L, static_cast<int>(blocks));
 }
 
+// What a team of whole warps spends on a row goes by what its lanes could hold, there or not.
+inline int held_by(int width, int each) { return (width + 32 * each - 1) / (32 * each) * each; }
+
 template <typename T, typename S, int E, bool BRANCH, int MOVES>
 cudaError_t launch_widths(const NormLaunch &L, cudaStream_t stream) {
+    constexpr int kBytes = static_cast<int>(sizeof(S) + (BRANCH ? sizeof(T) : 0));
+    const int w = L.width;
     if (L.backward) {
-        if (L.width <= 256) return backward<T, S, E, 8, BRANCH, MOVES>(L, stream);
-        if (L.width <= 8192) return backward<T, S, E, 16, BRANCH, MOVES>(L, stream);
-        return backward<T, S, E, 32, BRANCH, MOVES>(L, stream);
+        if (w <= 256) return backward<T, S, E, 8, BRANCH, MOVES>(L, stream);
+        if constexpr (sizeof(S) == 2) {
+            // Sixteen elements of a row a thread keep the gain and the deviations in registers, which is best for the norm
+            // alone; a join, whose mask takes registers too, does better with one warp a row.
+            if (w > 512 && w <= 8192) {
+                if (held_by(w, 24) < held_by(w, 16)) return backward<T, S, E, 24, BRANCH, MOVES>(L, stream);
+                if (BRANCH && held_by(w, 32) <= held_by(w, 24)) return backward<T, S, E, 32, BRANCH, MOVES>(L, stream);
+            }
+        }
+        if (w > 8192) return backward<T, S, E, 32, BRANCH, MOVES>(L, stream);
+        return backward<T, S, E, 16, BRANCH, MOVES>(L, stream);
     }
-    constexpr int kRows = sizeof(S) + (BRANCH ? sizeof(T) : 0) > 6 ? 1 : 2;   // what leaves room for two stages
-    if (L.width <= 256) return forward<T, S, E, 8, 2 * kRows, BRANCH, MOVES>(L, stream);
-    if (L.width <= 8192) return forward<T, S, E, 16, kRows, BRANCH, MOVES>(L, stream);
-    return forward<T, S, E, 32, 1, BRANCH, MOVES>(L, stream);
+    constexpr int kRows = kBytes > 6 ? 1 : 2;   // what leaves room for two stages
+    if (w <= 256) return forward<T, S, E, 8, 2 * kRows, BRANCH, MOVES>(L, stream);
+    if (w > 8192) return forward<T, S, E, 32, 1, BRANCH, MOVES>(L, stream);
+    if (held_by(w, 24) < held_by(w, 16)) return forward<T, S, E, 24, 1, BRANCH, MOVES>(L, stream);
+    return forward<T, S, E, 16, kRows, BRANCH, MOVES>(L, stream);
 }
 
 template <typename T, typename S, int E, int MOVES>

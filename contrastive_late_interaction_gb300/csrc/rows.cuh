@@ -33,8 +33,8 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) 
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
-// How a call's chunks can be moved: whole (aligned to their size, and the rows
-// a multiple of it), else by the widest pieces that their alignment allows,
+// How a call's rows can be moved: whole chunks (aligned to their size, and the
+// rows a multiple of it), else the widest pieces that their alignment allows,
 // words of 4 bytes or halves of 2.
 enum Moves { kWhole = 0, kWords = 1, kHalves = 2 };
 
@@ -44,6 +44,10 @@ struct Chunk {
     static_assert(kBytes == 8 || kBytes == 16, "a chunk is one access");
     uint32_t w[kWords4];
 
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kWords4; ++i) w[i] = 0u;
+    }
     __device__ __forceinline__ void load(const T *p) {
         if constexpr (kBytes == 8) {
             const uint2 u = *reinterpret_cast<const uint2 *>(p);
@@ -58,34 +62,6 @@ struct Chunk {
             *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
         else
             *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-
-    // The first n elements at p, the others 0, in words or halves.
-    template <int MOVES>
-    __device__ __forceinline__ void load_some(const T *p, int n) {
-        if constexpr (sizeof(T) == 2 && MOVES == kHalves) {
-#pragma unroll
-            for (int i = 0; i < E; i += 2) {
-                const uint32_t lo = i < n ? reinterpret_cast<const uint16_t *>(p)[i] : 0u;
-                const uint32_t hi = i + 1 < n ? reinterpret_cast<const uint16_t *>(p)[i + 1] : 0u;
-                w[i / 2] = lo | hi << 16;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWords4; ++i) w[i] = i * E < n * kWords4 ? reinterpret_cast<const uint32_t *>(p)[i] : 0u;
-        }
-    }
-    template <int MOVES>
-    __device__ __forceinline__ void store_some(T *p, int n) const {
-        if constexpr (sizeof(T) == 2 && MOVES == kHalves) {
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (i < n) reinterpret_cast<uint16_t *>(p)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWords4; ++i)
-                if (i * E < n * kWords4) reinterpret_cast<uint32_t *>(p)[i] = w[i];
-        }
     }
 
     __device__ __forceinline__ void floats(float2 (&v)[E / 2]) const {
@@ -108,41 +84,100 @@ struct Chunk {
     }
 };
 
-// The n elements of a chunk that are there, from and to global memory.
-template <int MOVES, typename T, int E>
-__device__ __forceinline__ void take(Chunk<T, E> &c, const T *p, int n) {
-    if constexpr (MOVES == kWhole) {
-        if (n > 0) c.load(p);
-    } else {
-        c.template load_some<MOVES>(p, n);
+// Where the elements of a thread's chunks lie in a row of `width`.  The lanes of
+// a warp that take the row together, `part` of them, have chunks side by side,
+// a chunk being
+//   whole: E neighbouring elements, one access;
+//   else:  pieces of kPiece elements, each next to the other lanes' pieces, so
+//          that an access of the warp's covers whole lines all the same (a
+//          thread's words side by side would be written as four parts of every
+//          32 bytes: fp32 rows of 771 took 39 us where these take 24).
+// PART: `part` where it is known, else 0.
+template <typename T, int E, int MOVES, int PART>
+struct Layout {
+    static constexpr int kPiece = MOVES == kWhole ? E : MOVES == kWords && sizeof(T) == 2 ? 2 : 1, kPieces = E / kPiece;
+    int part_, lane, column;   // column: of the first chunk's first element
+    __device__ __forceinline__ Layout(int part, int lane_, int start) : part_(part), lane(lane_), column(start + lane_ * kPiece) {}
+    __device__ __forceinline__ int part() const { return PART ? PART : part_; }
+    __device__ __forceinline__ int chunk(int j) const { return j * part() * E; }        // from `column`
+    __device__ __forceinline__ int piece(int k) const { return k * part() * kPiece; }   // from the chunk's first
+    __device__ __forceinline__ int element(int j, int i) const { return column + chunk(j) + piece(i / kPiece) + i % kPiece; }
+    // The first column of the i-th block of four columns that a lane draws for chunk j: its own, or where a block lies with
+    // several lanes, the one of the piece that is the lane's to draw.
+    __device__ __forceinline__ int drawer() const { return lane & (kPieces - 1); }
+    __device__ __forceinline__ int first_of(int j, int i) const {
+        return kPieces == 1 ? column + chunk(j) + 4 * i : ((column + chunk(j)) & ~3) + piece(drawer());
     }
-}
-template <int MOVES, typename T, int E>
-__device__ __forceinline__ void put(const Chunk<T, E> &c, T *p, int n) {
-    if constexpr (MOVES == kWhole) {
-        if (n > 0) c.store(p);
-    } else {
-        c.template store_some<MOVES>(p, n);
-    }
-}
-
-// E consecutive floats of a vector of `width` from `at` (a multiple of 4); the vector is aligned to 4 bytes alone.  What
-// lies past it, or the vector's absence, is `otherwise`.
-template <int E>
-__device__ __forceinline__ void vector_of(const float *p, int at, int width, float otherwise, float2 (&v)[E / 2]) {
-    if (p && at + E <= width && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    // Bit j * kPieces + k: piece k of chunk j is there (a piece is wholly there or not at all).
+    template <int C>
+    __device__ __forceinline__ uint32_t there(int width) const {
+        static_assert(C * kPieces <= 32, "");
+        uint32_t bits = 0;
 #pragma unroll
-        for (int i = 0; i < E; i += 4) {
-            const float4 f = __ldg(reinterpret_cast<const float4 *>(p + at + i));
-            v[i / 2] = make_float2(f.x, f.y), v[i / 2 + 1] = make_float2(f.z, f.w);
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) bits |= column + chunk(j) + piece(k) < width ? 1u << (j * kPieces + k) : 0u;
+        return bits;
+    }
+    // A float of a vector for each element of chunk j; what lies past it, or its absence, is `otherwise`.
+    __device__ __forceinline__ void vector(const float *p, int j, int width, float otherwise, float2 (&v)[E / 2]) const {
+        const int at = column + chunk(j);   // a multiple of 4 where chunks are whole
+        if (MOVES == kWhole && p && at < width && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+#pragma unroll
+            for (int i = 0; i < E; i += 4) {
+                const float4 f = __ldg(reinterpret_cast<const float4 *>(p + at + i));
+                v[i / 2] = make_float2(f.x, f.y), v[i / 2 + 1] = make_float2(f.z, f.w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; i += 2) {
+                const int a = element(j, i), b = element(j, i + 1);
+                v[i / 2] = make_float2(p && a < width ? __ldg(p + a) : otherwise, p && b < width ? __ldg(p + b) : otherwise);
+            }
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < E; i += 2)
-            v[i / 2] = make_float2(p && at + i < width ? __ldg(p + at + i) : otherwise,
-                                   p && at + i + 1 < width ? __ldg(p + at + i + 1) : otherwise);
     }
-}
+    // The pieces of a chunk that `there` names (from bit 0), at p, which is the chunk's first element; the others are 0.
+    template <typename M>
+    __device__ __forceinline__ void load(Chunk<M, E> &c, const M *p, uint32_t there) const {
+        if constexpr (MOVES == kWhole) {
+            c.clear();
+            if (there & 1u) c.load(p);
+        } else if constexpr (sizeof(M) == 4 || kPiece == 2) {
+            constexpr int kWords4 = kPiece * static_cast<int>(sizeof(M)) / 4;   // of a piece
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k)
+#pragma unroll
+                for (int w = 0; w < kWords4; ++w)
+                    c.w[k * kWords4 + w] = there >> k & 1u ? reinterpret_cast<const uint32_t *>(p + piece(k))[w] : 0u;
+        } else {
+            uint32_t h[kPieces];
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) h[k] = there >> k & 1u ? *reinterpret_cast<const uint16_t *>(p + piece(k)) : 0u;
+#pragma unroll
+            for (int k = 0; k < kPieces; k += 2) c.w[k / 2] = __byte_perm(h[k], h[k + 1], 0x5410);
+        }
+    }
+    template <typename M>
+    __device__ __forceinline__ void store(const Chunk<M, E> &c, M *p, uint32_t there) const {
+        if constexpr (MOVES == kWhole) {
+            if (there & 1u) c.store(p);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                if (!(there >> k & 1u)) continue;
+                M *to = p + piece(k);
+                if constexpr (sizeof(M) == 4) {
+#pragma unroll
+                    for (int i = 0; i < kPiece; ++i) reinterpret_cast<uint32_t *>(to)[i] = c.w[k * kPiece + i];
+                } else if constexpr (kPiece == 2) {
+                    *reinterpret_cast<uint32_t *>(to) = c.w[k];
+                } else {
+                    *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(c.w[k / 2] >> (16 * (k & 1)));
+                }
+            }
+        }
+    }
+};
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t to, const void *from) {
@@ -152,40 +187,55 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void *from) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
 }
 
-// A thread's chunks of one matrix, N a step, on their way to it through its own
-// places in shared memory.  No other thread reads those, so that the thread's
-// own wait for its copies is all that a step needs.  Halves, which no
-// asynchronous copy takes, wait in registers for one step.
-template <typename T, int E, int N, int MOVES>
+// A thread's chunks of one matrix of type M, N a step, on their way to it
+// through its own places in shared memory.  No other thread reads those, so
+// that the thread's own wait for its copies is all that a step needs.  Halves,
+// which no asynchronous copy takes, wait in registers for one step.
+template <typename M, int E, int N, int MOVES>
 struct Feed {
-    static constexpr int kUnit = Chunk<T, E>::kBytes;
-    static constexpr bool kHeld = MOVES == kHalves && sizeof(T) == 2;
+    static constexpr bool kHeld = MOVES == kHalves && sizeof(M) == 2;
+    // Copies of words go to places a word wide, a thread's side by side with the others', so that they meet no bank twice.
+    static constexpr int kBytes = Chunk<M, E>::kBytes, kUnit = MOVES == kWhole || kHeld ? kBytes : 4, kUnits = kBytes / kUnit;
     uint32_t at;   // of chunk 0 of stage 0
-    Chunk<T, E> held[kHeld ? N : 1];
+    Chunk<M, E> held[kHeld ? N : 1];
 
-    // `base`: where the block's places for this matrix start, [stages][N][threads] units.  Places that no copy writes,
+    // `base`: where the block's places for this matrix start, [stages][N][units][threads].  Places that no copy writes,
     // those past a row's end, are 0.
     __device__ __forceinline__ Feed(uint32_t base, int stages) {
         at = base + threadIdx.x * kUnit;
-        for (int i = 0; i < stages * N; ++i) {
+        for (int i = 0; i < stages * N * kUnits; ++i) {
+            const uint32_t to = at + i * blockDim.x * kUnit;
             if constexpr (kUnit == 16)
-                st_shared_v4(at + i * blockDim.x * kUnit, 0, 0, 0, 0);
+                st_shared_v4(to, 0, 0, 0, 0);
+            else if constexpr (kUnit == 8)
+                asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(to), "r"(0) : "memory");
             else
-                asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(at + i * blockDim.x * kUnit), "r"(0) : "memory");
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(0) : "memory");
+        }
+        if constexpr (kHeld) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) held[i].w[0] = held[i].w[1] = 0u;
         }
     }
-    __device__ __forceinline__ uint32_t place(int stage, int i) const { return at + (stage * N + i) * blockDim.x * kUnit; }
-    __device__ __forceinline__ void copy(int stage, int i, const T *p, int n) {
-        const uint32_t to = place(stage, i);
+    __device__ __forceinline__ uint32_t place(int stage, int i, int unit = 0) const {
+        return at + ((stage * N + i) * kUnits + unit) * blockDim.x * kUnit;
+    }
+    // Chunk i of a step, whose first element is at p.
+    template <typename L>
+    __device__ __forceinline__ void copy(const L &layout, int stage, int i, const M *p, uint32_t there) {
         if constexpr (kHeld) {
-            held[i].template load_some<MOVES>(p, n);
+            layout.load(held[i], p, there);
         } else if constexpr (MOVES == kWhole) {
-            if (n > 0) copy_async<kUnit>(to, p);
+            if (there & 1u) copy_async<kUnit>(place(stage, i), p);
         } else {
-            constexpr int kWords4 = kUnit / 4;
 #pragma unroll
-            for (int k = 0; k < kWords4; ++k)
-                if (k * E < n * kWords4) copy_async<4>(to + 4 * k, reinterpret_cast<const uint32_t *>(p) + k);
+            for (int k = 0; k < L::kPieces; ++k) {
+                if (!(there >> k & 1u)) continue;
+                constexpr int kWords4 = L::kPiece * static_cast<int>(sizeof(M)) / 4;   // of a piece
+#pragma unroll
+                for (int w = 0; w < kWords4; ++w)
+                    copy_async<4>(place(stage, i, k * kWords4 + w), reinterpret_cast<const uint32_t *>(p + layout.piece(k)) + w);
+            }
         }
     }
     // What is held, to its stage.
@@ -196,12 +246,17 @@ struct Feed {
                 asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(place(stage, i)), "r"(held[i].w[0]), "r"(held[i].w[1]) : "memory");
         }
     }
-    __device__ __forceinline__ Chunk<T, E> chunk(int stage, int i) const {
-        Chunk<T, E> c;
-        if constexpr (kUnit == 16)
+    __device__ __forceinline__ Chunk<M, E> chunk(int stage, int i) const {
+        Chunk<M, E> c;
+        if constexpr (kUnit == 16) {
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(c.w[0]), "=r"(c.w[1]), "=r"(c.w[2]), "=r"(c.w[3]) : "r"(place(stage, i)) : "memory");
-        else
+        } else if constexpr (kUnit == 8) {
             asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(c.w[0]), "=r"(c.w[1]) : "r"(place(stage, i)) : "memory");
+        } else {
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k)
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(c.w[k]) : "r"(place(stage, i, k)) : "memory");
+        }
         return c;
     }
     __device__ __forceinline__ void floats(int stage, int i, float2 (&v)[E / 2]) const { chunk(stage, i).floats(v); }
@@ -214,15 +269,48 @@ struct Feed {
 // Philox 4x32 of ten rounds (Salmon, Moraes, Dror, Shaw: Parallel random
 // numbers: as easy as 1, 2, 3; 2011): four words of 32 bits from a counter of
 // four and a key of two.
-__device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
-#pragma unroll
-    for (int i = 0; i < 10; ++i) {
-        const uint64_t p = static_cast<uint64_t>(0xD2511F53u) * c.x, q = static_cast<uint64_t>(0xCD9E8D57u) * c.z;
-        c = make_uint4(static_cast<uint32_t>(q >> 32) ^ c.y ^ (k0 + i * 0x9E3779B9u), static_cast<uint32_t>(q),
-                       static_cast<uint32_t>(p >> 32) ^ c.w ^ (k1 + i * 0xBB67AE85u), static_cast<uint32_t>(p));
-    }
-    return c;
+constexpr uint32_t kMul0 = 0xD2511F53u, kMul1 = 0xCD9E8D57u, kWeyl0 = 0x9E3779B9u, kWeyl1 = 0xBB67AE85u;
+__device__ __forceinline__ uint2 product(uint32_t a, uint32_t b) {   // x: the low word
+    const uint64_t p = static_cast<uint64_t>(a) * b;
+    return make_uint2(static_cast<uint32_t>(p), static_cast<uint32_t>(p >> 32));
 }
+
+// The rounds' keys, added up where they are used.
+struct Keys {
+    uint32_t k0, k1;
+    __device__ __forceinline__ uint32_t a(int i) const { return k0 + i * kWeyl0; }
+    __device__ __forceinline__ uint32_t b(int i) const { return k1 + i * kWeyl1; }
+};
+
+// What a counter's column and step come to in the first rounds, before the row has reached every word (counter: column
+// block, row, step, step).  A multiplication of 32 x 32 to 64 bits goes out every fourth cycle, so that these decide what
+// a mask costs: 15 of 20 are left to a row, and one that a row's blocks share.
+struct Block {
+    uint32_t d, f, g, h;
+    template <typename K>
+    __device__ __forceinline__ Block(const K &k, uint32_t column, uint32_t step0, uint32_t step1) {
+        const uint2 p0 = product(kMul0, column), q0 = product(kMul1, step0);
+        const uint2 q1 = product(kMul1, p0.y ^ step1 ^ k.b(0));
+        const uint2 p2 = product(kMul0, q1.y ^ q0.x ^ k.a(1));
+        d = p0.x ^ k.b(1), f = q1.x ^ k.a(2), g = p2.y ^ k.b(2), h = p2.x ^ k.b(3);
+    }
+    // `p1`: the product of the row's word, the same for every block of a row.
+    template <typename K>
+    __device__ __forceinline__ uint4 words(const K &k, uint2 p1) const {
+        uint2 q = product(kMul1, p1.y ^ d);
+        uint4 c;
+        c.x = q.y ^ f, c.y = q.x, c.z = g ^ p1.x;
+        uint2 p = product(kMul0, c.x);
+        q = product(kMul1, c.z);
+        c = make_uint4(q.y ^ c.y ^ k.a(3), q.x, p.y ^ h, p.x);
+#pragma unroll
+        for (int i = 4; i < 10; ++i) {
+            p = product(kMul0, c.x), q = product(kMul1, c.z);
+            c = make_uint4(q.y ^ c.y ^ k.a(i), q.x, p.y ^ c.w ^ k.b(i), p.x);
+        }
+        return c;
+    }
+};
 
 // A call's mask, its seed and step read from the device: a captured call draws another mask at each step.
 struct Mask {
@@ -232,23 +320,79 @@ struct Mask {
         : k0(0), k1(0), step0(0), step1(0), site(m.site << 16), least(m.least), scale(m.scale) {
         if (least) {
             const uint2 key = *reinterpret_cast<const uint2 *>(m.seed), step = *reinterpret_cast<const uint2 *>(m.seed + 1);
-            // through a shuffle, which tells the compiler that these are the warp's: the rounds' keys are then added up
-            // beside the other arithmetic
-            k0 = __shfl_sync(0xffffffffu, key.x, 0), k1 = __shfl_sync(0xffffffffu, key.y, 0);
-            step0 = __shfl_sync(0xffffffffu, step.x, 0), step1 = __shfl_sync(0xffffffffu, step.y, 0);
+            k0 = key.x, k1 = key.y, step0 = step.x, step1 = step.y;
         }
     }
-    // E elements of row `row` from column `at` (a multiple of 4): kept ones times scale, the others 0 whatever they hold.
+    __device__ __forceinline__ uint32_t block_of(int column) const { return static_cast<uint32_t>(column >> 2) | site; }
+    // The row's word after the first round, times what the second takes it.
+    __device__ __forceinline__ uint2 row_product(uint32_t row) const { return product(kMul0, product(kMul1, step0).y ^ row ^ k0); }
+    __device__ __forceinline__ uint4 draw(uint32_t row, int column) const {
+        // row >> 31 is 0, but as far as the compiler knows the keys are another row's each time: kept from row to row, the
+        // 18 sums would take the registers that the row's sums need (164 bytes of spills in the join's gradient)
+        const Keys k{k0 ^ row >> 31, k1 ^ row >> 31};
+        return Block(k, block_of(column), step0, step1).words(k, row_product(row));
+    }
+    __device__ __forceinline__ float2 keep(float2 v, uint32_t a, uint32_t b) const {
+        v = __fmul2_rn(v, make_float2(scale, scale));
+        return make_float2(a >= least ? v.x : 0.0f, b >= least ? v.y : 0.0f);
+    }
+    // The words of a chunk's elements, four at a time, from the blocks that `drawn` gives (the i-th of the chunk's).  Where a
+    // block's four columns lie with several lanes, each of these draws another of their blocks, and they hand the words
+    // round: the lanes of such a group have to call this together.
+    template <int E, typename L, typename F, typename U>
+    __device__ __forceinline__ void words(const L &layout, F drawn, U use) const {
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+            uint4 r = drawn(i);
+            if constexpr (L::kPiece != E) {
+                const int mine = layout.drawer();
+                auto swap = [](uint32_t x, int o) { return __shfl_xor_sync(0xffffffffu, x, o); };
+                if constexpr (L::kPieces == 4) {   // r: words x, y, z, w of block `mine`; then word `mine` of blocks 0 to 3
+                    uint32_t t = swap(mine & 1 ? r.x : r.y, 1), u = swap(mine & 1 ? r.z : r.w, 1);
+                    if (mine & 1) r.x = t, r.z = u; else r.y = t, r.w = u;
+                    t = swap(mine & 2 ? r.x : r.z, 2), u = swap(mine & 2 ? r.y : r.w, 2);
+                    if (mine & 2) r.x = t, r.y = u; else r.z = t, r.w = u;
+                } else {   // then words 2 mine and 2 mine + 1 of blocks 0 and 1
+                    const uint32_t t = swap(mine ? r.x : r.z, 1), u = swap(mine ? r.y : r.w, 1);
+                    if (mine) r.x = t, r.y = u; else r.z = t, r.w = u;
+                }
+            }
+            use(i, r);
+        }
+    }
+    // Chunk j of row `row`: kept elements times scale, the others 0 whatever they hold.
+    template <int E, typename L>
+    __device__ __forceinline__ void apply(const L &layout, float2 (&v)[E / 2], uint32_t row, int j) const {
+        if (!least) return;
+        apply<E>(layout, v, [&](int i) { return draw(row, layout.first_of(j, i)); });
+    }
+    template <int E, typename L, typename F>
+    __device__ __forceinline__ void apply(const L &layout, float2 (&v)[E / 2], F drawn) const {
+        words<E>(layout, drawn, [&](int i, const uint4 &r) {
+            v[2 * i] = keep(v[2 * i], r.x, r.y);
+            v[2 * i + 1] = keep(v[2 * i + 1], r.z, r.w);
+        });
+    }
+    // The same in two steps: a bit for each element of C chunks, and a chunk through its bits (from bit 0).
+    template <int E, int C, typename L>
+    __device__ __forceinline__ uint32_t bits(const L &layout, uint32_t row) const {
+        uint32_t kept = 0;
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+            words<E>(layout, [&](int i) { return draw(row, layout.first_of(j, i)); }, [&](int i, const uint4 &r) {
+                const int at = j * E + 4 * i;
+                kept |= (r.x >= least ? 1u << at : 0u) | (r.y >= least ? 2u << at : 0u) | (r.z >= least ? 4u << at : 0u) |
+                        (r.w >= least ? 8u << at : 0u);
+            });
+        return kept;
+    }
     template <int E>
-    __device__ __forceinline__ void apply(float2 (&v)[E / 2], uint32_t row, int at) const {
+    __device__ __forceinline__ void apply(float2 (&v)[E / 2], uint32_t kept) const {
         if (!least) return;
 #pragma unroll
-        for (int i = 0; i < E / 2; i += 2) {
-            const uint4 r = philox(make_uint4(static_cast<uint32_t>((at + 2 * i) >> 2) | site, row, step0, step1), k0, k1);
-            v[i].x = r.x >= least ? v[i].x * scale : 0.0f;
-            v[i].y = r.y >= least ? v[i].y * scale : 0.0f;
-            v[i + 1].x = r.z >= least ? v[i + 1].x * scale : 0.0f;
-            v[i + 1].y = r.w >= least ? v[i + 1].y * scale : 0.0f;
+        for (int i = 0; i < E / 2; ++i) {
+            v[i] = __fmul2_rn(v[i], make_float2(scale, scale));
+            v[i] = make_float2(kept >> (2 * i) & 1u ? v[i].x : 0.0f, kept >> (2 * i + 1) & 1u ? v[i].y : 0.0f);
         }
     }
 };
@@ -319,12 +463,14 @@ struct Team {
                     for (int i = 0; i < N; ++i) scratch[(lane >> 5) * N + i] = v[i];
                 }
                 named_barrier_sync(1 + id, lanes);
+                if (warps == 2) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) v[i] = scratch[i];
-#pragma unroll 1
-                for (int w = 1; w < warps; ++w) {
+                    for (int i = 0; i < N; ++i) v[i] = scratch[i] + scratch[N + i];
+                } else {   // a warp's sums a lane
+                    const int w = threadIdx.x & 31;
 #pragma unroll
-                    for (int i = 0; i < N; ++i) v[i] += scratch[w * N + i];
+                    for (int i = 0; i < N; ++i) v[i] = w < warps ? scratch[w * N + i] : 0.0f;
+                    warp_sum(v);
                 }
             }
         }
