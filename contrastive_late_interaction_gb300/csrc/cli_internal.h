@@ -276,7 +276,7 @@ struct MaskLaunch {
 struct NormLaunch {
     int dtype, stream_dtype, backward, join;
     long long rows;
-    int width, lanes;   // lanes: of a team
+    int width, lanes, stages;   // lanes: of a team; stages: of its threads' copies
     int moves;          // how chunks of 4 can be moved (rows.cuh)
     float inv_width, epsilon;
     const void *in, *branch, *d_out, *d_sum;

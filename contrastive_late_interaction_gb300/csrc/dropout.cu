@@ -16,23 +16,24 @@ namespace cli {
 namespace rows {
 namespace {
 
-constexpr int kUnroll = 4;
 
-// The rounds' keys in registers: 18 additions a row less.  They come by way of shared memory, or the compiler would add
-// them up again in each row.
+// The rounds' keys in registers.  They come by way of shared memory, or the compiler would add them up again in each row:
+// 233 us where these take 195 (131072 x 2048 in bf16, with the blocks' first rounds in registers too).
 struct HeldKeys {
-    uint32_t k[20];
-    __device__ __forceinline__ uint32_t a(int i) const { return k[i]; }
-    __device__ __forceinline__ uint32_t b(int i) const { return k[10 + i]; }
-    __device__ __forceinline__ explicit HeldKeys(const Mask &mask) {
-        __shared__ uint32_t keys[20];
+    uint32_t a3, k[12];
+    __device__ __forceinline__ uint4 two(int i) const { return make_uint4(k[2 * i - 8], k[2 * i - 7], k[2 * i - 6], k[2 * i - 5]); }
+    __device__ __forceinline__ explicit HeldKeys(const Seed &seed) {
+        __shared__ uint32_t keys[13];
         const int i = threadIdx.x;
-        if (i < 20) keys[i] = i < 10 ? mask.k0 + i * kWeyl0 : mask.k1 + (i - 10) * kWeyl1;
+        if (i < 13) keys[i] = i == 12 ? seed.a(3) : i & 1 ? seed.b(4 + i / 2) : seed.a(4 + i / 2);
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 20; ++j) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(k[j]) : "r"(smem_u32(keys + j)));
+        for (int j = 0; j < 12; ++j) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(k[j]) : "r"(smem_u32(keys + j)));
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a3) : "r"(smem_u32(keys + 12)));
     }
 };
+
+template <int MOVES> constexpr int kUnroll = MOVES == kWhole ? 4 : 3;   // 4 for pieces: 33 us where 3 take 29 (30011 rows of 517)
 
 // Lanes whose chunks make a span: whole chunks stand for themselves; pieces of 16 lanes are 32 bytes at least.
 template <int MOVES> constexpr int kPart = MOVES == kWhole ? 1 : 16;
@@ -42,38 +43,42 @@ template <typename T, int E, int MOVES>
 __global__ void __launch_bounds__(512) dropout_kernel(const __grid_constant__ DropoutLaunch P, int spans, int height) {
     constexpr int part = kPart<MOVES>;
     using L = Layout<T, E, MOVES, part>;
-    const Mask mask(P.mask);
+    const Seed seed(P.mask);
     const int group = threadIdx.x / part, span = blockIdx.y * spans + group % spans, down = group / spans;
     const L layout(part, threadIdx.x - group * part, span * part * E);
     const uint32_t rows = static_cast<uint32_t>(P.rows), stride = gridDim.x * height;
     const uint32_t there = down < height ? layout.template there<1>(P.width) : 0u;
-    const HeldKeys keys(mask);
-    const Block blocks[2] = {{keys, mask.block_of(layout.first_of(0, 0)), mask.step0, mask.step1},
-                             {keys, mask.block_of(layout.first_of(0, E == 8 ? 1 : 0)), mask.step0, mask.step1}};
-    const uint32_t row_word = product(kMul1, mask.step0).y ^ keys.a(0);
+    const HeldKeys keys(seed);
+    Block blocks[E / 4];
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) blocks[i] = Block(seed, P.mask.site, layout.first_of(0, i));
+    const uint32_t row_word = seed.row_word();
     const T *in = static_cast<const T *>(P.in) + layout.column;
     T *out = static_cast<T *>(P.out) + layout.column;
-    Chunk<T, E> next[kUnroll];
+    Chunk<T, E> next[kUnroll<MOVES>];
     auto load = [&](uint32_t row) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u, row += stride)
+        for (int u = 0; u < kUnroll<MOVES>; ++u, row += stride)
             layout.load(next[u], in + row * P.in_row, row < rows ? there : 0u);
     };
     uint32_t base = blockIdx.x * height;   // of the block
     load(base + down);
-    for (; base < rows; base += kUnroll * stride) {
+    for (; base < rows; base += kUnroll<MOVES> * stride) {
         uint32_t row = base + down;
-        Chunk<T, E> now[kUnroll];
+        Chunk<T, E> now[kUnroll<MOVES>];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) now[u] = next[u];
-        load(row + kUnroll * stride);
+        for (int u = 0; u < kUnroll<MOVES>; ++u) now[u] = next[u];
+        load(row + kUnroll<MOVES> * stride);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u, row += stride) {
+        for (int u = 0; u < kUnroll<MOVES>; ++u, row += stride) {
             float2 v[E / 2];
             now[u].floats(v);
-            if (mask.least) {
-                const uint2 p = product(kMul0, row ^ row_word);
-                mask.apply<E>(layout, v, [&](int i) { return blocks[i].words(keys, p); });
+            if (P.mask.least) {
+                uint4 r[E / 4];
+                draw(blocks, keys, product(kMul0, row ^ row_word), r);
+#pragma unroll
+                for (int i = 0; i < E / 4; ++i) hand_round(layout, r[i]);
+                keep<E>(v, r, P.mask.least, P.mask.scale);
             }
             now[u].set(v);
             layout.store(now[u], out + row * P.out_row, row < rows ? there : 0u);

@@ -48,33 +48,109 @@ __device__ __forceinline__ void deviations(float2 (&v)[E / 2], float m, uint32_t
         v[i / 2] = __fadd2_rn(v[i / 2], make_float2(there >> (i / L::kPiece) & 1u ? -m : 0.0f, there >> ((i + 1) / L::kPiece) & 1u ? -m : 0.0f));
 }
 
-// Stages of a thread's places, `bytes` a step: up to 400 bytes in all, so that 512 threads' fit an SM.
-constexpr int stages_of(int bytes) { return bytes > 200 ? 1 : bytes >= 100 ? 400 / bytes : 4; }
-static_assert(stages_of(64) == 4 && stages_of(128) == 3 && stages_of(192) == 2 && stages_of(384) == 1, "");
-
-template <typename T, typename S, int E, int NE, int R, bool BRANCH>
-struct Forward {
-    static constexpr int kChunks = NE / E * R, kBytes = NE * R * static_cast<int>(sizeof(S) + (BRANCH ? sizeof(T) : 0));
-    static constexpr int kStages = stages_of(kBytes);
+// What a team's lanes need of the mask and the gain in every row, in shared memory: as many registers would displace the
+// row.  A lane's blocks and gains lie beside the other lanes', the block's teams share them.
+//   keys    3 x 16 bytes: a and b of rounds 4 to 9
+//   blocks  [NE / 4][lanes of a team] x 16 bytes, with BLOCKS; else they are worked out again in each row
+//   gains   [NE / 4][lanes of a team] x 16 bytes, with GAIN
+template <int E, int NE, bool BLOCKS, bool GAIN>
+struct Table {
+    uint32_t at, blocks, gains, step, row_word, a3;   // step: from a lane's 16 bytes to its next
+    Seed seed;
+    static __host__ __device__ uint32_t bytes(int lanes) { return 48 + ((BLOCKS ? 1u : 0u) + (GAIN ? 1u : 0u)) * (NE / 4) * lanes * 16; }
+    Table() = default;
+    template <typename L>
+    __device__ __forceinline__ Table(uint32_t base, const NormLaunch &P, const Team &team, const L &layout)
+        : at(base), blocks(base + 48 + team.lane * 16), gains(blocks + (BLOCKS ? NE / 4 : 0) * team.lanes * 16),
+          step(team.lanes * 16), seed(P.mask) {
+        row_word = seed.row_word(), a3 = seed.a(3);
+        if (P.mask.least && threadIdx.x < 3) {
+            const int i = 4 + 2 * threadIdx.x;
+            st_shared_v4(at + threadIdx.x * 16, seed.a(i), seed.b(i), seed.a(i + 1), seed.b(i + 1));
+        }
+        if (team.id == 0) {
+#pragma unroll
+            for (int j = 0; j < NE / E; ++j) {
+                float2 gain[E / 2];
+                if (GAIN) layout.vector(P.gain, j, P.width, 1.0f, gain);
+#pragma unroll
+                for (int i = 0; i < E / 4; ++i) {
+                    const uint32_t to = (j * (E / 4) + i) * step;
+                    if (BLOCKS && P.mask.least) {
+                        const Block b(seed, P.mask.site, layout.first_of(j, i));
+                        st_shared_v4(blocks + to, b.d, b.f, b.g, b.h);
+                    }
+                    if (GAIN)
+                        st_shared_v4(gains + to, __float_as_uint(gain[2 * i].x), __float_as_uint(gain[2 * i].y),
+                                     __float_as_uint(gain[2 * i + 1].x), __float_as_uint(gain[2 * i + 1].y));
+                }
+            }
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ uint4 two(int i) const { return shared16(at + (i - 4) * 8); }
+    __device__ __forceinline__ void gain(int j, float2 (&v)[E / 2]) const {
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+            const uint4 u = shared16(gains + (j * (E / 4) + i) * step);
+            v[2 * i] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+            v[2 * i + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+        }
+    }
+    // Chunk j of a row through the mask.
+    template <typename L>
+    __device__ __forceinline__ void mask(const L &layout, const MaskLaunch &m, float2 (&v)[E / 2], uint32_t row, int j) const {
+        if (!m.least) return;
+        Block b[E / 4];
+        uint4 r[E / 4];
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+            if constexpr (BLOCKS) {
+                const uint4 u = shared16(blocks + (j * (E / 4) + i) * step);
+                b[i].d = u.x, b[i].f = u.y, b[i].g = u.z, b[i].h = u.w;
+            } else {
+                b[i] = Block(seed, m.site, layout.first_of(j, i));
+            }
+        }
+        draw(b, *this, product(kMul0, row ^ row_word), r);
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) hand_round(layout, r[i]);
+        keep<E>(v, r, m.least, m.scale);
+    }
 };
+
+// Waits until all but the last `ahead` of the thread's groups of copies are there.
+__device__ __forceinline__ void wait_copies(int ahead) {
+    switch (ahead) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    }
+}
 
 // T: type of the branch and the output.  S: the stream's.  E: elements of a
 // chunk; NE: of a row that a thread has; R: rows that a team takes at a time.
 // BRANCH: a branch joins.
 template <typename T, typename S, int E, int NE, int R, bool BRANCH, int MOVES>
 __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant__ NormLaunch P) {
-    using F = Forward<T, S, E, NE, R, BRANCH>;
-    constexpr int C = NE / E, kStages = F::kStages;
+    constexpr int C = NE / E;
+    const int stages = P.stages;
     constexpr bool kHold = NE <= 16;   // the gain and the bias stay in registers
     extern __shared__ __align__(16) float scratch[];   // teams of several warps: R * 48 floats each; then the feeds
     const Team team(P.lanes);
     float *sums = scratch + team.id * R * 48;
-    const uint32_t places = smem_u32(scratch) + (team.lanes > 32 ? team.in_block * R * 192 : 0);
-    Feed<S, E, C * R, MOVES> in(places, kStages);
-    Feed<T, E, C * R, MOVES> branch(places + (BRANCH ? kStages * C * R * E * static_cast<int>(sizeof(S)) * blockDim.x : 0), BRANCH ? kStages : 0);
-    const Mask mask(P.mask);
+    uint32_t places = smem_u32(scratch) + (team.lanes > 32 ? team.in_block * R * 192 : 0);
     using L = RowLayout<T, E, NE, MOVES>;
+    using Tab = Table<E, NE, true, false>;
     const L layout = layout_of<L, NE>(team);
+    const Tab table = [&] {
+        if constexpr (BRANCH) return Tab(places, P, team, layout);
+        else return Tab();
+    }();
+    if (BRANCH) places += Tab::bytes(team.lanes);
+    Feed<S, E, C * R, MOVES> in(places, stages);
+    Feed<T, E, C * R, MOVES> branch(places + stages * NE * R * static_cast<int>(sizeof(S)) * blockDim.x, BRANCH ? stages : 0);
     const uint32_t there = layout.template there<C>(P.width);
     float2 gain[kHold ? C : 1][E / 2], bias[kHold ? C : 1][E / 2];
 #pragma unroll
@@ -105,20 +181,19 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
         if constexpr (BRANCH) branch.settle(stage);
     };
     constexpr bool kHeld = MOVES == kHalves && (BRANCH || sizeof(S) == 2);
-    constexpr int kAhead = kHeld && kStages > 1 ? 1 : kStages - 1;   // steps
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
+    const int ahead = kHeld && stages > 1 ? 1 : stages - 1;   // steps
+    for (int k = 0; k < ahead; ++k) {
         copy(k * stride, k);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    if constexpr (kHeld && kAhead) settle(0);
+    if (kHeld && ahead) settle(0);
     int stage = 0;
     for (uint32_t base = 0; base + first < rows; base += stride) {
-        const int next = stage + kAhead >= kStages ? stage + kAhead - kStages : stage + kAhead;
-        copy(base + kAhead * stride, next);   // what was there was used up a step ago
+        const int next = stage + ahead >= stages ? stage + ahead - stages : stage + ahead;
+        copy(base + ahead * stride, next);   // what was there was used up a step ago
         asm volatile("cp.async.commit_group;" ::: "memory");
-        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
-        if constexpr (kHeld && !kAhead) settle(stage);
+        wait_copies(ahead);
+        if (kHeld && !ahead) settle(stage);
         float2 v[R][C][E / 2];
         float s[R], s2[2 * R];
 #pragma unroll
@@ -133,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
                 if constexpr (BRANCH) {
                     float2 f[E / 2];
                     branch.floats(stage, r * C + j, f);
-                    mask.apply<E>(layout, f, row, j);
+                    table.mask(layout, P.mask, f, row, j);
 #pragma unroll
                     for (int i = 0; i < E / 2; ++i) v[r][j][i] = __fadd2_rn(v[r][j][i], f[i]);
                     if (P.sum) {
@@ -186,40 +261,49 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
                 layout.store(c, static_cast<T *>(P.out) + row * P.out_row + layout.column + layout.chunk(j), row < rows ? there >> (j * L::kPieces) : 0u);
             }
         }
-        if constexpr (kHeld && kAhead) settle(next);
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+        if (kHeld && ahead) settle(next);
+        stage = stage + 1 == stages ? 0 : stage + 1;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <typename T, typename S, int NE, bool BRANCH>
-struct Backward {
-    static constexpr int kBytes = NE * static_cast<int>(sizeof(S) * (BRANCH ? 2 : 1) + sizeof(T));
-    static constexpr int kStages = stages_of(kBytes);
-};
+// Where a backward call's gains are: in registers, or read again in each row from shared memory, or (where that is full of
+// stages) from global memory.
+enum Gains { kHeldGain, kSharedGain, kGlobalGain };
+template <typename S, int NE, bool BRANCH>
+constexpr Gains kGains = NE > 8 && sizeof(S) == 2 && (BRANCH || NE > 16) ? kSharedGain : NE <= 16 ? kHeldGain : kGlobalGain;
+
+// Where the blocks are kept for the mask: not beside the widest rows of fp32, which leave no room.
+template <typename T, int NE, bool BRANCH> constexpr bool kBlocks = BRANCH && !(NE == 32 && sizeof(T) == 4);
 
 template <typename T, typename S, int E, int NE, bool BRANCH, int MOVES>
 __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ NormLaunch P) {
-    using B = Backward<T, S, NE, BRANCH>;
-    constexpr int C = NE / E, kStages = B::kStages;
-    constexpr bool kHold = NE <= 16;   // the gain and the row's deviations stay in registers
+    constexpr int C = NE / E;
+    constexpr bool kHold = NE <= 16;   // the row's deviations stay in registers
+    constexpr Gains kGain = kGains<S, NE, BRANCH>;
+    const int stages = P.stages;
     extern __shared__ __align__(16) float scratch[];   // teams of several warps: 80 floats each; then the feeds.  At the end, the block's sums
     const Team team(P.lanes);
     float *sums = scratch + team.id * 80;
     uint32_t places = smem_u32(scratch) + (team.lanes > 32 ? team.in_block * 320 : 0);
-    Feed<S, E, C, MOVES> in(places, kStages);
-    places += kStages * NE * static_cast<int>(sizeof(S)) * blockDim.x;
-    Feed<T, E, C, MOVES> d_out(places, kStages);
-    places += kStages * NE * static_cast<int>(sizeof(T)) * blockDim.x;
-    Feed<S, E, C, MOVES> d_sum(places, BRANCH ? kStages : 0);
-    const Mask mask(P.mask);
     using L = RowLayout<T, E, NE, MOVES>;
+    using Tab = Table<E, NE, kBlocks<T, NE, BRANCH>, kGain == kSharedGain>;
     const L layout = layout_of<L, NE>(team);
+    const Tab table = [&] {
+        if constexpr (BRANCH || kGain == kSharedGain) return Tab(places, P, team, layout);
+        else return Tab();
+    }();
+    if (BRANCH || kGain == kSharedGain) places += Tab::bytes(team.lanes);
+    Feed<S, E, C, MOVES> in(places, stages);
+    places += stages * NE * static_cast<int>(sizeof(S)) * blockDim.x;
+    Feed<T, E, C, MOVES> d_out(places, stages);
+    places += stages * NE * static_cast<int>(sizeof(T)) * blockDim.x;
+    Feed<S, E, C, MOVES> d_sum(places, BRANCH ? stages : 0);
     const uint32_t there = layout.template there<C>(P.width);
-    float2 gain[kHold ? C : 1][E / 2], d_gain[C][E / 2], d_bias[C][E / 2];
+    float2 gain[kGain == kHeldGain ? C : 1][E / 2], d_gain[C][E / 2], d_bias[C][E / 2];
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-        if constexpr (kHold) layout.vector(P.gain, j, P.width, 1.0f, gain[j]);
+        if constexpr (kGain == kHeldGain) layout.vector(P.gain, j, P.width, 1.0f, gain[j]);
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) d_gain[j][i] = d_bias[j][i] = both(0.0f);
     }
@@ -245,20 +329,19 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
         if constexpr (BRANCH) d_sum.settle(stage);
     };
     constexpr bool kHeld = MOVES == kHalves;
-    constexpr int kAhead = kHeld && kStages > 1 ? 1 : kStages - 1;   // steps
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
+    const int ahead = kHeld && stages > 1 ? 1 : stages - 1;   // steps
+    for (int k = 0; k < ahead; ++k) {
         copy(k * stride, k);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    if constexpr (kHeld && kAhead) settle(0);
+    if (kHeld && ahead) settle(0);
     int stage = 0;
     for (uint32_t base = 0; base + first < rows; base += stride) {
-        const int next = stage + kAhead >= kStages ? stage + kAhead - kStages : stage + kAhead;
-        copy(base + kAhead * stride, next);   // what was there was used up a step ago
+        const int next = stage + ahead >= stages ? stage + ahead - stages : stage + ahead;
+        copy(base + ahead * stride, next);   // what was there was used up a step ago
         asm volatile("cp.async.commit_group;" ::: "memory");
-        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
-        if constexpr (kHeld && !kAhead) settle(stage);
+        wait_copies(ahead);
+        if (kHeld && !ahead) settle(stage);
         const uint32_t row = base + mine;
         const bool on = row < rows;
         float2 d[kHold ? C : 1][E / 2];
@@ -282,7 +365,12 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
             if constexpr (!kHold) in.floats(stage, j, d[0]);
             deviations<E, L>(d[kHold ? j : 0], m, there >> (j * L::kPieces));
             dy[kHold ? j : 0] = d_out.chunk(stage, j);
-            if constexpr (!kHold) layout.vector(P.gain, j, P.width, 1.0f, gain[0]);
+        };
+        auto gain_of = [&](int j) -> const float2 (&)[E / 2] {
+            if constexpr (kGain == kHeldGain) return gain[j];
+            if constexpr (kGain == kSharedGain) table.gain(j, gain[0]);
+            if constexpr (kGain == kGlobalGain) layout.vector(P.gain, j, P.width, 1.0f, gain[0]);
+            return gain[0];
         };
         {
             float2 sum = both(0.0f), squares = sum, sum_t = sum, sum_td = sum;
@@ -292,9 +380,10 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
                 const int k = kHold ? j : 0;
                 float2 g[E / 2];
                 dy[k].floats(g);
+                const float2 (&w)[E / 2] = gain_of(j);
 #pragma unroll
                 for (int i = 0; i < E / 2; ++i) {
-                    const float2 t = __fmul2_rn(g[i], gain[k][i]);
+                    const float2 t = __fmul2_rn(g[i], w[i]);
                     sum = __fadd2_rn(sum, d[k][i]);
                     squares = __ffma2_rn(d[k][i], d[k][i], squares);
                     sum_t = __fadd2_rn(sum_t, t);
@@ -318,6 +407,7 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
                 const uint32_t pieces = on ? there >> (j * L::kPieces) : 0u;
                 float2 v[E / 2], g[E / 2];
                 dy[k].floats(g);
+                const float2 (&w)[E / 2] = gain_of(j);
 #pragma unroll
                 for (int i = 0; i < E / 2; ++i) {
                     const float2 norm = __ffma2_rn(d[k][i], scale, shift);
@@ -325,7 +415,7 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
                         d_gain[j][i] = __ffma2_rn(g[i], norm, d_gain[j][i]);
                         d_bias[j][i] = __fadd2_rn(d_bias[j][i], g[i]);
                     }
-                    v[i] = __ffma2_rn(__fmul2_rn(g[i], gain[k][i]), scale, __ffma2_rn(norm, less_n, less));
+                    v[i] = __ffma2_rn(__fmul2_rn(g[i], w[i]), scale, __ffma2_rn(norm, less_n, less));
                 }
                 if constexpr (BRANCH) {
                     d_sum.floats(stage, j, g);
@@ -337,7 +427,7 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
                 layout.store(c, to + layout.chunk(j), pieces);
                 if constexpr (BRANCH) {
                     if (P.d_branch && (L::kPiece != E || pieces)) {   // warps whose lanes have none are spared the mask
-                        mask.apply<E>(layout, v, row, j);
+                        table.mask(layout, P.mask, v, row, j);
                         Chunk<T, E> b;
                         b.set(v);
                         layout.store(b, to_x + layout.chunk(j), pieces);
@@ -345,8 +435,8 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
                 }
             }
         }
-        if constexpr (kHeld && kAhead) settle(next);
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+        if (kHeld && ahead) settle(next);
+        stage = stage + 1 == stages ? 0 : stage + 1;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!P.partials) return;
@@ -409,11 +499,22 @@ inline int lanes_of(int width, int each) {   // of a team whose lanes have `each
     return lanes;
 }
 
-// Blocks of `threads` with `smem` bytes each that an SM of 227 KB holds, given 128 registers a thread.
-inline int resident(int threads, size_t smem) {
-    const int by_threads = 512 / threads, by_smem = static_cast<int>(226 * 1024 / (smem + 1024));
-    return by_threads < by_smem ? by_threads : by_smem < 1 ? 1 : by_smem;
-}
+// A launch's shape: `fixed` bytes of shared memory a block, and `stage` for each stage of its threads' places.  As many
+// stages, up to 4, as leave an SM its 512 threads of 128 registers; two at least, if one block has room for them.
+struct Shape {
+    int stages, resident;   // resident: blocks an SM holds
+    size_t smem;
+    Shape(int threads, size_t fixed, size_t stage) {
+        constexpr size_t kRoom = 227 * 1024, kBlock = 1024;   // of an SM; of which each block takes some
+        const int most = 512 / threads;
+        stages = 4;
+        while (stages > 2 && most * (fixed + stages * stage + kBlock) > kRoom + kBlock) --stages;
+        if (fixed + stages * stage > kRoom) stages = 1;
+        smem = fixed + stages * stage;
+        const int fit = static_cast<int>((kRoom + kBlock) / (smem + kBlock));
+        resident = fit < most ? fit : most;
+    }
+};
 
 template <typename K>
 cudaError_t allow(K kernel, size_t smem) {   // more shared memory than a kernel has without asking
@@ -422,16 +523,17 @@ cudaError_t allow(K kernel, size_t smem) {   // more shared memory than a kernel
 
 template <typename T, typename S, int E, int NE, int R, bool BRANCH, int MOVES>
 cudaError_t forward(NormLaunch L, cudaStream_t stream) {
-    using F = Forward<T, S, E, NE, R, BRANCH>;
     L.lanes = lanes_of(L.width, NE);
     const int threads = L.lanes > 256 ? L.lanes : 256 / L.lanes * L.lanes, teams = threads / L.lanes;
-    const size_t smem = (L.lanes > 32 ? teams * R * 192 : 0) + static_cast<size_t>(F::kStages) * F::kBytes * threads;
+    const Shape shape(threads, (L.lanes > 32 ? teams * R * 192 : 0) + (BRANCH ? Table<E, NE, true, false>::bytes(L.lanes) : 0),
+                      NE * R * (sizeof(S) + (BRANCH ? sizeof(T) : 0)) * threads);
+    L.stages = shape.stages;
     const long long want = (L.rows + static_cast<long long>(teams) * R - 1) / (static_cast<long long>(teams) * R);
-    const long long most = static_cast<long long>(resident(threads, smem)) * L.sm_count;
+    const long long most = static_cast<long long>(shape.resident) * L.sm_count;
     auto kernel = forward_kernel<T, S, E, NE, R, BRANCH, MOVES>;
-    const cudaError_t e = allow(kernel, smem);
+    const cudaError_t e = allow(kernel, shape.smem);
     if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(want < most ? want : most), threads, smem, stream>>>(L);
+    kernel<<<static_cast<unsigned>(want < most ? want : most), threads, shape.smem, stream>>>(L);
     return cudaGetLastError();
 }
 
@@ -440,14 +542,15 @@ constexpr int kFewRows = 4;
 
 template <typename T, typename S, int E, int NE, bool BRANCH, int MOVES>
 cudaError_t backward(NormLaunch L, cudaStream_t stream) {
-    using B = Backward<T, S, NE, BRANCH>;
+    constexpr bool kShared = kGains<S, NE, BRANCH> == kSharedGain;
     L.lanes = lanes_of(L.width, NE);
     const int threads = L.lanes > 256 ? L.lanes : 256 / L.lanes * L.lanes, teams = threads / L.lanes;
-    size_t smem = (L.lanes > 32 ? teams * 320 : 0) + static_cast<size_t>(B::kStages) * B::kBytes * threads;
-    const size_t sums = static_cast<size_t>(threads) * NE * sizeof(float);
-    if (smem < sums) smem = sums;
+    const Shape shape(threads, (L.lanes > 32 ? teams * 320 : 0) + (BRANCH || kShared ? Table<E, NE, kBlocks<T, NE, BRANCH>, kShared>::bytes(L.lanes) : 0),
+                      NE * (sizeof(S) * (BRANCH ? 2 : 1) + sizeof(T)) * threads);
+    L.stages = shape.stages;
+    const size_t sums = static_cast<size_t>(threads) * NE * sizeof(float), smem = shape.smem > sums ? shape.smem : sums;
     long long blocks = (L.rows + teams - 1) / teams;
-    const long long most = static_cast<long long>(resident(threads, smem)) * L.sm_count;
+    const long long most = static_cast<long long>(shape.resident) * L.sm_count;
     blocks = blocks < 1 ? 1 : blocks < most ? blocks : most;
     if (L.partials && L.rows <= kFewRows * teams) blocks = 1;
     auto kernel = backward_kernel<T, S, E, NE, BRANCH, MOVES>;

@@ -275,127 +275,96 @@ __device__ __forceinline__ uint2 product(uint32_t a, uint32_t b) {   // x: the l
     return make_uint2(static_cast<uint32_t>(p), static_cast<uint32_t>(p >> 32));
 }
 
-// The rounds' keys, added up where they are used.
-struct Keys {
-    uint32_t k0, k1;
-    __device__ __forceinline__ uint32_t a(int i) const { return k0 + i * kWeyl0; }
+// A call's mask as its kernels start: its seed and step are read from the device, so that a captured call draws another
+// mask at each step.
+struct Seed {
+    uint32_t k0, k1, step0, step1;
+    Seed() = default;
+    __device__ __forceinline__ explicit Seed(const MaskLaunch &m) : k0(0), k1(0), step0(0), step1(0) {
+        if (!m.least) return;
+        const uint2 key = *reinterpret_cast<const uint2 *>(m.seed), step = *reinterpret_cast<const uint2 *>(m.seed + 1);
+        k0 = key.x, k1 = key.y, step0 = step.x, step1 = step.y;
+    }
+    __device__ __forceinline__ uint32_t a(int i) const { return k0 + i * kWeyl0; }   // the rounds' keys
     __device__ __forceinline__ uint32_t b(int i) const { return k1 + i * kWeyl1; }
+    // What the first round makes of the row, but for the row itself.
+    __device__ __forceinline__ uint32_t row_word() const { return product(kMul1, step0).y ^ a(0); }
 };
 
-// What a counter's column and step come to in the first rounds, before the row has reached every word (counter: column
+// What the first rounds make of a block's columns and of the step before the row has reached every word (counter: column
 // block, row, step, step).  A multiplication of 32 x 32 to 64 bits goes out every fourth cycle, so that these decide what
-// a mask costs: 15 of 20 are left to a row, and one that a row's blocks share.
+// a mask costs: of 20 a block, 15 are left to each row, and one that the row's blocks share.
 struct Block {
     uint32_t d, f, g, h;
-    template <typename K>
-    __device__ __forceinline__ Block(const K &k, uint32_t column, uint32_t step0, uint32_t step1) {
-        const uint2 p0 = product(kMul0, column), q0 = product(kMul1, step0);
-        const uint2 q1 = product(kMul1, p0.y ^ step1 ^ k.b(0));
-        const uint2 p2 = product(kMul0, q1.y ^ q0.x ^ k.a(1));
-        d = p0.x ^ k.b(1), f = q1.x ^ k.a(2), g = p2.y ^ k.b(2), h = p2.x ^ k.b(3);
-    }
-    // `p1`: the product of the row's word, the same for every block of a row.
-    template <typename K>
-    __device__ __forceinline__ uint4 words(const K &k, uint2 p1) const {
-        uint2 q = product(kMul1, p1.y ^ d);
-        uint4 c;
-        c.x = q.y ^ f, c.y = q.x, c.z = g ^ p1.x;
-        uint2 p = product(kMul0, c.x);
-        q = product(kMul1, c.z);
-        c = make_uint4(q.y ^ c.y ^ k.a(3), q.x, p.y ^ h, p.x);
-#pragma unroll
-        for (int i = 4; i < 10; ++i) {
-            p = product(kMul0, c.x), q = product(kMul1, c.z);
-            c = make_uint4(q.y ^ c.y ^ k.a(i), q.x, p.y ^ c.w ^ k.b(i), p.x);
-        }
-        return c;
+    Block() = default;
+    __device__ __forceinline__ Block(const Seed &s, uint32_t site, int column) {
+        const uint2 p0 = product(kMul0, static_cast<uint32_t>(column >> 2) | site << 16), q0 = product(kMul1, s.step0);
+        const uint2 q1 = product(kMul1, p0.y ^ s.step1 ^ s.b(0));
+        const uint2 p2 = product(kMul0, q1.y ^ q0.x ^ s.a(1));
+        d = p0.x ^ s.b(1), f = q1.x ^ s.a(2), g = p2.y ^ s.b(2), h = p2.x ^ s.b(3);
     }
 };
 
-// A call's mask, its seed and step read from the device: a captured call draws another mask at each step.
-struct Mask {
-    uint32_t k0, k1, step0, step1, site, least;
-    float scale;
-    __device__ __forceinline__ explicit Mask(const MaskLaunch &m)
-        : k0(0), k1(0), step0(0), step1(0), site(m.site << 16), least(m.least), scale(m.scale) {
-        if (least) {
-            const uint2 key = *reinterpret_cast<const uint2 *>(m.seed), step = *reinterpret_cast<const uint2 *>(m.seed + 1);
-            k0 = key.x, k1 = key.y, step0 = step.x, step1 = step.y;
+// The words of N blocks of a row, round by round together.  `row`: the row's word, multiplied.  K gives the keys: a3 of
+// round 3, and two(i) the a and b of rounds i and i + 1.
+template <int N, typename K>
+__device__ __forceinline__ void draw(const Block (&b)[N], const K &keys, uint2 row, uint4 (&c)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        uint2 q = product(kMul1, row.y ^ b[n].d);
+        const uint32_t x = q.y ^ b[n].f, y = q.x, z = b[n].g ^ row.x;
+        const uint2 p = product(kMul0, x);
+        q = product(kMul1, z);
+        c[n] = make_uint4(q.y ^ y ^ keys.a3, q.x, p.y ^ b[n].h, p.x);
+    }
+#pragma unroll
+    for (int i = 4; i < 10; i += 2) {
+        const uint4 k = keys.two(i);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            uint2 p = product(kMul0, c[n].x), q = product(kMul1, c[n].z);
+            c[n] = make_uint4(q.y ^ c[n].y ^ k.x, q.x, p.y ^ c[n].w ^ k.y, p.x);
+            p = product(kMul0, c[n].x), q = product(kMul1, c[n].z);
+            c[n] = make_uint4(q.y ^ c[n].y ^ k.z, q.x, p.y ^ c[n].w ^ k.w, p.x);
         }
     }
-    __device__ __forceinline__ uint32_t block_of(int column) const { return static_cast<uint32_t>(column >> 2) | site; }
-    // The row's word after the first round, times what the second takes it.
-    __device__ __forceinline__ uint2 row_product(uint32_t row) const { return product(kMul0, product(kMul1, step0).y ^ row ^ k0); }
-    __device__ __forceinline__ uint4 draw(uint32_t row, int column) const {
-        // row >> 31 is 0, but as far as the compiler knows the keys are another row's each time: kept from row to row, the
-        // 18 sums would take the registers that the row's sums need (164 bytes of spills in the join's gradient)
-        const Keys k{k0 ^ row >> 31, k1 ^ row >> 31};
-        return Block(k, block_of(column), step0, step1).words(k, row_product(row));
-    }
-    __device__ __forceinline__ float2 keep(float2 v, uint32_t a, uint32_t b) const {
-        v = __fmul2_rn(v, make_float2(scale, scale));
-        return make_float2(a >= least ? v.x : 0.0f, b >= least ? v.y : 0.0f);
-    }
-    // The words of a chunk's elements, four at a time, from the blocks that `drawn` gives (the i-th of the chunk's).  Where a
-    // block's four columns lie with several lanes, each of these draws another of their blocks, and they hand the words
-    // round: the lanes of such a group have to call this together.
-    template <int E, typename L, typename F, typename U>
-    __device__ __forceinline__ void words(const L &layout, F drawn, U use) const {
-#pragma unroll
-        for (int i = 0; i < E / 4; ++i) {
-            uint4 r = drawn(i);
-            if constexpr (L::kPiece != E) {
-                const int mine = layout.drawer();
-                auto swap = [](uint32_t x, int o) { return __shfl_xor_sync(0xffffffffu, x, o); };
-                if constexpr (L::kPieces == 4) {   // r: words x, y, z, w of block `mine`; then word `mine` of blocks 0 to 3
-                    uint32_t t = swap(mine & 1 ? r.x : r.y, 1), u = swap(mine & 1 ? r.z : r.w, 1);
-                    if (mine & 1) r.x = t, r.z = u; else r.y = t, r.w = u;
-                    t = swap(mine & 2 ? r.x : r.z, 2), u = swap(mine & 2 ? r.y : r.w, 2);
-                    if (mine & 2) r.x = t, r.y = u; else r.z = t, r.w = u;
-                } else {   // then words 2 mine and 2 mine + 1 of blocks 0 and 1
-                    const uint32_t t = swap(mine ? r.x : r.z, 1), u = swap(mine ? r.y : r.w, 1);
-                    if (mine) r.x = t, r.y = u; else r.z = t, r.w = u;
-                }
-            }
-            use(i, r);
+}
+
+// The words of a lane's elements from the blocks that it drew.  Where a block's four columns lie with several lanes, each
+// of these draws another of their blocks, and they hand the words round: the lanes of such a group call this together.
+template <typename L>
+__device__ __forceinline__ void hand_round(const L &layout, uint4 &r) {
+    if constexpr (L::kPieces > 1) {
+        const int mine = layout.drawer();
+        auto swap = [](uint32_t x, int o) { return __shfl_xor_sync(0xffffffffu, x, o); };
+        if constexpr (L::kPieces == 4) {   // r: words x, y, z, w of block `mine`; then word `mine` of blocks 0 to 3
+            uint32_t t = swap(mine & 1 ? r.x : r.y, 1), u = swap(mine & 1 ? r.z : r.w, 1);
+            if (mine & 1) r.x = t, r.z = u; else r.y = t, r.w = u;
+            t = swap(mine & 2 ? r.x : r.z, 2), u = swap(mine & 2 ? r.y : r.w, 2);
+            if (mine & 2) r.x = t, r.y = u; else r.z = t, r.w = u;
+        } else {   // then words 2 mine and 2 mine + 1 of blocks 0 and 1
+            const uint32_t t = swap(mine ? r.x : r.z, 1), u = swap(mine ? r.y : r.w, 1);
+            if (mine) r.x = t, r.y = u; else r.z = t, r.w = u;
         }
     }
-    // Chunk j of row `row`: kept elements times scale, the others 0 whatever they hold.
-    template <int E, typename L>
-    __device__ __forceinline__ void apply(const L &layout, float2 (&v)[E / 2], uint32_t row, int j) const {
-        if (!least) return;
-        apply<E>(layout, v, [&](int i) { return draw(row, layout.first_of(j, i)); });
-    }
-    template <int E, typename L, typename F>
-    __device__ __forceinline__ void apply(const L &layout, float2 (&v)[E / 2], F drawn) const {
-        words<E>(layout, drawn, [&](int i, const uint4 &r) {
-            v[2 * i] = keep(v[2 * i], r.x, r.y);
-            v[2 * i + 1] = keep(v[2 * i + 1], r.z, r.w);
-        });
-    }
-    // The same in two steps: a bit for each element of C chunks, and a chunk through its bits (from bit 0).
-    template <int E, int C, typename L>
-    __device__ __forceinline__ uint32_t bits(const L &layout, uint32_t row) const {
-        uint32_t kept = 0;
+}
+
+// A chunk through its words: kept elements times scale, the others 0 whatever they hold.
+template <int E>
+__device__ __forceinline__ void keep(float2 (&v)[E / 2], const uint4 (&r)[E / 4], uint32_t least, float scale) {
 #pragma unroll
-        for (int j = 0; j < C; ++j)
-            words<E>(layout, [&](int i) { return draw(row, layout.first_of(j, i)); }, [&](int i, const uint4 &r) {
-                const int at = j * E + 4 * i;
-                kept |= (r.x >= least ? 1u << at : 0u) | (r.y >= least ? 2u << at : 0u) | (r.z >= least ? 4u << at : 0u) |
-                        (r.w >= least ? 8u << at : 0u);
-            });
-        return kept;
+    for (int i = 0; i < E / 4; ++i) {
+        const float2 a = __fmul2_rn(v[2 * i], make_float2(scale, scale)), b = __fmul2_rn(v[2 * i + 1], make_float2(scale, scale));
+        v[2 * i] = make_float2(r[i].x >= least ? a.x : 0.0f, r[i].y >= least ? a.y : 0.0f);
+        v[2 * i + 1] = make_float2(r[i].z >= least ? b.x : 0.0f, r[i].w >= least ? b.y : 0.0f);
     }
-    template <int E>
-    __device__ __forceinline__ void apply(float2 (&v)[E / 2], uint32_t kept) const {
-        if (!least) return;
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            v[i] = __fmul2_rn(v[i], make_float2(scale, scale));
-            v[i] = make_float2(kept >> (2 * i) & 1u ? v[i].x : 0.0f, kept >> (2 * i + 1) & 1u ? v[i].y : 0.0f);
-        }
-    }
-};
+}
+
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
 
 // ----------------------------------------------------------------------------
 // teams
