@@ -276,16 +276,22 @@ constexpr Gains kGains = NE > 8 && sizeof(S) == 2 && (BRANCH || NE > 16) ? kShar
 // Where the blocks are kept for the mask: not beside the widest rows of fp32, which leave no room.
 template <typename T, int NE, bool BRANCH> constexpr bool kBlocks = BRANCH && !(NE == 32 && sizeof(T) == 4);
 
+// Where a row's mean comes with the sums of the row before it, so that a team meets once a row (the join's gradient over
+// 131072 x 1024 in bf16: 284 -> 255 us, over 8192 x 8192 204 -> 146): with three stages, for which there is room.
+template <typename T, typename S, int NE, bool BRANCH, int MOVES>
+constexpr bool kPiped = !(MOVES == kHalves && sizeof(T) == 2) &&
+                        (NE == 8 || (NE == 16 && !(BRANCH && sizeof(S) == 4)) || (NE == 24 && !BRANCH));
+
 template <typename T, typename S, int E, int NE, bool BRANCH, int MOVES>
 __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ NormLaunch P) {
     constexpr int C = NE / E;
     constexpr bool kHold = NE <= 16;   // the row's deviations stay in registers
     constexpr Gains kGain = kGains<S, NE, BRANCH>;
     const int stages = P.stages;
-    extern __shared__ __align__(16) float scratch[];   // teams of several warps: 80 floats each; then the feeds.  At the end, the block's sums
+    extern __shared__ __align__(16) float scratch[];   // teams of several warps: 176 floats each; then the table and the feeds.  At the end, the block's sums
     const Team team(P.lanes);
-    float *sums = scratch + team.id * 80;
-    uint32_t places = smem_u32(scratch) + (team.lanes > 32 ? team.in_block * 320 : 0);
+    float *sums = scratch + team.id * 176;
+    uint32_t places = smem_u32(scratch) + (team.lanes > 32 ? team.in_block * 704 : 0);
     using L = RowLayout<T, E, NE, MOVES>;
     using Tab = Table<E, NE, kBlocks<T, NE, BRANCH>, kGain == kSharedGain>;
     const L layout = layout_of<L, NE>(team);
@@ -335,34 +341,43 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
     if (kHeld && ahead) settle(0);
-    int stage = 0;
+    auto total_of = [&](int from) {   // a thread's
+        float2 sum = both(0.0f);
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            float2 v[E / 2];
+            in.floats(from, j, v);
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) sum = __fadd2_rn(sum, v[i]);   // 0 past the row's end
+        }
+        return sum.x + sum.y;
+    };
+    auto mean_of = [&](int from) {
+        float s[1] = {total_of(from)};
+        team.sum<1, (NE > 8)>(s, sums);
+        return s[0] * P.inv_width;
+    };
+    constexpr bool kPipe = kPiped<T, S, NE, BRANCH, MOVES>;
+    int stage = 0, parity = 0;
+    float m = 0.0f;
+    if constexpr (kPipe) {
+        wait_copies(ahead - 1);
+        m = mean_of(0);
+    }
     for (uint32_t base = 0; base + first < rows; base += stride) {
         const int next = stage + ahead >= stages ? stage + ahead - stages : stage + ahead;
         copy(base + ahead * stride, next);   // what was there was used up a step ago
         asm volatile("cp.async.commit_group;" ::: "memory");
-        wait_copies(ahead);
+        wait_copies(kPipe ? ahead - 1 : ahead);
         if (kHeld && !ahead) settle(stage);
         const uint32_t row = base + mine;
         const bool on = row < rows;
         float2 d[kHold ? C : 1][E / 2];
         Chunk<T, E> dy[kHold ? C : 1];
-        float s[1], s4[4];
-        {
-            float2 sum = both(0.0f);
-#pragma unroll
-            for (int j = 0; j < C; ++j) {
-                float2 (&v)[E / 2] = d[kHold ? j : 0];
-                in.floats(stage, j, v);
-#pragma unroll
-                for (int i = 0; i < E / 2; ++i) sum = __fadd2_rn(sum, v[i]);   // 0 past the row's end
-            }
-            s[0] = sum.x + sum.y;
-        }
-        team.sum<1, (NE > 8)>(s, sums);
-        const float m = s[0] * P.inv_width;
+        if constexpr (!kPipe) m = mean_of(stage);
         // A chunk's deviations and gradient: kept with kHold, else computed again where they are used.
         auto load = [&](int j) {
-            if constexpr (!kHold) in.floats(stage, j, d[0]);
+            in.floats(stage, j, d[kHold ? j : 0]);
             deviations<E, L>(d[kHold ? j : 0], m, there >> (j * L::kPieces));
             dy[kHold ? j : 0] = d_out.chunk(stage, j);
         };
@@ -372,6 +387,7 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
             if constexpr (kGain == kGlobalGain) layout.vector(P.gain, j, P.width, 1.0f, gain[0]);
             return gain[0];
         };
+        float s[kPipe ? 5 : 4];
         {
             float2 sum = both(0.0f), squares = sum, sum_t = sum, sum_td = sum;
 #pragma unroll
@@ -390,12 +406,14 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
                     sum_td = __ffma2_rn(t, d[k][i], sum_td);
                 }
             }
-            s4[0] = sum.x + sum.y, s4[1] = squares.x + squares.y, s4[2] = sum_t.x + sum_t.y, s4[3] = sum_td.x + sum_td.y;
+            s[0] = sum.x + sum.y, s[1] = squares.x + squares.y, s[2] = sum_t.x + sum_t.y, s[3] = sum_td.x + sum_td.y;
         }
-        team.sum<4, (NE > 8)>(s4, sums + 16);
+        if constexpr (kPipe) s[4] = total_of(stage + 1 == stages ? 0 : stage + 1);
+        team.sum<kPipe ? 5 : 4, (NE > 8)>(s, sums + 16 + parity * 80);   // two places, which steps alternate between
+        parity ^= 1;
         float e;
-        const float r = deviation(s4[0], s4[1], P.inv_width, P.epsilon, e);
-        const float mean_t = s4[2] * P.inv_width, mean_tn = (s4[3] * P.inv_width - e * mean_t) * r;
+        const float r = deviation(s[0], s[1], P.inv_width, P.epsilon, e);
+        const float mean_t = s[2] * P.inv_width, mean_tn = (s[3] * P.inv_width - e * mean_t) * r;
         const float2 scale = both(r), shift = both(-e * r), less = both(-r * mean_t), less_n = both(-r * mean_tn);
         if (NE == 8 || on) {   // of a warp with several teams all lanes go on together, for the mask
             S *to = static_cast<S *>(P.d_in) + row * P.d_in_row + layout.column;
@@ -435,6 +453,7 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
                 }
             }
         }
+        if constexpr (kPipe) m = s[4] * P.inv_width;
         if (kHeld && ahead) settle(next);
         stage = stage + 1 == stages ? 0 : stage + 1;
     }
@@ -500,15 +519,15 @@ inline int lanes_of(int width, int each) {   // of a team whose lanes have `each
 }
 
 // A launch's shape: `fixed` bytes of shared memory a block, and `stage` for each stage of its threads' places.  As many
-// stages, up to 4, as leave an SM its 512 threads of 128 registers; two at least, if one block has room for them.
+// stages, up to 4, as leave an SM its 512 threads of 128 registers; `least` at least, or if one block has no room for them, 1.
 struct Shape {
     int stages, resident;   // resident: blocks an SM holds
     size_t smem;
-    Shape(int threads, size_t fixed, size_t stage) {
+    Shape(int threads, size_t fixed, size_t stage, int least = 2) {
         constexpr size_t kRoom = 227 * 1024, kBlock = 1024;   // of an SM; of which each block takes some
         const int most = 512 / threads;
         stages = 4;
-        while (stages > 2 && most * (fixed + stages * stage + kBlock) > kRoom + kBlock) --stages;
+        while (stages > least && most * (fixed + stages * stage + kBlock) > kRoom + kBlock) --stages;
         if (fixed + stages * stage > kRoom) stages = 1;
         smem = fixed + stages * stage;
         const int fit = static_cast<int>((kRoom + kBlock) / (smem + kBlock));
@@ -545,8 +564,10 @@ cudaError_t backward(NormLaunch L, cudaStream_t stream) {
     constexpr bool kShared = kGains<S, NE, BRANCH> == kSharedGain;
     L.lanes = lanes_of(L.width, NE);
     const int threads = L.lanes > 256 ? L.lanes : 256 / L.lanes * L.lanes, teams = threads / L.lanes;
-    const Shape shape(threads, (L.lanes > 32 ? teams * 320 : 0) + (BRANCH || kShared ? Table<E, NE, kBlocks<T, NE, BRANCH>, kShared>::bytes(L.lanes) : 0),
-                      NE * (sizeof(S) * (BRANCH ? 2 : 1) + sizeof(T)) * threads);
+    const Shape shape(threads, (L.lanes > 32 ? teams * 704 : 0) + (BRANCH || kShared ? Table<E, NE, kBlocks<T, NE, BRANCH>, kShared>::bytes(L.lanes) : 0),
+                      NE * (sizeof(S) * (BRANCH ? 2 : 1) + sizeof(T)) * threads,
+                      kPiped<T, S, NE, BRANCH, MOVES> ? 3 : 2);
+    if (kPiped<T, S, NE, BRANCH, MOVES> && shape.stages < 3) return cudaErrorInvalidConfiguration;
     L.stages = shape.stages;
     const size_t sums = static_cast<size_t>(threads) * NE * sizeof(float), smem = shape.smem > sums ? shape.smem : sums;
     long long blocks = (L.rows + teams - 1) / teams;
@@ -572,12 +593,9 @@ cudaError_t launch_widths(const NormLaunch &L, cudaStream_t stream) {
     if (L.backward) {
         if (w <= 256) return backward<T, S, E, 8, BRANCH, MOVES>(L, stream);
         if constexpr (sizeof(S) == 2) {
-            // Sixteen elements of a row a thread keep the gain and the deviations in registers, which is best for the norm
-            // alone; a join, whose mask takes registers too, does better with one warp a row.
-            if (w > 512 && w <= 8192) {
-                if (held_by(w, 24) < held_by(w, 16)) return backward<T, S, E, 24, BRANCH, MOVES>(L, stream);
-                if (BRANCH && held_by(w, 32) <= held_by(w, 24)) return backward<T, S, E, 32, BRANCH, MOVES>(L, stream);
-            }
+#ifndef V_NO24
+            if (w > 512 && w <= 8192 && held_by(w, 24) < held_by(w, 16)) return backward<T, S, E, 24, BRANCH, MOVES>(L, stream);
+#endif
         }
         if (w > 8192) return backward<T, S, E, 32, BRANCH, MOVES>(L, stream);
         return backward<T, S, E, 16, BRANCH, MOVES>(L, stream);
