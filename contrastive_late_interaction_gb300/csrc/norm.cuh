@@ -518,20 +518,34 @@ inline int lanes_of(int width, int each) {   // of a team whose lanes have `each
     return lanes;
 }
 
-// A launch's shape: `fixed` bytes of shared memory a block, and `stage` for each stage of its threads' places.  As many
-// stages, up to 4, as leave an SM its 512 threads of 128 registers; `least` at least, or if one block has no room for them, 1.
+// Threads of a block: whole teams, 256 of them or the first number above that leaves fewer of an SM's 512 idle.
+inline int threads_of(int lanes) {
+    int best = lanes;
+    for (int t = lanes; t <= 512; t += lanes)
+        if (t / lanes <= 15 || lanes <= 32)   // there are 16 barriers
+            if (best < 256 ? t <= 256 || 512 / t * t >= 512 / best * best : 512 / t * t > 512 / best * best) best = t;
+    return best;
+}
+
+// A launch's shape, for `groups` of rows that a team takes at a time: `fixed` bytes of shared memory a block, and `stage`
+// for each stage of its threads' places.  As many stages, up to 4 and to a team's steps, as leave an SM its 512 threads of
+// 128 registers; `least` at least, or if one block has no room for them, 1.
 struct Shape {
-    int stages, resident;   // resident: blocks an SM holds
+    int stages;
+    long long blocks;
     size_t smem;
-    Shape(int threads, size_t fixed, size_t stage, int least = 2) {
+    Shape(int threads, int teams, long long groups, int sm_count, size_t fixed, size_t stage, int least) {
         constexpr size_t kRoom = 227 * 1024, kBlock = 1024;   // of an SM; of which each block takes some
         const int most = 512 / threads;
         stages = 4;
         while (stages > least && most * (fixed + stages * stage + kBlock) > kRoom + kBlock) --stages;
         if (fixed + stages * stage > kRoom) stages = 1;
+        const int fit = static_cast<int>((kRoom + kBlock) / (fixed + stages * stage + kBlock));
+        const long long across = static_cast<long long>(fit < most ? fit : most) * sm_count, want = (groups + teams - 1) / teams;
+        blocks = want < 1 ? 1 : want < across ? want : across;
+        const long long steps = (want + blocks - 1) / blocks;
+        if (stages > steps && stages > least) stages = steps > least ? static_cast<int>(steps) : least;
         smem = fixed + stages * stage;
-        const int fit = static_cast<int>((kRoom + kBlock) / (smem + kBlock));
-        resident = fit < most ? fit : most;
     }
 };
 
@@ -543,16 +557,15 @@ cudaError_t allow(K kernel, size_t smem) {   // more shared memory than a kernel
 template <typename T, typename S, int E, int NE, int R, bool BRANCH, int MOVES>
 cudaError_t forward(NormLaunch L, cudaStream_t stream) {
     L.lanes = lanes_of(L.width, NE);
-    const int threads = L.lanes > 256 ? L.lanes : 256 / L.lanes * L.lanes, teams = threads / L.lanes;
-    const Shape shape(threads, (L.lanes > 32 ? teams * R * 192 : 0) + (BRANCH ? Table<E, NE, true, false>::bytes(L.lanes) : 0),
-                      NE * R * (sizeof(S) + (BRANCH ? sizeof(T) : 0)) * threads);
+    const int threads = threads_of(L.lanes), teams = threads / L.lanes;
+    const Shape shape(threads, teams, (L.rows + R - 1) / R, L.sm_count,
+                      (L.lanes > 32 ? teams * R * 192 : 0) + (BRANCH ? Table<E, NE, true, false>::bytes(L.lanes) : 0),
+                      NE * R * (sizeof(S) + (BRANCH ? sizeof(T) : 0)) * threads, 1);
     L.stages = shape.stages;
-    const long long want = (L.rows + static_cast<long long>(teams) * R - 1) / (static_cast<long long>(teams) * R);
-    const long long most = static_cast<long long>(shape.resident) * L.sm_count;
     auto kernel = forward_kernel<T, S, E, NE, R, BRANCH, MOVES>;
     const cudaError_t e = allow(kernel, shape.smem);
     if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(want < most ? want : most), threads, shape.smem, stream>>>(L);
+    kernel<<<static_cast<unsigned>(shape.blocks), threads, shape.smem, stream>>>(L);
     return cudaGetLastError();
 }
 
@@ -563,17 +576,15 @@ template <typename T, typename S, int E, int NE, bool BRANCH, int MOVES>
 cudaError_t backward(NormLaunch L, cudaStream_t stream) {
     constexpr bool kShared = kGains<S, NE, BRANCH> == kSharedGain;
     L.lanes = lanes_of(L.width, NE);
-    const int threads = L.lanes > 256 ? L.lanes : 256 / L.lanes * L.lanes, teams = threads / L.lanes;
-    const Shape shape(threads, (L.lanes > 32 ? teams * 704 : 0) + (BRANCH || kShared ? Table<E, NE, kBlocks<T, NE, BRANCH>, kShared>::bytes(L.lanes) : 0),
-                      NE * (sizeof(S) * (BRANCH ? 2 : 1) + sizeof(T)) * threads,
-                      kPiped<T, S, NE, BRANCH, MOVES> ? 3 : 2);
-    if (kPiped<T, S, NE, BRANCH, MOVES> && shape.stages < 3) return cudaErrorInvalidConfiguration;
+    const int threads = threads_of(L.lanes), teams = threads / L.lanes;
+    constexpr bool kPipe = kPiped<T, S, NE, BRANCH, MOVES>;
+    const Shape shape(threads, teams, L.rows, L.sm_count,
+                      (L.lanes > 32 ? teams * 704 : 0) + (BRANCH || kShared ? Table<E, NE, kBlocks<T, NE, BRANCH>, kShared>::bytes(L.lanes) : 0),
+                      NE * (sizeof(S) * (BRANCH ? 2 : 1) + sizeof(T)) * threads, kPipe ? 3 : 1);
+    if (kPipe && shape.stages < 3) return cudaErrorInvalidConfiguration;
     L.stages = shape.stages;
     const size_t sums = static_cast<size_t>(threads) * NE * sizeof(float), smem = shape.smem > sums ? shape.smem : sums;
-    long long blocks = (L.rows + teams - 1) / teams;
-    const long long most = static_cast<long long>(shape.resident) * L.sm_count;
-    blocks = blocks < 1 ? 1 : blocks < most ? blocks : most;
-    if (L.partials && L.rows <= kFewRows * teams) blocks = 1;
+    const long long blocks = L.partials && L.rows <= kFewRows * teams ? 1 : shape.blocks;
     auto kernel = backward_kernel<T, S, E, NE, BRANCH, MOVES>;
     cudaError_t e = allow(kernel, smem);
     if (e != cudaSuccess) return e;
@@ -583,27 +594,29 @@ cudaError_t backward(NormLaunch L, cudaStream_t stream) {
     return launch_after(gain_kernel, dim3((L.width + 31) / 32, 2), 1024, 0, stream, L, static_cast<int>(blocks));
 }
 
-// What a team of whole warps spends on a row goes by what its lanes could hold, there or not.
-inline int held_by(int width, int each) { return (width + 32 * each - 1) / (32 * each) * each; }
-
+// How many elements of a row a thread has.  Sixteen leave it room for what the row and its columns need from one step to
+// the next, and the team meets once (its gradient) or twice (for two rows of 16-bit types).  Measured for 16-bit rows, as
+// shares of the copy's rate with 16 | 24 | 32:
+//   norm            0.81 | 0.49 | 0.71 at 1024, 0.74 | 0.44 | 0.57 at 4096, 0.66 | 0.42 | 0.55 at 8192
+//   its gradient    0.61 | 0.69 | 0.68 at 768, 0.74 | 0.52 | 0.67 at 1024, 0.69 | 0.65 | 0.63 at 1536, 0.63 | 0.64 | 0.68 at
+//                   2048, 0.61 | 0.53 | 0.67 at 4096, 0.55 | 0.50 | 0.64 at 8192
+//   join's gradient 0.67 | 0.75 | 0.55 at 768, 0.76 | 0.61 | 0.61 at 1024, 0.73 | 0.69 | 0.53 at 2048, 0.64 | 0.57 | 0.43 at
+//                   8192
 template <typename T, typename S, int E, bool BRANCH, int MOVES>
 cudaError_t launch_widths(const NormLaunch &L, cudaStream_t stream) {
-    constexpr int kBytes = static_cast<int>(sizeof(S) + (BRANCH ? sizeof(T) : 0));
     const int w = L.width;
     if (L.backward) {
         if (w <= 256) return backward<T, S, E, 8, BRANCH, MOVES>(L, stream);
         if constexpr (sizeof(S) == 2) {
-#ifndef V_NO24
-            if (w > 512 && w <= 8192 && held_by(w, 24) < held_by(w, 16)) return backward<T, S, E, 24, BRANCH, MOVES>(L, stream);
-#endif
+            if (w > 512 && w <= 768) return backward<T, S, E, 24, BRANCH, MOVES>(L, stream);
+            if (!BRANCH && w > 1536) return backward<T, S, E, 32, BRANCH, MOVES>(L, stream);
         }
         if (w > 8192) return backward<T, S, E, 32, BRANCH, MOVES>(L, stream);
         return backward<T, S, E, 16, BRANCH, MOVES>(L, stream);
     }
-    constexpr int kRows = kBytes > 6 ? 1 : 2;   // what leaves room for two stages
+    constexpr int kRows = sizeof(S) + (BRANCH ? sizeof(T) : 0) > 6 ? 1 : 2;   // what leaves room for two stages
     if (w <= 256) return forward<T, S, E, 8, 2 * kRows, BRANCH, MOVES>(L, stream);
     if (w > 8192) return forward<T, S, E, 32, 1, BRANCH, MOVES>(L, stream);
-    if (held_by(w, 24) < held_by(w, 16)) return forward<T, S, E, 24, 1, BRANCH, MOVES>(L, stream);
     return forward<T, S, E, 16, kRows, BRANCH, MOVES>(L, stream);
 }
 
