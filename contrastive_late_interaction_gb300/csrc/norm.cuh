@@ -24,12 +24,12 @@ using namespace rows;
 
 constexpr int kThreads = 512;   // the most of a block: one team of the widest rows
 
-// A thread's chunks lie a constant apart where its team is whole warps (NE > 8).
-template <typename T, int E, int NE, int MOVES>
-using RowLayout = Layout<T, E, MOVES, NE == 8 ? 0 : 32>;
-template <typename L, int NE>
+// A thread's chunks lie a constant apart unless its team is a part of a warp (SUB).
+template <typename T, int E, bool SUB, int MOVES>
+using RowLayout = Layout<T, E, MOVES, SUB ? 0 : 32>;
+template <typename L, int NE, bool SUB>
 __device__ __forceinline__ L layout_of(const Team &team) {
-    return NE == 8 ? L(team.lanes, team.lane, 0) : L(32, team.lane & 31, (team.lane >> 5) * (32 * NE));
+    return SUB ? L(team.lanes, team.lane, 0) : L(32, team.lane & 31, (team.lane >> 5) * (32 * NE));
 }
 
 // 1 / sqrt(variance + epsilon) of `width` deviations that sum to `sum` and whose squares sum to `squares`; e: their mean.
@@ -132,7 +132,7 @@ __device__ __forceinline__ void wait_copies(int ahead) {
 // T: type of the branch and the output.  S: the stream's.  E: elements of a
 // chunk; NE: of a row that a thread has; R: rows that a team takes at a time.
 // BRANCH: a branch joins.
-template <typename T, typename S, int E, int NE, int R, bool BRANCH, int MOVES>
+template <typename T, typename S, int E, int NE, bool SUB, int R, bool BRANCH, int MOVES>
 __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant__ NormLaunch P) {
     constexpr int C = NE / E;
     const int stages = P.stages;
@@ -141,23 +141,14 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
     const Team team(P.lanes);
     float *sums = scratch + team.id * R * 48;
     uint32_t places = smem_u32(scratch) + (team.lanes > 32 ? team.in_block * R * 192 : 0);
-    using L = RowLayout<T, E, NE, MOVES>;
+    using L = RowLayout<T, E, SUB, MOVES>;
     using Tab = Table<E, NE, true, false>;
-    const L layout = layout_of<L, NE>(team);
-    const Tab table = [&] {
-        if constexpr (BRANCH) return Tab(places, P, team, layout);
-        else return Tab();
-    }();
+    const L layout = layout_of<L, NE, SUB>(team);
+    const uint32_t table_at = places;
     if (BRANCH) places += Tab::bytes(team.lanes);
     Feed<S, E, C * R, MOVES> in(places, stages);
     Feed<T, E, C * R, MOVES> branch(places + stages * NE * R * static_cast<int>(sizeof(S)) * blockDim.x, BRANCH ? stages : 0);
     const uint32_t there = layout.template there<C>(P.width);
-    float2 gain[kHold ? C : 1][E / 2], bias[kHold ? C : 1][E / 2];
-#pragma unroll
-    for (int j = 0; j < C && kHold; ++j) {
-        layout.vector(P.gain, j, P.width, 1.0f, gain[j]);
-        layout.vector(P.bias, j, P.width, 0.0f, bias[j]);
-    }
     const uint32_t rows = static_cast<uint32_t>(P.rows), stride = team.count * R, mine = team.index * R;
     const uint32_t first = team.first * R;   // of the warp
 
@@ -185,6 +176,17 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
     for (int k = 0; k < ahead; ++k) {
         copy(k * stride, k);
         asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // While these are on their way, what the rows share.
+    const Tab table = [&] {
+        if constexpr (BRANCH) return Tab(table_at, P, team, layout);
+        else return Tab();
+    }();
+    float2 gain[kHold ? C : 1][E / 2], bias[kHold ? C : 1][E / 2];
+#pragma unroll
+    for (int j = 0; j < C && kHold; ++j) {
+        layout.vector(P.gain, j, P.width, 1.0f, gain[j]);
+        layout.vector(P.bias, j, P.width, 0.0f, bias[j]);
     }
     if (kHeld && ahead) settle(0);
     int stage = 0;
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
             }
             s[r] = sum.x + sum.y;
         }
-        team.sum<R, (NE > 8)>(s, sums);
+        team.sum<R, !SUB>(s, sums);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const float m = s[r] * P.inv_width;
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
             s2[2 * r] = sum.x + sum.y;
             s2[2 * r + 1] = squares.x + squares.y;
         }
-        team.sum<2 * R, (NE > 8)>(s2, sums + R * 16);
+        team.sum<2 * R, !SUB>(s2, sums + R * 16);
 #pragma unroll
         for (int r = 0; r < R; ++r) s[r] = deviation(s2[2 * r], s2[2 * r + 1], P.inv_width, P.epsilon, s2[2 * r]);
 #pragma unroll
@@ -282,7 +284,7 @@ template <typename T, typename S, int NE, bool BRANCH, int MOVES>
 constexpr bool kPiped = !(MOVES == kHalves && sizeof(T) == 2) &&
                         (NE == 8 || (NE == 16 && !(BRANCH && sizeof(S) == 4)) || (NE == 24 && !BRANCH));
 
-template <typename T, typename S, int E, int NE, bool BRANCH, int MOVES>
+template <typename T, typename S, int E, int NE, bool SUB, bool BRANCH, int MOVES>
 __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ NormLaunch P) {
     constexpr int C = NE / E;
     constexpr bool kHold = NE <= 16;   // the row's deviations stay in registers
@@ -292,9 +294,9 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
     const Team team(P.lanes);
     float *sums = scratch + team.id * 176;
     uint32_t places = smem_u32(scratch) + (team.lanes > 32 ? team.in_block * 704 : 0);
-    using L = RowLayout<T, E, NE, MOVES>;
+    using L = RowLayout<T, E, SUB, MOVES>;
     using Tab = Table<E, NE, kBlocks<T, NE, BRANCH>, kGain == kSharedGain>;
-    const L layout = layout_of<L, NE>(team);
+    const L layout = layout_of<L, NE, SUB>(team);
     const Tab table = [&] {
         if constexpr (BRANCH || kGain == kSharedGain) return Tab(places, P, team, layout);
         else return Tab();
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
     };
     auto mean_of = [&](int from) {
         float s[1] = {total_of(from)};
-        team.sum<1, (NE > 8)>(s, sums);
+        team.sum<1, !SUB>(s, sums);
         return s[0] * P.inv_width;
     };
     constexpr bool kPipe = kPiped<T, S, NE, BRANCH, MOVES>;
@@ -409,13 +411,13 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
             s[0] = sum.x + sum.y, s[1] = squares.x + squares.y, s[2] = sum_t.x + sum_t.y, s[3] = sum_td.x + sum_td.y;
         }
         if constexpr (kPipe) s[4] = total_of(stage + 1 == stages ? 0 : stage + 1);
-        team.sum<kPipe ? 5 : 4, (NE > 8)>(s, sums + 16 + parity * 80);   // two places, which steps alternate between
+        team.sum<kPipe ? 5 : 4, !SUB>(s, sums + 16 + parity * 80);   // two places, which steps alternate between
         parity ^= 1;
         float e;
         const float r = deviation(s[0], s[1], P.inv_width, P.epsilon, e);
         const float mean_t = s[2] * P.inv_width, mean_tn = (s[3] * P.inv_width - e * mean_t) * r;
         const float2 scale = both(r), shift = both(-e * r), less = both(-r * mean_t), less_n = both(-r * mean_tn);
-        if (NE == 8 || on) {   // of a warp with several teams all lanes go on together, for the mask
+        if (SUB || on) {   // of a warp with several teams all lanes go on together, for the mask
             S *to = static_cast<S *>(P.d_in) + row * P.d_in_row + layout.column;
             T *to_x = static_cast<T *>(P.d_branch) + row * P.d_branch_row + layout.column;
 #pragma unroll
@@ -528,7 +530,7 @@ inline int threads_of(int lanes) {
 }
 
 // A launch's shape, for `groups` of rows that a team takes at a time: `fixed` bytes of shared memory a block, and `stage`
-// for each stage of its threads' places.  As many stages, up to 4 and to a team's steps, as leave an SM its 512 threads of
+// for each stage of its threads' places.  As many stages, up to 4 and one more than a team's steps, as leave an SM its 512 threads of
 // 128 registers; `least` at least, or if one block has no room for them, 1.
 struct Shape {
     int stages;
@@ -544,7 +546,7 @@ struct Shape {
         const long long across = static_cast<long long>(fit < most ? fit : most) * sm_count, want = (groups + teams - 1) / teams;
         blocks = want < 1 ? 1 : want < across ? want : across;
         const long long steps = (want + blocks - 1) / blocks;
-        if (stages > steps && stages > least) stages = steps > least ? static_cast<int>(steps) : least;
+        if (stages > steps + 1 && stages > least) stages = steps + 1 > least ? static_cast<int>(steps) + 1 : least;
         smem = fixed + stages * stage;
     }
 };
@@ -554,7 +556,7 @@ cudaError_t allow(K kernel, size_t smem) {   // more shared memory than a kernel
     return smem > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) : cudaSuccess;
 }
 
-template <typename T, typename S, int E, int NE, int R, bool BRANCH, int MOVES>
+template <typename T, typename S, int E, int NE, bool SUB, int R, bool BRANCH, int MOVES>
 cudaError_t forward(NormLaunch L, cudaStream_t stream) {
     L.lanes = lanes_of(L.width, NE);
     const int threads = threads_of(L.lanes), teams = threads / L.lanes;
@@ -562,7 +564,7 @@ cudaError_t forward(NormLaunch L, cudaStream_t stream) {
                       (L.lanes > 32 ? teams * R * 192 : 0) + (BRANCH ? Table<E, NE, true, false>::bytes(L.lanes) : 0),
                       NE * R * (sizeof(S) + (BRANCH ? sizeof(T) : 0)) * threads, 1);
     L.stages = shape.stages;
-    auto kernel = forward_kernel<T, S, E, NE, R, BRANCH, MOVES>;
+    auto kernel = forward_kernel<T, S, E, NE, SUB, R, BRANCH, MOVES>;
     const cudaError_t e = allow(kernel, shape.smem);
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(shape.blocks), threads, shape.smem, stream>>>(L);
@@ -572,7 +574,7 @@ cudaError_t forward(NormLaunch L, cudaStream_t stream) {
 // With so few rows a team and gradients over them one block takes them all, and no second kernel adds its sums up.
 constexpr int kFewRows = 4;
 
-template <typename T, typename S, int E, int NE, bool BRANCH, int MOVES>
+template <typename T, typename S, int E, int NE, bool SUB, bool BRANCH, int MOVES>
 cudaError_t backward(NormLaunch L, cudaStream_t stream) {
     constexpr bool kShared = kGains<S, NE, BRANCH> == kSharedGain;
     L.lanes = lanes_of(L.width, NE);
@@ -585,7 +587,7 @@ cudaError_t backward(NormLaunch L, cudaStream_t stream) {
     L.stages = shape.stages;
     const size_t sums = static_cast<size_t>(threads) * NE * sizeof(float), smem = shape.smem > sums ? shape.smem : sums;
     const long long blocks = L.partials && L.rows <= kFewRows * teams ? 1 : shape.blocks;
-    auto kernel = backward_kernel<T, S, E, NE, BRANCH, MOVES>;
+    auto kernel = backward_kernel<T, S, E, NE, SUB, BRANCH, MOVES>;
     cudaError_t e = allow(kernel, smem);
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(blocks), threads, smem, stream>>>(L);
@@ -594,7 +596,8 @@ cudaError_t backward(NormLaunch L, cudaStream_t stream) {
     return launch_after(gain_kernel, dim3((L.width + 31) / 32, 2), 1024, 0, stream, L, static_cast<int>(blocks));
 }
 
-// How many elements of a row a thread has.  Sixteen leave it room for what the row and its columns need from one step to
+// How many elements of a row a thread has, and whether a team is a part of a warp: up to 256 elements (with eight a thread
+// the norm takes 0.75 at 256 where sixteen take 0.89, its gradient 0.62 against 0.88).  Sixteen leave it room for what the row and its columns need from one step to
 // the next, and the team meets once (its gradient) or twice (for two rows of 16-bit types).  Measured for 16-bit rows, as
 // shares of the copy's rate with 16 | 24 | 32:
 //   norm            0.81 | 0.49 | 0.71 at 1024, 0.74 | 0.44 | 0.57 at 4096, 0.66 | 0.42 | 0.55 at 8192
@@ -606,18 +609,20 @@ template <typename T, typename S, int E, bool BRANCH, int MOVES>
 cudaError_t launch_widths(const NormLaunch &L, cudaStream_t stream) {
     const int w = L.width;
     if (L.backward) {
-        if (w <= 256) return backward<T, S, E, 8, BRANCH, MOVES>(L, stream);
+        if (w <= 32) return backward<T, S, E, 8, true, BRANCH, MOVES>(L, stream);
+        if (w <= 256) return backward<T, S, E, 16, true, BRANCH, MOVES>(L, stream);
         if constexpr (sizeof(S) == 2) {
-            if (w > 512 && w <= 768) return backward<T, S, E, 24, BRANCH, MOVES>(L, stream);
-            if (!BRANCH && w > 1536) return backward<T, S, E, 32, BRANCH, MOVES>(L, stream);
+            if (w > 512 && w <= 768) return backward<T, S, E, 24, false, BRANCH, MOVES>(L, stream);
+            if (!BRANCH && w > 1536) return backward<T, S, E, 32, false, BRANCH, MOVES>(L, stream);
         }
-        if (w > 8192) return backward<T, S, E, 32, BRANCH, MOVES>(L, stream);
-        return backward<T, S, E, 16, BRANCH, MOVES>(L, stream);
+        if (w > 8192) return backward<T, S, E, 32, false, BRANCH, MOVES>(L, stream);
+        return backward<T, S, E, 16, false, BRANCH, MOVES>(L, stream);
     }
     constexpr int kRows = sizeof(S) + (BRANCH ? sizeof(T) : 0) > 6 ? 1 : 2;   // what leaves room for two stages
-    if (w <= 256) return forward<T, S, E, 8, 2 * kRows, BRANCH, MOVES>(L, stream);
-    if (w > 8192) return forward<T, S, E, 32, 1, BRANCH, MOVES>(L, stream);
-    return forward<T, S, E, 16, kRows, BRANCH, MOVES>(L, stream);
+    if (w <= 32) return forward<T, S, E, 8, true, 2 * kRows, BRANCH, MOVES>(L, stream);
+    if (w <= 256) return forward<T, S, E, 16, true, kRows, BRANCH, MOVES>(L, stream);
+    if (w > 8192) return forward<T, S, E, 32, false, 1, BRANCH, MOVES>(L, stream);
+    return forward<T, S, E, 16, false, kRows, BRANCH, MOVES>(L, stream);
 }
 
 template <typename T, typename S, int E, int MOVES>
