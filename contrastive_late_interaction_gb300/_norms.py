@@ -145,6 +145,8 @@ def _workspace(workspace, wanted, shape, like, device):
     if not wanted:
         return None, 0, 0
     need = _b.lib.layer_norm_backward_workspace_bytes(*shape)
+    if not need:
+        return None, 0, 0
     workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
     return workspace, workspace.data_ptr(), need
 

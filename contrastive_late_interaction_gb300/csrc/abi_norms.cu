@@ -158,7 +158,7 @@ cli_status_t norm_call(const Norm &a) {
     if ((st = mask_of(a.mask, L.mask)) != CLI_OK) return st;
     const bool sums = d_gain || d_bias;
     const size_t ws_bytes = sums ? layer_norm_backward_workspace_bytes(a.rows, a.width) : 0, vector = a.width * sizeof(float);
-    if (sums && (!a.workspace || !aligned(a.workspace, 256) || a.workspace_bytes < ws_bytes)) return CLI_INVALID_ARGUMENT;
+    if (ws_bytes && (!a.workspace || !aligned(a.workspace, 256) || a.workspace_bytes < ws_bytes)) return CLI_INVALID_ARGUMENT;
 
     Call c;
     auto rows = [&](const cli_rows_t &r, int dtype, bool there) { return there ? Rows(r, a.rows, a.width, dtype) : Rows(); };
@@ -178,13 +178,13 @@ cli_status_t norm_call(const Norm &a) {
     c.small_in[2] = range_of(a.mask.seed, a.mask.rate > 0.0 ? 16 : 0);
     c.small_out[0] = range_of(d_gain, d_gain ? vector : 0);
     c.small_out[1] = range_of(d_bias, d_bias ? vector : 0);
-    c.small_out[2] = range_of(sums ? a.workspace : nullptr, ws_bytes);
+    c.small_out[2] = range_of(ws_bytes ? a.workspace : nullptr, ws_bytes);
     if ((st = c.check()) != CLI_OK) return st;
     if (a.rows == 0 && !sums) return CLI_OK;
 
     L.sm_count = sm_count();
     if (L.sm_count <= 0) return CLI_DEVICE;
-    if (sums && 2ull * norm_blocks(static_cast<long long>(a.rows), L.sm_count) * vector > ws_bytes) return CLI_UNSUPPORTED;
+    if (ws_bytes && 2ull * norm_blocks(static_cast<long long>(a.rows), L.sm_count) * vector > ws_bytes) return CLI_UNSUPPORTED;
     L.dtype = a.t;
     L.stream_dtype = a.s;
     L.backward = a.backward;
@@ -207,7 +207,7 @@ cli_status_t norm_call(const Norm &a) {
     L.bias = bias;
     L.d_gain = d_gain;
     L.d_bias = d_bias;
-    L.partials = sums ? static_cast<float *>(a.workspace) : nullptr;
+    L.partials = ws_bytes ? static_cast<float *>(a.workspace) : nullptr;
     return launched(launch_norm(L, static_cast<cudaStream_t>(a.stream)));
 }
 
@@ -279,7 +279,7 @@ cli_status_t layer_norm(const cli_layer_norm_t *a) { return layer_norm_call(a, f
 cli_status_t layer_norm_backward(const cli_layer_norm_t *a) { return layer_norm_call(a, true); }
 
 size_t layer_norm_backward_workspace_bytes(size_t rows, size_t width) {
-    if (sizes_ok(rows, width) != CLI_OK) return 0;
+    if (sizes_ok(rows, width) != CLI_OK || norm_few(rows, width)) return 0;
     // Two rows of partial sums a block; 256 SMs cover the GPUs this library is built for.
     return align256(2 * static_cast<size_t>(norm_blocks(static_cast<long long>(rows), 256)) * width * sizeof(float));
 }

@@ -283,13 +283,15 @@ struct NormLaunch {
     void *sum, *out, *d_in, *d_branch;
     long long in_row, branch_row, sum_row, out_row, d_out_row, d_sum_row, d_in_row, d_branch_row;
     const float *gain, *bias;
-    float *d_gain, *d_bias, *partials;   // partials: [2][blocks][width], or NULL
+    float *d_gain, *d_bias, *partials;   // partials: [2][blocks][width]; NULL for a call on few rows
     MaskLaunch mask;
     int sm_count;
     bool wide;          // chunks of 8 are whole, in 16-bit types
 };
 
 constexpr size_t kMaxRowWidth = 16384;
+// A gradient over so few rows is one block's, which needs no partial sums and no second kernel to add them up.
+inline bool norm_few(unsigned long long rows, unsigned long long width) { return rows <= 256 && rows * width <= 16384; }
 // The most blocks of a backward call, each of which has a row of partial sums.
 inline long long norm_blocks(long long rows, int sm_count) { return rows < 4ll * sm_count ? (rows < 1 ? 1 : rows) : 4ll * sm_count; }
 cudaError_t launch_norm(const NormLaunch &L, cudaStream_t stream);

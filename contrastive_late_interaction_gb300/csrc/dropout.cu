@@ -55,7 +55,8 @@ __global__ void __launch_bounds__(512) dropout_kernel(const __grid_constant__ Dr
     const uint32_t row_word = seed.row_word();
     const T *in = static_cast<const T *>(P.in) + layout.column;
     T *out = static_cast<T *>(P.out) + layout.column;
-    Chunk<T, E> next[kUnroll<MOVES>];
+    using Raw = typename L::template Raw<T>;
+    Raw next[kUnroll<MOVES>];
     auto load = [&](uint32_t row) {
 #pragma unroll
         for (int u = 0; u < kUnroll<MOVES>; ++u, row += stride)
@@ -65,14 +66,15 @@ __global__ void __launch_bounds__(512) dropout_kernel(const __grid_constant__ Dr
     load(base + down);
     for (; base < rows; base += kUnroll<MOVES> * stride) {
         uint32_t row = base + down;
-        Chunk<T, E> now[kUnroll<MOVES>];
+        Raw now[kUnroll<MOVES>];
 #pragma unroll
         for (int u = 0; u < kUnroll<MOVES>; ++u) now[u] = next[u];
         load(row + kUnroll<MOVES> * stride);
 #pragma unroll
         for (int u = 0; u < kUnroll<MOVES>; ++u, row += stride) {
             float2 v[E / 2];
-            now[u].floats(v);
+            Chunk<T, E> c = now[u].chunk();
+            c.floats(v);
             if (P.mask.least) {
                 uint4 r[E / 4];
                 draw(blocks, keys, product(kMul0, row ^ row_word), r);
@@ -80,8 +82,8 @@ __global__ void __launch_bounds__(512) dropout_kernel(const __grid_constant__ Dr
                 for (int i = 0; i < E / 4; ++i) hand_round(layout, r[i]);
                 keep<E>(v, r, P.mask.least, P.mask.scale);
             }
-            now[u].set(v);
-            layout.store(now[u], out + row * P.out_row, row < rows ? there : 0u);
+            c.set(v);
+            layout.store(c, out + row * P.out_row, row < rows ? there : 0u);
         }
     }
 }

@@ -460,12 +460,12 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
         stage = stage + 1 == stages ? 0 : stage + 1;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (!P.partials) return;
+    if (!P.d_gain && !P.d_bias) return;
     // The block's sums: its teams' in their order.  A block by itself has the gradients.
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         float *to = P.partials + (static_cast<size_t>(which) * gridDim.x + blockIdx.x) * P.width;
-        if (gridDim.x == 1) to = which ? P.d_bias : P.d_gain;
+        if (!P.partials) to = which ? P.d_bias : P.d_gain;
         if (!to) continue;
         const int slot = NE * team.lanes;   // of a team
         __syncthreads();
@@ -571,9 +571,6 @@ cudaError_t forward(NormLaunch L, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-// With so few rows a team and gradients over them one block takes them all, and no second kernel adds its sums up.
-constexpr int kFewRows = 4;
-
 template <typename T, typename S, int E, int NE, bool SUB, bool BRANCH, int MOVES>
 cudaError_t backward(NormLaunch L, cudaStream_t stream) {
     constexpr bool kShared = kGains<S, NE, BRANCH> == kSharedGain;
@@ -586,13 +583,13 @@ cudaError_t backward(NormLaunch L, cudaStream_t stream) {
     if (kPipe && shape.stages < 3) return cudaErrorInvalidConfiguration;
     L.stages = shape.stages;
     const size_t sums = static_cast<size_t>(threads) * NE * sizeof(float), smem = shape.smem > sums ? shape.smem : sums;
-    const long long blocks = L.partials && L.rows <= kFewRows * teams ? 1 : shape.blocks;
+    const long long blocks = (L.d_gain || L.d_bias) && !L.partials ? 1 : shape.blocks;
     auto kernel = backward_kernel<T, S, E, NE, SUB, BRANCH, MOVES>;
     cudaError_t e = allow(kernel, smem);
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(blocks), threads, smem, stream>>>(L);
     e = cudaGetLastError();
-    if (e != cudaSuccess || !L.partials || blocks == 1) return e;
+    if (e != cudaSuccess || !L.partials) return e;
     return launch_after(gain_kernel, dim3((L.width + 31) / 32, 2), 1024, 0, stream, L, static_cast<int>(blocks));
 }
 

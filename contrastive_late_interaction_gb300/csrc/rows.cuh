@@ -137,24 +137,36 @@ struct Layout {
         }
     }
     // The pieces of a chunk that `there` names (from bit 0), at p, which is the chunk's first element; the others are 0.
+    // As they were loaded: halves a register each, so that nothing waits for them before they are put together.
     template <typename M>
-    __device__ __forceinline__ void load(Chunk<M, E> &c, const M *p, uint32_t there) const {
+    struct Raw {
+        static constexpr bool kApart = MOVES == kHalves && sizeof(M) == 2;
+        uint32_t w[kApart ? E : Chunk<M, E>::kWords4];
+        __device__ __forceinline__ Chunk<M, E> chunk() const {
+            Chunk<M, E> c;
+#pragma unroll
+            for (int i = 0; i < Chunk<M, E>::kWords4; ++i) c.w[i] = kApart ? __byte_perm(w[kApart ? 2 * i : i], w[kApart ? 2 * i + 1 : i], 0x5410) : w[i];
+            return c;
+        }
+    };
+    template <typename M>
+    __device__ __forceinline__ void load(Raw<M> &c, const M *p, uint32_t there) const {
         if constexpr (MOVES == kWhole) {
-            c.clear();
-            if (there & 1u) c.load(p);
-        } else if constexpr (sizeof(M) == 4 || kPiece == 2) {
+            Chunk<M, E> whole;
+            whole.clear();
+            if (there & 1u) whole.load(p);
+#pragma unroll
+            for (int i = 0; i < Chunk<M, E>::kWords4; ++i) c.w[i] = whole.w[i];
+        } else if constexpr (Raw<M>::kApart) {
+#pragma unroll
+            for (int k = 0; k < E; ++k) c.w[k] = there >> k & 1u ? *reinterpret_cast<const uint16_t *>(p + piece(k)) : 0u;
+        } else {
             constexpr int kWords4 = kPiece * static_cast<int>(sizeof(M)) / 4;   // of a piece
 #pragma unroll
             for (int k = 0; k < kPieces; ++k)
 #pragma unroll
                 for (int w = 0; w < kWords4; ++w)
                     c.w[k * kWords4 + w] = there >> k & 1u ? reinterpret_cast<const uint32_t *>(p + piece(k))[w] : 0u;
-        } else {
-            uint32_t h[kPieces];
-#pragma unroll
-            for (int k = 0; k < kPieces; ++k) h[k] = there >> k & 1u ? *reinterpret_cast<const uint16_t *>(p + piece(k)) : 0u;
-#pragma unroll
-            for (int k = 0; k < kPieces; k += 2) c.w[k / 2] = __byte_perm(h[k], h[k + 1], 0x5410);
         }
     }
     template <typename M>
@@ -224,7 +236,9 @@ struct Feed {
     template <typename L>
     __device__ __forceinline__ void copy(const L &layout, int stage, int i, const M *p, uint32_t there) {
         if constexpr (kHeld) {
-            layout.load(held[i], p, there);
+            typename L::template Raw<M> raw;
+            layout.load(raw, p, there);
+            held[i] = raw.chunk();
         } else if constexpr (MOVES == kWhole) {
             if (there & 1u) copy_async<kUnit>(place(stage, i), p);
         } else {

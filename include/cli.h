@@ -693,7 +693,8 @@ typedef struct {
  *   epsilon         > 0
  *   workspace       layer_norm_backward with a d_gain or d_bias alone: device, >=
  *                   layer_norm_backward_workspace_bytes(rows, width), 256-byte
- *                   aligned; contents on entry are ignored
+ *                   aligned; contents on entry are ignored; may be NULL where
+ *                   that is 0, for few rows
  */
 typedef struct {
     int x_dtype, y_dtype;

@@ -64,25 +64,25 @@ def rows(b, place, stride=64, off=0):
 
 
 def norm_args(b, **over):
-    args = dict(x_dtype=0, y_dtype=0, rows=100, width=64, x=rows(b, 1), y=rows(b, 2), d_y=rows(b, 3), d_x=rows(b, 4),
+    args = dict(x_dtype=0, y_dtype=0, rows=1000, width=64, x=rows(b, 1), y=rows(b, 2), d_y=rows(b, 3), d_x=rows(b, 4),
                 gain=A * 5, bias=A * 6, d_gain=A * 7, d_bias=A * 8, epsilon=1e-5, workspace=A * 9,
-                workspace_bytes=b.lib.layer_norm_backward_workspace_bytes(100, 64))
+                workspace_bytes=b.lib.layer_norm_backward_workspace_bytes(1000, 64))
     args.update(over)
     return b.LayerNormArgs(**args)
 
 
 def dropout_args(b, **over):
-    args = dict(dtype=0, rows=100, width=64, x=rows(b, 1), y=rows(b, 2), d_y=rows(b, 3), d_x=rows(b, 4),
+    args = dict(dtype=0, rows=1000, width=64, x=rows(b, 1), y=rows(b, 2), d_y=rows(b, 3), d_x=rows(b, 4),
                 mask=b.DropoutMaskArgs(0.1, A * 10, 0))
     args.update(over)
     return b.DropoutArgs(**args)
 
 
 def join_args(b, **over):
-    args = dict(dtype=0, stream_dtype=0, rows=100, width=64, x=rows(b, 1), residual=rows(b, 2), sum=rows(b, 3),
+    args = dict(dtype=0, stream_dtype=0, rows=1000, width=64, x=rows(b, 1), residual=rows(b, 2), sum=rows(b, 3),
                 y=rows(b, 4), d_y=rows(b, 11), d_sum=rows(b, 12), d_residual=rows(b, 13), d_x=rows(b, 14),
                 mask=b.DropoutMaskArgs(0.1, A * 10, 0), gain=A * 5, bias=A * 6, d_gain=A * 7, d_bias=A * 8, epsilon=1e-5,
-                workspace=A * 9, workspace_bytes=b.lib.layer_norm_backward_workspace_bytes(100, 64))
+                workspace=A * 9, workspace_bytes=b.lib.layer_norm_backward_workspace_bytes(1000, 64))
     args.update(over)
     return b.DropoutLayerNormArgs(**args)
 
@@ -185,7 +185,7 @@ def test_columns_of_one_buffer_are_apart(b):
 
 @pytest.mark.parametrize("verb", BACKWARD_NORMS)
 def test_workspace(b, verb):
-    need = b.lib.layer_norm_backward_workspace_bytes(100, 64)
+    need = b.lib.layer_norm_backward_workspace_bytes(1000, 64)
     assert need % 256 == 0 and need > 0
     for over in (dict(workspace=None), dict(workspace=A * 9 + 8), dict(workspace_bytes=need - 1)):
         assert status(b, verb, **over) == b.CLI_INVALID_ARGUMENT
@@ -193,6 +193,11 @@ def test_workspace(b, verb):
     assert status(b, verb, d_gain=A * 9 + 4) == b.CLI_INVALID_ARGUMENT        # inside the workspace
     for name in ("gain", "d_gain", "d_bias"):
         assert status(b, verb, **{name: A * 15 + 2}) == b.CLI_INVALID_ARGUMENT
+    few = dict(rows=16, width=1024, workspace=None)                           # one block: no partial sums
+    assert b.lib.layer_norm_backward_workspace_bytes(16, 1024) == 0 < b.lib.layer_norm_backward_workspace_bytes(17, 1024)
+    assert b.lib.layer_norm_backward_workspace_bytes(256, 1) == 0 < b.lib.layer_norm_backward_workspace_bytes(257, 1)
+    apart = {n: b.RowsArgs(A * (30 + i), 1024) for i, n in enumerate(READS[verb] + WRITES[verb])}
+    assert status(b, verb, **few, **apart) not in (b.CLI_INVALID_ARGUMENT, b.CLI_SHAPE_MISMATCH)
     assert b.lib.layer_norm_backward_workspace_bytes(100, 0) == 0
     assert b.lib.layer_norm_backward_workspace_bytes(100, 16385) == 0
     assert b.lib.layer_norm_backward_workspace_bytes(1 << 31, 64) == 0
