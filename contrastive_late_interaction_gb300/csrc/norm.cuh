@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
     const L layout = layout_of<L, NE, SUB>(team);
     const uint32_t table_at = places;
     if (BRANCH) places += Tab::bytes(team.lanes);
-    Feed<S, E, C * R, MOVES> in(places, stages);
-    Feed<T, E, C * R, MOVES> branch(places + stages * NE * R * static_cast<int>(sizeof(S)) * blockDim.x, BRANCH ? stages : 0);
+    Feed<S, L, E, C * R, MOVES, true> in(places, stages);
+    Feed<T, L, E, C * R, MOVES, true> branch(places + stages * NE * R * static_cast<int>(sizeof(S)) * blockDim.x, BRANCH ? stages : 0);
     const uint32_t there = layout.template there<C>(P.width);
     const uint32_t rows = static_cast<uint32_t>(P.rows), stride = team.count * R, mine = team.index * R;
     const uint32_t first = team.first * R;   // of the warp
@@ -302,11 +302,11 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
         else return Tab();
     }();
     if (BRANCH || kGain == kSharedGain) places += Tab::bytes(team.lanes);
-    Feed<S, E, C, MOVES> in(places, stages);
+    Feed<S, L, E, C, MOVES, false> in(places, stages);
     places += stages * NE * static_cast<int>(sizeof(S)) * blockDim.x;
-    Feed<T, E, C, MOVES> d_out(places, stages);
+    Feed<T, L, E, C, MOVES, false> d_out(places, stages);
     places += stages * NE * static_cast<int>(sizeof(T)) * blockDim.x;
-    Feed<S, E, C, MOVES> d_sum(places, BRANCH ? stages : 0);
+    Feed<S, L, E, C, MOVES, false> d_sum(places, BRANCH ? stages : 0);
     const uint32_t there = layout.template there<C>(P.width);
     float2 gain[kGain == kHeldGain ? C : 1][E / 2], d_gain[C][E / 2], d_bias[C][E / 2];
 #pragma unroll
@@ -615,7 +615,8 @@ cudaError_t launch_widths(const NormLaunch &L, cudaStream_t stream) {
         if (w > 8192) return backward<T, S, E, 32, false, BRANCH, MOVES>(L, stream);
         return backward<T, S, E, 16, false, BRANCH, MOVES>(L, stream);
     }
-    constexpr int kRows = sizeof(S) + (BRANCH ? sizeof(T) : 0) > 6 ? 1 : 2;   // what leaves room for two stages
+    // Two rows at a time where there is room for two stages of them, and they need no registers on their way.
+    constexpr int kRows = sizeof(S) + (BRANCH ? sizeof(T) : 0) > 6 || MOVES == kHalves ? 1 : 2;
     if (w <= 32) return forward<T, S, E, 8, true, 2 * kRows, BRANCH, MOVES>(L, stream);
     if (w <= 256) return forward<T, S, E, 16, true, kRows, BRANCH, MOVES>(L, stream);
     if (w > 8192) return forward<T, S, E, 32, false, 1, BRANCH, MOVES>(L, stream);

@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "cli_device.cuh"
 #include "cli_internal.h"
 #include "launch.cuh"
@@ -136,8 +138,7 @@ struct Layout {
             }
         }
     }
-    // The pieces of a chunk that `there` names (from bit 0), at p, which is the chunk's first element; the others are 0.
-    // As they were loaded: halves a register each, so that nothing waits for them before they are put together.
+    // A chunk as it was loaded: halves a register each, so that nothing waits for them before they are put together.
     template <typename M>
     struct Raw {
         static constexpr bool kApart = MOVES == kHalves && sizeof(M) == 2;
@@ -149,6 +150,7 @@ struct Layout {
             return c;
         }
     };
+    // The pieces of a chunk that `there` names (from bit 0), at p, which is the chunk's first element; the others are 0.
     template <typename M>
     __device__ __forceinline__ void load(Raw<M> &c, const M *p, uint32_t there) const {
         if constexpr (MOVES == kWhole) {
@@ -202,14 +204,18 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void *from) {
 // A thread's chunks of one matrix of type M, N a step, on their way to it
 // through its own places in shared memory.  No other thread reads those, so
 // that the thread's own wait for its copies is all that a step needs.  Halves,
-// which no asynchronous copy takes, wait in registers for one step.
-template <typename M, int E, int N, int MOVES>
+// which no asynchronous copy takes, wait in registers for one step: each in one
+// of its own with APART, else put together as they come, which waits for them
+// (rows of 771 in bf16: the join takes 289 us apart and 413 together, its
+// gradient, which has no registers left, 543 and 442).
+template <typename M, typename L, int E, int N, int MOVES, bool APART>
 struct Feed {
     static constexpr bool kHeld = MOVES == kHalves && sizeof(M) == 2;
     // Copies of words go to places a word wide, a thread's side by side with the others', so that they meet no bank twice.
     static constexpr int kBytes = Chunk<M, E>::kBytes, kUnit = MOVES == kWhole || kHeld ? kBytes : 4, kUnits = kBytes / kUnit;
     uint32_t at;   // of chunk 0 of stage 0
-    Chunk<M, E> held[kHeld ? N : 1];
+    using Raw = typename L::template Raw<M>;
+    std::conditional_t<APART, Raw, Chunk<M, E>> held[kHeld ? N : 1];
 
     // `base`: where the block's places for this matrix start, [stages][N][units][threads].  Places that no copy writes,
     // those past a row's end, are 0.
@@ -224,21 +230,20 @@ struct Feed {
             else
                 asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(0) : "memory");
         }
-        if constexpr (kHeld) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) held[i].w[0] = held[i].w[1] = 0u;
-        }
     }
     __device__ __forceinline__ uint32_t place(int stage, int i, int unit = 0) const {
         return at + ((stage * N + i) * kUnits + unit) * blockDim.x * kUnit;
     }
     // Chunk i of a step, whose first element is at p.
-    template <typename L>
     __device__ __forceinline__ void copy(const L &layout, int stage, int i, const M *p, uint32_t there) {
         if constexpr (kHeld) {
-            typename L::template Raw<M> raw;
-            layout.load(raw, p, there);
-            held[i] = raw.chunk();
+            if constexpr (APART) {
+                layout.load(held[i], p, there);
+            } else {
+                Raw raw;
+                layout.load(raw, p, there);
+                held[i] = raw.chunk();
+            }
         } else if constexpr (MOVES == kWhole) {
             if (there & 1u) copy_async<kUnit>(place(stage, i), p);
         } else {
@@ -256,8 +261,11 @@ struct Feed {
     __device__ __forceinline__ void settle(int stage) {
         if constexpr (kHeld) {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(place(stage, i)), "r"(held[i].w[0]), "r"(held[i].w[1]) : "memory");
+            for (int i = 0; i < N; ++i) {
+                Chunk<M, E> c;
+                if constexpr (APART) c = held[i].chunk(); else c = held[i];
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(place(stage, i)), "r"(c.w[0]), "r"(c.w[1]) : "memory");
+            }
         }
     }
     __device__ __forceinline__ Chunk<M, E> chunk(int stage, int i) const {
