@@ -9,6 +9,13 @@
 // Work.  A thread has a chunk of one row in every few, always the same columns:
 // what the generator's first rounds make of those and of the step is worked out
 // once.  It takes kUnroll rows at a time, the next ones on their way.
+//
+// Bound: the generator.  A block of four words is 15 multiplications to 64 bits
+// that go out every fourth cycle, so four elements cost a scheduler 60 cycles
+// on that pipe and some 70 on the one of exclusive ors and comparisons, beside
+// 88 that HBM gives a warp's elements in bf16: 131072 x 2048 take 188 us (5.7
+// TB/s), where the bytes alone would take 158; fp32 runs at 0.95 of the copy's
+// rate.  Odd 16-bit rows go element by element: 0.4 at 771 columns.
 
 #include "rows.cuh"
 
@@ -16,9 +23,8 @@ namespace cli {
 namespace rows {
 namespace {
 
-
 // The rounds' keys in registers.  They come by way of shared memory, or the compiler would add them up again in each row:
-// 233 us where these take 195 (131072 x 2048 in bf16, with the blocks' first rounds in registers too).
+// 233 us where these took 195 (131072 x 2048 in bf16, with the blocks' first rounds in registers too).
 struct HeldKeys {
     uint32_t a3, k[12];
     __device__ __forceinline__ uint4 two(int i) const { return make_uint4(k[2 * i - 8], k[2 * i - 7], k[2 * i - 6], k[2 * i - 5]); }
@@ -33,14 +39,17 @@ struct HeldKeys {
     }
 };
 
-template <int MOVES> constexpr int kUnroll = MOVES == kWhole ? 4 : 3;   // 4 for pieces: 33 us where 3 take 29 (30011 rows of 517)
+// Rows that a thread takes at a time.  131072 x 2048 in bf16: 2 take 226 us, 4 194, 6 188, 8 189; fp32 rows of 1024, shares
+// of the copy's rate: 2 0.95, 4 0.84, 6 0.91, 8 0.87; 30011 rows of 517 in fp16, in pieces: 2 29 us, 3 27, 4 33.  (With the registers that a bound
+// of 512 threads alone leaves the compiler to choose, six rows took 221.)
+template <typename T, int MOVES> constexpr int kUnroll = MOVES != kWhole ? 3 : sizeof(T) == 2 ? 6 : 2;
 
 // Lanes whose chunks make a span: whole chunks stand for themselves; pieces of 16 lanes are 32 bytes at least.
 template <int MOVES> constexpr int kPart = MOVES == kWhole ? 1 : 16;
 
 // spans: that the block has of each row; height: rows that it takes side by side.
 template <typename T, int E, int MOVES>
-__global__ void __launch_bounds__(512) dropout_kernel(const __grid_constant__ DropoutLaunch P, int spans, int height) {
+__global__ void __launch_bounds__(512, 1) dropout_kernel(const __grid_constant__ DropoutLaunch P, int spans, int height) {
     constexpr int part = kPart<MOVES>;
     using L = Layout<T, E, MOVES, part>;
     const Seed seed(P.mask);
@@ -56,22 +65,22 @@ __global__ void __launch_bounds__(512) dropout_kernel(const __grid_constant__ Dr
     const T *in = static_cast<const T *>(P.in) + layout.column;
     T *out = static_cast<T *>(P.out) + layout.column;
     using Raw = typename L::template Raw<T>;
-    Raw next[kUnroll<MOVES>];
+    Raw next[kUnroll<T, MOVES>];
     auto load = [&](uint32_t row) {
 #pragma unroll
-        for (int u = 0; u < kUnroll<MOVES>; ++u, row += stride)
+        for (int u = 0; u < kUnroll<T, MOVES>; ++u, row += stride)
             layout.load(next[u], in + row * P.in_row, row < rows ? there : 0u);
     };
     uint32_t base = blockIdx.x * height;   // of the block
     load(base + down);
-    for (; base < rows; base += kUnroll<MOVES> * stride) {
+    for (; base < rows; base += kUnroll<T, MOVES> * stride) {
         uint32_t row = base + down;
-        Raw now[kUnroll<MOVES>];
+        Raw now[kUnroll<T, MOVES>];
 #pragma unroll
-        for (int u = 0; u < kUnroll<MOVES>; ++u) now[u] = next[u];
-        load(row + kUnroll<MOVES> * stride);
+        for (int u = 0; u < kUnroll<T, MOVES>; ++u) now[u] = next[u];
+        load(row + kUnroll<T, MOVES> * stride);
 #pragma unroll
-        for (int u = 0; u < kUnroll<MOVES>; ++u, row += stride) {
+        for (int u = 0; u < kUnroll<T, MOVES>; ++u, row += stride) {
             float2 v[E / 2];
             Chunk<T, E> c = now[u].chunk();
             c.floats(v);

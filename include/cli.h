@@ -682,6 +682,9 @@ typedef struct {
  * layer_norm_backward -- its gradients: with t = gain d_y,
  *     d_x = (t - mean t - n mean(t n)) / sqrt(mean (x - mean x)^2 + epsilon),
  *     d_gain = sum over rows of d_y n,  d_bias = sum over rows of d_y.
+ * The variance is taken from deviations, so that a mean far from 0 costs it no
+ * digits.  Rows whose deviations' squares sum past fp32's range (around 10^19
+ * each) have n = 0.
  *
  *   x_dtype         of x and d_x: y_dtype, or CLI_F32 beside 16-bit outputs
  *   y_dtype         of y and d_y
