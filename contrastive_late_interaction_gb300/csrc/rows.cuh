@@ -392,7 +392,7 @@ __device__ __forceinline__ uint4 shared16(uint32_t at) {
 // teams
 // ----------------------------------------------------------------------------
 
-// Sums over a warp of N values (1, 2, 4 or 5), the same in each lane: with several, halves of the warp take some of them each
+// Sums over a warp of N values, the same in each lane: with several, halves of the warp take some of them each
 // and hand them round at the end, 9 shuffles for four sums instead of 20.
 template <int N>
 __device__ __forceinline__ void warp_sum(float (&v)[N]) {
@@ -408,13 +408,16 @@ __device__ __forceinline__ void warp_sum(float (&v)[N]) {
         for (int o = 8; o; o >>= 1) t += swap(t, o);
         const float u = swap(t, 16);
         v[0] = upper ? u : t, v[1] = upper ? t : u;
-    } else if constexpr (N == 5) {
-        float a[4] = {v[0], v[1], v[2], v[3]}, b[1] = {v[4]};
-        warp_sum(a);
-        warp_sum(b);
-        v[0] = a[0], v[1] = a[1], v[2] = a[2], v[3] = a[3], v[4] = b[0];
+    } else if constexpr (N != 4) {   // as 4 or 2 and the rest: each the same sum as by itself
+        constexpr int kHead = N > 4 ? 4 : 2;
+        float head[kHead], rest[N - kHead];
+#pragma unroll
+        for (int i = 0; i < N; ++i) (i < kHead ? head[i < kHead ? i : 0] : rest[i < kHead ? 0 : i - kHead]) = v[i];
+        warp_sum(head);
+        warp_sum(rest);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = i < kHead ? head[i < kHead ? i : 0] : rest[i < kHead ? 0 : i - kHead];
     } else {
-        static_assert(N == 4, "");
         const bool upper = lane & 16, odd = lane & 8;
         const float a = (upper ? v[2] : v[0]) + swap(upper ? v[0] : v[2], 16);
         const float b = (upper ? v[3] : v[1]) + swap(upper ? v[1] : v[3], 16);

@@ -237,7 +237,8 @@ def test_gradient_matches_differences(cli):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("rows, width", [(20011, 64), (9000, 200), (5000, 1024), (3001, 517), (1500, 4096)])
+@pytest.mark.parametrize("rows, width", [(20011, 64), (9000, 200), (5000, 1024), (3001, 517), (1500, 4096), (4000, 1100), (2500, 3200),
+                                         (1200, 8192), (700, 12000)])
 def test_more_rows_than_the_grid_takes_at_once(cli, rows, width, dtype):
     g = gen(rows)
     x, d_y = rand(g, rows, width, dtype=dtype, shift=0.3), rand(g, rows, width, dtype=dtype)
@@ -246,6 +247,9 @@ def test_more_rows_than_the_grid_takes_at_once(cli, rows, width, dtype):
     b, want = cli.layer_norm_backward(x, d_y, gain, bias), ref.layer_norm_backward(x, d_y, gain, 1e-5, dtype)
     for name in ("d_x", "d_gain", "d_bias"):
         within(b[name], want[name], name)
+    for n in (3, 700):   # whatever comes after them
+        assert torch.equal(cli.layer_norm(x[:n], gain, bias)["output"], cli.layer_norm(x, gain, bias)["output"][:n])
+        assert torch.equal(cli.layer_norm_backward(x[:n], d_y[:n], gain, bias)["d_x"], b["d_x"][:n])
     again = cli.layer_norm_backward(x, d_y, gain, bias)
     assert all(torch.equal(b[n], again[n]) for n in b)
     factor = cli.dropout(torch.ones(rows, width, device="cuda"), 0.2, seed_of(), SITE)["output"].double()
