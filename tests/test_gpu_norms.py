@@ -264,6 +264,15 @@ def test_more_rows_than_the_grid_takes_at_once(cli, rows, width, dtype):
     want = ref.join(x, d_y, (factor != 0) * kept, gain, bias, 1e-5)
     within(f["sum"], want["sum"], "sum")
     within(f["output"], want["output"], "joined output")
+    b = cli.dropout_layer_norm_backward(f["sum"], d_y, 0.2, seed_of(), SITE, x, gain, bias)
+    want = ref.join_backward(f["sum"], d_y, x, (factor != 0) * kept, gain, 1e-5)
+    for name in ("d_residual", "d_x", "d_gain", "d_bias"):
+        within(b[name], want[name], "joined " + name)
+    for n in (3, 700):
+        few = cli.dropout_layer_norm(x[:n], d_y[:n], 0.2, seed_of(), SITE, gain, bias)
+        back = cli.dropout_layer_norm_backward(f["sum"][:n], d_y[:n], 0.2, seed_of(), SITE, x[:n], gain, bias)
+        assert torch.equal(few["output"], f["output"][:n]) and torch.equal(few["sum"], f["sum"][:n])
+        assert torch.equal(back["d_residual"], b["d_residual"][:n]) and torch.equal(back["d_x"], b["d_x"][:n])
 
 
 def test_in_place(cli):
