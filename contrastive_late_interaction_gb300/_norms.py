@@ -48,15 +48,18 @@ def _call(verb, lead, device, args):
 # The checks below ask a tensor for little: each question costs a tenth of a microsecond.
 
 def _first(t, name):
-    """(shape, data type, device) of the call's first matrix [rows, width]."""
+    """(shape, data type, device, (data, row stride)) of the call's first matrix [rows, width]."""
     if not t.is_cuda:
         _b._check_cuda(t, name)
-    if t.dim() != 2:
-        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name} must be [rows, width], not {list(t.shape)}")
-    dtype = t.dtype
+    shape, dtype = t.shape, t.dtype
+    if len(shape) != 2:
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name} must be [rows, width], not {list(shape)}")
     if dtype not in DTYPES:
         raise UnsupportedError(CLI_UNSUPPORTED, f"{name}: {dtype}")
-    return t.shape, dtype, t.get_device()
+    row, inner = t.stride()
+    if inner != 1 and shape[1] > 1:
+        raise ShapeMismatchError(CLI_SHAPE_MISMATCH, f"{name}: the elements of a row must be adjacent")
+    return shape, dtype, t.get_device(), (t.data_ptr(), row)
 
 
 def _matrix(t, name, shape, dtype, device):
@@ -157,9 +160,8 @@ def layer_norm(x, gain=None, bias=None, epsilon=1e-5, dtype=None, out=None, stre
     fp32 `x` if wanted.  Returns dict(output); out['output'] may be `x` itself."""
     if stream is not None:
         return _b._on(stream, layer_norm, locals())
-    shape, stream_dtype, device = _first(x, "x")
+    shape, stream_dtype, device, given = _first(x, "x")
     to = _other(dtype, stream_dtype, "dtype")
-    given = _matrix(x, "x", shape, stream_dtype, device)
     g, b = _vector(gain, "gain", shape[1], device), _vector(bias, "bias", shape[1], device)
     y, made = _result(out, "output", shape, to, x, device)
     _call("layer_norm", x, device, (DTYPES[stream_dtype], DTYPES[to], *shape, *given, *made, 0, 0, 0, 0, g, b, 0, 0, epsilon,
@@ -173,9 +175,9 @@ def layer_norm_backward(x, d_output, gain=None, bias=None, epsilon=1e-5, out=Non
     type with it, `d_output`."""
     if stream is not None:
         return _b._on(stream, layer_norm_backward, locals())
-    shape, stream_dtype, device = _first(x, "x")
+    shape, stream_dtype, device, given = _first(x, "x")
     to = _other(d_output.dtype, stream_dtype, "d_output")
-    given, dy = _matrix(x, "x", shape, stream_dtype, device), _matrix(d_output, "d_output", shape, to, device)
+    dy = _matrix(d_output, "d_output", shape, to, device)
     g = _vector(gain, "gain", shape[1], device)
     _vector(bias, "bias", shape[1], device)
     dx, made = _result(out, "d_x", shape, stream_dtype, x, device)
@@ -193,8 +195,7 @@ def dropout(x, rate, seed, site=0, out=None, stream=None):
     may be `x` itself."""
     if stream is not None:
         return _b._on(stream, dropout, locals())
-    shape, dtype, device = _first(x, "x")
-    given = _matrix(x, "x", shape, dtype, device)
+    shape, dtype, device, given = _first(x, "x")
     mask = _mask(rate, seed, site, device)
     y, made = _result(out, "output", shape, dtype, x, device)
     _call("dropout", x, device, (DTYPES[dtype], *shape, *given, *made, 0, 0, 0, 0, *mask))
@@ -205,8 +206,7 @@ def dropout_backward(d_output, rate, seed, site=0, out=None, stream=None):
     """The gradient of dropout for its input: `d_output` through the same mask.  Returns dict(d_x)."""
     if stream is not None:
         return _b._on(stream, dropout_backward, locals())
-    shape, dtype, device = _first(d_output, "d_output")
-    given = _matrix(d_output, "d_output", shape, dtype, device)
+    shape, dtype, device, given = _first(d_output, "d_output")
     mask = _mask(rate, seed, site, device)
     dx, made = _result(out, "d_x", shape, dtype, d_output, device)
     _call("dropout_backward", d_output, device, (DTYPES[dtype], *shape, 0, 0, 0, 0, *given, *made, *mask))
@@ -221,10 +221,10 @@ def dropout_layer_norm(x, residual, rate, seed, site=0, gain=None, bias=None, ep
     `residual` and out['output'] `x`."""
     if stream is not None:
         return _b._on(stream, dropout_layer_norm, locals())
-    shape, dtype, device = _first(x, "x")
+    shape, dtype, device, given = _first(x, "x")
     stream_dtype = residual.dtype
     _other(dtype, stream_dtype, "x")
-    given, stay = _matrix(x, "x", shape, dtype, device), _matrix(residual, "residual", shape, stream_dtype, device)
+    stay = _matrix(residual, "residual", shape, stream_dtype, device)
     mask = _mask(rate, seed, site, device)
     g, b = _vector(gain, "gain", shape[1], device), _vector(bias, "bias", shape[1], device)
     total, total_made = _result(out, "sum", shape, stream_dtype, residual, device) if want_sum else (None, _NONE)
@@ -242,9 +242,9 @@ def dropout_layer_norm_backward(sum, d_output, rate, seed, site=0, d_sum=None, g
     d_x, d_gain, d_bias); out['d_residual'] may be `d_sum` or `sum`, and out['d_x'] `d_output`."""
     if stream is not None:
         return _b._on(stream, dropout_layer_norm_backward, locals())
-    shape, stream_dtype, device = _first(sum, "sum")
+    shape, stream_dtype, device, given = _first(sum, "sum")
     to = _other(d_output.dtype, stream_dtype, "d_output")
-    given, dy = _matrix(sum, "sum", shape, stream_dtype, device), _matrix(d_output, "d_output", shape, to, device)
+    dy = _matrix(d_output, "d_output", shape, to, device)
     onward = _NONE if d_sum is None else _matrix(d_sum, "d_sum", shape, stream_dtype, device)
     mask = _mask(rate, seed, site, device)
     g = _vector(gain, "gain", shape[1], device)
