@@ -13,6 +13,15 @@
 // warps, each thread NE elements of a row in chunks of E.  Teams walk the rows
 // at the grid's stride, and what a thread needs some steps from now is on its
 // way into its own places in shared memory (rows.cuh).
+//
+// Bound: HBM, where an element's instructions leave it time.  The norm of
+// 270336 x 1024 in bf16 takes 14 an element and 179 us (6.2 TB/s, 91% of the
+// copy's rate); the join of as many into an fp32 stream 31 and 509 us (6.5 TB/s);
+// the norm's gradient over 131072 x 1024 23 and 143 us (5.6 TB/s), the join's 40
+// and 259 us (5.2 TB/s), both at 53 to 57% of the issue slots, which is what 16
+// warps an SM reach: a thread's 128 registers are the columns' sums, the row and
+// the generator.  Over 8192 x 8192 without the stream's gradient, with fewer
+// bytes an element, the join's takes 148 us (3.6 TB/s).
 #pragma once
 
 #include "rows.cuh"
@@ -308,7 +317,7 @@ constexpr Gains kGains = NE > 8 && sizeof(S) == 2 && (BRANCH || NE > 16) ? kShar
 template <typename T, int NE, bool BRANCH> constexpr bool kBlocks = BRANCH && !(NE == 32 && sizeof(T) == 4);
 
 // Where a row's mean comes with the sums of the row before it, so that a team meets once a row (the join's gradient over
-// 131072 x 1024 in bf16: 284 -> 255 us, over 8192 x 8192 204 -> 146): with three stages, for which there is room.
+// 131072 x 1024 in bf16: 284 -> 259 us, over 8192 x 8192 204 -> 148): with three stages, for which there is room.
 template <typename T, typename S, int NE, bool BRANCH, int MOVES>
 constexpr bool kPiped = !(MOVES == kHalves && sizeof(T) == 2) &&
                         (NE == 8 || (NE == 16 && !(BRANCH && sizeof(S) == 4)) || (NE == 24 && !BRANCH));
@@ -559,8 +568,8 @@ inline int threads_of(int lanes) {
 }
 
 // A launch's shape, for `groups` of rows that a team takes at a time: `fixed` bytes of shared memory a block, and `stage`
-// for each stage of its threads' places.  As many stages, up to 4 and one more than a team's steps, as leave an SM its 512 threads of
-// 128 registers; `least` at least, or if one block has no room for them, 1.
+// for each stage of its threads' places.  As many stages, up to 4 and one more than a team's steps, as leave an SM its 512
+// threads of 128 registers; `least` at least, or if one block has no room for them, 1.
 struct Shape {
     int stages;
     long long blocks;
@@ -626,10 +635,11 @@ cudaError_t backward(NormLaunch L, cudaStream_t stream) {
 }
 
 // How many elements of a row a thread has, and whether a team is a part of a warp: up to 256 elements (with eight a thread
-// the norm takes 0.75 at 256 where sixteen take 0.89, its gradient 0.62 against 0.88).  Sixteen leave it room for what the row and its columns need from one step to
-// the next, and the team meets once (its gradient) or twice (for two rows of 16-bit types).  Measured for 16-bit rows, as
+// the norm runs at 0.75 of the copy's rate at 256 where it has 0.89 with sixteen, its gradient at 0.62 against 0.88).
+// Sixteen leave it room for what the row and its columns need from one step to the next.  Measured for 16-bit rows, as
 // shares of the copy's rate with 16 | 24 | 32:
-//   norm            0.81 | 0.49 | 0.71 at 1024, 0.74 | 0.44 | 0.57 at 4096, 0.66 | 0.42 | 0.55 at 8192
+//   norm            0.81 | 0.49 | 0.71 at 1024, 0.74 | 0.44 | 0.57 at 4096, 0.66 | 0.42 | 0.55 at 8192 (0.88, 0.78 and
+//                   0.73 with sixteen as they are now)
 //   its gradient    0.61 | 0.69 | 0.68 at 768, 0.74 | 0.52 | 0.67 at 1024, 0.69 | 0.65 | 0.63 at 1536, 0.63 | 0.64 | 0.68 at
 //                   2048, 0.61 | 0.53 | 0.67 at 4096, 0.55 | 0.50 | 0.64 at 8192
 //   join's gradient 0.67 | 0.75 | 0.55 at 768, 0.76 | 0.61 | 0.61 at 1024, 0.73 | 0.69 | 0.53 at 2048, 0.64 | 0.57 | 0.43 at
