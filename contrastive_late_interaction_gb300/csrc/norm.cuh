@@ -42,9 +42,12 @@ __device__ __forceinline__ L layout_of(const Team &team) {
 }
 
 // 1 / sqrt(variance + epsilon) of `width` deviations that sum to `sum` and whose squares sum to `squares`; e: their mean.
+// 0 where the squares pass fp32's range: their mean's own square may pass it too, and infinity less infinity is no variance
+// (nor does fmaxf let the NaN through).
 __device__ __forceinline__ float deviation(float sum, float squares, float inv_width, float epsilon, float &e) {
     e = sum * inv_width;
-    return rsqrtf(fmaxf(squares * inv_width - e * e, 0.0f) + epsilon);
+    const float r = rsqrtf(fmaxf(squares * inv_width - e * e, 0.0f) + epsilon);
+    return squares < INFINITY ? r : 0.0f;   // of a NaN too: e, and with it the row, is NaN then
 }
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
@@ -453,7 +456,8 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
         parity ^= 1;
         float e;
         const float r = deviation(s[0], s[1], P.inv_width, P.epsilon, e);
-        const float mean_t = s[2] * P.inv_width, mean_tn = (s[3] * P.inv_width - e * mean_t) * r;
+        // Where r is 0, so is n, whatever t and the deviations sum to.
+        const float mean_t = s[2] * P.inv_width, mean_tn = r != 0.0f ? (s[3] * P.inv_width - e * mean_t) * r : 0.0f;
         const float2 scale = both(r), shift = both(-e * r), less = both(-r * mean_t), less_n = both(-r * mean_tn);
         if (SUB || on) {   // of a warp with several teams all lanes go on together, for the mask
             S *to = static_cast<S *>(P.d_in) + row * P.d_in_row + layout.column;

@@ -685,7 +685,9 @@ typedef struct {
  *     d_gain = sum over rows of d_y n,  d_bias = sum over rows of d_y.
  * The variance is taken from deviations, so that a mean far from 0 costs it no
  * digits.  Rows whose deviations' squares sum past fp32's range (around 10^19
- * each) have n = 0.
+ * each, less in wide rows) have n = 0 and d_x = 0.  Rows whose elements or
+ * deviations themselves sum past it are NaN; d_x is not finite where t sums past
+ * it, or where t times the deviations does in a row that has an n.
  *
  *   x_dtype         of x and d_x: y_dtype, or CLI_F32 beside 16-bit outputs
  *   y_dtype         of y and d_y

@@ -1,0 +1,90 @@
+"""Layer norm, dropout and the residual join past tests/test_gpu_norms.py: the numbers, rows, strides and row counts at which
+they can go wrong unseen."""
+
+import pytest
+import torch
+
+import norms_reference as ref
+from test_gpu_norms import BF16, F16, F32, SITE, TYPES, gen, layout, rand, seed_of, vectors, within
+from test_gpu_norms import cli as _cli
+
+pytestmark = pytest.mark.gpu
+cli = _cli   # the fixture
+
+
+# ----------------------------------------------------------------------------
+# very large numbers
+# ----------------------------------------------------------------------------
+
+WIDTHS = [40, 200, 516, 771, 1024, 2100, 4096, 8200]
+
+
+def with_large(g, rows, width, stream, scale, shift):
+    """Ordinary rows, every third of them with one of `scale` around `shift` in its place; which those are."""
+    plain = rand(g, rows, width, dtype=stream)
+    large = torch.arange(rows, device="cuda") % 3 == 1
+    x = plain.clone()
+    x[large] = rand(g, int(large.sum()), width, scale=scale, shift=shift).to(stream)
+    return plain, x, large
+
+
+@pytest.mark.parametrize("types", [t for t in TYPES if t[1] != F16])
+@pytest.mark.parametrize("scale, shift", [(1e21, 0.0), (1e21, 1e22), (1e27, 1e27), (1e28, 0.0), (1e28, 1e29), (1e30, 0.0),
+                                          (1e30, 1e30), (1e32, 1e33), (1e35, 0.0)])
+def test_rows_whose_squares_pass_the_range(cli, types, scale, shift):
+    """They have n = 0: the output is the bias, the norm's part of the gradient 0, and nothing goes to the gain's."""
+    dtype, stream = types
+    for width in WIDTHS:
+        g = gen(width)
+        plain, x, large = with_large(g, 31, width, stream, scale, shift)
+        assert torch.isfinite(x).all() and torch.isfinite(x.float().sum(1)).all()
+        d_y, d_sum = rand(g, 31, width, dtype=dtype), rand(g, 31, width, dtype=stream)
+        gain, bias = vectors(g, width)
+        y, want = cli.layer_norm(x, gain, bias, dtype=dtype)["output"], cli.layer_norm(plain, gain, bias, dtype=dtype)["output"]
+        assert torch.equal(y[~large], want[~large]) and (y[large] == bias.to(dtype)).all(), width
+        b, want = cli.layer_norm_backward(x, d_y, gain, bias), cli.layer_norm_backward(plain, d_y, gain, bias)
+        assert torch.equal(b["d_x"][~large], want["d_x"][~large]) and not b["d_x"][large].any(), width
+        assert torch.equal(b["d_bias"], want["d_bias"]), width
+        none = d_y.clone()
+        none[large] = 0.0
+        assert torch.equal(b["d_gain"], cli.layer_norm_backward(plain, none, gain, bias)["d_gain"]), width
+        # joined
+        branch = rand(g, 31, width, dtype=dtype)
+        f = cli.dropout_layer_norm(branch, x, 0.2, seed_of(), SITE, gain, bias)
+        want = cli.dropout_layer_norm(branch, plain, 0.2, seed_of(), SITE, gain, bias)
+        assert torch.equal(f["output"][~large], want["output"][~large]) and (f["output"][large] == bias.to(dtype)).all(), width
+        b = cli.dropout_layer_norm_backward(x, d_y, 0.2, seed_of(), SITE, d_sum, gain, bias)
+        want = cli.dropout_layer_norm_backward(plain, d_y, 0.2, seed_of(), SITE, d_sum, gain, bias)
+        assert torch.equal(b["d_residual"][~large], want["d_residual"][~large]), width
+        assert torch.equal(b["d_residual"][large], d_sum[large]), width
+        through = cli.dropout(d_sum, 0.2, seed_of(), SITE)["output"].to(dtype)
+        assert torch.equal(b["d_x"][large], through[large]) and torch.equal(b["d_x"][~large], want["d_x"][~large]), width
+        assert torch.equal(b["d_bias"], want["d_bias"]), width
+
+
+@pytest.mark.parametrize("types", [t for t in TYPES if t[1] != F16])
+def test_rows_whose_sum_passes_the_range(cli, types):
+    """They are NaN, and no other row is."""
+    dtype, stream = types
+    for width in WIDTHS[2:]:
+        g = gen(width)
+        plain, x, large = with_large(g, 31, width, stream, 1e35, 2e36)
+        assert torch.isfinite(x).all()
+        d_y = rand(g, 31, width, dtype=dtype)
+        gain, bias = vectors(g, width)
+        y, want = cli.layer_norm(x, gain, bias, dtype=dtype)["output"], cli.layer_norm(plain, gain, bias, dtype=dtype)["output"]
+        assert torch.equal(y[~large], want[~large]) and y[large].isnan().all(), width
+        d, want = cli.layer_norm_backward(x, d_y, gain)["d_x"], cli.layer_norm_backward(plain, d_y, gain)["d_x"]
+        assert torch.equal(d[~large], want[~large]) and d[large].isnan().all(), width
+
+
+def test_large_rows_within_the_range(cli):
+    """10^17: the squares of 8200 such sum to 8 * 10^37."""
+    for width in WIDTHS:
+        g = gen(width)
+        x, d_y = rand(g, 30, width, scale=1e17, shift=3e17), rand(g, 30, width)
+        gain, bias = vectors(g, width)
+        within(cli.layer_norm(x, gain, bias)["output"], ref.layer_norm(x, gain, bias, 1e-5, F32), width)
+        b, want = cli.layer_norm_backward(x, d_y, gain, bias), ref.layer_norm_backward(x, d_y, gain, 1e-5, F32)
+        for name in ("d_x", "d_gain", "d_bias"):
+            within(b[name], want[name], f"{width} {name}")
