@@ -22,11 +22,13 @@ bool is_dtype(int dtype) { return dtype == CLI_BF16 || dtype == CLI_F16 || dtype
 struct Rows {
     uintptr_t at = 0;
     size_t rows = 0, inner = 0, row = 0, element = 1;   // inner: bytes of a row; row: stride in bytes, 0 where there is one
+    size_t step = 0;                                    // the stride in bytes as it was given, modulo 2^64
     bool none = true;
     Rows() = default;
     Rows(const cli_rows_t &r, size_t rows_, size_t width, int dtype)
         : at(reinterpret_cast<uintptr_t>(r.data)), rows(rows_), element(dtype == CLI_F32 ? 4 : 2), none(false) {
         inner = width * element;
+        step = r.row_stride * element;
         // past 2^40 elements it is more than ok() takes, and stays so
         row = rows > 1 ? (r.row_stride >> 40 ? 1ull << 40 : r.row_stride) * element : 0;
     }
@@ -38,8 +40,9 @@ struct Rows {
         if (row >= (1ull << 40) || (row && rows - 1 > (1ull << 61) / row)) return CLI_SHAPE_MISMATCH;
         return CLI_OK;
     }
-    bool pieces(size_t bytes) const {   // rows of whole, aligned pieces
-        return empty() || (at % bytes == 0 && row % bytes == 0 && inner % bytes == 0);
+    // Rows of whole, aligned pieces.  One row's stride counts too, so that it is moved, and its sums run, as beside others.
+    bool pieces(size_t bytes) const {
+        return empty() || (at % bytes == 0 && step % bytes == 0 && inner % bytes == 0);
     }
 };
 

@@ -659,17 +659,19 @@ size_t cross_attention_backward_workspace_bytes(const cli_attention_t *args);
  * Rows of `width` elements, 1 .. 16384 (wider ones: CLI_UNSUPPORTED), rows
  * < 2^31 (0 is a call on no rows).  Types are cli_dtype_t.  Arithmetic is in 32
  * bits, rounded once at the end.  Sums run in a fixed order, so every result
- * is bit-reproducible, and a row's results do not depend on the other rows or
- * their number (but for d_gain and d_bias, which sum over them in an order that
- * goes by the sizes, the matrices' alignment and the device).
+ * is bit-reproducible.  The order of a row's sums goes by the call, its types,
+ * the width and the alignment of the matrices and their strides: a row's results
+ * do not depend on the other rows or their number, so rows of the same matrices
+ * give the same bits in any call.  That of d_gain and d_bias, which sum over the
+ * rows, goes by the number of rows and the device as well.
  * ------------------------------------------------------------------------- */
 
 /* A matrix in device memory: element i of row r is data[r * row_stride + i].
- * `data` is aligned to an element; the stride, in elements, is any (one row's
- * is not read), but an output's rows may not overlap one another.  A call
- * whose matrices all start on 16 bytes and have widths and strides that are
- * multiples of 16 bytes moves them 16 bytes at a time; 16-bit ones on 8 bytes
- * go 8 at a time, others in words of 4 bytes or, on odd multiples of 2, in
+ * `data` is aligned to an element; the stride, in elements, is any (of one row's
+ * the alignment alone counts), but an output's rows may not overlap one another.
+ * A call whose matrices all start on 16 bytes and have widths and strides that
+ * are multiples of 16 bytes moves them 16 bytes at a time; 16-bit ones on 8
+ * bytes go 8 at a time, others in words of 4 bytes or, on odd multiples of 2, in
  * halves.  An output may be an input in place (the same data, stride and
  * type); it overlaps no other input or output otherwise. */
 typedef struct {

@@ -88,3 +88,35 @@ def test_large_rows_within_the_range(cli):
         b, want = cli.layer_norm_backward(x, d_y, gain, bias), ref.layer_norm_backward(x, d_y, gain, 1e-5, F32)
         for name in ("d_x", "d_gain", "d_bias"):
             within(b[name], want[name], f"{width} {name}")
+
+
+# ----------------------------------------------------------------------------
+# one row of several
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("width, gap", [(1024, 5), (1024, 2), (1024, 4), (1024, 8), (200, 1), (517, 3), (4096, 6), (8200, 3)])
+def test_a_row_alone_is_the_row_beside_others(cli, types, width, gap):
+    """Rows of a wider buffer, whose distance decides how they are moved: each alone gives the bits it gives among the others."""
+    dtype, stream = types
+    g = gen(width + gap)
+    rows = 9
+
+    def wide(t):
+        buffer = torch.zeros(rows, width + gap, dtype=t.dtype, device="cuda")
+        buffer[:, :width] = t
+        return buffer[:, :width]
+    x, res = wide(rand(g, rows, width, dtype=dtype)), wide(rand(g, rows, width, dtype=stream, shift=0.5))
+    d_y, d_sum = wide(rand(g, rows, width, dtype=dtype)), wide(rand(g, rows, width, dtype=stream))
+    gain, bias = vectors(g, width)
+
+    def calls(s):
+        f = cli.dropout_layer_norm(x[s], res[s], 0.0, None, 0, gain, bias)
+        b = cli.dropout_layer_norm_backward(res[s], d_y[s], 0.0, None, 0, d_sum[s], gain, bias)
+        return {"norm": cli.layer_norm(res[s], gain, bias, dtype=dtype)["output"], "sum": f["sum"], "joined": f["output"],
+                "d_x": cli.layer_norm_backward(res[s], d_y[s], gain)["d_x"], "d_residual": b["d_residual"], "d_branch": b["d_x"]}
+    want = calls(slice(0, rows))
+    for k in range(rows):
+        for n in (1, 2):
+            for name, got in calls(slice(k, k + n)).items():
+                assert torch.equal(got, want[name][k:k + n]), (name, k, n)
