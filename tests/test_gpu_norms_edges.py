@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import norms_reference as ref
+from norms_sums import gradient_sums
 from test_gpu_norms import BF16, F16, F32, SITE, TYPES, gen, layout, rand, seed_of, vectors, within
 from test_gpu_norms import cli as _cli
 
@@ -120,3 +121,60 @@ def test_a_row_alone_is_the_row_beside_others(cli, types, width, gap):
         for n in (1, 2):
             for name, got in calls(slice(k, k + n)).items():
                 assert torch.equal(got, want[name][k:k + n]), (name, k, n)
+
+
+# ----------------------------------------------------------------------------
+# the sums over rows
+# ----------------------------------------------------------------------------
+
+MANY = [(257, 64), (20011, 64), (9000, 200), (5000, 1024), (3001, 517), (4000, 1100), (2500, 3200), (1200, 8192), (700, 12000)]
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("rows, width", MANY)
+def test_every_row_is_counted_once(cli, types, rows, width):
+    """Column c of the gradient is bit c of the row's number, or 1: whole numbers below 2^24, which add up exactly in any
+    order.  A row lost or taken twice shows in the ones, one in another's place in the bits."""
+    dtype, stream = types
+    g = gen(rows)
+    x = rand(g, rows, width, dtype=stream)
+    gain, bias = vectors(g, width)
+    bits = torch.ones(rows, width, dtype=torch.int64, device="cuda")
+    for c in range(0, width - 17, 32):
+        for k in range(16):
+            bits[:, c + k] = torch.arange(rows, device="cuda") >> k & 1
+    d_y = bits.to(dtype)
+    want = bits.sum(0).float()
+    assert torch.equal(cli.layer_norm_backward(x, d_y, gain, bias)["d_bias"], want)
+    assert torch.equal(cli.dropout_layer_norm_backward(x, d_y, 0.1, seed_of(), gain=gain, bias=bias)["d_bias"], want)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("rows, width", [(20011, 64), (5000, 1024), (3001, 517), (1200, 8192)])
+def test_gradients_of_one_row(cli, types, rows, width):
+    """One row's d_y is 1, the others' 0: the bias's gradient is 1 and the gain's that row's n."""
+    dtype, stream = types
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    x = rand(gen(rows), rows, width, dtype=stream)
+    one, none = torch.ones(width, device="cuda"), torch.zeros(width, device="cuda")
+    for row in (0, 1, 31, 32, sms - 1, sms, 2 * sms - 1, 2 * sms, rows // 2, rows - 2, rows - 1):
+        d_y = torch.zeros(rows, width, dtype=dtype, device="cuda")
+        d_y[row] = 1.0
+        want = ref.layer_norm(x[row:row + 1], one, none, 1e-5, F32)
+        for b in (cli.layer_norm_backward(x, d_y, one, none),
+                  cli.dropout_layer_norm_backward(x, d_y, 0.1, seed_of(), gain=one, bias=none)):
+            assert (b["d_bias"] == 1.0).all(), row
+            within(b["d_gain"], (want[0][0], want[1][0]), row)
+
+
+def test_the_last_of_rows_past_32_bits(cli):
+    """Rows whose element offset passes 2^32: each is counted once, and the last ones' gradients are their own."""
+    rows, width = 2200000, 2048
+    x = torch.zeros(rows, width, dtype=BF16, device="cuda")
+    d_y = torch.ones(rows, width, dtype=BF16, device="cuda")
+    one, none = torch.ones(width, device="cuda"), torch.zeros(width, device="cuda")
+    x[-1] = rand(gen(8), width, dtype=BF16)
+    b = cli.layer_norm_backward(x, d_y, one, none)
+    assert (b["d_bias"] == rows).all()
+    want = ref.layer_norm(x[-1:], one, none, 1e-5, F32)
+    within(b["d_gain"], (want[0][0], want[1][0]), "d_gain")   # the other rows' n is 0
