@@ -178,3 +178,40 @@ def test_the_last_of_rows_past_32_bits(cli):
     assert (b["d_bias"] == rows).all()
     want = ref.layer_norm(x[-1:], one, none, 1e-5, F32)
     within(b["d_gain"], (want[0][0], want[1][0]), "d_gain")   # the other rows' n is 0
+
+
+# ----------------------------------------------------------------------------
+# many rows of every pair of types, in every layout
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["packed", "padded", "fours", "odd"])
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("rows, width", [(20011, 24), (9000, 200), (3001, 517), (4000, 1100), (1500, 2056), (700, 8200)])
+def test_many_rows(cli, types, kind, rows, width):
+    """A team takes several rows, and its copies' places go round: against the reference, sums over rows to within the
+    additions that they have in series."""
+    dtype, stream = types
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    g = gen(rows + width)
+    x, res = rand(g, rows, width, dtype=dtype), rand(g, rows, width, dtype=stream, shift=0.5)
+    d_y, d_sum = rand(g, rows, width, dtype=dtype), rand(g, rows, width, dtype=stream)
+    gain, bias = vectors(g, width)
+    at = [layout(t, kind) for t in (x, res, d_y, d_sum)]
+    within(cli.layer_norm(at[1], gain, bias, dtype=dtype)["output"], ref.layer_norm(res, gain, bias, 1e-5, dtype), "output")
+    b, want = cli.layer_norm_backward(at[1], at[2], gain, bias), ref.layer_norm_backward(res, d_y, gain, 1e-5, stream)
+    within(b["d_x"], want["d_x"], "d_x")
+    for name, value in gradient_sums(res, d_y, sms).items():
+        within(b[name], value, name)
+    kept = 2.0 ** 32 / (2 ** 32 - int(0.2 * 2 ** 32))
+    factor = (cli.dropout(torch.ones(rows, width, device="cuda"), 0.2, seed_of(), SITE)["output"] != 0) * kept
+    within(cli.dropout(at[0], 0.2, seed_of(), SITE)["output"], ref.dropout(x, factor, dtype), "dropped")
+    f = cli.dropout_layer_norm(at[0], at[1], 0.2, seed_of(), SITE, gain, bias)
+    want = ref.join(x, res, factor, gain, bias, 1e-5)
+    within(f["sum"], want["sum"], "sum")
+    within(f["output"], want["output"], "joined output")
+    b = cli.dropout_layer_norm_backward(layout(f["sum"], kind), at[2], 0.2, seed_of(), SITE, at[3], gain, bias)
+    want = ref.join_backward(f["sum"], d_y, d_sum, factor, gain, 1e-5)
+    for name in ("d_residual", "d_x"):
+        within(b[name], want[name], "joined " + name)
+    for name, value in gradient_sums(f["sum"], d_y, sms).items():
+        within(b[name], value, "joined " + name)
