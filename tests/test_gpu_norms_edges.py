@@ -215,3 +215,59 @@ def test_many_rows(cli, types, kind, rows, width):
         within(b[name], want[name], "joined " + name)
     for name, value in gradient_sums(f["sum"], d_y, sms).items():
         within(b[name], value, "joined " + name)
+
+
+# ----------------------------------------------------------------------------
+# columns of one buffer, and no workspace
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows", [1, 2, 700])
+@pytest.mark.parametrize("width, gap", [(64, 0), (61, 0), (200, 3), (1024, 8)])
+def test_columns_of_one_buffer(cli, rows, width, gap):
+    """Input and output side by side in the same rows, either first, are apart: as in buffers of their own, and what lies
+    between them stays."""
+    g = gen(width + rows)
+    x, other = rand(g, rows, width, dtype=BF16), rand(g, rows, width, dtype=BF16)
+    gain, bias = vectors(g, width)
+    seed = seed_of()
+    sums = cli.dropout_layer_norm(x, other, 0.3, seed, SITE, gain, bias)
+    for first in (True, False):
+        def call(into, verb):
+            buffer = torch.full((rows, 2 * width + gap), 7.0, dtype=BF16, device="cuda")
+            a, b = buffer[:, :width], buffer[:, width + gap:]
+            src, dst = (a, b) if first else (b, a)
+            src.copy_(into)
+            verb(src, dst)
+            assert torch.equal(src, into) and (buffer[:, width:width + gap] == 7.0).all()
+            return dst
+        got = call(x, lambda s, d: cli.layer_norm(s, gain, bias, out={"output": d}))
+        within(got, ref.layer_norm(x, gain, bias, 1e-5, BF16), "norm")
+        got = call(x, lambda s, d: cli.dropout(s, 0.3, seed, SITE, out={"output": d}))
+        assert torch.equal(got, cli.dropout(x, 0.3, seed, SITE)["output"])
+        got = call(other, lambda s, d: cli.dropout_layer_norm(x, s, 0.3, seed, SITE, gain, bias, out={"sum": d}))
+        assert torch.equal(got, sums["sum"])
+        got = call(x, lambda s, d: cli.layer_norm_backward(s, other, gain, out={"d_x": d}))
+        within(got, ref.layer_norm_backward(x, other, gain, 1e-5, BF16)["d_x"], "d_x")
+        got = call(other, lambda s, d: cli.dropout_backward(s, 0.3, seed, SITE, out={"d_x": d}))
+        assert torch.equal(got, cli.dropout(other, 0.3, seed, SITE)["output"])
+
+
+def test_gradients_of_few_rows_without_a_workspace(cli):
+    """A NULL workspace is taken where none is needed, and refused where one is."""
+    from contrastive_late_interaction_gb300 import _binding as b
+    import ctypes
+    for rows in (16, 17):
+        x, d_y = rand(gen(rows), rows, 1024, dtype=BF16), rand(gen(1), rows, 1024, dtype=BF16)
+        gain, bias = vectors(gen(2), 1024)
+        want = cli.layer_norm_backward(x, d_y, gain, bias)
+        out = {n: torch.zeros_like(t) for n, t in want.items()}
+        R = b.RowsArgs
+        args = b.LayerNormArgs(x_dtype=0, y_dtype=0, rows=rows, width=1024, x=R(x.data_ptr(), 1024), d_y=R(d_y.data_ptr(), 1024),
+                               d_x=R(out["d_x"].data_ptr(), 1024), gain=gain.data_ptr(), d_gain=out["d_gain"].data_ptr(),
+                               d_bias=out["d_bias"].data_ptr(), epsilon=1e-5,
+                               stream=torch.cuda.current_stream().cuda_stream)
+        got = b.lib.layer_norm_backward(ctypes.byref(args))
+        if rows == 16:
+            assert got == 0 and all(torch.equal(out[n], want[n]) for n in want)
+        else:
+            assert got == b.CLI_INVALID_ARGUMENT
