@@ -10,12 +10,13 @@
 // what the generator's first rounds make of those and of the step is worked out
 // once.  It takes kUnroll rows at a time, the next ones on their way.
 //
-// Bound: the generator.  A block of four words is 15 multiplications to 64 bits
-// that go out every fourth cycle, so four elements cost a scheduler 60 cycles
-// on that pipe and some 70 on the one of exclusive ors and comparisons, beside
-// 88 that HBM gives a warp's elements in bf16: 131072 x 2048 take 188 us (5.7
-// TB/s), where the bytes alone would take 158; fp32 runs at 0.95 of the copy's
-// rate.  Odd 16-bit rows go element by element: 0.4 at 771 columns.
+// Bound: the generator.  A block of four words is 15 multiplications to 64 bits,
+// and half of one that the row's two blocks share, which go out every fourth
+// cycle, so four elements cost a scheduler 62 cycles on that pipe and some 70 on
+// the one of exclusive ors and comparisons (73 in all, alone), beside 88 that
+// HBM gives a warp's elements in bf16: 131072 x 2048 take 188 us (5.7 TB/s),
+// where the bytes alone would take 158; fp32 runs at 0.98 of the copy's rate.
+// Odd 16-bit rows go element by element: 0.42 at 771 columns.
 
 #include "rows.cuh"
 
@@ -110,6 +111,10 @@ cudaError_t launch(const DropoutLaunch &L, cudaStream_t stream) {
         const double used = static_cast<double>(h * spans * part) / t;
         if (!threads || t <= 256 || used > best) height = h, threads = t, best = used;
     }
+    // Blocks for 1024 threads an SM and piece of a row, twice what it holds of the kernels for whole chunks of 16-bit types
+    // (110 to 124 registers): those come in waves, which costs nothing (131072 x 2048 in bf16: 187 us, with blocks for 512
+    // threads 188; 32768 x 8192 188 and 184).  The others need them: fp32 rows of 1024 take 162 us and 202, 30011 rows of 517
+    // in fp16 24.5 and 31.
     const long long want = (L.rows + height - 1) / height;
     const long long most = static_cast<long long>(L.sm_count) * (1024 / threads);
     long long across = want < most ? want : most;

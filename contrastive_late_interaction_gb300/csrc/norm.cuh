@@ -15,13 +15,15 @@
 // way into its own places in shared memory (rows.cuh).
 //
 // Bound: HBM, where an element's instructions leave it time.  The norm of
-// 270336 x 1024 in bf16 takes 14 an element and 179 us (6.2 TB/s, 91% of the
-// copy's rate); the join of as many into an fp32 stream 31 and 509 us (6.5 TB/s);
-// the norm's gradient over 131072 x 1024 23 and 143 us (5.6 TB/s), the join's 40
-// and 259 us (5.2 TB/s), both at 53 to 57% of the issue slots, which is what 16
-// warps an SM reach: a thread's 128 registers are the columns' sums, the row and
-// the generator.  Over 8192 x 8192 without the stream's gradient, with fewer
-// bytes an element, the join's takes 148 us (3.6 TB/s).
+// 270336 x 1024 in bf16 takes 14 an element and 171 us (6.5 TB/s, 95% of the
+// copy's rate); the join of as many into an fp32 stream 31 and 509 us (6.5 TB/s).
+// The gradients wait: 23 instructions an element and 146 us over 131072 x 1024
+// (5.5 TB/s), the join's 40 and 257 us (5.2 TB/s), with 53 to 57% of the issue
+// slots used.  16 warps an SM, which is what a thread's 128 registers allow (the
+// columns' sums, the row and the generator), do not cover the instruction
+// before, shared memory and the team's barrier.  Over 8192 x 8192 without the
+// stream's gradient, where the one team of an SM meets at that barrier and has
+// fewer bytes an element to wait for, the join's takes 148 us (3.6 TB/s).
 #pragma once
 
 #include "rows.cuh"
@@ -529,7 +531,8 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
     }
 }
 
-// The sums of the blocks' partials, 32 columns a block and a fixed share of the rows a warp.
+// The sums of the blocks' partials, 32 columns a block and a fixed share of the rows a warp.  It is launched ahead, but starts
+// when the last block of the gradient's kernel has ended, which does not let it start before.
 static __global__ void __launch_bounds__(1024) gain_kernel(const __grid_constant__ NormLaunch P, int blocks) {
     after_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
@@ -649,6 +652,11 @@ cudaError_t backward(NormLaunch L, cudaStream_t stream) {
 //                   2048, 0.61 | 0.53 | 0.67 at 4096, 0.55 | 0.50 | 0.64 at 8192
 //   join's gradient 0.67 | 0.75 | 0.55 at 768, 0.76 | 0.61 | 0.61 at 1024, 0.73 | 0.69 | 0.53 at 2048, 0.64 | 0.57 | 0.43 at
 //                   8192
+// The gradients' rule holds for rows in pieces as well, where the other kernels pay more often than not although they spill
+// up to 712 bytes a thread (as the rule has it | with sixteen; bf16, halves and then words):
+//   norm's gradient 0.26 | 0.21 at 517, 0.23 | 0.26 at 1537, 0.19 | 0.25 at 2051, 0.26 | 0.25 at 3001, 0.21 | 0.17 at 4099,
+//                   0.25 | 0.25 at 8191; 0.45 | 0.41 at 1538, 0.37 | 0.43 at 2050, 0.41 | 0.32 at 4098
+//   join's gradient 0.21 | 0.18 at 517
 template <typename T, typename S, int E, bool BRANCH, int MOVES>
 cudaError_t launch_widths(const NormLaunch &L, cudaStream_t stream) {
     const int w = L.width;
