@@ -652,11 +652,11 @@ cudaError_t backward(NormLaunch L, cudaStream_t stream) {
 //                   2048, 0.61 | 0.53 | 0.67 at 4096, 0.55 | 0.50 | 0.64 at 8192
 //   join's gradient 0.67 | 0.75 | 0.55 at 768, 0.76 | 0.61 | 0.61 at 1024, 0.73 | 0.69 | 0.53 at 2048, 0.64 | 0.57 | 0.43 at
 //                   8192
-// The gradients' rule holds for rows in pieces as well, where the other kernels pay more often than not although they spill
-// up to 712 bytes a thread (as the rule has it | with sixteen; bf16, halves and then words):
-//   norm's gradient 0.26 | 0.21 at 517, 0.23 | 0.26 at 1537, 0.19 | 0.25 at 2051, 0.26 | 0.25 at 3001, 0.21 | 0.17 at 4099,
-//                   0.25 | 0.25 at 8191; 0.45 | 0.41 at 1538, 0.37 | 0.43 at 2050, 0.41 | 0.32 at 4098
-//   join's gradient 0.21 | 0.18 at 517
+// The gradients' rule is that of rows in pieces as well, where its kernels spill up to 712 bytes a thread and are now the
+// faster ones and now the slower (as the rule has it | with sixteen; bf16, halves and then words):
+//   norm's gradient 0.24 | 0.23 at 517, 0.23 | 0.27 at 1537, 0.18 | 0.27 at 2051, 0.26 | 0.27 at 3001, 0.21 | 0.18 at 4099,
+//                   0.25 | 0.27 at 8191; 0.45 | 0.41 at 1538, 0.36 | 0.43 at 2050, 0.39 | 0.33 at 4098
+//   join's gradient 0.22 | 0.19 at 517
 template <typename T, typename S, int E, bool BRANCH, int MOVES>
 cudaError_t launch_widths(const NormLaunch &L, cudaStream_t stream) {
     const int w = L.width;
